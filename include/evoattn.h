@@ -350,6 +350,182 @@ evoattn_status evoattn_transition(const void* z, const void* o, const void* w_o,
                                   int B, int N, int C, int HD, int F, cudaStream_t stream);
 
 /*
+ * The seam between two blocks of the pair stack, fused: the norm after a
+ * block, its gate and residual scale, the residual add, and the norm before
+ * the next block (MegaFold technical summary, "Methodik" section 3
+ * "EvoFusion", Umfang: layer normalisation between the operators of a block,
+ * without an N x N intermediate in HBM; the norm after the block, its gate and
+ * its scale have no counterpart there).  For every row r = (b, i, j) of C
+ * channels, with n(v) = (v - mean v) / sqrt(var v + eps) (var: mean squared
+ * deviation) for EVOATTN_NORM_LAYER or v / sqrt(mean v^2 + eps) for
+ * EVOATTN_NORM_RMS:
+ *
+ *   x1 = x + scale * sigmoid(gate) * (n(u) * gamma_post + beta_post)
+ *   y  = n(x1) * gamma_pre + beta_pre      (of x1 in fp32, before its rounding)
+ *
+ *  x, x1      : [B, I, J, C] device, `stream_dtype`: the residual stream.
+ *  u, gate, y : [B, I, J, C] device, `dtype`: the block's output, its gate
+ *               (before the sigmoid) and the next block's input.
+ *  scale, gamma_*, beta_* : [C] device fp32, contiguous.
+ *  *_strides  : host arrays {b, i, j, c} in elements; the c stride is 1, the
+ *               others are non-negative (an axis of extent 1 may have any).
+ *               An input may repeat rows by a stride of 0; rows of an output
+ *               must not overlap.
+ *  Optional (NULL): u, and then gate, scale, gamma_post, beta_post and x1 are
+ *               NULL too (the norm before a block alone); y, and then
+ *               gamma_pre and beta_pre (the norm after a block alone); not
+ *               both.  A NULL scale or gamma is 1, a NULL beta 0, a NULL gate
+ *               multiplies by 1.
+ *  x1 may be x itself (same address and strides); otherwise outputs overlap
+ *               neither inputs nor each other.
+ * Supported: (stream_dtype, dtype) = (BF16, BF16), (F32, BF16) or (F32, F32),
+ * C <= 4096, B * I * J < 2^31 - 2^21 (otherwise EVOATTN_ERR_UNSUPPORTED).
+ * Rows whose address and strides are multiples of 16 bytes and C % 8 == 0 run
+ * at full speed; any others are read element by element.
+ */
+typedef enum { EVOATTN_NORM_LAYER = 0, EVOATTN_NORM_RMS = 1 } evoattn_norm_kind;
+
+evoattn_status evoattn_block_norm(const void* x, const int64_t x_strides[4],
+                                  const void* u, const int64_t u_strides[4],
+                                  const void* gate, const int64_t gate_strides[4],
+                                  const float* scale, const float* gamma_post,
+                                  const float* beta_post, const float* gamma_pre,
+                                  const float* beta_pre,
+                                  void* x1, const int64_t x1_strides[4],
+                                  void* y, const int64_t y_strides[4],
+                                  int B, int I, int J, int C, evoattn_dtype stream_dtype,
+                                  evoattn_dtype dtype, evoattn_norm_kind kind, float eps,
+                                  cudaStream_t stream);
+
+/* Bytes of device workspace evoattn_block_norm_bwd needs (0 for a C outside
+ * 1..4096). */
+size_t evoattn_block_norm_bwd_workspace_size(int C);
+
+/*
+ * Gradients of evoattn_block_norm.
+ *
+ *  dx1        : gradient of x1 from everything else that reads the stream,
+ *               `stream_dtype`; NULL for zero (then dy is given).
+ *  dy         : gradient of y, `dtype`; NULL when the forward had no y.
+ *  x1         : x1 as the forward stored it (the x of a forward without u);
+ *               read, and given, only with dy.
+ *  u, gate, scale, gamma_post, beta_post, gamma_pre : as in the forward.
+ *  dx         : gradient of x, `stream_dtype`, written; given exactly with dy
+ *               (without y the gradient of x is dx1).
+ *  du, dgate  : `dtype`, written; given exactly with u and gate.  Axes along
+ *               which the gate has stride 0 (and an extent above 1) share one
+ *               gate row: dgate has stride 0 there too, and receives the sum.
+ *  dscale, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre : [C] fp32, written;
+ *               each may be NULL.  The first three are NULL without u, the
+ *               others without dy.
+ *  dx may be dx1 itself (same address and strides).
+ *  workspace  : device, 256-byte aligned, at least
+ *               evoattn_block_norm_bwd_workspace_size(C) bytes; overwritten;
+ *               not to be used by another call that runs concurrently.
+ * All sums have a fixed order: repeated calls give the same bits.
+ */
+evoattn_status evoattn_block_norm_bwd(const void* dx1, const int64_t dx1_strides[4],
+                                      const void* dy, const int64_t dy_strides[4],
+                                      const void* x1, const int64_t x1_strides[4],
+                                      const void* u, const int64_t u_strides[4],
+                                      const void* gate, const int64_t gate_strides[4],
+                                      const float* scale, const float* gamma_post,
+                                      const float* beta_post, const float* gamma_pre,
+                                      void* dx, const int64_t dx_strides[4],
+                                      void* du, const int64_t du_strides[4],
+                                      void* dgate, const int64_t dgate_strides[4],
+                                      float* dscale, float* dgamma_post, float* dbeta_post,
+                                      float* dgamma_pre, float* dbeta_pre,
+                                      int B, int I, int J, int C, evoattn_dtype stream_dtype,
+                                      evoattn_dtype dtype, evoattn_norm_kind kind, float eps,
+                                      void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+
+/*
+ * One AdamW step over many tensors (no counterpart in the MegaFold pages: the
+ * optimiser of the training iteration whose operators they describe).  For
+ * every tensor and element, with t the number of this step (from 1):
+ *
+ *   g' = clip * g                        (clip = 1 without EVOATTN_ADAMW_CLIP)
+ *   m  = beta1 m + (1 - beta1) g'        v = beta2 v + (1 - beta2) g'^2
+ *   p  = p (1 - lr weight_decay)
+ *        - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ *   copy = bf16(p)
+ *
+ * States (state_bits) are fp32, or 8 bits: blocks of EVOATTN_ADAMW_BLOCK
+ * elements (the last one of a tensor may be shorter) hold m as e4m3 codes
+ * times exp_avg_scale[block], and sqrt(v) as e4m3 codes times
+ * exp_avg_sq_scale[block], with scale = (largest magnitude) / 448.  A positive
+ * sqrt(v) never gets the code 0 (it takes the smallest code instead), so the
+ * quotient stays bounded; a block whose largest magnitude is below 2^-100 is
+ * held as zeros.  The update itself uses m and v before they are rounded.
+ */
+#define EVOATTN_ADAMW_BLOCK 256
+#define EVOATTN_ADAMW_CLIP 1u /* flags: use the norm that evoattn_grad_norm left */
+
+typedef struct {
+    float* param;            /* [n] fp32, updated */
+    const void* grad;        /* [n], grad_dtype */
+    void* exp_avg;           /* [n] fp32 or e4m3, updated */
+    void* exp_avg_sq;        /* [n] fp32 (v) or e4m3 (sqrt v), updated */
+    float* exp_avg_scale;    /* [ceil(n / 256)], updated; NULL for 32-bit states */
+    float* exp_avg_sq_scale; /* likewise */
+    void* copy;              /* [n] bf16, written, or NULL */
+    int64_t n;               /* elements, >= 0 */
+    float weight_decay;      /* >= 0 */
+    int32_t grad_dtype;      /* evoattn_dtype */
+} evoattn_adamw_tensor;
+
+/* Device memory of one optimiser, zeroed by the caller before its first use
+ * (step may start at the number of steps already taken). */
+typedef struct {
+    int64_t step;        /* steps taken; evoattn_adamw counts it up */
+    float norm;          /* written by evoattn_grad_norm: norm of all gradients */
+    float clip;          /* min(1, max_norm / (norm + 1e-6)) */
+    uint32_t skip;       /* 1 when the norm is infinite or NaN */
+    uint32_t ticket[3];  /* the kernels' own; 0 between calls */
+} evoattn_optim_state;
+
+/* Bytes of device workspace evoattn_grad_norm needs (0 if count < 1). */
+size_t evoattn_grad_norm_workspace_size(int count);
+
+/*
+ * norm = sqrt(sum of g^2 over all elements of all tensors) into state->norm,
+ * with the clipping coefficient and the skip flag beside it.  Squares are
+ * summed in fp32 within a thread and in fp64 from there, in a fixed order: the same
+ * bits every time.  A norm beyond the fp32 range counts as infinite.
+ *
+ *  tensors  : host array; only grad, n and grad_dtype are read.
+ *  max_norm : > 0; INFINITY for the norm alone (clip = 1).
+ *  state    : device, 8-byte aligned.
+ *  workspace: device, 256-byte aligned; as for the other entry points.
+ */
+evoattn_status evoattn_grad_norm(const evoattn_adamw_tensor* tensors, int count, float max_norm,
+                                 evoattn_optim_state* state, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ *  tensors    : host array, read before the call returns (not needed after).
+ *               Tensors of one call do not overlap; all have the same state
+ *               width.  Contiguous; element alignment suffices (16 bytes for
+ *               full speed).
+ *  lr         : >= 0; lr_device, when not NULL, is a device fp32 scalar read
+ *               by the kernel instead (a captured graph then follows it).
+ *  beta1, beta2 in [0, 1), eps > 0.
+ *  state_bits : 32 or 8.
+ *  flags      : 0 or EVOATTN_ADAMW_CLIP: multiply the gradients by state->clip,
+ *               and when state->skip is set change nothing, not even step.
+ *  state      : device; step is read and counted up on the device, so a
+ *               captured step replays as the next one.
+ * One launch per 400 tensors.  Calls that share a state or a tensor must be
+ * ordered by the caller.
+ */
+evoattn_status evoattn_adamw(const evoattn_adamw_tensor* tensors, int count, float lr,
+                             const float* lr_device, double beta1, double beta2, float eps,
+                             int state_bits, unsigned flags, evoattn_optim_state* state,
+                             cudaStream_t stream);
+
+/*
  * Testing hook for the bounded-wait failure path; not needed in normal use.
  * Applies to every tcgen05 kernel enqueued after the call, on any device, by
  * any thread of the process.

@@ -115,7 +115,7 @@ using namespace evo;
 
 extern "C" {
 
-int evoattn_version(void) { return 200; }  // 0.2.0
+int evoattn_version(void) { return 300; }  // 0.3.0
 
 evoattn_status evoattn_debug_set_wait(unsigned long long limit_ns, int stall) {
   g_wait_limit_ns.store(limit_ns == 0 ? kWaitTimeoutNs : limit_ns);

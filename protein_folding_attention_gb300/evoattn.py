@@ -8,6 +8,7 @@ missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -21,11 +22,23 @@ BF16, F32 = 0, 1
 DBIAS_DETERMINISTIC, DBIAS_ATOMIC = 0, 1
 DQ_DETERMINISTIC = 2  # OR-ed with either: dq bit-identical too
 DBIAS_FUSED = 4  # dbias summed in the dK/dV pass (fp32 atomics)
+NORM_LAYER, NORM_RMS = 0, 1
+ADAMW_BLOCK = 256  # elements that share a scale in the 8-bit states
+ADAMW_CLIP = 1
 
 _lib = None
 _I64_5 = ctypes.c_int64 * 5
 _I64_4 = ctypes.c_int64 * 4
 _I64_3 = ctypes.c_int64 * 3
+
+
+class AdamwTensor(ctypes.Structure):
+    """evoattn_adamw_tensor: one tensor of an AdamW step."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
+                ("copy", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_float), ("grad_dtype", ctypes.c_int32)]
 
 
 class EvoAttnError(RuntimeError):
@@ -68,6 +81,20 @@ def load(path: str = LIB_PATH):
     lib.evoattn_transition.argtypes = [vp, vp, vp, fp, fp, vp, vp, ctypes.c_float, vp,
                                        i, i, i, i, i, vp]
     lib.evoattn_transition.restype = i
+    f, d = ctypes.c_float, ctypes.c_double
+    lib.evoattn_block_norm.argtypes = [vp, i64p] * 3 + [fp] * 5 + [vp, i64p] * 2 + [i] * 7 + [f, vp]
+    lib.evoattn_block_norm.restype = i
+    lib.evoattn_block_norm_bwd_workspace_size.argtypes = [i]
+    lib.evoattn_block_norm_bwd_workspace_size.restype = sz
+    lib.evoattn_block_norm_bwd.argtypes = ([vp, i64p] * 5 + [fp] * 4 + [vp, i64p] * 3 + [fp] * 5 +
+                                           [i] * 7 + [f, vp, sz, vp])
+    lib.evoattn_block_norm_bwd.restype = i
+    lib.evoattn_grad_norm_workspace_size.argtypes = [i]
+    lib.evoattn_grad_norm_workspace_size.restype = sz
+    lib.evoattn_grad_norm.argtypes = [ctypes.POINTER(AdamwTensor), i, f, vp, vp, sz, vp]
+    lib.evoattn_grad_norm.restype = i
+    lib.evoattn_adamw.argtypes = [ctypes.POINTER(AdamwTensor), i, f, vp, d, d, f, i, u, vp, vp]
+    lib.evoattn_adamw.restype = i
     lib.evoattn_debug_set_wait.argtypes = [ctypes.c_ulonglong, i]
     lib.evoattn_debug_set_wait.restype = i
     _lib = lib
@@ -228,6 +255,322 @@ def transition(z, gamma, beta, w1, w2, eps=1e-5, o=None, w_o=None, out=None, str
                                 _stream(stream))
     _check(st, "evoattn_transition")
     return out
+
+
+def _rows4(t, shape, dtype, device, name):
+    """Checks a [B, I, J, C] operand; returns its address and strides."""
+    if t is None:
+        return None, None
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr(), _I64_4(*t.stride())
+
+
+def _vec(t, C, device, name):
+    """Checks a [C] fp32 parameter; returns its address."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.shape != (C,) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous fp32 [{C}] tensor on {device}")
+    return t.data_ptr()
+
+
+def _on_device(t):
+    """The tensor's device, which has to be the current one (the library
+    enqueues on the current device's streams)."""
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device}: a CUDA tensor on the current device is needed")
+    return t.device
+
+
+def _allocate_on(stream):
+    """Tensors made inside belong to `stream` (None: the current one), so that
+    a workspace is not reused before the kernels on that stream are done."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _expanded(gate, shape):
+    if gate is None or gate.shape == shape:
+        return gate
+    if gate.dim() != 4 or any(g != n and g != 1 for g, n in zip(gate.shape, shape)) or \
+            gate.shape[3] != shape[3]:
+        raise ValueError(f"gate {tuple(gate.shape)} does not broadcast to {tuple(shape)}")
+    return gate.expand(shape)
+
+
+def block_norm(x, u=None, gate=None, scale=None, gamma_post=None, beta_post=None, gamma_pre=None,
+               beta_pre=None, kind=NORM_LAYER, eps=1e-5, pre=True, y_dtype=None, x1=None, y=None,
+               stream=None):
+    """The seam between two blocks (see evoattn_block_norm):
+
+        x1 = x + scale * sigmoid(gate) * (n(u) * gamma_post + beta_post)
+        y  = n(x1) * gamma_pre + beta_pre
+
+    x [B, I, J, C]: the residual stream, bf16 or fp32; u (the block's output)
+    and gate: bf16, or fp32 with an fp32 stream; gate may have extent 1 along
+    any row axis and is then shared.  scale and the norms' parameters: [C]
+    fp32.  `kind`: NORM_LAYER or NORM_RMS.  Any strides with unit stride along
+    C (16-byte aligned rows run at full speed).  Without u the call is the
+    norm before a block alone (x1 is x), with pre=False the norm after a block
+    alone (y is None).  y has u's type; y_dtype names it where there is no u
+    (default: x's).  Outputs take x's layout; x1=x updates the stream in place.
+    Returns (x1, y)."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, I, J, C]")
+    shape, dev = x.shape, _on_device(x)
+    C = shape[3]
+    io = u.dtype if u is not None else (y_dtype or x.dtype)
+    if y_dtype is not None and y_dtype != io:
+        raise ValueError("y has the type of u")
+    with _allocate_on(stream):
+        if u is not None and x1 is None:
+            x1 = torch.empty_like(x)
+        if pre and y is None:
+            y = torch.empty_like(x, dtype=io)
+    if not pre and y is not None:
+        raise ValueError("y without pre")
+    gate = _expanded(gate, shape)
+    out = x1 if u is not None else None
+    st = load().evoattn_block_norm(
+        *_rows4(x, shape, x.dtype, dev, "x"), *_rows4(u, shape, io, dev, "u"),
+        *_rows4(gate, shape, io, dev, "gate"), _vec(scale, C, dev, "scale"),
+        _vec(gamma_post, C, dev, "gamma_post"), _vec(beta_post, C, dev, "beta_post"),
+        _vec(gamma_pre, C, dev, "gamma_pre"), _vec(beta_pre, C, dev, "beta_pre"),
+        *_rows4(out, shape, x.dtype, dev, "x1"), *_rows4(y, shape, io, dev, "y"),
+        *shape, _dtype_code(x), F32 if io == torch.float32 else BF16, kind, eps, _stream(stream))
+    _check(st, "evoattn_block_norm")
+    return (x if u is None else x1), y
+
+
+def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_post=None,
+                   beta_post=None, gamma_pre=None, beta_pre=None, kind=NORM_LAYER, eps=1e-5,
+                   dx=None, workspace=None, stream=None):
+    """Gradients of block_norm (see evoattn_block_norm_bwd).  dx1: the gradient
+    of x1 from what else reads the stream (None for zero); dy: the gradient of
+    y (None when the forward had pre=False); x1: the stream as the forward
+    returned it (needed with dy); the rest as in the forward.  dx=dx1 works in
+    place.  Returns a dict with dx (dx1 itself without dy), du, dgate (in the
+    gate's own shape), and fp32 dscale, dgamma_post, dbeta_post, dgamma_pre,
+    dbeta_pre of the parameters that were given."""
+    lead = dx1 if dx1 is not None else x1
+    if lead is None or (dy is None and (u is None or dx1 is None)):
+        raise ValueError("dx1 with u, or dy with x1, is needed")
+    if lead.dim() != 4:
+        raise ValueError("gradients must be [B, I, J, C]")
+    shape, dev = lead.shape, _on_device(lead)
+    C = shape[3]
+    if dy is not None and x1 is None:
+        raise ValueError("dy needs x1")
+    if dy is None:
+        x1 = None
+    io = u.dtype if u is not None else dy.dtype
+    lib = load()
+    need = lib.evoattn_block_norm_bwd_workspace_size(C)
+    if gate is not None and any(n > 1 and s == 0 for n, s in zip(gate.shape, gate.stride())):
+        gate = gate.contiguous()  # an expanded view: its gradient is that of each row by itself
+    full = _expanded(gate, shape)
+    out = {}
+    with _allocate_on(stream):
+        if dy is not None:
+            out["dx"] = torch.empty_like(lead) if dx is None else dx
+        du = dgate = None
+        if u is not None:
+            out["du"] = du = torch.empty_like(u)
+            if gate is not None:
+                out["dgate"] = dgate = torch.empty_like(gate)
+        params = (("dscale", scale), ("dgamma_post", gamma_post), ("dbeta_post", beta_post),
+                  ("dgamma_pre", gamma_pre), ("dbeta_pre", beta_pre))
+        given = [name for name, t in params if t is not None]
+        if given:
+            for name, row in zip(given, torch.empty((len(given), C), device=dev,
+                                                    dtype=torch.float32).unbind(0)):
+                out[name] = row
+        if workspace is None:
+            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    _vec(beta_pre, C, dev, "beta_pre")
+    get = out.get
+    st = lib.evoattn_block_norm_bwd(
+        *_rows4(dx1, shape, lead.dtype, dev, "dx1"), *_rows4(dy, shape, io, dev, "dy"),
+        *_rows4(x1, shape, lead.dtype, dev, "x1"), *_rows4(u, shape, io, dev, "u"),
+        *_rows4(full, shape, io, dev, "gate"), _vec(scale, C, dev, "scale"),
+        _vec(gamma_post, C, dev, "gamma_post"), _vec(beta_post, C, dev, "beta_post"),
+        _vec(gamma_pre, C, dev, "gamma_pre"),
+        *_rows4(get("dx"), shape, lead.dtype, dev, "dx"), *_rows4(du, shape, io, dev, "du"),
+        *_rows4(_expanded(dgate, shape), shape, io, dev, "dgate"),
+        *(_ptr(get(name)) for name, _ in params), *shape, _dtype_code(lead),
+        F32 if io == torch.float32 else BF16, kind, eps, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "evoattn_block_norm_bwd")
+    if dy is None:
+        out["dx"] = dx1
+    return out
+
+
+def _grad_table(grads):
+    """An evoattn_adamw_tensor array with the gradients' fields filled in."""
+    table = (AdamwTensor * len(grads))()
+    for row, g in zip(table, grads):
+        row.grad, row.n, row.grad_dtype = g.data_ptr(), g.numel(), _dtype_code(g)
+    return table
+
+
+def _check_flat(t, n, dtype, device, name):
+    if t.dtype != dtype or t.numel() != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements on {device}")
+
+
+class AdamW:
+    """AdamW over many tensors at once, states in 32 or 8 bits (see
+    evoattn_adamw), optionally clipped by the norm of all gradients.
+
+    params: fp32 tensors (contiguous); grads: the bf16 or fp32 gradient buffer
+    of each, which the backward pass fills before every step (step(grads=...)
+    takes others); copies: bf16 tensors that receive the rounded parameters,
+    or None (for all or for some).  weight_decay: a number, or one per tensor.
+    lr: a number (`opt.lr` may be changed), or a one-element fp32 CUDA tensor
+    that the kernel reads (a captured step then follows it).
+
+    The states are flat tensors in which each parameter starts at the next
+    multiple of ADAMW_BLOCK elements (`opt.offsets`); exp_avg, exp_avg_sq and,
+    for 8 bits, the scales of both (one fp32 per block) may be handed in to
+    resume.  With state_bits=8 they are torch.float8_e4m3fn codes: the first
+    moment is code * scale, the root of the second one code * scale.  Their
+    padding is never written.  The step counter lives on the device.  One
+    optimiser is used on one stream at a time.
+    """
+
+    def __init__(self, params, grads, *, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+                 weight_decay=0.01, state_bits=32, exp_avg=None, exp_avg_sq=None,
+                 exp_avg_scale=None, exp_avg_sq_scale=None, step=0):
+        self.params, self.grads = list(params), list(grads)
+        n = len(self.params)
+        self.copies = [None] * n if copies is None else list(copies)
+        if n == 0 or len(self.grads) != n or len(self.copies) != n:
+            raise ValueError("as many gradients and copies as parameters, at least one")
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits is 32 or 8")
+        decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        if len(decay) != n:
+            raise ValueError("one weight_decay, or one per parameter")
+        self.device = dev = _on_device(self.params[0])
+        self.lr, self.betas, self.eps, self.state_bits = lr, betas, eps, state_bits
+        self.offsets, total = [], 0
+        for p in self.params:
+            self.offsets.append(total)
+            total += -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
+        wide = state_bits == 32
+        dtype = torch.float32 if wide else torch.float8_e4m3fn
+
+        def state(t, count, kind, name):
+            if t is None:
+                return torch.zeros(count, device=dev, dtype=kind)
+            _check_flat(t, count, kind, dev, name)
+            return t
+
+        self.exp_avg = state(exp_avg, total, dtype, "exp_avg")
+        self.exp_avg_sq = state(exp_avg_sq, total, dtype, "exp_avg_sq")
+        if wide:
+            if exp_avg_scale is not None or exp_avg_sq_scale is not None:
+                raise ValueError("scales belong to 8-bit states")
+            self.exp_avg_scale = self.exp_avg_sq_scale = None
+        else:
+            blocks = total // ADAMW_BLOCK
+            self.exp_avg_scale = state(exp_avg_scale, blocks, torch.float32, "exp_avg_scale")
+            self.exp_avg_sq_scale = state(exp_avg_sq_scale, blocks, torch.float32, "exp_avg_sq_scale")
+        self._table = (AdamwTensor * n)()
+        written = []
+        size = self.exp_avg.element_size()
+        for i, (row, p, c) in enumerate(zip(self._table, self.params, self.copies)):
+            _check_flat(p, p.numel(), torch.float32, dev, f"parameter {i}")
+            written.append((p.data_ptr(), 4 * p.numel()))
+            if c is not None:
+                _check_flat(c, p.numel(), torch.bfloat16, dev, f"copy {i}")
+                written.append((c.data_ptr(), 2 * p.numel()))
+                row.copy = c.data_ptr()
+            at = self.offsets[i]
+            row.param, row.n, row.weight_decay = p.data_ptr(), p.numel(), decay[i]
+            row.exp_avg = self.exp_avg.data_ptr() + at * size
+            row.exp_avg_sq = self.exp_avg_sq.data_ptr() + at * size
+            if not wide:
+                row.exp_avg_scale = self.exp_avg_scale.data_ptr() + at // ADAMW_BLOCK * 4
+                row.exp_avg_sq_scale = self.exp_avg_sq_scale.data_ptr() + at // ADAMW_BLOCK * 4
+        written += [(t.data_ptr(), t.numel() * t.element_size()) for t in
+                    (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
+                    if t is not None]
+        written = sorted(w for w in written if w[1])
+        if any(a + k > b for (a, k), (b, _) in zip(written, written[1:])):
+            raise ValueError("parameters, copies and states overlap (is a tensor listed twice?)")
+        self._bind(self.grads)
+        # evoattn_optim_state: step, norm, clip, skip, tickets
+        self._state = torch.zeros(8, device=dev, dtype=torch.int32)
+        self._state[:2].view(torch.int64).fill_(step)
+        #: norm of all gradients at the last clipped step (0-dim fp32, device)
+        self.norm = self._state[2:3].view(torch.float32)[0]
+        self._workspace = torch.empty(load().evoattn_grad_norm_workspace_size(n), device=dev,
+                                      dtype=torch.uint8)
+
+    def _bind(self, grads):
+        if len(grads) != len(self.params):
+            raise ValueError("as many gradients as parameters")
+        for i, (row, g) in enumerate(zip(self._table, grads)):
+            if g.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"gradient {i}: bf16 or fp32, got {g.dtype}")
+            _check_flat(g, row.n, g.dtype, self.device, f"gradient {i}")
+            row.grad, row.grad_dtype = g.data_ptr(), _dtype_code(g)
+        self.grads = grads
+
+    def step(self, max_norm=None, grads=None, stream=None):
+        """One step.  max_norm: clip by the norm of all gradients, which is
+        returned (the tensor `norm`, overwritten by the next such step); a step
+        whose norm is infinite or NaN then changes nothing.  grads: gradients
+        to use from now on instead of those bound before."""
+        if grads is not None:
+            self._bind(list(grads))
+        lib, n = load(), len(self.params)
+        st = _stream(stream)
+        if stream is not None:  # not to be reused before that stream is done with them
+            for t in (self._state, self._workspace, self.exp_avg, self.exp_avg_sq,
+                      self.exp_avg_scale, self.exp_avg_sq_scale):
+                if t is not None:
+                    t.record_stream(stream)
+        lr, lr_device = self.lr, None
+        if isinstance(lr, torch.Tensor):
+            _check_flat(lr, 1, torch.float32, self.device, "lr")
+            lr, lr_device = 0.0, lr.data_ptr()
+        state = self._state.data_ptr()
+        if max_norm is not None:
+            _check(lib.evoattn_grad_norm(self._table, n, max_norm, state,
+                                         self._workspace.data_ptr(), self._workspace.numel(), st),
+                   "evoattn_grad_norm")
+        _check(lib.evoattn_adamw(self._table, n, lr, lr_device, self.betas[0], self.betas[1],
+                                 self.eps, self.state_bits, 0 if max_norm is None else ADAMW_CLIP,
+                                 state, st), "evoattn_adamw")
+        return None if max_norm is None else self.norm
+
+    def steps_taken(self) -> int:
+        """Steps taken so far (waits for the device)."""
+        return int(self._state[:2].view(torch.int64).item())
+
+
+def grad_norm(grads, stream=None):
+    """sqrt of the sum of squares of all elements of the bf16 or fp32 tensors
+    `grads` (contiguous), as a 0-dim fp32 tensor (see evoattn_grad_norm)."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    dev = _on_device(grads[0])
+    for i, g in enumerate(grads):
+        if g.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"gradient {i}: bf16 or fp32, got {g.dtype}")
+        _check_flat(g, g.numel(), g.dtype, dev, f"gradient {i}")
+    lib = load()
+    with _allocate_on(stream):
+        state = torch.zeros(8, device=dev, dtype=torch.int32)
+        ws = torch.empty(lib.evoattn_grad_norm_workspace_size(len(grads)), device=dev, dtype=torch.uint8)
+    _check(lib.evoattn_grad_norm(_grad_table(grads), len(grads), float("inf"), state.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), _stream(stream)), "evoattn_grad_norm")
+    return state[2:3].view(torch.float32)[0]
 
 
 def debug_set_wait(limit_ns: int = 0, stall: bool = False) -> None:
