@@ -26,12 +26,13 @@
 // Layout: a row belongs to a group of G threads, 8 channels each, so that a
 // bf16 row is one 16-byte access per thread and its values stay in registers
 // from load to store.  G = 8, 16 or 32 lanes of a warp up to C = 256 (sums by
-// shuffles); above that W warps (sums by shuffles, then through shared memory
-// with one named barrier per sum).  Persistent CTAs walk the rows, each thread
-// keeping its channels' parameters, and in the backward the parameter
-// gradients of its rows, in registers; the next row is loaded while the
-// current one is worked on.  The CTAs' sums go to the workspace and a second
-// kernel adds them in a fixed order: repeated calls give the same bits.
+// shuffles); above that several warps (sums by shuffles, then through shared
+// memory with one named barrier per sum).  Persistent CTAs walk the rows.  A thread
+// copies its own channels of the coming rows into a ring in shared memory
+// (cp.async, no registers held meanwhile, no barrier: it reads only what it
+// copied), and keeps the parameter gradients of its channels over all its rows
+// in registers.  The CTAs' sums go to the workspace and a second kernel adds
+// them in a fixed order: repeated calls give the same bits.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,12 +42,24 @@
 #include <atomic>
 
 #include "block_norm.h"
+#include "common.cuh"
 
 namespace evo {
 namespace norm {
 
-constexpr int kE = 8;          // channels per thread
-constexpr int kThreads = 256;  // threads of a CTA at most, where a row takes at most 8 warps
+constexpr int kE = 8;             // channels per thread
+constexpr int kP = kE / 2;        // pairs of channels (packed fp32 arithmetic)
+constexpr int kThreads = 256;     // threads of a CTA where a row takes at most 8 warps
+constexpr int kMaxThreads = 512;  // ... 16 warps (C = 4096)
+
+// How a row is laid over threads: 8, 16 or 32 lanes of a warp, several warps
+// (up to 8, with the ring), or any number of warps without a ring, whose rows
+// and parameters are read as they are needed (more than 8 warps, or rows that
+// cannot be copied 16 bytes at a time).
+constexpr int kWarps = 0, kPlain = -1;
+constexpr bool warps_of(int G) { return G <= 0; }
+constexpr bool ring_of(int G, bool vec) { return vec && G >= 0; }
+constexpr int threads_of(int G) { return G == kPlain ? kMaxThreads : kThreads; }
 
 // ---------------------------------------------------------------------------
 // rows
@@ -82,14 +95,15 @@ __device__ __forceinline__ RowPos row_pos(const Rows& R, uint32_t row) {
   const uint32_t b = div_by(a, R.d1);
   return RowPos{b, a - b * R.d1.d, row - a * R.d2.d};
 }
-__device__ __forceinline__ char* row_ptr(const Operand& o, const RowPos& r, bool flat) {
+__device__ __forceinline__ char* row_ptr(const Operand& o, const RowPos& r, const Rows& R) {
   char* p = o.p + r.i2 * o.s2;
-  if (!flat) p += r.i1 * o.s1 + r.i0 * o.s0;
+  if (!R.flat) p += r.i1 * o.s1 + r.i0 * o.s0;
   return p;
 }
 
 struct Params {
-  Rows rows_of;
+  Rows rows_of;   // row axes of every operand
+  Rows gate_of;   // row axes of gate and dgate where gate rows are shared
   uint32_t rows;
   int C;
   int lanes;      // threads of a row's group (a multiple of 32 where it spans warps)
@@ -98,7 +112,7 @@ struct Params {
   Operand x, u, gate, x1, y, dx1, dy, dx, du, dgate;
   const float *scale, *gamma_post, *beta_post, *gamma_pre, *beta_pre;
   float* out[5];  // dscale, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre
-  float* part;    // [CTAs][5][C], or out[] itself when there is one CTA
+  float* part;    // [CTAs][5][C]
   // a gate row shared by `share` consecutive rows: `segs` items of at most
   // `seg_rows` rows each per gate row
   uint32_t share, segs, seg_rows, items;
@@ -107,94 +121,82 @@ struct Params {
 };
 
 // ---------------------------------------------------------------------------
-// a thread's 8 channels of a row
+// a thread's 8 channels of a row, as four pairs
 // ---------------------------------------------------------------------------
-template <typename T, bool VEC>
-struct Raw;
-template <>
-struct Raw<__nv_bfloat16, true> {
-  uint4 v;
-};
-template <>
-struct Raw<float, true> {
-  float4 a, b;
-};
-template <>
-struct Raw<__nv_bfloat16, false> {
-  __nv_bfloat16 v[kE];
-};
-template <>
-struct Raw<float, false> {
-  float v[kE];
-};
-
 // VEC: channels 8 * lane + e, with C a multiple of 8 and 16-byte aligned rows.
 // Otherwise channels e * lanes + lane, one element per access.
 template <bool VEC>
 __device__ __forceinline__ int channel(int lane, int lanes, int e) {
   return VEC ? lane * kE + e : e * lanes + lane;
 }
+struct V {
+  float2 p[kP];
+  __device__ __forceinline__ float& operator[](int e) { return e & 1 ? p[e >> 1].y : p[e >> 1].x; }
+  __device__ __forceinline__ float operator[](int e) const { return e & 1 ? p[e >> 1].y : p[e >> 1].x; }
+};
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float sum(const V& v) {
+  const float2 s = add2(add2(v.p[0], v.p[1]), add2(v.p[2], v.p[3]));
+  return s.x + s.y;
+}
+__device__ __forceinline__ float dot(const V& a, const V& b) {
+  const float2 s = fma2(a.p[0], b.p[0], mul2(a.p[1], b.p[1]));
+  const float2 t = fma2(a.p[2], b.p[2], mul2(a.p[3], b.p[3]));
+  const float2 r = add2(s, t);
+  return r.x + r.y;
+}
 
-__device__ __forceinline__ void load(Raw<__nv_bfloat16, true>& r, const char* row, int lane, int, int) {
-  r.v = *(reinterpret_cast<const uint4*>(row) + lane);
-}
-__device__ __forceinline__ void load(Raw<float, true>& r, const char* row, int lane, int, int) {
-  const float4* p = reinterpret_cast<const float4*>(row) + 2 * lane;
-  r.a = p[0];
-  r.b = p[1];
-}
+// 16-byte units of a thread's channels
 template <typename T>
-__device__ __forceinline__ void load(Raw<T, false>& r, const char* row, int lane, int lanes, int C) {
-  const T* p = reinterpret_cast<const T*>(row);
+constexpr int units() { return kE * (int)sizeof(T) / 16; }
+
+template <typename T>
+__device__ __forceinline__ V widen(const uint4 (&r)[units<T>()]) {
+  V v;
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
 #pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    const int c = e * lanes + lane;
-    r.v[e] = c < C ? p[c] : T(0.f);
+    for (int k = 0; k < kP; ++k) v.p[k] = make_float2(bf16lo(w[k]), bf16hi(w[k]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < kP; ++k) {
+      const uint4 q = r[k >> 1];
+      v.p[k] = k & 1 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
+                     : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    }
   }
-}
-
-__device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-
-__device__ __forceinline__ void widen(const Raw<__nv_bfloat16, true>& r, float (&v)[kE]) {
-  v[0] = lo_bf16(r.v.x); v[1] = hi_bf16(r.v.x); v[2] = lo_bf16(r.v.y); v[3] = hi_bf16(r.v.y);
-  v[4] = lo_bf16(r.v.z); v[5] = hi_bf16(r.v.z); v[6] = lo_bf16(r.v.w); v[7] = hi_bf16(r.v.w);
-}
-__device__ __forceinline__ void widen(const Raw<float, true>& r, float (&v)[kE]) {
-  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
-  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
-}
-template <typename T>
-__device__ __forceinline__ void widen(const Raw<T, false>& r, float (&v)[kE]) {
-#pragma unroll
-  for (int e = 0; e < kE; ++e) v[e] = static_cast<float>(r.v[e]);
+  return v;
 }
 
 template <typename T, bool VEC>
-struct Store;
-template <>
-struct Store<__nv_bfloat16, true> {
-  static __device__ __forceinline__ void put(char* row, int lane, int, int, const float (&v)[kE]) {
-    *(reinterpret_cast<uint4*>(row) + lane) =
-        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+__device__ __forceinline__ V load(const char* row, int lane, int lanes, int C) {
+  if constexpr (VEC) {
+    uint4 r[units<T>()];
+#pragma unroll
+    for (int k = 0; k < units<T>(); ++k) r[k] = reinterpret_cast<const uint4*>(row)[units<T>() * lane + k];
+    return widen<T>(r);
+  } else {
+    const T* p = reinterpret_cast<const T*>(row);
+    V v;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const int c = e * lanes + lane;
+      v[e] = c < C ? static_cast<float>(p[c]) : 0.f;
+    }
+    return v;
   }
-};
-template <>
-struct Store<float, true> {
-  static __device__ __forceinline__ void put(char* row, int lane, int, int, const float (&v)[kE]) {
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store(char* row, int lane, int lanes, int C, const V& v) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    reinterpret_cast<uint4*>(row)[lane] =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  } else if constexpr (VEC) {
     float4* p = reinterpret_cast<float4*>(row) + 2 * lane;
     p[0] = make_float4(v[0], v[1], v[2], v[3]);
     p[1] = make_float4(v[4], v[5], v[6], v[7]);
-  }
-};
-template <typename T>
-struct Store<T, false> {
-  static __device__ __forceinline__ void put(char* row, int lane, int lanes, int C, const float (&v)[kE]) {
+  } else {
     T* p = reinterpret_cast<T*>(row);
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
@@ -202,405 +204,559 @@ struct Store<T, false> {
       if (c < C) p[c] = static_cast<T>(v[e]);
     }
   }
-};
+}
 
 // A thread's channels of a parameter vector (`absent` without one).
 template <bool VEC>
-__device__ __forceinline__ void param(const float* p, float absent, int lane, int lanes, int C,
-                                      float (&v)[kE]) {
+__device__ __forceinline__ V param(const float* p, float absent, int lane, int lanes, int C) {
+  V v;
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
     const int c = channel<VEC>(lane, lanes, e);
     v[e] = c < C ? (p ? p[c] : absent) : 0.f;
   }
+  return v;
+}
+
+// The ring: a thread's own 16-byte slots, `UNITS` per stage.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  // (bytes = 0 reads nothing and fills with zeros)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T>
+__device__ __forceinline__ void ring_put(uint32_t slot, uint32_t unit, const char* row, int lane, uint32_t bytes) {
+#pragma unroll
+  for (int k = 0; k < units<T>(); ++k)
+    copy16(slot + k * unit, row + (size_t)(units<T>() * lane + k) * 16, bytes);
+}
+template <typename T>
+__device__ __forceinline__ V ring_get(const char* slot, uint32_t unit) {
+  uint4 r[units<T>()];
+#pragma unroll
+  for (int k = 0; k < units<T>(); ++k) r[k] = *reinterpret_cast<const uint4*>(slot + k * unit);
+  return widen<T>(r);
 }
 
 // ---------------------------------------------------------------------------
 // sums over a row's group
 // ---------------------------------------------------------------------------
-// G lanes of a warp, or (G = 0) several warps: then every warp leaves its sum
+// G lanes of a warp, or several warps: then every warp leaves its sum
 // in shared memory and reads all of them behind one barrier.  Two buffers take
 // turns, so that a sum's values are read before the barrier that precedes
 // their buffer's next use.
 constexpr int kMaxWarps = 16;
-struct GroupSum {
-  float2* buf;   // [2][kMaxWarps]
-  int warps, warp, barrier, turn;
+struct Group {
+  int lane, lanes;  // place in the row's group
+  int slot, slots;  // the group's place in the CTA
+  bool act;         // VEC: the thread has channels
+  float2* buf;      // [2][kMaxWarps]
+  int turn;
 };
 
-template <int G>
-__device__ __forceinline__ float2 group_sum(float2 v, GroupSum& g) {
-#pragma unroll
-  for (int o = (G == 0 ? 32 : G) / 2; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  if constexpr (G == 0) {
-    float2* b = g.buf + (g.turn ? kMaxWarps : 0);
-    g.turn ^= 1;
-    if ((threadIdx.x & 31) == 0) b[g.warp] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(g.barrier), "r"(g.warps * 32) : "memory");
-    v = make_float2(0.f, 0.f);
-    for (int i = 0; i < g.warps; ++i) {
-      v.x += b[i].x;
-      v.y += b[i].y;
-    }
-  }
+__device__ __forceinline__ float2 across_warps(float2 v, Group& g) {
+  float2* b = g.buf + (g.turn ? kMaxWarps : 0);
+  g.turn ^= 1;
+  const int warps = g.lanes >> 5;
+  if ((threadIdx.x & 31) == 0) b[g.lane >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + g.slot), "r"(g.lanes) : "memory");
+  v = make_float2(0.f, 0.f);
+  for (int i = 0; i < warps; ++i) v = add2(v, b[i]);
   return v;
 }
-
-// What a thread knows of its group.
-struct Group {
-  int lane, lanes;   // place in the row's group
-  int slot, slots;   // the group's place in the CTA
-  bool act;          // VEC: the thread has channels
-  GroupSum sum;
-};
+template <int G>
+__device__ __forceinline__ float2 group_sum(float2 v, Group& g) {
+#pragma unroll
+  for (int o = (warps_of(G) ? 32 : G) / 2; o > 0; o >>= 1)
+    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  if constexpr (warps_of(G)) v = across_warps(v, g);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v, Group& g) {
+#pragma unroll
+  for (int o = (warps_of(G) ? 32 : G) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (warps_of(G)) v = across_warps(make_float2(v, 0.f), g).x;
+  return v;
+}
 
 template <int G, bool VEC>
 __device__ __forceinline__ Group make_group(const Params& p, float2 (*smem)[2 * kMaxWarps]) {
   Group g;
-  if constexpr (G > 0) {
-    g.lanes = G;
-    g.slots = (int)blockDim.x / G;
-    g.slot = (int)threadIdx.x / G;
-    g.lane = (int)threadIdx.x % G;
-    g.sum = GroupSum{nullptr, 1, 0, 0, 0};
-  } else {
-    g.lanes = p.lanes;
-    g.slots = (int)blockDim.x / p.lanes;
-    g.slot = (int)threadIdx.x / p.lanes;
-    g.lane = (int)threadIdx.x - g.slot * p.lanes;
-    g.sum = GroupSum{smem[g.slot], p.lanes / 32, g.lane / 32, 1 + g.slot, 0};
-  }
+  g.lanes = G > 0 ? G : p.lanes;
+  g.slots = (int)blockDim.x / g.lanes;
+  g.slot = (int)threadIdx.x / g.lanes;
+  g.lane = (int)threadIdx.x - g.slot * g.lanes;
+  g.buf = G > 0 ? nullptr : smem[g.slot];
+  g.turn = 0;
   g.act = VEC ? g.lane * kE < p.C : true;
   return g;
 }
 
-// Whether this thread's channel e exists (VEC: all or none do, see Group::act).
+// v - mean, absent channels kept at zero (VEC: a thread has all its channels
+// or none, and one without is left out of the sums by Group::act).
 template <bool VEC>
-__device__ __forceinline__ bool has(const Group& g, int e, int C) {
-  return VEC ? true : e * g.lanes + g.lane < C;
+__device__ __forceinline__ void centre(V& v, float mean, const Group& g, int C) {
+  const float2 m = both(-mean);
+#pragma unroll
+  for (int k = 0; k < kP; ++k) v.p[k] = add2(v.p[k], m);
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+      if (e * g.lanes + g.lane >= C) v[e] = 0.f;
+  }
+}
+__device__ __forceinline__ void times(V& v, float r) {
+#pragma unroll
+  for (int k = 0; k < kP; ++k) v.p[k] = mul2(v.p[k], both(r));
 }
 
-// Statistics of one or two rows at once (the second where `two`): mean (0 for
-// rms) and 1 / sqrt(variance + eps); v becomes (v - mean) * rstd.  Two passes
-// over registers, the deviations squared after the mean is removed.
-template <int G, bool VEC, bool TWO>
-__device__ __forceinline__ float2 standardise(float (&a)[kE], float (&b)[kE], Group& g,
-                                              const Params& p) {
-  float2 mean = make_float2(0.f, 0.f);
+// v becomes (v - mean) * rstd (rms: v * rstd); returns rstd.  Two passes over
+// registers, the deviations squared after the mean is removed.
+template <int G, bool VEC>
+__device__ __forceinline__ float standardise(V& v, Group& g, const Params& p) {
   if (!p.rms) {
-    float2 s = make_float2(0.f, 0.f);
-    if (g.act) {  // (without VEC, absent channels hold zeros)
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        s.x += a[e];
-        if (TWO) s.y += b[e];
-      }
-    }
-    mean = group_sum<G>(s, g.sum);
-    mean.x *= p.inv_c;
-    mean.y *= p.inv_c;
+    const float s = sum(v);
+    centre<VEC>(v, group_sum<G>(g.act ? s : 0.f, g) * p.inv_c, g, p.C);
   }
-  float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    const bool ok = has<VEC>(g, e, p.C);
-    a[e] = ok ? a[e] - mean.x : 0.f;
-    s.x = fmaf(a[e], a[e], s.x);
-    if (TWO) {
-      b[e] = ok ? b[e] - mean.y : 0.f;
-      s.y = fmaf(b[e], b[e], s.y);
-    }
+  const float s = dot(v, v);
+  const float r = rsqrtf(fmaf(group_sum<G>(g.act ? s : 0.f, g), p.inv_c, p.eps));
+  times(v, r);
+  return r;
+}
+// Two rows at once, their sums side by side.
+template <int G, bool VEC>
+__device__ __forceinline__ float2 standardise(V& a, V& b, Group& g, const Params& p) {
+  if (!p.rms) {
+    const float2 s = make_float2(sum(a), sum(b));
+    const float2 m = group_sum<G>(g.act ? s : both(0.f), g);
+    centre<VEC>(a, m.x * p.inv_c, g, p.C);
+    centre<VEC>(b, m.y * p.inv_c, g, p.C);
   }
-  if (!g.act) s = make_float2(0.f, 0.f);
-  s = group_sum<G>(s, g.sum);
-  const float2 r = make_float2(rsqrtf(fmaf(s.x, p.inv_c, p.eps)), rsqrtf(fmaf(s.y, p.inv_c, p.eps)));
-#pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    a[e] *= r.x;
-    if (TWO) b[e] *= r.y;
-  }
+  const float2 s = make_float2(dot(a, a), dot(b, b));
+  const float2 t = group_sum<G>(g.act ? s : both(0.f), g);
+  const float2 r = make_float2(rsqrtf(fmaf(t.x, p.inv_c, p.eps)), rsqrtf(fmaf(t.y, p.inv_c, p.eps)));
+  times(a, r.x);
+  times(b, r.y);
   return r;
 }
 
-__device__ __forceinline__ float sigmoid(float v) {
-  return __fdividef(1.f, 1.f + __expf(-v));
+// 1 / (1 + 2^(-v log2 e)): relative error of a few 2^-23 beside |v| 2^-24 of
+// the exponent; far below zero the quotient underflows to 0 (v < -87).
+__device__ __forceinline__ void sigmoid(V& v) {
+#pragma unroll
+  for (int k = 0; k < kP; ++k) {
+    float2 t = mul2(v.p[k], both(-1.4426950408889634f));
+    t = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v.p[k].x) : "f"(t.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v.p[k].y) : "f"(t.y));
+  }
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
+template <typename TS, typename TI, bool POST>
+struct FwdRing {
+  static constexpr int UNITS = units<TS>() + (POST ? 2 * units<TI>() : 0);
+  // enough stages for about 150 bytes in flight per thread, 24 warps per SM
+  static constexpr int STAGES = 144 / (UNITS * 16) < 2 ? 2 : 144 / (UNITS * 16) > 4 ? 4 : 144 / (UNITS * 16);
+  static constexpr size_t bytes(int threads) { return (size_t)STAGES * UNITS * 16 * threads; }
+};
+
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE>
-__global__ void __launch_bounds__(G == 0 ? 512 : kThreads)
+__global__ void __launch_bounds__(threads_of(G))
     k_block_norm_fwd(const __grid_constant__ Params p) {
-  __shared__ float2 sums[8][2 * kMaxWarps];
+  using Ring = FwdRing<TS, TI, POST>;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
   Group g = make_group<G, VEC>(p, sums);
   const int C = p.C;
-  const bool flat = p.rows_of.flat, gated = POST && p.gate.p != nullptr;
+  const bool gated = POST && p.gate.p != nullptr;
+  const bool shared_gate = p.share > 1;
 
   // scale folded into the post-norm's parameters
-  float g1[kE], b1[kE], g2[kE], b2[kE];
+  V g1, b1, g2, b2;
   if (POST) {
-    float s[kE];
-    param<VEC>(p.scale, 1.f, g.lane, g.lanes, C, s);
-    param<VEC>(p.gamma_post, 1.f, g.lane, g.lanes, C, g1);
-    param<VEC>(p.beta_post, 0.f, g.lane, g.lanes, C, b1);
+    const V s = param<VEC>(p.scale, 1.f, g.lane, g.lanes, C);
+    g1 = param<VEC>(p.gamma_post, 1.f, g.lane, g.lanes, C);
+    b1 = param<VEC>(p.beta_post, 0.f, g.lane, g.lanes, C);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      g1[e] *= s[e];
-      b1[e] *= s[e];
+    for (int k = 0; k < kP; ++k) {
+      g1.p[k] = mul2(g1.p[k], s.p[k]);
+      b1.p[k] = mul2(b1.p[k], s.p[k]);
     }
   }
   if (PRE) {
-    param<VEC>(p.gamma_pre, 1.f, g.lane, g.lanes, C, g2);
-    param<VEC>(p.beta_pre, 0.f, g.lane, g.lanes, C, b2);
+    g2 = param<VEC>(p.gamma_pre, 1.f, g.lane, g.lanes, C);
+    b2 = param<VEC>(p.beta_pre, 0.f, g.lane, g.lanes, C);
   }
 
-  struct In {
-    Raw<TS, VEC> x;
-    Raw<TI, VEC> u, gate;
+  const uint32_t unit = blockDim.x * 16, stage_bytes = Ring::UNITS * unit;
+  const char* mine = smem + threadIdx.x * 16;
+  const uint32_t mine_s = smem_u32(mine);
+  auto gate_row = [&](uint32_t row, const RowPos& r) {
+    return shared_gate ? row_ptr(p.gate, row_pos(p.gate_of, row), p.gate_of) : row_ptr(p.gate, r, p.rows_of);
   };
-  auto fetch = [&](In& in, uint32_t row) {
-    const RowPos r = row_pos(p.rows_of, row);
-    if (!g.act) return;
-    load(in.x, row_ptr(p.x, r, flat), g.lane, g.lanes, C);
+  auto fetch = [&](uint32_t stage, uint32_t row) {
+    const uint32_t bytes = row < p.rows && g.act ? 16u : 0u;
+    const uint32_t at = bytes ? row : 0u;
+    const RowPos r = row_pos(p.rows_of, at);
+    uint32_t slot = mine_s + stage * stage_bytes;
+    const int lane = bytes ? g.lane : 0;
+    ring_put<TS>(slot, unit, row_ptr(p.x, r, p.rows_of), lane, bytes);
     if (POST) {
-      load(in.u, row_ptr(p.u, r, flat), g.lane, g.lanes, C);
-      if (gated) load(in.gate, row_ptr(p.gate, r, flat), g.lane, g.lanes, C);
+      slot += units<TS>() * unit;
+      ring_put<TI>(slot, unit, row_ptr(p.u, r, p.rows_of), lane, bytes);
+      if (gated) ring_put<TI>(slot + units<TI>() * unit, unit, gate_row(at, r), lane, bytes);
     }
   };
 
   // every thread of a warp (or of a row's warps) takes part in the sums, so
   // all groups of a CTA make the same number of turns
   const uint32_t step = gridDim.x * g.slots;
-  uint32_t first = blockIdx.x * g.slots;
-  In cur{}, nxt{};
-  if (first + g.slot < p.rows) fetch(cur, first + g.slot);
-  for (; first < p.rows; first += step) {
-    const uint32_t row = first + g.slot;
-    const bool live = row < p.rows;
-    if (row + step < p.rows) fetch(nxt, row + step);
-    const RowPos r = row_pos(p.rows_of, live ? row : 0);
-    float x[kE];
-    widen(cur.x, x);
-    if (POST) {
-      float u[kE];
-      widen(cur.u, u);
-      standardise<G, VEC, false>(u, u, g, p);
-      if (gated) {
-        float q[kE];
-        widen(cur.gate, q);
+  uint32_t row = blockIdx.x * g.slots + g.slot;
+  const uint32_t base = blockIdx.x * g.slots;
+  uint32_t turns = base < p.rows ? (p.rows - base + step - 1) / step : 0;
+  uint32_t stage = 0;
+  if constexpr (ring_of(G, VEC)) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) x[e] = fmaf(fmaf(u[e], g1[e], b1[e]), sigmoid(q[e]), x[e]);
+    for (int s = 0; s < Ring::STAGES - 1; ++s) {
+      fetch(s, row + s * step);
+      copies_close();
+    }
+  }
+  for (; turns > 0; --turns, row += step) {
+    const bool live = row < p.rows;
+    const RowPos r = row_pos(p.rows_of, live ? row : 0);
+    V x, u, q;
+    if constexpr (ring_of(G, VEC)) {
+      const uint32_t ahead = stage == 0 ? Ring::STAGES - 1 : stage - 1;
+      fetch(ahead, row + (Ring::STAGES - 1) * step);
+      copies_close();
+      copies_wait<Ring::STAGES - 1>();
+      const char* slot = mine + stage * stage_bytes;
+      x = ring_get<TS>(slot, unit);
+      if (POST) {
+        slot += units<TS>() * unit;
+        u = ring_get<TI>(slot, unit);
+        if (gated) q = ring_get<TI>(slot + units<TI>() * unit, unit);
+      }
+      stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
+    } else {
+      x = u = q = V{};
+      if (live && g.act) {
+        x = load<TS, VEC>(row_ptr(p.x, r, p.rows_of), g.lane, g.lanes, C);
+        if (POST) {
+          u = load<TI, VEC>(row_ptr(p.u, r, p.rows_of), g.lane, g.lanes, C);
+          if (gated) q = load<TI, VEC>(gate_row(row, r), g.lane, g.lanes, C);
+        }
+      }
+    }
+    if (POST) {
+      standardise<G, VEC>(u, g, p);
+      if (gated) {
+        sigmoid(q);
+#pragma unroll
+        for (int k = 0; k < kP; ++k) x.p[k] = fma2(fma2(u.p[k], g1.p[k], b1.p[k]), q.p[k], x.p[k]);
       } else {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) x[e] += fmaf(u[e], g1[e], b1[e]);
+        for (int k = 0; k < kP; ++k) x.p[k] = add2(x.p[k], fma2(u.p[k], g1.p[k], b1.p[k]));
       }
-      if (live && g.act)
-        Store<TS, VEC>::put(row_ptr(p.x1, r, flat), g.lane, g.lanes, C, x);
+      if (live && g.act) store<TS, VEC>(row_ptr(p.x1, r, p.rows_of), g.lane, g.lanes, C, x);
     }
     if (PRE) {
-      standardise<G, VEC, false>(x, x, g, p);
+      standardise<G, VEC>(x, g, p);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) x[e] = fmaf(x[e], g2[e], b2[e]);
-      if (live && g.act)
-        Store<TI, VEC>::put(row_ptr(p.y, r, flat), g.lane, g.lanes, C, x);
+      for (int k = 0; k < kP; ++k) x.p[k] = fma2(x.p[k], g2.p[k], b2.p[k]);
+      if (live && g.act) store<TI, VEC>(row_ptr(p.y, r, p.rows_of), g.lane, g.lanes, C, x);
     }
-    cur = nxt;
   }
+  if constexpr (ring_of(G, VEC)) copies_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
+// The rows that a group works on, turn by turn: every `hop`-th row of one
+// stretch, or (gate rows shared) of the stretches of its items.  All groups of
+// a CTA make the same number of turns; a group out of rows has row >= end.
+template <bool GROUPED>
+struct Walk {
+  uint32_t row, end, hop, left;  // left: turns left in this stretch
+  uint32_t item, gate_row;
+
+  __device__ __forceinline__ void open(const Params& p, const Group& g) {
+    if constexpr (GROUPED) {
+      left = 0;
+      if ((p.by_cta ? item : item - g.slot) >= p.items) return;
+      const bool mine = item < p.items;
+      gate_row = mine ? item / p.segs : 0;
+      const uint32_t seg = mine ? item - gate_row * p.segs : 0;
+      const uint32_t top = gate_row * p.share;
+      row = top + seg * p.seg_rows;
+      end = mine ? min(top + p.share, row + p.seg_rows) : row;
+      left = p.by_cta ? (end - row + g.slots - 1) / g.slots : p.seg_rows;
+      if (p.by_cta) row += g.slot;
+    }
+  }
+  __device__ __forceinline__ void start(const Params& p, const Group& g) {
+    if constexpr (GROUPED) {
+      hop = p.by_cta ? (uint32_t)g.slots : 1u;
+      item = p.by_cta ? blockIdx.x : blockIdx.x * g.slots + g.slot;
+      open(p, g);
+    } else {
+      hop = gridDim.x * g.slots;
+      const uint32_t base = blockIdx.x * g.slots;
+      row = base + g.slot;
+      end = p.rows;
+      left = base < p.rows ? (p.rows - base + hop - 1) / hop : 0;
+      item = gate_row = 0;
+    }
+  }
+  // To the next turn; true where a stretch ended.
+  __device__ __forceinline__ bool advance(const Params& p, const Group& g) {
+    row += hop;
+    if (--left > 0) return false;
+    if constexpr (GROUPED) {
+      item += gridDim.x * (p.by_cta ? 1u : (uint32_t)g.slots);
+      open(p, g);
+    }
+    return true;
+  }
+};
+
+template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED>
+struct BwdRing {
+  static constexpr int UNITS = units<TS>() * (PRE ? 2 : 1) + (PRE ? units<TI>() : 0) +
+                               (POST ? units<TI>() * (GROUPED ? 1 : 2) : 0);
+  // about 320 bytes in flight per thread, 16 warps per SM
+  static constexpr int STAGES = 320 / (UNITS * 16) < 2 ? 2 : 320 / (UNITS * 16) > 4 ? 4 : 320 / (UNITS * 16);
+  static constexpr size_t bytes(int threads) { return (size_t)STAGES * UNITS * 16 * threads; }
+};
+
+// Shared memory of the backward: a row of sums per group, and with a ring four
+// parameter vectors by thread of a group.
+constexpr size_t bwd_sums_bytes(int threads) { return (size_t)threads * kE * 4; }
+constexpr size_t bwd_params_bytes(int lanes) { return (size_t)lanes * kE * 4 * 4; }
+
 // GROUPED: gate rows shared by consecutive rows, whose gradients are summed.
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED>
-__global__ void __launch_bounds__(G == 0 ? 512 : kThreads)
+__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     k_block_norm_bwd(const __grid_constant__ Params p) {
-  __shared__ float2 sums[8][2 * kMaxWarps];
-  extern __shared__ float red[];  // [slots][lanes * 8]
+  using Ring = BwdRing<TS, TI, POST, PRE, GROUPED>;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
   Group g = make_group<G, VEC>(p, sums);
   const int C = p.C;
-  const bool flat = p.rows_of.flat;
   const bool gated = POST && (GROUPED || p.gate.p != nullptr);
+  const bool with_dx1 = p.dx1.p != nullptr;
 
-  float sc[kE], g1[kE], b1[kE], g2[kE];
-  if (POST) {
-    param<VEC>(p.scale, 1.f, g.lane, g.lanes, C, sc);
-    param<VEC>(p.gamma_post, 1.f, g.lane, g.lanes, C, g1);
-    param<VEC>(p.beta_post, 0.f, g.lane, g.lanes, C, b1);
-  }
-  if (PRE) param<VEC>(p.gamma_pre, 1.f, g.lane, g.lanes, C, g2);
-
-  float acc[5][kE];
-#pragma unroll
-  for (int k = 0; k < 5; ++k)
-#pragma unroll
-    for (int e = 0; e < kE; ++e) acc[k][e] = 0.f;
-  float q[kE], dg[kE];  // sigmoid(gate) and the gate's gradient
-#pragma unroll
-  for (int e = 0; e < kE; ++e) q[e] = 1.f;
-
-  struct In {
-    Raw<TS, VEC> x1, dx1;
-    Raw<TI, VEC> u, gate, dy;
+  constexpr bool RING = ring_of(G, VEC);
+  float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
+  // parameters: [vector][half][lane] float4, read back without bank conflicts
+  float4* const prm = reinterpret_cast<float4*>(smem + bwd_sums_bytes(blockDim.x));
+  char* const ring = reinterpret_cast<char*>(prm) + bwd_params_bytes(g.lanes);
+  auto read = [&](int k) {
+    const float* src = k == 0 ? p.scale : k == 1 ? p.gamma_post : k == 2 ? p.beta_post : p.gamma_pre;
+    return param<VEC>(src, k == 2 ? 0.f : 1.f, g.lane, g.lanes, C);
   };
-  auto fetch = [&](In& in, uint32_t row) {
-    const RowPos r = row_pos(p.rows_of, row);
-    if (!g.act) return;
-    if (p.dx1.p) load(in.dx1, row_ptr(p.dx1, r, flat), g.lane, g.lanes, C);
+  if (RING) {
+    if (g.slot == 0) {
+#pragma unroll
+      for (int k = POST ? 0 : 3; k < (PRE ? 4 : 3); ++k) {
+        const V v = read(k);
+        prm[(2 * k) * g.lanes + g.lane] = make_float4(v[0], v[1], v[2], v[3]);
+        prm[(2 * k + 1) * g.lanes + g.lane] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+    __syncthreads();
+  }
+  auto get = [&](int k) {
+    if constexpr (!RING) return read(k);
+    const float4 a = prm[(2 * k) * g.lanes + g.lane], b = prm[(2 * k + 1) * g.lanes + g.lane];
+    return V{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+  };
+
+  const V zero{{both(0.f), both(0.f), both(0.f), both(0.f)}};
+  V acc[5] = {zero, zero, zero, zero, zero};
+  V q{{both(1.f), both(1.f), both(1.f), both(1.f)}};  // sigmoid(gate)
+  V dg = zero;                                        // the gate's gradient
+
+  const uint32_t unit = blockDim.x * 16, stage_bytes = Ring::UNITS * unit;
+  const char* mine = ring + threadIdx.x * 16;
+  const uint32_t mine_s = smem_u32(mine);
+  // ring order: dx1, (x1, dy), (u, gate)
+  auto fetch = [&](uint32_t stage, uint32_t row, bool live) {
+    const uint32_t bytes = live && g.act ? 16u : 0u;
+    const RowPos r = row_pos(p.rows_of, bytes ? row : 0u);
+    const int lane = bytes ? g.lane : 0;
+    uint32_t slot = mine_s + stage * stage_bytes;
+    if (with_dx1) ring_put<TS>(slot, unit, row_ptr(p.dx1, r, p.rows_of), lane, bytes);
+    slot += units<TS>() * unit;
     if (PRE) {
-      load(in.x1, row_ptr(p.x, r, flat), g.lane, g.lanes, C);
-      load(in.dy, row_ptr(p.dy, r, flat), g.lane, g.lanes, C);
+      ring_put<TS>(slot, unit, row_ptr(p.x, r, p.rows_of), lane, bytes);
+      slot += units<TS>() * unit;
+      ring_put<TI>(slot, unit, row_ptr(p.dy, r, p.rows_of), lane, bytes);
+      slot += units<TI>() * unit;
     }
     if (POST) {
-      load(in.u, row_ptr(p.u, r, flat), g.lane, g.lanes, C);
-      if (!GROUPED && gated) load(in.gate, row_ptr(p.gate, r, flat), g.lane, g.lanes, C);
+      ring_put<TI>(slot, unit, row_ptr(p.u, r, p.rows_of), lane, bytes);
+      slot += units<TI>() * unit;
+      if (!GROUPED && gated) ring_put<TI>(slot, unit, row_ptr(p.gate, r, p.rows_of), lane, bytes);
     }
   };
 
-  // one row's gradients; a group without a row (live = false) only takes part
-  // in the sums, on the zeros that it holds
-  auto work = [&](In& in, uint32_t row, bool live) {
-    const RowPos r = row_pos(p.rows_of, live ? row : 0);
-    if (!live) in = In{};
-    float D[kE], u[kE], h[kE];
-    widen(in.dx1, D);
-    float2 rstd;
-    if (POST) widen(in.u, u);
-    if (PRE) {
-      widen(in.x1, h);
-      rstd = standardise<G, VEC, POST>(h, u, g, p);
-    } else {
-      rstd = standardise<G, VEC, false>(u, u, g, p);
-      rstd.y = rstd.x;
-    }
-    if (PRE) {
-      float dy[kE];
-      widen(in.dy, dy);
-      float2 s = make_float2(0.f, 0.f);
+  Walk<GROUPED> at, ahead;
+  at.start(p, g);
+  if constexpr (RING) {
+    ahead = at;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        acc[3][e] = fmaf(dy[e], h[e], acc[3][e]);
-        acc[4][e] += dy[e];
-        dy[e] *= g2[e];
-        s.x += dy[e];
-        s.y = fmaf(dy[e], h[e], s.y);
+    for (int s = 0; s < Ring::STAGES - 1; ++s) {
+      if (ahead.left > 0) {
+        fetch(s, ahead.row, ahead.row < ahead.end);
+        ahead.advance(p, g);
       }
-      if (!g.act) s = make_float2(0.f, 0.f);
-      s = group_sum<G>(s, g.sum);
-      const float m0 = p.rms ? 0.f : s.x * p.inv_c, m1 = s.y * p.inv_c;
+      copies_close();
+    }
+  }
+  uint32_t stage = 0;
+  bool fresh = true;  // a stretch begins
+  while (at.left > 0) {
+    const uint32_t row = at.row;
+    const bool live = row < at.end;  // a group without a row works on zeros
+    const RowPos r = row_pos(p.rows_of, live ? row : 0);
+    if constexpr (GROUPED) {
+      if (fresh) {
+        const RowPos rg = row_pos(p.gate_of, at.gate_row * p.share);
+        q = g.act ? load<TI, VEC>(row_ptr(p.gate, rg, p.gate_of), g.lane, g.lanes, C) : zero;
+        sigmoid(q);
+        dg = zero;
+      }
+    }
+    V D = zero, h, dy, u, gt;
+    if constexpr (RING) {
+      const uint32_t to = stage == 0 ? Ring::STAGES - 1 : stage - 1;
+      if (ahead.left > 0) {
+        fetch(to, ahead.row, ahead.row < ahead.end);
+        ahead.advance(p, g);
+      }
+      copies_close();
+      copies_wait<Ring::STAGES - 1>();
+      const char* slot = mine + stage * stage_bytes;
+      if (with_dx1) D = ring_get<TS>(slot, unit);
+      slot += units<TS>() * unit;
+      if (PRE) {
+        h = ring_get<TS>(slot, unit);
+        slot += units<TS>() * unit;
+        dy = ring_get<TI>(slot, unit);
+        slot += units<TI>() * unit;
+      }
+      if (POST) {
+        u = ring_get<TI>(slot, unit);
+        if (!GROUPED && gated) gt = ring_get<TI>(slot + units<TI>() * unit, unit);
+      }
+      stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
+    } else {
+      auto get_row = [&](const Operand& o, auto type) {
+        return live && g.act ? load<decltype(type), VEC>(row_ptr(o, r, p.rows_of), g.lane, g.lanes, C) : zero;
+      };
+      if (with_dx1) D = get_row(p.dx1, TS(0.f));
+      if (PRE) {
+        h = get_row(p.x, TS(0.f));
+        dy = get_row(p.dy, TI(0.f));
+      }
+      if (POST) {
+        u = get_row(p.u, TI(0.f));
+        if (!GROUPED && gated) gt = get_row(p.gate, TI(0.f));
+      }
+    }
+
+    float2 rstd = both(0.f);  // of x1 and of u
+    if (PRE && POST) rstd = standardise<G, VEC>(h, u, g, p);
+    else if (PRE) rstd.x = standardise<G, VEC>(h, g, p);
+    else rstd.y = standardise<G, VEC>(u, g, p);
+    if (PRE) {
+      const V g2 = get(3);
 #pragma unroll
-      for (int e = 0; e < kE; ++e)
-        D[e] = fmaf(rstd.x, fmaf(-m1, h[e], dy[e] - m0), D[e]);
-      if (live && g.act)
-        Store<TS, VEC>::put(row_ptr(p.dx, r, flat), g.lane, g.lanes, C, D);
+      for (int k = 0; k < kP; ++k) {
+        acc[3].p[k] = fma2(dy.p[k], h.p[k], acc[3].p[k]);
+        acc[4].p[k] = add2(acc[4].p[k], dy.p[k]);
+        dy.p[k] = mul2(dy.p[k], g2.p[k]);
+      }
+      float2 s = make_float2(sum(dy), dot(dy, h));
+      s = group_sum<G>(g.act ? s : both(0.f), g);
+      const float2 m0 = both(p.rms ? 0.f : -s.x * p.inv_c), m1 = both(-s.y * p.inv_c), rs = both(rstd.x);
+#pragma unroll
+      for (int k = 0; k < kP; ++k)
+        D.p[k] = fma2(rs, fma2(m1, h.p[k], add2(dy.p[k], m0)), D.p[k]);
+      if (live && g.act) store<TS, VEC>(row_ptr(p.dx, r, p.rows_of), g.lane, g.lanes, C, D);
     }
     if (POST) {
       if (!GROUPED && gated) {
-        float v[kE];
-        widen(in.gate, v);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) q[e] = sigmoid(v[e]);
+        q = gt;
+        sigmoid(q);
       }
-      float b[kE];
-      float2 s = make_float2(0.f, 0.f);
+      const V sc = get(0), g1 = get(1), b1 = get(2);
+      V b;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const float w = fmaf(u[e], g1[e], b1[e]);
-        const float dq = D[e] * q[e];
-        acc[0][e] = fmaf(dq, w, acc[0][e]);
-        const float en = dq * sc[e];
+      for (int k = 0; k < kP; ++k) {
+        const float2 w = fma2(u.p[k], g1.p[k], b1.p[k]);
+        const float2 dq = mul2(D.p[k], q.p[k]);
+        acc[0].p[k] = fma2(dq, w, acc[0].p[k]);
+        const float2 e = mul2(dq, sc.p[k]);
         if (GROUPED)
-          dg[e] = fmaf(en, w, dg[e]);  // (1 - q) is applied once, at the end
+          dg.p[k] = fma2(e, w, dg.p[k]);  // (1 - q) is applied once, at the end
         else
-          dg[e] = en * w * (1.f - q[e]);
-        acc[1][e] = fmaf(en, u[e], acc[1][e]);
-        acc[2][e] += en;
-        b[e] = en * g1[e];
-        s.x += b[e];
-        s.y = fmaf(b[e], u[e], s.y);
+          dg.p[k] = mul2(mul2(e, w), fma2(q.p[k], both(-1.f), both(1.f)));
+        acc[1].p[k] = fma2(e, u.p[k], acc[1].p[k]);
+        acc[2].p[k] = add2(acc[2].p[k], e);
+        b.p[k] = mul2(e, g1.p[k]);
       }
-      if (!g.act) s = make_float2(0.f, 0.f);
-      s = group_sum<G>(s, g.sum);
-      const float m0 = p.rms ? 0.f : s.x * p.inv_c, m1 = s.y * p.inv_c;
+      float2 s = make_float2(sum(b), dot(b, u));
+      s = group_sum<G>(g.act ? s : both(0.f), g);
+      const float2 m0 = both(p.rms ? 0.f : -s.x * p.inv_c), m1 = both(-s.y * p.inv_c), rs = both(rstd.y);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) b[e] = rstd.y * fmaf(-m1, u[e], b[e] - m0);
+      for (int k = 0; k < kP; ++k) b.p[k] = mul2(rs, fma2(m1, u.p[k], add2(b.p[k], m0)));
       if (live && g.act) {
-        Store<TI, VEC>::put(row_ptr(p.du, r, flat), g.lane, g.lanes, C, b);
-        if (!GROUPED && gated)
-          Store<TI, VEC>::put(row_ptr(p.dgate, r, flat), g.lane, g.lanes, C, dg);
+        store<TI, VEC>(row_ptr(p.du, r, p.rows_of), g.lane, g.lanes, C, b);
+        if (!GROUPED && gated) store<TI, VEC>(row_ptr(p.dgate, r, p.rows_of), g.lane, g.lanes, C, dg);
       }
     }
-  };
 
-  if (!GROUPED) {
-    const uint32_t step = gridDim.x * g.slots;
-    uint32_t first = blockIdx.x * g.slots;
-    In cur{}, nxt{};
-    if (first + g.slot < p.rows) fetch(cur, first + g.slot);
-    for (; first < p.rows; first += step) {
-      const uint32_t row = first + g.slot;
-      if (row + step < p.rows) fetch(nxt, row + step);
-      work(cur, row, row < p.rows);
-      cur = nxt;
-    }
-  } else {
-    // items of consecutive rows under one gate row: spread over the CTA's
-    // groups, or walked by one group each
-    const uint32_t per_cta = p.by_cta ? 1u : (uint32_t)g.slots;
-    const uint32_t hop = p.by_cta ? (uint32_t)g.slots : 1u;
-    for (uint32_t first = blockIdx.x * per_cta; first < p.items; first += gridDim.x * per_cta) {
-      const uint32_t item = p.by_cta ? first : first + g.slot;
-      const bool mine = item < p.items;
-      const uint32_t gate_row = mine ? item / p.segs : 0;
-      const uint32_t seg = mine ? item - gate_row * p.segs : 0;
-      const uint32_t begin = gate_row * p.share + seg * p.seg_rows;
-      const uint32_t end = mine ? min(gate_row * p.share + p.share, begin + p.seg_rows) : begin;
-      const RowPos at = row_pos(p.rows_of, gate_row * p.share);
-      Raw<TI, VEC> raw{};
-      if (g.act) load(raw, row_ptr(p.gate, at, flat), g.lane, g.lanes, C);
-      widen(raw, q);
+    const Walk<GROUPED> was = at;
+    fresh = at.advance(p, g);
+    if constexpr (GROUPED) {
+      if (fresh) {
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        q[e] = sigmoid(q[e]);
-        dg[e] = 0.f;
-      }
-      uint32_t row = begin + (p.by_cta ? (uint32_t)g.slot : 0u);
-      In cur{}, nxt{};
-      if (row < end) fetch(cur, row);
-      // the same number of turns for every group of the CTA
-      for (uint32_t t = 0; t < p.seg_rows; t += hop, row += hop) {
-        if (row + hop < end) fetch(nxt, row + hop);
-        work(cur, row, row < end);
-        cur = nxt;
-      }
+        for (int k = 0; k < kP; ++k) dg.p[k] = mul2(dg.p[k], fma2(q.p[k], both(-1.f), both(1.f)));
+        const bool owns = p.by_cta || was.item < p.items;
+        if (p.by_cta && g.slots > 1) {
+          const int width = g.lanes * kE;
+          __syncthreads();
 #pragma unroll
-      for (int e = 0; e < kE; ++e) dg[e] *= 1.f - q[e];
-      if (p.by_cta && g.slots > 1) {
-        const int width = g.lanes * kE;
-        __syncthreads();
+          for (int e = 0; e < kE; ++e) red[g.slot * width + channel<VEC>(g.lane, g.lanes, e)] = dg[e];
+          __syncthreads();
+          if (g.slot == 0) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e)
-          red[g.slot * width + channel<VEC>(g.lane, g.lanes, e)] = dg[e];
-        __syncthreads();
-        if (g.slot == 0) {
-#pragma unroll
-          for (int e = 0; e < kE; ++e) {
-            float s = 0.f;
-            for (int i = 0; i < g.slots; ++i) s += red[i * width + channel<VEC>(g.lane, g.lanes, e)];
-            dg[e] = s;
+            for (int e = 0; e < kE; ++e) {
+              float s = 0.f;
+              for (int i = 0; i < g.slots; ++i) s += red[i * width + channel<VEC>(g.lane, g.lanes, e)];
+              dg[e] = s;
+            }
           }
         }
-      }
-      if (mine && g.act && (!p.by_cta || g.slot == 0)) {
-        if (p.segs == 1)
-          Store<TI, VEC>::put(row_ptr(p.dgate, at, flat), g.lane, g.lanes, C, dg);
-        else
-          Store<float, VEC>::put(reinterpret_cast<char*>(p.gate_part + (size_t)item * C), g.lane,
-                                 g.lanes, C, dg);
+        if (owns && g.act && (!p.by_cta || g.slot == 0)) {
+          if (p.segs == 1) {
+            const RowPos rg = row_pos(p.gate_of, was.gate_row * p.share);
+            store<TI, VEC>(row_ptr(p.dgate, rg, p.gate_of), g.lane, g.lanes, C, dg);
+          } else {
+            store<float, VEC>(reinterpret_cast<char*>(p.gate_part + (size_t)was.item * C), g.lane, g.lanes, C, dg);
+          }
+        }
       }
     }
   }
@@ -612,8 +768,7 @@ __global__ void __launch_bounds__(G == 0 ? 512 : kThreads)
     if (p.out[k] == nullptr) continue;
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kE; ++e)
-      red[g.slot * width + channel<VEC>(g.lane, g.lanes, e)] = acc[k][e];
+    for (int e = 0; e < kE; ++e) red[g.slot * width + channel<VEC>(g.lane, g.lanes, e)] = acc[k][e];
     __syncthreads();
     float* dst = gridDim.x == 1 ? p.out[k] : p.part + ((size_t)blockIdx.x * 5 + k) * C;
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
@@ -627,10 +782,12 @@ __global__ void __launch_bounds__(G == 0 ? 512 : kThreads)
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// Resident CTAs of a kernel per SM times the SMs, looked up once per device.
+// Resident CTAs of a kernel per SM times the SMs, looked up once per device
+// and CTA size; `most` is the shared memory of its largest CTA.
 template <typename K>
-cudaError_t resident_ctas(K kernel, int threads, size_t smem, std::atomic<int> (&cache)[64][17],
-                          int key, int* n) {
+cudaError_t resident_ctas(K kernel, int threads, size_t smem, size_t most,
+                          std::atomic<int> (&cache)[64][17], int* n) {
+  const int key = threads / 32;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -638,7 +795,8 @@ cudaError_t resident_ctas(K kernel, int threads, size_t smem, std::atomic<int> (
   else *n = 0;
   if (*n > 0) return cudaSuccess;
   int sms = 0, per = 0;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
   if (e != cudaSuccess) return e;
   *n = std::max(1, sms) * std::max(1, per);
@@ -646,88 +804,99 @@ cudaError_t resident_ctas(K kernel, int threads, size_t smem, std::atomic<int> (
   return cudaSuccess;
 }
 
-// The launch's row space.  Axes along which the gate does not move come last,
-// the others by the stride of the first operand given; neighbouring axes that every
-// operand walks as one become one (never across the border between the two
-// kinds, which is where a gate row's rows begin).
-struct Axes {
-  uint32_t n[3];
-  int64_t s[3][10];
+// The launch's row space.  Axes along which the gate repeats its rows come
+// last, so that a gate row's rows are consecutive; the others are ordered by
+// the stride of the first operand given.
+struct Axis {
+  uint32_t n;
+  int64_t s[10];
+  bool shared;
+};
+struct Space {
+  Axis ax[3];
+  int count;
   uint32_t share;
 };
-inline Axes order_axes(const int (&n)[3], const RowOperand* const* ops, int count, int gate_at) {
-  struct Axis {
-    uint32_t n;
-    int64_t s[10];
-    bool shared;
-  };
-  Axis ax[3];
-  int k = 0;
+inline Space order_axes(const int (&n)[3], const RowOperand* const* ops, int count, int gate_at) {
+  Space sp{};
   for (int d = 0; d < 3; ++d) {
     if (n[d] == 1) continue;
-    ax[k].n = (uint32_t)n[d];
-    for (int i = 0; i < count; ++i) ax[k].s[i] = ops[i]->p ? ops[i]->s[d] : 0;
-    ax[k].shared = gate_at >= 0 && ax[k].s[gate_at] == 0;
-    ++k;
+    Axis& a = sp.ax[sp.count++];
+    a.n = (uint32_t)n[d];
+    for (int i = 0; i < count; ++i) a.s[i] = ops[i]->p ? ops[i]->s[d] : 0;
+    a.shared = gate_at >= 0 && a.s[gate_at] == 0;
   }
   int lead = 0;
   while (lead + 1 < count && !ops[lead]->p) ++lead;
-  std::stable_sort(ax, ax + k, [lead](const Axis& a, const Axis& b) {
+  std::stable_sort(sp.ax, sp.ax + sp.count, [lead](const Axis& a, const Axis& b) {
     if (a.shared != b.shared) return !a.shared;
     return a.s[lead] > b.s[lead];
   });
-  Axes out{};
-  out.share = 1;
-  for (int d = 0; d < k; ++d)
-    if (ax[d].shared) out.share *= ax[d].n;
+  sp.share = 1;
+  for (int d = 0; d < sp.count; ++d)
+    if (sp.ax[d].shared) sp.share *= sp.ax[d].n;
+  return sp;
+}
+
+// Three axes (the innermost last) of the operands in `use`: neighbouring axes
+// that all of them walk as one become one.
+inline Rows join_axes(const Space& sp, const RowOperand* const* ops, Operand* const* dst,
+                      const int* esize, int count, const bool* use) {
+  Axis ax[3];
   int m = 0;
-  for (int d = 0; d < k; ++d) {
-    bool join = m > 0 && ax[m - 1].shared == ax[d].shared;
+  for (int d = 0; d < sp.count; ++d) {
+    bool join = m > 0;
     for (int i = 0; join && i < count; ++i)
-      if (ops[i]->p) join = ax[m - 1].s[i] == ax[d].s[i] * (int64_t)ax[d].n;
+      if (use[i] && ops[i]->p) join = ax[m - 1].s[i] == sp.ax[d].s[i] * (int64_t)sp.ax[d].n;
     if (join) {
       const uint32_t outer = ax[m - 1].n;
-      ax[m - 1] = ax[d];
-      ax[m - 1].n = outer * ax[d].n;
+      ax[m - 1] = sp.ax[d];
+      ax[m - 1].n = outer * sp.ax[d].n;
     } else {
-      ax[m++] = ax[d];
+      ax[m++] = sp.ax[d];
     }
   }
-  for (int d = 0; d < 3; ++d) {  // right-aligned: the innermost axis is [2]
+  uint32_t n[3];
+  for (int d = 0; d < 3; ++d) {  // right-aligned
     const int from = d - (3 - m);
-    out.n[d] = from >= 0 ? ax[from].n : 1u;
-    for (int i = 0; i < count; ++i) out.s[d][i] = from >= 0 ? ax[from].s[i] : 0;
+    n[d] = from >= 0 ? ax[from].n : 1u;
+    for (int i = 0; i < count; ++i) {
+      if (!use[i] || !ops[i]->p) continue;
+      int64_t& s = d == 0 ? dst[i]->s0 : d == 1 ? dst[i]->s1 : dst[i]->s2;
+      s = from >= 0 ? ax[from].s[i] * esize[i] : 0;
+    }
   }
-  return out;
+  return Rows{fast_div(n[2]), fast_div(n[1]), n[0] == 1 && n[1] == 1};
 }
 
 struct Plan {
   Params p;
-  int g;        // lanes of a row's group: 8, 16, 32, or 0 for several warps
+  int g;        // lanes of a row's group: 8, 16, 32, kWarps or kPlain
   bool vec;
   int threads, slots;
 };
 
 // Sizes and operands, for both directions: `ops` go to `dst` (parts of pl.p),
-// their element sizes in `esize`.
+// their element sizes in `esize`; the gate and its gradient (`is_gate`) have
+// row axes of their own where gate rows are shared.
 inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Operand* const* dst,
-                      const int* esize, int count, int gate_at, Plan& pl) {
+                      const int* esize, const bool* is_gate, int count, int gate_at, Plan& pl) {
   Params& p = pl.p;
-  const Axes ax = order_axes(c.n, ops, count, gate_at);
-  p.rows = ax.n[0] * ax.n[1] * ax.n[2];
-  p.rows_of.d2 = fast_div(ax.n[2]);
-  p.rows_of.d1 = fast_div(ax.n[1]);
-  p.rows_of.flat = ax.n[0] == 1 && ax.n[1] == 1;
-  p.share = ax.share;
+  const Space sp = order_axes(c.n, ops, count, c.gate.p ? gate_at : -1);
+  p.share = sp.share;
+  bool rows[10], gates[10];
+  for (int i = 0; i < count; ++i) {
+    gates[i] = is_gate[i] && sp.share > 1;
+    rows[i] = !gates[i];
+  }
+  p.rows_of = join_axes(sp, ops, dst, esize, count, rows);
+  p.gate_of = join_axes(sp, ops, dst, esize, count, gates);
+  p.rows = (uint32_t)((int64_t)c.n[0] * c.n[1] * c.n[2]);
   pl.vec = c.C % kE == 0;
   for (int i = 0; i < count; ++i) {
     Operand& o = *dst[i];
     o.p = static_cast<char*>(ops[i]->p);
-    if (!o.p) continue;
-    o.s0 = ax.s[0][i] * esize[i];
-    o.s1 = ax.s[1][i] * esize[i];
-    o.s2 = ax.s[2][i] * esize[i];
-    if (reinterpret_cast<uintptr_t>(o.p) % 16 || o.s0 % 16 || o.s1 % 16 || o.s2 % 16) pl.vec = false;
+    if (o.p && (reinterpret_cast<uintptr_t>(o.p) % 16 || o.s0 % 16 || o.s1 % 16 || o.s2 % 16)) pl.vec = false;
   }
   p.C = c.C;
   p.rms = c.rms;
@@ -744,7 +913,7 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     p.lanes = pl.g;
     pl.threads = kThreads;
   } else {
-    pl.g = 0;
+    pl.g = pl.vec && need <= kThreads ? kWarps : kPlain;
     const int warps = (need + 31) / 32;
     p.lanes = warps * 32;
     pl.threads = p.lanes * std::max(1, kThreads / 32 / warps);
@@ -781,7 +950,7 @@ __global__ void __launch_bounds__(256) k_block_norm_reduce(const __grid_constant
     if (is_param) {
       p.out[what][c] = s;
     } else {
-      char* row = row_ptr(p.dgate, row_pos(p.rows_of, (uint32_t)what * p.share), p.rows_of.flat);
+      char* row = row_ptr(p.dgate, row_pos(p.gate_of, (uint32_t)what * p.share), p.gate_of);
       reinterpret_cast<TI*>(row)[c] = static_cast<TI>(s);
     }
   }
@@ -791,11 +960,14 @@ template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE>
 cudaError_t launch_fwd(const Plan& pl, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
   auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE>;
+  using Ring = FwdRing<TS, TI, POST>;
+  constexpr bool RING = ring_of(G, VEC);
+  const size_t smem = RING ? Ring::bytes(pl.threads) : 0;
   int ctas = 0;
-  cudaError_t e = resident_ctas(kern, pl.threads, 0, cache, pl.threads / 32, &ctas);
+  cudaError_t e = resident_ctas(kern, pl.threads, smem, RING ? Ring::bytes(kThreads) : 0, cache, &ctas);
   if (e != cudaSuccess) return e;
   const unsigned need = (pl.p.rows + pl.slots - 1) / pl.slots;
-  kern<<<std::min<unsigned>(need, (unsigned)ctas), pl.threads, 0, st>>>(pl.p);
+  kern<<<std::min<unsigned>(need, (unsigned)ctas), pl.threads, smem, st>>>(pl.p);
   return cudaGetLastError();
 }
 
@@ -804,9 +976,14 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
   auto kern = k_block_norm_bwd<TS, TI, G, VEC, POST, PRE, GROUPED>;
   Params& p = pl.p;
-  const size_t smem = (size_t)pl.slots * p.lanes * kE * sizeof(float);
+  using Ring = BwdRing<TS, TI, POST, PRE, GROUPED>;
+  constexpr bool RING = ring_of(G, VEC);
+  const size_t smem = bwd_sums_bytes(pl.threads) + (RING ? bwd_params_bytes(p.lanes) + Ring::bytes(pl.threads) : 0);
+  constexpr size_t most =
+      bwd_sums_bytes(threads_of(G)) + (RING ? bwd_params_bytes(kThreads) + Ring::bytes(kThreads) : 0);
+  static_assert(most <= 227 * 1024 - 4096, "shared memory");
   int ctas = 0;
-  cudaError_t e = resident_ctas(kern, pl.threads, smem, cache, pl.threads / 32, &ctas);
+  cudaError_t e = resident_ctas(kern, pl.threads, smem, most, cache, &ctas);
   if (e != cudaSuccess) return e;
   ctas = std::min(ctas, kNormMaxCtas);
   unsigned need = (p.rows + pl.slots - 1) / pl.slots;
@@ -847,30 +1024,30 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
 
 template <typename TS, typename TI, bool POST, bool PRE>
 cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
-  if (pl.vec) {
-    switch (pl.g) {
-      case 8: return launch_fwd<TS, TI, 8, true, POST, PRE>(pl, st);
-      case 16: return launch_fwd<TS, TI, 16, true, POST, PRE>(pl, st);
-      case 32: return launch_fwd<TS, TI, 32, true, POST, PRE>(pl, st);
-      default: return launch_fwd<TS, TI, 0, true, POST, PRE>(pl, st);
-    }
+  if (!pl.vec)
+    return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE>(pl, st)
+                      : launch_fwd<TS, TI, kPlain, false, POST, PRE>(pl, st);
+  switch (pl.g) {
+    case 8: return launch_fwd<TS, TI, 8, true, POST, PRE>(pl, st);
+    case 16: return launch_fwd<TS, TI, 16, true, POST, PRE>(pl, st);
+    case 32: return launch_fwd<TS, TI, 32, true, POST, PRE>(pl, st);
+    case kWarps: return launch_fwd<TS, TI, kWarps, true, POST, PRE>(pl, st);
+    default: return launch_fwd<TS, TI, kPlain, true, POST, PRE>(pl, st);
   }
-  return pl.g ? launch_fwd<TS, TI, 32, false, POST, PRE>(pl, st)
-              : launch_fwd<TS, TI, 0, false, POST, PRE>(pl, st);
 }
 
 template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED>
 cudaError_t dispatch_bwd(const Plan& pl, float* ws, cudaStream_t st) {
-  if (pl.vec) {
-    switch (pl.g) {
-      case 8: return launch_bwd<TS, TI, 8, true, POST, PRE, GROUPED>(pl, ws, st);
-      case 16: return launch_bwd<TS, TI, 16, true, POST, PRE, GROUPED>(pl, ws, st);
-      case 32: return launch_bwd<TS, TI, 32, true, POST, PRE, GROUPED>(pl, ws, st);
-      default: return launch_bwd<TS, TI, 0, true, POST, PRE, GROUPED>(pl, ws, st);
-    }
+  if (!pl.vec)
+    return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED>(pl, ws, st)
+                      : launch_bwd<TS, TI, kPlain, false, POST, PRE, GROUPED>(pl, ws, st);
+  switch (pl.g) {
+    case 8: return launch_bwd<TS, TI, 8, true, POST, PRE, GROUPED>(pl, ws, st);
+    case 16: return launch_bwd<TS, TI, 16, true, POST, PRE, GROUPED>(pl, ws, st);
+    case 32: return launch_bwd<TS, TI, 32, true, POST, PRE, GROUPED>(pl, ws, st);
+    case kWarps: return launch_bwd<TS, TI, kWarps, true, POST, PRE, GROUPED>(pl, ws, st);
+    default: return launch_bwd<TS, TI, kPlain, true, POST, PRE, GROUPED>(pl, ws, st);
   }
-  return pl.g ? launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED>(pl, ws, st)
-              : launch_bwd<TS, TI, 0, false, POST, PRE, GROUPED>(pl, ws, st);
 }
 
 template <typename TS, typename TI>
@@ -881,7 +1058,8 @@ cudaError_t run_fwd(const BlockNormCall& c, cudaStream_t st) {
   const RowOperand* ops[] = {&c.x, &c.u, &c.gate, &c.x1, &c.y};
   Operand* dst[] = {&p.x, &p.u, &p.gate, &p.x1, &p.y};
   const int es[] = {S, I, I, S, I};
-  make_plan(c, ops, dst, es, 5, -1, pl);
+  const bool gates[] = {false, false, true, false, false};
+  make_plan(c, ops, dst, es, gates, 5, 2, pl);
   if (c.u.p && c.y.p) return dispatch_fwd<TS, TI, true, true>(pl, st);
   if (c.u.p) return dispatch_fwd<TS, TI, true, false>(pl, st);
   return dispatch_fwd<TS, TI, false, true>(pl, st);
@@ -895,7 +1073,8 @@ cudaError_t run_bwd(const BlockNormCall& c, cudaStream_t st) {
   const RowOperand* ops[] = {&c.dx1, &c.x, &c.u, &c.gate, &c.dy, &c.dx, &c.du, &c.dgate};
   Operand* dst[] = {&p.dx1, &p.x, &p.u, &p.gate, &p.dy, &p.dx, &p.du, &p.dgate};
   const int es[] = {S, S, I, I, I, S, I, I};
-  make_plan(c, ops, dst, es, 8, c.gate.p ? 3 : -1, pl);
+  const bool gates[] = {false, false, false, true, false, false, false, true};
+  make_plan(c, ops, dst, es, gates, 8, 3, pl);
   p.out[0] = c.dscale;
   p.out[1] = c.dgamma_post;
   p.out[2] = c.dbeta_post;

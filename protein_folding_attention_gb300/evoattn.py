@@ -257,37 +257,61 @@ def transition(z, gamma, beta, w1, w2, eps=1e-5, o=None, w_o=None, out=None, str
     return out
 
 
-def _rows4(t, shape, dtype, device, name):
-    """Checks a [B, I, J, C] operand; returns its address and strides."""
+_strides = {}  # stride tuple -> int64_t[4], so that a call does not build its arrays anew
+
+
+def _strides4(t):
+    s = t.stride()
+    a = _strides.get(s)
+    if a is None:
+        if len(_strides) > 4096:
+            _strides.clear()
+        a = _strides[s] = _I64_4(*s)
+    return a
+
+
+def _rows4(t, shape, dtype, index, name):
+    """Checks a [B, I, J, C] operand on device `index`; returns its address
+    and strides."""
     if t is None:
         return None, None
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, "
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{index}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    return t.data_ptr(), _I64_4(*t.stride())
+    return t.data_ptr(), _strides4(t)
 
 
-def _vec(t, C, device, name):
+def _vec(t, C, index, name):
     """Checks a [C] fp32 parameter; returns its address."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.shape != (C,) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous fp32 [{C}] tensor on {device}")
+    if t.dtype is not torch.float32 or t.shape != (C,) or t.get_device() != index or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous fp32 [{C}] tensor on cuda:{index}")
     return t.data_ptr()
 
 
 def _on_device(t):
-    """The tensor's device, which has to be the current one (the library
-    enqueues on the current device's streams)."""
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    """Index of the tensor's device, which has to be the current one (the
+    library enqueues on the current device's streams)."""
+    index = t.get_device()
+    if index < 0 or index != torch.cuda.current_device():
         raise ValueError(f"tensors on {t.device}: a CUDA tensor on the current device is needed")
-    return t.device
+    return index
+
+
+def _raw_stream(stream, index):
+    """The cudaStream_t of `stream` (None: the current one of device `index`)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+_HERE_AND_NOW = contextlib.nullcontext()
 
 
 def _allocate_on(stream):
     """Tensors made inside belong to `stream` (None: the current one), so that
     a workspace is not reused before the kernels on that stream are done."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE_AND_NOW if stream is None else torch.cuda.stream(stream)
 
 
 def _expanded(gate, shape):
@@ -330,7 +354,8 @@ def block_norm(x, u=None, gate=None, scale=None, gamma_post=None, beta_post=None
             y = torch.empty_like(x, dtype=io)
     if not pre and y is not None:
         raise ValueError("y without pre")
-    gate = _expanded(gate, shape)
+    if gate is not None:
+        gate = _expanded(gate, shape)
     out = x1 if u is not None else None
     st = load().evoattn_block_norm(
         *_rows4(x, shape, x.dtype, dev, "x"), *_rows4(u, shape, io, dev, "u"),
@@ -338,8 +363,9 @@ def block_norm(x, u=None, gate=None, scale=None, gamma_post=None, beta_post=None
         _vec(gamma_post, C, dev, "gamma_post"), _vec(beta_post, C, dev, "beta_post"),
         _vec(gamma_pre, C, dev, "gamma_pre"), _vec(beta_pre, C, dev, "beta_pre"),
         *_rows4(out, shape, x.dtype, dev, "x1"), *_rows4(y, shape, io, dev, "y"),
-        *shape, _dtype_code(x), F32 if io == torch.float32 else BF16, kind, eps, _stream(stream))
-    _check(st, "evoattn_block_norm")
+        *shape, _dtype_code(x), F32 if io is torch.float32 else BF16, kind, eps, _raw_stream(stream, dev))
+    if st != OK:
+        _check(st, "evoattn_block_norm")
     return (x if u is None else x1), y
 
 
@@ -369,7 +395,7 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
     need = lib.evoattn_block_norm_bwd_workspace_size(C)
     if gate is not None and any(n > 1 and s == 0 for n, s in zip(gate.shape, gate.stride())):
         gate = gate.contiguous()  # an expanded view: its gradient is that of each row by itself
-    full = _expanded(gate, shape)
+    full = _expanded(gate, shape) if gate is not None else None
     out = {}
     with _allocate_on(stream):
         if dy is not None:
@@ -383,11 +409,11 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
                   ("dgamma_pre", gamma_pre), ("dbeta_pre", beta_pre))
         given = [name for name, t in params if t is not None]
         if given:
-            for name, row in zip(given, torch.empty((len(given), C), device=dev,
+            for name, row in zip(given, torch.empty((len(given), C), device=lead.device,
                                                     dtype=torch.float32).unbind(0)):
                 out[name] = row
         if workspace is None:
-            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+            workspace = torch.empty(need, device=lead.device, dtype=torch.uint8)
     _vec(beta_pre, C, dev, "beta_pre")
     get = out.get
     st = lib.evoattn_block_norm_bwd(
@@ -397,11 +423,12 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
         _vec(gamma_post, C, dev, "gamma_post"), _vec(beta_post, C, dev, "beta_post"),
         _vec(gamma_pre, C, dev, "gamma_pre"),
         *_rows4(get("dx"), shape, lead.dtype, dev, "dx"), *_rows4(du, shape, io, dev, "du"),
-        *_rows4(_expanded(dgate, shape), shape, io, dev, "dgate"),
-        *(_ptr(get(name)) for name, _ in params), *shape, _dtype_code(lead),
-        F32 if io == torch.float32 else BF16, kind, eps, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "evoattn_block_norm_bwd")
+        *_rows4(dgate if dgate is None else _expanded(dgate, shape), shape, io, dev, "dgate"),
+        *[None if t is None else get(name).data_ptr() for name, t in params], *shape, _dtype_code(lead),
+        F32 if io is torch.float32 else BF16, kind, eps, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+    if st != OK:
+        _check(st, "evoattn_block_norm_bwd")
     if dy is None:
         out["dx"] = dx1
     return out
@@ -453,7 +480,8 @@ class AdamW:
         decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
         if len(decay) != n:
             raise ValueError("one weight_decay, or one per parameter")
-        self.device = dev = _on_device(self.params[0])
+        self._index = _on_device(self.params[0])
+        self.device = dev = self.params[0].device
         self.lr, self.betas, self.eps, self.state_bits = lr, betas, eps, state_bits
         self.offsets, total = [], 0
         for p in self.params:
@@ -528,7 +556,7 @@ class AdamW:
         if grads is not None:
             self._bind(list(grads))
         lib, n = load(), len(self.params)
-        st = _stream(stream)
+        st = _raw_stream(stream, self._index)
         if stream is not None:  # not to be reused before that stream is done with them
             for t in (self._state, self._workspace, self.exp_avg, self.exp_avg_sq,
                       self.exp_avg_scale, self.exp_avg_sq_scale):
@@ -559,7 +587,7 @@ def grad_norm(grads, stream=None):
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
-    dev = _on_device(grads[0])
+    index, dev = _on_device(grads[0]), grads[0].device
     for i, g in enumerate(grads):
         if g.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError(f"gradient {i}: bf16 or fp32, got {g.dtype}")
@@ -569,7 +597,8 @@ def grad_norm(grads, stream=None):
         state = torch.zeros(8, device=dev, dtype=torch.int32)
         ws = torch.empty(lib.evoattn_grad_norm_workspace_size(len(grads)), device=dev, dtype=torch.uint8)
     _check(lib.evoattn_grad_norm(_grad_table(grads), len(grads), float("inf"), state.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), _stream(stream)), "evoattn_grad_norm")
+                                 ws.data_ptr(), ws.numel(), _raw_stream(stream, index)),
+           "evoattn_grad_norm")
     return state[2:3].view(torch.float32)[0]
 
 
