@@ -105,6 +105,7 @@ struct Params {
   Rows rows_of;   // row axes of every operand
   Rows gate_of;   // row axes of gate and dgate where gate rows are shared
   uint32_t rows;
+  uint32_t stride_s, stride_i;  // DENSE: bytes between rows of the stream's and the block's operands
   int C;
   int lanes;      // threads of a row's group (a multiple of 32 where it spans warps)
   bool rms;
@@ -118,6 +119,31 @@ struct Params {
   uint32_t share, segs, seg_rows, items;
   bool by_cta;       // an item's rows are spread over the CTA (else one group walks them)
   float* gate_part;  // [items][C] where segs > 1
+};
+
+// Where a row lies.  DENSE: every operand has one row axis, with one stride
+// for all of the stream's operands and one for all of the block's (the usual
+// case; a third of the address arithmetic).
+template <bool DENSE>
+struct At {
+  RowPos r;
+  uint64_t s, i;
+  __device__ __forceinline__ At(const Params& p, uint32_t row) {
+    if constexpr (DENSE) {
+      s = (uint64_t)row * p.stride_s;
+      i = (uint64_t)row * p.stride_i;
+    } else {
+      r = row_pos(p.rows_of, row);
+    }
+  }
+  __device__ __forceinline__ char* stream(const Params& p, const Operand& o) const {
+    if constexpr (DENSE) return o.p + s;
+    else return row_ptr(o, r, p.rows_of);
+  }
+  __device__ __forceinline__ char* block(const Params& p, const Operand& o) const {
+    if constexpr (DENSE) return o.p + i;
+    else return row_ptr(o, r, p.rows_of);
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -227,11 +253,28 @@ __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// A thread's unit k of a row is 2 * lane + k in fp32: neighbouring threads
+// would then copy every other 16 bytes.  So the threads of a group (of a warp,
+// where a row spans several) copy consecutive units and leave each in its
+// owner's slot; in bf16 a thread's only unit is its own.
+struct Share {
+  int lane, lanes;   // place among the threads that copy together
+  int first;         // CTA-wide index of the first of them
+  int left;          // threads of them that have channels
+};
 template <typename T>
-__device__ __forceinline__ void ring_put(uint32_t slot, uint32_t unit, const char* row, int lane, uint32_t bytes) {
+__device__ __forceinline__ void ring_put(uint32_t stage, uint32_t unit, const char* row, const Share& s, bool live) {
+  if constexpr (units<T>() == 1) {
+    const uint32_t bytes = live && s.lane < s.left ? 16u : 0u;
+    copy16(stage + (s.first + s.lane) * 16, row + (bytes ? s.lane * 16 : 0), bytes);
+  } else {
 #pragma unroll
-  for (int k = 0; k < units<T>(); ++k)
-    copy16(slot + k * unit, row + (size_t)(units<T>() * lane + k) * 16, bytes);
+    for (int k = 0; k < 2; ++k) {
+      const int at = k * s.lanes + s.lane;
+      const uint32_t bytes = live && at < 2 * s.left ? 16u : 0u;
+      copy16(stage + (at & 1) * unit + (s.first + (at >> 1)) * 16, row + (bytes ? at * 16 : 0), bytes);
+    }
+  }
 }
 template <typename T>
 __device__ __forceinline__ V ring_get(const char* slot, uint32_t unit) {
@@ -294,6 +337,16 @@ __device__ __forceinline__ Group make_group(const Params& p, float2 (*smem)[2 * 
   g.turn = 0;
   g.act = VEC ? g.lane * kE < p.C : true;
   return g;
+}
+
+template <int G>
+__device__ __forceinline__ Share make_share(const Group& g, int C) {
+  Share s;
+  s.lanes = warps_of(G) ? 32 : G;
+  s.lane = g.lane % s.lanes;
+  s.first = (int)threadIdx.x - s.lane;
+  s.left = min(max(C / kE - (g.lane - s.lane), 0), s.lanes);
+  return s;
 }
 
 // v - mean, absent channels kept at zero (VEC: a thread has all its channels
@@ -367,7 +420,7 @@ struct FwdRing {
   static constexpr size_t bytes(int threads) { return (size_t)STAGES * UNITS * 16 * threads; }
 };
 
-template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE>
+template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
 __global__ void __launch_bounds__(threads_of(G))
     k_block_norm_fwd(const __grid_constant__ Params p) {
   using Ring = FwdRing<TS, TI, POST>;
@@ -397,21 +450,23 @@ __global__ void __launch_bounds__(threads_of(G))
 
   const uint32_t unit = blockDim.x * 16, stage_bytes = Ring::UNITS * unit;
   const char* mine = smem + threadIdx.x * 16;
-  const uint32_t mine_s = smem_u32(mine);
-  auto gate_row = [&](uint32_t row, const RowPos& r) {
-    return shared_gate ? row_ptr(p.gate, row_pos(p.gate_of, row), p.gate_of) : row_ptr(p.gate, r, p.rows_of);
+  const uint32_t ring_s = smem_u32(smem);
+  const Share share = make_share<G>(g, C);
+  // a warp's threads' part of a row begins at the first of them
+  const int from = g.lane - share.lane;
+  auto gate_row = [&](uint32_t row, const At<DENSE>& r) {
+    return shared_gate ? row_ptr(p.gate, row_pos(p.gate_of, row), p.gate_of) : r.block(p, p.gate);
   };
   auto fetch = [&](uint32_t stage, uint32_t row) {
-    const uint32_t bytes = row < p.rows && g.act ? 16u : 0u;
-    const uint32_t at = bytes ? row : 0u;
-    const RowPos r = row_pos(p.rows_of, at);
-    uint32_t slot = mine_s + stage * stage_bytes;
-    const int lane = bytes ? g.lane : 0;
-    ring_put<TS>(slot, unit, row_ptr(p.x, r, p.rows_of), lane, bytes);
+    const bool live = row < p.rows;
+    const uint32_t at = live ? row : 0u;
+    const At<DENSE> r(p, at);
+    uint32_t slot = ring_s + stage * stage_bytes;
+    ring_put<TS>(slot, unit, r.stream(p, p.x) + from * kE * sizeof(TS), share, live);
     if (POST) {
       slot += units<TS>() * unit;
-      ring_put<TI>(slot, unit, row_ptr(p.u, r, p.rows_of), lane, bytes);
-      if (gated) ring_put<TI>(slot + units<TI>() * unit, unit, gate_row(at, r), lane, bytes);
+      ring_put<TI>(slot, unit, r.block(p, p.u) + from * kE * sizeof(TI), share, live);
+      if (gated) ring_put<TI>(slot + units<TI>() * unit, unit, gate_row(at, r) + from * kE * sizeof(TI), share, live);
     }
   };
 
@@ -431,13 +486,15 @@ __global__ void __launch_bounds__(threads_of(G))
   }
   for (; turns > 0; --turns, row += step) {
     const bool live = row < p.rows;
-    const RowPos r = row_pos(p.rows_of, live ? row : 0);
+    const At<DENSE> r(p, live ? row : 0);
     V x, u, q;
     if constexpr (ring_of(G, VEC)) {
       const uint32_t ahead = stage == 0 ? Ring::STAGES - 1 : stage - 1;
+      __syncwarp();  // the warp has read that stage
       fetch(ahead, row + (Ring::STAGES - 1) * step);
       copies_close();
       copies_wait<Ring::STAGES - 1>();
+      __syncwarp();  // what the warp's other threads copied
       const char* slot = mine + stage * stage_bytes;
       x = ring_get<TS>(slot, unit);
       if (POST) {
@@ -449,9 +506,9 @@ __global__ void __launch_bounds__(threads_of(G))
     } else {
       x = u = q = V{};
       if (live && g.act) {
-        x = load<TS, VEC>(row_ptr(p.x, r, p.rows_of), g.lane, g.lanes, C);
+        x = load<TS, VEC>(r.stream(p, p.x), g.lane, g.lanes, C);
         if (POST) {
-          u = load<TI, VEC>(row_ptr(p.u, r, p.rows_of), g.lane, g.lanes, C);
+          u = load<TI, VEC>(r.block(p, p.u), g.lane, g.lanes, C);
           if (gated) q = load<TI, VEC>(gate_row(row, r), g.lane, g.lanes, C);
         }
       }
@@ -466,13 +523,13 @@ __global__ void __launch_bounds__(threads_of(G))
 #pragma unroll
         for (int k = 0; k < kP; ++k) x.p[k] = add2(x.p[k], fma2(u.p[k], g1.p[k], b1.p[k]));
       }
-      if (live && g.act) store<TS, VEC>(row_ptr(p.x1, r, p.rows_of), g.lane, g.lanes, C, x);
+      if (live && g.act) store<TS, VEC>(r.stream(p, p.x1), g.lane, g.lanes, C, x);
     }
     if (PRE) {
       standardise<G, VEC>(x, g, p);
 #pragma unroll
       for (int k = 0; k < kP; ++k) x.p[k] = fma2(x.p[k], g2.p[k], b2.p[k]);
-      if (live && g.act) store<TI, VEC>(row_ptr(p.y, r, p.rows_of), g.lane, g.lanes, C, x);
+      if (live && g.act) store<TI, VEC>(r.block(p, p.y), g.lane, g.lanes, C, x);
     }
   }
   if constexpr (ring_of(G, VEC)) copies_wait<0>();
@@ -544,7 +601,8 @@ constexpr size_t bwd_sums_bytes(int threads) { return (size_t)threads * kE * 4; 
 constexpr size_t bwd_params_bytes(int lanes) { return (size_t)lanes * kE * 4 * 4; }
 
 // GROUPED: gate rows shared by consecutive rows, whose gradients are summed.
-template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED>
+template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED,
+          bool DENSE>
 __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     k_block_norm_bwd(const __grid_constant__ Params p) {
   using Ring = BwdRing<TS, TI, POST, PRE, GROUPED>;
@@ -588,25 +646,26 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
 
   const uint32_t unit = blockDim.x * 16, stage_bytes = Ring::UNITS * unit;
   const char* mine = ring + threadIdx.x * 16;
-  const uint32_t mine_s = smem_u32(mine);
+  const uint32_t ring_s = smem_u32(ring);
+  const Share share = make_share<G>(g, C);
+  const size_t from_s = (size_t)(g.lane - share.lane) * kE * sizeof(TS);
+  const size_t from_i = (size_t)(g.lane - share.lane) * kE * sizeof(TI);
   // ring order: dx1, (x1, dy), (u, gate)
   auto fetch = [&](uint32_t stage, uint32_t row, bool live) {
-    const uint32_t bytes = live && g.act ? 16u : 0u;
-    const RowPos r = row_pos(p.rows_of, bytes ? row : 0u);
-    const int lane = bytes ? g.lane : 0;
-    uint32_t slot = mine_s + stage * stage_bytes;
-    if (with_dx1) ring_put<TS>(slot, unit, row_ptr(p.dx1, r, p.rows_of), lane, bytes);
+    const At<DENSE> r(p, live ? row : 0u);
+    uint32_t slot = ring_s + stage * stage_bytes;
+    if (with_dx1) ring_put<TS>(slot, unit, r.stream(p, p.dx1) + from_s, share, live);
     slot += units<TS>() * unit;
     if (PRE) {
-      ring_put<TS>(slot, unit, row_ptr(p.x, r, p.rows_of), lane, bytes);
+      ring_put<TS>(slot, unit, r.stream(p, p.x) + from_s, share, live);
       slot += units<TS>() * unit;
-      ring_put<TI>(slot, unit, row_ptr(p.dy, r, p.rows_of), lane, bytes);
+      ring_put<TI>(slot, unit, r.block(p, p.dy) + from_i, share, live);
       slot += units<TI>() * unit;
     }
     if (POST) {
-      ring_put<TI>(slot, unit, row_ptr(p.u, r, p.rows_of), lane, bytes);
+      ring_put<TI>(slot, unit, r.block(p, p.u) + from_i, share, live);
       slot += units<TI>() * unit;
-      if (!GROUPED && gated) ring_put<TI>(slot, unit, row_ptr(p.gate, r, p.rows_of), lane, bytes);
+      if (!GROUPED && gated) ring_put<TI>(slot, unit, r.block(p, p.gate) + from_i, share, live);
     }
   };
 
@@ -628,7 +687,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   while (at.left > 0) {
     const uint32_t row = at.row;
     const bool live = row < at.end;  // a group without a row works on zeros
-    const RowPos r = row_pos(p.rows_of, live ? row : 0);
+    const At<DENSE> r(p, live ? row : 0);
     if constexpr (GROUPED) {
       if (fresh) {
         const RowPos rg = row_pos(p.gate_of, at.gate_row * p.share);
@@ -640,12 +699,14 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     V D = zero, h, dy, u, gt;
     if constexpr (RING) {
       const uint32_t to = stage == 0 ? Ring::STAGES - 1 : stage - 1;
+      __syncwarp();  // the warp has read that stage
       if (ahead.left > 0) {
         fetch(to, ahead.row, ahead.row < ahead.end);
         ahead.advance(p, g);
       }
       copies_close();
       copies_wait<Ring::STAGES - 1>();
+      __syncwarp();  // what the warp's other threads copied
       const char* slot = mine + stage * stage_bytes;
       if (with_dx1) D = ring_get<TS>(slot, unit);
       slot += units<TS>() * unit;
@@ -661,17 +722,20 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
     } else {
-      auto get_row = [&](const Operand& o, auto type) {
-        return live && g.act ? load<decltype(type), VEC>(row_ptr(o, r, p.rows_of), g.lane, g.lanes, C) : zero;
+      auto stream = [&](const Operand& o) {
+        return live && g.act ? load<TS, VEC>(r.stream(p, o), g.lane, g.lanes, C) : zero;
       };
-      if (with_dx1) D = get_row(p.dx1, TS(0.f));
+      auto block = [&](const Operand& o) {
+        return live && g.act ? load<TI, VEC>(r.block(p, o), g.lane, g.lanes, C) : zero;
+      };
+      if (with_dx1) D = stream(p.dx1);
       if (PRE) {
-        h = get_row(p.x, TS(0.f));
-        dy = get_row(p.dy, TI(0.f));
+        h = stream(p.x);
+        dy = block(p.dy);
       }
       if (POST) {
-        u = get_row(p.u, TI(0.f));
-        if (!GROUPED && gated) gt = get_row(p.gate, TI(0.f));
+        u = block(p.u);
+        if (!GROUPED && gated) gt = block(p.gate);
       }
     }
 
@@ -693,7 +757,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
 #pragma unroll
       for (int k = 0; k < kP; ++k)
         D.p[k] = fma2(rs, fma2(m1, h.p[k], add2(dy.p[k], m0)), D.p[k]);
-      if (live && g.act) store<TS, VEC>(row_ptr(p.dx, r, p.rows_of), g.lane, g.lanes, C, D);
+      if (live && g.act) store<TS, VEC>(r.stream(p, p.dx), g.lane, g.lanes, C, D);
     }
     if (POST) {
       if (!GROUPED && gated) {
@@ -722,8 +786,8 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
 #pragma unroll
       for (int k = 0; k < kP; ++k) b.p[k] = mul2(rs, fma2(m1, u.p[k], add2(b.p[k], m0)));
       if (live && g.act) {
-        store<TI, VEC>(row_ptr(p.du, r, p.rows_of), g.lane, g.lanes, C, b);
-        if (!GROUPED && gated) store<TI, VEC>(row_ptr(p.dgate, r, p.rows_of), g.lane, g.lanes, C, dg);
+        store<TI, VEC>(r.block(p, p.du), g.lane, g.lanes, C, b);
+        if (!GROUPED && gated) store<TI, VEC>(r.block(p, p.dgate), g.lane, g.lanes, C, dg);
       }
     }
 
@@ -761,6 +825,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     }
   }
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the CTA's sums of the parameter gradients, group by group in order
   const int width = g.lanes * kE;
 #pragma unroll
@@ -872,15 +937,17 @@ inline Rows join_axes(const Space& sp, const RowOperand* const* ops, Operand* co
 struct Plan {
   Params p;
   int g;        // lanes of a row's group: 8, 16, 32, kWarps or kPlain
-  bool vec;
+  bool vec, dense;
   int threads, slots;
 };
 
 // Sizes and operands, for both directions: `ops` go to `dst` (parts of pl.p),
 // their element sizes in `esize`; the gate and its gradient (`is_gate`) have
-// row axes of their own where gate rows are shared.
+// row axes of their own where gate rows are shared.  `is_stream`: operands of
+// the residual stream.
 inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Operand* const* dst,
-                      const int* esize, const bool* is_gate, int count, int gate_at, Plan& pl) {
+                      const int* esize, const bool* is_stream, const bool* is_gate, int count,
+                      int gate_at, Plan& pl) {
   Params& p = pl.p;
   const Space sp = order_axes(c.n, ops, count, c.gate.p ? gate_at : -1);
   p.share = sp.share;
@@ -898,6 +965,16 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     o.p = static_cast<char*>(ops[i]->p);
     if (o.p && (reinterpret_cast<uintptr_t>(o.p) % 16 || o.s0 % 16 || o.s1 % 16 || o.s2 % 16)) pl.vec = false;
   }
+  int64_t stride[2] = {-1, -1};
+  pl.dense = p.rows_of.flat;
+  for (int i = 0; i < count; ++i) {
+    if (!rows[i] || !dst[i]->p) continue;
+    int64_t& st = stride[is_stream[i] ? 0 : 1];
+    if (st < 0) st = dst[i]->s2;
+    if (dst[i]->s2 != st || st > 0xFFFFFFFFll) pl.dense = false;
+  }
+  p.stride_s = (uint32_t)std::max<int64_t>(stride[0], 0);
+  p.stride_i = (uint32_t)std::max<int64_t>(stride[1], 0);
   p.C = c.C;
   p.rms = c.rms;
   p.eps = c.eps;
@@ -922,11 +999,14 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
 }
 
 // Sums of the CTAs' partial sums: one block per 32 columns of one of the five
-// parameter gradients or of one gate row, 8 warps taking every 8th partial.
+// parameter gradients or of one gate row, 32 warps taking every 32nd partial.
+// Launched while the kernel before it drains, it waits for that one's end.
+constexpr int kReduceWarps = 32;
 template <typename TI>
-__global__ void __launch_bounds__(256) k_block_norm_reduce(const __grid_constant__ Params p,
-                                                           int ctas, int param_blocks) {
-  __shared__ float red[8][32];
+__global__ void __launch_bounds__(kReduceWarps * 32)
+    k_block_norm_reduce(const __grid_constant__ Params p, int ctas, int param_blocks) {
+  __shared__ float red[kReduceWarps][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per = (p.C + 31) / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blk = blockIdx.x;
@@ -940,13 +1020,13 @@ __global__ void __launch_bounds__(256) k_block_norm_reduce(const __grid_constant
   float s = 0.f;
   if (c < p.C) {
 #pragma unroll 4
-    for (int i = warp; i < depth; i += 8) s += src[i * stride + c];
+    for (int i = warp; i < depth; i += kReduceWarps) s += src[i * stride + c];
   }
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < p.C) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][lane];
+    for (int i = 1; i < kReduceWarps; ++i) s += red[i][lane];
     if (is_param) {
       p.out[what][c] = s;
     } else {
@@ -956,10 +1036,10 @@ __global__ void __launch_bounds__(256) k_block_norm_reduce(const __grid_constant
   }
 }
 
-template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE>
+template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
 cudaError_t launch_fwd(const Plan& pl, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
-  auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE>;
+  auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE, DENSE>;
   using Ring = FwdRing<TS, TI, POST>;
   constexpr bool RING = ring_of(G, VEC);
   const size_t smem = RING ? Ring::bytes(pl.threads) : 0;
@@ -971,10 +1051,10 @@ cudaError_t launch_fwd(const Plan& pl, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED>
+template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED, bool DENSE>
 cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
-  auto kern = k_block_norm_bwd<TS, TI, G, VEC, POST, PRE, GROUPED>;
+  auto kern = k_block_norm_bwd<TS, TI, G, VEC, POST, PRE, GROUPED, DENSE>;
   Params& p = pl.p;
   using Ring = BwdRing<TS, TI, POST, PRE, GROUPED>;
   constexpr bool RING = ring_of(G, VEC);
@@ -1016,38 +1096,55 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   const int param_blocks = any && grid > 1 ? 5 * per : 0;
   const int gate_blocks = GROUPED && p.segs > 1 ? (int)(p.rows / p.share) * per : 0;
   if (param_blocks + gate_blocks > 0) {
-    k_block_norm_reduce<TI><<<param_blocks + gate_blocks, 256, 0, st>>>(p, (int)grid, param_blocks);
-    e = cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(param_blocks + gate_blocks);
+    cfg.blockDim = dim3(kReduceWarps * 32);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_block_norm_reduce<TI>, p, (int)grid, param_blocks);
   }
   return e;
 }
 
-template <typename TS, typename TI, bool POST, bool PRE>
-cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
-  if (!pl.vec)
-    return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE>(pl, st)
-                      : launch_fwd<TS, TI, kPlain, false, POST, PRE>(pl, st);
+template <typename TS, typename TI, bool POST, bool PRE, bool DENSE>
+cudaError_t ring_fwd(const Plan& pl, cudaStream_t st) {
   switch (pl.g) {
-    case 8: return launch_fwd<TS, TI, 8, true, POST, PRE>(pl, st);
-    case 16: return launch_fwd<TS, TI, 16, true, POST, PRE>(pl, st);
-    case 32: return launch_fwd<TS, TI, 32, true, POST, PRE>(pl, st);
-    case kWarps: return launch_fwd<TS, TI, kWarps, true, POST, PRE>(pl, st);
-    default: return launch_fwd<TS, TI, kPlain, true, POST, PRE>(pl, st);
+    case 8: return launch_fwd<TS, TI, 8, true, POST, PRE, DENSE>(pl, st);
+    case 16: return launch_fwd<TS, TI, 16, true, POST, PRE, DENSE>(pl, st);
+    case 32: return launch_fwd<TS, TI, 32, true, POST, PRE, DENSE>(pl, st);
+    default: return launch_fwd<TS, TI, kWarps, true, POST, PRE, DENSE>(pl, st);
   }
 }
+template <typename TS, typename TI, bool POST, bool PRE>
+cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
+  if (pl.vec && pl.g != kPlain)
+    return pl.dense ? ring_fwd<TS, TI, POST, PRE, true>(pl, st) : ring_fwd<TS, TI, POST, PRE, false>(pl, st);
+  if (pl.vec) return launch_fwd<TS, TI, kPlain, true, POST, PRE, false>(pl, st);
+  return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE, false>(pl, st)
+                    : launch_fwd<TS, TI, kPlain, false, POST, PRE, false>(pl, st);
+}
 
+template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED, bool DENSE>
+cudaError_t ring_bwd(const Plan& pl, float* ws, cudaStream_t st) {
+  switch (pl.g) {
+    case 8: return launch_bwd<TS, TI, 8, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
+    case 16: return launch_bwd<TS, TI, 16, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
+    case 32: return launch_bwd<TS, TI, 32, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
+    default: return launch_bwd<TS, TI, kWarps, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
+  }
+}
 template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED>
 cudaError_t dispatch_bwd(const Plan& pl, float* ws, cudaStream_t st) {
-  if (!pl.vec)
-    return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED>(pl, ws, st)
-                      : launch_bwd<TS, TI, kPlain, false, POST, PRE, GROUPED>(pl, ws, st);
-  switch (pl.g) {
-    case 8: return launch_bwd<TS, TI, 8, true, POST, PRE, GROUPED>(pl, ws, st);
-    case 16: return launch_bwd<TS, TI, 16, true, POST, PRE, GROUPED>(pl, ws, st);
-    case 32: return launch_bwd<TS, TI, 32, true, POST, PRE, GROUPED>(pl, ws, st);
-    case kWarps: return launch_bwd<TS, TI, kWarps, true, POST, PRE, GROUPED>(pl, ws, st);
-    default: return launch_bwd<TS, TI, kPlain, true, POST, PRE, GROUPED>(pl, ws, st);
-  }
+  if (pl.vec && pl.g != kPlain)
+    return pl.dense ? ring_bwd<TS, TI, POST, PRE, GROUPED, true>(pl, ws, st)
+                    : ring_bwd<TS, TI, POST, PRE, GROUPED, false>(pl, ws, st);
+  if (pl.vec) return launch_bwd<TS, TI, kPlain, true, POST, PRE, GROUPED, false>(pl, ws, st);
+  return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED, false>(pl, ws, st)
+                    : launch_bwd<TS, TI, kPlain, false, POST, PRE, GROUPED, false>(pl, ws, st);
 }
 
 template <typename TS, typename TI>
@@ -1058,8 +1155,9 @@ cudaError_t run_fwd(const BlockNormCall& c, cudaStream_t st) {
   const RowOperand* ops[] = {&c.x, &c.u, &c.gate, &c.x1, &c.y};
   Operand* dst[] = {&p.x, &p.u, &p.gate, &p.x1, &p.y};
   const int es[] = {S, I, I, S, I};
+  const bool stream[] = {true, false, false, true, false};
   const bool gates[] = {false, false, true, false, false};
-  make_plan(c, ops, dst, es, gates, 5, 2, pl);
+  make_plan(c, ops, dst, es, stream, gates, 5, 2, pl);
   if (c.u.p && c.y.p) return dispatch_fwd<TS, TI, true, true>(pl, st);
   if (c.u.p) return dispatch_fwd<TS, TI, true, false>(pl, st);
   return dispatch_fwd<TS, TI, false, true>(pl, st);
@@ -1073,8 +1171,9 @@ cudaError_t run_bwd(const BlockNormCall& c, cudaStream_t st) {
   const RowOperand* ops[] = {&c.dx1, &c.x, &c.u, &c.gate, &c.dy, &c.dx, &c.du, &c.dgate};
   Operand* dst[] = {&p.dx1, &p.x, &p.u, &p.gate, &p.dy, &p.dx, &p.du, &p.dgate};
   const int es[] = {S, S, I, I, I, S, I, I};
+  const bool stream[] = {true, true, false, false, false, true, false, false};
   const bool gates[] = {false, false, false, true, false, false, false, true};
-  make_plan(c, ops, dst, es, gates, 8, 3, pl);
+  make_plan(c, ops, dst, es, stream, gates, 8, 3, pl);
   p.out[0] = c.dscale;
   p.out[1] = c.dgamma_post;
   p.out[2] = c.dbeta_post;
