@@ -517,7 +517,7 @@ evoattn_status evoattn_grad_norm(const evoattn_adamw_tensor* tensors, int count,
  *               and when state->skip is set change nothing, not even step.
  *  state      : device; step is read and counted up on the device, so a
  *               captured step replays as the next one.
- * One launch per 400 tensors.  Calls that share a state or a tensor must be
+ * One launch per 536 tensors (416 with 8-bit states).  Calls that share a state or a tensor must be
  * ordered by the caller.
  */
 evoattn_status evoattn_adamw(const evoattn_adamw_tensor* tensors, int count, float lr,

@@ -43,6 +43,7 @@
 
 #include "block_norm.h"
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace evo {
 namespace norm {
@@ -256,14 +257,20 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 // A thread's unit k of a row is 2 * lane + k in fp32: neighbouring threads
 // would then copy every other 16 bytes.  So the threads of a group (of a warp,
 // where a row spans several) copy consecutive units and leave each in its
-// owner's slot; in bf16 a thread's only unit is its own.
+// owner's slot; in bf16 a thread's only unit is its own.  The second units lie
+// 64 bytes further than a plane, so that both halves of an owner's 32 bytes
+// are written without a bank conflict.
+template <typename T>
+__host__ __device__ constexpr uint32_t ring_bytes(uint32_t threads) {
+  return sizeof(T) == 2 ? threads * 16 : threads * 32 + 128;
+}
 struct Share {
   int lane, lanes;   // place among the threads that copy together
   int first;         // CTA-wide index of the first of them
   int left;          // threads of them that have channels
 };
 template <typename T>
-__device__ __forceinline__ void ring_put(uint32_t stage, uint32_t unit, const char* row, const Share& s, bool live) {
+__device__ __forceinline__ void ring_put(uint32_t stage, const char* row, const Share& s, bool live) {
   if constexpr (units<T>() == 1) {
     const uint32_t bytes = live && s.lane < s.left ? 16u : 0u;
     copy16(stage + (s.first + s.lane) * 16, row + (bytes ? s.lane * 16 : 0), bytes);
@@ -272,15 +279,16 @@ __device__ __forceinline__ void ring_put(uint32_t stage, uint32_t unit, const ch
     for (int k = 0; k < 2; ++k) {
       const int at = k * s.lanes + s.lane;
       const uint32_t bytes = live && at < 2 * s.left ? 16u : 0u;
-      copy16(stage + (at & 1) * unit + (s.first + (at >> 1)) * 16, row + (bytes ? at * 16 : 0), bytes);
+      copy16(stage + (at & 1) * (blockDim.x * 16 + 64) + (s.first + (at >> 1)) * 16, row + (bytes ? at * 16 : 0), bytes);
     }
   }
 }
 template <typename T>
-__device__ __forceinline__ V ring_get(const char* slot, uint32_t unit) {
+__device__ __forceinline__ V ring_get(const char* slot) {
   uint4 r[units<T>()];
 #pragma unroll
-  for (int k = 0; k < units<T>(); ++k) r[k] = *reinterpret_cast<const uint4*>(slot + k * unit);
+  for (int k = 0; k < units<T>(); ++k)
+    r[k] = *reinterpret_cast<const uint4*>(slot + k * (blockDim.x * 16 + 64));
   return widen<T>(r);
 }
 
@@ -415,9 +423,12 @@ __device__ __forceinline__ void sigmoid(V& v) {
 template <typename TS, typename TI, bool POST>
 struct FwdRing {
   static constexpr int UNITS = units<TS>() + (POST ? 2 * units<TI>() : 0);
-  // enough stages for about 150 bytes in flight per thread, 24 warps per SM
-  static constexpr int STAGES = 144 / (UNITS * 16) < 2 ? 2 : 144 / (UNITS * 16) > 4 ? 4 : 144 / (UNITS * 16);
-  static constexpr size_t bytes(int threads) { return (size_t)STAGES * UNITS * 16 * threads; }
+  // as many stages (at most 4) as leave room for three CTAs per SM
+  static constexpr int STAGES = 18 / UNITS > 4 ? 4 : 18 / UNITS;
+  __host__ __device__ static constexpr uint32_t stage(uint32_t threads) {
+    return ring_bytes<TS>(threads) + (POST ? 2 * ring_bytes<TI>(threads) : 0);
+  }
+  static constexpr size_t bytes(int threads) { return (size_t)STAGES * stage(threads); }
 };
 
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
@@ -426,6 +437,8 @@ __global__ void __launch_bounds__(threads_of(G))
   using Ring = FwdRing<TS, TI, POST>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
+  wait_for_earlier_work();
+  let_next_start();
   Group g = make_group<G, VEC>(p, sums);
   const int C = p.C;
   const bool gated = POST && p.gate.p != nullptr;
@@ -448,7 +461,7 @@ __global__ void __launch_bounds__(threads_of(G))
     b2 = param<VEC>(p.beta_pre, 0.f, g.lane, g.lanes, C);
   }
 
-  const uint32_t unit = blockDim.x * 16, stage_bytes = Ring::UNITS * unit;
+  const uint32_t stage_bytes = Ring::stage(blockDim.x);
   const char* mine = smem + threadIdx.x * 16;
   const uint32_t ring_s = smem_u32(smem);
   const Share share = make_share<G>(g, C);
@@ -462,11 +475,11 @@ __global__ void __launch_bounds__(threads_of(G))
     const uint32_t at = live ? row : 0u;
     const At<DENSE> r(p, at);
     uint32_t slot = ring_s + stage * stage_bytes;
-    ring_put<TS>(slot, unit, r.stream(p, p.x) + from * kE * sizeof(TS), share, live);
+    ring_put<TS>(slot, r.stream(p, p.x) + from * kE * sizeof(TS), share, live);
     if (POST) {
-      slot += units<TS>() * unit;
-      ring_put<TI>(slot, unit, r.block(p, p.u) + from * kE * sizeof(TI), share, live);
-      if (gated) ring_put<TI>(slot + units<TI>() * unit, unit, gate_row(at, r) + from * kE * sizeof(TI), share, live);
+      slot += ring_bytes<TS>(blockDim.x);
+      ring_put<TI>(slot, r.block(p, p.u) + from * kE * sizeof(TI), share, live);
+      if (gated) ring_put<TI>(slot + ring_bytes<TI>(blockDim.x), gate_row(at, r) + from * kE * sizeof(TI), share, live);
     }
   };
 
@@ -496,11 +509,11 @@ __global__ void __launch_bounds__(threads_of(G))
       copies_wait<Ring::STAGES - 1>();
       __syncwarp();  // what the warp's other threads copied
       const char* slot = mine + stage * stage_bytes;
-      x = ring_get<TS>(slot, unit);
+      x = ring_get<TS>(slot);
       if (POST) {
-        slot += units<TS>() * unit;
-        u = ring_get<TI>(slot, unit);
-        if (gated) q = ring_get<TI>(slot + units<TI>() * unit, unit);
+        slot += ring_bytes<TS>(blockDim.x);
+        u = ring_get<TI>(slot);
+        if (gated) q = ring_get<TI>(slot + ring_bytes<TI>(blockDim.x));
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
     } else {
@@ -590,9 +603,13 @@ template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED>
 struct BwdRing {
   static constexpr int UNITS = units<TS>() * (PRE ? 2 : 1) + (PRE ? units<TI>() : 0) +
                                (POST ? units<TI>() * (GROUPED ? 1 : 2) : 0);
-  // about 320 bytes in flight per thread, 16 warps per SM
-  static constexpr int STAGES = 320 / (UNITS * 16) < 2 ? 2 : 320 / (UNITS * 16) > 4 ? 4 : 320 / (UNITS * 16);
-  static constexpr size_t bytes(int threads) { return (size_t)STAGES * UNITS * 16 * threads; }
+  // as many stages (at most 4) as leave room for two CTAs per SM
+  static constexpr int STAGES = 24 / UNITS > 4 ? 4 : 24 / UNITS;
+  __host__ __device__ static constexpr uint32_t stage(uint32_t threads) {
+    return ring_bytes<TS>(threads) * (PRE ? 2 : 1) + (PRE ? ring_bytes<TI>(threads) : 0) +
+           (POST ? ring_bytes<TI>(threads) * (GROUPED ? 1 : 2) : 0);
+  }
+  static constexpr size_t bytes(int threads) { return (size_t)STAGES * stage(threads); }
 };
 
 // Shared memory of the backward: a row of sums per group, and with a ring four
@@ -608,6 +625,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   using Ring = BwdRing<TS, TI, POST, PRE, GROUPED>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
+  wait_for_earlier_work();
   Group g = make_group<G, VEC>(p, sums);
   const int C = p.C;
   const bool gated = POST && (GROUPED || p.gate.p != nullptr);
@@ -644,7 +662,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   V q{{both(1.f), both(1.f), both(1.f), both(1.f)}};  // sigmoid(gate)
   V dg = zero;                                        // the gate's gradient
 
-  const uint32_t unit = blockDim.x * 16, stage_bytes = Ring::UNITS * unit;
+  const uint32_t stage_bytes = Ring::stage(blockDim.x);
   const char* mine = ring + threadIdx.x * 16;
   const uint32_t ring_s = smem_u32(ring);
   const Share share = make_share<G>(g, C);
@@ -654,18 +672,18 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   auto fetch = [&](uint32_t stage, uint32_t row, bool live) {
     const At<DENSE> r(p, live ? row : 0u);
     uint32_t slot = ring_s + stage * stage_bytes;
-    if (with_dx1) ring_put<TS>(slot, unit, r.stream(p, p.dx1) + from_s, share, live);
-    slot += units<TS>() * unit;
+    if (with_dx1) ring_put<TS>(slot, r.stream(p, p.dx1) + from_s, share, live);
+    slot += ring_bytes<TS>(blockDim.x);
     if (PRE) {
-      ring_put<TS>(slot, unit, r.stream(p, p.x) + from_s, share, live);
-      slot += units<TS>() * unit;
-      ring_put<TI>(slot, unit, r.block(p, p.dy) + from_i, share, live);
-      slot += units<TI>() * unit;
+      ring_put<TS>(slot, r.stream(p, p.x) + from_s, share, live);
+      slot += ring_bytes<TS>(blockDim.x);
+      ring_put<TI>(slot, r.block(p, p.dy) + from_i, share, live);
+      slot += ring_bytes<TI>(blockDim.x);
     }
     if (POST) {
-      ring_put<TI>(slot, unit, r.block(p, p.u) + from_i, share, live);
-      slot += units<TI>() * unit;
-      if (!GROUPED && gated) ring_put<TI>(slot, unit, r.block(p, p.gate) + from_i, share, live);
+      ring_put<TI>(slot, r.block(p, p.u) + from_i, share, live);
+      slot += ring_bytes<TI>(blockDim.x);
+      if (!GROUPED && gated) ring_put<TI>(slot, r.block(p, p.gate) + from_i, share, live);
     }
   };
 
@@ -708,17 +726,17 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
       copies_wait<Ring::STAGES - 1>();
       __syncwarp();  // what the warp's other threads copied
       const char* slot = mine + stage * stage_bytes;
-      if (with_dx1) D = ring_get<TS>(slot, unit);
-      slot += units<TS>() * unit;
+      if (with_dx1) D = ring_get<TS>(slot);
+      slot += ring_bytes<TS>(blockDim.x);
       if (PRE) {
-        h = ring_get<TS>(slot, unit);
-        slot += units<TS>() * unit;
-        dy = ring_get<TI>(slot, unit);
-        slot += units<TI>() * unit;
+        h = ring_get<TS>(slot);
+        slot += ring_bytes<TS>(blockDim.x);
+        dy = ring_get<TI>(slot);
+        slot += ring_bytes<TI>(blockDim.x);
       }
       if (POST) {
-        u = ring_get<TI>(slot, unit);
-        if (!GROUPED && gated) gt = ring_get<TI>(slot + units<TI>() * unit, unit);
+        u = ring_get<TI>(slot);
+        if (!GROUPED && gated) gt = ring_get<TI>(slot + ring_bytes<TI>(blockDim.x));
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
     } else {
@@ -825,7 +843,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     }
   }
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   // the CTA's sums of the parameter gradients, group by group in order
   const int width = g.lanes * kE;
 #pragma unroll
@@ -1006,7 +1024,7 @@ template <typename TI>
 __global__ void __launch_bounds__(kReduceWarps * 32)
     k_block_norm_reduce(const __grid_constant__ Params p, int ctas, int param_blocks) {
   __shared__ float red[kReduceWarps][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_earlier_work();
   const int per = (p.C + 31) / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blk = blockIdx.x;
@@ -1047,8 +1065,7 @@ cudaError_t launch_fwd(const Plan& pl, cudaStream_t st) {
   cudaError_t e = resident_ctas(kern, pl.threads, smem, RING ? Ring::bytes(kThreads) : 0, cache, &ctas);
   if (e != cudaSuccess) return e;
   const unsigned need = (pl.p.rows + pl.slots - 1) / pl.slots;
-  kern<<<std::min<unsigned>(need, (unsigned)ctas), pl.threads, smem, st>>>(pl.p);
-  return cudaGetLastError();
+  return launch_early(kern, std::min<unsigned>(need, (unsigned)ctas), pl.threads, smem, st, pl.p);
 }
 
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED, bool DENSE>
@@ -1087,8 +1104,7 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   const unsigned grid = std::min<unsigned>(need, (unsigned)ctas);
   p.part = ws;
   p.gate_part = ws + (size_t)kNormMaxCtas * 5 * p.C;
-  kern<<<grid, pl.threads, smem, st>>>(p);
-  e = cudaGetLastError();
+  e = launch_early(kern, grid, pl.threads, smem, st, p);
   if (e != cudaSuccess) return e;
   const int per = (p.C + 31) / 32;
   bool any = false;
@@ -1096,16 +1112,8 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   const int param_blocks = any && grid > 1 ? 5 * per : 0;
   const int gate_blocks = GROUPED && p.segs > 1 ? (int)(p.rows / p.share) * per : 0;
   if (param_blocks + gate_blocks > 0) {
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(param_blocks + gate_blocks);
-    cfg.blockDim = dim3(kReduceWarps * 32);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_block_norm_reduce<TI>, p, (int)grid, param_blocks);
+    e = launch_early(k_block_norm_reduce<TI>, param_blocks + gate_blocks, kReduceWarps * 32, 0, st, p, (int)grid,
+                     param_blocks);
   }
   return e;
 }

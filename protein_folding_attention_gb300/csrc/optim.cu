@@ -4,13 +4,15 @@
 //   p  = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
 //
 // Bound by HBM: 28 bytes per element with fp32 states, bf16 gradients and a
-// bf16 copy, 16 with 8-bit states, against about 20 fp32 operations.
+// bf16 copy, 16 with 8-bit states, against about 20 and 30 fp32 operations.
 //
-// The tensors of a launch are a table in the kernel's parameters (up to 400
-// rows of 72 bytes: no copy to the device, nothing to keep alive, and a
-// captured launch carries its own table).  Each CTA takes an even share of the
-// chunks of all tensors in order, so it looks its first tensor up once and
-// walks on from there; small tensors cost a chunk each.
+// The tensors of a launch are a table in the kernel's parameters (no copy to
+// the device, nothing to keep alive, and a captured launch carries its own
+// table).  All tensors are cut into blocks of 256 elements; a CTA takes an
+// even share of consecutive blocks, its warps every eighth of them, so small
+// tensors cost a block each and no CTA waits for another.  Each warp copies
+// its coming blocks into a ring in shared memory (cp.async): what is in flight
+// does not depend on how many warps are between loading and storing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -19,6 +21,8 @@
 #include <algorithm>
 #include <atomic>
 
+#include "common.cuh"
+#include "launch.cuh"
 #include "optim.h"
 
 namespace evo {
@@ -26,105 +30,152 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlock = EVOATTN_ADAMW_BLOCK;  // elements per warp and turn; a block of the 8-bit states
-constexpr int kStepChunk = kWarps * kBlock;  // elements per CTA and turn
-constexpr int kNormUnroll = 4;
-constexpr int kNormChunk = kNormUnroll * kThreads * 8;
-constexpr int kNormCtas = 1216;              // partial sums per launch at most (8 per SM)
+constexpr int kBlock = EVOATTN_ADAMW_BLOCK;  // elements a warp works on at a time
 static_assert(kBlock == 256, "a lane holds 8 elements of a block");
+constexpr int kStepCtas = 608;   // CTAs of a step's launch at most
+constexpr int kNormCtas = 1216;  // partial sums of a norm's launch at most
+constexpr int kNormUnroll = 4;
+constexpr int kNormChunk = kNormUnroll * kThreads * 8;  // elements a CTA sums at a time
 
+// Flags of a tensor, above the 48 bits of its element count.
+constexpr uint64_t kGradBf16 = 1ull << 48, kVec = 1ull << 49, kCount = (1ull << 48) - 1;
+
+template <bool BITS8>
 struct Entry {
   float* p;
   const void* g;
   void *m, *v;
-  float *ms, *vs;
   __nv_bfloat16* copy;
-  int64_t n;
+  uint64_t n;      // elements and flags
   float wd;
-  uint32_t flags;  // kGradBf16, kVec
+  uint32_t start;  // its first block
 };
-constexpr uint32_t kGradBf16 = 1u, kVec = 2u;
+template <>
+struct Entry<true> {
+  float* p;
+  const void* g;
+  void *m, *v;
+  __nv_bfloat16* copy;
+  uint64_t n;
+  float wd;
+  uint32_t start;
+  float *ms, *vs;
+};
 
-constexpr int kMaxTensors = 400;
-template <int T>
-struct Table {
-  Entry e[T];
-  uint32_t start[T + 1];  // first chunk of each tensor
-  int count;
-};
-template <int T>
+// Tensors of a launch: as many as the 32,764 bytes of kernel parameters hold,
+// or few, which keeps the launch short.
+template <bool BITS8>
+constexpr int kManyTensors = BITS8 ? 416 : 536;
+constexpr int kFewTensors = 32;
+
+template <bool BITS8, int T>
 struct StepParams {
-  Table<T> t;
+  Entry<BITS8> e[T + 1];     // (the last one's successor holds the end)
+  uint16_t first[kStepCtas];  // the tensor that each CTA begins in
   evoattn_optim_state* state;
   const float* lr_device;
-  float lr, b1, b1c, b2, b2c, log_b1, log_b2, eps;
+  float lr, b1, b1_low, b1c, b1c_low, b2, b2c, log_b1, log_b2, eps;
   int clip, last;  // last: this launch counts the step up
+  uint32_t blocks;
 };
+
+struct NormEntry {
+  const void* g;
+  uint64_t n;
+};
+constexpr int kNormTensors = 1408;
 template <int T>
 struct NormParams {
-  Table<T> t;
+  NormEntry e[T];
+  uint32_t start[T + 1];
+  uint16_t first[kNormCtas];
   evoattn_optim_state* state;
-  double* part;    // this launch's partial sums; all launches' begin at part_all
+  double* part;      // this launch's partial sums; all launches' begin at part_all
   double* part_all;
   int parts_before, last;
   float max_norm;
 };
-static_assert(sizeof(StepParams<kMaxTensors>) <= 32764 && sizeof(NormParams<kMaxTensors>) <= 32764,
+static_assert(sizeof(StepParams<false, kManyTensors<false>>) <= 32764 &&
+                  sizeof(StepParams<true, kManyTensors<true>>) <= 32764 &&
+                  sizeof(NormParams<kNormTensors>) <= 32764,
               "kernel parameters");
 
-// The tensor that holds a chunk.
-template <int T>
-__device__ __forceinline__ int find_tensor(const Table<T>& t, uint32_t chunk) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.start[mid] <= chunk) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// This CTA's even share [first, end) of the chunks.
-template <int T>
-__device__ __forceinline__ void my_share(const Table<T>& t, uint32_t* first, uint32_t* end) {
-  const uint64_t total = t.start[t.count];
-  *first = (uint32_t)(total * blockIdx.x / gridDim.x);
-  *end = (uint32_t)(total * (blockIdx.x + 1) / gridDim.x);
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-
-__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // e4m3 codes: four to a word, rounded to nearest even (beyond 448 to 448).
-__device__ __forceinline__ uint32_t to_e4m3(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t to_e4m3(float2 a, float2 b) {
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-__device__ __forceinline__ void from_e4m3(uint32_t w, float* v) {
+__device__ __forceinline__ void from_e4m3(uint32_t w, float2* v) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t f16x2;
     const uint16_t two = (uint16_t)(w >> (16 * h));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f16x2) : "h"(two));
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n"
-        : "=f"(v[2 * h]), "=f"(v[2 * h + 1])
+        : "=f"(v[h].x), "=f"(v[h].y)
         : "r"(f16x2));
   }
 }
+__device__ __forceinline__ float sqrt_approx(float a) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-__device__ __forceinline__ float warp_max(float v) {
+__device__ __forceinline__ float2 warp_max(float2 v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+    v.y = fmaxf(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+  }
   return v;
 }
 
-// Elements of a lane within its warp's block of 256: 4 * lane + {0..3} of each
-// half, so that an access of the warp covers 128 elements without gaps.
+// A lane's 8 elements of a block are 4 * lane + {0..3} of each half, so that a
+// warp's access covers 128 elements without gaps.
 __device__ __forceinline__ int element(int lane, int k) { return (k >> 2) * 128 + 4 * lane + (k & 3); }
 
+// A warp's stage of the ring: p, g (bf16 in the first half), then m and v,
+// and with 8 bits their scales.
+template <bool BITS8>
+struct Ring {
+  static constexpr uint32_t G = 1024, M = 2048, V = BITS8 ? 2304 : 3072;
+  [[maybe_unused]] static constexpr uint32_t S = 2560;
+  static constexpr uint32_t STAGE = BITS8 ? 2576 : 4096;
+  static constexpr int STAGES = BITS8 ? 4 : 3;  // two CTAs per SM
+  static constexpr uint32_t BYTES = STAGE * STAGES * kWarps;
+};
+
+// Where a warp is: a block and the tensor that holds it.
 template <bool BITS8, int T>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ StepParams<T> P) {
+struct Cursor {
+  uint32_t b;
+  int i;
+  __device__ __forceinline__ void settle(const StepParams<BITS8, T>& P) {
+    while (b >= P.e[i + 1].start) ++i;
+  }
+};
+
+template <bool BITS8, int T>
+__global__ void __launch_bounds__(kThreads, 2)
+    k_adamw(const __grid_constant__ StepParams<BITS8, T> P) {
+  using R = Ring<BITS8>;
+  extern __shared__ __align__(16) char smem[];
+  wait_for_earlier_work();
+  let_next_start();
   // every CTA reads the step before the last one to do so counts it up
   const float t = (float)(P.state->step + 1);
   const float clip = P.clip ? P.state->clip : 1.f;
@@ -144,146 +195,214 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Step
   // 1 - b^t without cancellation
   const float c1 = -expm1f(t * P.log_b1), c2 = -expm1f(t * P.log_b2);
   const float rate = lr / c1, root = rsqrtf(c2);
+  // (1 - b1) clip as the sum of two floats
+  const float gm = P.b1c * clip, gm_low = fmaf(P.b1c, clip, -gm) + P.b1c_low * clip;
 
-  uint32_t chunk, end;
-  my_share(P.t, &chunk, &end);
-  if (chunk >= end) return;
-  int i = find_tensor(P.t, chunk);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (; chunk < end; ++chunk) {
-    while (chunk >= P.t.start[i + 1]) ++i;
-    const Entry& e = P.t.e[i];
-    const int64_t base = (int64_t)(chunk - P.t.start[i]) * kStepChunk + warp * kBlock;
-    if (base >= e.n) continue;
-    const bool vec = (e.flags & kVec) && base + kBlock <= e.n;
-    float p[8], g[8], m[8], v[8];
+  const uint32_t end = (uint32_t)((uint64_t)P.blocks * (blockIdx.x + 1) / gridDim.x);
+  Cursor<BITS8, T> at{(uint32_t)((uint64_t)P.blocks * blockIdx.x / gridDim.x) + warp, P.first[blockIdx.x]};
+  char* const ring = smem + warp * (R::STAGE * R::STAGES);
+  const uint32_t ring_s = smem_u32(ring);
+
+  auto whole = [&](const Entry<BITS8>& e, int64_t base) {
+    return (e.n & kVec) && base + kBlock <= (int64_t)(e.n & kCount);
+  };
+  auto fetch = [&](int stage, Cursor<BITS8, T>& c) {
+    if (c.b < end) {
+      c.settle(P);
+      const Entry<BITS8>& e = P.e[c.i];
+      const int64_t base = (int64_t)(c.b - e.start) * kBlock;
+      if (whole(e, base)) {
+        const uint32_t to = ring_s + stage * R::STAGE + lane * 16;
+        const float* p = e.p + base + 4 * lane;
+        copy16(to, p);
+        copy16(to + 512, p + 128);
+        if (e.n & kGradBf16) {
+          copy16(to + R::G, static_cast<const __nv_bfloat16*>(e.g) + base + 8 * lane);
+        } else {
+          const float* g = static_cast<const float*>(e.g) + base + 4 * lane;
+          copy16(to + R::G, g);
+          copy16(to + R::G + 512, g + 128);
+        }
+        if constexpr (BITS8) {
+          // 256 bytes of each: half a warp's copies
+          const char* src = static_cast<const char*>(lane < 16 ? e.m : e.v) + base + (lane & 15) * 16;
+          copy16(to + R::M, src);  // (V follows M by 256 bytes)
+          if (lane < 2)
+            copy4(ring_s + stage * R::STAGE + R::S + 4 * lane, (lane == 0 ? e.ms : e.vs) + base / kBlock);
+        } else {
+          const float *m = static_cast<const float*>(e.m) + base + 4 * lane,
+                      *v = static_cast<const float*>(e.v) + base + 4 * lane;
+          copy16(to + R::M, m);
+          copy16(to + R::M + 512, m + 128);
+          copy16(to + R::V, v);
+          copy16(to + R::V + 512, v + 128);
+        }
+      }
+      c.b += kWarps;
+    }
+    copies_close();
+  };
+
+  Cursor<BITS8, T> ahead = at;
+#pragma unroll
+  for (int s = 0; s < R::STAGES - 1; ++s) fetch(s, ahead);
+  int stage = 0;
+  for (; at.b < end; at.b += kWarps) {
+    at.settle(P);
+    const Entry<BITS8>& e = P.e[at.i];
+    const int64_t n = (int64_t)(e.n & kCount), base = (int64_t)(at.b - e.start) * kBlock;
+    const bool vec = whole(e, base);
+    __syncwarp();  // the warp has read the stage that is filled next
+    fetch(stage == 0 ? R::STAGES - 1 : stage - 1, ahead);
+    copies_wait<R::STAGES - 1>();
+    __syncwarp();
+    const char* from = ring + stage * R::STAGE;
+    stage = stage + 1 == R::STAGES ? 0 : stage + 1;
+
+    float2 p[4], g[4], m[4], v[4];
+    float ms = 0.f, vs = 0.f;
     if (vec) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t at = base + element(lane, 4 * h);
-        *reinterpret_cast<float4*>(p + 4 * h) = *reinterpret_cast<const float4*>(e.p + at);
-        if (e.flags & kGradBf16) {
-          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.g) + at);
-          g[4 * h] = bf_lo(w.x); g[4 * h + 1] = bf_hi(w.x);
-          g[4 * h + 2] = bf_lo(w.y); g[4 * h + 3] = bf_hi(w.y);
+        auto four = [&](uint32_t off, float2* d) {
+          const float4 q = *reinterpret_cast<const float4*>(from + off + h * 512 + lane * 16);
+          d[2 * h] = make_float2(q.x, q.y);
+          d[2 * h + 1] = make_float2(q.z, q.w);
+        };
+        four(0, p);
+        if (e.n & kGradBf16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(from + R::G + h * 256 + lane * 8);
+          g[2 * h] = make_float2(bf16lo(w.x), bf16hi(w.x));
+          g[2 * h + 1] = make_float2(bf16lo(w.y), bf16hi(w.y));
         } else {
-          *reinterpret_cast<float4*>(g + 4 * h) =
-              *reinterpret_cast<const float4*>(static_cast<const float*>(e.g) + at);
+          four(R::G, g);
         }
-        if (BITS8) {
-          from_e4m3(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.m) + at), m + 4 * h);
-          from_e4m3(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.v) + at), v + 4 * h);
+        if constexpr (BITS8) {
+          from_e4m3(*reinterpret_cast<const uint32_t*>(from + R::M + h * 128 + lane * 4), m + 2 * h);
+          from_e4m3(*reinterpret_cast<const uint32_t*>(from + R::V + h * 128 + lane * 4), v + 2 * h);
         } else {
-          *reinterpret_cast<float4*>(m + 4 * h) =
-              *reinterpret_cast<const float4*>(static_cast<const float*>(e.m) + at);
-          *reinterpret_cast<float4*>(v + 4 * h) =
-              *reinterpret_cast<const float4*>(static_cast<const float*>(e.v) + at);
+          four(R::M, m);
+          four(R::V, v);
         }
+      }
+      if constexpr (BITS8) {
+        ms = *reinterpret_cast<const float*>(from + R::S);
+        vs = *reinterpret_cast<const float*>(from + R::S + 4);
       }
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int64_t at = base + element(lane, k);
-        const bool ok = at < e.n;
-        p[k] = ok ? e.p[at] : 0.f;
-        g[k] = !ok ? 0.f
-                   : (e.flags & kGradBf16) ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[at])
-                                           : static_cast<const float*>(e.g)[at];
-        if (BITS8) {
-          float w[4];
-          from_e4m3(ok ? static_cast<const uint8_t*>(e.m)[at] : 0u, w);
-          m[k] = w[0];
-          from_e4m3(ok ? static_cast<const uint8_t*>(e.v)[at] : 0u, w);
-          v[k] = w[0];
+        const int64_t a = base + element(lane, k);
+        const bool ok = a < n;
+        auto put = [&](float2* d, float x) { (k & 1 ? d[k >> 1].y : d[k >> 1].x) = x; };
+        put(p, ok ? e.p[a] : 0.f);
+        put(g, !ok ? 0.f
+                   : (e.n & kGradBf16) ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[a])
+                                       : static_cast<const float*>(e.g)[a]);
+        if constexpr (BITS8) {
+          float2 w[2];
+          from_e4m3(ok ? static_cast<const uint8_t*>(e.m)[a] : 0u, w);
+          put(m, w[0].x);
+          from_e4m3(ok ? static_cast<const uint8_t*>(e.v)[a] : 0u, w);
+          put(v, w[0].x);
         } else {
-          m[k] = ok ? static_cast<const float*>(e.m)[at] : 0.f;
-          v[k] = ok ? static_cast<const float*>(e.v)[at] : 0.f;
+          put(m, ok ? static_cast<const float*>(e.m)[a] : 0.f);
+          put(v, ok ? static_cast<const float*>(e.v)[a] : 0.f);
         }
       }
+      if constexpr (BITS8) {
+        ms = e.ms[base / kBlock];
+        vs = e.vs[base / kBlock];
+      }
+    }
+
+    // 8 bits: m is code * ms and v (code * vs)^2, so the block's factors
+    // b1 ms and b2 vs^2 take the codes; as sums of two floats where their
+    // rounding would move the whole block's codes one way
+    float fm = P.b1, fm_low = 0.f, fv = P.b2;
+    if constexpr (BITS8) {
+      fm = P.b1 * ms;
+      fm_low = fmaf(P.b1, ms, -fm) + P.b1_low * ms;
+      fv = P.b2 * (vs * vs);
     }
     const float keep = 1.f - lr * e.wd;
-    float ms = 0.f, vs = 0.f;
-    if (BITS8) {
-      ms = e.ms[base / kBlock];
-      vs = e.vs[base / kBlock];
-    }
-    // one rounding per operation (no fused multiply-add), so that the codes of
-    // the 8-bit states do not depend on how an expression is compiled
-    float top_m = 0.f, top_v = 0.f;
+    float2 r[4], top = both(0.f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float gk = __fmul_rn(clip, g[k]);
-      if (BITS8) {
-        m[k] = __fmul_rn(m[k], ms);
-        v[k] = __fmul_rn(v[k], vs);
-        v[k] = __fmul_rn(v[k], v[k]);
+    for (int k = 0; k < 4; ++k) {
+      float2 add = mul2(g[k], both(gm));
+      if constexpr (BITS8) {
+        add = fma2(m[k], both(fm_low), fma2(g[k], both(gm_low), add));
+        v[k] = mul2(v[k], v[k]);
       }
-      m[k] = __fadd_rn(__fmul_rn(P.b1, m[k]), __fmul_rn(P.b1c, gk));
-      v[k] = __fadd_rn(__fmul_rn(P.b2, v[k]), __fmul_rn(P.b2c, __fmul_rn(gk, gk)));
-      const float r = BITS8 ? __fsqrt_rn(v[k]) : sqrtf(v[k]);
-      p[k] = fmaf(-rate, __fdividef(m[k], fmaf(r, root, P.eps)), p[k] * keep);
-      if (BITS8) {
-        v[k] = r;  // the root is what is stored
-        top_m = fmaxf(top_m, fabsf(m[k]));
-        top_v = fmaxf(top_v, r);
+      m[k] = fma2(m[k], both(fm), add);
+      const float2 c = mul2(g[k], both(clip));
+      v[k] = fma2(v[k], both(fv), mul2(mul2(c, c), both(P.b2c)));
+      r[k] = make_float2(sqrt_approx(v[k].x), sqrt_approx(v[k].y));
+      const float2 d = fma2(r[k], both(root), both(P.eps));
+      const float2 q = make_float2(__fdividef(m[k].x, d.x), __fdividef(m[k].y, d.y));
+      p[k] = fma2(q, both(-rate), mul2(p[k], both(keep)));
+      if constexpr (BITS8) {
+        top.x = fmaxf(top.x, fmaxf(fabsf(m[k].x), fabsf(m[k].y)));
+        top.y = fmaxf(top.y, fmaxf(r[k].x, r[k].y));
       }
     }
-    if (BITS8) {
-      top_m = warp_max(top_m);
-      top_v = warp_max(top_v);
-      const bool hold_m = top_m >= 0x1p-100f, hold_v = top_v >= 0x1p-100f;
-      const float im = hold_m ? __fdiv_rn(448.f, top_m) : 0.f;
-      const float iv = hold_v ? __fdiv_rn(448.f, top_v) : 0.f;
+    if constexpr (BITS8) {
+      top = warp_max(top);
+      const bool hold_m = top.x >= 0x1p-100f, hold_v = top.y >= 0x1p-100f;
+      const float im = hold_m ? __fdiv_rn(448.f, top.x) : 0.f;
+      const float iv = hold_v ? __fdiv_rn(448.f, top.y) : 0.f;
       if (lane == 0) {
-        e.ms[base / kBlock] = hold_m ? __fdiv_rn(top_m, 448.f) : 0.f;
-        e.vs[base / kBlock] = hold_v ? __fdiv_rn(top_v, 448.f) : 0.f;
+        e.ms[base / kBlock] = hold_m ? __fdiv_rn(top.x, 448.f) : 0.f;
+        e.vs[base / kBlock] = hold_v ? __fdiv_rn(top.y, 448.f) : 0.f;
       }
+      // a positive root takes at least the smallest code (2^-9)
+      const float least = hold_v ? 0x1p-9f : 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] = __fmul_rn(m[k], im);
-        // a positive root takes at least the smallest code (2^-9)
-        const float q = __fmul_rn(v[k], iv);
-        v[k] = v[k] > 0.f && hold_v ? fmaxf(q, 0x1p-9f) : q;
+      for (int k = 0; k < 4; ++k) {
+        m[k] = mul2(m[k], both(im));
+        r[k] = mul2(r[k], both(iv));
+        if (v[k].x > 0.f) r[k].x = fmaxf(r[k].x, least);
+        if (v[k].y > 0.f) r[k].y = fmaxf(r[k].y, least);
       }
     }
     if (vec) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t at = base + element(lane, 4 * h);
-        const float* q = p + 4 * h;
-        *reinterpret_cast<float4*>(e.p + at) = make_float4(q[0], q[1], q[2], q[3]);
-        if (e.copy) {
-          uint2 w;
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(q[1]), "f"(q[0]));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(q[3]), "f"(q[2]));
-          *reinterpret_cast<uint2*>(e.copy + at) = w;
-        }
-        const float *mk = m + 4 * h, *vk = v + 4 * h;
-        if (BITS8) {
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.m) + at) = to_e4m3(mk[0], mk[1], mk[2], mk[3]);
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.v) + at) = to_e4m3(vk[0], vk[1], vk[2], vk[3]);
+        const int64_t a = base + element(lane, 4 * h);
+        const float2 x = p[2 * h], y = p[2 * h + 1];
+        *reinterpret_cast<float4*>(e.p + a) = make_float4(x.x, x.y, y.x, y.y);
+        if (e.copy)
+          *reinterpret_cast<uint2*>(e.copy + a) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(y.x, y.y));
+        if constexpr (BITS8) {
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.m) + a) = to_e4m3(m[2 * h], m[2 * h + 1]);
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.v) + a) = to_e4m3(r[2 * h], r[2 * h + 1]);
         } else {
-          *reinterpret_cast<float4*>(static_cast<float*>(e.m) + at) = make_float4(mk[0], mk[1], mk[2], mk[3]);
-          *reinterpret_cast<float4*>(static_cast<float*>(e.v) + at) = make_float4(vk[0], vk[1], vk[2], vk[3]);
+          *reinterpret_cast<float4*>(static_cast<float*>(e.m) + a) =
+              make_float4(m[2 * h].x, m[2 * h].y, m[2 * h + 1].x, m[2 * h + 1].y);
+          *reinterpret_cast<float4*>(static_cast<float*>(e.v) + a) =
+              make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
         }
       }
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int64_t at = base + element(lane, k);
-        if (at >= e.n) continue;
-        e.p[at] = p[k];
-        if (e.copy) e.copy[at] = __float2bfloat16_rn(p[k]);
-        if (BITS8) {
-          static_cast<uint8_t*>(e.m)[at] = (uint8_t)to_e4m3(m[k], 0.f, 0.f, 0.f);
-          static_cast<uint8_t*>(e.v)[at] = (uint8_t)to_e4m3(v[k], 0.f, 0.f, 0.f);
+        const int64_t a = base + element(lane, k);
+        if (a >= n) continue;
+        auto one = [&](const float2* d) { return k & 1 ? d[k >> 1].y : d[k >> 1].x; };
+        e.p[a] = one(p);
+        if (e.copy) e.copy[a] = __float2bfloat16_rn(one(p));
+        if constexpr (BITS8) {
+          static_cast<uint8_t*>(e.m)[a] = (uint8_t)to_e4m3(make_float2(one(m), 0.f), both(0.f));
+          static_cast<uint8_t*>(e.v)[a] = (uint8_t)to_e4m3(make_float2(one(r), 0.f), both(0.f));
         } else {
-          static_cast<float*>(e.m)[at] = m[k];
-          static_cast<float*>(e.v)[at] = v[k];
+          static_cast<float*>(e.m)[a] = one(m);
+          static_cast<float*>(e.v)[a] = one(v);
         }
       }
     }
   }
+  copies_wait<0>();
 }
 
 // Sum over a CTA in fp64, valid in thread 0.
@@ -299,64 +418,65 @@ __device__ __forceinline__ double cta_sum(double v) {
   return v;
 }
 
-// The last CTA to finish adds all partial sums in order, so the order of
-// arrival changes nothing.
+// A CTA takes an even share of the chunks of all tensors in order.  The last
+// CTA to finish adds all partial sums in order, so the order of arrival
+// changes nothing.
 template <int T>
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormParams<T> P) {
-  uint32_t chunk, end;
-  my_share(P.t, &chunk, &end);
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormParams<T> P,
+                                                        uint32_t chunks) {
+  wait_for_earlier_work();
+  let_next_start();
+  uint32_t chunk = (uint32_t)((uint64_t)chunks * blockIdx.x / gridDim.x);
+  const uint32_t end = (uint32_t)((uint64_t)chunks * (blockIdx.x + 1) / gridDim.x);
   double total = 0.0;
-  if (chunk < end) {
-    int i = find_tensor(P.t, chunk);
-    for (; chunk < end; ++chunk) {
-      while (chunk >= P.t.start[i + 1]) ++i;
-      const Entry& e = P.t.e[i];
-      const int64_t base = (int64_t)(chunk - P.t.start[i]) * kNormChunk;
-      const bool vec = (e.flags & kVec) && base + kNormChunk <= e.n;
-      float s[kNormUnroll];
+  int i = P.first[blockIdx.x];
+  for (; chunk < end; ++chunk) {
+    while (chunk >= P.start[i + 1]) ++i;
+    const NormEntry& e = P.e[i];
+    const int64_t n = (int64_t)(e.n & kCount), base = (int64_t)(chunk - P.start[i]) * kNormChunk;
+    const bool vec = (e.n & kVec) && base + kNormChunk <= n;
+    float s[kNormUnroll];
 #pragma unroll
-      for (int u = 0; u < kNormUnroll; ++u) s[u] = 0.f;
-      if (vec && (e.flags & kGradBf16)) {
-        uint4 w[kNormUnroll];
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.g) + base + 8 * threadIdx.x;
+    for (int u = 0; u < kNormUnroll; ++u) s[u] = 0.f;
+    if (vec && (e.n & kGradBf16)) {
+      uint4 w[kNormUnroll];
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.g) + base + 8 * threadIdx.x;
 #pragma unroll
-        for (int u = 0; u < kNormUnroll; ++u)
-          w[u] = *reinterpret_cast<const uint4*>(src + u * kThreads * 8);
+      for (int u = 0; u < kNormUnroll; ++u)
+        w[u] = *reinterpret_cast<const uint4*>(src + u * kThreads * 8);
 #pragma unroll
-        for (int u = 0; u < kNormUnroll; ++u) {
-          const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      for (int u = 0; u < kNormUnroll; ++u) {
+        const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s[u] = fmaf(bf_lo(q[k]), bf_lo(q[k]), s[u]);
-            s[u] = fmaf(bf_hi(q[k]), bf_hi(q[k]), s[u]);
-          }
-        }
-      } else if (vec) {
-        float4 w[2 * kNormUnroll];
-        const float* src = static_cast<const float*>(e.g) + base + 4 * threadIdx.x;
-#pragma unroll
-        for (int u = 0; u < 2 * kNormUnroll; ++u)
-          w[u] = *reinterpret_cast<const float4*>(src + u * kThreads * 4);
-#pragma unroll
-        for (int u = 0; u < 2 * kNormUnroll; ++u) {
-          float& d = s[u >> 1];
-          d = fmaf(w[u].x, w[u].x, d);
-          d = fmaf(w[u].y, w[u].y, d);
-          d = fmaf(w[u].z, w[u].z, d);
-          d = fmaf(w[u].w, w[u].w, d);
-        }
-      } else {
-        const int64_t stop = min(e.n, base + (int64_t)kNormChunk);
-#pragma unroll 4
-        for (int64_t at = base + threadIdx.x; at < stop; at += kThreads) {
-          const float g = (e.flags & kGradBf16)
-                              ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[at])
-                              : static_cast<const float*>(e.g)[at];
-          s[0] = fmaf(g, g, s[0]);
+        for (int k = 0; k < 4; ++k) {
+          s[u] = fmaf(bf16lo(q[k]), bf16lo(q[k]), s[u]);
+          s[u] = fmaf(bf16hi(q[k]), bf16hi(q[k]), s[u]);
         }
       }
-      total += (double)((s[0] + s[1]) + (s[2] + s[3]));
+    } else if (vec) {
+      float4 w[2 * kNormUnroll];
+      const float* src = static_cast<const float*>(e.g) + base + 4 * threadIdx.x;
+#pragma unroll
+      for (int u = 0; u < 2 * kNormUnroll; ++u)
+        w[u] = *reinterpret_cast<const float4*>(src + u * kThreads * 4);
+#pragma unroll
+      for (int u = 0; u < 2 * kNormUnroll; ++u) {
+        float& d = s[u >> 1];
+        d = fmaf(w[u].x, w[u].x, d);
+        d = fmaf(w[u].y, w[u].y, d);
+        d = fmaf(w[u].z, w[u].z, d);
+        d = fmaf(w[u].w, w[u].w, d);
+      }
+    } else {
+      const int64_t stop = min(n, base + (int64_t)kNormChunk);
+#pragma unroll 4
+      for (int64_t a = base + threadIdx.x; a < stop; a += kThreads) {
+        const float g = (e.n & kGradBf16) ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[a])
+                                          : static_cast<const float*>(e.g)[a];
+        s[0] = fmaf(g, g, s[0]);
+      }
     }
+    total += (double)((s[0] + s[1]) + (s[2] + s[3]));
   }
   total = cta_sum(total);
   __shared__ int is_last;
@@ -389,67 +509,76 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Rows [from, from + count) of the call's tensors; false when the chunks do
-// not fit 32 bits.
-template <int T>
-bool fill_table(Table<T>& t, const evoattn_adamw_tensor* src, int count, int chunk_elems, int bits) {
-  uint64_t chunks = 0;
-  t.count = 0;
-  for (int i = 0; i < count; ++i) {
-    const evoattn_adamw_tensor& s = src[i];
-    if (s.n == 0) continue;
-    Entry& e = t.e[t.count];
-    e = Entry{s.param, s.grad, s.exp_avg, s.exp_avg_sq, s.exp_avg_scale, s.exp_avg_sq_scale,
-              static_cast<__nv_bfloat16*>(s.copy), s.n, s.weight_decay, 0u};
-    const bool bf16 = s.grad_dtype == EVOATTN_BF16;
-    bool vec = aligned(s.grad, 16);
-    if (bits) {
-      const size_t state = bits == 8 ? 4 : 16;
-      vec = vec && aligned(s.param, 16) && aligned(s.exp_avg, state) && aligned(s.exp_avg_sq, state) &&
-            aligned(s.copy, 8);
-    }
-    e.flags = (bf16 ? kGradBf16 : 0u) | (vec ? kVec : 0u);
-    t.start[t.count++] = (uint32_t)chunks;
-    chunks += (uint64_t)(s.n + chunk_elems - 1) / (uint64_t)chunk_elems;
-    if (chunks > 0x7FFFFFFFull) return false;
-  }
-  if (t.count == 0) {  // nothing to do but the bookkeeping
-    t.start[0] = 0;
-    t.count = 1;
-    t.e[0] = Entry{};
-  }
-  t.start[t.count] = (uint32_t)chunks;
-  return true;
+uint64_t grad_flags(const evoattn_adamw_tensor& s) {
+  return (uint64_t)s.n | (s.grad_dtype == EVOATTN_BF16 ? kGradBf16 : 0) | (aligned(s.grad, 16) ? kVec : 0);
 }
 
 // Resident CTAs of a kernel on the current device, looked up once.
 template <typename K>
-cudaError_t resident_ctas(K kernel, std::atomic<int> (&cache)[64], int* n) {
+cudaError_t resident_ctas(K kernel, size_t smem, std::atomic<int> (&cache)[64], int* n) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   *n = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
   if (*n > 0) return cudaSuccess;
   int sms = 0, per = 0;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, 0);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem);
   if (e != cudaSuccess) return e;
   *n = std::max(1, sms) * std::max(1, per);
   if (dev < 64) cache[dev].store(*n, std::memory_order_relaxed);
   return cudaSuccess;
 }
 
+// The tensor in which each CTA's share of `total` pieces begins.
+template <typename StartOf>
+void first_tensors(uint16_t* first, unsigned grid, uint64_t total, StartOf start_of) {
+  int i = 0;
+  for (unsigned c = 0; c < grid; ++c) {
+    const uint64_t b = total * c / grid;
+    while (b < total && b >= start_of(i + 1)) ++i;
+    first[c] = (uint16_t)i;
+  }
+}
+
 template <bool BITS8, int T>
 cudaError_t step_part(const evoattn_adamw_tensor* t, int count, const AdamwScalars& s,
                       evoattn_optim_state* state, bool last, cudaStream_t st) {
   static std::atomic<int> cache[64];
-  StepParams<T> P;
-  if (!fill_table(P.t, t, count, kStepChunk, BITS8 ? 8 : 32)) return cudaErrorInvalidConfiguration;
+  StepParams<BITS8, T> P;
+  uint64_t blocks = 0;
+  int k = 0;
+  for (int i = 0; i < count; ++i) {
+    const evoattn_adamw_tensor& a = t[i];
+    if (a.n == 0) continue;
+    Entry<BITS8>& e = P.e[k++];
+    e.p = a.param;
+    e.g = a.grad;
+    e.m = a.exp_avg;
+    e.v = a.exp_avg_sq;
+    e.copy = static_cast<__nv_bfloat16*>(a.copy);
+    e.wd = a.weight_decay;
+    e.n = grad_flags(a);
+    if (!aligned(a.param, 16) || !aligned(a.exp_avg, 16) || !aligned(a.exp_avg_sq, 16) || !aligned(a.copy, 8))
+      e.n &= ~kVec;
+    if constexpr (BITS8) {
+      e.ms = a.exp_avg_scale;
+      e.vs = a.exp_avg_sq_scale;
+    }
+    e.start = (uint32_t)blocks;
+    blocks += (uint64_t)(a.n + kBlock - 1) / kBlock;
+    if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  }
+  P.e[k].start = (uint32_t)blocks;
+  P.blocks = (uint32_t)blocks;
   P.state = state;
   P.lr_device = s.lr_device;
   P.lr = s.lr;
   P.b1 = (float)s.beta1;
+  P.b1_low = (float)(s.beta1 - (double)P.b1);
   P.b1c = (float)(1.0 - s.beta1);
+  P.b1c_low = (float)((1.0 - s.beta1) - (double)P.b1c);
   P.b2 = (float)s.beta2;
   P.b2c = (float)(1.0 - s.beta2);
   P.log_b1 = (float)log(s.beta1);
@@ -458,22 +587,24 @@ cudaError_t step_part(const evoattn_adamw_tensor* t, int count, const AdamwScala
   P.clip = s.clip ? 1 : 0;
   P.last = last ? 1 : 0;
   int ctas = 0;
-  cudaError_t e = resident_ctas(k_adamw<BITS8, T>, cache, &ctas);
+  cudaError_t e = resident_ctas(k_adamw<BITS8, T>, Ring<BITS8>::BYTES, cache, &ctas);
   if (e != cudaSuccess) return e;
-  const unsigned grid = std::max(1u, std::min<unsigned>(P.t.start[P.t.count], (unsigned)ctas));
-  k_adamw<BITS8, T><<<grid, kThreads, 0, st>>>(P);
-  return cudaGetLastError();
+  // a CTA for every 8 blocks (one per warp), at least one for the bookkeeping
+  const uint64_t want = std::max<uint64_t>(1, (blocks + kWarps - 1) / kWarps);
+  const unsigned grid = (unsigned)std::min<uint64_t>(want, (uint64_t)std::min(ctas, kStepCtas));
+  first_tensors(P.first, grid, blocks, [&](int i) { return P.e[i].start; });
+  return launch_early(k_adamw<BITS8, T>, grid, kThreads, Ring<BITS8>::BYTES, st, P);
 }
 
 template <bool BITS8>
 cudaError_t step_all(const evoattn_adamw_tensor* t, int count, const AdamwScalars& s,
                      evoattn_optim_state* state, cudaStream_t st) {
-  for (int from = 0; from < count; from += kMaxTensors) {
-    const int k = std::min(kMaxTensors, count - from);
+  constexpr int kMany = kManyTensors<BITS8>;
+  for (int from = 0; from < count; from += kMany) {
+    const int k = std::min(kMany, count - from);
     const bool last = from + k == count;
-    // (a short table keeps a launch of few tensors short)
-    const cudaError_t e = k <= 32 ? step_part<BITS8, 32>(t + from, k, s, state, last, st)
-                                  : step_part<BITS8, kMaxTensors>(t + from, k, s, state, last, st);
+    const cudaError_t e = k <= kFewTensors ? step_part<BITS8, kFewTensors>(t + from, k, s, state, last, st)
+                                           : step_part<BITS8, kMany>(t + from, k, s, state, last, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -485,7 +616,16 @@ cudaError_t norm_part(const evoattn_adamw_tensor* t, int count, float max_norm,
                       cudaStream_t st) {
   static std::atomic<int> cache[64];
   NormParams<T> P;
-  if (!fill_table(P.t, t, count, kNormChunk, 0)) return cudaErrorInvalidConfiguration;
+  uint64_t chunks = 0;
+  int k = 0;
+  for (int i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    P.e[k] = NormEntry{t[i].grad, grad_flags(t[i])};
+    P.start[k++] = (uint32_t)chunks;
+    chunks += (uint64_t)(t[i].n + kNormChunk - 1) / kNormChunk;
+    if (chunks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  }
+  P.start[k] = (uint32_t)chunks;
   P.state = state;
   P.part_all = part_all;
   P.part = part_all + *parts;
@@ -493,31 +633,31 @@ cudaError_t norm_part(const evoattn_adamw_tensor* t, int count, float max_norm,
   P.last = last ? 1 : 0;
   P.max_norm = max_norm;
   int ctas = 0;
-  cudaError_t e = resident_ctas(k_grad_norm<T>, cache, &ctas);
+  cudaError_t e = resident_ctas(k_grad_norm<T>, 0, cache, &ctas);
   if (e != cudaSuccess) return e;
-  ctas = std::min(ctas, kNormCtas);
-  const unsigned grid = std::max(1u, std::min<unsigned>(P.t.start[P.t.count], (unsigned)ctas));
-  k_grad_norm<T><<<grid, kThreads, 0, st>>>(P);
+  const unsigned grid =
+      (unsigned)std::min<uint64_t>(std::max<uint64_t>(chunks, 1), (uint64_t)std::min(ctas, kNormCtas));
+  first_tensors(P.first, grid, chunks, [&](int i) { return P.start[i]; });
   *parts += (int)grid;
-  return cudaGetLastError();
+  return launch_early(k_grad_norm<T>, grid, kThreads, 0, st, P, (uint32_t)chunks);
 }
 
 }  // namespace
 
 size_t grad_norm_workspace_bytes(int count) {
-  return (size_t)((count + kMaxTensors - 1) / kMaxTensors) * kNormCtas * sizeof(double);
+  return (size_t)((count + kNormTensors - 1) / kNormTensors) * kNormCtas * sizeof(double);
 }
 
 cudaError_t grad_norm(const evoattn_adamw_tensor* t, int count, float max_norm,
                       evoattn_optim_state* state, void* ws, cudaStream_t st) {
   int parts = 0;
-  for (int from = 0; from < count; from += kMaxTensors) {
-    const int k = std::min(kMaxTensors, count - from);
+  for (int from = 0; from < count; from += kNormTensors) {
+    const int k = std::min(kNormTensors, count - from);
     const bool last = from + k == count;
     double* part = static_cast<double*>(ws);
     const cudaError_t e =
-        k <= 32 ? norm_part<32>(t + from, k, max_norm, state, part, &parts, last, st)
-                : norm_part<kMaxTensors>(t + from, k, max_norm, state, part, &parts, last, st);
+        k <= kFewTensors ? norm_part<kFewTensors>(t + from, k, max_norm, state, part, &parts, last, st)
+                         : norm_part<kNormTensors>(t + from, k, max_norm, state, part, &parts, last, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -171,7 +171,7 @@ def test_grad_norm_rejects_bad_arguments(lib):
     need = lib.evoattn_grad_norm_workspace_size(2)
     assert need > 0 and lib.evoattn_grad_norm_workspace_size(0) == 0
     assert norm(lib, tensors(), ws_bytes=need - 1) == W
-    assert lib.evoattn_grad_norm_workspace_size(401) == 2 * need
+    assert lib.evoattn_grad_norm_workspace_size(10_000) > need
 
 
 def test_python_refuses_tensors_that_are_not_on_the_current_gpu():
