@@ -491,9 +491,9 @@ size_t evoattn_grad_norm_workspace_size(int count);
 
 /*
  * norm = sqrt(sum of g^2 over all elements of all tensors) into state->norm,
- * with the clipping coefficient and the skip flag beside it.  Squares are
- * summed in fp32 within a thread and in fp64 from there, in a fixed order: the same
- * bits every time.  A norm beyond the fp32 range counts as infinite.
+ * with the clipping coefficient and the skip flag beside it.  Sums have a
+ * fixed order (the same bits every time) and are compensated or in fp64 where
+ * they are long.  A sum of squares beyond the fp32 range counts as infinite.
  *
  *  tensors  : host array; only grad, n and grad_dtype are read.
  *  max_norm : > 0; INFINITY for the norm alone (clip = 1).

@@ -214,21 +214,36 @@ __device__ __forceinline__ V load(const char* row, int lane, int lanes, int C) {
   }
 }
 
+// Writes a thread's channels where `live`; every thread of the warp calls it.
 template <typename T, bool VEC>
-__device__ __forceinline__ void store(char* row, int lane, int lanes, int C, const V& v) {
+__device__ __forceinline__ void store(bool live, char* row, int lane, int lanes, int C, const V& v) {
   if constexpr (VEC && sizeof(T) == 2) {
-    reinterpret_cast<uint4*>(row)[lane] =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    if (live && lane * kE < C)
+      reinterpret_cast<uint4*>(row)[lane] =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
   } else if constexpr (VEC) {
-    float4* p = reinterpret_cast<float4*>(row) + 2 * lane;
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    // Neighbouring threads exchange half of their 32 bytes, so that each of
+    // the two stores fills whole 32-byte sectors.  (A thread without channels
+    // may so store its neighbour's.)
+    const bool odd = lane & 1;
+    const float4 own = odd ? make_float4(v[4], v[5], v[6], v[7]) : make_float4(v[0], v[1], v[2], v[3]);
+    const float4 give = odd ? make_float4(v[0], v[1], v[2], v[3]) : make_float4(v[4], v[5], v[6], v[7]);
+    float4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+    got.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+    got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+    // of a pair's four units an even thread now has 0 and 2, an odd one 1 and 3
+    const int at = 4 * (lane >> 1) + (odd ? 1 : 0);
+    float4* p = reinterpret_cast<float4*>(row) + at;
+    if (live && 4 * at < C) p[0] = odd ? got : own;
+    if (live && 4 * (at + 2) < C) p[2] = odd ? own : got;
   } else {
     T* p = reinterpret_cast<T*>(row);
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
       const int c = e * lanes + lane;
-      if (c < C) p[c] = static_cast<T>(v[e]);
+      if (live && c < C) p[c] = static_cast<T>(v[e]);
     }
   }
 }
@@ -536,13 +551,13 @@ __global__ void __launch_bounds__(threads_of(G))
 #pragma unroll
         for (int k = 0; k < kP; ++k) x.p[k] = add2(x.p[k], fma2(u.p[k], g1.p[k], b1.p[k]));
       }
-      if (live && g.act) store<TS, VEC>(r.stream(p, p.x1), g.lane, g.lanes, C, x);
+      store<TS, VEC>(live, r.stream(p, p.x1), g.lane, g.lanes, C, x);
     }
     if (PRE) {
       standardise<G, VEC>(x, g, p);
 #pragma unroll
       for (int k = 0; k < kP; ++k) x.p[k] = fma2(x.p[k], g2.p[k], b2.p[k]);
-      if (live && g.act) store<TI, VEC>(r.block(p, p.y), g.lane, g.lanes, C, x);
+      store<TI, VEC>(live, r.block(p, p.y), g.lane, g.lanes, C, x);
     }
   }
   if constexpr (ring_of(G, VEC)) copies_wait<0>();
@@ -775,7 +790,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
 #pragma unroll
       for (int k = 0; k < kP; ++k)
         D.p[k] = fma2(rs, fma2(m1, h.p[k], add2(dy.p[k], m0)), D.p[k]);
-      if (live && g.act) store<TS, VEC>(r.stream(p, p.dx), g.lane, g.lanes, C, D);
+      store<TS, VEC>(live, r.stream(p, p.dx), g.lane, g.lanes, C, D);
     }
     if (POST) {
       if (!GROUPED && gated) {
@@ -803,10 +818,8 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
       const float2 m0 = both(p.rms ? 0.f : -s.x * p.inv_c), m1 = both(-s.y * p.inv_c), rs = both(rstd.y);
 #pragma unroll
       for (int k = 0; k < kP; ++k) b.p[k] = mul2(rs, fma2(m1, u.p[k], add2(b.p[k], m0)));
-      if (live && g.act) {
-        store<TI, VEC>(r.block(p, p.du), g.lane, g.lanes, C, b);
-        if (!GROUPED && gated) store<TI, VEC>(r.block(p, p.dgate), g.lane, g.lanes, C, dg);
-      }
+      store<TI, VEC>(live, r.block(p, p.du), g.lane, g.lanes, C, b);
+      if (!GROUPED && gated) store<TI, VEC>(live, r.block(p, p.dgate), g.lane, g.lanes, C, dg);
     }
 
     const Walk<GROUPED> was = at;
@@ -831,13 +844,12 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
             }
           }
         }
-        if (owns && g.act && (!p.by_cta || g.slot == 0)) {
-          if (p.segs == 1) {
-            const RowPos rg = row_pos(p.gate_of, was.gate_row * p.share);
-            store<TI, VEC>(row_ptr(p.dgate, rg, p.gate_of), g.lane, g.lanes, C, dg);
-          } else {
-            store<float, VEC>(reinterpret_cast<char*>(p.gate_part + (size_t)was.item * C), g.lane, g.lanes, C, dg);
-          }
+        const bool writes = owns && (!p.by_cta || g.slot == 0);
+        if (p.segs == 1) {
+          const RowPos rg = row_pos(p.gate_of, was.gate_row * p.share);
+          store<TI, VEC>(writes, row_ptr(p.dgate, rg, p.gate_of), g.lane, g.lanes, C, dg);
+        } else {
+          store<float, VEC>(writes, reinterpret_cast<char*>(p.gate_part + (size_t)was.item * C), g.lane, g.lanes, C, dg);
         }
       }
     }

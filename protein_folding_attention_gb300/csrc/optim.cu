@@ -34,8 +34,7 @@ constexpr int kBlock = EVOATTN_ADAMW_BLOCK;  // elements a warp works on at a ti
 static_assert(kBlock == 256, "a lane holds 8 elements of a block");
 constexpr int kStepCtas = 608;   // CTAs of a step's launch at most
 constexpr int kNormCtas = 1216;  // partial sums of a norm's launch at most
-constexpr int kNormUnroll = 4;
-constexpr int kNormChunk = kNormUnroll * kThreads * 8;  // elements a CTA sums at a time
+constexpr int kNormUnroll = 4;   // blocks a warp loads before it sums them
 
 // Flags of a tensor, above the 48 bits of its element count.
 constexpr uint64_t kGradBf16 = 1ull << 48, kVec = 1ull << 49, kCount = (1ull << 48) - 1;
@@ -94,6 +93,7 @@ struct NormParams {
   double* part_all;
   int parts_before, last;
   float max_norm;
+  uint32_t blocks;
 };
 static_assert(sizeof(StepParams<false, kManyTensors<false>>) <= 32764 &&
                   sizeof(StepParams<true, kManyTensors<true>>) <= 32764 &&
@@ -153,7 +153,8 @@ __device__ __forceinline__ int element(int lane, int k) { return (k >> 2) * 128 
 template <bool BITS8>
 struct Ring {
   static constexpr uint32_t G = 1024, M = 2048, V = BITS8 ? 2304 : 3072;
-  [[maybe_unused]] static constexpr uint32_t S = 2560;
+  static constexpr uint32_t S = 2560;
+  static_assert(!BITS8 || S + 8 <= 2576, "the scales are a stage's last");
   static constexpr uint32_t STAGE = BITS8 ? 2576 : 4096;
   static constexpr int STAGES = BITS8 ? 4 : 3;  // two CTAs per SM
   static constexpr uint32_t BYTES = STAGE * STAGES * kWarps;
@@ -405,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   copies_wait<0>();
 }
 
-// Sum over a CTA in fp64, valid in thread 0.
+// Sum over a CTA, valid in thread 0.  (fp64 arithmetic is slow on this part,
+// so only few fp64 additions are made.)
 __device__ __forceinline__ double cta_sum(double v) {
   __shared__ double part[kWarps];
 #pragma unroll
@@ -418,69 +420,97 @@ __device__ __forceinline__ double cta_sum(double v) {
   return v;
 }
 
-// A CTA takes an even share of the chunks of all tensors in order.  The last
-// CTA to finish adds all partial sums in order, so the order of arrival
-// changes nothing.
+// A CTA takes an even share of consecutive blocks, its warps every eighth of
+// them, four at a time.  A block's squares are summed in fp32 (8 per lane),
+// the blocks' sums with their rounding errors carried along.  The last CTA to
+// finish adds all partial sums in order, so the order of arrival changes
+// nothing.
 template <int T>
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormParams<T> P,
-                                                        uint32_t chunks) {
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormParams<T> P) {
   wait_for_earlier_work();
   let_next_start();
-  uint32_t chunk = (uint32_t)((uint64_t)chunks * blockIdx.x / gridDim.x);
-  const uint32_t end = (uint32_t)((uint64_t)chunks * (blockIdx.x + 1) / gridDim.x);
-  double total = 0.0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t b = (uint32_t)((uint64_t)P.blocks * blockIdx.x / gridDim.x) + warp;
+  const uint32_t end = (uint32_t)((uint64_t)P.blocks * (blockIdx.x + 1) / gridDim.x);
   int i = P.first[blockIdx.x];
-  for (; chunk < end; ++chunk) {
-    while (chunk >= P.start[i + 1]) ++i;
-    const NormEntry& e = P.e[i];
-    const int64_t n = (int64_t)(e.n & kCount), base = (int64_t)(chunk - P.start[i]) * kNormChunk;
-    const bool vec = (e.n & kVec) && base + kNormChunk <= n;
-    float s[kNormUnroll];
+  float sum = 0.f, low = 0.f;
+  for (; b < end; b += kNormUnroll * kWarps) {
+    uint4 w[kNormUnroll][2];
+    int kind[kNormUnroll];  // 0 nothing, 1 bf16, 2 fp32 (as loaded), 3 a partial sum
 #pragma unroll
-    for (int u = 0; u < kNormUnroll; ++u) s[u] = 0.f;
-    if (vec && (e.n & kGradBf16)) {
-      uint4 w[kNormUnroll];
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.g) + base + 8 * threadIdx.x;
-#pragma unroll
-      for (int u = 0; u < kNormUnroll; ++u)
-        w[u] = *reinterpret_cast<const uint4*>(src + u * kThreads * 8);
-#pragma unroll
-      for (int u = 0; u < kNormUnroll; ++u) {
-        const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          s[u] = fmaf(bf16lo(q[k]), bf16lo(q[k]), s[u]);
-          s[u] = fmaf(bf16hi(q[k]), bf16hi(q[k]), s[u]);
+    for (int u = 0; u < kNormUnroll; ++u) {
+      kind[u] = 0;
+      const uint32_t at = b + u * kWarps;
+      if (at >= end) continue;
+      while (at >= P.start[i + 1]) ++i;
+      const NormEntry& e = P.e[i];
+      const int64_t n = (int64_t)(e.n & kCount), base = (int64_t)(at - P.start[i]) * kBlock;
+      if ((e.n & kVec) && base + kBlock <= n) {
+        if (e.n & kGradBf16) {
+          w[u][0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.g) + base + 8 * lane);
+          kind[u] = 1;
+        } else {
+          const float* g = static_cast<const float*>(e.g) + base + 4 * lane;
+          w[u][0] = *reinterpret_cast<const uint4*>(g);
+          w[u][1] = *reinterpret_cast<const uint4*>(g + 128);
+          kind[u] = 2;
         }
-      }
-    } else if (vec) {
-      float4 w[2 * kNormUnroll];
-      const float* src = static_cast<const float*>(e.g) + base + 4 * threadIdx.x;
+      } else {
+        float s = 0.f;
 #pragma unroll
-      for (int u = 0; u < 2 * kNormUnroll; ++u)
-        w[u] = *reinterpret_cast<const float4*>(src + u * kThreads * 4);
-#pragma unroll
-      for (int u = 0; u < 2 * kNormUnroll; ++u) {
-        float& d = s[u >> 1];
-        d = fmaf(w[u].x, w[u].x, d);
-        d = fmaf(w[u].y, w[u].y, d);
-        d = fmaf(w[u].z, w[u].z, d);
-        d = fmaf(w[u].w, w[u].w, d);
-      }
-    } else {
-      const int64_t stop = min(n, base + (int64_t)kNormChunk);
-#pragma unroll 4
-      for (int64_t a = base + threadIdx.x; a < stop; a += kThreads) {
-        const float g = (e.n & kGradBf16) ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[a])
-                                          : static_cast<const float*>(e.g)[a];
-        s[0] = fmaf(g, g, s[0]);
+        for (int k = 0; k < 8; ++k) {
+          const int64_t a = base + k * 32 + lane;
+          const float g = a >= n ? 0.f
+                          : (e.n & kGradBf16) ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[a])
+                                              : static_cast<const float*>(e.g)[a];
+          s = fmaf(g, g, s);
+        }
+        w[u][0].x = __float_as_uint(s);
+        kind[u] = 3;
       }
     }
-    total += (double)((s[0] + s[1]) + (s[2] + s[3]));
+#pragma unroll
+    for (int u = 0; u < kNormUnroll; ++u) {
+      const uint4 x = w[u][0], y = w[u][1];
+      float s = 0.f;
+      if (kind[u] == 1) {
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+        float2 t = both(0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 g = make_float2(bf16lo(q[k]), bf16hi(q[k]));
+          t = fma2(g, g, t);
+        }
+        s = t.x + t.y;
+      } else if (kind[u] == 2) {
+        const uint32_t q[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        float2 t = both(0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 g = make_float2(__uint_as_float(q[2 * k]), __uint_as_float(q[2 * k + 1]));
+          t = fma2(g, g, t);
+        }
+        s = t.x + t.y;
+      } else if (kind[u] == 3) {
+        s = __uint_as_float(x.x);
+      }
+      // sum + s exactly, as a rounded sum and its error (Knuth's two-sum)
+      const float t = sum + s, back = t - sum;
+      low += (sum - (t - back)) + (s - back);
+      sum = t;
+    }
   }
-  total = cta_sum(total);
+  // (an infinite sum's error would be NaN: the norm is infinite either way)
+  float mine = isfinite(sum) ? sum + low : sum;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  __shared__ float part[kWarps];
   __shared__ int is_last;
+  if (lane == 0) part[warp] = mine;
+  __syncthreads();
   if (threadIdx.x == 0) {
+    double total = 0.0;
+    for (int k = 0; k < kWarps; ++k) total += (double)part[k];
     P.part[blockIdx.x] = total;
     __threadfence();
     is_last = P.last && atomicAdd(&P.state->ticket[1], 1u) == gridDim.x - 1;
@@ -492,7 +522,6 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
   const int parts = P.parts_before + (int)gridDim.x;
   double all = 0.0;
   for (int k = threadIdx.x; k < parts; k += kThreads) all += __ldcg(P.part_all + k);
-  __syncthreads();  // cta_sum's shared sums are reused
   all = cta_sum(all);
   if (threadIdx.x == 0) {
     const float norm = (float)sqrt(all);
@@ -616,16 +645,17 @@ cudaError_t norm_part(const evoattn_adamw_tensor* t, int count, float max_norm,
                       cudaStream_t st) {
   static std::atomic<int> cache[64];
   NormParams<T> P;
-  uint64_t chunks = 0;
+  uint64_t blocks = 0;
   int k = 0;
   for (int i = 0; i < count; ++i) {
     if (t[i].n == 0) continue;
     P.e[k] = NormEntry{t[i].grad, grad_flags(t[i])};
-    P.start[k++] = (uint32_t)chunks;
-    chunks += (uint64_t)(t[i].n + kNormChunk - 1) / kNormChunk;
-    if (chunks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    P.start[k++] = (uint32_t)blocks;
+    blocks += (uint64_t)(t[i].n + kBlock - 1) / kBlock;
+    if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
   }
-  P.start[k] = (uint32_t)chunks;
+  P.start[k] = (uint32_t)blocks;
+  P.blocks = (uint32_t)blocks;
   P.state = state;
   P.part_all = part_all;
   P.part = part_all + *parts;
@@ -635,11 +665,12 @@ cudaError_t norm_part(const evoattn_adamw_tensor* t, int count, float max_norm,
   int ctas = 0;
   cudaError_t e = resident_ctas(k_grad_norm<T>, 0, cache, &ctas);
   if (e != cudaSuccess) return e;
-  const unsigned grid =
-      (unsigned)std::min<uint64_t>(std::max<uint64_t>(chunks, 1), (uint64_t)std::min(ctas, kNormCtas));
-  first_tensors(P.first, grid, chunks, [&](int i) { return P.start[i]; });
+  // a CTA for every 8 blocks (one per warp), at least one for the bookkeeping
+  const uint64_t want = std::max<uint64_t>(1, (blocks + kWarps - 1) / kWarps);
+  const unsigned grid = (unsigned)std::min<uint64_t>(want, (uint64_t)std::min(ctas, kNormCtas));
+  first_tensors(P.first, grid, blocks, [&](int i) { return P.start[i]; });
   *parts += (int)grid;
-  return launch_early(k_grad_norm<T>, grid, kThreads, 0, st, P, (uint32_t)chunks);
+  return launch_early(k_grad_norm<T>, grid, kThreads, 0, st, P);
 }
 
 }  // namespace
