@@ -511,7 +511,7 @@ evoattn_status evoattn_grad_norm(const evoattn_adamw_tensor* tensors, int count,
  *               full speed).
  *  lr         : >= 0; lr_device, when not NULL, is a device fp32 scalar read
  *               by the kernel instead (a captured graph then follows it).
- *  beta1, beta2 in [0, 1), eps > 0.
+ *  beta1, beta2 in [0, 1), eps a normal fp32 number > 0.
  *  state_bits : 32 or 8.
  *  flags      : 0 or EVOATTN_ADAMW_CLIP: multiply the gradients by state->clip,
  *               and when state->skip is set change nothing, not even step.

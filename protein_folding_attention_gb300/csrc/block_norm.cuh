@@ -19,6 +19,8 @@
 //   du = rstd (b - mean(b) - k mean(b k))
 //   dgamma_pre = sum dy h      dbeta_pre = sum dy
 //
+// With A = sum D q k and B = sum D q, kept per channel, dscale is
+// gamma_post A + beta_post B, dgamma_post is scale A and dbeta_post scale B.
 // (rms: mean = 0 and no mean(a), mean(b) terms.)  Everything is held in fp32;
 // each stored tensor is rounded once.  Bound by HBM: 10 bytes per element
 // forward and 16 backward in bf16, against about 20 and 50 fp32 operations.
@@ -48,6 +50,7 @@
 namespace evo {
 namespace norm {
 
+constexpr int kSums = 4;          // vectors that the backward sums over rows
 constexpr int kE = 8;             // channels per thread
 constexpr int kP = kE / 2;        // pairs of channels (packed fp32 arithmetic)
 constexpr int kThreads = 256;     // threads of a CTA where a row takes at most 8 warps
@@ -113,8 +116,9 @@ struct Params {
   float eps, inv_c;
   Operand x, u, gate, x1, y, dx1, dy, dx, du, dgate;
   const float *scale, *gamma_post, *beta_post, *gamma_pre, *beta_pre;
-  float* out[5];  // dscale, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre
-  float* part;    // [CTAs][5][C]
+  float *dscale, *dgamma_post, *dbeta_post, *dgamma_pre, *dbeta_pre;
+  bool wanted[2];  // any gradient of the post-norm's, of the pre-norm's parameters
+  float* part;     // [CTAs][kSums][C]
   // a gate row shared by `share` consecutive rows: `segs` items of at most
   // `seg_rows` rows each per gate row
   uint32_t share, segs, seg_rows, items;
@@ -627,10 +631,10 @@ struct BwdRing {
   static constexpr size_t bytes(int threads) { return (size_t)STAGES * stage(threads); }
 };
 
-// Shared memory of the backward: a row of sums per group, and with a ring four
+// Shared memory of the backward: a row of sums per group, and with a ring three
 // parameter vectors by thread of a group.
 constexpr size_t bwd_sums_bytes(int threads) { return (size_t)threads * kE * 4; }
-constexpr size_t bwd_params_bytes(int lanes) { return (size_t)lanes * kE * 4 * 4; }
+constexpr size_t bwd_params_bytes(int lanes) { return (size_t)lanes * kE * 4 * 3; }
 
 // GROUPED: gate rows shared by consecutive rows, whose gradients are summed.
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED,
@@ -651,14 +655,19 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   // parameters: [vector][half][lane] float4, read back without bank conflicts
   float4* const prm = reinterpret_cast<float4*>(smem + bwd_sums_bytes(blockDim.x));
   char* const ring = reinterpret_cast<char*>(prm) + bwd_params_bytes(g.lanes);
+  // scale * gamma_post, scale * beta_post, gamma_pre
   auto read = [&](int k) {
-    const float* src = k == 0 ? p.scale : k == 1 ? p.gamma_post : k == 2 ? p.beta_post : p.gamma_pre;
-    return param<VEC>(src, k == 2 ? 0.f : 1.f, g.lane, g.lanes, C);
+    if (k == 2) return param<VEC>(p.gamma_pre, 1.f, g.lane, g.lanes, C);
+    V v = param<VEC>(k == 0 ? p.gamma_post : p.beta_post, k == 0 ? 1.f : 0.f, g.lane, g.lanes, C);
+    const V s = param<VEC>(p.scale, 1.f, g.lane, g.lanes, C);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) v.p[j] = mul2(v.p[j], s.p[j]);
+    return v;
   };
   if (RING) {
     if (g.slot == 0) {
 #pragma unroll
-      for (int k = POST ? 0 : 3; k < (PRE ? 4 : 3); ++k) {
+      for (int k = POST ? 0 : 2; k < (PRE ? 3 : 2); ++k) {
         const V v = read(k);
         prm[(2 * k) * g.lanes + g.lane] = make_float4(v[0], v[1], v[2], v[3]);
         prm[(2 * k + 1) * g.lanes + g.lane] = make_float4(v[4], v[5], v[6], v[7]);
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   };
 
   const V zero{{both(0.f), both(0.f), both(0.f), both(0.f)}};
-  V acc[5] = {zero, zero, zero, zero, zero};
+  V acc[4] = {zero, zero, zero, zero};                // sums of D q k, D q, dy h, dy
   V q{{both(1.f), both(1.f), both(1.f), both(1.f)}};  // sigmoid(gate)
   V dg = zero;                                        // the gate's gradient
 
@@ -777,11 +786,11 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     else if (PRE) rstd.x = standardise<G, VEC>(h, g, p);
     else rstd.y = standardise<G, VEC>(u, g, p);
     if (PRE) {
-      const V g2 = get(3);
+      const V g2 = get(2);
 #pragma unroll
       for (int k = 0; k < kP; ++k) {
-        acc[3].p[k] = fma2(dy.p[k], h.p[k], acc[3].p[k]);
-        acc[4].p[k] = add2(acc[4].p[k], dy.p[k]);
+        acc[2].p[k] = fma2(dy.p[k], h.p[k], acc[2].p[k]);
+        acc[3].p[k] = add2(acc[3].p[k], dy.p[k]);
         dy.p[k] = mul2(dy.p[k], g2.p[k]);
       }
       float2 s = make_float2(sum(dy), dot(dy, h));
@@ -797,21 +806,19 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
         q = gt;
         sigmoid(q);
       }
-      const V sc = get(0), g1 = get(1), b1 = get(2);
+      const V g1 = get(0), b1 = get(1);
       V b;
 #pragma unroll
       for (int k = 0; k < kP; ++k) {
-        const float2 w = fma2(u.p[k], g1.p[k], b1.p[k]);
+        const float2 w = fma2(u.p[k], g1.p[k], b1.p[k]);  // (with the scale)
         const float2 dq = mul2(D.p[k], q.p[k]);
-        acc[0].p[k] = fma2(dq, w, acc[0].p[k]);
-        const float2 e = mul2(dq, sc.p[k]);
+        acc[0].p[k] = fma2(dq, u.p[k], acc[0].p[k]);
+        acc[1].p[k] = add2(acc[1].p[k], dq);
         if (GROUPED)
-          dg.p[k] = fma2(e, w, dg.p[k]);  // (1 - q) is applied once, at the end
+          dg.p[k] = fma2(dq, w, dg.p[k]);  // (1 - q) is applied once, at the end
         else
-          dg.p[k] = mul2(mul2(e, w), fma2(q.p[k], both(-1.f), both(1.f)));
-        acc[1].p[k] = fma2(e, u.p[k], acc[1].p[k]);
-        acc[2].p[k] = add2(acc[2].p[k], e);
-        b.p[k] = mul2(e, g1.p[k]);
+          dg.p[k] = mul2(mul2(dq, w), fma2(q.p[k], both(-1.f), both(1.f)));
+        b.p[k] = mul2(dq, g1.p[k]);
       }
       float2 s = make_float2(sum(b), dot(b, u));
       s = group_sum<G>(g.act ? s : both(0.f), g);
@@ -856,16 +863,16 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   }
 
   let_next_start();
-  // the CTA's sums of the parameter gradients, group by group in order
+  // the CTA's sums, group by group in order
   const int width = g.lanes * kE;
 #pragma unroll
-  for (int k = POST ? 0 : 3; k < (PRE ? 5 : 3); ++k) {
-    if (p.out[k] == nullptr) continue;
+  for (int k = POST ? 0 : 2; k < (PRE ? 4 : 2); ++k) {
+    if (!p.wanted[k >> 1]) continue;
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < kE; ++e) red[g.slot * width + channel<VEC>(g.lane, g.lanes, e)] = acc[k][e];
     __syncthreads();
-    float* dst = gridDim.x == 1 ? p.out[k] : p.part + ((size_t)blockIdx.x * 5 + k) * C;
+    float* dst = p.part + ((size_t)blockIdx.x * kSums + k) * C;
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
       float s = 0.f;
       for (int i = 0; i < g.slots; ++i) s += red[i * width + c];
@@ -1028,41 +1035,53 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
   pl.slots = pl.threads / p.lanes;
 }
 
-// Sums of the CTAs' partial sums: one block per 32 columns of one of the five
-// parameter gradients or of one gate row, 32 warps taking every 32nd partial.
-// Launched while the kernel before it drains, it waits for that one's end.
+// Sums of the CTAs' partial sums: one block per 32 columns of the post-norm's
+// sums, of the pre-norm's, or of one gate row, 32 warps taking every 32nd
+// partial sum.
 constexpr int kReduceWarps = 32;
 template <typename TI>
 __global__ void __launch_bounds__(kReduceWarps * 32)
     k_block_norm_reduce(const __grid_constant__ Params p, int ctas, int param_blocks) {
-  __shared__ float red[kReduceWarps][32];
+  __shared__ float2 red[kReduceWarps][32];
   wait_for_earlier_work();
   const int per = (p.C + 31) / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int blk = blockIdx.x;
-  const bool is_param = blk < param_blocks;
-  const int what = (is_param ? blk : blk - param_blocks) / per;
-  const int c = ((is_param ? blk : blk - param_blocks) - what * per) * 32 + lane;
-  if (is_param && p.out[what] == nullptr) return;
-  const int depth = is_param ? ctas : (int)p.segs;
-  const float* src = is_param ? p.part + (size_t)what * p.C : p.gate_part + (size_t)what * p.segs * p.C;
-  const size_t stride = (size_t)p.C * (is_param ? 5 : 1);
-  float s = 0.f;
+  const bool is_param = (int)blockIdx.x < param_blocks;
+  const int blk = is_param ? blockIdx.x : blockIdx.x - param_blocks;
+  const int what = blk / per, c = (blk - what * per) * 32 + lane;
+  if (is_param && !p.wanted[what]) return;
+  float2 s = both(0.f);
   if (c < p.C) {
+    if (is_param) {
+      const float* src = p.part + (size_t)(2 * what) * p.C + c;
 #pragma unroll 4
-    for (int i = warp; i < depth; i += kReduceWarps) s += src[i * stride + c];
+      for (int i = warp; i < ctas; i += kReduceWarps) {
+        const float* at = src + (size_t)i * kSums * p.C;
+        s = add2(s, make_float2(at[0], at[p.C]));
+      }
+    } else {
+      const float* src = p.gate_part + (size_t)what * p.segs * p.C + c;
+#pragma unroll 4
+      for (int i = warp; i < (int)p.segs; i += kReduceWarps) s.x += src[(size_t)i * p.C];
+    }
   }
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < p.C) {
+  if (warp != 0 || c >= p.C) return;
 #pragma unroll
-    for (int i = 1; i < kReduceWarps; ++i) s += red[i][lane];
-    if (is_param) {
-      p.out[what][c] = s;
-    } else {
-      char* row = row_ptr(p.dgate, row_pos(p.gate_of, (uint32_t)what * p.share), p.gate_of);
-      reinterpret_cast<TI*>(row)[c] = static_cast<TI>(s);
-    }
+  for (int i = 1; i < kReduceWarps; ++i) s = add2(s, red[i][lane]);
+  if (!is_param) {
+    char* row = row_ptr(p.dgate, row_pos(p.gate_of, (uint32_t)what * p.share), p.gate_of);
+    reinterpret_cast<TI*>(row)[c] = static_cast<TI>(s.x);
+  } else if (what == 0) {
+    const float sc = p.scale ? p.scale[c] : 1.f;
+    if (p.dscale)
+      p.dscale[c] = (p.gamma_post ? p.gamma_post[c] : 1.f) * s.x + (p.beta_post ? p.beta_post[c] : 0.f) * s.y;
+    if (p.dgamma_post) p.dgamma_post[c] = sc * s.x;
+    if (p.dbeta_post) p.dbeta_post[c] = sc * s.y;
+  } else {
+    if (p.dgamma_pre) p.dgamma_pre[c] = s.x;
+    if (p.dbeta_pre) p.dbeta_pre[c] = s.y;
   }
 }
 
@@ -1115,13 +1134,11 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   }
   const unsigned grid = std::min<unsigned>(need, (unsigned)ctas);
   p.part = ws;
-  p.gate_part = ws + (size_t)kNormMaxCtas * 5 * p.C;
+  p.gate_part = ws + (size_t)kNormMaxCtas * kSums * p.C;
   e = launch_early(kern, grid, pl.threads, smem, st, p);
   if (e != cudaSuccess) return e;
   const int per = (p.C + 31) / 32;
-  bool any = false;
-  for (int k = 0; k < 5; ++k) any = any || p.out[k] != nullptr;
-  const int param_blocks = any && grid > 1 ? 5 * per : 0;
+  const int param_blocks = p.wanted[0] || p.wanted[1] ? 2 * per : 0;
   const int gate_blocks = GROUPED && p.segs > 1 ? (int)(p.rows / p.share) * per : 0;
   if (param_blocks + gate_blocks > 0) {
     e = launch_early(k_block_norm_reduce<TI>, param_blocks + gate_blocks, kReduceWarps * 32, 0, st, p, (int)grid,
@@ -1194,11 +1211,13 @@ cudaError_t run_bwd(const BlockNormCall& c, cudaStream_t st) {
   const bool stream[] = {true, true, false, false, false, true, false, false};
   const bool gates[] = {false, false, false, true, false, false, false, true};
   make_plan(c, ops, dst, es, stream, gates, 8, 3, pl);
-  p.out[0] = c.dscale;
-  p.out[1] = c.dgamma_post;
-  p.out[2] = c.dbeta_post;
-  p.out[3] = c.dgamma_pre;
-  p.out[4] = c.dbeta_pre;
+  p.dscale = c.dscale;
+  p.dgamma_post = c.dgamma_post;
+  p.dbeta_post = c.dbeta_post;
+  p.dgamma_pre = c.dgamma_pre;
+  p.dbeta_pre = c.dbeta_pre;
+  p.wanted[0] = c.dscale || c.dgamma_post || c.dbeta_post;
+  p.wanted[1] = c.dgamma_pre || c.dbeta_pre;
   const bool grouped = c.gate.p && p.share > 1;
   if (c.u.p && c.dy.p)
     return grouped ? dispatch_bwd<TS, TI, true, true, true>(pl, c.ws, st)

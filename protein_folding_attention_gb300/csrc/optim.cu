@@ -8,9 +8,11 @@
 //
 // The tensors of a launch are a table in the kernel's parameters (no copy to
 // the device, nothing to keep alive, and a captured launch carries its own
-// table).  All tensors are cut into blocks of 256 elements; a CTA takes an
-// even share of consecutive blocks, its warps every eighth of them, so small
-// tensors cost a block each and no CTA waits for another.  Each warp copies
+// table).  All tensors are cut into blocks of 256 elements; small tensors cost
+// a block each.  All warps of the launch sweep over the blocks together, a
+// block each at a time: the memory then sees a few narrow fronts that move
+// on, not a stream per CTA (107M parameters with 8-bit states: 355 us with a
+// consecutive share of the blocks for each CTA, 264 us so).  Each warp copies
 // its coming blocks into a ring in shared memory (cp.async): what is in flight
 // does not depend on how many warps are between loading and storing.
 #include <cuda_bf16.h>
@@ -32,9 +34,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = EVOATTN_ADAMW_BLOCK;  // elements a warp works on at a time
 static_assert(kBlock == 256, "a lane holds 8 elements of a block");
-constexpr int kStepCtas = 608;   // CTAs of a step's launch at most
-constexpr int kNormCtas = 1216;  // partial sums of a norm's launch at most
-constexpr int kNormUnroll = 4;   // blocks a warp loads before it sums them
+constexpr int kCoarse = 1024;    // entries of the table from blocks to tensors
+constexpr int kNormCtas = 912;   // partial sums of a norm's launch at most
+constexpr int kNormUnroll = 4;   // blocks that a warp of the norm loads at once
+constexpr int kNormUnit = kNormUnroll * kBlock;
 
 // Flags of a tensor, above the 48 bits of its element count.
 constexpr uint64_t kGradBf16 = 1ull << 48, kVec = 1ull << 49, kCount = (1ull << 48) - 1;
@@ -69,11 +72,12 @@ constexpr int kFewTensors = 32;
 
 template <bool BITS8, int T>
 struct StepParams {
-  Entry<BITS8> e[T + 1];     // (the last one's successor holds the end)
-  uint16_t first[kStepCtas];  // the tensor that each CTA begins in
+  Entry<BITS8> e[T + 1];    // (the last one's successor holds the end)
+  uint16_t coarse[kCoarse];  // the tensor that holds block k << shift
+  int shift;
   evoattn_optim_state* state;
   const float* lr_device;
-  float lr, b1, b1_low, b1c, b1c_low, b2, b2c, log_b1, log_b2, eps;
+  float lr, b1, b1c, b2, b2c, log_b1, log_b2, eps;
   int clip, last;  // last: this launch counts the step up
   uint32_t blocks;
 };
@@ -87,13 +91,14 @@ template <int T>
 struct NormParams {
   NormEntry e[T];
   uint32_t start[T + 1];
-  uint16_t first[kNormCtas];
+  uint16_t coarse[kCoarse];
+  int shift;
   evoattn_optim_state* state;
   double* part;      // this launch's partial sums; all launches' begin at part_all
   double* part_all;
   int parts_before, last;
   float max_norm;
-  uint32_t blocks;
+  uint32_t units;
 };
 static_assert(sizeof(StepParams<false, kManyTensors<false>>) <= 32764 &&
                   sizeof(StepParams<true, kManyTensors<true>>) <= 32764 &&
@@ -133,6 +138,18 @@ __device__ __forceinline__ float sqrt_approx(float a) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
+__device__ __forceinline__ float rcp_approx(float a) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+// 448 / top (0 for a block that is held as zeros), the approximate quotient
+// corrected by its own remainder.
+constexpr float kLeast = 0x1p-100f;
+__device__ __forceinline__ float inverse448(float top) {
+  const float y = rcp_approx(top), q = 448.f * y;
+  return top >= kLeast ? fmaf(fmaf(-q, top, 448.f), y, q) : 0.f;
+}
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 __device__ __forceinline__ float2 warp_max(float2 v) {
@@ -149,29 +166,51 @@ __device__ __forceinline__ float2 warp_max(float2 v) {
 __device__ __forceinline__ int element(int lane, int k) { return (k >> 2) * 128 + 4 * lane + (k & 3); }
 
 // A warp's stage of the ring: p, g (bf16 in the first half), then m and v,
-// and with 8 bits their scales.
+// and with 8 bits their scales.  As many stages as leave room for one CTA per
+// SM: 8 warps with 6 stages run at 96 % of the copy rate (264 us for 107M
+// parameters), 16 warps with 4 stages at 87 % (293 us; the fronts are wider).
 template <bool BITS8>
 struct Ring {
   static constexpr uint32_t G = 1024, M = 2048, V = BITS8 ? 2304 : 3072;
   static constexpr uint32_t S = 2560;
   static_assert(!BITS8 || S + 8 <= 2576, "the scales are a stage's last");
   static constexpr uint32_t STAGE = BITS8 ? 2576 : 4096;
-  static constexpr int STAGES = BITS8 ? 4 : 3;  // two CTAs per SM
+  static constexpr int STAGES = BITS8 ? 6 : 4;
   static constexpr uint32_t BYTES = STAGE * STAGES * kWarps;
 };
 
-// Where a warp is: a block and the tensor that holds it.
+// Where a warp is: a block, the tensor that holds it, and that tensor's
+// addresses as the lane uses them (looked up when a tensor begins).
 template <bool BITS8, int T>
 struct Cursor {
-  uint32_t b;
+  uint32_t b, start, next;  // block; first block of this tensor and of the next
+  uint32_t full;            // blocks of it that can be copied whole
   int i;
-  __device__ __forceinline__ void settle(const StepParams<BITS8, T>& P) {
+  bool bf16;
+  const char *p, *g, *m, *v, *s;
+
+  __device__ __forceinline__ void open(const StepParams<BITS8, T>& P, int lane) {
+    i = P.coarse[b >> P.shift];
     while (b >= P.e[i + 1].start) ++i;
+    const Entry<BITS8>& e = P.e[i];
+    start = e.start;
+    next = P.e[i + 1].start;
+    full = e.n & kVec ? (uint32_t)((e.n & kCount) / kBlock) : 0u;
+    bf16 = (e.n & kGradBf16) != 0;
+    p = reinterpret_cast<const char*>(e.p) + lane * 16;
+    g = static_cast<const char*>(e.g) + lane * 16;
+    if constexpr (BITS8) {  // half a warp's copies each; two lanes copy the scales
+      m = static_cast<const char*>(lane < 16 ? e.m : e.v) + (lane & 15) * 16;
+      s = reinterpret_cast<const char*>(lane == 0 ? e.ms : e.vs);
+    } else {
+      m = static_cast<const char*>(e.m) + lane * 16;
+      v = static_cast<const char*>(e.v) + lane * 16;
+    }
   }
 };
 
 template <bool BITS8, int T>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     k_adamw(const __grid_constant__ StepParams<BITS8, T> P) {
   using R = Ring<BITS8>;
   extern __shared__ __align__(16) char smem[];
@@ -196,51 +235,41 @@ __global__ void __launch_bounds__(kThreads, 2)
   // 1 - b^t without cancellation
   const float c1 = -expm1f(t * P.log_b1), c2 = -expm1f(t * P.log_b2);
   const float rate = lr / c1, root = rsqrtf(c2);
-  // (1 - b1) clip as the sum of two floats
-  const float gm = P.b1c * clip, gm_low = fmaf(P.b1c, clip, -gm) + P.b1c_low * clip;
+  const float gm = P.b1c * clip;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t end = (uint32_t)((uint64_t)P.blocks * (blockIdx.x + 1) / gridDim.x);
-  Cursor<BITS8, T> at{(uint32_t)((uint64_t)P.blocks * blockIdx.x / gridDim.x) + warp, P.first[blockIdx.x]};
+  const uint32_t end = P.blocks, hop = gridDim.x * kWarps;
+  Cursor<BITS8, T> at;
+  at.b = blockIdx.x * kWarps + warp;
+  if (at.b >= end) return;
+  at.open(P, lane);
   char* const ring = smem + warp * (R::STAGE * R::STAGES);
   const uint32_t ring_s = smem_u32(ring);
 
-  auto whole = [&](const Entry<BITS8>& e, int64_t base) {
-    return (e.n & kVec) && base + kBlock <= (int64_t)(e.n & kCount);
-  };
   auto fetch = [&](int stage, Cursor<BITS8, T>& c) {
     if (c.b < end) {
-      c.settle(P);
-      const Entry<BITS8>& e = P.e[c.i];
-      const int64_t base = (int64_t)(c.b - e.start) * kBlock;
-      if (whole(e, base)) {
+      if (c.b >= c.next) c.open(P, lane);
+      const uint32_t rel = c.b - c.start;
+      if (rel < c.full) {
         const uint32_t to = ring_s + stage * R::STAGE + lane * 16;
-        const float* p = e.p + base + 4 * lane;
+        const char* p = c.p + (uint64_t)rel * (kBlock * 4);
         copy16(to, p);
-        copy16(to + 512, p + 128);
-        if (e.n & kGradBf16) {
-          copy16(to + R::G, static_cast<const __nv_bfloat16*>(e.g) + base + 8 * lane);
-        } else {
-          const float* g = static_cast<const float*>(e.g) + base + 4 * lane;
-          copy16(to + R::G, g);
-          copy16(to + R::G + 512, g + 128);
-        }
+        copy16(to + 512, p + 512);
+        const char* g = c.g + (uint64_t)rel * (c.bf16 ? kBlock * 2 : kBlock * 4);
+        copy16(to + R::G, g);
+        if (!c.bf16) copy16(to + R::G + 512, g + 512);
         if constexpr (BITS8) {
-          // 256 bytes of each: half a warp's copies
-          const char* src = static_cast<const char*>(lane < 16 ? e.m : e.v) + base + (lane & 15) * 16;
-          copy16(to + R::M, src);  // (V follows M by 256 bytes)
-          if (lane < 2)
-            copy4(ring_s + stage * R::STAGE + R::S + 4 * lane, (lane == 0 ? e.ms : e.vs) + base / kBlock);
+          copy16(to + R::M, c.m + (uint64_t)rel * kBlock);  // (V follows M by 256 bytes)
+          if (lane < 2) copy4(ring_s + stage * R::STAGE + R::S + 4 * lane, c.s + (uint64_t)rel * 4);
         } else {
-          const float *m = static_cast<const float*>(e.m) + base + 4 * lane,
-                      *v = static_cast<const float*>(e.v) + base + 4 * lane;
+          const char *m = c.m + (uint64_t)rel * (kBlock * 4), *v = c.v + (uint64_t)rel * (kBlock * 4);
           copy16(to + R::M, m);
-          copy16(to + R::M + 512, m + 128);
+          copy16(to + R::M + 512, m + 512);
           copy16(to + R::V, v);
-          copy16(to + R::V + 512, v + 128);
+          copy16(to + R::V + 512, v + 512);
         }
       }
-      c.b += kWarps;
+      c.b += hop;
     }
     copies_close();
   };
@@ -249,11 +278,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
   for (int s = 0; s < R::STAGES - 1; ++s) fetch(s, ahead);
   int stage = 0;
-  for (; at.b < end; at.b += kWarps) {
-    at.settle(P);
+  for (; at.b < end; at.b += hop) {
+    if (at.b >= at.next) at.open(P, lane);
     const Entry<BITS8>& e = P.e[at.i];
-    const int64_t n = (int64_t)(e.n & kCount), base = (int64_t)(at.b - e.start) * kBlock;
-    const bool vec = whole(e, base);
+    const uint32_t rel = at.b - at.start;
+    const bool vec = rel < at.full;
+    const int64_t base = (int64_t)rel * kBlock;
     __syncwarp();  // the warp has read the stage that is filled next
     fetch(stage == 0 ? R::STAGES - 1 : stage - 1, ahead);
     copies_wait<R::STAGES - 1>();
@@ -272,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           d[2 * h + 1] = make_float2(q.z, q.w);
         };
         four(0, p);
-        if (e.n & kGradBf16) {
+        if (at.bf16) {
           const uint2 w = *reinterpret_cast<const uint2*>(from + R::G + h * 256 + lane * 8);
           g[2 * h] = make_float2(bf16lo(w.x), bf16hi(w.x));
           g[2 * h + 1] = make_float2(bf16lo(w.y), bf16hi(w.y));
@@ -292,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         vs = *reinterpret_cast<const float*>(from + R::S + 4);
       }
     } else {
+      const int64_t n = (int64_t)(e.n & kCount);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int64_t a = base + element(lane, k);
@@ -299,8 +330,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto put = [&](float2* d, float x) { (k & 1 ? d[k >> 1].y : d[k >> 1].x) = x; };
         put(p, ok ? e.p[a] : 0.f);
         put(g, !ok ? 0.f
-                   : (e.n & kGradBf16) ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[a])
-                                       : static_cast<const float*>(e.g)[a]);
+                   : at.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[a])
+                             : static_cast<const float*>(e.g)[a]);
         if constexpr (BITS8) {
           float2 w[2];
           from_e4m3(ok ? static_cast<const uint8_t*>(e.m)[a] : 0u, w);
@@ -313,52 +344,41 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if constexpr (BITS8) {
-        ms = e.ms[base / kBlock];
-        vs = e.vs[base / kBlock];
+        ms = e.ms[rel];
+        vs = e.vs[rel];
       }
     }
 
-    // 8 bits: m is code * ms and v (code * vs)^2, so the block's factors
-    // b1 ms and b2 vs^2 take the codes; as sums of two floats where their
-    // rounding would move the whole block's codes one way
-    float fm = P.b1, fm_low = 0.f, fv = P.b2;
-    if constexpr (BITS8) {
-      fm = P.b1 * ms;
-      fm_low = fmaf(P.b1, ms, -fm) + P.b1_low * ms;
-      fv = P.b2 * (vs * vs);
-    }
+    // 8 bits: m is code * ms and v is (code * vs)^2; the factors b1 ms and
+    // b2 vs^2 of the block take the codes directly
+    const float fm = BITS8 ? P.b1 * ms : P.b1, fv = BITS8 ? P.b2 * (vs * vs) : P.b2;
     const float keep = 1.f - lr * e.wd;
     float2 r[4], top = both(0.f);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float2 add = mul2(g[k], both(gm));
-      if constexpr (BITS8) {
-        add = fma2(m[k], both(fm_low), fma2(g[k], both(gm_low), add));
-        v[k] = mul2(v[k], v[k]);
-      }
-      m[k] = fma2(m[k], both(fm), add);
+      if (BITS8) v[k] = mul2(v[k], v[k]);
+      m[k] = fma2(m[k], both(fm), mul2(g[k], both(gm)));
       const float2 c = mul2(g[k], both(clip));
       v[k] = fma2(v[k], both(fv), mul2(mul2(c, c), both(P.b2c)));
       r[k] = make_float2(sqrt_approx(v[k].x), sqrt_approx(v[k].y));
       const float2 d = fma2(r[k], both(root), both(P.eps));
-      const float2 q = make_float2(__fdividef(m[k].x, d.x), __fdividef(m[k].y, d.y));
+      const float2 q = mul2(m[k], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
       p[k] = fma2(q, both(-rate), mul2(p[k], both(keep)));
-      if constexpr (BITS8) {
-        top.x = fmaxf(top.x, fmaxf(fabsf(m[k].x), fabsf(m[k].y)));
-        top.y = fmaxf(top.y, fmaxf(r[k].x, r[k].y));
+      if (BITS8) {
+        top.x = fmax3(top.x, fabsf(m[k].x), fabsf(m[k].y));
+        top.y = fmax3(top.y, r[k].x, r[k].y);
       }
     }
     if constexpr (BITS8) {
       top = warp_max(top);
-      const bool hold_m = top.x >= 0x1p-100f, hold_v = top.y >= 0x1p-100f;
-      const float im = hold_m ? __fdiv_rn(448.f, top.x) : 0.f;
-      const float iv = hold_v ? __fdiv_rn(448.f, top.y) : 0.f;
-      if (lane == 0) {
-        e.ms[base / kBlock] = hold_m ? __fdiv_rn(top.x, 448.f) : 0.f;
-        e.vs[base / kBlock] = hold_v ? __fdiv_rn(top.y, 448.f) : 0.f;
+      const float im = inverse448(top.x), iv = inverse448(top.y);
+      if (lane < 2) {
+        const float high = lane == 0 ? top.x : top.y;
+        float* to = (lane == 0 ? e.ms : e.vs) + rel;
+        *to = high >= kLeast ? high * (1.f / 448.f) : 0.f;
       }
       // a positive root takes at least the smallest code (2^-9)
-      const float least = hold_v ? 0x1p-9f : 0.f;
+      const float least = iv > 0.f ? 0x1p-9f : 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         m[k] = mul2(m[k], both(im));
@@ -368,24 +388,40 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (vec) {
+      const int first = 4 * lane;
+      float* to_p = e.p + base + first;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t a = base + element(lane, 4 * h);
         const float2 x = p[2 * h], y = p[2 * h + 1];
-        *reinterpret_cast<float4*>(e.p + a) = make_float4(x.x, x.y, y.x, y.y);
-        if (e.copy)
-          *reinterpret_cast<uint2*>(e.copy + a) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(y.x, y.y));
-        if constexpr (BITS8) {
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.m) + a) = to_e4m3(m[2 * h], m[2 * h + 1]);
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.v) + a) = to_e4m3(r[2 * h], r[2 * h + 1]);
-        } else {
-          *reinterpret_cast<float4*>(static_cast<float*>(e.m) + a) =
+        *reinterpret_cast<float4*>(to_p + 128 * h) = make_float4(x.x, x.y, y.x, y.y);
+      }
+      if (e.copy) {
+        __nv_bfloat16* to = e.copy + base + first;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 x = p[2 * h], y = p[2 * h + 1];
+          *reinterpret_cast<uint2*>(to + 128 * h) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(y.x, y.y));
+        }
+      }
+      if constexpr (BITS8) {
+        uint8_t *to_m = static_cast<uint8_t*>(e.m) + base + first, *to_v = static_cast<uint8_t*>(e.v) + base + first;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          *reinterpret_cast<uint32_t*>(to_m + 128 * h) = to_e4m3(m[2 * h], m[2 * h + 1]);
+          *reinterpret_cast<uint32_t*>(to_v + 128 * h) = to_e4m3(r[2 * h], r[2 * h + 1]);
+        }
+      } else {
+        float *to_m = static_cast<float*>(e.m) + base + first, *to_v = static_cast<float*>(e.v) + base + first;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          *reinterpret_cast<float4*>(to_m + 128 * h) =
               make_float4(m[2 * h].x, m[2 * h].y, m[2 * h + 1].x, m[2 * h + 1].y);
-          *reinterpret_cast<float4*>(static_cast<float*>(e.v) + a) =
+          *reinterpret_cast<float4*>(to_v + 128 * h) =
               make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
         }
       }
     } else {
+      const int64_t n = (int64_t)(e.n & kCount);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int64_t a = base + element(lane, k);
@@ -420,8 +456,7 @@ __device__ __forceinline__ double cta_sum(double v) {
   return v;
 }
 
-// A CTA takes an even share of consecutive blocks, its warps every eighth of
-// them, four at a time.  A block's squares are summed in fp32 (8 per lane),
+// The launch's warps sweep over units of four blocks.  A block's squares are summed in fp32 (8 per lane),
 // the blocks' sums with their rounding errors carried along.  The last CTA to
 // finish adds all partial sums in order, so the order of arrival changes
 // nothing.
@@ -430,70 +465,62 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
   wait_for_earlier_work();
   let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t b = (uint32_t)((uint64_t)P.blocks * blockIdx.x / gridDim.x) + warp;
-  const uint32_t end = (uint32_t)((uint64_t)P.blocks * (blockIdx.x + 1) / gridDim.x);
-  int i = P.first[blockIdx.x];
   float sum = 0.f, low = 0.f;
-  for (; b < end; b += kNormUnroll * kWarps) {
-    uint4 w[kNormUnroll][2];
-    int kind[kNormUnroll];  // 0 nothing, 1 bf16, 2 fp32 (as loaded), 3 a partial sum
+  for (uint32_t b = blockIdx.x * kWarps + warp; b < P.units; b += gridDim.x * kWarps) {
+    int i = P.coarse[b >> P.shift];
+    while (b >= P.start[i + 1]) ++i;
+    const NormEntry& e = P.e[i];
+    const int64_t base = (int64_t)(b - P.start[i]) * kNormUnit;
+    // whole blocks of this unit, and elements behind them
+    const int64_t left = (int64_t)(e.n & kCount) - base;
+    const int count = left < kNormUnit ? (int)left : kNormUnit;
+    const int whole = e.n & kVec ? count / kBlock : 0;
+    float part[kNormUnroll];
+    if (e.n & kGradBf16) {
+      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(e.g) + base;
+      uint4 w[kNormUnroll];
 #pragma unroll
-    for (int u = 0; u < kNormUnroll; ++u) {
-      kind[u] = 0;
-      const uint32_t at = b + u * kWarps;
-      if (at >= end) continue;
-      while (at >= P.start[i + 1]) ++i;
-      const NormEntry& e = P.e[i];
-      const int64_t n = (int64_t)(e.n & kCount), base = (int64_t)(at - P.start[i]) * kBlock;
-      if ((e.n & kVec) && base + kBlock <= n) {
-        if (e.n & kGradBf16) {
-          w[u][0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.g) + base + 8 * lane);
-          kind[u] = 1;
-        } else {
-          const float* g = static_cast<const float*>(e.g) + base + 4 * lane;
-          w[u][0] = *reinterpret_cast<const uint4*>(g);
-          w[u][1] = *reinterpret_cast<const uint4*>(g + 128);
-          kind[u] = 2;
-        }
-      } else {
-        float s = 0.f;
+      for (int u = 0; u < kNormUnroll; ++u)
+        w[u] = u < whole ? *reinterpret_cast<const uint4*>(g + u * kBlock + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int64_t a = base + k * 32 + lane;
-          const float g = a >= n ? 0.f
-                          : (e.n & kGradBf16) ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[a])
-                                              : static_cast<const float*>(e.g)[a];
-          s = fmaf(g, g, s);
+      for (int u = 0; u < kNormUnroll; ++u) {
+        const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        float2 t = both(0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = make_float2(bf16lo(q[k]), bf16hi(q[k]));
+          t = fma2(x, x, t);
         }
-        w[u][0].x = __float_as_uint(s);
-        kind[u] = 3;
+        part[u] = t.x + t.y;
       }
+      for (int k = whole * kBlock + lane; k < count; k += 32) {
+        const float x = __bfloat162float(g[k]);
+        part[0] = fmaf(x, x, part[0]);
+      }
+    } else {
+      const float* g = static_cast<const float*>(e.g) + base;
+      float4 w[kNormUnroll][2];
+#pragma unroll
+      for (int u = 0; u < kNormUnroll; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[u][h] = u < whole ? *reinterpret_cast<const float4*>(g + u * kBlock + 128 * h + 4 * lane)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < kNormUnroll; ++u) {
+        float2 t = both(0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 x = make_float2(w[u][h].x, w[u][h].y), y = make_float2(w[u][h].z, w[u][h].w);
+          t = fma2(x, x, fma2(y, y, t));
+        }
+        part[u] = t.x + t.y;
+      }
+      for (int k = whole * kBlock + lane; k < count; k += 32) part[0] = fmaf(g[k], g[k], part[0]);
     }
 #pragma unroll
     for (int u = 0; u < kNormUnroll; ++u) {
-      const uint4 x = w[u][0], y = w[u][1];
-      float s = 0.f;
-      if (kind[u] == 1) {
-        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
-        float2 t = both(0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 g = make_float2(bf16lo(q[k]), bf16hi(q[k]));
-          t = fma2(g, g, t);
-        }
-        s = t.x + t.y;
-      } else if (kind[u] == 2) {
-        const uint32_t q[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        float2 t = both(0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 g = make_float2(__uint_as_float(q[2 * k]), __uint_as_float(q[2 * k + 1]));
-          t = fma2(g, g, t);
-        }
-        s = t.x + t.y;
-      } else if (kind[u] == 3) {
-        s = __uint_as_float(x.x);
-      }
+      const float s = part[u];
       // sum + s exactly, as a rounded sum and its error (Knuth's two-sum)
       const float t = sum + s, back = t - sum;
       low += (sum - (t - back)) + (s - back);
@@ -504,13 +531,13 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
   float mine = isfinite(sum) ? sum + low : sum;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  __shared__ float part[kWarps];
+  __shared__ float sums[kWarps];
   __shared__ int is_last;
-  if (lane == 0) part[warp] = mine;
+  if (lane == 0) sums[warp] = mine;
   __syncthreads();
   if (threadIdx.x == 0) {
     double total = 0.0;
-    for (int k = 0; k < kWarps; ++k) total += (double)part[k];
+    for (int k = 0; k < kWarps; ++k) total += (double)sums[k];
     P.part[blockIdx.x] = total;
     __threadfence();
     is_last = P.last && atomicAdd(&P.state->ticket[1], 1u) == gridDim.x - 1;
@@ -560,15 +587,16 @@ cudaError_t resident_ctas(K kernel, size_t smem, std::atomic<int> (&cache)[64], 
   return cudaSuccess;
 }
 
-// The tensor in which each CTA's share of `total` pieces begins.
+// The tensor that holds every 2^shift-th of `total` pieces.
 template <typename StartOf>
-void first_tensors(uint16_t* first, unsigned grid, uint64_t total, StartOf start_of) {
-  int i = 0;
-  for (unsigned c = 0; c < grid; ++c) {
-    const uint64_t b = total * c / grid;
-    while (b < total && b >= start_of(i + 1)) ++i;
-    first[c] = (uint16_t)i;
+int coarse_table(uint16_t (&table)[kCoarse], uint64_t total, StartOf start_of) {
+  int shift = 0;
+  while (total >> shift >= (uint64_t)kCoarse) ++shift;
+  for (uint64_t c = 0, i = 0; (c << shift) < total; ++c) {
+    while (c << shift >= start_of((int)i + 1)) ++i;
+    table[c] = (uint16_t)i;
   }
+  return shift;
 }
 
 template <bool BITS8, int T>
@@ -605,9 +633,7 @@ cudaError_t step_part(const evoattn_adamw_tensor* t, int count, const AdamwScala
   P.lr_device = s.lr_device;
   P.lr = s.lr;
   P.b1 = (float)s.beta1;
-  P.b1_low = (float)(s.beta1 - (double)P.b1);
   P.b1c = (float)(1.0 - s.beta1);
-  P.b1c_low = (float)((1.0 - s.beta1) - (double)P.b1c);
   P.b2 = (float)s.beta2;
   P.b2c = (float)(1.0 - s.beta2);
   P.log_b1 = (float)log(s.beta1);
@@ -620,8 +646,8 @@ cudaError_t step_part(const evoattn_adamw_tensor* t, int count, const AdamwScala
   if (e != cudaSuccess) return e;
   // a CTA for every 8 blocks (one per warp), at least one for the bookkeeping
   const uint64_t want = std::max<uint64_t>(1, (blocks + kWarps - 1) / kWarps);
-  const unsigned grid = (unsigned)std::min<uint64_t>(want, (uint64_t)std::min(ctas, kStepCtas));
-  first_tensors(P.first, grid, blocks, [&](int i) { return P.e[i].start; });
+  const unsigned grid = (unsigned)std::min<uint64_t>(want, (uint64_t)ctas);
+  P.shift = coarse_table(P.coarse, blocks, [&](int i) { return (uint64_t)P.e[i].start; });
   return launch_early(k_adamw<BITS8, T>, grid, kThreads, Ring<BITS8>::BYTES, st, P);
 }
 
@@ -645,17 +671,17 @@ cudaError_t norm_part(const evoattn_adamw_tensor* t, int count, float max_norm,
                       cudaStream_t st) {
   static std::atomic<int> cache[64];
   NormParams<T> P;
-  uint64_t blocks = 0;
+  uint64_t units = 0;
   int k = 0;
   for (int i = 0; i < count; ++i) {
     if (t[i].n == 0) continue;
     P.e[k] = NormEntry{t[i].grad, grad_flags(t[i])};
-    P.start[k++] = (uint32_t)blocks;
-    blocks += (uint64_t)(t[i].n + kBlock - 1) / kBlock;
-    if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    P.start[k++] = (uint32_t)units;
+    units += (uint64_t)(t[i].n + kNormUnit - 1) / kNormUnit;
+    if (units > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
   }
-  P.start[k] = (uint32_t)blocks;
-  P.blocks = (uint32_t)blocks;
+  P.start[k] = (uint32_t)units;
+  P.units = (uint32_t)units;
   P.state = state;
   P.part_all = part_all;
   P.part = part_all + *parts;
@@ -665,10 +691,10 @@ cudaError_t norm_part(const evoattn_adamw_tensor* t, int count, float max_norm,
   int ctas = 0;
   cudaError_t e = resident_ctas(k_grad_norm<T>, 0, cache, &ctas);
   if (e != cudaSuccess) return e;
-  // a CTA for every 8 blocks (one per warp), at least one for the bookkeeping
-  const uint64_t want = std::max<uint64_t>(1, (blocks + kWarps - 1) / kWarps);
+  // a CTA for every 8 units (one per warp), at least one for the bookkeeping
+  const uint64_t want = std::max<uint64_t>(1, (units + kWarps - 1) / kWarps);
   const unsigned grid = (unsigned)std::min<uint64_t>(want, (uint64_t)std::min(ctas, kNormCtas));
-  first_tensors(P.first, grid, blocks, [&](int i) { return P.start[i]; });
+  P.shift = coarse_table(P.coarse, units, [&](int i) { return (uint64_t)P.start[i]; });
   *parts += (int)grid;
   return launch_early(k_grad_norm<T>, grid, kThreads, 0, st, P);
 }

@@ -3,6 +3,7 @@
 // validation and dispatch.  Every check happens before anything is enqueued;
 // see include/evoattn.h for the contract.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -231,7 +232,7 @@ evoattn_status evoattn_adamw(const evoattn_adamw_tensor* tensors, int count, flo
   const evoattn_status st = check_grads(tensors, count, state);
   if (st != EVOATTN_OK) return st;
   if (!(lr >= 0.f) || !(lr < INFINITY) || !(beta1 >= 0.0 && beta1 < 1.0) ||
-      !(beta2 >= 0.0 && beta2 < 1.0) || !(eps > 0.f) || !(eps < INFINITY))
+      !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= FLT_MIN) || !(eps < INFINITY))
     return EVOATTN_ERR_INVALID_ARG;
   if (flags & ~EVOATTN_ADAMW_CLIP) return EVOATTN_ERR_INVALID_ARG;
   if (state_bits != 32 && state_bits != 8) return EVOATTN_ERR_UNSUPPORTED;

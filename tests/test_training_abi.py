@@ -145,7 +145,7 @@ def test_adamw_rejects_bad_arguments(lib):
     for b in (-0.1, 1.0, math.nan):
         assert step(lib, tensors(), b1=b) == I
         assert step(lib, tensors(), b2=b) == I
-    for eps in (0.0, math.nan, math.inf):
+    for eps in (0.0, 1e-40, math.nan, math.inf):
         assert step(lib, tensors(), eps=eps) == I
     assert step(lib, tensors(), bits=16) == U
     assert step(lib, tensors(), flags=2) == I
