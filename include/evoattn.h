@@ -442,6 +442,19 @@ evoattn_status evoattn_block_norm_bwd(const void* dx1, const int64_t dx1_strides
                                       cudaStream_t stream);
 
 /*
+ * The two calls above with their arguments in one array of 64-bit words, for
+ * bindings to which every argument is a cost: the same arguments in the same
+ * order, where a tensor with its strides is five words (address, b, i, j, c;
+ * all ignored but the address when that is 0) and eps is the bits of a double.
+ * evoattn_block_norm_packed takes EVOATTN_BLOCK_NORM_WORDS words,
+ * evoattn_block_norm_bwd_packed EVOATTN_BLOCK_NORM_BWD_WORDS.
+ */
+#define EVOATTN_BLOCK_NORM_WORDS 38
+#define EVOATTN_BLOCK_NORM_BWD_WORDS 59
+evoattn_status evoattn_block_norm_packed(const int64_t* words, cudaStream_t stream);
+evoattn_status evoattn_block_norm_bwd_packed(const int64_t* words, cudaStream_t stream);
+
+/*
  * One AdamW step over many tensors (no counterpart in the MegaFold pages: the
  * optimiser of the training iteration whose operators they describe).  For
  * every tensor and element, with t the number of this step (from 1):

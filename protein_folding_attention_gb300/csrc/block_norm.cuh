@@ -49,6 +49,9 @@
 
 namespace evo {
 namespace norm {
+// (each including file has its own copies: a function's static data must not
+// be shared with another copy of this library in the process)
+namespace {
 
 constexpr int kSums = 4;          // vectors that the backward sums over rows
 constexpr int kE = 8;             // channels per thread
@@ -1228,5 +1231,6 @@ cudaError_t run_bwd(const BlockNormCall& c, cudaStream_t st) {
   return dispatch_bwd<TS, TI, false, true, false>(pl, c.ws, st);
 }
 
+}  // namespace
 }  // namespace norm
 }  // namespace evo

@@ -30,7 +30,7 @@
 namespace evo {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a CTA of the norm's kernel
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = EVOATTN_ADAMW_BLOCK;  // elements a warp works on at a time
 static_assert(kBlock == 256, "a lane holds 8 elements of a block");
@@ -166,17 +166,15 @@ __device__ __forceinline__ float2 warp_max(float2 v) {
 __device__ __forceinline__ int element(int lane, int k) { return (k >> 2) * 128 + 4 * lane + (k & 3); }
 
 // A warp's stage of the ring: p, g (bf16 in the first half), then m and v,
-// and with 8 bits their scales.  As many stages as leave room for one CTA per
-// SM: 8 warps with 6 stages run at 96 % of the copy rate (264 us for 107M
-// parameters), 16 warps with 4 stages at 87 % (293 us; the fronts are wider).
+// and with 8 bits their scales.  16 warps per SM in flight.
 template <bool BITS8>
 struct Ring {
   static constexpr uint32_t G = 1024, M = 2048, V = BITS8 ? 2304 : 3072;
   static constexpr uint32_t S = 2560;
   static_assert(!BITS8 || S + 8 <= 2576, "the scales are a stage's last");
   static constexpr uint32_t STAGE = BITS8 ? 2576 : 4096;
-  static constexpr int STAGES = BITS8 ? 6 : 4;
-  static constexpr uint32_t BYTES = STAGE * STAGES * kWarps;
+  static constexpr int STAGES = BITS8 ? 4 : 3;
+  static constexpr uint32_t BYTES = STAGE * STAGES;  // per warp
 };
 
 // Where a warp is: a block, the tensor that holds it, and that tensor's
@@ -209,8 +207,13 @@ struct Cursor {
   }
 };
 
-template <bool BITS8, int T>
-__global__ void __launch_bounds__(kThreads, 1)
+// WARPS: 8, two CTAs per SM; or 16 and one CTA, whose warps meet every fourth
+// turn.  Left to themselves the warps drift apart over a long tensor and the
+// front that they sweep widens (8-bit states, tensors of 2M elements: 230 us
+// with 8 warps, 208 with 16; of 0.26M: 47.5 and 51, so the meetings are kept
+// for large tensors; with 32-bit states the two differ by less than 1 %).
+template <bool BITS8, int T, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     k_adamw(const __grid_constant__ StepParams<BITS8, T> P) {
   using R = Ring<BITS8>;
   extern __shared__ __align__(16) char smem[];
@@ -238,9 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float gm = P.b1c * clip;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t end = P.blocks, hop = gridDim.x * kWarps;
+  const uint32_t end = P.blocks, hop = gridDim.x * WARPS;
   Cursor<BITS8, T> at;
-  at.b = blockIdx.x * kWarps + warp;
+  at.b = blockIdx.x * WARPS + warp;
+  // turns that every warp of the launch takes
+  uint32_t common = WARPS == 16 ? end / hop : 0;
   if (at.b >= end) return;
   at.open(P, lane);
   char* const ring = smem + warp * (R::STAGE * R::STAGES);
@@ -284,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rel = at.b - at.start;
     const bool vec = rel < at.full;
     const int64_t base = (int64_t)rel * kBlock;
+    if (WARPS == 16 && common > 0 && (--common & 3) == 0) __syncthreads();
     __syncwarp();  // the warp has read the stage that is filled next
     fetch(stage == 0 ? R::STAGES - 1 : stage - 1, ahead);
     copies_wait<R::STAGES - 1>();
@@ -571,7 +577,7 @@ uint64_t grad_flags(const evoattn_adamw_tensor& s) {
 
 // Resident CTAs of a kernel on the current device, looked up once.
 template <typename K>
-cudaError_t resident_ctas(K kernel, size_t smem, std::atomic<int> (&cache)[64], int* n) {
+cudaError_t resident_ctas(K kernel, int threads, size_t smem, std::atomic<int> (&cache)[64], int* n) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -580,7 +586,7 @@ cudaError_t resident_ctas(K kernel, size_t smem, std::atomic<int> (&cache)[64], 
   int sms = 0, per = 0;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
   if (e != cudaSuccess) return e;
   *n = std::max(1, sms) * std::max(1, per);
   if (dev < 64) cache[dev].store(*n, std::memory_order_relaxed);
@@ -599,10 +605,21 @@ int coarse_table(uint16_t (&table)[kCoarse], uint64_t total, StartOf start_of) {
   return shift;
 }
 
+template <bool BITS8, int T, int WARPS>
+cudaError_t launch_step(const StepParams<BITS8, T>& P, cudaStream_t st) {
+  static std::atomic<int> cache[64];
+  constexpr size_t smem = (size_t)Ring<BITS8>::BYTES * WARPS;
+  int ctas = 0;
+  const cudaError_t e = resident_ctas(k_adamw<BITS8, T, WARPS>, WARPS * 32, smem, cache, &ctas);
+  if (e != cudaSuccess) return e;
+  // a warp for every block, at least one CTA for the bookkeeping
+  const uint32_t want = std::max(1u, (P.blocks + WARPS - 1) / WARPS);
+  return launch_early(k_adamw<BITS8, T, WARPS>, std::min(want, (uint32_t)ctas), WARPS * 32, smem, st, P);
+}
+
 template <bool BITS8, int T>
 cudaError_t step_part(const evoattn_adamw_tensor* t, int count, const AdamwScalars& s,
                       evoattn_optim_state* state, bool last, cudaStream_t st) {
-  static std::atomic<int> cache[64];
   StepParams<BITS8, T> P;
   uint64_t blocks = 0;
   int k = 0;
@@ -641,14 +658,12 @@ cudaError_t step_part(const evoattn_adamw_tensor* t, int count, const AdamwScala
   P.eps = s.eps;
   P.clip = s.clip ? 1 : 0;
   P.last = last ? 1 : 0;
-  int ctas = 0;
-  cudaError_t e = resident_ctas(k_adamw<BITS8, T>, Ring<BITS8>::BYTES, cache, &ctas);
-  if (e != cudaSuccess) return e;
-  // a CTA for every 8 blocks (one per warp), at least one for the bookkeeping
-  const uint64_t want = std::max<uint64_t>(1, (blocks + kWarps - 1) / kWarps);
-  const unsigned grid = (unsigned)std::min<uint64_t>(want, (uint64_t)ctas);
   P.shift = coarse_table(P.coarse, blocks, [&](int i) { return (uint64_t)P.e[i].start; });
-  return launch_early(k_adamw<BITS8, T>, grid, kThreads, Ring<BITS8>::BYTES, st, P);
+  // large tensors: 2048 blocks, half a million elements, on average
+  if constexpr (BITS8) {
+    if (blocks >= 2048ull * (uint64_t)std::max(k, 1)) return launch_step<BITS8, T, 16>(P, st);
+  }
+  return launch_step<BITS8, T, 8>(P, st);
 }
 
 template <bool BITS8>
@@ -689,7 +704,7 @@ cudaError_t norm_part(const evoattn_adamw_tensor* t, int count, float max_norm,
   P.last = last ? 1 : 0;
   P.max_norm = max_norm;
   int ctas = 0;
-  cudaError_t e = resident_ctas(k_grad_norm<T>, 0, cache, &ctas);
+  cudaError_t e = resident_ctas(k_grad_norm<T>, kThreads, 0, cache, &ctas);
   if (e != cudaSuccess) return e;
   // a CTA for every 8 units (one per warp), at least one for the bookkeeping
   const uint64_t want = std::max<uint64_t>(1, (units + kWarps - 1) / kWarps);

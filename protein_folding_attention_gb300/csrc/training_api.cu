@@ -6,6 +6,7 @@
 #include <float.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -89,6 +90,39 @@ RowOperand operand(const void* p, const int64_t* s) {
     for (int k = 0; k < 3; ++k) r.s[k] = s[k];
   return r;
 }
+
+// Reads the arguments of a packed call one after another.
+class Words {
+ public:
+  struct Rows {
+    void* p;
+    const int64_t* s;
+  };
+  Words(const int64_t* w, int count) : w_(w), end_(w + count) {}
+  Rows rows() {
+    const int64_t* at = w_;
+    w_ += 5;
+    return Rows{reinterpret_cast<void*>(at[0]), at[0] ? at + 1 : nullptr};
+  }
+  template <typename T>
+  T* pointer() { return reinterpret_cast<T*>(*w_++); }
+  int integer() {
+    const int64_t v = *w_++;
+    if (v != (int64_t)(int)v) fits_ = false;
+    return (int)v;
+  }
+  float real() {
+    double d;
+    memcpy(&d, w_++, sizeof(d));
+    return (float)d;
+  }
+  size_t size() { return (size_t)*w_++; }
+  bool complete() const { return fits_ && w_ == end_; }
+
+ private:
+  const int64_t *w_, *end_;
+  bool fits_ = true;
+};
 
 evoattn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? EVOATTN_OK : EVOATTN_ERR_CUDA; }
 
@@ -193,6 +227,44 @@ evoattn_status evoattn_block_norm_bwd(
   c.ws = static_cast<float*>(workspace);
   if (stream_dtype == EVOATTN_BF16) return cuda_status(block_norm_bwd_bf16(c, stream));
   return cuda_status(dtype == EVOATTN_BF16 ? block_norm_bwd_mixed(c, stream) : block_norm_bwd_f32(c, stream));
+}
+
+evoattn_status evoattn_block_norm_packed(const int64_t* words, cudaStream_t stream) {
+  if (!words) return EVOATTN_ERR_INVALID_ARG;
+  Words w(words, EVOATTN_BLOCK_NORM_WORDS);
+  const Words::Rows x = w.rows(), u = w.rows(), gate = w.rows();
+  float* prm[5];
+  for (float*& p : prm) p = w.pointer<float>();
+  const Words::Rows x1 = w.rows(), y = w.rows();
+  int n[7];
+  for (int& v : n) v = w.integer();
+  const float eps = w.real();
+  if (!w.complete()) return EVOATTN_ERR_INVALID_ARG;
+  return evoattn_block_norm(x.p, x.s, u.p, u.s, gate.p, gate.s, prm[0], prm[1], prm[2], prm[3], prm[4],
+                            x1.p, x1.s, y.p, y.s, n[0], n[1], n[2], n[3], (evoattn_dtype)n[4],
+                            (evoattn_dtype)n[5], (evoattn_norm_kind)n[6], eps, stream);
+}
+
+evoattn_status evoattn_block_norm_bwd_packed(const int64_t* words, cudaStream_t stream) {
+  if (!words) return EVOATTN_ERR_INVALID_ARG;
+  Words w(words, EVOATTN_BLOCK_NORM_BWD_WORDS);
+  const Words::Rows dx1 = w.rows(), dy = w.rows(), x1 = w.rows(), u = w.rows(), gate = w.rows();
+  float* prm[4];
+  for (float*& p : prm) p = w.pointer<float>();
+  const Words::Rows dx = w.rows(), du = w.rows(), dgate = w.rows();
+  float* grad[5];
+  for (float*& p : grad) p = w.pointer<float>();
+  int n[7];
+  for (int& v : n) v = w.integer();
+  const float eps = w.real();
+  void* ws = w.pointer<void>();
+  const size_t bytes = w.size();
+  if (!w.complete()) return EVOATTN_ERR_INVALID_ARG;
+  return evoattn_block_norm_bwd(dx1.p, dx1.s, dy.p, dy.s, x1.p, x1.s, u.p, u.s, gate.p, gate.s, prm[0],
+                                prm[1], prm[2], prm[3], dx.p, dx.s, du.p, du.s, dgate.p, dgate.s, grad[0],
+                                grad[1], grad[2], grad[3], grad[4], n[0], n[1], n[2], n[3],
+                                (evoattn_dtype)n[4], (evoattn_dtype)n[5], (evoattn_norm_kind)n[6], eps,
+                                ws, bytes, stream);
 }
 
 size_t evoattn_grad_norm_workspace_size(int count) {

@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -89,6 +90,10 @@ def load(path: str = LIB_PATH):
     lib.evoattn_block_norm_bwd.argtypes = ([vp, i64p] * 5 + [fp] * 4 + [vp, i64p] * 3 + [fp] * 5 +
                                            [i] * 7 + [f, vp, sz, vp])
     lib.evoattn_block_norm_bwd.restype = i
+    lib.evoattn_block_norm_packed.argtypes = [ctypes.c_char_p, vp]
+    lib.evoattn_block_norm_packed.restype = i
+    lib.evoattn_block_norm_bwd_packed.argtypes = [ctypes.c_char_p, vp]
+    lib.evoattn_block_norm_bwd_packed.restype = i
     lib.evoattn_grad_norm_workspace_size.argtypes = [i]
     lib.evoattn_grad_norm_workspace_size.restype = sz
     lib.evoattn_grad_norm.argtypes = [ctypes.POINTER(AdamwTensor), i, f, vp, vp, sz, vp]
@@ -257,47 +262,45 @@ def transition(z, gamma, beta, w1, w2, eps=1e-5, o=None, w_o=None, out=None, str
     return out
 
 
-_strides = {}  # stride tuple -> int64_t[4], so that a call does not build its arrays anew
-
-
-def _strides4(t):
-    s = t.stride()
-    a = _strides.get(s)
-    if a is None:
-        if len(_strides) > 4096:
-            _strides.clear()
-        a = _strides[s] = _I64_4(*s)
-    return a
-
-
-def _rows4(t, shape, dtype, index, name):
-    """Checks a [B, I, J, C] operand on device `index`; returns its address
-    and strides."""
-    if t is None:
-        return None, None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{index}, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    return t.data_ptr(), _strides4(t)
-
-
-def _vec(t, C, index, name):
-    """Checks a [C] fp32 parameter; returns its address."""
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 or t.shape != (C,) or t.get_device() != index or \
-            not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous fp32 [{C}] tensor on cuda:{index}")
-    return t.data_ptr()
-
-
 def _on_device(t):
     """Index of the tensor's device, which has to be the current one (the
     library enqueues on the current device's streams)."""
     index = t.get_device()
-    if index < 0 or index != torch.cuda.current_device():
+    if index < 0 or index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {t.device}: a CUDA tensor on the current device is needed")
     return index
+
+
+_NO_ROWS = (0, 0, 0, 0, 0)
+_PACK_FWD = struct.Struct("=37qd").pack
+_PACK_BWD = struct.Struct("=56qd2q").pack
+
+
+def _add_rows(words, operands, shape, index):
+    """Checks [B, I, J, C] operands (tensor, dtype, name) on device `index`
+    and appends the address and strides of each."""
+    for t, dtype, name in operands:
+        if t is None:
+            words += _NO_ROWS
+            continue
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+            raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{index}, "
+                             f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+        words.append(t.data_ptr())
+        words += t.stride()
+
+
+def _add_vectors(words, vectors, C, index):
+    """Checks [C] fp32 parameters (tensor, name) and appends their addresses."""
+    shape = (C,)
+    for t, name in vectors:
+        if t is None:
+            words.append(0)
+            continue
+        if t.dtype is not torch.float32 or t.shape != shape or t.get_device() != index or \
+                not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous fp32 [{C}] tensor on cuda:{index}")
+        words.append(t.data_ptr())
 
 
 def _raw_stream(stream, index):
@@ -340,33 +343,46 @@ def block_norm(x, u=None, gate=None, scale=None, gamma_post=None, beta_post=None
     alone (y is None).  y has u's type; y_dtype names it where there is no u
     (default: x's).  Outputs take x's layout; x1=x updates the stream in place.
     Returns (x1, y)."""
-    if x.dim() != 4:
+    shape = x.shape
+    if len(shape) != 4:
         raise ValueError("x must be [B, I, J, C]")
-    shape, dev = x.shape, _on_device(x)
-    C = shape[3]
-    io = u.dtype if u is not None else (y_dtype or x.dtype)
-    if y_dtype is not None and y_dtype != io:
+    dev, sd = _on_device(x), x.dtype
+    io = u.dtype if u is not None else (y_dtype or sd)
+    if y_dtype is not None and y_dtype is not io:
         raise ValueError("y has the type of u")
-    with _allocate_on(stream):
-        if u is not None and x1 is None:
-            x1 = torch.empty_like(x)
-        if pre and y is None:
-            y = torch.empty_like(x, dtype=io)
-    if not pre and y is not None:
+    if y is not None and not pre:
         raise ValueError("y without pre")
     if gate is not None:
         gate = _expanded(gate, shape)
-    out = x1 if u is not None else None
-    st = load().evoattn_block_norm(
-        *_rows4(x, shape, x.dtype, dev, "x"), *_rows4(u, shape, io, dev, "u"),
-        *_rows4(gate, shape, io, dev, "gate"), _vec(scale, C, dev, "scale"),
-        _vec(gamma_post, C, dev, "gamma_post"), _vec(beta_post, C, dev, "beta_post"),
-        _vec(gamma_pre, C, dev, "gamma_pre"), _vec(beta_pre, C, dev, "beta_pre"),
-        *_rows4(out, shape, x.dtype, dev, "x1"), *_rows4(y, shape, io, dev, "y"),
-        *shape, _dtype_code(x), F32 if io is torch.float32 else BF16, kind, eps, _raw_stream(stream, dev))
+    words = []
+    _add_rows(words, ((x, sd, "x"), (u, io, "u"), (gate, io, "gate")), shape, dev)
+    _add_vectors(words, ((scale, "scale"), (gamma_post, "gamma_post"), (beta_post, "beta_post"),
+                         (gamma_pre, "gamma_pre"), (beta_pre, "beta_pre")), shape[3], dev)
+    with _allocate_on(stream):
+        if u is None:
+            x1 = x
+            words += _NO_ROWS
+        elif x1 is None:
+            x1 = torch.empty_like(x)
+            words.append(x1.data_ptr())
+            words += x1.stride()
+        else:
+            _add_rows(words, ((x1, sd, "x1"),), shape, dev)
+        if not pre:
+            words += _NO_ROWS
+        elif y is None:
+            y = torch.empty_like(x, dtype=io)
+            words.append(y.data_ptr())
+            words += y.stride()
+        else:
+            _add_rows(words, ((y, io, "y"),), shape, dev)
+    words += shape
+    st = load().evoattn_block_norm_packed(
+        _PACK_FWD(*words, _dtype_code(x), F32 if io is torch.float32 else BF16, kind, eps),
+        _raw_stream(stream, dev))
     if st != OK:
         _check(st, "evoattn_block_norm")
-    return (x if u is None else x1), y
+    return x1, y
 
 
 def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_post=None,
@@ -382,55 +398,68 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
     lead = dx1 if dx1 is not None else x1
     if lead is None or (dy is None and (u is None or dx1 is None)):
         raise ValueError("dx1 with u, or dy with x1, is needed")
-    if lead.dim() != 4:
+    shape = lead.shape
+    if len(shape) != 4:
         raise ValueError("gradients must be [B, I, J, C]")
-    shape, dev = lead.shape, _on_device(lead)
-    C = shape[3]
-    if dy is not None and x1 is None:
-        raise ValueError("dy needs x1")
     if dy is None:
         x1 = None
+    elif x1 is None:
+        raise ValueError("dy needs x1")
+    dev, sd, C = _on_device(lead), lead.dtype, shape[3]
     io = u.dtype if u is not None else dy.dtype
+    if gate is not None and 0 in gate.stride():
+        gate = gate.contiguous()  # an expanded view: each of its rows has its own gradient
+    full = gate if gate is None else _expanded(gate, shape)
+    words, out = [], {}
+    _add_rows(words, ((dx1, sd, "dx1"), (dy, io, "dy"), (x1, sd, "x1"), (u, io, "u"),
+                      (full, io, "gate")), shape, dev)
+    _add_vectors(words, ((scale, "scale"), (gamma_post, "gamma_post"), (beta_post, "beta_post"),
+                         (gamma_pre, "gamma_pre")), C, dev)
     lib = load()
-    need = lib.evoattn_block_norm_bwd_workspace_size(C)
-    if gate is not None and any(n > 1 and s == 0 for n, s in zip(gate.shape, gate.stride())):
-        gate = gate.contiguous()  # an expanded view: its gradient is that of each row by itself
-    full = _expanded(gate, shape) if gate is not None else None
-    out = {}
     with _allocate_on(stream):
-        if dy is not None:
-            out["dx"] = torch.empty_like(lead) if dx is None else dx
-        du = dgate = None
-        if u is not None:
+        if dy is None:
+            words += _NO_ROWS
+            out["dx"] = dx1
+        else:
+            if dx is None:
+                dx = torch.empty_like(lead)
+            _add_rows(words, ((dx, sd, "dx"),), shape, dev)
+            out["dx"] = dx
+        if u is None:
+            words += _NO_ROWS
+        else:
             out["du"] = du = torch.empty_like(u)
-            if gate is not None:
-                out["dgate"] = dgate = torch.empty_like(gate)
+            words.append(du.data_ptr())
+            words += du.stride()
+        if gate is None:
+            words += _NO_ROWS
+        else:
+            out["dgate"] = dgate = torch.empty_like(gate)
+            words.append(dgate.data_ptr())
+            words += (dgate if full is gate else dgate.expand(shape)).stride()
         params = (("dscale", scale), ("dgamma_post", gamma_post), ("dbeta_post", beta_post),
                   ("dgamma_pre", gamma_pre), ("dbeta_pre", beta_pre))
-        given = [name for name, t in params if t is not None]
+        given = sum(t is not None for _, t in params)
         if given:
-            for name, row in zip(given, torch.empty((len(given), C), device=lead.device,
-                                                    dtype=torch.float32).unbind(0)):
-                out[name] = row
+            rows = iter(torch.empty((given, C), device=lead.device, dtype=torch.float32).unbind(0))
+        for name, t in params:
+            if t is None:
+                words.append(0)
+            else:
+                out[name] = row = next(rows)
+                words.append(row.data_ptr())
         if workspace is None:
-            workspace = torch.empty(need, device=lead.device, dtype=torch.uint8)
-    _vec(beta_pre, C, dev, "beta_pre")
-    get = out.get
-    st = lib.evoattn_block_norm_bwd(
-        *_rows4(dx1, shape, lead.dtype, dev, "dx1"), *_rows4(dy, shape, io, dev, "dy"),
-        *_rows4(x1, shape, lead.dtype, dev, "x1"), *_rows4(u, shape, io, dev, "u"),
-        *_rows4(full, shape, io, dev, "gate"), _vec(scale, C, dev, "scale"),
-        _vec(gamma_post, C, dev, "gamma_post"), _vec(beta_post, C, dev, "beta_post"),
-        _vec(gamma_pre, C, dev, "gamma_pre"),
-        *_rows4(get("dx"), shape, lead.dtype, dev, "dx"), *_rows4(du, shape, io, dev, "du"),
-        *_rows4(dgate if dgate is None else _expanded(dgate, shape), shape, io, dev, "dgate"),
-        *[None if t is None else get(name).data_ptr() for name, t in params], *shape, _dtype_code(lead),
-        F32 if io is torch.float32 else BF16, kind, eps, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+            workspace = torch.empty(lib.evoattn_block_norm_bwd_workspace_size(C), device=lead.device,
+                                    dtype=torch.uint8)
+    if beta_pre is not None:
+        _add_vectors([], ((beta_pre, "beta_pre"),), C, dev)
+    words += shape
+    st = lib.evoattn_block_norm_bwd_packed(
+        _PACK_BWD(*words, _dtype_code(lead), F32 if io is torch.float32 else BF16, kind, eps,
+                  workspace.data_ptr(), workspace.numel() * workspace.element_size()),
+        _raw_stream(stream, dev))
     if st != OK:
         _check(st, "evoattn_block_norm_bwd")
-    if dy is None:
-        out["dx"] = dx1
     return out
 
 

@@ -312,6 +312,11 @@ def test_repeated_input_rows():
     got = evoattn.block_norm_bwd(*[g[n] for n in BWD_ARGS])
     assert got["dgate"].shape == (2, 6, 5, 128)   # an expanded gate: each row's own gradient
     check_bwd(b, got, False)
+    # a gate shared along j that is itself expanded along b
+    b["gate"] = b["gate"][:1, :, :1].contiguous().expand(2, 6, 1, 128)
+    g["gate"] = b["gate"][:1].to(DEV).expand(2, 6, 1, 128)
+    got = evoattn.block_norm_bwd(*[g[n] for n in BWD_ARGS])
+    check_bwd(b, got, False)
 
 
 def test_in_place_gives_the_same_bits():
@@ -477,6 +482,37 @@ def test_capture_and_other_streams():
     assert torch.equal(a[0], want[0][0]) and torch.equal(a[1], want[0][1])
     for n in b:
         assert torch.equal(b[n], want[1][n]), n
+
+
+@pytest.mark.parametrize("gate", ["none", "full", "row"])
+def test_flat_and_packed_calls_agree(gate):
+    """The two forms of the C entry points give the same bits."""
+    import ctypes
+    lib = evoattn.load()
+    shape = (2, 5, 7, 72)
+    S4 = ctypes.c_int64 * 4
+    stream = torch.cuda.current_stream().cuda_stream
+    p = lambda t: None if t is None else t.data_ptr()
+    s = lambda t: None if t is None else S4(*t.stride())
+    ps = lambda t: (p(t), s(t))
+    wide = lambda t: None if t is None else t.expand(shape)
+    k = to_gpu(draw(shape, "mixed", gate, seed=30))
+    x1, y = evoattn.block_norm(*[k[n] for n in ("x", "u", "gate") + PARAMS])
+    a, b = torch.empty_like(x1), torch.empty_like(y)
+    assert lib.evoattn_block_norm(*ps(k["x"]), *ps(k["u"]), *ps(wide(k["gate"])), *[p(k[n]) for n in PARAMS],
+                                  *ps(a), *ps(b), *shape, evoattn.F32, evoattn.BF16, 0, 1e-5, stream) == 0
+    assert torch.equal(a, x1) and torch.equal(b, y)
+    k = to_gpu(draw(shape, "mixed", gate, seed=31, backward=True))
+    want = evoattn.block_norm_bwd(*[k[n] for n in BWD_ARGS])
+    got = {n: torch.empty_like(t) for n, t in want.items()}
+    ws = torch.empty(lib.evoattn_block_norm_bwd_workspace_size(72), device=DEV, dtype=torch.uint8)
+    assert lib.evoattn_block_norm_bwd(
+        *[v for n in ("dx1", "dy", "x1", "u") for v in ps(k[n])], *ps(wide(k["gate"])),
+        *[p(k[n]) for n in PARAMS[:4]], *ps(got["dx"]), *ps(got["du"]), *ps(wide(got.get("dgate"))),
+        *[p(got["d" + n]) for n in PARAMS], *shape, evoattn.F32, evoattn.BF16, 0, 1e-5, ws.data_ptr(),
+        ws.numel(), stream) == 0
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
 
 
 def test_python_refusals():
