@@ -42,6 +42,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "block_norm.h"
 #include "common.cuh"
@@ -110,12 +111,15 @@ __device__ __forceinline__ char* row_ptr(const Operand& o, const RowPos& r, cons
 
 struct Params {
   Rows rows_of;   // row axes of every operand
-  Rows gate_of;   // row axes of gate and dgate where gate rows are shared
+  Rows gate_of;   // axes of the gate's own rows, where rows share them
+  FastDiv by_share;
   uint32_t rows;
+  uint32_t turns;  // forward: rows of each group of a CTA
   uint32_t stride_s, stride_i;  // DENSE: bytes between rows of the stream's and the block's operands
   int C;
   int lanes;      // threads of a row's group (a multiple of 32 where it spans warps)
   bool rms;
+  bool wide_params;  // the parameter vectors are 16-byte aligned
   float eps, inv_c;
   Operand x, u, gate, x1, y, dx1, dy, dx, du, dgate;
   const float *scale, *gamma_post, *beta_post, *gamma_pre, *beta_pre;
@@ -157,12 +161,15 @@ struct At {
 // ---------------------------------------------------------------------------
 // a thread's 8 channels of a row, as four pairs
 // ---------------------------------------------------------------------------
-// VEC: channels 8 * lane + e, with C a multiple of 8 and 16-byte aligned rows.
-// Otherwise channels e * lanes + lane, one element per access.
-template <bool VEC>
-__device__ __forceinline__ int channel(int lane, int lanes, int e) {
-  return VEC ? lane * kE + e : e * lanes + lane;
-}
+// Which channels: 8 in a row (16 bytes of bf16); where the stream is fp32 two
+// runs of 4, the second behind the first runs of all threads that share a row
+// (of a warp, where a row spans several), so that neighbouring threads touch
+// neighbouring 16 bytes; or, where C is no multiple of 8 or a row is not
+// 16-byte aligned, every lanes-th channel, one element per access.
+enum Layout { kRun, kSplit, kSingle };
+template <typename TS, bool VEC>
+constexpr Layout layout_of() { return !VEC ? kSingle : sizeof(TS) == 2 ? kRun : kSplit; }
+
 struct V {
   float2 p[kP];
   __device__ __forceinline__ float& operator[](int e) { return e & 1 ? p[e >> 1].y : p[e >> 1].x; }
@@ -180,94 +187,106 @@ __device__ __forceinline__ float dot(const V& a, const V& b) {
   return r.x + r.y;
 }
 
-// 16-byte units of a thread's channels
-template <typename T>
-constexpr int units() { return kE * (int)sizeof(T) / 16; }
+// What a thread knows of its group.
+struct Group {
+  int lane, lanes;  // place in the row's group
+  int slot, slots;  // the group's place in the CTA
+  int c0, c1;       // first channels of its two runs of 4
+  int l, first;     // place in its warp's part of the group, and that part's first thread
+  int base;         // that part's first channel
+  bool act;         // it has channels
+  float2* buf;      // sums across warps, [2][kMaxWarps]
+  int turn;
+};
+template <Layout L>
+__device__ __forceinline__ int channel(const Group& g, int e) {
+  return L == kSingle ? e * g.lanes + g.lane : e < 4 ? g.c0 + e : g.c1 + e - 4;
+}
 
-template <typename T>
-__device__ __forceinline__ V widen(const uint4 (&r)[units<T>()]) {
+__device__ __forceinline__ void put_quad(V& v, int h, float4 q) {
+  v.p[2 * h] = make_float2(q.x, q.y);
+  v.p[2 * h + 1] = make_float2(q.z, q.w);
+}
+__device__ __forceinline__ void put_quad(V& v, int h, uint2 q) {
+  v.p[2 * h] = make_float2(bf16lo(q.x), bf16hi(q.x));
+  v.p[2 * h + 1] = make_float2(bf16lo(q.y), bf16hi(q.y));
+}
+__device__ __forceinline__ V widen(uint4 q) {
   V v;
-  if constexpr (sizeof(T) == 2) {
-    const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+  put_quad(v, 0, make_uint2(q.x, q.y));
+  put_quad(v, 1, make_uint2(q.z, q.w));
+  return v;
+}
+__device__ __forceinline__ uint2 narrow(const V& v, int h) {
+  const float2 a = v.p[2 * h], b = v.p[2 * h + 1];
+  return make_uint2(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y));
+}
+
+template <typename T, Layout L>
+__device__ __forceinline__ V load(const char* row, const Group& g, int C) {
+  V v{};
+  const T* p = reinterpret_cast<const T*>(row);
+  if constexpr (L == kSingle) {
 #pragma unroll
-    for (int k = 0; k < kP; ++k) v.p[k] = make_float2(bf16lo(w[k]), bf16hi(w[k]));
-  } else {
-#pragma unroll
-    for (int k = 0; k < kP; ++k) {
-      const uint4 q = r[k >> 1];
-      v.p[k] = k & 1 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
-                     : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    for (int e = 0; e < kE; ++e) {
+      const int c = channel<L>(g, e);
+      if (c < C) v[e] = static_cast<float>(p[c]);
     }
+  } else if constexpr (L == kRun && sizeof(T) == 2) {
+    if (g.c0 < C) v = widen(*reinterpret_cast<const uint4*>(p + g.c0));
+  } else {
+    using Quad = typename std::conditional<sizeof(T) == 2, uint2, float4>::type;
+    if (g.c0 < C) put_quad(v, 0, *reinterpret_cast<const Quad*>(p + g.c0));
+    if (g.c1 < C) put_quad(v, 1, *reinterpret_cast<const Quad*>(p + g.c1));
   }
   return v;
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ V load(const char* row, int lane, int lanes, int C) {
-  if constexpr (VEC) {
-    uint4 r[units<T>()];
-#pragma unroll
-    for (int k = 0; k < units<T>(); ++k) r[k] = reinterpret_cast<const uint4*>(row)[units<T>() * lane + k];
-    return widen<T>(r);
-  } else {
-    const T* p = reinterpret_cast<const T*>(row);
-    V v;
+// Writes a thread's channels where `live`.
+template <typename T, Layout L>
+__device__ __forceinline__ void store(bool live, char* row, const Group& g, int C, const V& v) {
+  T* p = reinterpret_cast<T*>(row);
+  if constexpr (L == kSingle) {
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
-      const int c = e * lanes + lane;
-      v[e] = c < C ? static_cast<float>(p[c]) : 0.f;
-    }
-    return v;
-  }
-}
-
-// Writes a thread's channels where `live`; every thread of the warp calls it.
-template <typename T, bool VEC>
-__device__ __forceinline__ void store(bool live, char* row, int lane, int lanes, int C, const V& v) {
-  if constexpr (VEC && sizeof(T) == 2) {
-    if (live && lane * kE < C)
-      reinterpret_cast<uint4*>(row)[lane] =
-          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  } else if constexpr (VEC) {
-    // Neighbouring threads exchange half of their 32 bytes, so that each of
-    // the two stores fills whole 32-byte sectors.  (A thread without channels
-    // may so store its neighbour's.)
-    const bool odd = lane & 1;
-    const float4 own = odd ? make_float4(v[4], v[5], v[6], v[7]) : make_float4(v[0], v[1], v[2], v[3]);
-    const float4 give = odd ? make_float4(v[0], v[1], v[2], v[3]) : make_float4(v[4], v[5], v[6], v[7]);
-    float4 got;
-    got.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
-    got.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
-    got.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
-    got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
-    // of a pair's four units an even thread now has 0 and 2, an odd one 1 and 3
-    const int at = 4 * (lane >> 1) + (odd ? 1 : 0);
-    float4* p = reinterpret_cast<float4*>(row) + at;
-    if (live && 4 * at < C) p[0] = odd ? got : own;
-    if (live && 4 * (at + 2) < C) p[2] = odd ? own : got;
-  } else {
-    T* p = reinterpret_cast<T*>(row);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int c = e * lanes + lane;
+      const int c = channel<L>(g, e);
       if (live && c < C) p[c] = static_cast<T>(v[e]);
+    }
+  } else if constexpr (L == kRun && sizeof(T) == 2) {
+    const uint2 a = narrow(v, 0), b = narrow(v, 1);
+    if (live && g.c0 < C) *reinterpret_cast<uint4*>(p + g.c0) = make_uint4(a.x, a.y, b.x, b.y);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = h ? g.c1 : g.c0;
+      if (!live || c >= C) continue;
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(p + c) = narrow(v, h);
+      else
+        *reinterpret_cast<float4*>(p + c) =
+            make_float4(v.p[2 * h].x, v.p[2 * h].y, v.p[2 * h + 1].x, v.p[2 * h + 1].y);
     }
   }
 }
 
 // A thread's channels of a parameter vector (`absent` without one).
-template <bool VEC>
-__device__ __forceinline__ V param(const float* p, float absent, int lane, int lanes, int C) {
-  V v;
+template <Layout L>
+__device__ __forceinline__ V param(const float* p, float absent, const Group& g, int C, bool wide) {
+  V v{};
+  if (L != kSingle && wide && p) {
+    if (g.c0 < C) put_quad(v, 0, *reinterpret_cast<const float4*>(p + g.c0));
+    if (g.c1 < C) put_quad(v, 1, *reinterpret_cast<const float4*>(p + g.c1));
+    return v;
+  }
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
-    const int c = channel<VEC>(lane, lanes, e);
+    const int c = channel<L>(g, e);
     v[e] = c < C ? (p ? p[c] : absent) : 0.f;
   }
   return v;
 }
 
-// The ring: a thread's own 16-byte slots, `UNITS` per stage.
+// The ring: copies of 16 bytes, consecutive threads to consecutive places.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   // (bytes = 0 reads nothing and fills with zeros)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -276,42 +295,47 @@ __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A thread's unit k of a row is 2 * lane + k in fp32: neighbouring threads
-// would then copy every other 16 bytes.  So the threads of a group (of a warp,
-// where a row spans several) copy consecutive units and leave each in its
-// owner's slot; in bf16 a thread's only unit is its own.  The second units lie
-// 64 bytes further than a plane, so that both halves of an owner's 32 bytes
-// are written without a bank conflict.
+// 16-byte units of a thread's channels
 template <typename T>
-__host__ __device__ constexpr uint32_t ring_bytes(uint32_t threads) {
-  return sizeof(T) == 2 ? threads * 16 : threads * 32 + 128;
-}
-struct Share {
-  int lane, lanes;   // place among the threads that copy together
-  int first;         // CTA-wide index of the first of them
-  int left;          // threads of them that have channels
-};
+constexpr int units() { return kE * (int)sizeof(T) / 16; }
 template <typename T>
-__device__ __forceinline__ void ring_put(uint32_t stage, const char* row, const Share& s, bool live) {
-  if constexpr (units<T>() == 1) {
-    const uint32_t bytes = live && s.lane < s.left ? 16u : 0u;
-    copy16(stage + (s.first + s.lane) * 16, row + (bytes ? s.lane * 16 : 0), bytes);
+__host__ __device__ constexpr uint32_t ring_bytes(uint32_t threads) { return threads * 16 * units<T>(); }
+
+// G lanes of a warp copy what they share of a row.  A thread reads what it
+// copied itself, but for the bf16 rows of kSplit, of which it copies 8
+// channels in a row and reads its two runs of 4.
+template <typename T, Layout L, int G>
+__device__ __forceinline__ void ring_put(uint32_t stage, const char* row, const Group& g, int C, bool live) {
+  constexpr int W = warps_of(G) ? 32 : G;
+  if constexpr (sizeof(T) == 2) {
+    const int c = g.base + kE * g.l;
+    const uint32_t bytes = live && c < C ? 16u : 0u;
+    copy16(stage + threadIdx.x * 16, row + (bytes ? c * 2 : 0), bytes);
   } else {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int at = k * s.lanes + s.lane;
-      const uint32_t bytes = live && at < 2 * s.left ? 16u : 0u;
-      copy16(stage + (at & 1) * (blockDim.x * 16 + 64) + (s.first + (at >> 1)) * 16, row + (bytes ? at * 16 : 0), bytes);
-    }
+    const uint32_t to = stage + g.first * 32 + g.l * 16;
+    const uint32_t b0 = live && g.c0 < C ? 16u : 0u, b1 = live && g.c1 < C ? 16u : 0u;
+    copy16(to, row + (b0 ? g.c0 * 4 : 0), b0);
+    copy16(to + W * 16, row + (b1 ? g.c1 * 4 : 0), b1);
   }
 }
-template <typename T>
-__device__ __forceinline__ V ring_get(const char* slot) {
-  uint4 r[units<T>()];
-#pragma unroll
-  for (int k = 0; k < units<T>(); ++k)
-    r[k] = *reinterpret_cast<const uint4*>(slot + k * (blockDim.x * 16 + 64));
-  return widen<T>(r);
+template <typename T, Layout L, int G>
+__device__ __forceinline__ V ring_get(const char* stage, const Group& g) {
+  constexpr int W = warps_of(G) ? 32 : G;
+  if constexpr (sizeof(T) == 2 && L == kRun) {
+    return widen(*reinterpret_cast<const uint4*>(stage + threadIdx.x * 16));
+  } else if constexpr (sizeof(T) == 2) {
+    V v;
+    const char* at = stage + g.first * 16 + g.l * 8;
+    put_quad(v, 0, *reinterpret_cast<const uint2*>(at));
+    put_quad(v, 1, *reinterpret_cast<const uint2*>(at + W * 8));
+    return v;
+  } else {
+    V v;
+    const char* at = stage + g.first * 32 + g.l * 16;
+    put_quad(v, 0, *reinterpret_cast<const float4*>(at));
+    put_quad(v, 1, *reinterpret_cast<const float4*>(at + W * 16));
+    return v;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -322,14 +346,6 @@ __device__ __forceinline__ V ring_get(const char* slot) {
 // turns, so that a sum's values are read before the barrier that precedes
 // their buffer's next use.
 constexpr int kMaxWarps = 16;
-struct Group {
-  int lane, lanes;  // place in the row's group
-  int slot, slots;  // the group's place in the CTA
-  bool act;         // VEC: the thread has channels
-  float2* buf;      // [2][kMaxWarps]
-  int turn;
-};
-
 __device__ __forceinline__ float2 across_warps(float2 v, Group& g) {
   float2* b = g.buf + (g.turn ? kMaxWarps : 0);
   g.turn ^= 1;
@@ -356,40 +372,40 @@ __device__ __forceinline__ float group_sum(float v, Group& g) {
   return v;
 }
 
-template <int G, bool VEC>
+template <int G, Layout L>
 __device__ __forceinline__ Group make_group(const Params& p, float2 (*smem)[2 * kMaxWarps]) {
+  constexpr int W = warps_of(G) ? 32 : G;
   Group g;
   g.lanes = G > 0 ? G : p.lanes;
   g.slots = (int)blockDim.x / g.lanes;
   g.slot = (int)threadIdx.x / g.lanes;
   g.lane = (int)threadIdx.x - g.slot * g.lanes;
+  g.l = g.lane % W;
+  g.first = (int)threadIdx.x - g.l;
+  g.base = (g.lane - g.l) * kE;
+  g.c0 = g.base + (L == kSplit ? 4 : kE) * g.l;
+  g.c1 = g.c0 + (L == kSplit ? 4 * W : 4);
+  g.act = L == kSingle || g.c0 < p.C;
   g.buf = G > 0 ? nullptr : smem[g.slot];
   g.turn = 0;
-  g.act = VEC ? g.lane * kE < p.C : true;
   return g;
 }
 
-template <int G>
-__device__ __forceinline__ Share make_share(const Group& g, int C) {
-  Share s;
-  s.lanes = warps_of(G) ? 32 : G;
-  s.lane = g.lane % s.lanes;
-  s.first = (int)threadIdx.x - s.lane;
-  s.left = min(max(C / kE - (g.lane - s.lane), 0), s.lanes);
-  return s;
-}
-
-// v - mean, absent channels kept at zero (VEC: a thread has all its channels
-// or none, and one without is left out of the sums by Group::act).
-template <bool VEC>
+// v - mean, absent channels kept at zero (a thread without any is left out of
+// the sums by Group::act).
+template <Layout L>
 __device__ __forceinline__ void centre(V& v, float mean, const Group& g, int C) {
   const float2 m = both(-mean);
 #pragma unroll
   for (int k = 0; k < kP; ++k) v.p[k] = add2(v.p[k], m);
-  if constexpr (!VEC) {
+  if constexpr (L == kSplit) {
+    if (C < g.lanes * kE) {
+      if (g.c1 >= C) v.p[2] = v.p[3] = both(0.f);
+    }
+  } else if constexpr (L == kSingle) {
 #pragma unroll
     for (int e = 0; e < kE; ++e)
-      if (e * g.lanes + g.lane >= C) v[e] = 0.f;
+      if (channel<L>(g, e) >= C) v[e] = 0.f;
   }
 }
 __device__ __forceinline__ void times(V& v, float r) {
@@ -399,11 +415,11 @@ __device__ __forceinline__ void times(V& v, float r) {
 
 // v becomes (v - mean) * rstd (rms: v * rstd); returns rstd.  Two passes over
 // registers, the deviations squared after the mean is removed.
-template <int G, bool VEC>
+template <int G, Layout L>
 __device__ __forceinline__ float standardise(V& v, Group& g, const Params& p) {
   if (!p.rms) {
     const float s = sum(v);
-    centre<VEC>(v, group_sum<G>(g.act ? s : 0.f, g) * p.inv_c, g, p.C);
+    centre<L>(v, group_sum<G>(g.act ? s : 0.f, g) * p.inv_c, g, p.C);
   }
   const float s = dot(v, v);
   const float r = rsqrtf(fmaf(group_sum<G>(g.act ? s : 0.f, g), p.inv_c, p.eps));
@@ -411,13 +427,13 @@ __device__ __forceinline__ float standardise(V& v, Group& g, const Params& p) {
   return r;
 }
 // Two rows at once, their sums side by side.
-template <int G, bool VEC>
+template <int G, Layout L>
 __device__ __forceinline__ float2 standardise(V& a, V& b, Group& g, const Params& p) {
   if (!p.rms) {
     const float2 s = make_float2(sum(a), sum(b));
     const float2 m = group_sum<G>(g.act ? s : both(0.f), g);
-    centre<VEC>(a, m.x * p.inv_c, g, p.C);
-    centre<VEC>(b, m.y * p.inv_c, g, p.C);
+    centre<L>(a, m.x * p.inv_c, g, p.C);
+    centre<L>(b, m.y * p.inv_c, g, p.C);
   }
   const float2 s = make_float2(dot(a, a), dot(b, b));
   const float2 t = group_sum<G>(g.act ? s : both(0.f), g);
@@ -445,8 +461,8 @@ __device__ __forceinline__ void sigmoid(V& v) {
 template <typename TS, typename TI, bool POST>
 struct FwdRing {
   static constexpr int UNITS = units<TS>() + (POST ? 2 * units<TI>() : 0);
-  // as many stages (at most 4) as leave room for three CTAs per SM
-  static constexpr int STAGES = 18 / UNITS > 4 ? 4 : 18 / UNITS;
+  // (UNITS is 3 to 6; three CTAs per SM)
+  static constexpr int STAGES = 12 / UNITS > 4 ? 4 : 12 / UNITS;
   __host__ __device__ static constexpr uint32_t stage(uint32_t threads) {
     return ring_bytes<TS>(threads) + (POST ? 2 * ring_bytes<TI>(threads) : 0);
   }
@@ -454,64 +470,47 @@ struct FwdRing {
 };
 
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
-__global__ void __launch_bounds__(threads_of(G))
+__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 3)
     k_block_norm_fwd(const __grid_constant__ Params p) {
   using Ring = FwdRing<TS, TI, POST>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
   wait_for_earlier_work();
   let_next_start();
-  Group g = make_group<G, VEC>(p, sums);
+  constexpr Layout L = layout_of<TS, VEC>();
+  constexpr bool CROSS = L == kSplit && sizeof(TI) == 2;  // a warp's threads read each other's copies
+  Group g = make_group<G, L>(p, sums);
   const int C = p.C;
   const bool gated = POST && p.gate.p != nullptr;
   const bool shared_gate = p.share > 1;
 
-  // scale folded into the post-norm's parameters
-  V g1, b1, g2, b2;
-  if (POST) {
-    const V s = param<VEC>(p.scale, 1.f, g.lane, g.lanes, C);
-    g1 = param<VEC>(p.gamma_post, 1.f, g.lane, g.lanes, C);
-    b1 = param<VEC>(p.beta_post, 0.f, g.lane, g.lanes, C);
-#pragma unroll
-    for (int k = 0; k < kP; ++k) {
-      g1.p[k] = mul2(g1.p[k], s.p[k]);
-      b1.p[k] = mul2(b1.p[k], s.p[k]);
-    }
-  }
-  if (PRE) {
-    g2 = param<VEC>(p.gamma_pre, 1.f, g.lane, g.lanes, C);
-    b2 = param<VEC>(p.beta_pre, 0.f, g.lane, g.lanes, C);
-  }
-
   const uint32_t stage_bytes = Ring::stage(blockDim.x);
-  const char* mine = smem + threadIdx.x * 16;
   const uint32_t ring_s = smem_u32(smem);
-  const Share share = make_share<G>(g, C);
-  // a warp's threads' part of a row begins at the first of them
-  const int from = g.lane - share.lane;
   auto gate_row = [&](uint32_t row, const At<DENSE>& r) {
-    return shared_gate ? row_ptr(p.gate, row_pos(p.gate_of, row), p.gate_of) : r.block(p, p.gate);
+    return shared_gate ? row_ptr(p.gate, row_pos(p.gate_of, div_by(row, p.by_share)), p.gate_of)
+                       : r.block(p, p.gate);
   };
+  // this CTA's rows: `turns` of every group, one behind the other
+  const uint32_t base = blockIdx.x * g.slots * p.turns;
+  const uint32_t last = min(p.rows, base + g.slots * p.turns);
   auto fetch = [&](uint32_t stage, uint32_t row) {
-    const bool live = row < p.rows;
+    const bool live = row < last;
     const uint32_t at = live ? row : 0u;
     const At<DENSE> r(p, at);
     uint32_t slot = ring_s + stage * stage_bytes;
-    ring_put<TS>(slot, r.stream(p, p.x) + from * kE * sizeof(TS), share, live);
+    ring_put<TS, L, G>(slot, r.stream(p, p.x), g, C, live);
     if (POST) {
       slot += ring_bytes<TS>(blockDim.x);
-      ring_put<TI>(slot, r.block(p, p.u) + from * kE * sizeof(TI), share, live);
-      if (gated) ring_put<TI>(slot + ring_bytes<TI>(blockDim.x), gate_row(at, r) + from * kE * sizeof(TI), share, live);
+      ring_put<TI, L, G>(slot, r.block(p, p.u), g, C, live);
+      if (gated) ring_put<TI, L, G>(slot + ring_bytes<TI>(blockDim.x), gate_row(at, r), g, C, live);
     }
   };
 
-  // every thread of a warp (or of a row's warps) takes part in the sums, so
-  // all groups of a CTA make the same number of turns
-  const uint32_t step = gridDim.x * g.slots;
-  uint32_t row = blockIdx.x * g.slots + g.slot;
-  const uint32_t base = blockIdx.x * g.slots;
-  uint32_t turns = base < p.rows ? (p.rows - base + step - 1) / step : 0;
-  uint32_t stage = 0;
+  // Every thread of a warp (or of a row's warps) takes part in the sums, so
+  // all groups of a CTA make the same number of turns.
+  const uint32_t step = g.slots;
+  uint32_t turns = (last - base + step - 1) / step;
+  uint32_t row = base + g.slot, stage = 0;
   if constexpr (ring_of(G, VEC)) {
 #pragma unroll
     for (int s = 0; s < Ring::STAGES - 1; ++s) {
@@ -519,37 +518,54 @@ __global__ void __launch_bounds__(threads_of(G))
       copies_close();
     }
   }
+  // scale folded into the post-norm's parameters
+  V g1, b1, g2, b2;
+  if (POST) {
+    const V s = param<L>(p.scale, 1.f, g, C, p.wide_params);
+    g1 = param<L>(p.gamma_post, 1.f, g, C, p.wide_params);
+    b1 = param<L>(p.beta_post, 0.f, g, C, p.wide_params);
+#pragma unroll
+    for (int k = 0; k < kP; ++k) {
+      g1.p[k] = mul2(g1.p[k], s.p[k]);
+      b1.p[k] = mul2(b1.p[k], s.p[k]);
+    }
+  }
+  if (PRE) {
+    g2 = param<L>(p.gamma_pre, 1.f, g, C, p.wide_params);
+    b2 = param<L>(p.beta_pre, 0.f, g, C, p.wide_params);
+  }
+
   for (; turns > 0; --turns, row += step) {
-    const bool live = row < p.rows;
+    const bool live = row < last;
     const At<DENSE> r(p, live ? row : 0);
     V x, u, q;
     if constexpr (ring_of(G, VEC)) {
       const uint32_t ahead = stage == 0 ? Ring::STAGES - 1 : stage - 1;
-      __syncwarp();  // the warp has read that stage
+      if (CROSS) __syncwarp();  // the warp has read that stage
       fetch(ahead, row + (Ring::STAGES - 1) * step);
       copies_close();
       copies_wait<Ring::STAGES - 1>();
-      __syncwarp();  // what the warp's other threads copied
-      const char* slot = mine + stage * stage_bytes;
-      x = ring_get<TS>(slot);
+      if (CROSS) __syncwarp();  // what the warp's other threads copied
+      const char* slot = smem + stage * stage_bytes;
+      x = ring_get<TS, L, G>(slot, g);
       if (POST) {
         slot += ring_bytes<TS>(blockDim.x);
-        u = ring_get<TI>(slot);
-        if (gated) q = ring_get<TI>(slot + ring_bytes<TI>(blockDim.x));
+        u = ring_get<TI, L, G>(slot, g);
+        if (gated) q = ring_get<TI, L, G>(slot + ring_bytes<TI>(blockDim.x), g);
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
     } else {
       x = u = q = V{};
       if (live && g.act) {
-        x = load<TS, VEC>(r.stream(p, p.x), g.lane, g.lanes, C);
+        x = load<TS, L>(r.stream(p, p.x), g, C);
         if (POST) {
-          u = load<TI, VEC>(r.block(p, p.u), g.lane, g.lanes, C);
-          if (gated) q = load<TI, VEC>(gate_row(row, r), g.lane, g.lanes, C);
+          u = load<TI, L>(r.block(p, p.u), g, C);
+          if (gated) q = load<TI, L>(gate_row(row, r), g, C);
         }
       }
     }
     if (POST) {
-      standardise<G, VEC>(u, g, p);
+      standardise<G, L>(u, g, p);
       if (gated) {
         sigmoid(q);
 #pragma unroll
@@ -558,13 +574,13 @@ __global__ void __launch_bounds__(threads_of(G))
 #pragma unroll
         for (int k = 0; k < kP; ++k) x.p[k] = add2(x.p[k], fma2(u.p[k], g1.p[k], b1.p[k]));
       }
-      store<TS, VEC>(live, r.stream(p, p.x1), g.lane, g.lanes, C, x);
+      store<TS, L>(live, r.stream(p, p.x1), g, C, x);
     }
     if (PRE) {
-      standardise<G, VEC>(x, g, p);
+      standardise<G, L>(x, g, p);
 #pragma unroll
       for (int k = 0; k < kP; ++k) x.p[k] = fma2(x.p[k], g2.p[k], b2.p[k]);
-      store<TI, VEC>(live, r.block(p, p.y), g.lane, g.lanes, C, x);
+      store<TI, L>(live, r.block(p, p.y), g, C, x);
     }
   }
   if constexpr (ring_of(G, VEC)) copies_wait<0>();
@@ -625,8 +641,9 @@ template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED>
 struct BwdRing {
   static constexpr int UNITS = units<TS>() * (PRE ? 2 : 1) + (PRE ? units<TI>() : 0) +
                                (POST ? units<TI>() * (GROUPED ? 1 : 2) : 0);
-  // as many stages (at most 4) as leave room for two CTAs per SM
-  static constexpr int STAGES = 24 / UNITS > 4 ? 4 : 24 / UNITS;
+  // One row ahead is enough: with more the rows in flight lie further apart
+  // (N = 768, bf16, warps in step: 206 us with 4 stages, 196 with 3, 184 with 2).
+  static constexpr int STAGES = 2;
   __host__ __device__ static constexpr uint32_t stage(uint32_t threads) {
     return ring_bytes<TS>(threads) * (PRE ? 2 : 1) + (PRE ? ring_bytes<TI>(threads) : 0) +
            (POST ? ring_bytes<TI>(threads) * (GROUPED ? 1 : 2) : 0);
@@ -648,21 +665,24 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
   wait_for_earlier_work();
-  Group g = make_group<G, VEC>(p, sums);
+  constexpr Layout L = layout_of<TS, VEC>();
+  constexpr bool CROSS = L == kSplit && sizeof(TI) == 2;  // a warp's threads read each other's copies
+  Group g = make_group<G, L>(p, sums);
   const int C = p.C;
   const bool gated = POST && (GROUPED || p.gate.p != nullptr);
   const bool with_dx1 = p.dx1.p != nullptr;
 
   constexpr bool RING = ring_of(G, VEC);
+  constexpr bool STEP = RING && !GROUPED && !warps_of(G) && sizeof(TI) == 2;
   float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
   // parameters: [vector][half][lane] float4, read back without bank conflicts
   float4* const prm = reinterpret_cast<float4*>(smem + bwd_sums_bytes(blockDim.x));
   char* const ring = reinterpret_cast<char*>(prm) + bwd_params_bytes(g.lanes);
   // scale * gamma_post, scale * beta_post, gamma_pre
   auto read = [&](int k) {
-    if (k == 2) return param<VEC>(p.gamma_pre, 1.f, g.lane, g.lanes, C);
-    V v = param<VEC>(k == 0 ? p.gamma_post : p.beta_post, k == 0 ? 1.f : 0.f, g.lane, g.lanes, C);
-    const V s = param<VEC>(p.scale, 1.f, g.lane, g.lanes, C);
+    if (k == 2) return param<L>(p.gamma_pre, 1.f, g, C, p.wide_params);
+    V v = param<L>(k == 0 ? p.gamma_post : p.beta_post, k == 0 ? 1.f : 0.f, g, C, p.wide_params);
+    const V s = param<L>(p.scale, 1.f, g, C, p.wide_params);
 #pragma unroll
     for (int j = 0; j < kP; ++j) v.p[j] = mul2(v.p[j], s.p[j]);
     return v;
@@ -690,27 +710,23 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   V dg = zero;                                        // the gate's gradient
 
   const uint32_t stage_bytes = Ring::stage(blockDim.x);
-  const char* mine = ring + threadIdx.x * 16;
   const uint32_t ring_s = smem_u32(ring);
-  const Share share = make_share<G>(g, C);
-  const size_t from_s = (size_t)(g.lane - share.lane) * kE * sizeof(TS);
-  const size_t from_i = (size_t)(g.lane - share.lane) * kE * sizeof(TI);
   // ring order: dx1, (x1, dy), (u, gate)
   auto fetch = [&](uint32_t stage, uint32_t row, bool live) {
     const At<DENSE> r(p, live ? row : 0u);
     uint32_t slot = ring_s + stage * stage_bytes;
-    if (with_dx1) ring_put<TS>(slot, r.stream(p, p.dx1) + from_s, share, live);
+    if (with_dx1) ring_put<TS, L, G>(slot, r.stream(p, p.dx1), g, C, live);
     slot += ring_bytes<TS>(blockDim.x);
     if (PRE) {
-      ring_put<TS>(slot, r.stream(p, p.x) + from_s, share, live);
+      ring_put<TS, L, G>(slot, r.stream(p, p.x), g, C, live);
       slot += ring_bytes<TS>(blockDim.x);
-      ring_put<TI>(slot, r.block(p, p.dy) + from_i, share, live);
+      ring_put<TI, L, G>(slot, r.block(p, p.dy), g, C, live);
       slot += ring_bytes<TI>(blockDim.x);
     }
     if (POST) {
-      ring_put<TI>(slot, r.block(p, p.u) + from_i, share, live);
+      ring_put<TI, L, G>(slot, r.block(p, p.u), g, C, live);
       slot += ring_bytes<TI>(blockDim.x);
-      if (!GROUPED && gated) ring_put<TI>(slot, r.block(p, p.gate) + from_i, share, live);
+      if (!GROUPED && gated) ring_put<TI, L, G>(slot, r.block(p, p.gate), g, C, live);
     }
   };
 
@@ -735,8 +751,8 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     const At<DENSE> r(p, live ? row : 0);
     if constexpr (GROUPED) {
       if (fresh) {
-        const RowPos rg = row_pos(p.gate_of, at.gate_row * p.share);
-        q = g.act ? load<TI, VEC>(row_ptr(p.gate, rg, p.gate_of), g.lane, g.lanes, C) : zero;
+        const RowPos rg = row_pos(p.gate_of, at.gate_row);
+        q = g.act ? load<TI, L>(row_ptr(p.gate, rg, p.gate_of), g, C) : zero;
         sigmoid(q);
         dg = zero;
       }
@@ -744,34 +760,38 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     V D = zero, h, dy, u, gt;
     if constexpr (RING) {
       const uint32_t to = stage == 0 ? Ring::STAGES - 1 : stage - 1;
-      __syncwarp();  // the warp has read that stage
+      // The CTA's warps stay in step: left to themselves they drift apart and the
+      // rows in flight with them (N = 768, bf16: 221 us so, 184 in step).  Not
+      // where a row takes several warps, which meet anyway, nor for fp32 rows.
+      if (STEP) __syncthreads();
+      if (CROSS) __syncwarp();  // the warp has read that stage
       if (ahead.left > 0) {
         fetch(to, ahead.row, ahead.row < ahead.end);
         ahead.advance(p, g);
       }
       copies_close();
       copies_wait<Ring::STAGES - 1>();
-      __syncwarp();  // what the warp's other threads copied
-      const char* slot = mine + stage * stage_bytes;
-      if (with_dx1) D = ring_get<TS>(slot);
+      if (CROSS) __syncwarp();  // what the warp's other threads copied
+      const char* slot = ring + stage * stage_bytes;
+      if (with_dx1) D = ring_get<TS, L, G>(slot, g);
       slot += ring_bytes<TS>(blockDim.x);
       if (PRE) {
-        h = ring_get<TS>(slot);
+        h = ring_get<TS, L, G>(slot, g);
         slot += ring_bytes<TS>(blockDim.x);
-        dy = ring_get<TI>(slot);
+        dy = ring_get<TI, L, G>(slot, g);
         slot += ring_bytes<TI>(blockDim.x);
       }
       if (POST) {
-        u = ring_get<TI>(slot);
-        if (!GROUPED && gated) gt = ring_get<TI>(slot + ring_bytes<TI>(blockDim.x));
+        u = ring_get<TI, L, G>(slot, g);
+        if (!GROUPED && gated) gt = ring_get<TI, L, G>(slot + ring_bytes<TI>(blockDim.x), g);
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
     } else {
       auto stream = [&](const Operand& o) {
-        return live && g.act ? load<TS, VEC>(r.stream(p, o), g.lane, g.lanes, C) : zero;
+        return live && g.act ? load<TS, L>(r.stream(p, o), g, C) : zero;
       };
       auto block = [&](const Operand& o) {
-        return live && g.act ? load<TI, VEC>(r.block(p, o), g.lane, g.lanes, C) : zero;
+        return live && g.act ? load<TI, L>(r.block(p, o), g, C) : zero;
       };
       if (with_dx1) D = stream(p.dx1);
       if (PRE) {
@@ -785,9 +805,9 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     }
 
     float2 rstd = both(0.f);  // of x1 and of u
-    if (PRE && POST) rstd = standardise<G, VEC>(h, u, g, p);
-    else if (PRE) rstd.x = standardise<G, VEC>(h, g, p);
-    else rstd.y = standardise<G, VEC>(u, g, p);
+    if (PRE && POST) rstd = standardise<G, L>(h, u, g, p);
+    else if (PRE) rstd.x = standardise<G, L>(h, g, p);
+    else rstd.y = standardise<G, L>(u, g, p);
     if (PRE) {
       const V g2 = get(2);
 #pragma unroll
@@ -802,7 +822,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
 #pragma unroll
       for (int k = 0; k < kP; ++k)
         D.p[k] = fma2(rs, fma2(m1, h.p[k], add2(dy.p[k], m0)), D.p[k]);
-      store<TS, VEC>(live, r.stream(p, p.dx), g.lane, g.lanes, C, D);
+      store<TS, L>(live, r.stream(p, p.dx), g, C, D);
     }
     if (POST) {
       if (!GROUPED && gated) {
@@ -828,8 +848,8 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
       const float2 m0 = both(p.rms ? 0.f : -s.x * p.inv_c), m1 = both(-s.y * p.inv_c), rs = both(rstd.y);
 #pragma unroll
       for (int k = 0; k < kP; ++k) b.p[k] = mul2(rs, fma2(m1, u.p[k], add2(b.p[k], m0)));
-      store<TI, VEC>(live, r.block(p, p.du), g.lane, g.lanes, C, b);
-      if (!GROUPED && gated) store<TI, VEC>(live, r.block(p, p.dgate), g.lane, g.lanes, C, dg);
+      store<TI, L>(live, r.block(p, p.du), g, C, b);
+      if (!GROUPED && gated) store<TI, L>(live, r.block(p, p.dgate), g, C, dg);
     }
 
     const Walk<GROUPED> was = at;
@@ -843,23 +863,23 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
           const int width = g.lanes * kE;
           __syncthreads();
 #pragma unroll
-          for (int e = 0; e < kE; ++e) red[g.slot * width + channel<VEC>(g.lane, g.lanes, e)] = dg[e];
+          for (int e = 0; e < kE; ++e) red[g.slot * width + channel<L>(g, e)] = dg[e];
           __syncthreads();
           if (g.slot == 0) {
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
               float s = 0.f;
-              for (int i = 0; i < g.slots; ++i) s += red[i * width + channel<VEC>(g.lane, g.lanes, e)];
+              for (int i = 0; i < g.slots; ++i) s += red[i * width + channel<L>(g, e)];
               dg[e] = s;
             }
           }
         }
         const bool writes = owns && (!p.by_cta || g.slot == 0);
         if (p.segs == 1) {
-          const RowPos rg = row_pos(p.gate_of, was.gate_row * p.share);
-          store<TI, VEC>(writes, row_ptr(p.dgate, rg, p.gate_of), g.lane, g.lanes, C, dg);
+          const RowPos rg = row_pos(p.gate_of, was.gate_row);
+          store<TI, L>(writes, row_ptr(p.dgate, rg, p.gate_of), g, C, dg);
         } else {
-          store<float, VEC>(writes, reinterpret_cast<char*>(p.gate_part + (size_t)was.item * C), g.lane, g.lanes, C, dg);
+          store<float, L>(writes, reinterpret_cast<char*>(p.gate_part + (size_t)was.item * C), g, C, dg);
         }
       }
     }
@@ -873,7 +893,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     if (!p.wanted[k >> 1]) continue;
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kE; ++e) red[g.slot * width + channel<VEC>(g.lane, g.lanes, e)] = acc[k][e];
+    for (int e = 0; e < kE; ++e) red[g.slot * width + channel<L>(g, e)] = acc[k][e];
     __syncthreads();
     float* dst = p.part + ((size_t)blockIdx.x * kSums + k) * C;
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
@@ -944,12 +964,14 @@ inline Space order_axes(const int (&n)[3], const RowOperand* const* ops, int cou
 }
 
 // Three axes (the innermost last) of the operands in `use`: neighbouring axes
-// that all of them walk as one become one.
+// that all of them walk as one become one.  `own_rows`: without the axes along
+// which the gate repeats.
 inline Rows join_axes(const Space& sp, const RowOperand* const* ops, Operand* const* dst,
-                      const int* esize, int count, const bool* use) {
+                      const int* esize, int count, const bool* use, bool own_rows) {
   Axis ax[3];
   int m = 0;
   for (int d = 0; d < sp.count; ++d) {
+    if (own_rows && sp.ax[d].shared) continue;
     bool join = m > 0;
     for (int i = 0; join && i < count; ++i)
       if (use[i] && ops[i]->p) join = ax[m - 1].s[i] == sp.ax[d].s[i] * (int64_t)sp.ax[d].n;
@@ -996,8 +1018,9 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     gates[i] = is_gate[i] && sp.share > 1;
     rows[i] = !gates[i];
   }
-  p.rows_of = join_axes(sp, ops, dst, esize, count, rows);
-  p.gate_of = join_axes(sp, ops, dst, esize, count, gates);
+  p.rows_of = join_axes(sp, ops, dst, esize, count, rows, false);
+  p.gate_of = join_axes(sp, ops, dst, esize, count, gates, true);
+  p.by_share = fast_div(sp.share);
   p.rows = (uint32_t)((int64_t)c.n[0] * c.n[1] * c.n[2]);
   pl.vec = c.C % kE == 0;
   for (int i = 0; i < count; ++i) {
@@ -1024,6 +1047,9 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
   p.beta_post = c.beta_post;
   p.gamma_pre = c.gamma_pre;
   p.beta_pre = c.beta_pre;
+  p.wide_params = true;
+  for (const float* v : {c.scale, c.gamma_post, c.beta_post, c.gamma_pre, c.beta_pre})
+    if (reinterpret_cast<uintptr_t>(v) % 16) p.wide_params = false;
   const int need = (c.C + kE - 1) / kE;  // threads of a row
   if (need <= 32) {
     pl.g = pl.vec ? (need <= 8 ? 8 : need <= 16 ? 16 : 32) : 32;
@@ -1074,7 +1100,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
 #pragma unroll
   for (int i = 1; i < kReduceWarps; ++i) s = add2(s, red[i][lane]);
   if (!is_param) {
-    char* row = row_ptr(p.dgate, row_pos(p.gate_of, (uint32_t)what * p.share), p.gate_of);
+    char* row = row_ptr(p.dgate, row_pos(p.gate_of, (uint32_t)what), p.gate_of);
     reinterpret_cast<TI*>(row)[c] = static_cast<TI>(s.x);
   } else if (what == 0) {
     const float sc = p.scale ? p.scale[c] : 1.f;
@@ -1089,7 +1115,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
 }
 
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
-cudaError_t launch_fwd(const Plan& pl, cudaStream_t st) {
+cudaError_t launch_fwd(Plan pl, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
   auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE, DENSE>;
   using Ring = FwdRing<TS, TI, POST>;
@@ -1098,8 +1124,15 @@ cudaError_t launch_fwd(const Plan& pl, cudaStream_t st) {
   int ctas = 0;
   cudaError_t e = resident_ctas(kern, pl.threads, smem, RING ? Ring::bytes(kThreads) : 0, cache, &ctas);
   if (e != cudaSuccess) return e;
-  const unsigned need = (pl.p.rows + pl.slots - 1) / pl.slots;
-  return launch_early(kern, std::min<unsigned>(need, (unsigned)ctas), pl.threads, smem, st, pl.p);
+  // The CTAs are many and short (up to 8 turns), so that the rows that are in
+  // flight lie close together: CTAs that walk the rows with a stride of the
+  // grid drift apart, which costs a fifth of the memory rate (N = 768, bf16:
+  // 136 us so, 113 with 8 turns per CTA).
+  Params p = pl.p;
+  const unsigned need = (p.rows + pl.slots - 1) / pl.slots;
+  p.turns = std::max(1u, std::min<unsigned>(8, need / (unsigned)ctas));
+  const unsigned per_cta = pl.slots * p.turns;
+  return launch_early(kern, (p.rows + per_cta - 1) / per_cta, pl.threads, smem, st, p);
 }
 
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED, bool DENSE>

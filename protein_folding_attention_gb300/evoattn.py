@@ -437,17 +437,13 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
             out["dgate"] = dgate = torch.empty_like(gate)
             words.append(dgate.data_ptr())
             words += (dgate if full is gate else dgate.expand(shape)).stride()
-        params = (("dscale", scale), ("dgamma_post", gamma_post), ("dbeta_post", beta_post),
-                  ("dgamma_pre", gamma_pre), ("dbeta_pre", beta_pre))
-        given = sum(t is not None for _, t in params)
-        if given:
-            rows = iter(torch.empty((given, C), device=lead.device, dtype=torch.float32).unbind(0))
-        for name, t in params:
+        for name, t in (("dscale", scale), ("dgamma_post", gamma_post), ("dbeta_post", beta_post),
+                        ("dgamma_pre", gamma_pre), ("dbeta_pre", beta_pre)):
             if t is None:
                 words.append(0)
             else:
-                out[name] = row = next(rows)
-                words.append(row.data_ptr())
+                out[name] = t = torch.empty_like(t)
+                words.append(t.data_ptr())
         if workspace is None:
             workspace = torch.empty(lib.evoattn_block_norm_bwd_workspace_size(C), device=lead.device,
                                     dtype=torch.uint8)
