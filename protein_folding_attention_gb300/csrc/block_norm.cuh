@@ -28,8 +28,9 @@
 // Layout: a row belongs to a group of G threads, 8 channels each, so that a
 // bf16 row is one 16-byte access per thread and its values stay in registers
 // from load to store.  G = 8, 16 or 32 lanes of a warp up to C = 256 (sums by
-// shuffles); above that several warps (sums by shuffles, then through shared
-// memory with one named barrier per sum).  Persistent CTAs walk the rows.  A thread
+// shuffles); a warp with two such parts per lane up to C = 512; above that
+// several warps (sums by shuffles, then through shared memory with one named
+// barrier per sum).  Persistent CTAs walk the rows.  A thread
 // copies its own channels of the coming rows into a ring in shared memory
 // (cp.async, no registers held meanwhile, no barrier: it reads only what it
 // copied), and keeps the parameter gradients of its channels over all its rows
@@ -55,19 +56,20 @@ namespace norm {
 namespace {
 
 constexpr int kSums = 4;          // vectors that the backward sums over rows
-constexpr int kE = 8;             // channels per thread
-constexpr int kP = kE / 2;        // pairs of channels (packed fp32 arithmetic)
+constexpr int kE = 8;             // channels of a part: what a thread has of a row, or half of it
 constexpr int kThreads = 256;     // threads of a CTA where a row takes at most 8 warps
 constexpr int kMaxThreads = 512;  // ... 16 warps (C = 4096)
 
-// How a row is laid over threads: 8, 16 or 32 lanes of a warp, several warps
-// (up to 8, with the ring), or any number of warps without a ring, whose rows
-// and parameters are read as they are needed (more than 8 warps, or rows that
-// cannot be copied 16 bytes at a time).
-constexpr int kWarps = 0, kPlain = -1;
+// How a row is laid over threads: 8, 16 or 32 lanes of a warp; a whole warp
+// with two parts per lane; several warps (up to 8); or any number of warps
+// without a ring, whose rows and parameters are read as they are needed (more
+// than 8 warps, or rows that cannot be copied 16 bytes at a time).
+constexpr int kTwice = 64, kWarps = 0, kPlain = -1;
 constexpr bool warps_of(int G) { return G <= 0; }
+constexpr int width_of(int G) { return G <= 0 || G > 32 ? 32 : G; }  // lanes of a warp that share a row
+constexpr int parts_of(int G) { return G == kTwice ? 2 : 1; }
 constexpr bool ring_of(int G, bool vec) { return vec && G >= 0; }
-constexpr int threads_of(int G) { return G == kPlain ? kMaxThreads : kThreads; }
+constexpr int threads_of(int G) { return G == kPlain ? kMaxThreads : G == kTwice ? kThreads / 2 : kThreads; }
 
 // ---------------------------------------------------------------------------
 // rows
@@ -159,7 +161,7 @@ struct At {
 };
 
 // ---------------------------------------------------------------------------
-// a thread's 8 channels of a row, as four pairs
+// a thread's channels of a row, in pairs
 // ---------------------------------------------------------------------------
 // Which channels: 8 in a row (16 bytes of bf16); where the stream is fp32 two
 // runs of 4, the second behind the first runs of all threads that share a row
@@ -170,19 +172,30 @@ enum Layout { kRun, kSplit, kSingle };
 template <typename TS, bool VEC>
 constexpr Layout layout_of() { return !VEC ? kSingle : sizeof(TS) == 2 ? kRun : kSplit; }
 
-struct V {
-  float2 p[kP];
+template <int Q>
+struct Vec {
+  static constexpr int E = kE * Q, P = E / 2;
+  float2 p[P];
   __device__ __forceinline__ float& operator[](int e) { return e & 1 ? p[e >> 1].y : p[e >> 1].x; }
   __device__ __forceinline__ float operator[](int e) const { return e & 1 ? p[e >> 1].y : p[e >> 1].x; }
 };
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
-__device__ __forceinline__ float sum(const V& v) {
-  const float2 s = add2(add2(v.p[0], v.p[1]), add2(v.p[2], v.p[3]));
+template <int Q>
+__device__ __forceinline__ float sum(const Vec<Q>& v) {
+  float2 s = add2(add2(v.p[0], v.p[1]), add2(v.p[2], v.p[3]));
+  if constexpr (Q == 2) s = add2(s, add2(add2(v.p[4], v.p[5]), add2(v.p[6], v.p[7])));
   return s.x + s.y;
 }
-__device__ __forceinline__ float dot(const V& a, const V& b) {
-  const float2 s = fma2(a.p[0], b.p[0], mul2(a.p[1], b.p[1]));
-  const float2 t = fma2(a.p[2], b.p[2], mul2(a.p[3], b.p[3]));
+template <int Q>
+__device__ __forceinline__ float dot(const Vec<Q>& a, const Vec<Q>& b) {
+  float2 s = mul2(a.p[1], b.p[1]), t = mul2(a.p[3], b.p[3]);
+  s = fma2(a.p[0], b.p[0], s);
+  t = fma2(a.p[2], b.p[2], t);
+#pragma unroll
+  for (int k = 4; k < Vec<Q>::P; k += 2) {
+    s = fma2(a.p[k], b.p[k], s);
+    t = fma2(a.p[k + 1], b.p[k + 1], t);
+  }
   const float2 r = add2(s, t);
   return r.x + r.y;
 }
@@ -198,67 +211,89 @@ struct Group {
   float2* buf;      // sums across warps, [2][kMaxWarps]
   int turn;
 };
-template <Layout L>
+template <Layout L, int G>
 __device__ __forceinline__ int channel(const Group& g, int e) {
-  return L == kSingle ? e * g.lanes + g.lane : e < 4 ? g.c0 + e : g.c1 + e - 4;
+  if (L == kSingle) return e * g.lanes + g.lane;
+  const int f = e % kE;
+  return (f < 4 ? g.c0 + f : g.c1 + f - 4) + e / kE * (kE * width_of(G));
+}
+// First channel of a run of 4.
+template <int G>
+__device__ __forceinline__ int run(const Group& g, int h) {
+  return (h & 1 ? g.c1 : g.c0) + h / 2 * (kE * width_of(G));
 }
 
-__device__ __forceinline__ void put_quad(V& v, int h, float4 q) {
+template <int Q>
+__device__ __forceinline__ void put_run(Vec<Q>& v, int h, float4 q) {
   v.p[2 * h] = make_float2(q.x, q.y);
   v.p[2 * h + 1] = make_float2(q.z, q.w);
 }
-__device__ __forceinline__ void put_quad(V& v, int h, uint2 q) {
+template <int Q>
+__device__ __forceinline__ void put_run(Vec<Q>& v, int h, uint2 q) {
   v.p[2 * h] = make_float2(bf16lo(q.x), bf16hi(q.x));
   v.p[2 * h + 1] = make_float2(bf16lo(q.y), bf16hi(q.y));
 }
-__device__ __forceinline__ V widen(uint4 q) {
-  V v;
-  put_quad(v, 0, make_uint2(q.x, q.y));
-  put_quad(v, 1, make_uint2(q.z, q.w));
-  return v;
+template <int Q>
+__device__ __forceinline__ void put_part(Vec<Q>& v, int k, uint4 q) {
+  put_run(v, 2 * k, make_uint2(q.x, q.y));
+  put_run(v, 2 * k + 1, make_uint2(q.z, q.w));
 }
-__device__ __forceinline__ uint2 narrow(const V& v, int h) {
+template <int Q>
+__device__ __forceinline__ uint2 narrow(const Vec<Q>& v, int h) {
   const float2 a = v.p[2 * h], b = v.p[2 * h + 1];
   return make_uint2(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y));
 }
 
-template <typename T, Layout L>
-__device__ __forceinline__ V load(const char* row, const Group& g, int C) {
-  V v{};
+template <typename T, Layout L, int G>
+__device__ __forceinline__ Vec<parts_of(G)> load(const char* row, const Group& g, int C) {
+  constexpr int Q = parts_of(G);
+  Vec<Q> v{};
   const T* p = reinterpret_cast<const T*>(row);
   if constexpr (L == kSingle) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int c = channel<L>(g, e);
+    for (int e = 0; e < v.E; ++e) {
+      const int c = channel<L, G>(g, e);
       if (c < C) v[e] = static_cast<float>(p[c]);
     }
   } else if constexpr (L == kRun && sizeof(T) == 2) {
-    if (g.c0 < C) v = widen(*reinterpret_cast<const uint4*>(p + g.c0));
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      const int c = run<G>(g, 2 * k);
+      if (c < C) put_part(v, k, *reinterpret_cast<const uint4*>(p + c));
+    }
   } else {
-    using Quad = typename std::conditional<sizeof(T) == 2, uint2, float4>::type;
-    if (g.c0 < C) put_quad(v, 0, *reinterpret_cast<const Quad*>(p + g.c0));
-    if (g.c1 < C) put_quad(v, 1, *reinterpret_cast<const Quad*>(p + g.c1));
+    using Run = typename std::conditional<sizeof(T) == 2, uint2, float4>::type;
+#pragma unroll
+    for (int h = 0; h < 2 * Q; ++h) {
+      const int c = run<G>(g, h);
+      if (c < C) put_run(v, h, *reinterpret_cast<const Run*>(p + c));
+    }
   }
   return v;
 }
 
 // Writes a thread's channels where `live`.
-template <typename T, Layout L>
-__device__ __forceinline__ void store(bool live, char* row, const Group& g, int C, const V& v) {
+template <typename T, Layout L, int G>
+__device__ __forceinline__ void store(bool live, char* row, const Group& g, int C, const Vec<parts_of(G)>& v) {
+  constexpr int Q = parts_of(G);
   T* p = reinterpret_cast<T*>(row);
   if constexpr (L == kSingle) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int c = channel<L>(g, e);
+    for (int e = 0; e < v.E; ++e) {
+      const int c = channel<L, G>(g, e);
       if (live && c < C) p[c] = static_cast<T>(v[e]);
     }
   } else if constexpr (L == kRun && sizeof(T) == 2) {
-    const uint2 a = narrow(v, 0), b = narrow(v, 1);
-    if (live && g.c0 < C) *reinterpret_cast<uint4*>(p + g.c0) = make_uint4(a.x, a.y, b.x, b.y);
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      const int c = run<G>(g, 2 * k);
+      const uint2 a = narrow(v, 2 * k), b = narrow(v, 2 * k + 1);
+      if (live && c < C) *reinterpret_cast<uint4*>(p + c) = make_uint4(a.x, a.y, b.x, b.y);
+    }
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = h ? g.c1 : g.c0;
+    for (int h = 0; h < 2 * Q; ++h) {
+      const int c = run<G>(g, h);
       if (!live || c >= C) continue;
       if constexpr (sizeof(T) == 2)
         *reinterpret_cast<uint2*>(p + c) = narrow(v, h);
@@ -270,17 +305,20 @@ __device__ __forceinline__ void store(bool live, char* row, const Group& g, int 
 }
 
 // A thread's channels of a parameter vector (`absent` without one).
-template <Layout L>
-__device__ __forceinline__ V param(const float* p, float absent, const Group& g, int C, bool wide) {
-  V v{};
+template <Layout L, int G>
+__device__ __forceinline__ Vec<parts_of(G)> param(const float* p, float absent, const Group& g, int C, bool wide) {
+  Vec<parts_of(G)> v{};
   if (L != kSingle && wide && p) {
-    if (g.c0 < C) put_quad(v, 0, *reinterpret_cast<const float4*>(p + g.c0));
-    if (g.c1 < C) put_quad(v, 1, *reinterpret_cast<const float4*>(p + g.c1));
+#pragma unroll
+    for (int h = 0; h < 2 * parts_of(G); ++h) {
+      const int c = run<G>(g, h);
+      if (c < C) put_run(v, h, *reinterpret_cast<const float4*>(p + c));
+    }
     return v;
   }
 #pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    const int c = channel<L>(g, e);
+  for (int e = 0; e < v.E; ++e) {
+    const int c = channel<L, G>(g, e);
     v[e] = c < C ? (p ? p[c] : absent) : 0.f;
   }
   return v;
@@ -295,47 +333,55 @@ __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// 16-byte units of a thread's channels
+// 16-byte units of a part
 template <typename T>
 constexpr int units() { return kE * (int)sizeof(T) / 16; }
-template <typename T>
-__host__ __device__ constexpr uint32_t ring_bytes(uint32_t threads) { return threads * 16 * units<T>(); }
+template <typename T, int G>
+__host__ __device__ constexpr uint32_t ring_bytes(uint32_t threads) {
+  return threads * 16 * units<T>() * parts_of(G);
+}
 
-// G lanes of a warp copy what they share of a row.  A thread reads what it
-// copied itself, but for the bf16 rows of kSplit, of which it copies 8
+// The lanes of a warp that share a row copy it part by part.  A thread reads
+// what it copied itself, but for the bf16 rows of kSplit, of which it copies 8
 // channels in a row and reads its two runs of 4.
 template <typename T, Layout L, int G>
 __device__ __forceinline__ void ring_put(uint32_t stage, const char* row, const Group& g, int C, bool live) {
-  constexpr int W = warps_of(G) ? 32 : G;
-  if constexpr (sizeof(T) == 2) {
-    const int c = g.base + kE * g.l;
-    const uint32_t bytes = live && c < C ? 16u : 0u;
-    copy16(stage + threadIdx.x * 16, row + (bytes ? c * 2 : 0), bytes);
-  } else {
-    const uint32_t to = stage + g.first * 32 + g.l * 16;
-    const uint32_t b0 = live && g.c0 < C ? 16u : 0u, b1 = live && g.c1 < C ? 16u : 0u;
-    copy16(to, row + (b0 ? g.c0 * 4 : 0), b0);
-    copy16(to + W * 16, row + (b1 ? g.c1 * 4 : 0), b1);
+  constexpr int W = width_of(G), Q = parts_of(G);
+  const uint32_t to = stage + g.first * (16 * units<T>() * Q) + g.l * 16;
+#pragma unroll
+  for (int k = 0; k < Q; ++k) {
+    if constexpr (sizeof(T) == 2) {
+      const int c = g.base + kE * (g.l + k * W);
+      const uint32_t bytes = live && c < C ? 16u : 0u;
+      copy16(to + k * (W * 16), row + (bytes ? c * 2 : 0), bytes);
+    } else {
+      const int a = run<G>(g, 2 * k), b = run<G>(g, 2 * k + 1);
+      const uint32_t na = live && a < C ? 16u : 0u, nb = live && b < C ? 16u : 0u;
+      copy16(to + k * (W * 32), row + (na ? a * 4 : 0), na);
+      copy16(to + k * (W * 32) + W * 16, row + (nb ? b * 4 : 0), nb);
+    }
   }
 }
 template <typename T, Layout L, int G>
-__device__ __forceinline__ V ring_get(const char* stage, const Group& g) {
-  constexpr int W = warps_of(G) ? 32 : G;
-  if constexpr (sizeof(T) == 2 && L == kRun) {
-    return widen(*reinterpret_cast<const uint4*>(stage + threadIdx.x * 16));
-  } else if constexpr (sizeof(T) == 2) {
-    V v;
-    const char* at = stage + g.first * 16 + g.l * 8;
-    put_quad(v, 0, *reinterpret_cast<const uint2*>(at));
-    put_quad(v, 1, *reinterpret_cast<const uint2*>(at + W * 8));
-    return v;
-  } else {
-    V v;
-    const char* at = stage + g.first * 32 + g.l * 16;
-    put_quad(v, 0, *reinterpret_cast<const float4*>(at));
-    put_quad(v, 1, *reinterpret_cast<const float4*>(at + W * 16));
-    return v;
+__device__ __forceinline__ Vec<parts_of(G)> ring_get(const char* stage, const Group& g) {
+  constexpr int W = width_of(G), Q = parts_of(G);
+  Vec<Q> v;
+  const char* from = stage + g.first * (16 * units<T>() * Q);
+#pragma unroll
+  for (int k = 0; k < Q; ++k) {
+    if constexpr (sizeof(T) == 2 && L == kRun) {
+      put_part(v, k, *reinterpret_cast<const uint4*>(from + g.l * 16 + k * (W * 16)));
+    } else if constexpr (sizeof(T) == 2) {
+      const char* at = from + g.l * 8 + k * (W * 16);
+      put_run(v, 2 * k, *reinterpret_cast<const uint2*>(at));
+      put_run(v, 2 * k + 1, *reinterpret_cast<const uint2*>(at + W * 8));
+    } else {
+      const char* at = from + g.l * 16 + k * (W * 32);
+      put_run(v, 2 * k, *reinterpret_cast<const float4*>(at));
+      put_run(v, 2 * k + 1, *reinterpret_cast<const float4*>(at + W * 16));
+    }
   }
+  return v;
 }
 
 // ---------------------------------------------------------------------------
@@ -359,7 +405,7 @@ __device__ __forceinline__ float2 across_warps(float2 v, Group& g) {
 template <int G>
 __device__ __forceinline__ float2 group_sum(float2 v, Group& g) {
 #pragma unroll
-  for (int o = (warps_of(G) ? 32 : G) / 2; o > 0; o >>= 1)
+  for (int o = width_of(G) / 2; o > 0; o >>= 1)
     v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
   if constexpr (warps_of(G)) v = across_warps(v, g);
   return v;
@@ -367,16 +413,16 @@ __device__ __forceinline__ float2 group_sum(float2 v, Group& g) {
 template <int G>
 __device__ __forceinline__ float group_sum(float v, Group& g) {
 #pragma unroll
-  for (int o = (warps_of(G) ? 32 : G) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = width_of(G) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (warps_of(G)) v = across_warps(make_float2(v, 0.f), g).x;
   return v;
 }
 
 template <int G, Layout L>
 __device__ __forceinline__ Group make_group(const Params& p, float2 (*smem)[2 * kMaxWarps]) {
-  constexpr int W = warps_of(G) ? 32 : G;
+  constexpr int W = width_of(G);
   Group g;
-  g.lanes = G > 0 ? G : p.lanes;
+  g.lanes = G > 0 ? W : p.lanes;
   g.slots = (int)blockDim.x / g.lanes;
   g.slot = (int)threadIdx.x / g.lanes;
   g.lane = (int)threadIdx.x - g.slot * g.lanes;
@@ -393,33 +439,36 @@ __device__ __forceinline__ Group make_group(const Params& p, float2 (*smem)[2 * 
 
 // v - mean, absent channels kept at zero (a thread without any is left out of
 // the sums by Group::act).
-template <Layout L>
-__device__ __forceinline__ void centre(V& v, float mean, const Group& g, int C) {
+template <Layout L, int G, int Q>
+__device__ __forceinline__ void centre(Vec<Q>& v, float mean, const Group& g, int C) {
   const float2 m = both(-mean);
 #pragma unroll
-  for (int k = 0; k < kP; ++k) v.p[k] = add2(v.p[k], m);
-  if constexpr (L == kSplit) {
-    if (C < g.lanes * kE) {
-      if (g.c1 >= C) v.p[2] = v.p[3] = both(0.f);
-    }
-  } else if constexpr (L == kSingle) {
+  for (int k = 0; k < v.P; ++k) v.p[k] = add2(v.p[k], m);
+  if constexpr (L == kSingle) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e)
-      if (channel<L>(g, e) >= C) v[e] = 0.f;
+    for (int e = 0; e < v.E; ++e)
+      if (channel<L, G>(g, e) >= C) v[e] = 0.f;
+  } else if constexpr (L == kSplit || Q > 1) {
+    if (C < g.lanes * v.E) {
+#pragma unroll
+      for (int h = 1; h < 2 * Q; ++h)
+        if (run<G>(g, h) >= C) v.p[2 * h] = v.p[2 * h + 1] = both(0.f);
+    }
   }
 }
-__device__ __forceinline__ void times(V& v, float r) {
+template <int Q>
+__device__ __forceinline__ void times(Vec<Q>& v, float r) {
 #pragma unroll
-  for (int k = 0; k < kP; ++k) v.p[k] = mul2(v.p[k], both(r));
+  for (int k = 0; k < v.P; ++k) v.p[k] = mul2(v.p[k], both(r));
 }
 
 // v becomes (v - mean) * rstd (rms: v * rstd); returns rstd.  Two passes over
 // registers, the deviations squared after the mean is removed.
-template <int G, Layout L>
-__device__ __forceinline__ float standardise(V& v, Group& g, const Params& p) {
+template <int G, Layout L, int Q>
+__device__ __forceinline__ float standardise(Vec<Q>& v, Group& g, const Params& p) {
   if (!p.rms) {
     const float s = sum(v);
-    centre<L>(v, group_sum<G>(g.act ? s : 0.f, g) * p.inv_c, g, p.C);
+    centre<L, G>(v, group_sum<G>(g.act ? s : 0.f, g) * p.inv_c, g, p.C);
   }
   const float s = dot(v, v);
   const float r = rsqrtf(fmaf(group_sum<G>(g.act ? s : 0.f, g), p.inv_c, p.eps));
@@ -427,13 +476,13 @@ __device__ __forceinline__ float standardise(V& v, Group& g, const Params& p) {
   return r;
 }
 // Two rows at once, their sums side by side.
-template <int G, Layout L>
-__device__ __forceinline__ float2 standardise(V& a, V& b, Group& g, const Params& p) {
+template <int G, Layout L, int Q>
+__device__ __forceinline__ float2 standardise(Vec<Q>& a, Vec<Q>& b, Group& g, const Params& p) {
   if (!p.rms) {
     const float2 s = make_float2(sum(a), sum(b));
     const float2 m = group_sum<G>(g.act ? s : both(0.f), g);
-    centre<L>(a, m.x * p.inv_c, g, p.C);
-    centre<L>(b, m.y * p.inv_c, g, p.C);
+    centre<L, G>(a, m.x * p.inv_c, g, p.C);
+    centre<L, G>(b, m.y * p.inv_c, g, p.C);
   }
   const float2 s = make_float2(dot(a, a), dot(b, b));
   const float2 t = group_sum<G>(g.act ? s : both(0.f), g);
@@ -445,9 +494,10 @@ __device__ __forceinline__ float2 standardise(V& a, V& b, Group& g, const Params
 
 // 1 / (1 + 2^(-v log2 e)): relative error of a few 2^-23 beside |v| 2^-24 of
 // the exponent; far below zero the quotient underflows to 0 (v < -87).
-__device__ __forceinline__ void sigmoid(V& v) {
+template <int Q>
+__device__ __forceinline__ void sigmoid(Vec<Q>& v) {
 #pragma unroll
-  for (int k = 0; k < kP; ++k) {
+  for (int k = 0; k < v.P; ++k) {
     float2 t = mul2(v.p[k], both(-1.4426950408889634f));
     t = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v.p[k].x) : "f"(t.x));
@@ -458,26 +508,27 @@ __device__ __forceinline__ void sigmoid(V& v) {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename TS, typename TI, bool POST>
+template <typename TS, typename TI, int G, bool POST>
 struct FwdRing {
   static constexpr int UNITS = units<TS>() + (POST ? 2 * units<TI>() : 0);
   // (UNITS is 3 to 6; three CTAs per SM)
   static constexpr int STAGES = 12 / UNITS > 4 ? 4 : 12 / UNITS;
   __host__ __device__ static constexpr uint32_t stage(uint32_t threads) {
-    return ring_bytes<TS>(threads) + (POST ? 2 * ring_bytes<TI>(threads) : 0);
+    return ring_bytes<TS, G>(threads) + (POST ? 2 * ring_bytes<TI, G>(threads) : 0);
   }
   static constexpr size_t bytes(int threads) { return (size_t)STAGES * stage(threads); }
 };
 
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
-__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 3)
+__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ? 4 : 3)
     k_block_norm_fwd(const __grid_constant__ Params p) {
-  using Ring = FwdRing<TS, TI, POST>;
+  using Ring = FwdRing<TS, TI, G, POST>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
   wait_for_earlier_work();
   let_next_start();
   constexpr Layout L = layout_of<TS, VEC>();
+  using V = Vec<parts_of(G)>;
   constexpr bool CROSS = L == kSplit && sizeof(TI) == 2;  // a warp's threads read each other's copies
   Group g = make_group<G, L>(p, sums);
   const int C = p.C;
@@ -500,9 +551,9 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 3)
     uint32_t slot = ring_s + stage * stage_bytes;
     ring_put<TS, L, G>(slot, r.stream(p, p.x), g, C, live);
     if (POST) {
-      slot += ring_bytes<TS>(blockDim.x);
+      slot += ring_bytes<TS, G>(blockDim.x);
       ring_put<TI, L, G>(slot, r.block(p, p.u), g, C, live);
-      if (gated) ring_put<TI, L, G>(slot + ring_bytes<TI>(blockDim.x), gate_row(at, r), g, C, live);
+      if (gated) ring_put<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), gate_row(at, r), g, C, live);
     }
   };
 
@@ -521,18 +572,18 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 3)
   // scale folded into the post-norm's parameters
   V g1, b1, g2, b2;
   if (POST) {
-    const V s = param<L>(p.scale, 1.f, g, C, p.wide_params);
-    g1 = param<L>(p.gamma_post, 1.f, g, C, p.wide_params);
-    b1 = param<L>(p.beta_post, 0.f, g, C, p.wide_params);
+    const V s = param<L, G>(p.scale, 1.f, g, C, p.wide_params);
+    g1 = param<L, G>(p.gamma_post, 1.f, g, C, p.wide_params);
+    b1 = param<L, G>(p.beta_post, 0.f, g, C, p.wide_params);
 #pragma unroll
-    for (int k = 0; k < kP; ++k) {
+    for (int k = 0; k < V::P; ++k) {
       g1.p[k] = mul2(g1.p[k], s.p[k]);
       b1.p[k] = mul2(b1.p[k], s.p[k]);
     }
   }
   if (PRE) {
-    g2 = param<L>(p.gamma_pre, 1.f, g, C, p.wide_params);
-    b2 = param<L>(p.beta_pre, 0.f, g, C, p.wide_params);
+    g2 = param<L, G>(p.gamma_pre, 1.f, g, C, p.wide_params);
+    b2 = param<L, G>(p.beta_pre, 0.f, g, C, p.wide_params);
   }
 
   for (; turns > 0; --turns, row += step) {
@@ -549,18 +600,18 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 3)
       const char* slot = smem + stage * stage_bytes;
       x = ring_get<TS, L, G>(slot, g);
       if (POST) {
-        slot += ring_bytes<TS>(blockDim.x);
+        slot += ring_bytes<TS, G>(blockDim.x);
         u = ring_get<TI, L, G>(slot, g);
-        if (gated) q = ring_get<TI, L, G>(slot + ring_bytes<TI>(blockDim.x), g);
+        if (gated) q = ring_get<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), g);
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
     } else {
       x = u = q = V{};
       if (live && g.act) {
-        x = load<TS, L>(r.stream(p, p.x), g, C);
+        x = load<TS, L, G>(r.stream(p, p.x), g, C);
         if (POST) {
-          u = load<TI, L>(r.block(p, p.u), g, C);
-          if (gated) q = load<TI, L>(gate_row(row, r), g, C);
+          u = load<TI, L, G>(r.block(p, p.u), g, C);
+          if (gated) q = load<TI, L, G>(gate_row(row, r), g, C);
         }
       }
     }
@@ -569,18 +620,18 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 3)
       if (gated) {
         sigmoid(q);
 #pragma unroll
-        for (int k = 0; k < kP; ++k) x.p[k] = fma2(fma2(u.p[k], g1.p[k], b1.p[k]), q.p[k], x.p[k]);
+        for (int k = 0; k < V::P; ++k) x.p[k] = fma2(fma2(u.p[k], g1.p[k], b1.p[k]), q.p[k], x.p[k]);
       } else {
 #pragma unroll
-        for (int k = 0; k < kP; ++k) x.p[k] = add2(x.p[k], fma2(u.p[k], g1.p[k], b1.p[k]));
+        for (int k = 0; k < V::P; ++k) x.p[k] = add2(x.p[k], fma2(u.p[k], g1.p[k], b1.p[k]));
       }
-      store<TS, L>(live, r.stream(p, p.x1), g, C, x);
+      store<TS, L, G>(live, r.stream(p, p.x1), g, C, x);
     }
     if (PRE) {
       standardise<G, L>(x, g, p);
 #pragma unroll
-      for (int k = 0; k < kP; ++k) x.p[k] = fma2(x.p[k], g2.p[k], b2.p[k]);
-      store<TI, L>(live, r.block(p, p.y), g, C, x);
+      for (int k = 0; k < V::P; ++k) x.p[k] = fma2(x.p[k], g2.p[k], b2.p[k]);
+      store<TI, L, G>(live, r.block(p, p.y), g, C, x);
     }
   }
   if constexpr (ring_of(G, VEC)) copies_wait<0>();
@@ -637,7 +688,7 @@ struct Walk {
   }
 };
 
-template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED>
+template <typename TS, typename TI, int G, bool POST, bool PRE, bool GROUPED>
 struct BwdRing {
   static constexpr int UNITS = units<TS>() * (PRE ? 2 : 1) + (PRE ? units<TI>() : 0) +
                                (POST ? units<TI>() * (GROUPED ? 1 : 2) : 0);
@@ -645,27 +696,28 @@ struct BwdRing {
   // (N = 768, bf16, warps in step: 206 us with 4 stages, 196 with 3, 184 with 2).
   static constexpr int STAGES = 2;
   __host__ __device__ static constexpr uint32_t stage(uint32_t threads) {
-    return ring_bytes<TS>(threads) * (PRE ? 2 : 1) + (PRE ? ring_bytes<TI>(threads) : 0) +
-           (POST ? ring_bytes<TI>(threads) * (GROUPED ? 1 : 2) : 0);
+    return ring_bytes<TS, G>(threads) * (PRE ? 2 : 1) + (PRE ? ring_bytes<TI, G>(threads) : 0) +
+           (POST ? ring_bytes<TI, G>(threads) * (GROUPED ? 1 : 2) : 0);
   }
   static constexpr size_t bytes(int threads) { return (size_t)STAGES * stage(threads); }
 };
 
 // Shared memory of the backward: a row of sums per group, and with a ring three
 // parameter vectors by thread of a group.
-constexpr size_t bwd_sums_bytes(int threads) { return (size_t)threads * kE * 4; }
-constexpr size_t bwd_params_bytes(int lanes) { return (size_t)lanes * kE * 4 * 3; }
+constexpr size_t bwd_sums_bytes(int threads, int parts) { return (size_t)threads * kE * 4 * parts; }
+constexpr size_t bwd_params_bytes(int lanes, int parts) { return (size_t)lanes * kE * 4 * 3 * parts; }
 
 // GROUPED: gate rows shared by consecutive rows, whose gradients are summed.
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED,
           bool DENSE>
-__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
+__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice && VEC && !GROUPED ? 3 : 2)
     k_block_norm_bwd(const __grid_constant__ Params p) {
-  using Ring = BwdRing<TS, TI, POST, PRE, GROUPED>;
+  using Ring = BwdRing<TS, TI, G, POST, PRE, GROUPED>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
   wait_for_earlier_work();
   constexpr Layout L = layout_of<TS, VEC>();
+  using V = Vec<parts_of(G)>;
   constexpr bool CROSS = L == kSplit && sizeof(TI) == 2;  // a warp's threads read each other's copies
   Group g = make_group<G, L>(p, sums);
   const int C = p.C;
@@ -675,16 +727,16 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
   constexpr bool RING = ring_of(G, VEC);
   constexpr bool STEP = RING && !GROUPED && !warps_of(G) && sizeof(TI) == 2;
   float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
-  // parameters: [vector][half][lane] float4, read back without bank conflicts
-  float4* const prm = reinterpret_cast<float4*>(smem + bwd_sums_bytes(blockDim.x));
-  char* const ring = reinterpret_cast<char*>(prm) + bwd_params_bytes(g.lanes);
+  // parameters: [vector][run][lane] float4, read back without bank conflicts
+  float4* const prm = reinterpret_cast<float4*>(smem + bwd_sums_bytes(blockDim.x, parts_of(G)));
+  char* const ring = reinterpret_cast<char*>(prm) + bwd_params_bytes(g.lanes, parts_of(G));
   // scale * gamma_post, scale * beta_post, gamma_pre
   auto read = [&](int k) {
-    if (k == 2) return param<L>(p.gamma_pre, 1.f, g, C, p.wide_params);
-    V v = param<L>(k == 0 ? p.gamma_post : p.beta_post, k == 0 ? 1.f : 0.f, g, C, p.wide_params);
-    const V s = param<L>(p.scale, 1.f, g, C, p.wide_params);
+    if (k == 2) return param<L, G>(p.gamma_pre, 1.f, g, C, p.wide_params);
+    V v = param<L, G>(k == 0 ? p.gamma_post : p.beta_post, k == 0 ? 1.f : 0.f, g, C, p.wide_params);
+    const V s = param<L, G>(p.scale, 1.f, g, C, p.wide_params);
 #pragma unroll
-    for (int j = 0; j < kP; ++j) v.p[j] = mul2(v.p[j], s.p[j]);
+    for (int j = 0; j < V::P; ++j) v.p[j] = mul2(v.p[j], s.p[j]);
     return v;
   };
   if (RING) {
@@ -692,22 +744,30 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
 #pragma unroll
       for (int k = POST ? 0 : 2; k < (PRE ? 3 : 2); ++k) {
         const V v = read(k);
-        prm[(2 * k) * g.lanes + g.lane] = make_float4(v[0], v[1], v[2], v[3]);
-        prm[(2 * k + 1) * g.lanes + g.lane] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int h = 0; h < V::P / 2; ++h)
+          prm[(k * (V::P / 2) + h) * g.lanes + g.lane] =
+              make_float4(v.p[2 * h].x, v.p[2 * h].y, v.p[2 * h + 1].x, v.p[2 * h + 1].y);
       }
     }
     __syncthreads();
   }
   auto get = [&](int k) {
-    if constexpr (!RING) return read(k);
-    const float4 a = prm[(2 * k) * g.lanes + g.lane], b = prm[(2 * k + 1) * g.lanes + g.lane];
-    return V{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+    if constexpr (RING) {
+      V v;
+#pragma unroll
+      for (int h = 0; h < V::P / 2; ++h) put_run(v, h, prm[(k * (V::P / 2) + h) * g.lanes + g.lane]);
+      return v;
+    } else {
+      return read(k);
+    }
   };
 
-  const V zero{{both(0.f), both(0.f), both(0.f), both(0.f)}};
-  V acc[4] = {zero, zero, zero, zero};                // sums of D q k, D q, dy h, dy
-  V q{{both(1.f), both(1.f), both(1.f), both(1.f)}};  // sigmoid(gate)
-  V dg = zero;                                        // the gate's gradient
+  const V zero{};
+  V acc[4] = {zero, zero, zero, zero};  // sums of D q k, D q, dy h, dy
+  V q, dg = zero;  // sigmoid(gate) and the gate's gradient
+#pragma unroll
+  for (int k = 0; k < V::P; ++k) q.p[k] = both(1.f);
 
   const uint32_t stage_bytes = Ring::stage(blockDim.x);
   const uint32_t ring_s = smem_u32(ring);
@@ -716,16 +776,16 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     const At<DENSE> r(p, live ? row : 0u);
     uint32_t slot = ring_s + stage * stage_bytes;
     if (with_dx1) ring_put<TS, L, G>(slot, r.stream(p, p.dx1), g, C, live);
-    slot += ring_bytes<TS>(blockDim.x);
+    slot += ring_bytes<TS, G>(blockDim.x);
     if (PRE) {
       ring_put<TS, L, G>(slot, r.stream(p, p.x), g, C, live);
-      slot += ring_bytes<TS>(blockDim.x);
+      slot += ring_bytes<TS, G>(blockDim.x);
       ring_put<TI, L, G>(slot, r.block(p, p.dy), g, C, live);
-      slot += ring_bytes<TI>(blockDim.x);
+      slot += ring_bytes<TI, G>(blockDim.x);
     }
     if (POST) {
       ring_put<TI, L, G>(slot, r.block(p, p.u), g, C, live);
-      slot += ring_bytes<TI>(blockDim.x);
+      slot += ring_bytes<TI, G>(blockDim.x);
       if (!GROUPED && gated) ring_put<TI, L, G>(slot, r.block(p, p.gate), g, C, live);
     }
   };
@@ -752,7 +812,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     if constexpr (GROUPED) {
       if (fresh) {
         const RowPos rg = row_pos(p.gate_of, at.gate_row);
-        q = g.act ? load<TI, L>(row_ptr(p.gate, rg, p.gate_of), g, C) : zero;
+        q = g.act ? load<TI, L, G>(row_ptr(p.gate, rg, p.gate_of), g, C) : zero;
         sigmoid(q);
         dg = zero;
       }
@@ -774,24 +834,24 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
       if (CROSS) __syncwarp();  // what the warp's other threads copied
       const char* slot = ring + stage * stage_bytes;
       if (with_dx1) D = ring_get<TS, L, G>(slot, g);
-      slot += ring_bytes<TS>(blockDim.x);
+      slot += ring_bytes<TS, G>(blockDim.x);
       if (PRE) {
         h = ring_get<TS, L, G>(slot, g);
-        slot += ring_bytes<TS>(blockDim.x);
+        slot += ring_bytes<TS, G>(blockDim.x);
         dy = ring_get<TI, L, G>(slot, g);
-        slot += ring_bytes<TI>(blockDim.x);
+        slot += ring_bytes<TI, G>(blockDim.x);
       }
       if (POST) {
         u = ring_get<TI, L, G>(slot, g);
-        if (!GROUPED && gated) gt = ring_get<TI, L, G>(slot + ring_bytes<TI>(blockDim.x), g);
+        if (!GROUPED && gated) gt = ring_get<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), g);
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
     } else {
       auto stream = [&](const Operand& o) {
-        return live && g.act ? load<TS, L>(r.stream(p, o), g, C) : zero;
+        return live && g.act ? load<TS, L, G>(r.stream(p, o), g, C) : zero;
       };
       auto block = [&](const Operand& o) {
-        return live && g.act ? load<TI, L>(r.block(p, o), g, C) : zero;
+        return live && g.act ? load<TI, L, G>(r.block(p, o), g, C) : zero;
       };
       if (with_dx1) D = stream(p.dx1);
       if (PRE) {
@@ -811,7 +871,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     if (PRE) {
       const V g2 = get(2);
 #pragma unroll
-      for (int k = 0; k < kP; ++k) {
+      for (int k = 0; k < V::P; ++k) {
         acc[2].p[k] = fma2(dy.p[k], h.p[k], acc[2].p[k]);
         acc[3].p[k] = add2(acc[3].p[k], dy.p[k]);
         dy.p[k] = mul2(dy.p[k], g2.p[k]);
@@ -820,9 +880,9 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
       s = group_sum<G>(g.act ? s : both(0.f), g);
       const float2 m0 = both(p.rms ? 0.f : -s.x * p.inv_c), m1 = both(-s.y * p.inv_c), rs = both(rstd.x);
 #pragma unroll
-      for (int k = 0; k < kP; ++k)
+      for (int k = 0; k < V::P; ++k)
         D.p[k] = fma2(rs, fma2(m1, h.p[k], add2(dy.p[k], m0)), D.p[k]);
-      store<TS, L>(live, r.stream(p, p.dx), g, C, D);
+      store<TS, L, G>(live, r.stream(p, p.dx), g, C, D);
     }
     if (POST) {
       if (!GROUPED && gated) {
@@ -832,7 +892,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
       const V g1 = get(0), b1 = get(1);
       V b;
 #pragma unroll
-      for (int k = 0; k < kP; ++k) {
+      for (int k = 0; k < V::P; ++k) {
         const float2 w = fma2(u.p[k], g1.p[k], b1.p[k]);  // (with the scale)
         const float2 dq = mul2(D.p[k], q.p[k]);
         acc[0].p[k] = fma2(dq, u.p[k], acc[0].p[k]);
@@ -847,9 +907,9 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
       s = group_sum<G>(g.act ? s : both(0.f), g);
       const float2 m0 = both(p.rms ? 0.f : -s.x * p.inv_c), m1 = both(-s.y * p.inv_c), rs = both(rstd.y);
 #pragma unroll
-      for (int k = 0; k < kP; ++k) b.p[k] = mul2(rs, fma2(m1, u.p[k], add2(b.p[k], m0)));
-      store<TI, L>(live, r.block(p, p.du), g, C, b);
-      if (!GROUPED && gated) store<TI, L>(live, r.block(p, p.dgate), g, C, dg);
+      for (int k = 0; k < V::P; ++k) b.p[k] = mul2(rs, fma2(m1, u.p[k], add2(b.p[k], m0)));
+      store<TI, L, G>(live, r.block(p, p.du), g, C, b);
+      if (!GROUPED && gated) store<TI, L, G>(live, r.block(p, p.dgate), g, C, dg);
     }
 
     const Walk<GROUPED> was = at;
@@ -857,19 +917,19 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
     if constexpr (GROUPED) {
       if (fresh) {
 #pragma unroll
-        for (int k = 0; k < kP; ++k) dg.p[k] = mul2(dg.p[k], fma2(q.p[k], both(-1.f), both(1.f)));
+        for (int k = 0; k < V::P; ++k) dg.p[k] = mul2(dg.p[k], fma2(q.p[k], both(-1.f), both(1.f)));
         const bool owns = p.by_cta || was.item < p.items;
         if (p.by_cta && g.slots > 1) {
-          const int width = g.lanes * kE;
+          const int width = g.lanes * V::E;
           __syncthreads();
 #pragma unroll
-          for (int e = 0; e < kE; ++e) red[g.slot * width + channel<L>(g, e)] = dg[e];
+          for (int e = 0; e < V::E; ++e) red[g.slot * width + channel<L, G>(g, e)] = dg[e];
           __syncthreads();
           if (g.slot == 0) {
 #pragma unroll
-            for (int e = 0; e < kE; ++e) {
+            for (int e = 0; e < V::E; ++e) {
               float s = 0.f;
-              for (int i = 0; i < g.slots; ++i) s += red[i * width + channel<L>(g, e)];
+              for (int i = 0; i < g.slots; ++i) s += red[i * width + channel<L, G>(g, e)];
               dg[e] = s;
             }
           }
@@ -877,9 +937,9 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
         const bool writes = owns && (!p.by_cta || g.slot == 0);
         if (p.segs == 1) {
           const RowPos rg = row_pos(p.gate_of, was.gate_row);
-          store<TI, L>(writes, row_ptr(p.dgate, rg, p.gate_of), g, C, dg);
+          store<TI, L, G>(writes, row_ptr(p.dgate, rg, p.gate_of), g, C, dg);
         } else {
-          store<float, L>(writes, reinterpret_cast<char*>(p.gate_part + (size_t)was.item * C), g, C, dg);
+          store<float, L, G>(writes, reinterpret_cast<char*>(p.gate_part + (size_t)was.item * C), g, C, dg);
         }
       }
     }
@@ -887,13 +947,13 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : 2)
 
   let_next_start();
   // the CTA's sums, group by group in order
-  const int width = g.lanes * kE;
+  const int width = g.lanes * V::E;
 #pragma unroll
   for (int k = POST ? 0 : 2; k < (PRE ? 4 : 2); ++k) {
     if (!p.wanted[k >> 1]) continue;
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kE; ++e) red[g.slot * width + channel<L>(g, e)] = acc[k][e];
+    for (int e = 0; e < V::E; ++e) red[g.slot * width + channel<L, G>(g, e)] = acc[k][e];
     __syncthreads();
     float* dst = p.part + ((size_t)blockIdx.x * kSums + k) * C;
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
@@ -998,7 +1058,7 @@ inline Rows join_axes(const Space& sp, const RowOperand* const* ops, Operand* co
 
 struct Plan {
   Params p;
-  int g;        // lanes of a row's group: 8, 16, 32, kWarps or kPlain
+  int g;        // lanes of a row's group: 8, 16, 32, or kTwice, kWarps, kPlain
   bool vec, dense;
   int threads, slots;
 };
@@ -1055,6 +1115,10 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     pl.g = pl.vec ? (need <= 8 ? 8 : need <= 16 ? 16 : 32) : 32;
     p.lanes = pl.g;
     pl.threads = kThreads;
+  } else if (need <= kTwice) {
+    pl.g = kTwice;
+    p.lanes = 32;
+    pl.threads = threads_of(kTwice);
   } else {
     pl.g = pl.vec && need <= kThreads ? kWarps : kPlain;
     const int warps = (need + 31) / 32;
@@ -1118,11 +1182,11 @@ template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool D
 cudaError_t launch_fwd(Plan pl, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
   auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE, DENSE>;
-  using Ring = FwdRing<TS, TI, POST>;
+  using Ring = FwdRing<TS, TI, G, POST>;
   constexpr bool RING = ring_of(G, VEC);
   const size_t smem = RING ? Ring::bytes(pl.threads) : 0;
   int ctas = 0;
-  cudaError_t e = resident_ctas(kern, pl.threads, smem, RING ? Ring::bytes(kThreads) : 0, cache, &ctas);
+  cudaError_t e = resident_ctas(kern, pl.threads, smem, RING ? Ring::bytes(threads_of(G)) : 0, cache, &ctas);
   if (e != cudaSuccess) return e;
   // The CTAs are many and short (up to 8 turns), so that the rows that are in
   // flight lie close together: CTAs that walk the rows with a stride of the
@@ -1140,11 +1204,13 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
   auto kern = k_block_norm_bwd<TS, TI, G, VEC, POST, PRE, GROUPED, DENSE>;
   Params& p = pl.p;
-  using Ring = BwdRing<TS, TI, POST, PRE, GROUPED>;
+  using Ring = BwdRing<TS, TI, G, POST, PRE, GROUPED>;
   constexpr bool RING = ring_of(G, VEC);
-  const size_t smem = bwd_sums_bytes(pl.threads) + (RING ? bwd_params_bytes(p.lanes) + Ring::bytes(pl.threads) : 0);
+  constexpr int Q = parts_of(G);
+  const size_t smem = bwd_sums_bytes(pl.threads, Q) +
+                      (RING ? bwd_params_bytes(p.lanes, Q) + Ring::bytes(pl.threads) : 0);
   constexpr size_t most =
-      bwd_sums_bytes(threads_of(G)) + (RING ? bwd_params_bytes(kThreads) + Ring::bytes(kThreads) : 0);
+      bwd_sums_bytes(threads_of(G), Q) + (RING ? bwd_params_bytes(kThreads, Q) + Ring::bytes(threads_of(G)) : 0);
   static_assert(most <= 227 * 1024 - 4096, "shared memory");
   int ctas = 0;
   cudaError_t e = resident_ctas(kern, pl.threads, smem, most, cache, &ctas);
@@ -1189,6 +1255,7 @@ cudaError_t ring_fwd(const Plan& pl, cudaStream_t st) {
     case 8: return launch_fwd<TS, TI, 8, true, POST, PRE, DENSE>(pl, st);
     case 16: return launch_fwd<TS, TI, 16, true, POST, PRE, DENSE>(pl, st);
     case 32: return launch_fwd<TS, TI, 32, true, POST, PRE, DENSE>(pl, st);
+    case kTwice: return launch_fwd<TS, TI, kTwice, true, POST, PRE, DENSE>(pl, st);
     default: return launch_fwd<TS, TI, kWarps, true, POST, PRE, DENSE>(pl, st);
   }
 }
@@ -1197,6 +1264,7 @@ cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
   if (pl.vec && pl.g != kPlain)
     return pl.dense ? ring_fwd<TS, TI, POST, PRE, true>(pl, st) : ring_fwd<TS, TI, POST, PRE, false>(pl, st);
   if (pl.vec) return launch_fwd<TS, TI, kPlain, true, POST, PRE, false>(pl, st);
+  if (pl.g == kTwice) return launch_fwd<TS, TI, kTwice, false, POST, PRE, false>(pl, st);
   return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE, false>(pl, st)
                     : launch_fwd<TS, TI, kPlain, false, POST, PRE, false>(pl, st);
 }
@@ -1207,6 +1275,7 @@ cudaError_t ring_bwd(const Plan& pl, float* ws, cudaStream_t st) {
     case 8: return launch_bwd<TS, TI, 8, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
     case 16: return launch_bwd<TS, TI, 16, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
     case 32: return launch_bwd<TS, TI, 32, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
+    case kTwice: return launch_bwd<TS, TI, kTwice, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
     default: return launch_bwd<TS, TI, kWarps, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
   }
 }
@@ -1216,6 +1285,7 @@ cudaError_t dispatch_bwd(const Plan& pl, float* ws, cudaStream_t st) {
     return pl.dense ? ring_bwd<TS, TI, POST, PRE, GROUPED, true>(pl, ws, st)
                     : ring_bwd<TS, TI, POST, PRE, GROUPED, false>(pl, ws, st);
   if (pl.vec) return launch_bwd<TS, TI, kPlain, true, POST, PRE, GROUPED, false>(pl, ws, st);
+  if (pl.g == kTwice) return launch_bwd<TS, TI, kTwice, false, POST, PRE, GROUPED, false>(pl, ws, st);
   return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED, false>(pl, ws, st)
                     : launch_bwd<TS, TI, kPlain, false, POST, PRE, GROUPED, false>(pl, ws, st);
 }
