@@ -707,10 +707,16 @@ struct BwdRing {
 constexpr size_t bwd_sums_bytes(int threads, int parts) { return (size_t)threads * kE * 4 * parts; }
 constexpr size_t bwd_params_bytes(int lanes, int parts) { return (size_t)lanes * kE * 4 * 3 * parts; }
 
+// CTAs per SM that the registers are cut for.  Two parts per lane need up to
+// 255 registers: 8 warps without spills (147,456 rows of 512 bf16 channels:
+// 185 us) against 12 with some (208 us); with fp32 rows the 12 are faster
+// (98,304 rows of 384 channels: 195 us against 214).
+constexpr int resident_bwd(int G, bool fp32) { return G == kPlain ? 1 : G == kTwice && fp32 ? 3 : 2; }
+
 // GROUPED: gate rows shared by consecutive rows, whose gradients are summed.
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED,
           bool DENSE>
-__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice && VEC && !GROUPED ? 3 : 2)
+__global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4 && VEC && !GROUPED))
     k_block_norm_bwd(const __grid_constant__ Params p) {
   using Ring = BwdRing<TS, TI, G, POST, PRE, GROUPED>;
   extern __shared__ __align__(16) char smem[];
@@ -725,7 +731,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice &
   const bool with_dx1 = p.dx1.p != nullptr;
 
   constexpr bool RING = ring_of(G, VEC);
-  constexpr bool STEP = RING && !GROUPED && !warps_of(G) && sizeof(TI) == 2;
+  constexpr bool STEP = RING && !GROUPED && G > 0 && G <= 32 && sizeof(TI) == 2;
   float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
   // parameters: [vector][run][lane] float4, read back without bank conflicts
   float4* const prm = reinterpret_cast<float4*>(smem + bwd_sums_bytes(blockDim.x, parts_of(G)));
@@ -822,7 +828,8 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice &
       const uint32_t to = stage == 0 ? Ring::STAGES - 1 : stage - 1;
       // The CTA's warps stay in step: left to themselves they drift apart and the
       // rows in flight with them (N = 768, bf16: 221 us so, 184 in step).  Not
-      // where a row takes several warps, which meet anyway, nor for fp32 rows.
+      // where a row takes a warp of its own or several, nor for fp32 rows, where
+      // it costs more than it gives.
       if (STEP) __syncthreads();
       if (CROSS) __syncwarp();  // the warp has read that stage
       if (ahead.left > 0) {
