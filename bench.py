@@ -299,6 +299,65 @@ def measure_transition(N, dev, peaks, steps=10, warmup=3, B=1, C=128, F=512, HD=
             "intermediate_bytes_not_written": rows * ((2 if HD else 1) * C + 3 * F) * 2}
 
 
+def _median_ms(run, dev, steps=10, warmup=3):
+    import torch
+    for _ in range(warmup):
+        run()
+    ev = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
+          for _ in range(steps)]
+    for a, b in ev:
+        a.record()
+        run()
+        b.record()
+    torch.cuda.synchronize(dev)
+    return statistics.median(a.elapsed_time(b) for a, b in ev)
+
+
+def measure_block_norm(N, dev, peaks, C=128):
+    """The seam between two blocks (norm after a block, gate, residual scale,
+    norm before the next) on the [1, N, N, C] pair representation, forward and
+    backward: CUDA-event time and the HBM rate of its algorithmic bytes
+    (forward three tensors read, two written; backward five and three)."""
+    import torch
+
+    from protein_folding_attention_gb300 import evoattn
+    gen = torch.Generator(device=dev).manual_seed(N)
+    rows = lambda: torch.randn(1, N, N, C, device=dev, generator=gen).to(torch.bfloat16)
+    x, u, gate, dx1, dy = (rows() for _ in range(5))
+    prm = [1.0 + 0.1 * torch.randn(C, device=dev, generator=gen) for _ in range(5)]
+    x1, y = torch.empty_like(x), torch.empty_like(x)
+    fwd = _median_ms(lambda: evoattn.block_norm(x, u, gate, *prm, x1=x1, y=y), dev)
+    bwd = _median_ms(lambda: evoattn.block_norm_bwd(dx1, dy, x1, u, gate, *prm), dev)
+    one = N * N * C * 2
+    res = {"workload": f"pair_block_norm_n{N}", "N": N, "C": C}
+    for name, ms, tensors in (("fwd", fwd, 5), ("bwd", bwd, 8)):
+        gbs = tensors * one / ms / 1e6
+        res[name] = {"ms": ms, "hbm_bytes": tensors * one, "hbm_gbs": gbs,
+                     "frac_of_hbm_peak": gbs / peaks["hbm_gbs"]}
+    return res
+
+
+def measure_adamw(bits, dev, peaks, blocks=48, C=128, H=4):
+    """One clipped AdamW step over the parameters of a stack of pair blocks
+    (11 tensors each: the two projections, the transition, the norms and the
+    residual scale), bf16 gradients, fp32 parameters with bf16 copies."""
+    import torch
+
+    from protein_folding_attention_gb300 import evoattn
+    shapes = [(4 * C + H, C), (C,), (C,), (C, C), (8 * C, C), (C, 4 * C), (C,), (C,), (C,), (C,),
+              (C,)] * blocks
+    gen = torch.Generator(device=dev).manual_seed(bits)
+    p = [0.02 * torch.randn(s, device=dev, generator=gen) for s in shapes]
+    g = [0.01 * torch.randn(s, device=dev, generator=gen).to(torch.bfloat16) for s in shapes]
+    opt = evoattn.AdamW(p, g, copies=[t.to(torch.bfloat16) for t in p], state_bits=bits)
+    ms = _median_ms(lambda: opt.step(max_norm=1.0), dev)
+    n = sum(t.numel() for t in p)
+    bytes_ = n * (12 + (16 if bits == 32 else 4 + 16 / evoattn.ADAMW_BLOCK))
+    return {"workload": f"adamw{bits}_{blocks}_blocks", "tensors": len(p), "parameters": n, "ms": ms,
+            "hbm_bytes": bytes_, "hbm_gbs": bytes_ / ms / 1e6,
+            "frac_of_hbm_peak": bytes_ / ms / 1e6 / peaks["hbm_gbs"]}
+
+
 def held_bytes(B, S, H, N, D, gate=True, mask=True, flags=0):
     """Device bytes a caller holds for one bf16 forward + backward: q, k, v,
     dout (+ gate) and out, dq, dk, dv (+ dgate) [B,S,H,N,D]; the pair bias
@@ -705,13 +764,15 @@ def run_ours(args, w):
             per_config[name] = measure_config(synthetic.WORKLOADS[name], dev, peak,
                                               hbm_peak=peaks["hbm_gbs"], ex2_peak=ex2_cfg)
         per_config["memory_fit"] = memory_model()
-    evofusion = None
+    evofusion = training = None
     if rank == 0 and not args.no_per_config:
         evofusion = {f"n{n}": measure_ln_proj(n, dev, peaks) for n in (384, 768)}
         evofusion.update({f"transition_n{n}": measure_transition(n, dev, peaks)
                           for n in (384, 768)})
         evofusion.update({f"outproj_transition_n{n}": measure_transition(n, dev, peaks, HD=128)
                           for n in (384, 768)})
+        training = {f"block_norm_n{n}": measure_block_norm(n, dev, peaks) for n in (384, 768)}
+        training.update({f"adamw{b}": measure_adamw(b, dev, peaks) for b in (32, 8)})
 
     cpu = None
     if rank == 0 and ws == 1 and not args.no_cpu:
@@ -743,6 +804,7 @@ def run_ours(args, w):
             "dq_modes": dq_modes,
             "roofline": roof, "sfu": sfu, "cpu_baseline": cpu, "e2e": e2e,
             "per_config": per_config, "evofusion": evofusion,
+            "training": training,
             "clocks": clocks.summary(),
             "gpu_launches": args.steps * 6,
         }

@@ -200,6 +200,20 @@ def test_shapes_and_shared_gates(shape, gate):
     check_bwd(k, run_bwd(k, False), False)
 
 
+@pytest.mark.parametrize("C", [8, 33, 99, 136, 256, 300, 384, 511, 520, 777, 1096, 2056])
+@pytest.mark.parametrize("types,gate", [("bf16", "row"), ("mixed", "batch"), ("f32", "middle"),
+                                        ("f32", "row"), ("mixed", "none")])
+def test_widths_with_shared_gates(C, types, gate):
+    """Every way a row is laid over threads, gate rows shared by a few rows (a
+    group walks them) and by many (spread over a CTA)."""
+    for shape in ((2, 3, 5, C), (1, 2, 75, C)):
+        k = draw(shape, types, gate, seed=C)
+        x1, y = run_fwd(k, C % 2 == 0)
+        check_fwd(k, x1, y, C % 2 == 0)
+        k = draw(shape, types, gate, seed=C + 1, backward=True)
+        check_bwd(k, run_bwd(k, C % 2 == 0), C % 2 == 0)
+
+
 @pytest.mark.parametrize("types", list(TYPES))
 @pytest.mark.parametrize("post,pre", [(True, False), (False, True)])
 @pytest.mark.parametrize("C,gate", [(128, "full"), (50, "row"), (512, "none"), (300, "batch")])
@@ -513,6 +527,55 @@ def test_flat_and_packed_calls_agree(gate):
         ws.numel(), stream) == 0
     for n in want:
         assert torch.equal(got[n], want[n]), n
+
+
+def test_first_call_under_capture():
+    """A fresh process whose first calls of the library are captured."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from protein_folding_attention_gb300 import evoattn
+x, v = torch.randn(1, 7, 9, 128, device="cuda").bfloat16(), torch.ones(128, device="cuda")
+p, g = torch.ones(1000, device="cuda"), torch.ones(1000, device="cuda")
+opt = evoattn.AdamW([p], [g], lr=0.5, weight_decay=0.0, state_bits=8)
+evoattn.load()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    x1, y = evoattn.block_norm(x, x, x, v, v, v, v, v)
+    d = evoattn.block_norm_bwd(x, x, x1, x, x, v, v, v, v, v)
+    opt.step(max_norm=1.0)
+assert bool((p == 1).all())
+graph.replay()
+torch.cuda.synchronize()
+a, b = evoattn.block_norm(x, x, x, v, v, v, v, v)
+e = evoattn.block_norm_bwd(x, x, a, x, x, v, v, v, v, v)
+assert torch.equal(a, x1) and torch.equal(b, y) and all(torch.equal(d[k], e[k]) for k in e)
+assert abs(float(p[5]) - 0.5) < 1e-5 and opt.steps_taken() == 1
+print("done")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stdout + r.stderr
+
+
+def test_two_streams_at_once():
+    """Calls on two streams that overlap, each with a workspace of its own."""
+    ks = [draw((1, 200, 150, 128), "bf16", "row", seed=50 + i, backward=True) for i in range(2)]
+    want = [run_bwd(k, False) for k in ks]
+    gs = [to_gpu(k) for k in ks]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ks]
+    got = [None, None]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            got[i] = evoattn.block_norm_bwd(*[gs[i][n] for n in BWD_ARGS], stream=st)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for n in b:
+            assert torch.equal(a[n], b[n]), n
 
 
 def test_python_refusals():
