@@ -384,6 +384,14 @@ __device__ __forceinline__ Vec<parts_of(G)> ring_get(const char* stage, const Gr
   return v;
 }
 
+// Rows that cannot be copied one by one in 16-byte units (C no multiple of 8)
+// but lie one behind the other: the rows of a CTA's turn are then copied as
+// one piece, which begins and ends on 16 bytes (but for the last one's end).
+__device__ __forceinline__ void chunk_put(uint32_t stage, const char* src, uint32_t bytes) {
+  for (uint32_t at = threadIdx.x * 16; at < bytes; at += blockDim.x * 16)
+    copy16(stage + at, src + at, min(16u, bytes - at));
+}
+
 // ---------------------------------------------------------------------------
 // sums over a row's group
 // ---------------------------------------------------------------------------
@@ -535,7 +543,9 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
   const bool gated = POST && p.gate.p != nullptr;
   const bool shared_gate = p.share > 1;
 
-  const uint32_t stage_bytes = Ring::stage(blockDim.x);
+  constexpr bool CHUNK = !VEC && DENSE;
+  const uint32_t chunk_s = g.slots * C * sizeof(TS), chunk_i = g.slots * C * sizeof(TI);
+  const uint32_t stage_bytes = CHUNK ? chunk_s + 2 * chunk_i : Ring::stage(blockDim.x);
   const uint32_t ring_s = smem_u32(smem);
   auto gate_row = [&](uint32_t row, const At<DENSE>& r) {
     return shared_gate ? row_ptr(p.gate, row_pos(p.gate_of, div_by(row, p.by_share)), p.gate_of)
@@ -557,6 +567,18 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
     }
   };
 
+  auto fetch_chunk = [&](uint32_t stage, uint32_t first) {
+    if (first >= last) return;
+    const uint32_t n = min(last - first, (uint32_t)g.slots) * C;
+    const At<DENSE> r(p, first);
+    const uint32_t to = ring_s + stage * stage_bytes;
+    chunk_put(to, r.stream(p, p.x), n * sizeof(TS));
+    if (POST) {
+      chunk_put(to + chunk_s, r.block(p, p.u), n * sizeof(TI));
+      if (gated && !shared_gate) chunk_put(to + chunk_s + chunk_i, r.block(p, p.gate), n * sizeof(TI));
+    }
+  };
+
   // Every thread of a warp (or of a row's warps) takes part in the sums, so
   // all groups of a CTA make the same number of turns.
   const uint32_t step = g.slots;
@@ -568,6 +590,9 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
       fetch(s, row + s * step);
       copies_close();
     }
+  } else if constexpr (CHUNK) {
+    fetch_chunk(0, base);
+    copies_close();
   }
   // scale folded into the post-norm's parameters
   V g1, b1, g2, b2;
@@ -605,6 +630,22 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
         if (gated) q = ring_get<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), g);
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
+    } else if constexpr (CHUNK) {
+      copies_wait<0>();
+      __syncthreads();  // the turn's rows are here, and the other stage has been read
+      fetch_chunk(stage ^ 1, row - g.slot + step);
+      copies_close();
+      const char* from = smem + stage * stage_bytes;
+      stage ^= 1;
+      x = u = q = V{};
+      if (live) {
+        x = load<TS, L, G>(from + g.slot * C * sizeof(TS), g, C);
+        if (POST) {
+          from += chunk_s + g.slot * C * sizeof(TI);
+          u = load<TI, L, G>(from, g, C);
+          if (gated) q = load<TI, L, G>(shared_gate ? gate_row(row, r) : from + chunk_i, g, C);
+        }
+      }
     } else {
       x = u = q = V{};
       if (live && g.act) {
@@ -634,7 +675,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
       store<TI, L, G>(live, r.block(p, p.y), g, C, x);
     }
   }
-  if constexpr (ring_of(G, VEC)) copies_wait<0>();
+  if constexpr (ring_of(G, VEC) || CHUNK) copies_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -730,7 +771,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
   const bool gated = POST && (GROUPED || p.gate.p != nullptr);
   const bool with_dx1 = p.dx1.p != nullptr;
 
-  constexpr bool RING = ring_of(G, VEC);
+  constexpr bool RING = ring_of(G, VEC), CHUNK = !VEC && DENSE, KEEP = G != kPlain;
   constexpr bool STEP = RING && !GROUPED && G > 0 && G <= 32 && sizeof(TI) == 2;
   float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
   // parameters: [vector][run][lane] float4, read back without bank conflicts
@@ -745,7 +786,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     for (int j = 0; j < V::P; ++j) v.p[j] = mul2(v.p[j], s.p[j]);
     return v;
   };
-  if (RING) {
+  if (KEEP) {
     if (g.slot == 0) {
 #pragma unroll
       for (int k = POST ? 0 : 2; k < (PRE ? 3 : 2); ++k) {
@@ -759,7 +800,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     __syncthreads();
   }
   auto get = [&](int k) {
-    if constexpr (RING) {
+    if constexpr (KEEP) {
       V v;
 #pragma unroll
       for (int h = 0; h < V::P / 2; ++h) put_run(v, h, prm[(k * (V::P / 2) + h) * g.lanes + g.lane]);
@@ -775,7 +816,8 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
 #pragma unroll
   for (int k = 0; k < V::P; ++k) q.p[k] = both(1.f);
 
-  const uint32_t stage_bytes = Ring::stage(blockDim.x);
+  const uint32_t chunk_s = g.slots * C * sizeof(TS), chunk_i = g.slots * C * sizeof(TI);
+  const uint32_t stage_bytes = CHUNK ? 2 * chunk_s + 3 * chunk_i : Ring::stage(blockDim.x);
   const uint32_t ring_s = smem_u32(ring);
   // ring order: dx1, (x1, dy), (u, gate)
   auto fetch = [&](uint32_t stage, uint32_t row, bool live) {
@@ -796,6 +838,22 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     }
   };
 
+  auto fetch_chunk = [&](uint32_t stage, uint32_t first) {
+    if (first >= p.rows) return;
+    const uint32_t n = min(p.rows - first, (uint32_t)g.slots) * C;
+    const At<DENSE> r(p, first);
+    const uint32_t to = ring_s + stage * stage_bytes;
+    if (with_dx1) chunk_put(to, r.stream(p, p.dx1), n * sizeof(TS));
+    if (PRE) {
+      chunk_put(to + chunk_s, r.stream(p, p.x), n * sizeof(TS));
+      chunk_put(to + 2 * chunk_s, r.block(p, p.dy), n * sizeof(TI));
+    }
+    if (POST) {
+      chunk_put(to + 2 * chunk_s + chunk_i, r.block(p, p.u), n * sizeof(TI));
+      if (gated) chunk_put(to + 2 * chunk_s + 2 * chunk_i, r.block(p, p.gate), n * sizeof(TI));
+    }
+  };
+
   Walk<GROUPED> at, ahead;
   at.start(p, g);
   if constexpr (RING) {
@@ -808,6 +866,9 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
       }
       copies_close();
     }
+  } else if constexpr (CHUNK) {
+    fetch_chunk(0, at.row - g.slot);
+    copies_close();
   }
   uint32_t stage = 0;
   bool fresh = true;  // a stretch begins
@@ -853,6 +914,24 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
         if (!GROUPED && gated) gt = ring_get<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), g);
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
+    } else if constexpr (CHUNK) {
+      copies_wait<0>();
+      __syncthreads();  // the turn's rows are here, and the other stage has been read
+      fetch_chunk(stage ^ 1, row - g.slot + at.hop);
+      copies_close();
+      const char* from = ring + stage * stage_bytes + g.slot * C * sizeof(TS);
+      stage ^= 1;
+      h = dy = u = gt = zero;
+      if (live) {
+        if (with_dx1) D = load<TS, L, G>(from, g, C);
+        if (PRE) h = load<TS, L, G>(from + chunk_s, g, C);
+        from += 2 * chunk_s + g.slot * C * (sizeof(TI) - sizeof(TS));
+        if (PRE) dy = load<TI, L, G>(from, g, C);
+        if (POST) {
+          u = load<TI, L, G>(from + chunk_i, g, C);
+          if (gated) gt = load<TI, L, G>(from + 2 * chunk_i, g, C);
+        }
+      }
     } else {
       auto stream = [&](const Operand& o) {
         return live && g.act ? load<TS, L, G>(r.stream(p, o), g, C) : zero;
@@ -1066,7 +1145,7 @@ inline Rows join_axes(const Space& sp, const RowOperand* const* ops, Operand* co
 struct Plan {
   Params p;
   int g;        // lanes of a row's group: 8, 16, 32, or kTwice, kWarps, kPlain
-  bool vec, dense;
+  bool vec, dense, chunk;
   int threads, slots;
 };
 
@@ -1133,6 +1212,13 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     pl.threads = p.lanes * std::max(1, kThreads / 32 / warps);
   }
   pl.slots = pl.threads / p.lanes;
+  // rows one behind the other, a turn's rows a multiple of 16 bytes
+  pl.chunk = !pl.vec && pl.dense && pl.g != kPlain;
+  for (int i = 0; i < count && pl.chunk; ++i) {
+    if (!rows[i] || !dst[i]->p) continue;
+    const int64_t row = (int64_t)c.C * esize[i];
+    pl.chunk = dst[i]->s2 == row && row * pl.slots % 16 == 0 && reinterpret_cast<uintptr_t>(dst[i]->p) % 16 == 0;
+  }
 }
 
 // Sums of the CTAs' partial sums: one block per 32 columns of the post-norm's
@@ -1185,15 +1271,22 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
   }
 }
 
+// Two stages of chunks of `bytes` per channel, at the most rows times channels
+// of a CTA's turn.
+constexpr size_t chunk_bytes(size_t bytes) {
+  return 2 * bytes * std::max(kThreads / 32 * 32 * kE, threads_of(kTwice) / 32 * 64 * kE);
+}
+
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
 cudaError_t launch_fwd(Plan pl, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
   auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE, DENSE>;
   using Ring = FwdRing<TS, TI, G, POST>;
   constexpr bool RING = ring_of(G, VEC);
-  const size_t smem = RING ? Ring::bytes(pl.threads) : 0;
+  constexpr size_t chunks = VEC || !DENSE ? 0 : chunk_bytes(sizeof(TS) + 2 * sizeof(TI));
+  const size_t smem = RING ? Ring::bytes(pl.threads) : chunks;
   int ctas = 0;
-  cudaError_t e = resident_ctas(kern, pl.threads, smem, RING ? Ring::bytes(threads_of(G)) : 0, cache, &ctas);
+  cudaError_t e = resident_ctas(kern, pl.threads, smem, RING ? Ring::bytes(threads_of(G)) : chunks, cache, &ctas);
   if (e != cudaSuccess) return e;
   // The CTAs are many and short (up to 8 turns), so that the rows that are in
   // flight lie close together: CTAs that walk the rows with a stride of the
@@ -1214,10 +1307,11 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   using Ring = BwdRing<TS, TI, G, POST, PRE, GROUPED>;
   constexpr bool RING = ring_of(G, VEC);
   constexpr int Q = parts_of(G);
-  const size_t smem = bwd_sums_bytes(pl.threads, Q) +
-                      (RING ? bwd_params_bytes(p.lanes, Q) + Ring::bytes(pl.threads) : 0);
+  constexpr size_t chunks = VEC || !DENSE ? 0 : chunk_bytes(2 * sizeof(TS) + 3 * sizeof(TI));
+  const size_t smem = bwd_sums_bytes(pl.threads, Q) + (G != kPlain ? bwd_params_bytes(p.lanes, Q) : 0) +
+                      (RING ? Ring::bytes(pl.threads) : chunks);
   constexpr size_t most =
-      bwd_sums_bytes(threads_of(G), Q) + (RING ? bwd_params_bytes(kThreads, Q) + Ring::bytes(threads_of(G)) : 0);
+      bwd_sums_bytes(threads_of(G), Q) + bwd_params_bytes(kThreads, Q) + (RING ? Ring::bytes(threads_of(G)) : chunks);
   static_assert(most <= 227 * 1024 - 4096, "shared memory");
   int ctas = 0;
   cudaError_t e = resident_ctas(kern, pl.threads, smem, most, cache, &ctas);
@@ -1271,6 +1365,9 @@ cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
   if (pl.vec && pl.g != kPlain)
     return pl.dense ? ring_fwd<TS, TI, POST, PRE, true>(pl, st) : ring_fwd<TS, TI, POST, PRE, false>(pl, st);
   if (pl.vec) return launch_fwd<TS, TI, kPlain, true, POST, PRE, false>(pl, st);
+  if (pl.chunk)
+    return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE, true>(pl, st)
+                      : launch_fwd<TS, TI, kTwice, false, POST, PRE, true>(pl, st);
   if (pl.g == kTwice) return launch_fwd<TS, TI, kTwice, false, POST, PRE, false>(pl, st);
   return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE, false>(pl, st)
                     : launch_fwd<TS, TI, kPlain, false, POST, PRE, false>(pl, st);
@@ -1292,6 +1389,11 @@ cudaError_t dispatch_bwd(const Plan& pl, float* ws, cudaStream_t st) {
     return pl.dense ? ring_bwd<TS, TI, POST, PRE, GROUPED, true>(pl, ws, st)
                     : ring_bwd<TS, TI, POST, PRE, GROUPED, false>(pl, ws, st);
   if (pl.vec) return launch_bwd<TS, TI, kPlain, true, POST, PRE, GROUPED, false>(pl, ws, st);
+  if constexpr (!GROUPED) {
+    if (pl.chunk)
+      return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, false, true>(pl, ws, st)
+                        : launch_bwd<TS, TI, kTwice, false, POST, PRE, false, true>(pl, ws, st);
+  }
   if (pl.g == kTwice) return launch_bwd<TS, TI, kTwice, false, POST, PRE, GROUPED, false>(pl, ws, st);
   return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED, false>(pl, ws, st)
                     : launch_bwd<TS, TI, kPlain, false, POST, PRE, GROUPED, false>(pl, ws, st);
