@@ -851,7 +851,19 @@ def main():
     ap.add_argument("--transition-only", type=int, default=0, metavar="N",
                     help="profiling only: time the fused SwiGLU transition kernel on the "
                          "[1, N, N, 128] pair representation and print its JSON")
+    ap.add_argument("--training-only", type=int, default=0, metavar="N",
+                    help="profiling only: time the block norm on the [1, N, N, 128] pair "
+                         "representation and the AdamW steps and print their JSON")
     args = ap.parse_args()
+    if args.training_only:
+        import torch
+        dev = torch.device("cuda", 0)
+        torch.cuda.set_device(dev)
+        peaks, _ = load_peaks()
+        print(json.dumps(measure_block_norm(args.training_only, dev, peaks)))
+        for bits in (32, 8):
+            print(json.dumps(measure_adamw(bits, dev, peaks)))
+        return 0
     if args.transition_only:
         import torch
         dev = torch.device("cuda", 0)
