@@ -169,7 +169,7 @@ __device__ __forceinline__ int element(int lane, int k) { return (k >> 2) * 128 
 // and with 8 bits their scales.  16 warps per SM in flight.
 template <bool BITS8>
 struct Ring {
-  static constexpr uint32_t G = 1024, M = 2048, V = BITS8 ? 2304 : 3072;
+  static constexpr uint32_t G = 1024, M = 2048, V = M + (BITS8 ? 256 : 1024);
   static constexpr uint32_t S = 2560;
   static_assert(!BITS8 || S + 8 <= 2576, "the scales are a stage's last");
   static constexpr uint32_t STAGE = BITS8 ? 2576 : 4096;
