@@ -516,21 +516,25 @@ __device__ __forceinline__ void sigmoid(Vec<Q>& v) {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename TS, typename TI, int G, bool POST>
+template <typename TS, typename TI, int G, bool POST, bool HELD>
 struct FwdRing {
-  static constexpr int UNITS = units<TS>() + (POST ? 2 * units<TI>() : 0);
-  // (UNITS is 3 to 6; three CTAs per SM)
+  static constexpr int TAKEN = POST ? (HELD ? 1 : 2) : 0;  // of the block's operands
+  static constexpr int UNITS = units<TS>() + TAKEN * units<TI>();
+  // (UNITS is 1 to 6; three CTAs per SM)
   static constexpr int STAGES = 12 / UNITS > 4 ? 4 : 12 / UNITS;
   __host__ __device__ static constexpr uint32_t stage(uint32_t threads) {
-    return ring_bytes<TS, G>(threads) + (POST ? 2 * ring_bytes<TI, G>(threads) : 0);
+    return ring_bytes<TS, G>(threads) + TAKEN * ring_bytes<TI, G>(threads);
   }
   static constexpr size_t bytes(int threads) { return (size_t)STAGES * stage(threads); }
 };
 
-template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
+// HELD: a gate row is shared by many consecutive rows; its sigmoid is taken
+// when it changes and kept (N = 768, a gate row per 768 rows: 104 us with the
+// gate read for every row).
+template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE, bool HELD>
 __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ? 4 : 3)
     k_block_norm_fwd(const __grid_constant__ Params p) {
-  using Ring = FwdRing<TS, TI, G, POST>;
+  using Ring = FwdRing<TS, TI, G, POST, HELD>;
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 sums[warps_of(G) ? 4 : 1][2 * kMaxWarps];
   wait_for_earlier_work();
@@ -563,7 +567,8 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
     if (POST) {
       slot += ring_bytes<TS, G>(blockDim.x);
       ring_put<TI, L, G>(slot, r.block(p, p.u), g, C, live);
-      if (gated) ring_put<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), gate_row(at, r), g, C, live);
+      if (!HELD && gated)
+        ring_put<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), gate_row(at, r), g, C, live);
     }
   };
 
@@ -611,10 +616,20 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
     b2 = param<L, G>(p.beta_pre, 0.f, g, C, p.wide_params);
   }
 
+  V held{};
+  uint32_t holds = ~0u;  // the gate row that `held` is of
   for (; turns > 0; --turns, row += step) {
     const bool live = row < last;
     const At<DENSE> r(p, live ? row : 0);
     V x, u, q;
+    if constexpr (HELD) {
+      const uint32_t now = div_by(live ? row : last - 1, p.by_share);
+      if (now != holds) {
+        holds = now;
+        held = load<TI, L, G>(row_ptr(p.gate, row_pos(p.gate_of, now), p.gate_of), g, C);
+        sigmoid(held);
+      }
+    }
     if constexpr (ring_of(G, VEC)) {
       const uint32_t ahead = stage == 0 ? Ring::STAGES - 1 : stage - 1;
       if (CROSS) __syncwarp();  // the warp has read that stage
@@ -627,7 +642,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
       if (POST) {
         slot += ring_bytes<TS, G>(blockDim.x);
         u = ring_get<TI, L, G>(slot, g);
-        if (gated) q = ring_get<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), g);
+        if (!HELD && gated) q = ring_get<TI, L, G>(slot + ring_bytes<TI, G>(blockDim.x), g);
       }
       stage = stage + 1 == Ring::STAGES ? 0 : stage + 1;
     } else if constexpr (CHUNK) {
@@ -658,8 +673,9 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
     }
     if (POST) {
       standardise<G, L>(u, g, p);
-      if (gated) {
-        sigmoid(q);
+      if (HELD || gated) {
+        if constexpr (HELD) q = held;
+        else sigmoid(q);
 #pragma unroll
         for (int k = 0; k < V::P; ++k) x.p[k] = fma2(fma2(u.p[k], g1.p[k], b1.p[k]), q.p[k], x.p[k]);
       } else {
@@ -1277,11 +1293,11 @@ constexpr size_t chunk_bytes(size_t bytes) {
   return 2 * bytes * std::max(kThreads / 32 * 32 * kE, threads_of(kTwice) / 32 * 64 * kE);
 }
 
-template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE>
+template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE, bool HELD = false>
 cudaError_t launch_fwd(Plan pl, cudaStream_t st) {
   static std::atomic<int> cache[64][17];
-  auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE, DENSE>;
-  using Ring = FwdRing<TS, TI, G, POST>;
+  auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE, DENSE, HELD>;
+  using Ring = FwdRing<TS, TI, G, POST, HELD>;
   constexpr bool RING = ring_of(G, VEC);
   constexpr size_t chunks = VEC || !DENSE ? 0 : chunk_bytes(sizeof(TS) + 2 * sizeof(TI));
   const size_t smem = RING ? Ring::bytes(pl.threads) : chunks;
@@ -1350,20 +1366,27 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   return e;
 }
 
-template <typename TS, typename TI, bool POST, bool PRE, bool DENSE>
+template <typename TS, typename TI, bool POST, bool PRE, bool DENSE, bool HELD>
 cudaError_t ring_fwd(const Plan& pl, cudaStream_t st) {
   switch (pl.g) {
-    case 8: return launch_fwd<TS, TI, 8, true, POST, PRE, DENSE>(pl, st);
-    case 16: return launch_fwd<TS, TI, 16, true, POST, PRE, DENSE>(pl, st);
-    case 32: return launch_fwd<TS, TI, 32, true, POST, PRE, DENSE>(pl, st);
-    case kTwice: return launch_fwd<TS, TI, kTwice, true, POST, PRE, DENSE>(pl, st);
-    default: return launch_fwd<TS, TI, kWarps, true, POST, PRE, DENSE>(pl, st);
+    case 8: return launch_fwd<TS, TI, 8, true, POST, PRE, DENSE, HELD>(pl, st);
+    case 16: return launch_fwd<TS, TI, 16, true, POST, PRE, DENSE, HELD>(pl, st);
+    case 32: return launch_fwd<TS, TI, 32, true, POST, PRE, DENSE, HELD>(pl, st);
+    case kTwice: return launch_fwd<TS, TI, kTwice, true, POST, PRE, DENSE, HELD>(pl, st);
+    default: return launch_fwd<TS, TI, kWarps, true, POST, PRE, DENSE, HELD>(pl, st);
   }
 }
 template <typename TS, typename TI, bool POST, bool PRE>
 cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
-  if (pl.vec && pl.g != kPlain)
-    return pl.dense ? ring_fwd<TS, TI, POST, PRE, true>(pl, st) : ring_fwd<TS, TI, POST, PRE, false>(pl, st);
+  if (pl.vec && pl.g != kPlain) {
+    if constexpr (POST) {  // a gate row for at least the rows of a CTA
+      if (pl.p.gate.p && pl.p.share >= 8u * (uint32_t)pl.slots)
+        return pl.dense ? ring_fwd<TS, TI, POST, PRE, true, true>(pl, st)
+                        : ring_fwd<TS, TI, POST, PRE, false, true>(pl, st);
+    }
+    return pl.dense ? ring_fwd<TS, TI, POST, PRE, true, false>(pl, st)
+                    : ring_fwd<TS, TI, POST, PRE, false, false>(pl, st);
+  }
   if (pl.vec) return launch_fwd<TS, TI, kPlain, true, POST, PRE, false>(pl, st);
   if (pl.chunk)
     return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE, true>(pl, st)
