@@ -61,14 +61,14 @@ constexpr int kThreads = 256;     // threads of a CTA where a row takes at most 
 constexpr int kMaxThreads = 512;  // ... 16 warps (C = 4096)
 
 // How a row is laid over threads: 8, 16 or 32 lanes of a warp; a whole warp
-// with two parts per lane; several warps (up to 8); or any number of warps
-// without a ring, whose rows and parameters are read as they are needed (more
-// than 8 warps, or rows that cannot be copied 16 bytes at a time).
-constexpr int kTwice = 64, kWarps = 0, kPlain = -1;
+// with two parts per lane; up to 8 warps, with one part or two; or any number
+// of warps without a ring, whose rows and parameters are read as they are
+// needed (rows that cannot be copied 16 bytes at a time).
+constexpr int kTwice = 64, kWarps = 0, kPlain = -1, kWarpsTwice = -2;
 constexpr bool warps_of(int G) { return G <= 0; }
 constexpr int width_of(int G) { return G <= 0 || G > 32 ? 32 : G; }  // lanes of a warp that share a row
-constexpr int parts_of(int G) { return G == kTwice ? 2 : 1; }
-constexpr bool ring_of(int G, bool vec) { return vec && G >= 0; }
+constexpr int parts_of(int G) { return G == kTwice || G == kWarpsTwice ? 2 : 1; }
+constexpr bool ring_of(int G, bool vec) { return vec && G != kPlain; }
 constexpr int threads_of(int G) { return G == kPlain ? kMaxThreads : G == kTwice ? kThreads / 2 : kThreads; }
 
 // ---------------------------------------------------------------------------
@@ -436,7 +436,7 @@ __device__ __forceinline__ Group make_group(const Params& p, float2 (*smem)[2 * 
   g.lane = (int)threadIdx.x - g.slot * g.lanes;
   g.l = g.lane % W;
   g.first = (int)threadIdx.x - g.l;
-  g.base = (g.lane - g.l) * kE;
+  g.base = (g.lane - g.l) * (kE * parts_of(G));
   g.c0 = g.base + (L == kSplit ? 4 : kE) * g.l;
   g.c1 = g.c0 + (L == kSplit ? 4 * W : 4);
   g.act = L == kSingle || g.c0 < p.C;
@@ -532,7 +532,7 @@ struct FwdRing {
 // when it changes and kept (N = 768, a gate row per 768 rows: 104 us with the
 // gate read for every row).
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE, bool HELD>
-__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ? 4 : 3)
+__global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ? 4 : G == kWarpsTwice ? 2 : 3)
     k_block_norm_fwd(const __grid_constant__ Params p) {
   using Ring = FwdRing<TS, TI, G, POST, HELD>;
   extern __shared__ __align__(16) char smem[];
@@ -768,7 +768,9 @@ constexpr size_t bwd_params_bytes(int lanes, int parts) { return (size_t)lanes *
 // 255 registers: 8 warps without spills (147,456 rows of 512 bf16 channels:
 // 185 us) against 12 with some (208 us); with fp32 rows the 12 are faster
 // (98,304 rows of 384 channels: 195 us against 214).
-constexpr int resident_bwd(int G, bool fp32) { return G == kPlain ? 1 : G == kTwice && fp32 ? 3 : 2; }
+constexpr int resident_bwd(int G, bool fp32) {
+  return G == kPlain || G == kWarpsTwice ? 1 : G == kTwice && fp32 ? 3 : 2;
+}
 
 // GROUPED: gate rows shared by consecutive rows, whose gradients are summed.
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool GROUPED,
@@ -1160,7 +1162,7 @@ inline Rows join_axes(const Space& sp, const RowOperand* const* ops, Operand* co
 
 struct Plan {
   Params p;
-  int g;        // lanes of a row's group: 8, 16, 32, or kTwice, kWarps, kPlain
+  int g;        // lanes of a row's group: 8, 16, 32, or kTwice, kWarps, kWarpsTwice, kPlain
   bool vec, dense, chunk;
   int threads, slots;
 };
@@ -1171,7 +1173,7 @@ struct Plan {
 // the residual stream.
 inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Operand* const* dst,
                       const int* esize, const bool* is_stream, const bool* is_gate, int count,
-                      int gate_at, Plan& pl) {
+                      int gate_at, bool backward, Plan& pl) {
   Params& p = pl.p;
   const Space sp = order_axes(c.n, ops, count, c.gate.p ? gate_at : -1);
   p.share = sp.share;
@@ -1222,10 +1224,17 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     p.lanes = 32;
     pl.threads = threads_of(kTwice);
   } else {
-    pl.g = pl.vec && need <= kThreads ? kWarps : kPlain;
-    const int warps = (need + 31) / 32;
+    // Two parts per lane need fewer instructions and barriers per channel, but
+    // more registers: from 1024 channels on the backward gains (49,152 bf16
+    // rows of 2048: 347 -> 307 us) and the bf16 forward (255 -> 239), below
+    // both lose (98,304 rows of 768: 270 -> 299, 171 -> 195); the forward with
+    // an fp32 stream is faster with one part (24,576 fp32 rows of 2048: 149,
+    // 171 with two).
+    const bool two = pl.vec && (need > kThreads || (need >= 128 && (backward || esize[0] == 2)));
+    pl.g = two ? kWarpsTwice : pl.vec ? kWarps : kPlain;
+    const int warps = two ? (need + 63) / 64 : (need + 31) / 32;
     p.lanes = warps * 32;
-    pl.threads = p.lanes * std::max(1, kThreads / 32 / warps);
+    pl.threads = p.lanes * std::max(1, (two ? 4 : kThreads / 32) / warps);
   }
   pl.slots = pl.threads / p.lanes;
   // rows one behind the other, a turn's rows a multiple of 16 bytes
@@ -1328,7 +1337,7 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
                       (RING ? Ring::bytes(pl.threads) : chunks);
   constexpr size_t most =
       bwd_sums_bytes(threads_of(G), Q) + bwd_params_bytes(kThreads, Q) + (RING ? Ring::bytes(threads_of(G)) : chunks);
-  static_assert(most <= 227 * 1024 - 4096, "shared memory");
+  static_assert(most <= 227 * 1024 - 2048, "shared memory");
   int ctas = 0;
   cudaError_t e = resident_ctas(kern, pl.threads, smem, most, cache, &ctas);
   if (e != cudaSuccess) return e;
@@ -1373,12 +1382,13 @@ cudaError_t ring_fwd(const Plan& pl, cudaStream_t st) {
     case 16: return launch_fwd<TS, TI, 16, true, POST, PRE, DENSE, HELD>(pl, st);
     case 32: return launch_fwd<TS, TI, 32, true, POST, PRE, DENSE, HELD>(pl, st);
     case kTwice: return launch_fwd<TS, TI, kTwice, true, POST, PRE, DENSE, HELD>(pl, st);
-    default: return launch_fwd<TS, TI, kWarps, true, POST, PRE, DENSE, HELD>(pl, st);
+    case kWarps: return launch_fwd<TS, TI, kWarps, true, POST, PRE, DENSE, HELD>(pl, st);
+    default: return launch_fwd<TS, TI, kWarpsTwice, true, POST, PRE, DENSE, HELD>(pl, st);
   }
 }
 template <typename TS, typename TI, bool POST, bool PRE>
 cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
-  if (pl.vec && pl.g != kPlain) {
+  if (pl.vec) {
     if constexpr (POST) {  // a gate row for at least the rows of a CTA
       if (pl.p.gate.p && pl.p.share >= 8u * (uint32_t)pl.slots)
         return pl.dense ? ring_fwd<TS, TI, POST, PRE, true, true>(pl, st)
@@ -1387,7 +1397,6 @@ cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
     return pl.dense ? ring_fwd<TS, TI, POST, PRE, true, false>(pl, st)
                     : ring_fwd<TS, TI, POST, PRE, false, false>(pl, st);
   }
-  if (pl.vec) return launch_fwd<TS, TI, kPlain, true, POST, PRE, false>(pl, st);
   if (pl.chunk)
     return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE, true>(pl, st)
                       : launch_fwd<TS, TI, kTwice, false, POST, PRE, true>(pl, st);
@@ -1403,15 +1412,15 @@ cudaError_t ring_bwd(const Plan& pl, float* ws, cudaStream_t st) {
     case 16: return launch_bwd<TS, TI, 16, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
     case 32: return launch_bwd<TS, TI, 32, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
     case kTwice: return launch_bwd<TS, TI, kTwice, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
-    default: return launch_bwd<TS, TI, kWarps, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
+    case kWarps: return launch_bwd<TS, TI, kWarps, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
+    default: return launch_bwd<TS, TI, kWarpsTwice, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
   }
 }
 template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED>
 cudaError_t dispatch_bwd(const Plan& pl, float* ws, cudaStream_t st) {
-  if (pl.vec && pl.g != kPlain)
+  if (pl.vec)
     return pl.dense ? ring_bwd<TS, TI, POST, PRE, GROUPED, true>(pl, ws, st)
                     : ring_bwd<TS, TI, POST, PRE, GROUPED, false>(pl, ws, st);
-  if (pl.vec) return launch_bwd<TS, TI, kPlain, true, POST, PRE, GROUPED, false>(pl, ws, st);
   if constexpr (!GROUPED) {
     if (pl.chunk)
       return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, false, true>(pl, ws, st)
@@ -1432,7 +1441,7 @@ cudaError_t run_fwd(const BlockNormCall& c, cudaStream_t st) {
   const int es[] = {S, I, I, S, I};
   const bool stream[] = {true, false, false, true, false};
   const bool gates[] = {false, false, true, false, false};
-  make_plan(c, ops, dst, es, stream, gates, 5, 2, pl);
+  make_plan(c, ops, dst, es, stream, gates, 5, 2, false, pl);
   if (c.u.p && c.y.p) return dispatch_fwd<TS, TI, true, true>(pl, st);
   if (c.u.p) return dispatch_fwd<TS, TI, true, false>(pl, st);
   return dispatch_fwd<TS, TI, false, true>(pl, st);
@@ -1448,7 +1457,7 @@ cudaError_t run_bwd(const BlockNormCall& c, cudaStream_t st) {
   const int es[] = {S, S, I, I, I, S, I, I};
   const bool stream[] = {true, true, false, false, false, true, false, false};
   const bool gates[] = {false, false, false, true, false, false, false, true};
-  make_plan(c, ops, dst, es, stream, gates, 8, 3, pl);
+  make_plan(c, ops, dst, es, stream, gates, 8, 3, true, pl);
   p.dscale = c.dscale;
   p.dgamma_post = c.dgamma_post;
   p.dbeta_post = c.dbeta_post;

@@ -172,8 +172,8 @@ def run_bwd(k, rms, **kw):
                                   kind=evoattn.NORM_RMS if rms else evoattn.NORM_LAYER, **kw)
 
 
-WIDTHS = [1, 2, 7, 8, 31, 32, 33, 64, 72, 99, 128, 200, 256, 257, 264, 384, 500, 768, 1000, 2048,
-          2056, 4095, 4096]
+WIDTHS = [1, 2, 7, 8, 31, 32, 33, 64, 72, 99, 128, 200, 256, 257, 264, 384, 500, 768, 1000, 1024, 1032, 1600,
+          2048, 2056, 3000, 4000, 4095, 4096]
 
 
 @pytest.mark.parametrize("C", WIDTHS)
@@ -200,7 +200,7 @@ def test_shapes_and_shared_gates(shape, gate):
     check_bwd(k, run_bwd(k, False), False)
 
 
-@pytest.mark.parametrize("C", [8, 33, 99, 136, 256, 300, 384, 511, 520, 777, 1096, 2056])
+@pytest.mark.parametrize("C", [8, 33, 99, 136, 256, 300, 384, 511, 520, 777, 1096, 2056, 4088])
 @pytest.mark.parametrize("types,gate", [("bf16", "row"), ("mixed", "batch"), ("f32", "middle"),
                                         ("f32", "row"), ("mixed", "none")])
 def test_widths_with_shared_gates(C, types, gate):
