@@ -219,22 +219,24 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   extern __shared__ __align__(16) char smem[];
   wait_for_earlier_work();
   let_next_start();
-  // every CTA reads the step before the last one to do so counts it up
   const float t = (float)(P.state->step + 1);
   const float clip = P.clip ? P.state->clip : 1.f;
   const bool skip = P.clip && P.state->skip;
   const float lr = P.lr_device ? *P.lr_device : P.lr;
-  if (P.last) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
-      if (atomicAdd(&P.state->ticket[0], 1u) == gridDim.x - 1) {
-        P.state->ticket[0] = 0;
-        if (!skip) P.state->step += 1;
-      }
+  // Every CTA has read the step before the last one to end counts it up.
+  __syncthreads();
+  auto count_up = [&]() {
+    if (!P.last || threadIdx.x != 0) return;
+    __threadfence();
+    if (atomicAdd(&P.state->ticket[0], 1u) == gridDim.x - 1) {
+      P.state->ticket[0] = 0;
+      if (!skip) P.state->step += 1;
     }
+  };
+  if (skip) {
+    count_up();
+    return;
   }
-  if (skip) return;
   // 1 - b^t without cancellation
   const float c1 = -expm1f(t * P.log_b1), c2 = -expm1f(t * P.log_b2);
   const float rate = lr / c1, root = rsqrtf(c2);
@@ -246,7 +248,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   at.b = blockIdx.x * WARPS + warp;
   // turns that every warp of the launch takes
   uint32_t common = WARPS == 16 ? end / hop : 0;
-  if (at.b >= end) return;
+  if (at.b >= end) {
+    count_up();
+    return;
+  }
   at.open(P, lane);
   char* const ring = smem + warp * (R::STAGE * R::STAGES);
   const uint32_t ring_s = smem_u32(ring);
@@ -446,6 +451,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     }
   }
   copies_wait<0>();
+  count_up();
 }
 
 // Sum over a CTA, valid in thread 0.  (fp64 arithmetic is slow on this part,

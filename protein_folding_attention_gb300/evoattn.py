@@ -8,6 +8,7 @@ missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import bisect
 import contextlib
 import ctypes
 import os
@@ -342,7 +343,8 @@ def block_norm(x, u=None, gate=None, scale=None, gamma_post=None, beta_post=None
     norm before a block alone (x1 is x), with pre=False the norm after a block
     alone (y is None).  y has u's type; y_dtype names it where there is no u
     (default: x's).  Outputs take x's layout; x1=x updates the stream in place.
-    Returns (x1, y)."""
+    Everything is enqueued on, and allocated for, `stream` (default: the
+    current one).  Returns (x1, y)."""
     shape = x.shape
     if len(shape) != 4:
         raise ValueError("x must be [B, I, J, C]")
@@ -350,8 +352,8 @@ def block_norm(x, u=None, gate=None, scale=None, gamma_post=None, beta_post=None
     io = u.dtype if u is not None else (y_dtype or sd)
     if y_dtype is not None and y_dtype is not io:
         raise ValueError("y has the type of u")
-    if y is not None and not pre:
-        raise ValueError("y without pre")
+    if (y is not None and not pre) or (x1 is not None and u is None):
+        raise ValueError("y without pre, or x1 without u")
     if gate is not None:
         gate = _expanded(gate, shape)
     words = []
@@ -403,12 +405,15 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
         raise ValueError("gradients must be [B, I, J, C]")
     if dy is None:
         x1 = None
+        if dx is not None:
+            raise ValueError("dx without dy: the gradient of x is dx1")
     elif x1 is None:
         raise ValueError("dy needs x1")
     dev, sd, C = _on_device(lead), lead.dtype, shape[3]
     io = u.dtype if u is not None else dy.dtype
     if gate is not None and 0 in gate.stride():
-        gate = gate.contiguous()  # an expanded view: each of its rows has its own gradient
+        with _allocate_on(stream):  # an expanded view: each of its rows has its own gradient
+            gate = gate.contiguous()
     full = gate if gate is None else _expanded(gate, shape)
     words, out = [], {}
     _add_rows(words, ((dx1, sd, "dx1"), (dy, io, "dy"), (x1, sd, "x1"), (u, io, "u"),
@@ -554,6 +559,7 @@ class AdamW:
         written = sorted(w for w in written if w[1])
         if any(a + k > b for (a, k), (b, _) in zip(written, written[1:])):
             raise ValueError("parameters, copies and states overlap (is a tensor listed twice?)")
+        self._starts, self._ends = [a for a, _ in written], [a + k for a, k in written]
         self._bind(self.grads)
         # evoattn_optim_state: step, norm, clip, skip, tickets
         self._state = torch.zeros(8, device=dev, dtype=torch.int32)
@@ -570,7 +576,11 @@ class AdamW:
             if g.dtype not in (torch.bfloat16, torch.float32):
                 raise ValueError(f"gradient {i}: bf16 or fp32, got {g.dtype}")
             _check_flat(g, row.n, g.dtype, self.device, f"gradient {i}")
-            row.grad, row.grad_dtype = g.data_ptr(), _dtype_code(g)
+            at = g.data_ptr()
+            k = bisect.bisect_left(self._starts, at + g.numel() * g.element_size()) - 1
+            if row.n and k >= 0 and self._ends[k] > at:
+                raise ValueError(f"gradient {i} overlaps what a step writes")
+            row.grad, row.grad_dtype = at, _dtype_code(g)
         self.grads = grads
 
     def step(self, max_norm=None, grads=None, stream=None):
@@ -578,6 +588,7 @@ class AdamW:
         returned (the tensor `norm`, overwritten by the next such step); a step
         whose norm is infinite or NaN then changes nothing.  grads: gradients
         to use from now on instead of those bound before."""
+        _on_device(self._state)
         if grads is not None:
             self._bind(list(grads))
         lib, n = load(), len(self.params)

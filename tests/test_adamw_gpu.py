@@ -319,7 +319,8 @@ def test_python_refusals():
                 dict(grads=[gs[1], gs[0]]), dict(copies=[cs[0].float(), None]),
                 dict(exp_avg=torch.zeros(511, device=DEV)), dict(exp_avg_scale=torch.zeros(2, device=DEV)),
                 dict(params=[p.expand(2, -1) for p in ps], grads=[g.expand(2, -1) for g in gs]),
-                dict(params=[torch.zeros(200, device=DEV)[::2], ps[1]])):
+                dict(params=[torch.zeros(200, device=DEV)[::2], ps[1]]),
+                dict(grads=[ps[0], gs[1]]), dict(grads=[gs[0], cs[1]], copies=cs)):
         with pytest.raises(ValueError):
             ok(**bad)
     opt = ok()

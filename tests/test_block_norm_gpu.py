@@ -586,7 +586,8 @@ def test_python_refusals():
                 dict(gate=g["gate"][..., :8]), dict(gate=g["gate"][:, :, :2]), dict(gate=g["gate"].cpu()),
                 dict(gate=g["gate"].float()), dict(scale=g["scale"][:8]), dict(scale=g["scale"].bfloat16()),
                 dict(gamma_pre=torch.ones(32, device=DEV)[::2]), dict(y_dtype=torch.float32),
-                dict(pre=False, y=torch.empty_like(g["x"])), dict(x=g["x"][0])):
+                dict(pre=False, y=torch.empty_like(g["x"])), dict(x=g["x"][0]),
+                dict(u=None, gate=None, x1=torch.empty_like(g["x"]))):
         with pytest.raises(ValueError):
             call(**bad)
     with pytest.raises(TypeError):
@@ -599,7 +600,8 @@ def test_python_refusals():
         call(x1=g["x"][:, :1].expand(1, 2, 3, 16))                    # overlapping output rows
     b = to_gpu(draw((1, 2, 3, 16), "bf16", seed=29, backward=True))
     for bad in (dict(dx1=None, dy=None), dict(x1=None), dict(u=None, dy=None), dict(x1=b["x1"].float()),
-                dict(beta_pre=b["beta_pre"][:3]), dict(dx1=b["dx1"][0])):
+                dict(beta_pre=b["beta_pre"][:3]), dict(dx1=b["dx1"][0]),
+                dict(dy=None, gamma_pre=None, beta_pre=None, dx=torch.empty_like(b["dx1"]))):
         with pytest.raises(ValueError):
             evoattn.block_norm_bwd(**{**{n: b[n] for n in BWD_ARGS}, **bad})
     with pytest.raises(evoattn.EvoAttnError):
