@@ -62,8 +62,7 @@ constexpr int kMaxThreads = 512;  // ... 16 warps (C = 4096)
 
 // How a row is laid over threads: 8, 16 or 32 lanes of a warp; a whole warp
 // with two parts per lane; up to 8 warps, with one part or two; or any number
-// of warps without a ring, whose rows and parameters are read as they are
-// needed (rows that cannot be copied 16 bytes at a time).
+// of warps, one part each (rows that cannot be copied 16 bytes at a time).
 constexpr int kTwice = 64, kWarps = 0, kPlain = -1, kWarpsTwice = -2;
 constexpr bool warps_of(int G) { return G <= 0; }
 constexpr int width_of(int G) { return G <= 0 || G > 32 ? 32 : G; }  // lanes of a warp that share a row
@@ -385,11 +384,18 @@ __device__ __forceinline__ Vec<parts_of(G)> ring_get(const char* stage, const Gr
 }
 
 // Rows that cannot be copied one by one in 16-byte units (C no multiple of 8)
-// but lie one behind the other: the rows of a CTA's turn are then copied as
-// one piece, which begins and ends on 16 bytes (but for the last one's end).
-__device__ __forceinline__ void chunk_put(uint32_t stage, const char* src, uint32_t bytes) {
+// but lie one behind the other from a 16-byte aligned address on: the rows of
+// a CTA's turn are then copied as one piece, from the 16 bytes that its first
+// byte lies in to its last byte.  (The up to 14 bytes before the first are the
+// row's before it.)
+__host__ __device__ constexpr uint32_t chunk_size(uint32_t elements, uint32_t esize) {
+  return (elements * esize + 15) / 16 * 16 + 16;
+}
+__device__ __forceinline__ void chunk_put(uint32_t to, const char* src, uint32_t bytes, uint32_t shift) {
+  src -= shift;
+  bytes += shift;
   for (uint32_t at = threadIdx.x * 16; at < bytes; at += blockDim.x * 16)
-    copy16(stage + at, src + at, min(16u, bytes - at));
+    copy16(to + at, src + at, min(16u, bytes - at));
 }
 
 // ---------------------------------------------------------------------------
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
   const bool shared_gate = p.share > 1;
 
   constexpr bool CHUNK = !VEC && DENSE;
-  const uint32_t chunk_s = g.slots * C * sizeof(TS), chunk_i = g.slots * C * sizeof(TI);
+  const uint32_t chunk_s = chunk_size(g.slots * C, sizeof(TS)), chunk_i = chunk_size(g.slots * C, sizeof(TI));
   const uint32_t stage_bytes = CHUNK ? chunk_s + 2 * chunk_i : Ring::stage(blockDim.x);
   const uint32_t ring_s = smem_u32(smem);
   auto gate_row = [&](uint32_t row, const At<DENSE>& r) {
@@ -577,10 +583,11 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
     const uint32_t n = min(last - first, (uint32_t)g.slots) * C;
     const At<DENSE> r(p, first);
     const uint32_t to = ring_s + stage * stage_bytes;
-    chunk_put(to, r.stream(p, p.x), n * sizeof(TS));
+    const uint32_t ss = (first * p.stride_s) & 15, si = (first * p.stride_i) & 15;
+    chunk_put(to, r.stream(p, p.x), n * sizeof(TS), ss);
     if (POST) {
-      chunk_put(to + chunk_s, r.block(p, p.u), n * sizeof(TI));
-      if (gated && !shared_gate) chunk_put(to + chunk_s + chunk_i, r.block(p, p.gate), n * sizeof(TI));
+      chunk_put(to + chunk_s, r.block(p, p.u), n * sizeof(TI), si);
+      if (gated && !shared_gate) chunk_put(to + chunk_s + chunk_i, r.block(p, p.gate), n * sizeof(TI), si);
     }
   };
 
@@ -654,9 +661,10 @@ __global__ void __launch_bounds__(threads_of(G), G == kPlain ? 1 : G == kTwice ?
       stage ^= 1;
       x = u = q = V{};
       if (live) {
-        x = load<TS, L, G>(from + g.slot * C * sizeof(TS), g, C);
+        const uint32_t first = row - g.slot;
+        x = load<TS, L, G>(from + ((first * p.stride_s) & 15) + g.slot * C * sizeof(TS), g, C);
         if (POST) {
-          from += chunk_s + g.slot * C * sizeof(TI);
+          from += chunk_s + ((first * p.stride_i) & 15) + g.slot * C * sizeof(TI);
           u = load<TI, L, G>(from, g, C);
           if (gated) q = load<TI, L, G>(shared_gate ? gate_row(row, r) : from + chunk_i, g, C);
         }
@@ -759,8 +767,8 @@ struct BwdRing {
   static constexpr size_t bytes(int threads) { return (size_t)STAGES * stage(threads); }
 };
 
-// Shared memory of the backward: a row of sums per group, and with a ring three
-// parameter vectors by thread of a group.
+// Shared memory of the backward: a row of sums per group, three parameter
+// vectors by thread of a group, and the ring or the chunks.
 constexpr size_t bwd_sums_bytes(int threads, int parts) { return (size_t)threads * kE * 4 * parts; }
 constexpr size_t bwd_params_bytes(int lanes, int parts) { return (size_t)lanes * kE * 4 * 3 * parts; }
 
@@ -789,7 +797,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
   const bool gated = POST && (GROUPED || p.gate.p != nullptr);
   const bool with_dx1 = p.dx1.p != nullptr;
 
-  constexpr bool RING = ring_of(G, VEC), CHUNK = !VEC && DENSE, KEEP = G != kPlain;
+  constexpr bool RING = ring_of(G, VEC), CHUNK = !VEC && DENSE;
   constexpr bool STEP = RING && !GROUPED && G > 0 && G <= 32 && sizeof(TI) == 2;
   float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
   // parameters: [vector][run][lane] float4, read back without bank conflicts
@@ -804,28 +812,22 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     for (int j = 0; j < V::P; ++j) v.p[j] = mul2(v.p[j], s.p[j]);
     return v;
   };
-  if (KEEP) {
-    if (g.slot == 0) {
+  if (g.slot == 0) {
 #pragma unroll
-      for (int k = POST ? 0 : 2; k < (PRE ? 3 : 2); ++k) {
-        const V v = read(k);
+    for (int k = POST ? 0 : 2; k < (PRE ? 3 : 2); ++k) {
+      const V v = read(k);
 #pragma unroll
-        for (int h = 0; h < V::P / 2; ++h)
-          prm[(k * (V::P / 2) + h) * g.lanes + g.lane] =
-              make_float4(v.p[2 * h].x, v.p[2 * h].y, v.p[2 * h + 1].x, v.p[2 * h + 1].y);
-      }
+      for (int h = 0; h < V::P / 2; ++h)
+        prm[(k * (V::P / 2) + h) * g.lanes + g.lane] =
+            make_float4(v.p[2 * h].x, v.p[2 * h].y, v.p[2 * h + 1].x, v.p[2 * h + 1].y);
     }
-    __syncthreads();
   }
+  __syncthreads();
   auto get = [&](int k) {
-    if constexpr (KEEP) {
-      V v;
+    V v;
 #pragma unroll
-      for (int h = 0; h < V::P / 2; ++h) put_run(v, h, prm[(k * (V::P / 2) + h) * g.lanes + g.lane]);
-      return v;
-    } else {
-      return read(k);
-    }
+    for (int h = 0; h < V::P / 2; ++h) put_run(v, h, prm[(k * (V::P / 2) + h) * g.lanes + g.lane]);
+    return v;
   };
 
   const V zero{};
@@ -834,7 +836,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
 #pragma unroll
   for (int k = 0; k < V::P; ++k) q.p[k] = both(1.f);
 
-  const uint32_t chunk_s = g.slots * C * sizeof(TS), chunk_i = g.slots * C * sizeof(TI);
+  const uint32_t chunk_s = chunk_size(g.slots * C, sizeof(TS)), chunk_i = chunk_size(g.slots * C, sizeof(TI));
   const uint32_t stage_bytes = CHUNK ? 2 * chunk_s + 3 * chunk_i : Ring::stage(blockDim.x);
   const uint32_t ring_s = smem_u32(ring);
   // ring order: dx1, (x1, dy), (u, gate)
@@ -861,14 +863,15 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     const uint32_t n = min(p.rows - first, (uint32_t)g.slots) * C;
     const At<DENSE> r(p, first);
     const uint32_t to = ring_s + stage * stage_bytes;
-    if (with_dx1) chunk_put(to, r.stream(p, p.dx1), n * sizeof(TS));
+    const uint32_t ss = (first * p.stride_s) & 15, si = (first * p.stride_i) & 15;
+    if (with_dx1) chunk_put(to, r.stream(p, p.dx1), n * sizeof(TS), ss);
     if (PRE) {
-      chunk_put(to + chunk_s, r.stream(p, p.x), n * sizeof(TS));
-      chunk_put(to + 2 * chunk_s, r.block(p, p.dy), n * sizeof(TI));
+      chunk_put(to + chunk_s, r.stream(p, p.x), n * sizeof(TS), ss);
+      chunk_put(to + 2 * chunk_s, r.block(p, p.dy), n * sizeof(TI), si);
     }
     if (POST) {
-      chunk_put(to + 2 * chunk_s + chunk_i, r.block(p, p.u), n * sizeof(TI));
-      if (gated) chunk_put(to + 2 * chunk_s + 2 * chunk_i, r.block(p, p.gate), n * sizeof(TI));
+      chunk_put(to + 2 * chunk_s + chunk_i, r.block(p, p.u), n * sizeof(TI), si);
+      if (gated) chunk_put(to + 2 * chunk_s + 2 * chunk_i, r.block(p, p.gate), n * sizeof(TI), si);
     }
   };
 
@@ -937,13 +940,15 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
       __syncthreads();  // the turn's rows are here, and the other stage has been read
       fetch_chunk(stage ^ 1, row - g.slot + at.hop);
       copies_close();
-      const char* from = ring + stage * stage_bytes + g.slot * C * sizeof(TS);
+      const uint32_t first = row - g.slot;
+      const char* from = ring + stage * stage_bytes;
       stage ^= 1;
       h = dy = u = gt = zero;
       if (live) {
-        if (with_dx1) D = load<TS, L, G>(from, g, C);
-        if (PRE) h = load<TS, L, G>(from + chunk_s, g, C);
-        from += 2 * chunk_s + g.slot * C * (sizeof(TI) - sizeof(TS));
+        const char* at_s = from + ((first * p.stride_s) & 15) + g.slot * C * sizeof(TS);
+        if (with_dx1) D = load<TS, L, G>(at_s, g, C);
+        if (PRE) h = load<TS, L, G>(at_s + chunk_s, g, C);
+        from += 2 * chunk_s + ((first * p.stride_i) & 15) + g.slot * C * sizeof(TI);
         if (PRE) dy = load<TI, L, G>(from, g, C);
         if (POST) {
           u = load<TI, L, G>(from + chunk_i, g, C);
@@ -1237,13 +1242,11 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     pl.threads = p.lanes * std::max(1, (two ? 4 : kThreads / 32) / warps);
   }
   pl.slots = pl.threads / p.lanes;
-  // rows one behind the other, a turn's rows a multiple of 16 bytes
-  pl.chunk = !pl.vec && pl.dense && pl.g != kPlain;
-  for (int i = 0; i < count && pl.chunk; ++i) {
-    if (!rows[i] || !dst[i]->p) continue;
-    const int64_t row = (int64_t)c.C * esize[i];
-    pl.chunk = dst[i]->s2 == row && row * pl.slots % 16 == 0 && reinterpret_cast<uintptr_t>(dst[i]->p) % 16 == 0;
-  }
+  // rows one behind the other
+  pl.chunk = !pl.vec && pl.dense;
+  for (int i = 0; i < count && pl.chunk; ++i)
+    if (rows[i] && dst[i]->p)
+      pl.chunk = dst[i]->s2 == (int64_t)c.C * esize[i] && reinterpret_cast<uintptr_t>(dst[i]->p) % 16 == 0;
 }
 
 // Sums of the CTAs' partial sums: one block per 32 columns of the post-norm's
@@ -1296,10 +1299,12 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
   }
 }
 
-// Two stages of chunks of `bytes` per channel, at the most rows times channels
-// of a CTA's turn.
-constexpr size_t chunk_bytes(size_t bytes) {
-  return 2 * bytes * std::max(kThreads / 32 * 32 * kE, threads_of(kTwice) / 32 * 64 * kE);
+// Two stages of chunks: `of_s` operands of the stream and `of_i` of the block,
+// at the most channels that a CTA's turn can have.
+template <typename TS, typename TI>
+constexpr size_t chunk_bytes(int threads, int parts, int of_s, int of_i) {
+  return 2 * ((size_t)of_s * chunk_size(threads * kE * parts, sizeof(TS)) +
+              (size_t)of_i * chunk_size(threads * kE * parts, sizeof(TI)));
 }
 
 template <typename TS, typename TI, int G, bool VEC, bool POST, bool PRE, bool DENSE, bool HELD = false>
@@ -1308,10 +1313,13 @@ cudaError_t launch_fwd(Plan pl, cudaStream_t st) {
   auto kern = k_block_norm_fwd<TS, TI, G, VEC, POST, PRE, DENSE, HELD>;
   using Ring = FwdRing<TS, TI, G, POST, HELD>;
   constexpr bool RING = ring_of(G, VEC);
-  constexpr size_t chunks = VEC || !DENSE ? 0 : chunk_bytes(sizeof(TS) + 2 * sizeof(TI));
-  const size_t smem = RING ? Ring::bytes(pl.threads) : chunks;
+  constexpr bool CHUNK = !VEC && DENSE;
+  auto ring = [](int threads) {
+    return RING ? Ring::bytes(threads) : CHUNK ? chunk_bytes<TS, TI>(threads, parts_of(G), 1, 2) : 0;
+  };
+  const size_t smem = ring(pl.threads);
   int ctas = 0;
-  cudaError_t e = resident_ctas(kern, pl.threads, smem, RING ? Ring::bytes(threads_of(G)) : chunks, cache, &ctas);
+  cudaError_t e = resident_ctas(kern, pl.threads, smem, ring(threads_of(G)), cache, &ctas);
   if (e != cudaSuccess) return e;
   // The CTAs are many and short (up to 8 turns), so that the rows that are in
   // flight lie close together: CTAs that walk the rows with a stride of the
@@ -1332,11 +1340,12 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   using Ring = BwdRing<TS, TI, G, POST, PRE, GROUPED>;
   constexpr bool RING = ring_of(G, VEC);
   constexpr int Q = parts_of(G);
-  constexpr size_t chunks = VEC || !DENSE ? 0 : chunk_bytes(2 * sizeof(TS) + 3 * sizeof(TI));
-  const size_t smem = bwd_sums_bytes(pl.threads, Q) + (G != kPlain ? bwd_params_bytes(p.lanes, Q) : 0) +
-                      (RING ? Ring::bytes(pl.threads) : chunks);
-  constexpr size_t most =
-      bwd_sums_bytes(threads_of(G), Q) + bwd_params_bytes(kThreads, Q) + (RING ? Ring::bytes(threads_of(G)) : chunks);
+  constexpr bool CHUNK = !VEC && DENSE;
+  const size_t smem = bwd_sums_bytes(pl.threads, Q) + bwd_params_bytes(p.lanes, Q) +
+                      (RING ? Ring::bytes(pl.threads) : CHUNK ? chunk_bytes<TS, TI>(pl.threads, Q, 2, 3) : 0);
+  constexpr int T = threads_of(G);
+  constexpr size_t most = bwd_sums_bytes(T, Q) + bwd_params_bytes(std::max(T, 32), Q) +
+                          (RING ? Ring::bytes(T) : CHUNK ? chunk_bytes<TS, TI>(T, Q, 2, 3) : 0);
   static_assert(most <= 227 * 1024 - 2048, "shared memory");
   int ctas = 0;
   cudaError_t e = resident_ctas(kern, pl.threads, smem, most, cache, &ctas);
@@ -1386,6 +1395,14 @@ cudaError_t ring_fwd(const Plan& pl, cudaStream_t st) {
     default: return launch_fwd<TS, TI, kWarpsTwice, true, POST, PRE, DENSE, HELD>(pl, st);
   }
 }
+template <typename TS, typename TI, bool POST, bool PRE, bool CHUNK>
+cudaError_t single_fwd(const Plan& pl, cudaStream_t st) {
+  switch (pl.g) {
+    case 32: return launch_fwd<TS, TI, 32, false, POST, PRE, CHUNK>(pl, st);
+    case kTwice: return launch_fwd<TS, TI, kTwice, false, POST, PRE, CHUNK>(pl, st);
+    default: return launch_fwd<TS, TI, kPlain, false, POST, PRE, CHUNK>(pl, st);
+  }
+}
 template <typename TS, typename TI, bool POST, bool PRE>
 cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
   if (pl.vec) {
@@ -1397,12 +1414,7 @@ cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
     return pl.dense ? ring_fwd<TS, TI, POST, PRE, true, false>(pl, st)
                     : ring_fwd<TS, TI, POST, PRE, false, false>(pl, st);
   }
-  if (pl.chunk)
-    return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE, true>(pl, st)
-                      : launch_fwd<TS, TI, kTwice, false, POST, PRE, true>(pl, st);
-  if (pl.g == kTwice) return launch_fwd<TS, TI, kTwice, false, POST, PRE, false>(pl, st);
-  return pl.g == 32 ? launch_fwd<TS, TI, 32, false, POST, PRE, false>(pl, st)
-                    : launch_fwd<TS, TI, kPlain, false, POST, PRE, false>(pl, st);
+  return pl.chunk ? single_fwd<TS, TI, POST, PRE, true>(pl, st) : single_fwd<TS, TI, POST, PRE, false>(pl, st);
 }
 
 template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED, bool DENSE>
@@ -1416,19 +1428,23 @@ cudaError_t ring_bwd(const Plan& pl, float* ws, cudaStream_t st) {
     default: return launch_bwd<TS, TI, kWarpsTwice, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
   }
 }
+template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED, bool CHUNK>
+cudaError_t single_bwd(const Plan& pl, float* ws, cudaStream_t st) {
+  switch (pl.g) {
+    case 32: return launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED, CHUNK>(pl, ws, st);
+    case kTwice: return launch_bwd<TS, TI, kTwice, false, POST, PRE, GROUPED, CHUNK>(pl, ws, st);
+    default: return launch_bwd<TS, TI, kPlain, false, POST, PRE, GROUPED, CHUNK>(pl, ws, st);
+  }
+}
 template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED>
 cudaError_t dispatch_bwd(const Plan& pl, float* ws, cudaStream_t st) {
   if (pl.vec)
     return pl.dense ? ring_bwd<TS, TI, POST, PRE, GROUPED, true>(pl, ws, st)
                     : ring_bwd<TS, TI, POST, PRE, GROUPED, false>(pl, ws, st);
   if constexpr (!GROUPED) {
-    if (pl.chunk)
-      return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, false, true>(pl, ws, st)
-                        : launch_bwd<TS, TI, kTwice, false, POST, PRE, false, true>(pl, ws, st);
+    if (pl.chunk) return single_bwd<TS, TI, POST, PRE, false, true>(pl, ws, st);
   }
-  if (pl.g == kTwice) return launch_bwd<TS, TI, kTwice, false, POST, PRE, GROUPED, false>(pl, ws, st);
-  return pl.g == 32 ? launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED, false>(pl, ws, st)
-                    : launch_bwd<TS, TI, kPlain, false, POST, PRE, GROUPED, false>(pl, ws, st);
+  return single_bwd<TS, TI, POST, PRE, GROUPED, false>(pl, ws, st);
 }
 
 template <typename TS, typename TI>

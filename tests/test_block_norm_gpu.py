@@ -172,7 +172,7 @@ def run_bwd(k, rms, **kw):
                                   kind=evoattn.NORM_RMS if rms else evoattn.NORM_LAYER, **kw)
 
 
-WIDTHS = [1, 2, 7, 8, 31, 32, 33, 64, 72, 99, 128, 200, 256, 257, 264, 384, 500, 768, 1000, 1024, 1032, 1600,
+WIDTHS = [1, 2, 7, 8, 31, 32, 33, 64, 72, 99, 128, 200, 256, 257, 264, 384, 500, 509, 768, 1000, 1001, 1024, 1032, 1600,
           2048, 2056, 3000, 4000, 4095, 4096]
 
 
