@@ -78,6 +78,7 @@ struct StepParams {
   evoattn_optim_state* state;
   const float* lr_device;
   float lr, b1, b1c, b2, b2c, log_b1, log_b2, eps;
+  float one;       // 1, see sum2()
   int clip, last;  // last: this launch counts the step up
   uint32_t blocks;
 };
@@ -138,19 +139,52 @@ __device__ __forceinline__ float sqrt_approx(float a) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
+__device__ __forceinline__ float rsqrt_approx(float a) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
 __device__ __forceinline__ float rcp_approx(float a) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
-// 448 / top (0 for a block that is held as zeros), the approximate quotient
-// corrected by its own remainder.
+// 448 (1 / top), 0 for a block that is held as zeros.
 constexpr float kLeast = 0x1p-100f;
 __device__ __forceinline__ float inverse448(float top) {
-  const float y = rcp_approx(top), q = 448.f * y;
-  return top >= kLeast ? fmaf(fmaf(-q, top, 448.f), y, q) : 0.f;
+  return top >= kLeast ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// a + b, where a or b may be a product that has to be rounded before: the
+// assembler joins a packed multiplication and an addition to one fused
+// operation, in spite of their .rn, but not with a factor that it does not
+// know.  `one` is 1 and comes in as a parameter of the kernel.
+__device__ __forceinline__ float2 sum2(float2 a, float2 b, float one) { return fma2(a, both(one), b); }
+
+// Square roots, rounded to nearest, of a lane's eight values.  Inside the range
+// where no step overflows or loses bits: one Newton step from the approximate
+// reciprocal root y, with the residual v - (v y)^2 exact in fp32 (Markstein,
+// 1990): all but about one in a million are rounded correctly.  (The function
+// for one value tests that range for each of the eight: 289 us a step of 107M
+// parameters, 277 so.)
+__device__ __forceinline__ void roots(const float2* v, float2* r) {
+  const float low = fminf(fminf(fminf(v[0].x, v[0].y), fminf(v[1].x, v[1].y)),
+                          fminf(fminf(v[2].x, v[2].y), fminf(v[3].x, v[3].y)));
+  const float high = fmax3(fmax3(v[0].x, v[0].y, v[1].x), fmax3(v[1].y, v[2].x, v[2].y), fmaxf(v[3].x, v[3].y));
+  if (low >= 0x1p-96f && high < 0x1p96f) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 y = make_float2(rsqrt_approx(v[k].x), rsqrt_approx(v[k].y));
+      const float2 a = mul2(v[k], y);
+      const float2 rest = fma2(make_float2(-a.x, -a.y), a, v[k]);
+      r[k] = fma2(rest, mul2(y, both(0.5f)), a);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = make_float2(__fsqrt_rn(v[k].x), __fsqrt_rn(v[k].y));
+  }
+}
 
 __device__ __forceinline__ float2 warp_max(float2 v) {
 #pragma unroll
@@ -173,7 +207,7 @@ struct Ring {
   static constexpr uint32_t S = 2560;
   static_assert(!BITS8 || S + 8 <= 2576, "the scales are a stage's last");
   static constexpr uint32_t STAGE = BITS8 ? 2576 : 4096;
-  static constexpr int STAGES = BITS8 ? 4 : 3;
+  static constexpr int STAGES = 3;
   static constexpr uint32_t BYTES = STAGE * STAGES;  // per warp
 };
 
@@ -207,13 +241,16 @@ struct Cursor {
   }
 };
 
-// WARPS: 8, two CTAs per SM; or 16 and one CTA, whose warps meet every fourth
-// turn.  Left to themselves the warps drift apart over a long tensor and the
-// front that they sweep widens (8-bit states, tensors of 2M elements: 230 us
-// with 8 warps, 208 with 16; of 0.26M: 47.5 and 51, so the meetings are kept
-// for large tensors; with 32-bit states the two differ by less than 1 %).
+// WARPS: 8, with two CTAs per SM for 32-bit states and three for 8-bit ones
+// (12M parameters of small tensors: 47.6 us with two, 45.3 with three); or, with
+// 8-bit states, kFront in one CTA, which meet every fourth turn.  Left to
+// themselves the warps drift apart over a long tensor and the front that they
+// sweep widens (us of tensors of 62,000, 139,000, 0.4M and 18M elements on
+// average: 118, 131, 126 and 306 apart, 121, 124, 113 and 258 so); with 32-bit
+// states the two differ by less than 1 %.  More warps than 20 add nothing.
+constexpr int kFront = 20;
 template <bool BITS8, int T, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+__global__ void __launch_bounds__(WARPS * 32, WARPS == kFront ? 1 : BITS8 ? 3 : 2)
     k_adamw(const __grid_constant__ StepParams<BITS8, T> P) {
   using R = Ring<BITS8>;
   extern __shared__ __align__(16) char smem[];
@@ -240,14 +277,13 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   // 1 - b^t without cancellation
   const float c1 = -expm1f(t * P.log_b1), c2 = -expm1f(t * P.log_b2);
   const float rate = lr / c1, root = rsqrtf(c2);
-  const float gm = P.b1c * clip;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t end = P.blocks, hop = gridDim.x * WARPS;
   Cursor<BITS8, T> at;
   at.b = blockIdx.x * WARPS + warp;
   // turns that every warp of the launch takes
-  uint32_t common = WARPS == 16 ? end / hop : 0;
+  uint32_t common = WARPS == kFront ? end / hop : 0;
   if (at.b >= end) {
     count_up();
     return;
@@ -294,7 +330,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     const uint32_t rel = at.b - at.start;
     const bool vec = rel < at.full;
     const int64_t base = (int64_t)rel * kBlock;
-    if (WARPS == 16 && common > 0 && (--common & 3) == 0) __syncthreads();
+    if (WARPS == kFront && common > 0 && (--common & 3) == 0) __syncthreads();
     __syncwarp();  // the warp has read the stage that is filled next
     fetch(stage == 0 ? R::STAGES - 1 : stage - 1, ahead);
     copies_wait<R::STAGES - 1>();
@@ -360,22 +396,35 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
       }
     }
 
-    // 8 bits: m is code * ms and v is (code * vs)^2; the factors b1 ms and
-    // b2 vs^2 of the block take the codes directly
-    const float fm = BITS8 ? P.b1 * ms : P.b1, fv = BITS8 ? P.b2 * (vs * vs) : P.b2;
+    // With 8-bit states every operation is rounded by itself: a code then
+    // depends on the formula alone, and the same operations elsewhere give the
+    // same codes.
     const float keep = 1.f - lr * e.wd;
     float2 r[4], top = both(0.f);
+    if constexpr (BITS8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 c = mul2(g[k], both(clip));
+        m[k] = sum2(mul2(mul2(m[k], both(ms)), both(P.b1)), mul2(c, both(P.b1c)), P.one);
+        v[k] = mul2(v[k], both(vs));
+        v[k] = sum2(mul2(mul2(v[k], v[k]), both(P.b2)), mul2(mul2(c, c), both(P.b2c)), P.one);
+      }
+      roots(v, r);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 c = mul2(g[k], both(clip));
+        m[k] = fma2(m[k], both(P.b1), mul2(c, both(P.b1c)));
+        v[k] = fma2(v[k], both(P.b2), mul2(mul2(c, c), both(P.b2c)));
+        r[k] = make_float2(sqrt_approx(v[k].x), sqrt_approx(v[k].y));
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (BITS8) v[k] = mul2(v[k], v[k]);
-      m[k] = fma2(m[k], both(fm), mul2(g[k], both(gm)));
-      const float2 c = mul2(g[k], both(clip));
-      v[k] = fma2(v[k], both(fv), mul2(mul2(c, c), both(P.b2c)));
-      r[k] = make_float2(sqrt_approx(v[k].x), sqrt_approx(v[k].y));
       const float2 d = fma2(r[k], both(root), both(P.eps));
       const float2 q = mul2(m[k], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
       p[k] = fma2(q, both(-rate), mul2(p[k], both(keep)));
-      if (BITS8) {
+      if constexpr (BITS8) {
         top.x = fmax3(top.x, fabsf(m[k].x), fabsf(m[k].y));
         top.y = fmax3(top.y, r[k].x, r[k].y);
       }
@@ -386,7 +435,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
       if (lane < 2) {
         const float high = lane == 0 ? top.x : top.y;
         float* to = (lane == 0 ? e.ms : e.vs) + rel;
-        *to = high >= kLeast ? high * (1.f / 448.f) : 0.f;
+        *to = high >= kLeast ? __fmul_rn(high, 1.f / 448.f) : 0.f;
       }
       // a positive root takes at least the smallest code (2^-9)
       const float least = iv > 0.f ? 0x1p-9f : 0.f;
@@ -662,12 +711,13 @@ cudaError_t step_part(const evoattn_adamw_tensor* t, int count, const AdamwScala
   P.log_b1 = (float)log(s.beta1);
   P.log_b2 = (float)log(s.beta2);
   P.eps = s.eps;
+  P.one = 1.f;
   P.clip = s.clip ? 1 : 0;
   P.last = last ? 1 : 0;
   P.shift = coarse_table(P.coarse, blocks, [&](int i) { return (uint64_t)P.e[i].start; });
-  // large tensors: 2048 blocks, half a million elements, on average
+  // large tensors: 512 blocks on average
   if constexpr (BITS8) {
-    if (blocks >= 2048ull * (uint64_t)std::max(k, 1)) return launch_step<BITS8, T, 16>(P, st);
+    if (blocks >= 512ull * (uint64_t)std::max(k, 1)) return launch_step<BITS8, T, kFront>(P, st);
   }
   return launch_step<BITS8, T, 8>(P, st);
 }

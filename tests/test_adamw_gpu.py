@@ -190,6 +190,51 @@ def test_zero_gradients_only_decay(bits):
     assert not bool(opt.exp_avg.float().any()) and not bool(opt.exp_avg_sq.float().any())
 
 
+@pytest.mark.parametrize("grad,max_norm", [("bf16", None), ("f32", 0.5)])
+@pytest.mark.parametrize("sizes", [SIZES, [700000]])
+def test_codes_are_those_of_single_operations(grad, max_norm, sizes):
+    """8-bit codes and scales are the bits that the formula gives in fp32 with
+    every operation rounded by itself.  A root may be off by a last bit once in
+    a million; a scale of the roots by that bit.  Zeros, gradients whose squares
+    underflow, and large ones occur."""
+    ps, gs, _ = make(sizes, 31, grad)
+    for i, g in enumerate(gs):
+        g.mul_([1.0, 1e-14, 1e5][i % 3])
+        g[g.numel() // 2::7] = 0.0
+    opt = evoattn.AdamW(ps, gs, lr=1e-3, betas=(0.9, 0.98), state_bits=8)
+    ms = [torch.zeros(g.numel(), device=DEV) for g in gs]
+    vs = [torch.zeros(g.numel(), device=DEV) for g in gs]
+    b1, b2 = opt.betas
+
+    def code(t):
+        blocks = torch.nn.functional.pad(t, (0, -t.numel() % 256)).view(-1, 256)
+        top = blocks.abs().amax(1, keepdim=True)
+        held = top >= 2.0 ** -100
+        inverse = torch.where(held, (1.0 / top) * 448.0, torch.zeros_like(top))
+        scale = torch.where(held, top * torch.tensor(1 / 448, device=DEV), torch.zeros_like(top))
+        return blocks, held, (blocks * inverse).to(torch.float8_e4m3fn).float(), scale
+
+    for step in range(3):
+        norm = opt.step(max_norm=max_norm)
+        for i, g in enumerate(gs):
+            n, at = g.numel(), opt.offsets[i]
+            c = g.float()
+            if max_norm is not None:
+                c = c * torch.clamp(max_norm / (norm + 1e-6), max=1.0)
+            m = b1 * ms[i] + (1.0 - b1) * c
+            r = torch.sqrt(b2 * (vs[i] * vs[i]) + (1.0 - b2) * (c * c))
+            for t, keep, held_in, codes, scales in ((m, ms, False, opt.exp_avg, opt.exp_avg_scale),
+                                                    (r, vs, True, opt.exp_avg_sq, opt.exp_avg_sq_scale)):
+                blocks, held, want, scale = code(t)
+                if held_in:
+                    want = torch.where((blocks > 0) & held & (want == 0), torch.full_like(want, 2.0 ** -9), want)
+                got = scales[at // 256:at // 256 + scale.numel()].view(-1, 1)
+                assert bool(((got - scale).abs() <= (2 * U * scale if held_in else 0 * scale)).all()), (step, i)
+                assert torch.equal(codes[at:at + n].float(), want.reshape(-1)[:n]), (step, i)
+                keep[i] = (want * got).reshape(-1)[:n]
+            g.neg_().mul_(0.75)
+
+
 def test_wide_range_inside_a_block():
     """Gradients over 12 decades inside a block: the smallest roots take the
     smallest positive code, so no later step divides by eps alone."""
