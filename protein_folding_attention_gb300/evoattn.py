@@ -494,7 +494,9 @@ class AdamW:
     resume.  With state_bits=8 they are torch.float8_e4m3fn codes: the first
     moment is code * scale, the root of the second one code * scale.  Their
     padding is never written.  The step counter lives on the device.  One
-    optimiser is used on one stream at a time.
+    optimiser is used on one stream at a time.  The tensors' addresses are
+    taken here (the gradients' by step(grads=...) too): none of them may be
+    given other memory (`p.data = ...`) afterwards.
     """
 
     def __init__(self, params, grads, *, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
@@ -580,7 +582,8 @@ class AdamW:
             k = bisect.bisect_left(self._starts, at + g.numel() * g.element_size()) - 1
             if row.n and k >= 0 and self._ends[k] > at:
                 raise ValueError(f"gradient {i} overlaps what a step writes")
-            row.grad, row.grad_dtype = at, _dtype_code(g)
+        for row, g in zip(self._table, grads):  # all of them, or after an error none
+            row.grad, row.grad_dtype = g.data_ptr(), _dtype_code(g)
         self.grads = grads
 
     def step(self, max_norm=None, grads=None, stream=None):

@@ -378,3 +378,16 @@ def test_python_refusals():
         opt.step()
     with pytest.raises(ValueError):
         evoattn.grad_norm([gs[0].half()])
+
+
+def test_refused_gradients_leave_the_old_ones_bound():
+    """New gradients of which a later one is refused replace none."""
+    ps, gs, _ = make([300, 500], 21)
+    other = [p.clone() for p in ps]
+    a, b = evoattn.AdamW(ps, gs), evoattn.AdamW(other, gs)
+    fresh = [torch.ones_like(gs[0]), torch.ones(499, device=DEV)]
+    with pytest.raises(ValueError):
+        a.step(grads=fresh)
+    a.step(), b.step()
+    assert all(torch.equal(x, y) for x, y in zip(ps, other))
+    assert a.grads[0] is gs[0] and a.steps_taken() == 1
