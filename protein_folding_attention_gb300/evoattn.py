@@ -452,6 +452,8 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
         if workspace is None:
             workspace = torch.empty(lib.evoattn_block_norm_bwd_workspace_size(C), device=lead.device,
                                     dtype=torch.uint8)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
     if beta_pre is not None:
         _add_vectors([], ((beta_pre, "beta_pre"),), C, dev)
     words += shape

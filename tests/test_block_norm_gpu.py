@@ -607,3 +607,11 @@ def test_python_refusals():
     with pytest.raises(evoattn.EvoAttnError):
         evoattn.block_norm_bwd(*[b[n] for n in BWD_ARGS],
                                workspace=torch.empty(256, device=DEV, dtype=torch.uint8))
+
+
+def test_workspaces_that_the_kernels_cannot_use_are_refused():
+    b = to_gpu(draw((1, 2, 3, 16), "bf16", seed=29, backward=True))
+    n = evoattn.load().evoattn_block_norm_bwd_workspace_size(16)
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, device=DEV, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            evoattn.block_norm_bwd(*[b[k] for k in BWD_ARGS], workspace=ws)
