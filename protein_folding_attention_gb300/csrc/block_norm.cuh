@@ -30,7 +30,8 @@
 // from load to store.  G = 8, 16 or 32 lanes of a warp up to C = 256 (sums by
 // shuffles); a warp with two such parts per lane up to C = 512; above that
 // several warps (sums by shuffles, then through shared memory with one named
-// barrier per sum).  Persistent CTAs walk the rows.  A thread
+// barrier per sum).  The forward's CTAs are many and short, the backward's
+// persistent (launch_fwd, launch_bwd).  A thread
 // copies its own channels of the coming rows into a ring in shared memory
 // (cp.async, no registers held meanwhile, no barrier: it reads only what it
 // copied), and keeps the parameter gradients of its channels over all its rows
@@ -1221,7 +1222,9 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     if (reinterpret_cast<uintptr_t>(v) % 16) p.wide_params = false;
   const int need = (c.C + kE - 1) / kE;  // threads of a row
   if (need <= 32) {
-    pl.g = pl.vec ? (need <= 8 ? 8 : need <= 16 ? 16 : 32) : 32;
+    // (147,456 bf16 rows of 101, one element per access: a warp per row 88 us
+    // forward and 126 backward, 16 lanes 49 and 76)
+    pl.g = need <= 8 ? 8 : need <= 16 ? 16 : 32;
     p.lanes = pl.g;
     pl.threads = kThreads;
   } else if (need <= kTwice) {
@@ -1398,6 +1401,8 @@ cudaError_t ring_fwd(const Plan& pl, cudaStream_t st) {
 template <typename TS, typename TI, bool POST, bool PRE, bool CHUNK>
 cudaError_t single_fwd(const Plan& pl, cudaStream_t st) {
   switch (pl.g) {
+    case 8: return launch_fwd<TS, TI, 8, false, POST, PRE, CHUNK>(pl, st);
+    case 16: return launch_fwd<TS, TI, 16, false, POST, PRE, CHUNK>(pl, st);
     case 32: return launch_fwd<TS, TI, 32, false, POST, PRE, CHUNK>(pl, st);
     case kTwice: return launch_fwd<TS, TI, kTwice, false, POST, PRE, CHUNK>(pl, st);
     default: return launch_fwd<TS, TI, kPlain, false, POST, PRE, CHUNK>(pl, st);
@@ -1431,6 +1436,8 @@ cudaError_t ring_bwd(const Plan& pl, float* ws, cudaStream_t st) {
 template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED, bool CHUNK>
 cudaError_t single_bwd(const Plan& pl, float* ws, cudaStream_t st) {
   switch (pl.g) {
+    case 8: return launch_bwd<TS, TI, 8, false, POST, PRE, GROUPED, CHUNK>(pl, ws, st);
+    case 16: return launch_bwd<TS, TI, 16, false, POST, PRE, GROUPED, CHUNK>(pl, ws, st);
     case 32: return launch_bwd<TS, TI, 32, false, POST, PRE, GROUPED, CHUNK>(pl, ws, st);
     case kTwice: return launch_bwd<TS, TI, kTwice, false, POST, PRE, GROUPED, CHUNK>(pl, ws, st);
     default: return launch_bwd<TS, TI, kPlain, false, POST, PRE, GROUPED, CHUNK>(pl, ws, st);
