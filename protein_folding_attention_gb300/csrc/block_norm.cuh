@@ -859,9 +859,11 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     }
   };
 
-  auto fetch_chunk = [&](uint32_t stage, uint32_t first) {
-    if (first >= p.rows) return;
-    const uint32_t n = min(p.rows - first, (uint32_t)g.slots) * C;
+  // the rows of the CTA's turn at `w` (a group's row is g.slot rows behind the first)
+  auto fetch_chunk = [&](uint32_t stage, const Walk<GROUPED>& w) {
+    const uint32_t first = w.row - g.slot;
+    if (w.left == 0 || first >= w.end) return;
+    const uint32_t n = min(w.end - first, (uint32_t)g.slots) * C;
     const At<DENSE> r(p, first);
     const uint32_t to = ring_s + stage * stage_bytes;
     const uint32_t ss = (first * p.stride_s) & 15, si = (first * p.stride_i) & 15;
@@ -872,7 +874,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     }
     if (POST) {
       chunk_put(to + 2 * chunk_s + chunk_i, r.block(p, p.u), n * sizeof(TI), si);
-      if (gated) chunk_put(to + 2 * chunk_s + 2 * chunk_i, r.block(p, p.gate), n * sizeof(TI), si);
+      if (!GROUPED && gated) chunk_put(to + 2 * chunk_s + 2 * chunk_i, r.block(p, p.gate), n * sizeof(TI), si);
     }
   };
 
@@ -889,7 +891,8 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
       copies_close();
     }
   } else if constexpr (CHUNK) {
-    fetch_chunk(0, at.row - g.slot);
+    ahead = at;
+    fetch_chunk(0, ahead);
     copies_close();
   }
   uint32_t stage = 0;
@@ -939,7 +942,8 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     } else if constexpr (CHUNK) {
       copies_wait<0>();
       __syncthreads();  // the turn's rows are here, and the other stage has been read
-      fetch_chunk(stage ^ 1, row - g.slot + at.hop);
+      ahead.advance(p, g);
+      fetch_chunk(stage ^ 1, ahead);
       copies_close();
       const uint32_t first = row - g.slot;
       const char* from = ring + stage * stage_bytes;
@@ -953,7 +957,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
         if (PRE) dy = load<TI, L, G>(from, g, C);
         if (POST) {
           u = load<TI, L, G>(from + chunk_i, g, C);
-          if (gated) gt = load<TI, L, G>(from + 2 * chunk_i, g, C);
+          if (!GROUPED && gated) gt = load<TI, L, G>(from + 2 * chunk_i, g, C);
         }
       }
     } else {
@@ -1448,9 +1452,11 @@ cudaError_t dispatch_bwd(const Plan& pl, float* ws, cudaStream_t st) {
   if (pl.vec)
     return pl.dense ? ring_bwd<TS, TI, POST, PRE, GROUPED, true>(pl, ws, st)
                     : ring_bwd<TS, TI, POST, PRE, GROUPED, false>(pl, ws, st);
-  if constexpr (!GROUPED) {
-    if (pl.chunk) return single_bwd<TS, TI, POST, PRE, false, true>(pl, ws, st);
-  }
+  // (with shared gate rows the rows of a CTA's turn are one piece where a
+  // gate row's rows are spread over the CTA, see launch_bwd: 200,000 bf16 rows
+  // of 99 with a gate row per 256: 204 us read one by one, 103 so)
+  if (pl.chunk && (!GROUPED || pl.p.share >= (uint32_t)pl.slots))
+    return single_bwd<TS, TI, POST, PRE, GROUPED, true>(pl, ws, st);
   return single_bwd<TS, TI, POST, PRE, GROUPED, false>(pl, ws, st);
 }
 
