@@ -61,10 +61,10 @@ constexpr int kE = 8;             // channels of a part: what a thread has of a 
 constexpr int kThreads = 256;     // threads of a CTA where a row takes at most 8 warps
 constexpr int kMaxThreads = 512;  // ... 16 warps (C = 4096)
 
-// How a row is laid over threads: 8, 16 or 32 lanes of a warp; a whole warp
-// with two parts per lane; up to 8 warps, with one part or two; or any number
+// How a row is laid over threads: 8, 16 or 32 lanes of a warp, or as many as it
+// has parts; a whole warp with two parts per lane; up to 8 warps, with one part or two; or any number
 // of warps, one part each (rows that cannot be copied 16 bytes at a time).
-constexpr int kTwice = 64, kWarps = 0, kPlain = -1, kWarpsTwice = -2;
+constexpr int kTwice = 64, kWarps = 0, kPlain = -1, kWarpsTwice = -2, kPacked = 10;
 constexpr bool warps_of(int G) { return G <= 0; }
 constexpr int width_of(int G) { return G <= 0 || G > 32 ? 32 : G; }  // lanes of a warp that share a row
 constexpr int parts_of(int G) { return G == kTwice || G == kWarpsTwice ? 2 : 1; }
@@ -417,8 +417,21 @@ __device__ __forceinline__ float2 across_warps(float2 v, Group& g) {
   for (int i = 0; i < warps; ++i) v = add2(v, b[i]);
   return v;
 }
+// n <= 16 lanes, any number: lane l takes lane l + o, then all take the first's.
+__device__ __forceinline__ float packed_sum(float v, const Group& g) {
+  auto take = [&](int o) {
+    const float t = __shfl_down_sync(0xffffffffu, v, o);
+    if (g.l + o < g.lanes) v += t;
+  };
+  if (g.lanes > 8) take(8);
+  take(4);
+  take(2);
+  take(1);
+  return __shfl_sync(0xffffffffu, v, (int)(threadIdx.x & 31) - g.l);
+}
 template <int G>
 __device__ __forceinline__ float2 group_sum(float2 v, Group& g) {
+  if constexpr (G == kPacked) return make_float2(packed_sum(v.x, g), packed_sum(v.y, g));
 #pragma unroll
   for (int o = width_of(G) / 2; o > 0; o >>= 1)
     v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
@@ -427,6 +440,7 @@ __device__ __forceinline__ float2 group_sum(float2 v, Group& g) {
 }
 template <int G>
 __device__ __forceinline__ float group_sum(float v, Group& g) {
+  if constexpr (G == kPacked) return packed_sum(v, g);
 #pragma unroll
   for (int o = width_of(G) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (warps_of(G)) v = across_warps(make_float2(v, 0.f), g).x;
@@ -437,6 +451,24 @@ template <int G, Layout L>
 __device__ __forceinline__ Group make_group(const Params& p, float2 (*smem)[2 * kMaxWarps]) {
   constexpr int W = width_of(G);
   Group g;
+  if constexpr (G == kPacked) {
+    static_assert(L == kRun, "a part is one run");
+    const int per = 32 / p.lanes, at = (int)threadIdx.x & 31, k = at / p.lanes;
+    g.lanes = p.lanes;
+    g.slots = (int)blockDim.x / 32 * per;
+    // the lanes left over: a group behind the last one, without channels (its
+    // sums in `red` stay in there: fewer than 8 lanes a warp are left of it)
+    g.slot = k < per ? (int)threadIdx.x / 32 * per + k : g.slots;
+    g.lane = g.l = at - k * p.lanes;
+    g.first = (int)threadIdx.x - g.l;
+    g.base = k < per ? 0 : p.C;
+    g.c0 = k < per ? kE * g.l : p.C;
+    g.c1 = g.c0 + 4;
+    g.act = g.c0 < p.C;
+    g.buf = nullptr;
+    g.turn = 0;
+    return g;
+  }
   g.lanes = G > 0 ? W : p.lanes;
   g.slots = (int)blockDim.x / g.lanes;
   g.slot = (int)threadIdx.x / g.lanes;
@@ -1032,28 +1064,27 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
       if (fresh) {
 #pragma unroll
         for (int k = 0; k < V::P; ++k) dg.p[k] = mul2(dg.p[k], fma2(q.p[k], both(-1.f), both(1.f)));
-        const bool owns = p.by_cta || was.item < p.items;
+        const RowPos rg = row_pos(p.gate_of, was.gate_row);
+        char* const whole = row_ptr(p.dgate, rg, p.gate_of);
+        float* const part = p.gate_part + (size_t)was.item * C;  // (where segs > 1)
         if (p.by_cta && g.slots > 1) {
+          // a thread per channel adds the groups' sums (a group's threads,
+          // eight channels each: 589,824 bf16 rows of 32 74 us, 62 so)
           const int width = g.lanes * V::E;
           __syncthreads();
 #pragma unroll
           for (int e = 0; e < V::E; ++e) red[g.slot * width + channel<L, G>(g, e)] = dg[e];
           __syncthreads();
-          if (g.slot == 0) {
-#pragma unroll
-            for (int e = 0; e < V::E; ++e) {
-              float s = 0.f;
-              for (int i = 0; i < g.slots; ++i) s += red[i * width + channel<L, G>(g, e)];
-              dg[e] = s;
-            }
+          for (int c = threadIdx.x; c < C; c += blockDim.x) {
+            float s = 0.f;
+            for (int i = 0; i < g.slots; ++i) s += red[i * width + c];
+            if (p.segs == 1) reinterpret_cast<TI*>(whole)[c] = static_cast<TI>(s);
+            else part[c] = s;
           }
-        }
-        const bool writes = owns && (!p.by_cta || g.slot == 0);
-        if (p.segs == 1) {
-          const RowPos rg = row_pos(p.gate_of, was.gate_row);
-          store<TI, L, G>(writes, row_ptr(p.dgate, rg, p.gate_of), g, C, dg);
         } else {
-          store<float, L, G>(writes, reinterpret_cast<char*>(p.gate_part + (size_t)was.item * C), g, C, dg);
+          const bool writes = p.by_cta || was.item < p.items;
+          if (p.segs == 1) store<TI, L, G>(writes, whole, g, C, dg);
+          else store<float, L, G>(writes, reinterpret_cast<char*>(part), g, C, dg);
         }
       }
     }
@@ -1249,6 +1280,14 @@ inline void make_plan(const BlockNormCall& c, const RowOperand* const* ops, Oper
     pl.threads = p.lanes * std::max(1, (two ? 4 : kThreads / 32) / warps);
   }
   pl.slots = pl.threads / p.lanes;
+  // A group of as many lanes as a row has parts, where a warp holds more rows
+  // so (bf16 rows, forward and backward: 589,824 of 32 51 -> 33 and 91 -> 57 us,
+  // 200,000 of 80 38 -> 33 and 66 -> 58).
+  if (pl.vec && esize[0] == 2 && need <= 16 && 32 / need > 32 / p.lanes) {
+    pl.g = kPacked;
+    p.lanes = need;
+    pl.slots = pl.threads / 32 * (32 / need);
+  }
   // rows one behind the other
   pl.chunk = !pl.vec && pl.dense;
   for (int i = 0; i < count && pl.chunk; ++i)
@@ -1393,6 +1432,8 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
 
 template <typename TS, typename TI, bool POST, bool PRE, bool DENSE, bool HELD>
 cudaError_t ring_fwd(const Plan& pl, cudaStream_t st) {
+  if constexpr (sizeof(TS) == 2)
+    if (pl.g == kPacked) return launch_fwd<TS, TI, kPacked, true, POST, PRE, DENSE, HELD>(pl, st);
   switch (pl.g) {
     case 8: return launch_fwd<TS, TI, 8, true, POST, PRE, DENSE, HELD>(pl, st);
     case 16: return launch_fwd<TS, TI, 16, true, POST, PRE, DENSE, HELD>(pl, st);
@@ -1428,6 +1469,8 @@ cudaError_t dispatch_fwd(const Plan& pl, cudaStream_t st) {
 
 template <typename TS, typename TI, bool POST, bool PRE, bool GROUPED, bool DENSE>
 cudaError_t ring_bwd(const Plan& pl, float* ws, cudaStream_t st) {
+  if constexpr (sizeof(TS) == 2)
+    if (pl.g == kPacked) return launch_bwd<TS, TI, kPacked, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
   switch (pl.g) {
     case 8: return launch_bwd<TS, TI, 8, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
     case 16: return launch_bwd<TS, TI, 16, true, POST, PRE, GROUPED, DENSE>(pl, ws, st);
