@@ -1401,16 +1401,27 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
   if (GROUPED) {
     // A gate row's rows are walked by one group where they are fewer than the
     // CTA's groups (spreading them would leave groups idle), else spread over
-    // a CTA, in as many items per gate row as give every CTA one.
+    // a CTA, in as many items per gate row as give the CTAs the fewest turns:
+    // one item each for a few gate rows, several where whole gate rows would
+    // leave CTAs without one in the last round.  (An item's end costs about
+    // three turns.)
     const uint32_t gates = p.rows / p.share;
     p.by_cta = p.share >= (uint32_t)pl.slots;
     p.segs = 1;
     p.seg_rows = p.share;
-    if (p.by_cta && gates < (uint32_t)ctas) {
-      const uint32_t want = ((uint32_t)ctas + gates - 1) / gates;
-      p.seg_rows = std::max<uint32_t>(pl.slots, (p.share + want - 1) / want);
-      p.seg_rows = (p.seg_rows + pl.slots - 1) / pl.slots * pl.slots;
-      p.segs = (p.share + p.seg_rows - 1) / p.seg_rows;
+    if (p.by_cta) {
+      const uint32_t slots = pl.slots, n = ctas;
+      const auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
+      uint64_t least = up(gates, n) * (up(p.share, slots) + 3);
+      for (uint32_t rounds = 1; rounds <= 8; ++rounds) {
+        const uint64_t segs = std::min<uint64_t>((uint64_t)rounds * n, kNormMaxItems) / gates;
+        if (segs < 2) continue;
+        const uint64_t turns = up(up(p.share, segs), slots);
+        if (rounds * (turns + 3) >= least) continue;
+        least = rounds * (turns + 3);
+        p.seg_rows = (uint32_t)(turns * slots);
+        p.segs = (uint32_t)up(p.share, p.seg_rows);
+      }
     }
     p.items = gates * p.segs;
     need = p.by_cta ? p.items : (p.items + pl.slots - 1) / pl.slots;

@@ -16,6 +16,7 @@ struct RowOperand {
 
 constexpr int kNormMaxC = 4096;   // channels of a row
 constexpr int kNormMaxCtas = 640; // CTAs of a backward launch (one partial sum each)
+constexpr int kNormMaxItems = 4 * kNormMaxCtas;  // pieces of shared gate rows (one partial sum each)
 
 struct BlockNormCall {
   int n[3];  // B, I, J

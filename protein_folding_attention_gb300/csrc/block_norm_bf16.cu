@@ -12,8 +12,8 @@ cudaError_t block_norm_bwd_bf16(const BlockNormCall& c, cudaStream_t st) {
 }
 
 size_t block_norm_bwd_workspace_bytes(int C) {
-  // the sums of every CTA, and at most 2 * kNormMaxCtas items of shared gate rows
-  return (size_t)(norm::kSums * kNormMaxCtas + 2 * kNormMaxCtas) * C * sizeof(float);
+  // the sums of every CTA, and at most kNormMaxItems pieces of shared gate rows
+  return (size_t)(norm::kSums * kNormMaxCtas + kNormMaxItems) * C * sizeof(float);
 }
 
 }  // namespace evo
