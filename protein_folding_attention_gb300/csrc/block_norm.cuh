@@ -831,7 +831,9 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
   const bool with_dx1 = p.dx1.p != nullptr;
 
   constexpr bool RING = ring_of(G, VEC), CHUNK = !VEC && DENSE;
-  constexpr bool STEP = RING && !GROUPED && G > 0 && G <= 32 && sizeof(TI) == 2;
+  constexpr bool STEP = RING && (!GROUPED || sizeof(TS) == 4) && G > 0 && G <= 32 && sizeof(TI) == 2;
+  // (shared gate rows: with an fp32 stream, and where the rows fill their lanes)
+  const bool in_step = STEP && (!GROUPED || C > 6 * g.lanes);
   float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
   // parameters: [vector][run][lane] float4, read back without bank conflicts
   float4* const prm = reinterpret_cast<float4*>(smem + bwd_sums_bytes(blockDim.x, parts_of(G)));
@@ -947,8 +949,9 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
       // The CTA's warps stay in step: left to themselves they drift apart and the
       // rows in flight with them (N = 768, bf16: 221 us so, 184 in step).  Not
       // where a row takes a warp of its own or several, nor for fp32 rows, where
-      // it costs more than it gives.
-      if (STEP) __syncthreads();
+      // it costs more than it gives; with shared gate rows it gives with an fp32
+      // stream (N = 768, one gate row: 231 us, 206 in step).
+      if (in_step) __syncthreads();
       if (CROSS) __syncwarp();  // the warp has read that stage
       if (ahead.left > 0) {
         fetch(to, ahead.row, ahead.row < ahead.end);
