@@ -615,3 +615,29 @@ def test_workspaces_that_the_kernels_cannot_use_are_refused():
     for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, device=DEV, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError):
             evoattn.block_norm_bwd(*[b[k] for k in BWD_ARGS], workspace=ws)
+
+
+@pytest.mark.parametrize("C", [16, 24, 32, 40, 48, 72, 80])
+@pytest.mark.parametrize("gate", ["none", "full", "row", "batch"])
+def test_narrow_rows_that_share_a_warp(C, gate):
+    """Groups of as many lanes as a row has parts, lanes left over or not: one
+    row, part of a turn, and several turns."""
+    for shape in ((1, 1, 1, C), (2, 3, 17, C), (2, 40, 301, C)):
+        k = draw(shape, "bf16", gate, seed=C)
+        x1, y = run_fwd(k, C % 16 == 0)
+        check_fwd(k, x1, y, C % 16 == 0)
+        k = draw(shape, "bf16", gate, seed=C + 1, backward=True)
+        check_bwd(k, run_bwd(k, C % 16 == 0), C % 16 == 0)
+
+
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("shape", [(1, 400, 300, 24), (1, 400, 300, 37), (2, 3, 7000, 61), (1, 350, 64, 131),
+                                   (1, 5, 900, 301)])
+def test_gate_rows_cut_into_pieces(types, shape):
+    """More gate rows than CTAs, and few long ones: pieces of a gate row's rows
+    whose sums a second kernel joins, rows copied one by one or a turn at once."""
+    k = draw(shape, types, "row", seed=shape[3], backward=True)
+    got = run_bwd(k, False)
+    check_bwd(k, got, False)
+    again = run_bwd(k, False)
+    assert all(torch.equal(got[n], again[n]) for n in got)
