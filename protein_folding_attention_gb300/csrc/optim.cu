@@ -156,18 +156,20 @@ __device__ __forceinline__ float inverse448(float top) {
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-// a + b, where a or b may be a product that has to be rounded before: the
-// assembler joins a packed multiplication and an addition to one fused
-// operation, in spite of their .rn, but not with a factor that it does not
-// know.  `one` is 1 and comes in as a parameter of the kernel.
+// a + b, where a or b may be a product that has to be rounded before.  As a
+// fused operation with a factor that is not known when the kernel is compiled:
+// mul2 and add2 one after the other give the bits of one fma2 (a fifth of the
+// scales was off by an ulp).  `one` is 1 and comes in as a parameter of the kernel.
 __device__ __forceinline__ float2 sum2(float2 a, float2 b, float one) { return fma2(a, both(one), b); }
 
 // Square roots, rounded to nearest, of a lane's eight values.  Inside the range
-// where no step overflows or loses bits: one Newton step from the approximate
-// reciprocal root y, with the residual v - (v y)^2 exact in fp32 (Markstein,
-// 1990): all but about one in a million are rounded correctly.  (The function
-// for one value tests that range for each of the eight: 289 us a step of 107M
-// parameters, 277 so.)
+// where no step overflows or loses bits: from a = v y, y near 1 / sqrt(v), one
+// Newton step a + (v - a^2) y / 2 with the residual exact in fp32 (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// IBM J. Res. Dev. 34, 1990).  It gave the correctly rounded root for every
+// fp32 value in that range (all 1.6e9 compared on a GB300), so a root does not
+// depend on which way the lane's other values take.  __fsqrt_rn for each of the
+// eight: 271 us a step of 107M parameters, 258 so.
 __device__ __forceinline__ void roots(const float2* v, float2* r) {
   const float low = fminf(fminf(fminf(v[0].x, v[0].y), fminf(v[1].x, v[1].y)),
                           fminf(fminf(v[2].x, v[2].y), fminf(v[3].x, v[3].y)));

@@ -391,3 +391,22 @@ def test_refused_gradients_leave_the_old_ones_bound():
     a.step(), b.step()
     assert all(torch.equal(x, y) for x, y in zip(ps, other))
     assert a.grads[0] is gs[0] and a.steps_taken() == 1
+
+
+def test_roots_are_rounded_to_nearest_beside_any_values():
+    """The scale of a block's roots is its largest root / 448: for roots of
+    every exponent from 2^-50 to 2^50 and 80,000 mantissas, beside values as
+    large, zeros, and values outside the range of the step's own root, it is
+    the bits that the correctly rounded root gives."""
+    n, b2 = 80_000, 0.9
+    gen = torch.Generator().manual_seed(42)
+    top = ((1.0 + torch.rand(n, generator=gen)) * 2.0 ** (torch.arange(n) % 101 - 50).float()).to(DEV)
+    beside = torch.tensor([0.5, 0.0, 2.0 ** -60, 1.0], device=DEV)[torch.arange(n, device=DEV) // 101 % 4]
+    g = (top * beside)[:, None].repeat(1, 256)
+    g[:, 5] = top
+    opt = evoattn.AdamW([torch.zeros(n, 256, device=DEV)], [g], betas=(0.9, b2), state_bits=8)
+    opt.step()
+    f = lambda x: torch.tensor(x, dtype=torch.float32, device=DEV)
+    v = f(1.0 - b2) * (top * top)     # in fp32, the old v being zero
+    root = torch.sqrt(v.double()).float()   # (53 bits are enough to round a root of 24 bits right)
+    assert torch.equal(opt.exp_avg_sq_scale, root * f(1 / 448))
