@@ -136,7 +136,7 @@ __device__ __forceinline__ void from_e4m3(uint32_t w, float2* v) {
 }
 __device__ __forceinline__ float sqrt_approx(float a) {
   float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
 __device__ __forceinline__ float rsqrt_approx(float a) {

@@ -410,3 +410,22 @@ def test_roots_are_rounded_to_nearest_beside_any_values():
     v = f(1.0 - b2) * (top * top)     # in fp32, the old v being zero
     root = torch.sqrt(v.double()).float()   # (53 bits are enough to round a root of 24 bits right)
     assert torch.equal(opt.exp_avg_sq_scale, root * f(1 / 448))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_second_moments_below_the_normal_range(bits):
+    """An eps that is small against the root of a subnormal v: the root is not
+    taken as zero (the quotient would be m / eps).  v = (1 - beta2) g^2 is off
+    by half a unit 2^-149 for each of its two products, the quotient by half of
+    that relatively, beside its own 64 u."""
+    n = 1000
+    gen = torch.Generator().manual_seed(41)
+    g = ((1.0 + 3.0 * torch.rand(n, generator=gen)) * 1e-19 *
+         (1 - 2 * torch.randint(0, 2, (n,), generator=gen))).to(DEV)
+    p = torch.zeros(n, device=DEV)
+    opt = evoattn.AdamW([p], [g], lr=1e-3, betas=(0.9, 0.999), eps=1e-30, weight_decay=0.0, state_bits=bits)
+    opt.step()
+    zero = torch.zeros(n, dtype=torch.float64)
+    want, _, v = tr.adamw(zero, g, zero, zero, 1, 1e-3, (0.9, 0.999), 1e-30, 0.0)
+    assert float(v.max()) < 2.0 ** -126
+    close(p, want, (64 * U + 2.0 ** -149 / v) * want.abs(), "p")
