@@ -40,6 +40,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -551,6 +552,21 @@ __device__ __forceinline__ void sigmoid(Vec<Q>& v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v.p[k].y) : "f"(t.y));
   }
 }
+// The sigmoid, and in `away` its distance from 1 as t / (1 + t), t = e^(-v): the
+// difference 1 - q would have lost 1e-4 of itself at v = 8 and all at v = 17.
+// (Where t overflows or q underflows, the distance is 0 beside q = 0: only their
+// product is used.)
+template <int Q>
+__device__ __forceinline__ void sigmoid(Vec<Q>& v, Vec<Q>& away) {
+#pragma unroll
+  for (int k = 0; k < v.P; ++k) {
+    const float2 e = mul2(v.p[k], both(-1.4426950408889634f));
+    const float2 t = make_float2(ex2(e.x), ex2(e.y)), s = add2(t, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v.p[k].x) : "f"(s.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v.p[k].y) : "f"(s.y));
+    away.p[k] = mul2(make_float2(fminf(t.x, FLT_MAX), fminf(t.y, FLT_MAX)), v.p[k]);
+  }
+}
 
 // ---------------------------------------------------------------------------
 // forward
@@ -835,6 +851,10 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
   // (shared gate rows: with an fp32 stream, and where the rows fill their lanes)
   const bool in_step = STEP && (!GROUPED || C > 6 * g.lanes);
   float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
+  // a thread's own 1 - q of a shared gate row, in the sums' place between them
+  // (in registers it pushes others out)
+  float* const kept = red + threadIdx.x;
+  float4* const kept4 = reinterpret_cast<float4*>(smem) + threadIdx.x;
   // parameters: [vector][run][lane] float4, read back without bank conflicts
   float4* const prm = reinterpret_cast<float4*>(smem + bwd_sums_bytes(blockDim.x, parts_of(G)));
   char* const ring = reinterpret_cast<char*>(prm) + bwd_params_bytes(g.lanes, parts_of(G));
@@ -939,7 +959,17 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
       if (fresh) {
         const RowPos rg = row_pos(p.gate_of, at.gate_row);
         q = g.act ? load<TI, L, G>(row_ptr(p.gate, rg, p.gate_of), g, C) : zero;
-        sigmoid(q);
+        V away;
+        sigmoid(q, away);
+        if constexpr (VEC) {
+#pragma unroll
+          for (int h = 0; h < V::P / 2; ++h)
+            kept4[h * blockDim.x] =
+                make_float4(away.p[2 * h].x, away.p[2 * h].y, away.p[2 * h + 1].x, away.p[2 * h + 1].y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V::E; ++e) kept[e * blockDim.x] = away[e];
+        }
         dg = zero;
       }
     }
@@ -1034,22 +1064,26 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
       store<TS, L, G>(live, r.stream(p, p.dx), g, C, D);
     }
     if (POST) {
-      if (!GROUPED && gated) {
-        q = gt;
-        sigmoid(q);
-      }
       const V g1 = get(0), b1 = get(1);
+      if (!GROUPED && gated) {
+        V away;
+        q = gt;
+        sigmoid(q, away);
+#pragma unroll
+        for (int k = 0; k < V::P; ++k) {
+          D.p[k] = mul2(D.p[k], q.p[k]);
+          const float2 w = fma2(u.p[k], g1.p[k], b1.p[k]);  // (with the scale)
+          dg.p[k] = mul2(mul2(D.p[k], w), away.p[k]);
+        }
+      }
       V b;
 #pragma unroll
       for (int k = 0; k < V::P; ++k) {
-        const float2 w = fma2(u.p[k], g1.p[k], b1.p[k]);  // (with the scale)
-        const float2 dq = mul2(D.p[k], q.p[k]);
+        const float2 dq = GROUPED ? mul2(D.p[k], q.p[k]) : D.p[k];
         acc[0].p[k] = fma2(dq, u.p[k], acc[0].p[k]);
         acc[1].p[k] = add2(acc[1].p[k], dq);
-        if (GROUPED)
-          dg.p[k] = fma2(dq, w, dg.p[k]);  // (1 - q) is applied once, at the end
-        else
-          dg.p[k] = mul2(mul2(dq, w), fma2(q.p[k], both(-1.f), both(1.f)));
+        // (1 - q) is applied once, at the end
+        if (GROUPED) dg.p[k] = fma2(dq, fma2(u.p[k], g1.p[k], b1.p[k]), dg.p[k]);
         b.p[k] = mul2(dq, g1.p[k]);
       }
       float2 s = make_float2(sum(b), dot(b, u));
@@ -1065,8 +1099,17 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
     fresh = at.advance(p, g);
     if constexpr (GROUPED) {
       if (fresh) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < V::P; ++k) dg.p[k] = mul2(dg.p[k], fma2(q.p[k], both(-1.f), both(1.f)));
+          for (int h = 0; h < V::P / 2; ++h) {
+            const float4 away = kept4[h * blockDim.x];
+            dg.p[2 * h] = mul2(dg.p[2 * h], make_float2(away.x, away.y));
+            dg.p[2 * h + 1] = mul2(dg.p[2 * h + 1], make_float2(away.z, away.w));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V::E; ++e) dg[e] *= kept[e * blockDim.x];
+        }
         const RowPos rg = row_pos(p.gate_of, was.gate_row);
         char* const whole = row_ptr(p.dgate, rg, p.gate_of);
         float* const part = p.gate_part + (size_t)was.item * C;  // (where segs > 1)
@@ -1084,6 +1127,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
             if (p.segs == 1) reinterpret_cast<TI*>(whole)[c] = static_cast<TI>(s);
             else part[c] = s;
           }
+          __syncthreads();  // `kept` takes their place
         } else {
           const bool writes = p.by_cta || was.item < p.items;
           if (p.segs == 1) store<TI, L, G>(writes, whole, g, C, dg);

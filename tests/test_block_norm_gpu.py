@@ -641,3 +641,58 @@ def test_gate_rows_cut_into_pieces(types, shape):
     check_bwd(k, got, False)
     again = run_bwd(k, False)
     assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+def _check_dgate(k, got, most=0.0):
+    """dgate against float64 with a tolerance that shrinks with q (1 - q).
+    q = 1 / (1 + t), t = exp(-g): the exponent is off by 2 u |g|, and with it q
+    and 1 - q = t q by that relatively, beside a few roundings and the two
+    approximate operations: (64 + 4 |g|) u of q (1 - q).  `most`: what may be
+    lost where q or t leaves the range of fp32."""
+    rows = tuple(range(3))
+    h, _ = tr.normalise(k["u"].double(), False, 1e-5)
+    ku = 1 + kappa(k["u"], False)
+    s, g1, b1 = (k[n].double() for n in ("scale", "gamma_post", "beta_post"))
+    w = h * g1 + b1
+    werr = 64 * U * ku * (1 + h.abs()) * g1.abs() + 4 * U * b1.abs()
+    v = k["gate"].double().expand_as(h)
+    e = k["dx1"].double() * s
+    f = torch.sigmoid(v) * torch.sigmoid(-v)
+    ref, term = e * w * f, (e * w * f).abs()
+    err = (e * f).abs() * werr + (256 + 64 + 4 * v.abs().clamp_max(200)) * U * term + most * (e * w).abs()
+    over = [i for i in rows if k["gate"].shape[i] == 1]
+    if over:
+        ref, err = ref.sum(over, keepdim=True), err.sum(over, keepdim=True)
+    dtype = got["dgate"].dtype  # (the half step of a subnormal value is that of the smallest normal one)
+    close(got["dgate"], ref, half(dtype) * ref.abs().clamp_min(torch.finfo(dtype).tiny) + err, "dgate")
+
+
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("gate", ["full", "row", "batch"])
+@pytest.mark.parametrize("C", [40, 64, 99, 384, 1000])
+def test_gradients_of_gates_far_from_zero(types, gate, C):
+    """1 - q is taken without cancellation: gates from 5 to 30 and -5 to -30,
+    of each row and shared by a few rows and by many."""
+    for shape in ((2, 6, 40, C), (2, 5, 3, C)):
+        k = draw(shape, types, gate, pre=False, seed=60 + C, backward=True)
+        gen = torch.Generator().manual_seed(61)
+        values = torch.tensor([5.0, 8.0, 13.0, 17.0, 23.0, 30.0])
+        values = torch.cat([values, -values])
+        k["gate"] = values[torch.randint(0, 12, k["gate"].shape, generator=gen)].to(k["gate"].dtype)
+        _check_dgate(k, run_bwd(k, False))
+
+
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("gate", ["full", "row"])
+def test_gradients_of_gates_at_the_ends(types, gate):
+    """Gates whose sigmoid, or whose distance from 1, underflows: no NaN from
+    an exponential that overflows.  (Below 2^-126 fp32 and bf16 results may be
+    flushed to zero.)"""
+    k = draw((1, 6, 24, 64), types, gate, pre=False, seed=62, backward=True)
+    values = torch.tensor([float("inf"), 3e38, 100.0, 88.5, 88.0, 87.5, 87.0, 80.0])
+    values = torch.cat([values, -values])
+    gen = torch.Generator().manual_seed(63)
+    k["gate"] = values[torch.randint(0, 16, k["gate"].shape, generator=gen)].to(k["gate"].dtype)
+    got = run_bwd(k, False)
+    assert all(bool(torch.isfinite(t).all()) for t in got.values())
+    _check_dgate(k, got, most=2.0 ** -125)
