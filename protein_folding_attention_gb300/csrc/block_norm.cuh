@@ -1160,11 +1160,14 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
 // host side
 // ---------------------------------------------------------------------------
 // Resident CTAs of a kernel per SM times the SMs, looked up once per device
-// and CTA size; `most` is the shared memory of its largest CTA.
+// and number of lanes that share a row: a CTA's threads and shared memory
+// follow from it.  (From the threads alone the latter does not: fp32 rows of
+// 1001 and of 2047 channels both have 256, two and one CTAs per SM.)  `most` is
+// the shared memory of the kernel's largest CTA.
 template <typename K>
-cudaError_t resident_ctas(K kernel, int threads, size_t smem, size_t most,
+cudaError_t resident_ctas(K kernel, int lanes, int threads, size_t smem, size_t most,
                           std::atomic<int> (&cache)[64][17], int* n) {
-  const int key = threads / 32;
+  const int key = lanes % 32 ? lanes : lanes / 32;  // (a kernel has either kind)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1412,7 +1415,7 @@ cudaError_t launch_fwd(Plan pl, cudaStream_t st) {
   };
   const size_t smem = ring(pl.threads);
   int ctas = 0;
-  cudaError_t e = resident_ctas(kern, pl.threads, smem, ring(threads_of(G)), cache, &ctas);
+  cudaError_t e = resident_ctas(kern, pl.p.lanes, pl.threads, smem, ring(threads_of(G)), cache, &ctas);
   if (e != cudaSuccess) return e;
   // The CTAs are many and short (up to 8 turns), so that the rows that are in
   // flight lie close together: CTAs that walk the rows with a stride of the
@@ -1441,7 +1444,7 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
                           (RING ? Ring::bytes(T) : CHUNK ? chunk_bytes<TS, TI>(T, Q, 2, 3) : 0);
   static_assert(most <= 227 * 1024 - 2048, "shared memory");
   int ctas = 0;
-  cudaError_t e = resident_ctas(kern, pl.threads, smem, most, cache, &ctas);
+  cudaError_t e = resident_ctas(kern, p.lanes, pl.threads, smem, most, cache, &ctas);
   if (e != cudaSuccess) return e;
   ctas = std::min(ctas, kNormMaxCtas);
   unsigned need = (p.rows + pl.slots - 1) / pl.slots;

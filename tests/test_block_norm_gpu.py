@@ -696,3 +696,31 @@ def test_gradients_of_gates_at_the_ends(types, gate):
     got = run_bwd(k, False)
     assert all(bool(torch.isfinite(t).all()) for t in got.values())
     _check_dgate(k, got, most=2.0 ** -125)
+
+
+def test_sums_do_not_depend_on_earlier_calls():
+    """A process whose first call has other rows, of which fewer CTAs fit on an
+    SM, gives the same bits: fp32 rows of 1001 after rows of 2047 and the other
+    way round (both 256 threads, the latter with more shared memory)."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import hashlib, sys, torch
+from protein_folding_attention_gb300 import evoattn
+for C in map(int, sys.argv[1:]):
+    gen = torch.Generator(device="cuda").manual_seed(C)
+    dx1, dy, x1, u = (torch.randn(1, 1, 4000, C, device="cuda", generator=gen) for _ in range(4))
+    v = 1.0 + 0.1 * torch.randn(C, device="cuda", generator=gen)
+    out = evoattn.block_norm_bwd(dx1, dy, x1, u, None, v, v, v, v, v)
+print("bits", hashlib.sha256(b"".join(out[n].cpu().numpy().tobytes() for n in sorted(out))).hexdigest())
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+    def bits(*widths):
+        r = subprocess.run([sys.executable, "-c", code, *map(str, widths)], cwd=root, capture_output=True,
+                           text=True, timeout=300)
+        assert r.returncode == 0, r.stdout + r.stderr
+        return r.stdout.split("bits")[1].strip()
+    assert bits(2047, 1001) == bits(1001)
+    assert bits(1001, 2047) == bits(2047)
