@@ -318,6 +318,14 @@ def _allocate_on(stream):
     return _HERE_AND_NOW if stream is None else torch.cuda.stream(stream)
 
 
+def _used_on(stream, tensors):
+    """The memory of `tensors` (None among them) goes to nobody else before the
+    kernels enqueued on `stream` are done with it, whoever drops them."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _expanded(gate, shape):
     if gate is None or gate.shape == shape:
         return gate
@@ -563,6 +571,7 @@ class AdamW:
         written = sorted(w for w in written if w[1])
         if any(a + k > b for (a, k), (b, _) in zip(written, written[1:])):
             raise ValueError("parameters, copies and states overlap (is a tensor listed twice?)")
+        self._used = set()  # streams whose kernels read and write the rest
         self._starts, self._ends = [a for a, _ in written], [a + k for a, k in written]
         self._bind(self.grads)
         # evoattn_optim_state: step, norm, clip, skip, tickets
@@ -587,6 +596,7 @@ class AdamW:
         for row, g in zip(self._table, grads):  # all of them, or after an error none
             row.grad, row.grad_dtype = g.data_ptr(), _dtype_code(g)
         self.grads = grads
+        self._grads_used = set()  # streams whose kernels read them
 
     def step(self, max_norm=None, grads=None, stream=None):
         """One step.  max_norm: clip by the norm of all gradients, which is
@@ -598,14 +608,20 @@ class AdamW:
             self._bind(list(grads))
         lib, n = load(), len(self.params)
         st = _raw_stream(stream, self._index)
-        if stream is not None:  # not to be reused before that stream is done with them
-            for t in (self._state, self._workspace, self.exp_avg, self.exp_avg_sq,
-                      self.exp_avg_scale, self.exp_avg_sq_scale):
-                if t is not None:
-                    t.record_stream(stream)
+        if stream is not None:
+            # (once for each stream: a tensor's memory remembers it until it is freed)
+            if stream.cuda_stream not in self._used:
+                self._used.add(stream.cuda_stream)
+                _used_on(stream, (self._state, self._workspace, self.exp_avg, self.exp_avg_sq,
+                                  self.exp_avg_scale, self.exp_avg_sq_scale, *self.params, *self.copies))
+            if stream.cuda_stream not in self._grads_used:
+                self._grads_used.add(stream.cuda_stream)
+                _used_on(stream, self.grads)
         lr, lr_device = self.lr, None
         if isinstance(lr, torch.Tensor):
             _check_flat(lr, 1, torch.float32, self.device, "lr")
+            if stream is not None:
+                lr.record_stream(stream)
             lr, lr_device = 0.0, lr.data_ptr()
         state = self._state.data_ptr()
         if max_norm is not None:
