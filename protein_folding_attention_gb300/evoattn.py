@@ -386,6 +386,8 @@ def block_norm(x, u=None, gate=None, scale=None, gamma_post=None, beta_post=None
             words += y.stride()
         else:
             _add_rows(words, ((y, io, "y"),), shape, dev)
+    if stream is not None:
+        _used_on(stream, (x, u, gate, scale, gamma_post, beta_post, gamma_pre, beta_pre, x1, y))
     words += shape
     st = load().evoattn_block_norm_packed(
         _PACK_FWD(*words, _dtype_code(x), F32 if io is torch.float32 else BF16, kind, eps),
@@ -420,6 +422,8 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
     dev, sd, C = _on_device(lead), lead.dtype, shape[3]
     io = u.dtype if u is not None else dy.dtype
     if gate is not None and 0 in gate.stride():
+        if stream is not None:
+            _used_on(stream, (gate,))
         with _allocate_on(stream):  # an expanded view: each of its rows has its own gradient
             gate = gate.contiguous()
     full = gate if gate is None else _expanded(gate, shape)
@@ -464,6 +468,8 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
             raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
     if beta_pre is not None:
         _add_vectors([], ((beta_pre, "beta_pre"),), C, dev)
+    if stream is not None:
+        _used_on(stream, (dx1, dy, x1, u, gate, scale, gamma_post, beta_post, gamma_pre, dx, workspace))
     words += shape
     st = lib.evoattn_block_norm_bwd_packed(
         _PACK_BWD(*words, _dtype_code(lead), F32 if io is torch.float32 else BF16, kind, eps,
@@ -653,6 +659,8 @@ def grad_norm(grads, stream=None):
     with _allocate_on(stream):
         state = torch.zeros(8, device=dev, dtype=torch.int32)
         ws = torch.empty(lib.evoattn_grad_norm_workspace_size(len(grads)), device=dev, dtype=torch.uint8)
+    if stream is not None:
+        _used_on(stream, grads)
     _check(lib.evoattn_grad_norm(_grad_table(grads), len(grads), float("inf"), state.data_ptr(),
                                  ws.data_ptr(), ws.numel(), _raw_stream(stream, index)),
            "evoattn_grad_norm")
