@@ -525,6 +525,8 @@ class AdamW:
             raise ValueError("as many gradients and copies as parameters, at least one")
         if state_bits not in (32, 8):
             raise ValueError("state_bits is 32 or 8")
+        if step < 0:
+            raise ValueError("step: the number of steps already taken, not negative")
         decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
         if len(decay) != n:
             raise ValueError("one weight_decay, or one per parameter")

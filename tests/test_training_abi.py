@@ -187,3 +187,10 @@ def test_python_refuses_tensors_that_are_not_on_the_current_gpu():
         evoattn.grad_norm([torch.zeros(4)])
     with pytest.raises(ValueError):
         evoattn.grad_norm([])
+
+
+def test_a_negative_number_of_steps_taken_is_refused():
+    """(At step -1 the first bias correction would divide by zero.)"""
+    import torch
+    with pytest.raises(ValueError, match="steps already taken"):
+        evoattn.AdamW([torch.ones(3)], [torch.ones(3)], step=-1)
