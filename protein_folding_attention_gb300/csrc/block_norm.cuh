@@ -133,6 +133,7 @@ struct Params {
   // `seg_rows` rows each per gate row
   uint32_t share, segs, seg_rows, items;
   bool by_cta;       // an item's rows are spread over the CTA (else one group walks them)
+  bool in_step;      // the CTA's warps meet at every turn (see launch_bwd)
   float* gate_part;  // [items][C] where segs > 1
 };
 
@@ -848,8 +849,7 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
 
   constexpr bool RING = ring_of(G, VEC), CHUNK = !VEC && DENSE;
   constexpr bool STEP = RING && (!GROUPED || sizeof(TS) == 4) && G > 0 && G <= 32 && sizeof(TI) == 2;
-  // (shared gate rows: with an fp32 stream, and where the rows fill their lanes)
-  const bool in_step = STEP && (!GROUPED || C > 6 * g.lanes);
+  const bool in_step = STEP && (!GROUPED || p.in_step);
   float* const red = reinterpret_cast<float*>(smem);  // [slots][lanes * 8]
   // a thread's own 1 - q of a shared gate row, in the sums' place between them
   // (in registers it pushes others out)
@@ -979,8 +979,8 @@ __global__ void __launch_bounds__(threads_of(G), resident_bwd(G, sizeof(TI) == 4
       // The CTA's warps stay in step: left to themselves they drift apart and the
       // rows in flight with them (N = 768, bf16: 221 us so, 184 in step).  Not
       // where a row takes a warp of its own or several, nor for fp32 rows, where
-      // it costs more than it gives; with shared gate rows it gives with an fp32
-      // stream (N = 768, one gate row: 231 us, 206 in step).
+      // it costs more than it gives; with shared gate rows it may give with an
+      // fp32 stream, see launch_bwd.
       if (in_step) __syncthreads();
       if (CROSS) __syncwarp();  // the warp has read that stage
       if (ahead.left > 0) {
@@ -1473,6 +1473,12 @@ cudaError_t launch_bwd(Plan pl, float* ws, cudaStream_t st) {
         p.segs = (uint32_t)up(p.share, p.seg_rows);
       }
     }
+    // In step where a stretch has many turns and the rows fill their lanes
+    // (fp32 stream, us apart and in step: 589,824 rows of 128 with one gate row
+    // 227 and 205, with a gate row per 768, 48 turns, 224 and 222; a gate row
+    // per 512, 32 turns, 101 and 106, rows of 112 with one per 585 108 and 121;
+    // 196,608 rows of 192 with one per 512, lanes three quarters full, 133 and 136).
+    p.in_step = p.by_cta && p.seg_rows >= 48u * (uint32_t)pl.slots && p.C > 6 * p.lanes;
     p.items = gates * p.segs;
     need = p.by_cta ? p.items : (p.items + pl.slots - 1) / pl.slots;
   }
