@@ -381,7 +381,9 @@ evoattn_status evoattn_transition(const void* z, const void* o, const void* w_o,
  * Supported: (stream_dtype, dtype) = (BF16, BF16), (F32, BF16) or (F32, F32),
  * C <= 4096, B * I * J < 2^31 - 2^21 (otherwise EVOATTN_ERR_UNSUPPORTED).
  * Rows whose address and strides are multiples of 16 bytes and C % 8 == 0 run
- * at full speed; any others are read element by element.
+ * at full speed.  Rows of any other C that lie one behind the other from a
+ * 16-byte aligned address on are copied in 16-byte units, but computed with and
+ * stored element by element; any others are read element by element too.
  */
 typedef enum { EVOATTN_NORM_LAYER = 0, EVOATTN_NORM_RMS = 1 } evoattn_norm_kind;
 
@@ -472,6 +474,10 @@ evoattn_status evoattn_block_norm_bwd_packed(const int64_t* words, cudaStream_t 
  * sqrt(v) never gets the code 0 (it takes the smallest code instead), so the
  * quotient stays bounded; a block whose largest magnitude is below 2^-100 is
  * held as zeros.  The update itself uses m and v before they are rounded.
+ * In units of the scale a held value x is off by at most 2^-4 |x| from 2^-6 on
+ * and by 2^-10 below; a root below 2^-9 is held as 2^-9, however small it is.
+ * Without EVOATTN_ADAMW_CLIP an infinite gradient spoils its element with
+ * 32-bit states and its block's states with 8-bit ones.
  */
 #define EVOATTN_ADAMW_BLOCK 256
 #define EVOATTN_ADAMW_CLIP 1u /* flags: use the norm that evoattn_grad_norm left */
@@ -506,7 +512,8 @@ size_t evoattn_grad_norm_workspace_size(int count);
  * norm = sqrt(sum of g^2 over all elements of all tensors) into state->norm,
  * with the clipping coefficient and the skip flag beside it.  Sums have a
  * fixed order (the same bits every time) and are compensated or in fp64 where
- * they are long.  A sum of squares beyond the fp32 range counts as infinite.
+ * they are long.  A sum of squares beyond the fp32 range counts as infinite,
+ * and the squares of elements below 2^-63 lose bits (from 2^-75 down all).
  *
  *  tensors  : host array; only grad, n and grad_dtype are read.
  *  max_norm : > 0; INFINITY for the norm alone (clip = 1).

@@ -15,6 +15,7 @@
 //   D = dx1 + rstd (a - mean(a) - h mean(a h))             -> dx
 //   k = (u - mean) rstd        w = k gamma_post + beta_post,  q = s(gate)
 //   dscale = sum D q w         dgate = D scale w q (1 - q)    e = D scale q
+//                              (1 - q = e^-gate q, without cancellation)
 //   dgamma_post = sum e k      dbeta_post = sum e             b = e gamma_post
 //   du = rstd (b - mean(b) - k mean(b k))
 //   dgamma_pre = sum dy h      dbeta_pre = sum dy
@@ -27,7 +28,8 @@
 //
 // Layout: a row belongs to a group of G threads, 8 channels each, so that a
 // bf16 row is one 16-byte access per thread and its values stay in registers
-// from load to store.  G = 8, 16 or 32 lanes of a warp up to C = 256 (sums by
+// from load to store.  G = 8, 16 or 32 lanes of a warp up to C = 256, or for
+// narrow bf16 rows as many lanes as they have parts (sums by
 // shuffles); a warp with two such parts per lane up to C = 512; above that
 // several warps (sums by shuffles, then through shared memory with one named
 // barrier per sum).  The forward's CTAs are many and short, the backward's

@@ -202,7 +202,7 @@ __device__ __forceinline__ float2 warp_max(float2 v) {
 __device__ __forceinline__ int element(int lane, int k) { return (k >> 2) * 128 + 4 * lane + (k & 3); }
 
 // A warp's stage of the ring: p, g (bf16 in the first half), then m and v,
-// and with 8 bits their scales.  16 warps per SM in flight.
+// and with 8 bits their scales.
 template <bool BITS8>
 struct Ring {
   static constexpr uint32_t G = 1024, M = 2048, V = M + (BITS8 ? 256 : 1024);

@@ -351,8 +351,11 @@ def block_norm(x, u=None, gate=None, scale=None, gamma_post=None, beta_post=None
     norm before a block alone (x1 is x), with pre=False the norm after a block
     alone (y is None).  y has u's type; y_dtype names it where there is no u
     (default: x's).  Outputs take x's layout; x1=x updates the stream in place.
-    Everything is enqueued on, and allocated for, `stream` (default: the
-    current one).  Returns (x1, y)."""
+    No autograd node is made, whether inputs require gradients or not: the
+    gradients are block_norm_bwd's.  Everything is enqueued on, and allocated
+    for, `stream` (default: the current one); operands may be dropped after
+    the call, but the caller orders `stream` behind the work that writes them.
+    Returns (x1, y)."""
     shape = x.shape
     if len(shape) != 4:
         raise ValueError("x must be [B, I, J, C]")
@@ -406,7 +409,7 @@ def block_norm_bwd(dx1, dy=None, x1=None, u=None, gate=None, scale=None, gamma_p
     returned it (needed with dy); the rest as in the forward.  dx=dx1 works in
     place.  Returns a dict with dx (dx1 itself without dy), du, dgate (in the
     gate's own shape), and fp32 dscale, dgamma_post, dbeta_post, dgamma_pre,
-    dbeta_pre of the parameters that were given."""
+    dbeta_pre of the parameters that were given.  `stream` as in block_norm."""
     lead = dx1 if dx1 is not None else x1
     if lead is None or (dy is None and (u is None or dx1 is None)):
         raise ValueError("dx1 with u, or dy with x1, is needed")
@@ -513,6 +516,11 @@ class AdamW:
     optimiser is used on one stream at a time.  The tensors' addresses are
     taken here (the gradients' by step(grads=...) too): none of them may be
     given other memory (`p.data = ...`) afterwards.
+
+    One optimiser has one learning rate, and clips by the norm of its own
+    gradients only.  The gradients' buffers exist when it is made.  A step
+    changes the parameters without autograd's knowledge: a graph recorded
+    before it must not be walked backwards after it.
     """
 
     def __init__(self, params, grads, *, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
@@ -610,7 +618,10 @@ class AdamW:
         """One step.  max_norm: clip by the norm of all gradients, which is
         returned (the tensor `norm`, overwritten by the next such step); a step
         whose norm is infinite or NaN then changes nothing.  grads: gradients
-        to use from now on instead of those bound before."""
+        to use from now on instead of those bound before.  Everything is
+        enqueued on `stream` (default: the current one); gradients that a
+        later step replaces may be dropped, but the caller orders `stream`
+        behind the work that writes parameters, states and gradients."""
         _on_device(self._state)
         if grads is not None:
             self._bind(list(grads))
@@ -648,7 +659,8 @@ class AdamW:
 
 def grad_norm(grads, stream=None):
     """sqrt of the sum of squares of all elements of the bf16 or fp32 tensors
-    `grads` (contiguous), as a 0-dim fp32 tensor (see evoattn_grad_norm)."""
+    `grads` (contiguous), as a 0-dim fp32 tensor (see evoattn_grad_norm).
+    `stream` as in block_norm."""
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
