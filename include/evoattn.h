@@ -546,6 +546,170 @@ evoattn_status evoattn_adamw(const evoattn_adamw_tensor* tensors, int count, flo
                              cudaStream_t stream);
 
 /*
+ * The 8-bit projection path around a block of a pre-norm stack (no counterpart
+ * in the MegaFold pages beyond the layer normalisation and the linear
+ * projections of "Methodik" section 3 "EvoFusion", whose 8-bit form this is):
+ * the residual add with dropout, the norm whose output is e4m3 codes with a
+ * scale for each EVOATTN_GROUP8 channels, the quantisation of any matrix, and
+ * the product of two such matrices.  Arguments come in a struct of 64-bit
+ * fields, read before the call returns; fields that do not apply are 0.
+ *
+ * Codes and scales: a group of 128 consecutive elements of a row (the last group
+ * may be shorter) has the scale s = 2^k, the smallest power of two with
+ * max|x| <= 448 s (k >= -127; s = 1 for zeros), stored as the byte k + 127 (E8M0);
+ * its codes are e4m3(x / s), rounded to nearest even: off by at most 2^-4 |x|
+ * where |x / s| >= 2^-6 and by 2^-10 s below.  An infinite or NaN element has no
+ * part in the maximum and takes the NaN code.
+ *
+ * Dropout: keep * u / (1 - p), where an element's keep is a function of
+ * (seed, step, site) and its place: word c % 4 of the Philox4x32-10 block with
+ * the counter (c / 4, mask row, site, step mod 2^32) and the key seed, at or
+ * above round(p 2^32), for channel c.  The mask row is the row's index over the
+ * axes that are not in `shared` (bit 0: B, 1: I, 2: J).  No mask is stored: a
+ * backward pass with the same (seed, step, site) draws it again.
+ */
+#define EVOATTN_GROUP8 128
+
+typedef struct {       /* [B, I, J, C] rows */
+    void* p;           /* device; NULL: not given */
+    int64_t s[4];      /* element strides {b, i, j, c}, as in evoattn_block_norm */
+} evoattn_rows;
+
+typedef struct {
+    const int64_t* rng; /* device: seed, step (a captured call follows them); NULL with p = 0 */
+    double p;           /* in [0, 1) */
+    int64_t site;       /* 0 .. 2^32 - 1: tells the calls of one step apart */
+    int64_t shared;     /* axes along which rows share a mask row */
+} evoattn_dropout;
+
+/*
+ * out = x + keep * u / (1 - p); without x: out = keep * u / (1 - p), which is also
+ * the gradient of u for u = the gradient of out.
+ *
+ *  x, out : `stream_dtype`; u: `dtype`.  All four pairs of types.  out may be x
+ *           or u itself (same address, strides and type).
+ */
+typedef struct {
+    evoattn_rows x, u, out;
+    evoattn_dropout drop;
+    int64_t n[4];       /* B, I, J, C */
+    int64_t stream_dtype, dtype;
+} evoattn_dropout_add_args;
+evoattn_status evoattn_dropout_add(const evoattn_dropout_add_args* args, cudaStream_t stream);
+
+/*
+ *   x1 = x + keep * u / (1 - p)
+ *   y  = n(x1) * gamma + beta     (n as in evoattn_block_norm, of x1 in fp32)
+ *   codes, scales: y in groups of 128 channels
+ *
+ *  x, x1  : `stream_dtype`; u: `dtype`.  Types and sizes as in evoattn_block_norm.
+ *           Without u: x1 and the dropout are not given either (x1 is x).
+ *           x1 may be x itself.
+ *  codes  : e4m3, strides as of an output (c stride 1).
+ *  scales : bytes, [B, I, J, ceil(C / 128)], any strides without overlap.
+ *  gamma, beta : [C] fp32 or NULL (1 and 0).
+ */
+typedef struct {
+    evoattn_rows x, u, x1, codes, scales;
+    const float *gamma, *beta;
+    evoattn_dropout drop;
+    double eps;
+    int64_t n[4];
+    int64_t stream_dtype, dtype, kind;
+} evoattn_norm8_args;
+evoattn_status evoattn_norm8(const evoattn_norm8_args* args, cudaStream_t stream);
+
+/* Bytes of device workspace evoattn_norm8_bwd needs (0 for a C outside 1..4096). */
+size_t evoattn_norm8_bwd_workspace_size(int C);
+
+/*
+ * Gradients of evoattn_norm8, y's taken as of the unrounded y:
+ *
+ *   dx = dx1 + (gradient of y through the norm at x1)     du = keep * dx / (1 - p)
+ *
+ *  dx1   : `stream_dtype`, gradient of x1 from what else reads the stream, or NULL.
+ *  dy    : `dtype`.   x1: `stream_dtype`, as the forward stored it.
+ *  dx    : `stream_dtype`, written; may be dx1 itself.
+ *  du    : `dtype`, written (of dx in fp32); NULL for a forward without u.
+ *  dgamma, dbeta : [C] fp32, written; each may be NULL.
+ *  workspace : as for evoattn_block_norm_bwd.
+ * Sums have a fixed order: repeated calls give the same bits.
+ */
+typedef struct {
+    evoattn_rows dx1, dy, x1, dx, du;
+    const float* gamma;
+    float *dgamma, *dbeta;
+    evoattn_dropout drop;
+    double eps;
+    int64_t n[4];
+    int64_t stream_dtype, dtype, kind;
+    void* workspace;
+    int64_t workspace_bytes;
+} evoattn_norm8_bwd_args;
+evoattn_status evoattn_norm8_bwd(const evoattn_norm8_bwd_args* args, cudaStream_t stream);
+
+/*
+ * x [R, K] in codes and scales.
+ *
+ *  x       : `dtype`, row stride ld, columns contiguous.
+ *  codes   : [R, K], groups along the columns, with scales [R, ceil(K / 128)]
+ *            at r * s_row + g * s_group; or NULL.
+ *  codes_t : [K, R], x transposed, groups along its rows, with scales_t
+ *            [K, ceil(R / 128)] at k * st_row + g * st_group; or NULL.
+ *  blocks  : nonzero: one scale per 128 x 128 block for both, scales
+ *            [ceil(R / 128), ceil(K / 128)]; scales_t is then NULL.
+ *  Codes are 16-byte aligned with row strides that are multiples of 16
+ *  (otherwise EVOATTN_ERR_ALIGNMENT); bytes behind a row's end are not written.
+ */
+typedef struct {
+    const void* x;
+    int64_t R, K, ld, dtype, blocks;
+    void* codes;
+    int64_t ldc;
+    uint8_t* scales;
+    int64_t s_row, s_group;
+    void* codes_t;
+    int64_t ldt;
+    uint8_t* scales_t;
+    int64_t st_row, st_group;
+} evoattn_quantize8_args;
+evoattn_status evoattn_quantize8(const evoattn_quantize8_args* args, cudaStream_t stream);
+
+/* Bytes of device workspace evoattn_matmul8 needs on the current device (0: none). */
+size_t evoattn_matmul8_workspace_size(int M, int N, int K);
+
+/*
+ * out[m, n] = sum_k a[m, k] b[n, k] (+ add[m, n]), fp32 sums in a fixed order,
+ * rounded once.
+ *
+ *  a, b   : codes [M, K] and [N, K] (16-byte aligned, row strides multiples of
+ *           16) with scales at (row / rows_per_scale) * s_row + (k / 128) * s_group;
+ *           rows_per_scale is 1 or 128.
+ *  out    : [M, N], `dtype`, row stride ld_out.
+ *  add    : `dtype`, row stride ld_add (0: one row for all), or NULL; may be out
+ *           itself.  out overlaps no other operand.
+ *  workspace : 256-byte aligned, at least evoattn_matmul8_workspace_size bytes;
+ *           NULL where that is 0.
+ */
+typedef struct {
+    const void* codes;
+    int64_t ld;
+    const uint8_t* scales;
+    int64_t s_row, s_group, rows_per_scale;
+} evoattn_operand8;
+typedef struct {
+    evoattn_operand8 a, b;
+    int64_t M, N, K;
+    void* out;
+    int64_t ld_out;
+    const void* add;
+    int64_t ld_add, dtype;
+    void* workspace;
+    int64_t workspace_bytes;
+} evoattn_matmul8_args;
+evoattn_status evoattn_matmul8(const evoattn_matmul8_args* args, cudaStream_t stream);
+
+/*
  * Testing hook for the bounded-wait failure path; not needed in normal use.
  * Applies to every tcgen05 kernel enqueued after the call, on any device, by
  * any thread of the process.

@@ -18,7 +18,9 @@ LIB = os.path.join(HERE, "libevoattn.so")
 
 SOURCES = ["evoattn_api.cu", "simt_f32.cu", "tmap.cu", "fwd_sm103.cu", "bwd_sm103.cu",
            "fusion_sm103.cu", "transition_sm103.cu", "evoattn_noalloc.cu", "block_norm_bf16.cu",
-           "block_norm_mixed.cu", "block_norm_f32.cu", "optim.cu", "training_api.cu"]
+           "block_norm_mixed.cu", "block_norm_f32.cu", "optim.cu", "training_api.cu",
+           "norm8_bf16.cu", "norm8_mixed.cu", "norm8_f32.cu", "quantize8.cu", "matmul8_sm103.cu",
+           "eightbit_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + INCLUDE, "-I" + CSRC]

@@ -109,6 +109,14 @@ bool bf16_ok_bias(const void* p, const int64_t* s) {
 evoattn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? EVOATTN_OK : EVOATTN_ERR_CUDA; }
 
 }  // namespace
+
+bool wait_config(WaitCfg* w) {
+  bool ok = false;
+  unsigned int* status = status_word(&ok);
+  if (ok) *w = wait_base(status);
+  return ok;
+}
+
 }  // namespace evo
 
 using namespace evo;

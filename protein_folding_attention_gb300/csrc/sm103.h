@@ -20,6 +20,10 @@ struct Bf16Ptrs {
 // A fresh id for the next kernel launch (never 0).
 unsigned int next_launch_id();
 
+// The wait configuration of the next launches on the current device (false:
+// the device's status words cannot be reached).
+bool wait_config(WaitCfg* w);
+
 // The wait configuration of one launch: `base` with a fresh launch id.
 inline WaitCfg launch_wait(const WaitCfg& base) {
   WaitCfg c = base;

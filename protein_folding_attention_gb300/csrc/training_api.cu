@@ -13,83 +13,10 @@
 #include "block_norm.h"
 #include "evoattn.h"
 #include "optim.h"
+#include "row_checks.h"
 
 namespace evo {
 namespace {
-
-// One [B, I, J, C] operand as the caller gave it.
-struct Rows4 {
-  const void* p;
-  const int64_t* s;
-  evoattn_dtype dtype;
-  bool output;
-};
-
-bool all_null(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (p) return false;
-  return true;
-}
-
-evoattn_status check_sizes(int B, int I, int J, int C, evoattn_dtype sd, evoattn_dtype d,
-                           evoattn_norm_kind kind, float eps) {
-  if (B < 1 || I < 1 || J < 1 || C < 1) return EVOATTN_ERR_INVALID_ARG;
-  if (kind != EVOATTN_NORM_LAYER && kind != EVOATTN_NORM_RMS) return EVOATTN_ERR_INVALID_ARG;
-  if (!(eps > 0.f) || !(eps < INFINITY)) return EVOATTN_ERR_INVALID_ARG;
-  const bool pair = (sd == EVOATTN_BF16 && d == EVOATTN_BF16) ||
-                    (sd == EVOATTN_F32 && (d == EVOATTN_BF16 || d == EVOATTN_F32));
-  if (!pair || C > kNormMaxC) return EVOATTN_ERR_UNSUPPORTED;
-  const uint64_t limit = 0x7FFFFFFFull - (1u << 21);
-  const uint64_t bi = (uint64_t)B * (uint64_t)I;  // < 2^62
-  if (bi > limit || bi * (uint64_t)J > limit) return EVOATTN_ERR_UNSUPPORTED;
-  return EVOATTN_OK;
-}
-
-// Strides and alignment of the operands that are given; rows of an output may
-// not overlap, but for the axes along which `shared` (the gate) repeats one.
-evoattn_status check_rows(std::initializer_list<Rows4> ops, const int (&n)[3], int C,
-                          const int64_t* shared) {
-  for (const Rows4& o : ops)
-    if (o.p && !o.s) return EVOATTN_ERR_INVALID_ARG;
-  for (const Rows4& o : ops) {
-    if (!o.p) continue;
-    for (int k = 0; k < 3; ++k) {
-      if (n[k] == 1) continue;
-      // (a span that fits 62 bits: no address computation overflows)
-      if (o.s[k] < 0 || o.s[k] > (int64_t)1 << 58 || (__int128)o.s[k] * n[k] > (__int128)1 << 58)
-        return EVOATTN_ERR_INVALID_ARG;
-    }
-    if (!o.output) continue;
-    int axis[3], m = 0;
-    for (int k = 0; k < 3; ++k)
-      if (n[k] > 1 && !(shared && shared[k] == 0)) axis[m++] = k;
-    std::sort(axis, axis + m, [&](int a, int b) { return o.s[a] < o.s[b]; });
-    int64_t span = C;  // elements that the faster axes reach over
-    for (int k = 0; k < m; ++k) {
-      if (o.s[axis[k]] < span) return EVOATTN_ERR_INVALID_ARG;
-      span += o.s[axis[k]] * (int64_t)(n[axis[k]] - 1);
-    }
-  }
-  for (const Rows4& o : ops) {
-    if (!o.p) continue;
-    if (C > 1 && o.s[3] != 1) return EVOATTN_ERR_ALIGNMENT;
-    if (reinterpret_cast<uintptr_t>(o.p) % (o.dtype == EVOATTN_BF16 ? 2 : 4)) return EVOATTN_ERR_ALIGNMENT;
-  }
-  return EVOATTN_OK;
-}
-
-bool floats_aligned(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (reinterpret_cast<uintptr_t>(p) % 4) return false;
-  return true;
-}
-
-RowOperand operand(const void* p, const int64_t* s) {
-  RowOperand r{const_cast<void*>(p), {0, 0, 0}};
-  if (p)
-    for (int k = 0; k < 3; ++k) r.s[k] = s[k];
-  return r;
-}
 
 // Reads the arguments of a packed call one after another.
 class Words {
@@ -124,8 +51,6 @@ class Words {
   bool fits_ = true;
 };
 
-evoattn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? EVOATTN_OK : EVOATTN_ERR_CUDA; }
-
 }  // namespace
 }  // namespace evo
 
@@ -148,9 +73,9 @@ evoattn_status evoattn_block_norm(const void* x, const int64_t x_strides[4], con
   evoattn_status st = check_sizes(B, I, J, C, stream_dtype, dtype, kind, eps);
   if (st != EVOATTN_OK) return st;
   const int n[3] = {B, I, J};
-  st = check_rows({{x, x_strides, stream_dtype, false}, {u, u_strides, dtype, false},
-                   {gate, gate_strides, dtype, false}, {x1, x1_strides, stream_dtype, true},
-                   {y, y_strides, dtype, true}}, n, C, nullptr);
+  st = check_rows({{x, x_strides, bytes_of(stream_dtype), false}, {u, u_strides, bytes_of(dtype), false},
+                   {gate, gate_strides, bytes_of(dtype), false}, {x1, x1_strides, bytes_of(stream_dtype), true},
+                   {y, y_strides, bytes_of(dtype), true}}, n, C, nullptr);
   if (st != EVOATTN_OK) return st;
   if (!floats_aligned({scale, gamma_post, beta_post, gamma_pre, beta_pre})) return EVOATTN_ERR_ALIGNMENT;
   BlockNormCall c{};
@@ -192,13 +117,13 @@ evoattn_status evoattn_block_norm_bwd(
   evoattn_status st = check_sizes(B, I, J, C, stream_dtype, dtype, kind, eps);
   if (st != EVOATTN_OK) return st;
   const int n[3] = {B, I, J};
-  st = check_rows({{dx1, dx1_strides, stream_dtype, false}, {dy, dy_strides, dtype, false},
-                   {x1, x1_strides, stream_dtype, false}, {u, u_strides, dtype, false},
-                   {gate, gate_strides, dtype, false}, {dx, dx_strides, stream_dtype, true},
-                   {du, du_strides, dtype, true}}, n, C, nullptr);
+  st = check_rows({{dx1, dx1_strides, bytes_of(stream_dtype), false}, {dy, dy_strides, bytes_of(dtype), false},
+                   {x1, x1_strides, bytes_of(stream_dtype), false}, {u, u_strides, bytes_of(dtype), false},
+                   {gate, gate_strides, bytes_of(dtype), false}, {dx, dx_strides, bytes_of(stream_dtype), true},
+                   {du, du_strides, bytes_of(dtype), true}}, n, C, nullptr);
   if (st != EVOATTN_OK) return st;
   if (gate) {  // the gate's gradient repeats exactly the rows that the gate repeats
-    st = check_rows({{dgate, dgate_strides, dtype, true}}, n, C, gate_strides);
+    st = check_rows({{dgate, dgate_strides, bytes_of(dtype), true}}, n, C, gate_strides);
     if (st != EVOATTN_OK) return st;
     for (int k = 0; k < 3; ++k)
       if (n[k] > 1 && (gate_strides[k] == 0) != (dgate_strides[k] == 0)) return EVOATTN_ERR_INVALID_ARG;

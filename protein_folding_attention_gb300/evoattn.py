@@ -11,6 +11,7 @@ from __future__ import annotations
 import bisect
 import contextlib
 import ctypes
+import functools
 import os
 import struct
 
@@ -27,6 +28,7 @@ DBIAS_FUSED = 4  # dbias summed in the dK/dV pass (fp32 atomics)
 NORM_LAYER, NORM_RMS = 0, 1
 ADAMW_BLOCK = 256  # elements that share a scale in the 8-bit states
 ADAMW_CLIP = 1
+GROUP8 = 128  # elements that share a scale in 8-bit matrices
 
 _lib = None
 _I64_5 = ctypes.c_int64 * 5
@@ -101,6 +103,13 @@ def load(path: str = LIB_PATH):
     lib.evoattn_grad_norm.restype = i
     lib.evoattn_adamw.argtypes = [ctypes.POINTER(AdamwTensor), i, f, vp, d, d, f, i, u, vp, vp]
     lib.evoattn_adamw.restype = i
+    for name in ("dropout_add", "norm8", "norm8_bwd", "quantize8", "matmul8"):
+        call = getattr(lib, "evoattn_" + name)
+        call.argtypes, call.restype = [ctypes.c_char_p, vp], i
+    lib.evoattn_norm8_bwd_workspace_size.argtypes = [i]
+    lib.evoattn_norm8_bwd_workspace_size.restype = sz
+    lib.evoattn_matmul8_workspace_size.argtypes = [i, i, i]
+    lib.evoattn_matmul8_workspace_size.restype = sz
     lib.evoattn_debug_set_wait.argtypes = [ctypes.c_ulonglong, i]
     lib.evoattn_debug_set_wait.restype = i
     _lib = lib
@@ -679,6 +688,335 @@ def grad_norm(grads, stream=None):
                                  ws.data_ptr(), ws.numel(), _raw_stream(stream, index)),
            "evoattn_grad_norm")
     return state[2:3].view(torch.float32)[0]
+
+
+_PACK_DROPOUT = struct.Struct("=16qd8q").pack
+_PACK_NORM8 = struct.Struct("=28qd2qd7q").pack
+_PACK_NORM8_BWD = struct.Struct("=29qd2qd9q").pack
+_PACK_QUANTIZE8 = struct.Struct("=16q").pack
+_PACK_MATMUL8 = struct.Struct("=22q").pack
+
+
+def _dropout(p, rng, site, shared, index):
+    """The fields of evoattn_dropout."""
+    mask = 0
+    for axis in shared:
+        if not 0 <= axis <= 2:
+            raise ValueError("shared: row axes, 0 to 2")
+        mask |= 1 << axis
+    if p == 0.0:
+        return 0, 0.0, site, mask
+    if rng is None or rng.dtype is not torch.int64 or rng.shape != (2,) or rng.get_device() != index or \
+            not rng.is_contiguous():
+        raise ValueError(f"rng: expected a contiguous int64 tensor (seed, step) on cuda:{index}")
+    return rng.data_ptr(), p, site, mask
+
+
+def dropout_add(u, p, rng, x=None, site=0, shared=(), out=None, out_dtype=None, stream=None):
+    """out = x + keep * u / (1 - p), or without x keep * u / (1 - p) (see
+    evoattn_dropout_add).  u, x [B, I, J, C], each bf16 or fp32, any strides
+    with unit stride along C.  rng: an int64 CUDA tensor (seed, step), read by
+    the kernel (a captured call follows it); site: a number that tells the
+    calls of one step apart; shared: row axes (0 to 2) along which all rows
+    have the same mask.  The mask is a function of these and of an element's
+    place; it is stored nowhere: the gradient of u is
+    dropout_add(dout, p, rng, site=site, shared=shared, out_dtype=u.dtype).
+    out has x's type and layout (without x: out_dtype, by default u's) and may
+    be x or u itself.  `stream` as in block_norm, and like there no autograd
+    node is made."""
+    shape = u.shape
+    if len(shape) != 4:
+        raise ValueError("u must be [B, I, J, C]")
+    dev, io = _on_device(u), u.dtype
+    sd = x.dtype if x is not None else out.dtype if out is not None else out_dtype or io
+    if out_dtype is not None and out_dtype is not sd:
+        raise ValueError("out has the type of x")
+    drop = _dropout(p, rng, site, shared, dev)
+    words = []
+    _add_rows(words, ((x, sd, "x"), (u, io, "u")), shape, dev)
+    if out is None:
+        with _allocate_on(stream):
+            out = torch.empty_like(u if x is None else x, dtype=sd)
+        words.append(out.data_ptr())
+        words += out.stride()
+    else:
+        _add_rows(words, ((out, sd, "out"),), shape, dev)
+    if stream is not None:
+        _used_on(stream, (x, u, out, rng if p else None))
+    codes = _dtype_code(out), _dtype_code(u)
+    st = load().evoattn_dropout_add(_PACK_DROPOUT(*words, *drop, *shape, *codes), _raw_stream(stream, dev))
+    if st != OK:
+        _check(st, "evoattn_dropout_add")
+    return out
+
+
+def _codes8(lead, cols, device):
+    """Codes [*lead, cols] whose rows start at multiples of 16 bytes."""
+    ld = -(-cols // 16) * 16
+    t = torch.empty((*lead, ld), device=device, dtype=torch.float8_e4m3fn)
+    return t if ld == cols else t[..., :cols]
+
+
+def _scales8(lead, cols, rows, device):
+    """Scales of [*lead, cols] by groups of the last axis, the rows innermost
+    in memory."""
+    strides, at = [rows], 1
+    for n in reversed(lead):
+        strides.insert(0, at)
+        at *= n
+    return torch.empty_strided((*lead, -(-cols // GROUP8)), strides, device=device, dtype=torch.float8_e8m0fnu)
+
+
+def _matrix(t, name):
+    """(rows, row stride) of [..., cols] taken as a matrix with contiguous rows."""
+    rows, ld = 1, None
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n != 1:
+            if ld is None:
+                ld = s
+            elif s != ld * rows:
+                raise ValueError(f"{name}: the leading axes do not form one row axis")
+            rows *= n
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis is not contiguous")
+    return rows, -(-t.shape[-1] // 16) * 16 if ld is None else ld
+
+
+def norm8(x, u=None, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0.0, rng=None, site=0,
+          shared=(), x1=None, stream=None):
+    """The residual add with dropout and the norm before a block whose
+    projections run in 8 bits (see evoattn_norm8):
+
+        x1 = x + keep * u / (1 - p)
+        y  = n(x1) * gamma + beta
+
+    Returns (x1, codes, scales): y [B, I, J, C] as torch.float8_e4m3fn codes,
+    dense but for rows that start at multiples of 16 bytes, and its scales
+    [B, I, J, ceil(C / 128)] as torch.float8_e8m0fnu: what matmul8 takes.
+    Types, strides, kind, eps and stream as in block_norm; p, rng, site and
+    shared as in dropout_add.  Without u x1 is x; x1=x updates the stream in
+    place."""
+    shape = x.shape
+    if len(shape) != 4:
+        raise ValueError("x must be [B, I, J, C]")
+    dev, sd = _on_device(x), x.dtype
+    io = u.dtype if u is not None else sd
+    if x1 is not None and u is None:
+        raise ValueError("x1 without u")
+    drop = _dropout(p, rng, site, shared, dev)
+    words = []
+    _add_rows(words, ((x, sd, "x"), (u, io, "u")), shape, dev)
+    B, I, J, C = shape
+    with _allocate_on(stream):
+        if u is None:
+            x1 = x
+            words += _NO_ROWS
+        elif x1 is None:
+            x1 = torch.empty_like(x)
+            words.append(x1.data_ptr())
+            words += x1.stride()
+        else:
+            _add_rows(words, ((x1, sd, "x1"),), shape, dev)
+        codes = _codes8((B, I, J), C, x.device)
+        scales = _scales8((B, I, J), C, B * I * J, x.device)
+    for t in (codes, scales):
+        words.append(t.data_ptr())
+        words += t.stride()
+    _add_vectors(words, ((gamma, "gamma"), (beta, "beta")), C, dev)
+    if stream is not None:
+        _used_on(stream, (x, u, x1, gamma, beta, codes, scales, rng if p else None))
+    st = load().evoattn_norm8(
+        _PACK_NORM8(*words, *drop, eps, *shape, _dtype_code(x), F32 if io is torch.float32 else BF16, kind),
+        _raw_stream(stream, dev))
+    if st != OK:
+        _check(st, "evoattn_norm8")
+    return x1, codes, scales
+
+
+def norm8_bwd(dx1, dy, x1, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0.0, rng=None, site=0,
+              shared=(), branch=True, dx=None, workspace=None, stream=None):
+    """Gradients of norm8, the rounding of y passed through (see
+    evoattn_norm8_bwd).  dx1: the gradient of x1 from what else reads the
+    stream (None for zero); dy: the gradient of y; x1: the stream as the forward
+    returned it; branch: whether the forward had u; the rest as in the forward.
+    dx=dx1 works in place.  Returns a dict with dx, du (with `branch`; in dy's
+    type), and fp32 dgamma and dbeta of the parameters that were given."""
+    shape = x1.shape
+    if len(shape) != 4:
+        raise ValueError("x1 must be [B, I, J, C]")
+    dev, sd, io, C = _on_device(x1), x1.dtype, dy.dtype, shape[3]
+    drop = _dropout(p, rng, site, shared, dev)
+    words, out = [], {}
+    _add_rows(words, ((dx1, sd, "dx1"), (dy, io, "dy"), (x1, sd, "x1")), shape, dev)
+    lib = load()
+    with _allocate_on(stream):
+        if dx is None:
+            dx = torch.empty_like(x1)
+        out["dx"] = dx
+        if branch:
+            out["du"] = torch.empty_like(dy)
+        _add_rows(words, ((dx, sd, "dx"), (out.get("du"), io, "du")), shape, dev)
+        _add_vectors(words, ((gamma, "gamma"),), C, dev)
+        _add_vectors([], ((beta, "beta"),), C, dev)
+        for name, t in (("dgamma", gamma), ("dbeta", beta)):
+            if t is None:
+                words.append(0)
+            else:
+                out[name] = t = torch.empty_like(t)
+                words.append(t.data_ptr())
+        if workspace is None:
+            workspace = torch.empty(lib.evoattn_norm8_bwd_workspace_size(C), device=x1.device, dtype=torch.uint8)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
+    if stream is not None:
+        _used_on(stream, (dx1, dy, x1, gamma, dx, workspace, rng if p else None))
+    st = lib.evoattn_norm8_bwd(
+        _PACK_NORM8_BWD(*words, *drop, eps, *shape, _dtype_code(x1), F32 if io is torch.float32 else BF16,
+                        kind, workspace.data_ptr(), workspace.numel() * workspace.element_size()),
+        _raw_stream(stream, dev))
+    if st != OK:
+        _check(st, "evoattn_norm8_bwd")
+    return out
+
+
+def quantize8(x, rows=True, cols=False, blocks=False, stream=None):
+    """x [..., K] (bf16 or fp32, the leading axes taken as R rows) in e4m3 codes
+    with a power-of-two scale for each 128 elements (see evoattn_quantize8):
+
+      rows  codes [..., K] and scales [..., ceil(K / 128)], groups along K
+      cols  codes_t [K, R] and scales_t [K, ceil(R / 128)]: x transposed,
+            groups along its rows (for a product that sums over them)
+
+    With blocks one scale per 128 x 128 block serves both: scales
+    [ceil(R / 128), ceil(K / 128)] and its transpose (a weight, for a layer's
+    output and its input's gradient).  Returns (codes, scales), (codes_t,
+    scales_t) or all four.  Codes are torch.float8_e4m3fn with rows at
+    multiples of 16 bytes, scales torch.float8_e8m0fnu.  `stream` as in
+    block_norm."""
+    if not (rows or cols):
+        raise ValueError("rows, cols or both")
+    if x.dim() < 1:
+        raise ValueError("x must have a last axis")
+    dev, code = _on_device(x), _dtype_code(x)
+    R, ld = _matrix(x, "x")
+    lead, K, device = tuple(x.shape[:-1]), x.shape[-1], x.device
+    q = s = qt = t = None
+    with _allocate_on(stream):
+        if blocks:
+            s = torch.empty((-(-R // GROUP8), -(-K // GROUP8)), device=device, dtype=torch.float8_e8m0fnu)
+        if rows:
+            q = _codes8(lead, K, device)
+            if not blocks:
+                s = _scales8(lead, K, R, device)
+        if cols:
+            qt = _codes8((K,), R, device)
+            if not blocks:
+                t = _scales8((K,), R, K, device)
+    words = [x.data_ptr(), R, K, ld, code, blocks]
+    if q is None:
+        words += (0, 0)
+    else:
+        words += (q.data_ptr(), -(-K // 16) * 16)
+    if s is None:
+        words += (0, 0, 0)
+    elif blocks:
+        words += (s.data_ptr(), *s.stride())
+    else:
+        words += (s.data_ptr(), 1, R)
+    words += (0, 0) if qt is None else (qt.data_ptr(), qt.stride(0))
+    words += (0, 0, 0) if t is None else (t.data_ptr(), *t.stride())
+    if stream is not None:
+        _used_on(stream, (x,))
+    st = load().evoattn_quantize8(_PACK_QUANTIZE8(*words), _raw_stream(stream, dev))
+    if st != OK:
+        _check(st, "evoattn_quantize8")
+    if blocks:
+        t = s.t()
+    return (*((q, s) if rows else ()), *((qt, t) if cols else ()))
+
+
+def _operand8(codes, scales, name, index):
+    """The fields of evoattn_operand8, and the rows."""
+    if codes.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float8_e8m0fnu or \
+            codes.get_device() != index or scales.get_device() != index:
+        raise ValueError(f"{name}: expected float8_e4m3fn codes with float8_e8m0fnu scales on cuda:{index}")
+    rows, ld = _matrix(codes, name)
+    groups = -(-codes.shape[-1] // GROUP8)
+    if scales.shape == (*codes.shape[:-1], groups):
+        per, sr = 1, 0
+        n = 1
+        for size, stride in zip(reversed(scales.shape[:-1]), reversed(scales.stride()[:-1])):
+            if size != 1:
+                if n == 1:
+                    sr = stride
+                elif stride != sr * n:
+                    raise ValueError(f"{name}: the scales' leading axes do not form one row axis")
+                n *= size
+    elif scales.shape == (-(-rows // GROUP8), groups):
+        per, sr = GROUP8, scales.stride(0)
+    else:
+        raise ValueError(f"{name}: scales {tuple(scales.shape)} for codes {tuple(codes.shape)}")
+    return rows, (codes.data_ptr(), ld, scales.data_ptr(), sr, scales.stride(-1), per)
+
+
+@functools.lru_cache(maxsize=4096)
+def _matmul8_workspace(M, N, K, index):
+    return load().evoattn_matmul8_workspace_size(M, N, K)
+
+
+def matmul8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, add=None, out=None, workspace=None, stream=None):
+    """out = a b^T (+ add) of two matrices in 8 bits with block scales, as norm8
+    and quantize8 make them (see evoattn_matmul8).  a [..., K], b [N, K]:
+    float8_e4m3fn codes, rows at multiples of 16 bytes, contiguous along K;
+    scales float8_e8m0fnu, by row and 128 columns, or by 128 x 128 block.  out
+    [..., N] in out_dtype (bf16 or fp32); add: likewise, or [N] for all rows; it
+    may be out itself (a gradient that is added up).  `stream` as in
+    block_norm."""
+    dev = _on_device(a)
+    M, left = _operand8(a, a_scale, "a", dev)
+    N, right = _operand8(b, b_scale, "b", dev)
+    K = a.shape[-1]
+    if b.dim() != 2 or b.shape[1] != K:
+        raise ValueError(f"b: expected [N, {K}], got {tuple(b.shape)}")
+    shape = (*a.shape[:-1], N)
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out: bf16 or fp32, got {out_dtype}")
+    for t, name in ((add, "add"), (out, "out")):
+        if t is not None and (t.dtype is not out_dtype or t.get_device() != dev or t.shape != shape) and \
+                not (name == "add" and t.dtype is out_dtype and t.get_device() == dev and t.shape == (N,)):
+            raise ValueError(f"{name}: expected {shape} {out_dtype} on cuda:{dev}, got {tuple(t.shape)} {t.dtype} "
+                             f"on {t.device}")
+    ld_out, ld_add = N, 0
+    if out is not None:
+        m, ld_out = _matrix(out, "out")
+    if add is not None:
+        m, ld_add = _matrix(add, "add")
+        if add.shape != shape:
+            ld_add = 0
+    need = _matmul8_workspace(M, N, K, dev)
+    with _allocate_on(stream):
+        if out is None:
+            out = torch.empty(shape, device=a.device, dtype=out_dtype)
+        if need and workspace is None:
+            workspace = torch.empty(need, device=a.device, dtype=torch.uint8)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
+    if stream is not None:
+        _used_on(stream, (a, a_scale, b, b_scale, add, out, workspace))
+    ws = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = load().evoattn_matmul8(
+        _PACK_MATMUL8(*left, *right, M, N, K, out.data_ptr(), ld_out, 0 if add is None else add.data_ptr(),
+                      ld_add, F32 if out_dtype is torch.float32 else BF16, *ws), _raw_stream(stream, dev))
+    if st != OK:
+        _check(st, "evoattn_matmul8")
+    return out
+
+
+def matmul8_workspace_size(M, N, K) -> int:
+    """Bytes of matmul8's workspace on the current device (0: none needed)."""
+    return int(load().evoattn_matmul8_workspace_size(M, N, K))
 
 
 def debug_set_wait(limit_ns: int = 0, stall: bool = False) -> None:
