@@ -313,7 +313,7 @@ evoattn_status evoattn_matmul8(const evoattn_matmul8_args* args, cudaStream_t st
   int sms = 0;
   if (!sm_count(&sms) || !wait_config(&c.wait)) return EVOATTN_ERR_CUDA;
   const Matmul8Plan plan = matmul8_plan(c.M, c.N, c.K, sms);
-  if ((__int128)plan.tiles_m * plan.tiles_n * plan.splits > most) return EVOATTN_ERR_UNSUPPORTED;
+  if ((__int128)plan.tiles_p * plan.tiles_q * plan.splits > most) return EVOATTN_ERR_UNSUPPORTED;
   const size_t need = matmul8_workspace_bytes(c.M, c.N, c.K, sms);
   if (need && (!a.workspace || a.workspace_bytes < 0 || (size_t)a.workspace_bytes < need ||
                reinterpret_cast<uintptr_t>(a.workspace) % 256))

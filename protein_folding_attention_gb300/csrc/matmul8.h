@@ -30,10 +30,11 @@ struct Matmul8Call {
   WaitCfg wait;
 };
 
-// How a product is cut up: a tile is 128 columns and `bm` rows of out; the sum
-// over K is cut into `splits` pieces.
+// How a product is cut up: tiles of 128 rows of one operand by bq rows of the
+// other; the sum over K in `splits` pieces of per_split groups.
 struct Matmul8Plan {
-  int bm, tiles_m, tiles_n, groups, per_split, splits;
+  bool staged;            // a's rows are the 128, else b's
+  int bq, tiles_p, tiles_q, groups, per_split, splits;
 };
 Matmul8Plan matmul8_plan(int M, int N, int K, int sms);
 size_t matmul8_workspace_bytes(int M, int N, int K, int sms);

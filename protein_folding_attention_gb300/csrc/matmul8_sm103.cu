@@ -8,25 +8,31 @@
 // CUDA core touches it before the end.  (The hardware's block is 32 elements; the
 // four of a group of 128 get the same byte.)
 //
-// A tile of out is 128 columns n, one per TMEM lane, and BM rows m, one per TMEM
-// column: b's rows are the M = 128 operand of the MMA, a's rows the N = BM one.
-// With the columns of out on the lanes a warp's store of one row is consecutive
-// in memory, whatever out's stride and alignment, and few tokens (BM down to 16)
-// cost no more tensor work than they have to, while b, the larger operand then,
-// streams through the 128-row side.
+// One operand's rows lie on the 128 lanes of tensor memory (the M operand of the
+// MMA), the other's on BQ of its columns (the N operand).  With many rows a's are
+// on the lanes: a lane then holds consecutive columns of out, which go through a
+// staging buffer per warp (32 rows of 128 bytes, 16-byte units XORed with the row)
+// and leave in the widest units that out's base, row stride and width allow,
+// whole rows of 128 bytes at a time.  (Stores straight from the registers of the
+// other orientation, one element per lane, cost 500 instructions per 16 rows:
+// 131 us for 147,456 x 512 fp32 outputs at K = 128.)  With few rows (up to 64
+// tokens) b's are on the lanes, so that the MMA is no larger than the tokens (BQ
+// down to 16) and b, the larger operand then, streams through the 128-row side;
+// a warp stores 32 consecutive columns of a row.
 //
 // Long sums with few tiles are cut into pieces along k, one per CTA, which leave
-// fp32 partial sums [piece][m][n]; a second kernel adds them in order.
+// fp32 partial sums [piece][m][n], with b's rows on the lanes too; a second kernel
+// adds them in order.
 //
 // Warps (384 threads, one persistent CTA per SM, a ring of stages of 128 k):
-//   0      TMA producer: a's and b's codes (128-byte swizzle)
+//   0      TMA producer: both operands' codes (128-byte swizzle)
 //   1      MMA issuer: copies the stage's scales to tensor memory, four MMAs of
 //          32 k; commits free the stage
-//   2, 3   scales of b's and a's rows: bytes from global memory, each repeated
+//   2, 3   scales of the two operands' rows: bytes from global memory, each repeated
 //          over a word, in the order that the copy to tensor memory wants
 //          (word r / 32 of 16-byte row r % 32)
 //   4-11   epilogue: tensor memory -> registers -> out, two warps per lane
-//          quarter taking alternate chunks of 16 rows; the accumulator is double
+//          quarter with half the columns each; the accumulator is double
 //          buffered, so the next tile's sum runs meanwhile
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,32 +49,39 @@
 namespace evo {
 namespace {
 
-constexpr int kLanes = 128;  // columns of out in a tile
+constexpr int kLanes = 128;  // rows of the operand on the lanes
 constexpr int kGroup = 128;  // elements along k of a stage, and of a scale
 constexpr int kThreads = 384;
 
-template <int BM_>
+enum Mode { kStaged, kDirect, kPartial };  // a on the lanes; b on the lanes; that, and a piece of the sum
+
+template <int BQ_, Mode MODE>
 struct Cfg {
-  static constexpr int BM = BM_;
-  static constexpr uint32_t B_BYTES = kLanes * kGroup, A_BYTES = BM * kGroup;
+  static constexpr int BQ = BQ_;
+  static constexpr uint32_t P_BYTES = kLanes * kGroup, Q_BYTES = BQ * kGroup;
   static constexpr uint32_t S_BYTES = 512;  // scales of up to 128 rows
-  static constexpr uint32_t STAGE = B_BYTES + A_BYTES;
-  static constexpr int STAGES = std::min<int>(8, (200 * 1024) / (int)(STAGE + 2 * S_BYTES));
+  static constexpr uint32_t STAGE = P_BYTES + Q_BYTES;
+  static constexpr uint32_t STAGING = MODE == kStaged ? 8 * 4096 : 0;
+  static constexpr int STAGES = std::min<int>(8, (int)((220 * 1024 - STAGING) / (STAGE + 2 * S_BYTES)));
   static constexpr uint32_t OFF_S = STAGES * STAGE;
-  static constexpr uint32_t SMEM_ALLOC = OFF_S + STAGES * 2 * S_BYTES + 1024;
-  static constexpr uint32_t COL_S = 2 * BM < 32 ? 32 : 2 * BM;  // scales: 4 columns for b, 4 for a
+  static constexpr uint32_t OFF_STAGING = OFF_S + STAGES * 2 * S_BYTES;
+  static constexpr uint32_t SMEM_ALLOC = OFF_STAGING + STAGING + 1024;
+  static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ;  // scales: 4 columns for each operand
   static_assert(COL_S + 8 <= 512, "tensor memory");
-  static_assert(STAGE % 1024 == 0, "the swizzle repeats every 1024 bytes");
+  static_assert(STAGE % 1024 == 0 && OFF_STAGING % 1024 == 0, "the swizzle repeats every 1024 bytes");
 };
 
 struct Params8 {
-  Operand8 a, b;
+  Operand8 p, q;          // on the lanes, on the columns
+  int P, Q;               // their rows
+  int tiles_p, tiles_q, groups, per_split, items;
+  int fast_q;             // items run over q first
   int M, N;
-  int tiles_n, tiles_m, groups, per_split, items;
   void* out;
   int64_t ld_out;
   const void* add;
   int64_t ld_add;
+  int unit, unit_add;     // bytes that out is stored, and add read, in at a time (staged)
   float* ws;
   WaitCfg wc;
 };
@@ -94,14 +107,16 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) 
 
 // Where an item of work lies.
 struct Item {
-  int m0, n0, g0, g1, split;
+  int p0, q0, g0, g1, split;
 };
-__device__ __forceinline__ Item item_of(const Params8& p, int item, int bm) {
+__device__ __forceinline__ Item item_of(const Params8& p, int item, int bq) {
   Item w;
-  const int t = item / p.tiles_n;
-  w.n0 = (item - t * p.tiles_n) * kLanes;
-  w.split = t / p.tiles_m;
-  w.m0 = (t - w.split * p.tiles_m) * bm;
+  const int inner = p.fast_q ? p.tiles_q : p.tiles_p, outer = p.fast_q ? p.tiles_p : p.tiles_q;
+  const int t = item / inner, i = item - t * inner;
+  w.split = t / outer;
+  const int o = t - w.split * outer;
+  w.p0 = (p.fast_q ? o : i) * kLanes;
+  w.q0 = (p.fast_q ? i : o) * bq;
   w.g0 = w.split * p.per_split;
   w.g1 = min(p.groups, w.g0 + p.per_split);
   return w;
@@ -127,10 +142,96 @@ __device__ __forceinline__ float load_one<float>(const float* p) { return *p; }
 template <>
 __device__ __forceinline__ float load_one<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-template <typename T, int BM, bool SPLIT>
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Copies between a warp's staging buffer (rows of 128 bytes, 16-byte units XORed
+// with the row) and 32 rows of a matrix, V bytes per lane.  `at`: the first row's
+// first byte; `rows`, `width`: how many rows and bytes of a row there are (a
+// multiple of V).
+template <int V>
+struct Unit;
+template <>
+struct Unit<16> { using T = uint4; };
+template <>
+struct Unit<8> { using T = uint2; };
+template <>
+struct Unit<4> { using T = uint32_t; };
+template <>
+struct Unit<2> { using T = uint16_t; };
+
+template <int V, bool STORE>
+__device__ __forceinline__ void copy_rows(uint8_t* stg, uint8_t* at, int64_t stride, int rows, int width) {
+  using T = typename Unit<V>::T;
+  constexpr int PER = 128 / V;                     // units of a row
+  constexpr int STEP = PER <= 32 ? 32 / PER : 1;   // rows at a time
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < (PER <= 32 ? 1 : PER / 32); ++h) {
+    const int r0 = PER <= 32 ? lane / PER : 0, b = (PER <= 32 ? lane % PER : lane + 32 * h) * V;
+    if (b >= width) continue;
+    uint8_t* g = at + r0 * stride + b;
+#pragma unroll 8
+    for (int r = r0; r < rows; r += STEP, g += STEP * stride) {
+      T* const s = reinterpret_cast<T*>(stg + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
+      if constexpr (STORE)
+        *reinterpret_cast<T*>(g) = *s;
+      else
+        *s = *reinterpret_cast<const T*>(g);
+    }
+  }
+}
+template <bool STORE>
+__device__ __forceinline__ void copy_rows(int unit, uint8_t* stg, uint8_t* at, int64_t stride, int rows, int width) {
+  switch (unit) {
+    case 16: return copy_rows<16, STORE>(stg, at, stride, rows, width);
+    case 8: return copy_rows<8, STORE>(stg, at, stride, rows, width);
+    case 4: return copy_rows<4, STORE>(stg, at, stride, rows, width);
+    default: return copy_rows<2, STORE>(stg, at, stride, rows, width);
+  }
+}
+
+// 128 bytes of a row of out for this lane: from the accumulator's columns to the
+// lane's row of the staging buffer, with what the buffer holds of add.
+__device__ __forceinline__ void stage_row(uint8_t* stg, const uint32_t (&r)[32], bool add, float) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    float4* to = reinterpret_cast<float4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4));
+    float4 v = make_float4(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]), __uint_as_float(r[4 * c + 2]),
+                           __uint_as_float(r[4 * c + 3]));
+    if (add) {
+      const float4 a = *to;
+      v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+    }
+    *to = v;
+  }
+}
+__device__ __forceinline__ void stage_row(uint8_t* stg, const uint32_t (&lo)[32], const uint32_t (&hi)[32], bool add) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint4* to = reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4));
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(c < 4 ? lo[8 * c + e] : hi[8 * (c - 4) + e]);
+    if (add) {
+      const uint4 a = *to;
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[2 * e] += bf16lo(w[e]);
+        f[2 * e + 1] += bf16hi(w[e]);
+      }
+    }
+    *to = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+  }
+}
+
+template <typename T, int BQ, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_matmul8(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params8 p) {
-  using C = Cfg<BM>;
+    k_matmul8(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q, const Params8 p) {
+  using C = Cfg<BQ, MODE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -144,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&bar_full[i], 1);   // codes
-      mbar_init(&bar_scale[i], 2);  // scales of a and of b
+      mbar_init(&bar_scale[i], 2);  // scales of both operands
       mbar_init(&bar_empty[i], 1);  // the stage's MMAs have read it
     }
     for (int i = 0; i < 2; ++i) {
@@ -156,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&tmem_slot, 512);
-  if (warp == 0 && lane == 0) { tma_prefetch_desc(&tm_a); tma_prefetch_desc(&tm_b); }
+  if (warp == 0 && lane == 0) { tma_prefetch_desc(&tm_p); tma_prefetch_desc(&tm_q); }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -171,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int it = 0;
     for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-      const Item w = item_of(p, item, BM);
+      const Item w = item_of(p, item, BQ);
       for (int g = w.g0; g < w.g1; ++g, ++it) {
         const int st = it % C::STAGES;
         if (it >= C::STAGES) ok = mbar_wait(&bar_empty[st], ((it / C::STAGES) - 1) & 1, wctx);
@@ -179,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar_full[st], C::STAGE);
-          tma_load_2d(smem + st * C::STAGE, &tm_b, &bar_full[st], g * kGroup, w.n0);
-          tma_load_2d(smem + st * C::STAGE + C::B_BYTES, &tm_a, &bar_full[st], g * kGroup, w.m0);
+          tma_load_2d(smem + st * C::STAGE, &tm_p, &bar_full[st], g * kGroup, w.p0);
+          tma_load_2d(smem + st * C::STAGE + C::P_BYTES, &tm_q, &bar_full[st], g * kGroup, w.q0);
         }
         __syncwarp();
       }
@@ -193,15 +294,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ============================ MMA issuer ===============================
-    constexpr uint32_t id = idesc_mxf8(128, BM);
-    const uint64_t db0 = umma_desc(smem_u32(smem), 16, 1024, kSw128);
-    const uint64_t da0 = umma_desc(smem_u32(smem + C::B_BYTES), 16, 1024, kSw128);
+    constexpr uint32_t id = idesc_mxf8(128, BQ);
+    const uint64_t dp0 = umma_desc(smem_u32(smem), 16, 1024, kSw128);
+    const uint64_t dq0 = umma_desc(smem_u32(smem + C::P_BYTES), 16, 1024, kSw128);
     const uint64_t ds0 = umma_desc(smem_u32(smem + C::OFF_S), 16, 128, kSwNone);
-    const uint32_t sb = tmem + C::COL_S, sa = sb + 4;
+    const uint32_t sp = tmem + C::COL_S, sq = sp + 4;
     bool ok = true;
     int it = 0, n = 0;
     for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x, ++n) {
-      const Item w = item_of(p, item, BM);
+      const Item w = item_of(p, item, BQ);
       const int buf = n & 1;
       if (n >= 2) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bar_free[buf], ((n >> 1) - 1) & 1, wctx));
@@ -215,14 +316,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t db = db0 + ((uint32_t)(st * C::STAGE) >> 4), da = da0 + ((uint32_t)(st * C::STAGE) >> 4);
+        const uint64_t dp = dp0 + ((uint32_t)(st * C::STAGE) >> 4), dq = dq0 + ((uint32_t)(st * C::STAGE) >> 4);
         const uint64_t ds = ds0 + ((uint32_t)(st * 2 * C::S_BYTES) >> 4);
         if (elect_one()) {
-          tmem_copy_scales(sb, ds);
-          tmem_copy_scales(sa, ds + (C::S_BYTES >> 4));
+          tmem_copy_scales(sp, ds);
+          tmem_copy_scales(sq, ds + (C::S_BYTES >> 4));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_mxf8(tmem + buf * BM, db + 2 * kk, da + 2 * kk, id, sb, sa, g > w.g0 || kk > 0 ? 1u : 0u);
+            umma_mxf8(tmem + buf * BQ, dp + 2 * kk, dq + 2 * kk, id, sp, sq, g > w.g0 || kk > 0 ? 1u : 0u);
           umma_commit(&bar_empty[st]);
           if (g + 1 == w.g1) umma_commit(&bar_done[buf]);
         }
@@ -238,27 +339,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < 4) {
     // ============================ scales ===================================
-    const bool of_a = warp == 3;
-    const Operand8 o = of_a ? p.a : p.b;
-    const int rows = of_a ? p.M : p.N, width = of_a ? BM : kLanes;
+    const bool of_q = warp == 3;
+    const Operand8 o = of_q ? p.q : p.p;
+    const int rows = of_q ? p.Q : p.P, width = of_q ? BQ : kLanes;
+    // A ring of AHEAD steps in registers: the bytes of a step are requested AHEAD
+    // steps before they are written, across items too (with one step ahead every
+    // step waited for L2: 950 cycles a step where its MMAs take 256).
+    constexpr int AHEAD = 8;
+    uint32_t s[AHEAD][4];
+    int item = blockIdx.x, g = 0;  // the step that is requested next
+    Item w{};
+    if (item < p.items) { w = item_of(p, item, BQ); g = w.g0; }
+    const auto request = [&](uint32_t (&to)[4]) {
+      if (item >= p.items) return;
+      scale_bytes(o, rows, of_q ? w.q0 : w.p0, width, g, to);
+      if (++g == w.g1) {
+        item += gridDim.x;
+        if (item < p.items) { w = item_of(p, item, BQ); g = w.g0; }
+      }
+    };
+    int left = 0;  // steps of this CTA
+    for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+      const Item v = item_of(p, i, BQ);
+      left += v.g1 - v.g0;
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) request(s[k]);
     bool ok = true;
-    int it = 0;
-    for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-      const Item w = item_of(p, item, BM);
-      const int r0 = of_a ? w.m0 : w.n0;
-      uint32_t s[4];
-      scale_bytes(o, rows, r0, width, w.g0, s);
-      for (int g = w.g0; g < w.g1; ++g, ++it) {
-        const int st = it % C::STAGES;
-        const uint4 v = make_uint4(s[0] * 0x01010101u, s[1] * 0x01010101u, s[2] * 0x01010101u, s[3] * 0x01010101u);
-        if (g + 1 < w.g1) scale_bytes(o, rows, r0, width, g + 1, s);
-        if (it >= C::STAGES) ok = mbar_wait(&bar_empty[st], ((it / C::STAGES) - 1) & 1, wctx);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        *reinterpret_cast<uint4*>(smem + C::OFF_S + (st * 2 + (of_a ? 1 : 0)) * C::S_BYTES + lane * 16) = v;
-        fence_proxy_async_smem();  // generic writes, read by the copy to tensor memory
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_scale[st]);
+    for (int it0 = 0; it0 < left && ok; it0 += AHEAD) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int it = it0 + k;
+        if (it < left && ok) {
+          const int st = it % C::STAGES;
+          const uint4 v = make_uint4(s[k][0] * 0x01010101u, s[k][1] * 0x01010101u, s[k][2] * 0x01010101u,
+                                     s[k][3] * 0x01010101u);
+          request(s[k]);
+          if (it >= C::STAGES) ok = mbar_wait(&bar_empty[st], ((it / C::STAGES) - 1) & 1, wctx);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            *reinterpret_cast<uint4*>(smem + C::OFF_S + (st * 2 + (of_q ? 1 : 0)) * C::S_BYTES + lane * 16) = v;
+            fence_proxy_async_smem();  // generic writes, read by the copy to tensor memory
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_scale[st]);
+          }
+        }
       }
     }
   } else {
@@ -268,44 +393,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.wc.stall) ok = __all_sync(0xffffffffu, stall_wait(&bar_never, wctx));
     int n = 0;
     for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x, ++n) {
-      const Item w = item_of(p, item, BM);
+      const Item w = item_of(p, item, BQ);
       const int buf = n & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(&bar_done[buf], (n >> 1) & 1, wctx));
       if (!ok) break;
       tc_fence_after();
-      const int col = w.n0 + quad * 32 + lane;  // this thread's column of out
-      const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + buf * BM;
+      const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + buf * BQ;
+      if constexpr (MODE == kStaged) {
+        uint8_t* stg = smem + C::OFF_STAGING + (warp - 4) * 4096;
+        constexpr int SPAN = 128 / sizeof(T);  // columns of a chunk
+        const int m = w.p0 + quad * 32, rows = min(32, p.M - m);
 #pragma unroll 1
-      for (int c = half; c < BM / 16; c += 2) {
-        const int m = w.m0 + c * 16;
-        if (m >= p.M) break;  // (the same for the whole warp)
-        uint32_t r[16];
-        tmem_ld16(base + c * 16, r);
-        tmem_wait_ld();
-        reg_fence16(r);
-        const int rows = min(16, p.M - m);
-        if constexpr (SPLIT) {
-          float* to = p.ws + ((int64_t)w.split * p.M + m) * p.N + col;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (i < rows && col < p.N) to[(int64_t)i * p.N] = __uint_as_float(r[i]);
-        } else {
-          const T* add = static_cast<const T*>(p.add) + m * p.ld_add + col;
-          T* to = static_cast<T*>(p.out) + m * p.ld_out + col;
-          float f[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            f[i] = __uint_as_float(r[i]);
-            if (p.add && i < rows && col < p.N) f[i] += load_one<T>(add + i * p.ld_add);
+        for (int c = half * (BQ / 2); c < (half + 1) * (BQ / 2); c += SPAN) {
+          const int n = w.q0 + c, width = min(SPAN, p.N - n) * (int)sizeof(T);
+          if (width <= 0 || rows <= 0) break;  // (the same for the whole warp)
+          uint32_t lo[32], hi[32];
+          tmem_ld32(base + c, lo);
+          if constexpr (sizeof(T) == 2) tmem_ld32(base + c + 32, hi);
+          __syncwarp();  // the previous chunk has left the buffer
+          if (p.add) {
+            copy_rows<false>(p.unit_add, stg,
+                             static_cast<uint8_t*>(const_cast<void*>(p.add)) + (m * p.ld_add + n) * (int64_t)sizeof(T),
+                             p.ld_add * (int64_t)sizeof(T), rows, width);
+            __syncwarp();
           }
-          if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (i < rows && col < p.N) to[i * p.ld_out] = f[i];
+          tmem_wait_ld();
+          reg_fence32(lo);
+          if constexpr (sizeof(T) == 2) {
+            reg_fence32(hi);
+            stage_row(stg, lo, hi, p.add != nullptr);
           } else {
+            stage_row(stg, lo, p.add != nullptr, 0.f);
+          }
+          __syncwarp();
+          copy_rows<true>(p.unit, stg, static_cast<uint8_t*>(p.out) + (m * p.ld_out + n) * (int64_t)sizeof(T),
+                          p.ld_out * (int64_t)sizeof(T), rows, width);
+        }
+      } else {
+        const int col = w.p0 + quad * 32 + lane;  // this thread's column of out
+        const bool on = col < p.N;
+#pragma unroll 1
+        for (int c = half; c < BQ / 16; c += 2) {
+          const int m = w.q0 + c * 16, rows = min(16, p.M - m);
+          if (rows <= 0) break;  // (the same for the whole warp)
+          uint32_t r[16];
+          tmem_ld16(base + c * 16, r);
+          tmem_wait_ld();
+          reg_fence16(r);
+          if constexpr (MODE == kPartial) {
+            float* to = p.ws + ((int64_t)w.split * p.M + m) * p.N + col;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (i < rows && col < p.N) to[i * p.ld_out] = __float2bfloat16_rn(f[i]);
+            for (int i = 0; i < 16; ++i, to += p.N)
+              if (i < rows && on) *to = __uint_as_float(r[i]);
+          } else {
+            T* to = static_cast<T*>(p.out) + m * p.ld_out + col;
+            if (p.add) {
+              const T* add = static_cast<const T*>(p.add) + m * p.ld_add + col;
+#pragma unroll
+              for (int i = 0; i < 16; ++i, add += p.ld_add)
+                if (i < rows && on) r[i] = __float_as_uint(__uint_as_float(r[i]) + load_one<T>(add));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i, to += p.ld_out)
+              if (i < rows && on) store_one(to, __uint_as_float(r[i]));
           }
         }
       }
@@ -335,10 +485,7 @@ __global__ void __launch_bounds__(256)
     for (int k = 0; k < splits; ++k) s += ws[k * total + i];
     const int64_t m = i / N, n = i - m * N;
     if (add) s += load_one<T>(add + m * ld_add + n);
-    if constexpr (sizeof(T) == 4)
-      out[m * ld_out + n] = s;
-    else
-      out[m * ld_out + n] = __float2bfloat16_rn(s);
+    store_one(out + m * ld_out + n, s);
   }
 }
 
@@ -353,57 +500,87 @@ bool make_tmap_codes(CUtensorMap* map, const Operand8& o, int rows, int K, uint3
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int BM, bool SPLIT>
+// The widest unit in which rows of `width` bytes can be copied.
+int unit_of(const void* p, int64_t stride, int64_t width) {
+  const uint64_t bits = reinterpret_cast<uintptr_t>(p) | (uint64_t)stride | (uint64_t)width;
+  return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
+}
+
+template <typename T, int BQ, Mode MODE>
 cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  CUtensorMap ta, tb;
-  if (!make_tmap_codes(&ta, c.a, c.M, c.K, BM) || !make_tmap_codes(&tb, c.b, c.N, c.K, kLanes)) {
+  using C = Cfg<BQ, MODE>;
+  Params8 p{};
+  p.p = MODE == kStaged ? c.a : c.b;
+  p.q = MODE == kStaged ? c.b : c.a;
+  p.P = MODE == kStaged ? c.M : c.N;
+  p.Q = MODE == kStaged ? c.N : c.M;
+  CUtensorMap tp, tq;
+  if (!make_tmap_codes(&tp, p.p, p.P, c.K, kLanes) || !make_tmap_codes(&tq, p.q, p.Q, c.K, BQ)) {
     *tmap_ok = false;
     return cudaErrorInvalidValue;
   }
-  Params8 p{};
-  p.a = c.a; p.b = c.b;
-  p.M = c.M; p.N = c.N;
-  p.tiles_n = pl.tiles_n; p.tiles_m = pl.tiles_m;
+  p.tiles_p = pl.tiles_p; p.tiles_q = pl.tiles_q;
+  p.fast_q = MODE == kStaged;  // out's columns first: the rows of a that are in flight are few
   p.groups = pl.groups; p.per_split = pl.per_split;
-  p.items = pl.tiles_n * pl.tiles_m * pl.splits;
+  p.items = pl.tiles_p * pl.tiles_q * pl.splits;
+  p.M = c.M; p.N = c.N;
   p.out = c.out; p.ld_out = c.ld_out;
   p.add = c.add; p.ld_add = c.ld_add;
+  const int64_t size = sizeof(T);
+  p.unit = unit_of(c.out, c.ld_out * size, c.N * size);
+  p.unit_add = unit_of(c.add, c.ld_add * size, c.N * size);
   p.ws = c.ws;
   p.wc = launch_wait(c.wait);
-  auto kern = k_matmul8<T, BM, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BM>::SMEM_ALLOC);
+  auto kern = k_matmul8<T, BQ, MODE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
-  e = launch_early(kern, (unsigned)std::min(p.items, sms), kThreads, Cfg<BM>::SMEM_ALLOC, st, ta, tb, p);
-  if (e != cudaSuccess || !SPLIT) return e;
-  const int64_t blocks = ((int64_t)c.M * c.N + 255) / 256;
-  const unsigned grid = (unsigned)std::min<int64_t>(blocks, 8 * (int64_t)sms);
-  return c.f32 ? launch_early(k_matmul8_sum<float>, grid, 256, 0, st, (const float*)c.ws, pl.splits, c.M, c.N,
-                              static_cast<float*>(c.out), c.ld_out, static_cast<const float*>(c.add), c.ld_add)
-               : launch_early(k_matmul8_sum<__nv_bfloat16>, grid, 256, 0, st, (const float*)c.ws, pl.splits, c.M,
-                              c.N, static_cast<__nv_bfloat16*>(c.out), c.ld_out,
-                              static_cast<const __nv_bfloat16*>(c.add), c.ld_add);
+  return launch_early(kern, (unsigned)std::min(p.items, sms), kThreads, C::SMEM_ALLOC, st, tp, tq, p);
 }
 
-template <int BM>
-cudaError_t by_type(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  if (pl.splits > 1) return launch<float, BM, true>(c, pl, sms, st, tmap_ok);
-  return c.f32 ? launch<float, BM, false>(c, pl, sms, st, tmap_ok)
-               : launch<__nv_bfloat16, BM, false>(c, pl, sms, st, tmap_ok);
+template <typename T>
+cudaError_t launch_sum(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st) {
+  const int64_t blocks = ((int64_t)c.M * c.N + 255) / 256;
+  const unsigned grid = (unsigned)std::min<int64_t>(blocks, 8 * (int64_t)sms);
+  return launch_early(k_matmul8_sum<T>, grid, 256, 0, st, (const float*)c.ws, pl.splits, c.M, c.N,
+                      static_cast<T*>(c.out), c.ld_out, static_cast<const T*>(c.add), c.ld_add);
+}
+
+template <int BQ>
+cudaError_t few_rows(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
+  if (pl.splits > 1) {
+    const cudaError_t e = launch<float, BQ, kPartial>(c, pl, sms, st, tmap_ok);
+    if (e != cudaSuccess) return e;
+    return c.f32 ? launch_sum<float>(c, pl, sms, st) : launch_sum<__nv_bfloat16>(c, pl, sms, st);
+  }
+  return c.f32 ? launch<float, BQ, kDirect>(c, pl, sms, st, tmap_ok)
+               : launch<__nv_bfloat16, BQ, kDirect>(c, pl, sms, st, tmap_ok);
 }
 
 }  // namespace
 
 Matmul8Plan matmul8_plan(int M, int N, int K, int sms) {
   Matmul8Plan pl{};
-  pl.bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  pl.tiles_m = (int)(((int64_t)M + pl.bm - 1) / pl.bm);
-  pl.tiles_n = (int)(((int64_t)N + kLanes - 1) / kLanes);
-  pl.groups = (int)(((int64_t)K + kGroup - 1) / kGroup);
-  const int64_t tiles = (int64_t)pl.tiles_m * pl.tiles_n;
-  int64_t splits = 1;
-  if (2 * tiles <= sms) splits = std::min<int64_t>(sms / tiles, std::max(1, pl.groups / 2));
-  pl.per_split = (int)((pl.groups + splits - 1) / splits);
-  pl.splits = (pl.groups + pl.per_split - 1) / pl.per_split;
+  const auto tiles = [](int n, int by) { return (int)(((int64_t)n + by - 1) / by); };
+  pl.groups = tiles(K, kGroup);
+  // b's rows on the lanes, with the columns that a's few rows need
+  pl.bq = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  pl.tiles_p = tiles(N, kLanes);
+  pl.tiles_q = tiles(M, pl.bq);
+  pl.splits = 1;
+  pl.per_split = pl.groups;
+  const int64_t count = (int64_t)pl.tiles_p * pl.tiles_q;
+  if (2 * count <= sms && pl.groups > 3) {
+    // pieces of the sum, two groups at least, for as many CTAs as there are SMs
+    const int64_t most = std::min<int64_t>(sms / count, pl.groups / 2);
+    pl.per_split = (int)((pl.groups + most - 1) / most);
+    pl.splits = (pl.groups + pl.per_split - 1) / pl.per_split;
+  }
+  if (M > 64 && pl.splits == 1) {  // a's rows on the lanes
+    pl.staged = true;
+    pl.bq = 128;
+    pl.tiles_p = tiles(M, kLanes);
+    pl.tiles_q = tiles(N, pl.bq);
+  }
   return pl;
 }
 
@@ -413,11 +590,19 @@ size_t matmul8_workspace_bytes(int M, int N, int K, int sms) {
 }
 
 cudaError_t matmul8(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  switch (pl.bm) {
-    case 16: return by_type<16>(c, pl, sms, st, tmap_ok);
-    case 32: return by_type<32>(c, pl, sms, st, tmap_ok);
-    case 64: return by_type<64>(c, pl, sms, st, tmap_ok);
-    default: return by_type<128>(c, pl, sms, st, tmap_ok);
+  if (pl.staged)
+    return c.f32 ? launch<float, 128, kStaged>(c, pl, sms, st, tmap_ok)
+                 : launch<__nv_bfloat16, 128, kStaged>(c, pl, sms, st, tmap_ok);
+  switch (pl.bq) {
+    case 16: return few_rows<16>(c, pl, sms, st, tmap_ok);
+    case 32: return few_rows<32>(c, pl, sms, st, tmap_ok);
+    case 64: return few_rows<64>(c, pl, sms, st, tmap_ok);
+    default:  // (only in pieces)
+    {
+      const cudaError_t e = launch<float, 128, kPartial>(c, pl, sms, st, tmap_ok);
+      if (e != cudaSuccess) return e;
+      return c.f32 ? launch_sum<float>(c, pl, sms, st) : launch_sum<__nv_bfloat16>(c, pl, sms, st);
+    }
   }
 }
 

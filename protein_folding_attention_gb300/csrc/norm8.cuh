@@ -315,7 +315,6 @@ __global__ void __launch_bounds__(kThreads) k_norm8_fwd(const Params p, int turn
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) {
       const int c = L::chan(lane, k);
-      float amax = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const bool has = L::has(p.C, c, e);
@@ -323,26 +322,35 @@ __global__ void __launch_bounds__(kThreads) k_norm8_fwd(const Params p, int turn
         if (has && p.gamma) y *= p.gamma[c + L::off(e)];
         if (has && p.beta) y += p.beta[c + L::off(e)];
         x[k][e] = y;
-        amax = fmaxf(amax, finite_abs(y));
       }
+      const auto group_maximum = [&] {
+        float m = max_abs(x[k]);
 #pragma unroll
-      for (int o = (VEC ? (LANES < 16 ? LANES : 16) : 32) / 2; o > 0; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int o = (VEC ? (LANES < 16 ? LANES : 16) : 32) / 2; o > 0; o >>= 1)
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+      };
+      float amax = group_maximum();
+      if (__any_sync(0xffffffffu, amax > FLT_MAX)) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[k][e] = infinity_to_nan(x[k][e]);
+        amax = group_maximum();
+      }
       const uint32_t code = scale_code(amax);
       const float inv = scale_inverse(code);
       if constexpr (VEC) {
-        const uint32_t q0 = e4m3_pair(x[k][0], x[k][1], inv), q1 = e4m3_pair(x[k][2], x[k][3], inv),
-                       q2 = e4m3_pair(x[k][4], x[k][5], inv), q3 = e4m3_pair(x[k][6], x[k][7], inv);
+        const uint2 q = make_uint2(e4m3_four(x[k][0], x[k][1], x[k][2], x[k][3], inv),
+                                   e4m3_four(x[k][4], x[k][5], x[k][6], x[k][7], inv));
         if (on && c < p.C) {
-          *reinterpret_cast<uint2*>(p.codes + ac + c) = make_uint2(q0 | q1 << 16, q2 | q3 << 16);
+          *reinterpret_cast<uint2*>(p.codes + ac + c) = q;
           if ((c & 127) == 0) p.scales[as + (int64_t)(c >> 7) * p.scales_g] = (uint8_t)code;
         }
       } else {
-        const uint32_t q0 = e4m3_pair(x[k][0], x[k][1], inv), q1 = e4m3_pair(x[k][2], x[k][3], inv);
+        const uint32_t q = e4m3_four(x[k][0], x[k][1], x[k][2], x[k][3], inv);
         if (on) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (c + 32 * e < p.C) p.codes[ac + c + 32 * e] = (uint8_t)((e < 2 ? q0 : q1) >> (e & 1) * 8);
+            if (c + 32 * e < p.C) p.codes[ac + c + 32 * e] = (uint8_t)(q >> 8 * e);
           if ((c & 127) == 0 && c < p.C) p.scales[as + (int64_t)(c >> 7) * p.scales_g] = (uint8_t)code;
         }
       }

@@ -4,12 +4,20 @@
 //
 // Bound by memory: an element is read once and each copy written once.  A CTA
 // takes a 128 x 128 tile, the largest piece that a scale spans in both
-// directions; thread (ty, tx) holds the 8 x 8 elements of rows 8 ty and columns
-// 8 tx in registers, so that the eight loads of 16 bytes are in flight at once,
-// 16 neighbouring threads see a row and 16 strided ones a column, and eight
-// codes of a column are one 8-byte unit of the transposed tile.  That goes
-// through shared memory, where a unit's place in its 128-byte column is XORed
-// with the column's tx: 16 threads of a warp then hit 16 different units.
+// directions; thread (ty, tx) of its 512 holds the 4 x 8 elements of rows 4 ty and
+// columns 8 tx in registers, so that 16 neighbouring threads see a row and 32
+// strided ones a column, four loads of 16 bytes per thread are in flight at once
+// and four codes of a column are one word of the transposed tile.  That goes
+// through shared memory, where a word's place in its 128-byte column is XORed with
+// 2 tx: a warp's 32 words then hit 32 banks.
+//
+// With 4.4 bytes for each element (bf16, both copies) the memory rate leaves some
+// 20 instructions per element: maxima are taken three operands at a time on
+// magnitudes, which skips NaN, and infinities are looked for once per tile and
+// turned into NaN, instead of a test per element.
+//
+// Rows that are no whole 16-byte units come through shared memory too: a warp
+// reads a row's elements 32 at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,14 +28,15 @@
 namespace evo {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kRows = 4;  // of a thread
 
 template <typename T>
 struct Load;
 template <>
 struct Load<__nv_bfloat16> {
-  static __device__ __forceinline__ void eight(const __nv_bfloat16* p, float (&f)[8]) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  static constexpr int PITCH = 136;  // elements of a row in shared memory
+  static __device__ __forceinline__ void unpack(const uint4& a, float (&f)[8]) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -35,23 +44,28 @@ struct Load<__nv_bfloat16> {
       f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
     }
   }
-  static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ void eight(const __nv_bfloat16* p, float (&f)[8]) {
+    unpack(__ldcs(reinterpret_cast<const uint4*>(p)), f);
+  }
+  static __device__ __forceinline__ void eight_shared(const __nv_bfloat16* p, float (&f)[8]) {
+    unpack(*reinterpret_cast<const uint4*>(p), f);
+  }
 };
 template <>
 struct Load<float> {
-  static __device__ __forceinline__ void eight(const float* p, float (&f)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  static constexpr int PITCH = 132;
+  static __device__ __forceinline__ void unpack(const float4& a, const float4& b, float (&f)[8]) {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
-  static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ void eight(const float* p, float (&f)[8]) {
+    unpack(__ldcs(reinterpret_cast<const float4*>(p)), __ldcs(reinterpret_cast<const float4*>(p) + 1), f);
+  }
+  static __device__ __forceinline__ void eight_shared(const float* p, float (&f)[8]) {
+    unpack(reinterpret_cast<const float4*>(p)[0], reinterpret_cast<const float4*>(p)[1], f);
+  }
 };
 
-__device__ __forceinline__ uint2 eight_codes(const float (&f)[8], float inv) {
-  return make_uint2(e4m3_pair(f[0], f[1], inv) | e4m3_pair(f[2], f[3], inv) << 16,
-                    e4m3_pair(f[4], f[5], inv) | e4m3_pair(f[6], f[7], inv) << 16);
-}
 // The first `n` (1 to 8) of eight codes.
 __device__ __forceinline__ void put_codes(uint8_t* p, uint2 q, int n) {
   if (n >= 8) {
@@ -62,47 +76,84 @@ __device__ __forceinline__ void put_codes(uint8_t* p, uint2 q, int n) {
   for (int e = 0; e < n; ++e) p[e] = (uint8_t)(v >> 8 * e);
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_quantize8(const Quantize8Call c, uint32_t tiles_k) {
-  __shared__ float col_max[8][kGroup8];
+template <typename T, bool VEC, bool COLS>
+__global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c, uint32_t tiles_k) {
+  __shared__ float col_max[COLS ? kThreads / 32 : 1][kGroup8];
   __shared__ float col_inv[kGroup8];
-  __shared__ __align__(16) uint8_t turned[kGroup8 * kGroup8];
+  // the tile as it was read (rows that are no whole units), then transposed codes
+  extern __shared__ __align__(16) uint8_t tile[];
   wait_for_earlier_work();
   let_next_start();
   const uint32_t tr = blockIdx.x / tiles_k, tk = blockIdx.x - tr * tiles_k;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5;
-  const int64_t r0 = (int64_t)tr * kGroup8 + ty * 8;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r0 = (int64_t)tr * kGroup8 + ty * kRows;
   const int64_t k0 = (int64_t)tk * kGroup8 + tx * 8;
-  const int nk = (int)min((int64_t)8, c.K - k0);  // this thread's columns (may be negative)
-  const int nr = (int)min((int64_t)8, c.R - r0);  // and rows
-  float f[8][8];
+  const int nk = (int)min((int64_t)8, c.K - k0);      // this thread's columns (may be negative)
+  const int nr = (int)min((int64_t)kRows, c.R - r0);  // and rows
+  float f[kRows][8];
   const T* x = static_cast<const T*>(c.x);
+  if constexpr (VEC) {  // (K is a multiple of 8)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (VEC && i < nr && nk > 0) {  // (K is a multiple of 8)
-      Load<T>::eight(x + (r0 + i) * c.ld + k0, f[i]);
-    } else {
+    for (int i = 0; i < kRows; ++i) {
+      if (i < nr && nk > 0) {
+        Load<T>::eight(x + (r0 + i) * c.ld + k0, f[i]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = !VEC && i < nr && e < nk ? Load<T>::one(x + (r0 + i) * c.ld + k0 + e) : 0.f;
+        for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
+      }
     }
+  } else {
+    T* rows = reinterpret_cast<T*>(tile);
+    constexpr int PER = kGroup8 / (kThreads / 32);  // rows of a warp
+    T v[PER][4];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int64_t r = (int64_t)tr * kGroup8 + warp * PER + i, k = (int64_t)tk * kGroup8 + lane;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = r < c.R && k + 32 * e < c.K ? x[r * c.ld + k + 32 * e] : T(0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rows[(warp * PER + i) * Load<T>::PITCH + lane + 32 * e] = v[i][e];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) Load<T>::eight_shared(rows + (ty * kRows + i) * Load<T>::PITCH + tx * 8, f[i]);
   }
-  const bool cols = c.codes_t != nullptr || c.blocks;
+  // row maxima, and whether there is an infinity (in the warp's rows, or, where
+  // columns need it, in the tile)
+  float row[kRows];
+  const auto row_maxima = [&] {
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      row[i] = max_abs8(f[i]);
+      all = fmaxf(all, row[i]);
+    }
+    return all;
+  };
+  const bool infinite = row_maxima() > FLT_MAX;
+  if (COLS ? __syncthreads_or(infinite) : __any_sync(0xffffffffu, infinite)) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] = infinity_to_nan(f[i][e]);
+    row_maxima();
+  }
   float block = 0.f;
-  if (cols) {
-    // column maxima: 8 rows of this thread, the other half of the warp, 8 warps
+  if constexpr (COLS) {
+    // column maxima: 4 rows of this thread, the other half of the warp, 16 warps
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(f[i][e]));
+      float m = max_abs3(f[0][e], f[1][e], max_abs3(f[2][e], f[3][e], 0.f));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      if ((threadIdx.x & 16) == 0) col_max[warp][tx * 8 + e] = m;
+      if (lane < 16) col_max[warp][tx * 8 + e] = m;
     }
     __syncthreads();
     if (threadIdx.x < kGroup8) {
       float m = col_max[0][threadIdx.x];
 #pragma unroll
-      for (int k = 1; k < 8; ++k) m = fmaxf(m, col_max[k][threadIdx.x]);
+      for (int k = 1; k < kThreads / 32; ++k) m = fmaxf(m, col_max[k][threadIdx.x]);
       if (!c.blocks) {
         const uint32_t code = scale_code(m);
         m = scale_inverse(code);
@@ -115,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) k_quantize8(const Quantize8Call c, u
     if (c.blocks) {
       float m = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m = fmaxf(m, col_inv[(threadIdx.x & 31) + 32 * k]);
+      for (int k = 0; k < 4; ++k) m = fmaxf(m, col_inv[lane + 32 * k]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const uint32_t code = scale_code(m);
@@ -125,39 +176,39 @@ __global__ void __launch_bounds__(kThreads) k_quantize8(const Quantize8Call c, u
   }
   if (c.codes) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       float inv = block;
-      if (!c.blocks) {
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(f[i][e]));
+      if (!COLS || !c.blocks) {
+        float m = row[i];
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const uint32_t code = scale_code(m);
         inv = scale_inverse(code);
         if (tx == 0 && i < nr) c.scales[(r0 + i) * c.s_row + (int64_t)tk * c.s_group] = (uint8_t)code;
       }
-      if (i < nr && nk > 0) put_codes(c.codes + (r0 + i) * c.ldc + k0, eight_codes(f[i], inv), nk);
+      if (i < nr && nk > 0)
+        put_codes(c.codes + (r0 + i) * c.ldc + k0,
+                  make_uint2(e4m3_four(f[i][0], f[i][1], f[i][2], f[i][3], inv),
+                             e4m3_four(f[i][4], f[i][5], f[i][6], f[i][7], inv)), nk);
     }
   }
-  if (c.codes_t) {
+  if (COLS && c.codes_t) {
+    // (every thread is past its reads of the tile as it came: the barriers above)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int col = tx * 8 + e;
       const float inv = c.blocks ? block : col_inv[col];
-      float t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = f[i][e];
-      *reinterpret_cast<uint2*>(turned + col * kGroup8 + ((ty ^ tx) << 3)) = eight_codes(t, inv);
+      *reinterpret_cast<uint32_t*>(tile + col * kGroup8 + ((ty ^ 2 * tx) << 2)) =
+          e4m3_four(f[0][e], f[1][e], f[2][e], f[3][e], inv);
     }
     __syncthreads();
     // eight threads write a column of the tile (128 bytes), 16 bytes each
 #pragma unroll
-    for (int pass = 0; pass < 4; ++pass) {
-      const int col = pass * 32 + (threadIdx.x >> 3), unit = (threadIdx.x & 7) * 2;
-      const int64_t k = (int64_t)tk * kGroup8 + col, r = (int64_t)tr * kGroup8 + unit * 8;
-      const uint2 a = *reinterpret_cast<const uint2*>(turned + col * kGroup8 + ((unit ^ (col >> 3)) << 3));
-      const uint2 b = *reinterpret_cast<const uint2*>(turned + col * kGroup8 + (((unit + 1) ^ (col >> 3)) << 3));
+    for (int pass = 0; pass < 2; ++pass) {
+      const int col = pass * 64 + (threadIdx.x >> 3), word = (threadIdx.x & 7) * 4, turn = 2 * (col >> 3);
+      const int64_t k = (int64_t)tk * kGroup8 + col, r = (int64_t)tr * kGroup8 + word * 4;
+      const uint2 a = *reinterpret_cast<const uint2*>(tile + col * kGroup8 + ((word ^ turn) << 2));
+      const uint2 b = *reinterpret_cast<const uint2*>(tile + col * kGroup8 + (((word + 2) ^ turn) << 2));
       if (k >= c.K) continue;
       uint8_t* to = c.codes_t + k * c.ldt + r;
       if (r + 16 <= c.R) {
@@ -170,6 +221,18 @@ __global__ void __launch_bounds__(kThreads) k_quantize8(const Quantize8Call c, u
   }
 }
 
+template <typename T, bool VEC, bool COLS>
+cudaError_t launch(const Quantize8Call& c, uint64_t tiles, uint32_t tiles_k, cudaStream_t st) {
+  constexpr size_t raw = VEC ? 0 : (size_t)kGroup8 * Load<T>::PITCH * sizeof(T), turned = COLS ? kGroup8 * kGroup8 : 0;
+  constexpr size_t smem = raw > turned ? raw : turned;
+  auto kern = k_quantize8<T, VEC, COLS>;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_early(kern, (unsigned)tiles, kThreads, smem, st, c, tiles_k);
+}
+
 template <typename T>
 cudaError_t run(const Quantize8Call& c, cudaStream_t st) {
   const uint64_t tiles_k = (uint64_t)((c.K + kGroup8 - 1) / kGroup8);
@@ -177,8 +240,10 @@ cudaError_t run(const Quantize8Call& c, cudaStream_t st) {
   if (tiles > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
   const bool vec = c.K % 8 == 0 && reinterpret_cast<uintptr_t>(c.x) % 16 == 0 &&
                    c.ld * (int64_t)sizeof(T) % 16 == 0;
-  return vec ? launch_early(k_quantize8<T, true>, (unsigned)tiles, kThreads, 0, st, c, (uint32_t)tiles_k)
-             : launch_early(k_quantize8<T, false>, (unsigned)tiles, kThreads, 0, st, c, (uint32_t)tiles_k);
+  const uint32_t tk = (uint32_t)tiles_k;
+  if (c.codes_t || c.blocks)
+    return vec ? launch<T, true, true>(c, tiles, tk, st) : launch<T, false, true>(c, tiles, tk, st);
+  return vec ? launch<T, true, false>(c, tiles, tk, st) : launch<T, false, false>(c, tiles, tk, st);
 }
 
 }  // namespace

@@ -18,11 +18,16 @@ namespace evo {
 
 constexpr int kGroup8 = 128;  // elements that share a scale
 
-// |x| for a group's maximum.
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= FLT_MAX ? a : 0.f;
+// Maxima of magnitudes.  A NaN is skipped (the other operand is taken).
+__device__ __forceinline__ float max_abs3(float a, float b, float c) { return fmaxf(fmaxf(fabsf(a), fabsf(b)), c); }
+__device__ __forceinline__ float max_abs8(const float (&f)[8]) {
+  return max_abs3(f[0], f[1], max_abs3(f[2], f[3], max_abs3(f[4], f[5], max_abs3(f[6], f[7], 0.f))));
 }
+__device__ __forceinline__ float max_abs(const float (&f)[8]) { return max_abs8(f); }
+__device__ __forceinline__ float max_abs(const float (&f)[4]) { return max_abs3(f[0], f[1], max_abs3(f[2], f[3], 0.f)); }
+// Where a maximum turns out infinite, infinities become NaN and the maximum is
+// taken again: NaN converts to the NaN code, infinity would convert to 448.
+__device__ __forceinline__ float infinity_to_nan(float x) { return fabsf(x) > FLT_MAX ? __int_as_float(0x7FFFFFFF) : x; }
 
 // The scale's exponent in 8 bits: from the exponent and mantissa of the
 // largest magnitude, 1.m 2^e with 448 = 1.75 * 2^8.
@@ -35,14 +40,19 @@ __device__ __forceinline__ uint32_t scale_code(float amax) {
 __device__ __forceinline__ float scale_inverse(uint32_t code) {
   return code < 254u ? __uint_as_float((254u - code) << 23) : 0.f;
 }
-// Codes of two elements times the inverse scale, the first in the low byte.
-// x * 0 is NaN for an infinite or NaN x and nothing otherwise; without it the
-// conversion would turn infinity into 448.
+// Codes of elements (none infinite) times the inverse scale, the first in the low
+// byte.  The product with a power of two is exact.
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi, float inverse) {
   uint16_t r;
-  const float a = fmaf(lo, 0.f, lo * inverse), b = fmaf(hi, 0.f, hi * inverse);
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  uint64_t in, two, by;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(in) : "f"(lo), "f"(hi));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(by) : "f"(inverse));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(two) : "l"(in), "l"(by));
+  asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n cvt.rn.satfinite.e4m3x2.f32 %0, b, a;\n}\n" : "=h"(r) : "l"(two));
   return r;
+}
+__device__ __forceinline__ uint32_t e4m3_four(float a, float b, float c, float d, float inverse) {
+  return e4m3_pair(a, b, inverse) | e4m3_pair(c, d, inverse) << 16;
 }
 
 }  // namespace evo
