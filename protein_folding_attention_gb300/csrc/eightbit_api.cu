@@ -163,7 +163,8 @@ evoattn_status evoattn_dropout_add(const evoattn_dropout_add_args* args, cudaStr
   c.u = operand(a.u);
   c.x1 = operand(a.out);
   c.C = C;
-  merge_axes(n, {c.x.p ? c.x.s : nullptr, c.u.s, c.x1.s, c.drop ? c.mask.s : nullptr});
+  std::copy(n, n + 3, c.given);
+  merge_axes(n, {c.x.p ? c.x.s : nullptr, c.u.s, c.x1.s});
   std::copy(n, n + 3, c.n);
   if (a.stream_dtype == EVOATTN_BF16)
     return cuda_status(a.dtype == EVOATTN_BF16 ? dropout_add_bf16(c, stream) : dropout_add_narrow(c, stream));
@@ -202,8 +203,8 @@ evoattn_status evoattn_norm8(const evoattn_norm8_args* args, cudaStream_t stream
   c.C = C;
   c.rms = a.kind == EVOATTN_NORM_RMS;
   c.eps = (float)a.eps;
-  merge_axes(n, {c.x.s, c.u.p ? c.u.s : nullptr, c.u.p ? c.x1.s : nullptr, c.codes_s, c.scales_s,
-                 c.drop ? c.mask.s : nullptr});
+  std::copy(n, n + 3, c.given);
+  merge_axes(n, {c.x.s, c.u.p ? c.u.s : nullptr, c.u.p ? c.x1.s : nullptr, c.codes_s, c.scales_s});
   std::copy(n, n + 3, c.n);
   if (sd == EVOATTN_BF16) return cuda_status(norm8_fwd_bf16(c, stream));
   return cuda_status(d == EVOATTN_BF16 ? norm8_fwd_mixed(c, stream) : norm8_fwd_f32(c, stream));
@@ -247,8 +248,8 @@ evoattn_status evoattn_norm8_bwd(const evoattn_norm8_bwd_args* args, cudaStream_
   c.C = C;
   c.rms = a.kind == EVOATTN_NORM_RMS;
   c.eps = (float)a.eps;
-  merge_axes(n, {c.x1.s, c.dy.s, c.dx.s, c.dx1.p ? c.dx1.s : nullptr, c.du.p ? c.du.s : nullptr,
-                 c.drop ? c.mask.s : nullptr});
+  std::copy(n, n + 3, c.given);
+  merge_axes(n, {c.x1.s, c.dy.s, c.dx.s, c.dx1.p ? c.dx1.s : nullptr, c.du.p ? c.du.s : nullptr});
   std::copy(n, n + 3, c.n);
   if (sd == EVOATTN_BF16) return cuda_status(norm8_bwd_bf16(c, stream));
   return cuda_status(d == EVOATTN_BF16 ? norm8_bwd_mixed(c, stream) : norm8_bwd_f32(c, stream));

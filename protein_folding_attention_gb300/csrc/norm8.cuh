@@ -10,7 +10,15 @@
 //
 // All of it is bound by memory: each operand is touched once, a row stays in
 // registers between its sums and its stores, and the mask is drawn again
-// wherever it is needed (philox.cuh).
+// wherever it is needed (philox.cuh).  What the memory rate leaves at bf16 is some
+// 30 instructions per element, of which a block of the generator for four
+// elements takes 15; so
+// - a thread holds T rows at once (their loads in flight together, their sums
+//   interleaved), and where rows share a mask these are T rows that do, so that
+//   it is drawn once for them;
+// - divisions by extents are multiplications, and operands whose rows lie evenly
+//   spaced (FLAT) need none;
+// - arithmetic goes over pairs of fp32.
 //
 // A row lies over LANES threads.  Rows of whole 16-byte units (C % 8 == 0,
 // aligned): a thread holds parts of 8 consecutive channels, so 16 neighbouring
@@ -23,6 +31,7 @@
 
 #include <algorithm>
 
+#include "common.cuh"
 #include "launch.cuh"
 #include "norm8.h"
 #include "philox.cuh"
@@ -31,12 +40,32 @@
 namespace evo {
 namespace norm8 {
 
+// q = r / d for r < 2^31, by the high half of a product.
+struct Divide {
+  uint32_t d, mul, shift;
+};
+__device__ __forceinline__ uint32_t quotient(const Divide& v, uint32_t r) {
+  return (uint32_t)((uint64_t)r * v.mul >> 31 >> v.shift);
+}
+inline Divide divide_by(uint32_t d) {
+  uint32_t s = 0;
+  while (((uint64_t)1 << s) < d) ++s;  // 2^s >= d: r * (2^(31+s) / d + 1) is off by r / 2^(31+s) < 1 / d
+  return Divide{d, (uint32_t)(((uint64_t)1 << (31 + s)) / d + 1), s};
+}
+
 struct Params {
   uint32_t rows;
-  uint32_t n1, n2;  // row r = (b * n1 + i) * n2 + j
-  int C, groups;
+  Divide n1, n2;     // row r = (b * n1 + i) * n2 + j, axes merged where the operands allow it
+  Divide I, J;       // the same on the axes as they were given, for the mask
+  // Groups of T rows: consecutive ones, or (along_i) T neighbours along axis I
+  // with the same j, which share a mask row.
+  bool along_i, shared;  // shared: some rows share a mask row
+  uint32_t blocks_i;     // ceil(I / T)
+  Divide by_blocks_i;
+  uint32_t groups;       // of rows
+  int C;
   float inv_c, eps;
-  bool rms;
+  bool rms, drop;
   DropMask mask;
   RowOperand x, u, x1, dx1, dy, dx, du;
   uint8_t* codes;
@@ -47,19 +76,45 @@ struct Params {
   float *dgamma, *dbeta, *ws;
 };
 
+// A row of the operands.
+template <bool FLAT>
 struct Row {
   uint32_t b, i, j;
+  __device__ __forceinline__ Row(const Params& p, uint32_t r) {
+    if (FLAT) {
+      j = r;
+      return;
+    }
+    const uint32_t q = quotient(p.n2, r);
+    j = r - q * p.n2.d;
+    b = quotient(p.n1, q);
+    i = q - b * p.n1.d;
+  }
   __device__ __forceinline__ int64_t at(const int64_t (&s)[3]) const {
-    return (int64_t)b * s[0] + (int64_t)i * s[1] + (int64_t)j * s[2];
+    return FLAT ? (int64_t)j * s[2] : (int64_t)b * s[0] + (int64_t)i * s[1] + (int64_t)j * s[2];
   }
 };
-__device__ __forceinline__ Row row_of(const Params& p, uint32_t r) {
-  Row w;
-  const uint32_t q = p.n2 == 1 ? r : r / p.n2;
-  w.j = r - q * p.n2;
-  w.b = p.n1 == 1 ? q : q / p.n1;
-  w.i = q - w.b * p.n1;
-  return w;
+
+// The rows of group o (p.rows: there is none).
+template <int T>
+__device__ __forceinline__ void rows_of(const Params& p, uint32_t o, uint32_t (&r)[T]) {
+  if (o >= p.groups) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) r[t] = p.rows;
+  } else if (p.along_i) {
+    const uint32_t q = quotient(p.J, o), j = o - q * p.J.d, b = quotient(p.by_blocks_i, q),
+                   i = (q - b * p.blocks_i) * T;
+#pragma unroll
+    for (int t = 0; t < T; ++t) r[t] = i + t < p.I.d ? (b * p.I.d + i + t) * p.J.d + j : p.rows;
+  } else {
+#pragma unroll
+    for (int t = 0; t < T; ++t) r[t] = min(o * T + t, p.rows);
+  }
+}
+__device__ __forceinline__ uint32_t mask_row(const Params& p, uint32_t r) {
+  if (!p.shared) return r;
+  const uint32_t q = quotient(p.J, r), b = quotient(p.I, q);
+  return (uint32_t)(b * p.mask.s[0] + (q - b * p.I.d) * p.mask.s[1] + (r - q * p.J.d) * p.mask.s[2]);
 }
 
 // ---------------------------------------------------------------------------
@@ -151,9 +206,7 @@ struct Lay {
   static __device__ __forceinline__ int chan(int lane, int k) {
     return VEC ? k * SPAN + lane * 8 : k * SPAN + (lane >> 5) * 128 + (lane & 31);
   }
-  // channels from there on (VEC: as a truth value, parts are whole)
-  static __device__ __forceinline__ int left(int C, int c) { return C - c; }
-  static __device__ __forceinline__ bool has(int C, int c, int e) { return VEC ? c < C : c + 32 * e < C; }
+    static __device__ __forceinline__ bool has(int C, int c, int e) { return VEC ? c < C : c + 32 * e < C; }
   static __device__ __forceinline__ int off(int e) { return VEC ? e : 32 * e; }
 };
 
@@ -174,188 +227,297 @@ __device__ __forceinline__ void store_part(void* base, int64_t at, int c, int C,
     put(p, f, on ? C - c : 0);
 }
 
-// Keep bits of a thread's part (bit e: element e).
-template <bool VEC>
-__device__ __forceinline__ uint32_t keep_bits(const PhiloxKey& key, uint32_t threshold, int c, uint32_t row) {
+// The factor of each element of a thread's part: 0 or 1 / (1 - p).
+template <bool VEC, int E>
+__device__ __forceinline__ void mask_factors(const PhiloxKey& key, const DropMask& m, int c, uint32_t row,
+                                             float (&f)[E]) {
   if constexpr (VEC) {
     const uint32_t g = (uint32_t)c >> 2;
-    return philox_keep4(key, threshold, g, row) | philox_keep4(key, threshold, g + 1, row) << 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 w = philox(key, g + h, row);
+      f[4 * h] = w.x >= m.threshold ? m.scale : 0.f;
+      f[4 * h + 1] = w.y >= m.threshold ? m.scale : 0.f;
+      f[4 * h + 2] = w.z >= m.threshold ? m.scale : 0.f;
+      f[4 * h + 3] = w.w >= m.threshold ? m.scale : 0.f;
+    }
   } else {
     // the warp's 128 channels are 32 blocks, one per lane; element e of this
     // lane is word lane % 4 of block 8 e + lane / 4
     const int lane = threadIdx.x & 31;
-    const uint32_t mine = philox_keep4(key, threshold, ((uint32_t)(c - lane) >> 2) + lane, row);
-    uint32_t bits = 0;
+    const uint32_t mine = philox_keep4(key, m.threshold, ((uint32_t)(c - lane) >> 2) + lane, row);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      bits |= (__shfl_sync(0xffffffffu, mine, 8 * e + (lane >> 2)) >> (lane & 3) & 1u) << e;
-    return bits;
+      f[e] = (__shfl_sync(0xffffffffu, mine, 8 * e + (lane >> 2)) >> (lane & 3) & 1u) ? m.scale : 0.f;
   }
 }
+// f * u, 0 where the factor is 0 whatever u is.
+__device__ __forceinline__ float masked(float f, float u) { return f != 0.f ? f * u : 0.f; }
 
-// Sum over the LANES threads of a row, the same in all of them.  Rows wider than
-// a warp go through shared memory; `slot` alternates between calls.
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v, float (*buf)[32], int slot) {
+// Sums over the LANES threads of each of T rows, the same in all of them.  Rows
+// wider than a warp go through shared memory: one barrier for the T of them, and
+// `slot` differs between neighbouring calls.
+template <int LANES, int T>
+__device__ __forceinline__ void row_sums(float (&v)[T], float (*buf)[T][8], int slot) {
 #pragma unroll
-  for (int o = (LANES < 32 ? LANES : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = (LANES < 32 ? LANES : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int t = 0; t < T; ++t) v[t] += __shfl_xor_sync(0xffffffffu, v[t], o);
   if constexpr (LANES > 32) {
     constexpr int W = LANES / 32;
     const int warp = threadIdx.x >> 5, first = warp / W * W;
-    if ((threadIdx.x & 31) == 0) buf[slot][warp] = v;
-    __syncthreads();
-    v = buf[slot][first];
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int k = 1; k < W; ++k) v += buf[slot][first + k];
+      for (int t = 0; t < T; ++t) buf[slot][t][warp] = v[t];
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      v[t] = buf[slot][t][first];
+#pragma unroll
+      for (int k = 1; k < W; ++k) v[t] += buf[slot][t][first + k];
+    }
   }
-  return v;
+}
+
+constexpr int kThreads = 256;
+
+// gamma or beta (1 or 0 where there is none, and beyond C) of all N channels that
+// the threads of a row have places for, in shared memory.
+template <int N>
+__device__ __forceinline__ void load_params(float* to, const float* v, int C, float none) {
+  for (int c = threadIdx.x; c < N; c += kThreads) to[c] = v && c < C ? v[c] : none;
+}
+__device__ __forceinline__ void get_params(const float* from, int c, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(from + c), b = *reinterpret_cast<const float4*>(from + c + 4);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ void get_params(const float* from, int c, float (&f)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = from[c + 32 * e];
+}
+
+// Pairs of fp32.
+__device__ __forceinline__ float2 pair(const float* f) { return make_float2(f[0], f[1]); }
+__device__ __forceinline__ void put_pair(float* f, float2 v) { f[0] = v.x; f[1] = v.y; }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Rows minus their mean (layer norm), and 1 / sqrt(variance + eps).
+template <int LANES, int PARTS, bool VEC, int T, int E>
+__device__ __forceinline__ void centre(const Params& p, int lane, float (&x)[T][PARTS][E], float (&rstd)[T],
+                                       float (*buf)[T][8]) {
+  using L = Lay<LANES, VEC>;
+  float mean[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) mean[t] = 0.f;
+  if (!p.rms) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      float2 s = both(0.f);
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+        for (int e = 0; e < E; e += 2) s = add2(s, pair(&x[t][k][e]));
+      mean[t] = s.x + s.y;
+    }
+    row_sums<LANES, T>(mean, buf, 0);
+#pragma unroll
+    for (int t = 0; t < T; ++t) mean[t] *= p.inv_c;
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    float2 s = both(0.f);
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+      const int c = L::chan(lane, k);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 m = make_float2(L::has(p.C, c, e) ? -mean[t] : 0.f, L::has(p.C, c, e + 1) ? -mean[t] : 0.f);
+        const float2 d = add2(pair(&x[t][k][e]), m);
+        put_pair(&x[t][k][e], d);
+        s = fma2(d, d, s);
+      }
+    }
+    rstd[t] = s.x + s.y;
+  }
+  row_sums<LANES, T>(rstd, buf, 1);
+#pragma unroll
+  for (int t = 0; t < T; ++t) rstd[t] = rsqrtf(rstd[t] * p.inv_c + p.eps);
 }
 
 // ---------------------------------------------------------------------------
 // dropout and residual add
 // ---------------------------------------------------------------------------
-// Threads of a warp take consecutive parts of consecutive rows; nothing is
-// shared between them.
-template <typename S, typename IO, bool VEC>
-__global__ void __launch_bounds__(256) k_dropout_add(const Params p, uint64_t items, uint32_t per_row, bool drop) {
+// A thread takes one part of each of T rows; nothing is shared between threads.
+template <typename S, typename IO, bool VEC, bool FLAT, int T>
+__global__ void __launch_bounds__(kThreads) k_dropout_add(const Params p, Divide parts, uint32_t items) {
   wait_for_earlier_work();
   let_next_start();
   PhiloxKey key{};
-  if (drop) key = philox_key(p.mask);
-  const uint64_t id = (uint64_t)blockIdx.x * (VEC ? 256 : 8) + (VEC ? threadIdx.x : threadIdx.x >> 5);
-  const bool on = id < items;
-  const uint32_t r = on ? ((items >> 32) ? (uint32_t)(id / per_row) : (uint32_t)id / per_row) : 0;
-  const int at = on ? (int)(id - (uint64_t)r * per_row) : 0;
-  const int c = VEC ? at * 8 : at * 128 + (threadIdx.x & 31);
+  if (p.drop) key = philox_key(p.mask);
   constexpr int E = VEC ? 8 : 4;
-  const Row w = row_of(p, r);
-  Raw<IO, VEC> ru;
-  Raw<S, VEC> rx;
-  load_part<IO, VEC>(ru, p.u.p, w.at(p.u.s), c, p.C, on);
-  if (p.x.p) load_part<S, VEC>(rx, p.x.p, w.at(p.x.s), c, p.C, on);
-  float f[E], x[E];
-  ru.get(f);
-  if (drop) {
-    const uint32_t bits = keep_bits<VEC>(key, p.mask.threshold, c, (uint32_t)w.at(p.mask.s));
+  const uint32_t id = VEC ? blockIdx.x * kThreads + threadIdx.x : blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (id >= items) return;  // (whole warps, where a warp works together)
+  const uint32_t o = quotient(parts, id), part = id - o * parts.d;
+  const int c = VEC ? (int)part * 8 : (int)part * 128 + (threadIdx.x & 31);
+  uint32_t r[T];
+  rows_of<T>(p, o, r);
+  Raw<IO, VEC> ru[T];
+  Raw<S, VEC> rx[T];
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = (bits >> e & 1) ? f[e] * p.mask.scale : 0.f;
+  for (int t = 0; t < T; ++t) {
+    const bool on = r[t] < p.rows;
+    const Row<FLAT> w(p, on ? r[t] : 0);
+    load_part<IO, VEC>(ru[t], p.u.p, w.at(p.u.s), c, p.C, on);
+    if (p.x.p) load_part<S, VEC>(rx[t], p.x.p, w.at(p.x.s), c, p.C, on);
   }
-  if (p.x.p) {
-    rx.get(x);
+  float m[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] += x[e];
+  for (int e = 0; e < E; ++e) m[e] = 1.f;
+  uint32_t drawn = 0xFFFFFFFFu;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const bool on = r[t] < p.rows;
+    const Row<FLAT> w(p, on ? r[t] : 0);
+    float f[E], x[E];
+    ru[t].get(f);
+    if (p.drop) {
+      const uint32_t row = mask_row(p, on ? r[t] : 0);
+      if (row != drawn) mask_factors<VEC>(key, p.mask, c, row, m);
+      drawn = row;
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = masked(m[e], f[e]);
+    }
+    if (p.x.p) {
+      rx[t].get(x);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) put_pair(&f[e], add2(pair(&f[e]), pair(&x[e])));
+    }
+    store_part<S, VEC>(p.x1.p, w.at(p.x1.s), c, p.C, on, f);
   }
-  store_part<S, VEC>(p.x1.p, w.at(p.x1.s), c, p.C, on, f);
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 128;
-
-template <typename S, typename IO, int LANES, int PARTS, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_norm8_fwd(const Params p, int turns, bool drop) {
+template <typename S, typename IO, int LANES, int PARTS, bool VEC, bool FLAT, int T>
+__global__ void __launch_bounds__(kThreads) k_norm8_fwd(const Params p) {
   using L = Lay<LANES, VEC>;
   constexpr int E = L::E, PER = kThreads / LANES;
-  __shared__ float sums[2][32];
+  __shared__ float sums[2][T][8];
+  constexpr int N = PARTS * L::SPAN;  // channels that the threads of a row have places for
+  __shared__ __align__(16) float prm[2 * N];  // gamma, beta
+  float* const prm_b = prm + N;
   wait_for_earlier_work();
   let_next_start();
   const int lane = threadIdx.x % LANES;
-  PhiloxKey key{};
-  if (drop) key = philox_key(p.mask);
-  uint32_t r = (uint32_t)blockIdx.x * (uint32_t)(PER * turns) + threadIdx.x / LANES;
-#pragma unroll 1
-  for (int t = 0; t < turns; ++t, r += PER) {
-    if (r - threadIdx.x / LANES >= p.rows) break;  // (the same for the whole CTA)
-    const bool on = r < p.rows;
-    const Row w = row_of(p, on ? r : 0);
-    Raw<S, VEC> rx[PARTS];
-    Raw<IO, VEC> ru[PARTS];
+  uint32_t r[T];
+  rows_of<T>(p, blockIdx.x * PER + threadIdx.x / LANES, r);
+  Raw<S, VEC> rx[T][PARTS];
+  Raw<IO, VEC> ru[T][PARTS];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const bool on = r[t] < p.rows;
+    const Row<FLAT> w(p, on ? r[t] : 0);
     const int64_t ax = w.at(p.x.s), au = w.at(p.u.s);
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) {
-      load_part<S, VEC>(rx[k], p.x.p, ax, L::chan(lane, k), p.C, on);
-      if (p.u.p) load_part<IO, VEC>(ru[k], p.u.p, au, L::chan(lane, k), p.C, on);
+      load_part<S, VEC>(rx[t][k], p.x.p, ax, L::chan(lane, k), p.C, on);
+      if (p.u.p) load_part<IO, VEC>(ru[t][k], p.u.p, au, L::chan(lane, k), p.C, on);
     }
-    float x[PARTS][E];
-    float sum = 0.f;
-    const uint32_t mrow = drop ? (uint32_t)w.at(p.mask.s) : 0u;
+  }
+  load_params<N>(prm, p.gamma, p.C, 1.f);
+  load_params<N>(prm_b, p.beta, p.C, 0.f);
+  PhiloxKey key{};
+  if (p.drop) key = philox_key(p.mask);
+  __syncthreads();
+  float x[T][PARTS][E];
+  if (p.u.p) {
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) {
       const int c = L::chan(lane, k);
-      rx[k].get(x[k]);
-      if (p.u.p) {
+      float m[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) m[e] = 1.f;
+      uint32_t drawn = 0xFFFFFFFFu;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const bool on = r[t] < p.rows;
         float f[E];
-        ru[k].get(f);
-        if (drop) {
-          const uint32_t bits = keep_bits<VEC>(key, p.mask.threshold, c, mrow);
+        ru[t][k].get(f);
+        if (p.drop) {
+          const uint32_t row = mask_row(p, on ? r[t] : 0);
+          if (row != drawn) mask_factors<VEC>(key, p.mask, c, row, m);
+          drawn = row;
 #pragma unroll
-          for (int e = 0; e < E; ++e) f[e] = (bits >> e & 1) ? f[e] * p.mask.scale : 0.f;
+          for (int e = 0; e < E; ++e) f[e] = masked(m[e], f[e]);
         }
+        rx[t][k].get(x[t][k]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[k][e] += f[e];
-        store_part<S, VEC>(p.x1.p, w.at(p.x1.s), c, p.C, on, x[k]);
+        for (int e = 0; e < E; e += 2) put_pair(&x[t][k][e], add2(pair(&x[t][k][e]), pair(&f[e])));
+        const Row<FLAT> w(p, on ? r[t] : 0);
+        store_part<S, VEC>(p.x1.p, w.at(p.x1.s), c, p.C, on, x[t][k]);
       }
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum += x[k][e];
     }
-    float mean = 0.f;
-    if (!p.rms) mean = row_sum<LANES>(sum, sums, 0) * p.inv_c;
-    float sq = 0.f;
+  } else {
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k)
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = L::has(p.C, L::chan(lane, k), e) ? x[k][e] - mean : 0.f;
-        x[k][e] = d;
-        sq = fmaf(d, d, sq);
-      }
-    const float rstd = rsqrtf(row_sum<LANES>(sq, sums, 1) * p.inv_c + p.eps);
-    const int64_t ac = w.at(p.codes_s), as = w.at(p.scales_s);
+      for (int k = 0; k < PARTS; ++k) rx[t][k].get(x[t][k]);
+  }
+  float rstd[T];
+  centre<LANES, PARTS, VEC, T, E>(p, lane, x, rstd, sums);
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k) {
-      const int c = L::chan(lane, k);
+  for (int k = 0; k < PARTS; ++k) {
+    const int c = L::chan(lane, k);
+    float ga[E], be[E];
+    get_params(prm, c, ga);
+    get_params(prm_b, c, be);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const bool has = L::has(p.C, c, e);
-        float y = x[k][e] * rstd;
-        if (has && p.gamma) y *= p.gamma[c + L::off(e)];
-        if (has && p.beta) y += p.beta[c + L::off(e)];
-        x[k][e] = y;
+    for (int t = 0; t < T; ++t) {
+      const bool on = r[t] < p.rows;
+      const Row<FLAT> w(p, on ? r[t] : 0);
+      float(&y)[E] = x[t][k];
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        put_pair(&y[e], fma2(mul2(pair(&y[e]), both(rstd[t])), pair(&ga[e]), pair(&be[e])));
+      if (!VEC) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = L::has(p.C, c, e) ? y[e] : 0.f;
       }
       const auto group_maximum = [&] {
-        float m = max_abs(x[k]);
+        float m = max_abs(y);
 #pragma unroll
         for (int o = (VEC ? (LANES < 16 ? LANES : 16) : 32) / 2; o > 0; o >>= 1)
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         return m;
       };
+      if (VEC && c >= p.C) {  // (beta of a part beyond the row is 0, and so is y)
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = 0.f;
+      }
       float amax = group_maximum();
       if (__any_sync(0xffffffffu, amax > FLT_MAX)) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[k][e] = infinity_to_nan(x[k][e]);
+        for (int e = 0; e < E; ++e) y[e] = infinity_to_nan(y[e]);
         amax = group_maximum();
       }
       const uint32_t code = scale_code(amax);
       const float inv = scale_inverse(code);
+      const int64_t ac = w.at(p.codes_s);
       if constexpr (VEC) {
-        const uint2 q = make_uint2(e4m3_four(x[k][0], x[k][1], x[k][2], x[k][3], inv),
-                                   e4m3_four(x[k][4], x[k][5], x[k][6], x[k][7], inv));
-        if (on && c < p.C) {
-          *reinterpret_cast<uint2*>(p.codes + ac + c) = q;
-          if ((c & 127) == 0) p.scales[as + (int64_t)(c >> 7) * p.scales_g] = (uint8_t)code;
-        }
+        if (on && c < p.C)
+          *reinterpret_cast<uint2*>(p.codes + ac + c) =
+              make_uint2(e4m3_four(y[0], y[1], y[2], y[3], inv), e4m3_four(y[4], y[5], y[6], y[7], inv));
       } else {
-        const uint32_t q = e4m3_four(x[k][0], x[k][1], x[k][2], x[k][3], inv);
-        if (on) {
+        const uint32_t q = e4m3_four(y[0], y[1], y[2], y[3], inv);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + 32 * e < p.C) p.codes[ac + c + 32 * e] = (uint8_t)(q >> 8 * e);
-          if ((c & 127) == 0 && c < p.C) p.scales[as + (int64_t)(c >> 7) * p.scales_g] = (uint8_t)code;
-        }
+        for (int e = 0; e < 4; ++e)
+          if (on && c + 32 * e < p.C) p.codes[ac + c + 32 * e] = (uint8_t)(q >> 8 * e);
       }
+      if (on && (c & 127) == 0 && c < p.C)
+        p.scales[w.at(p.scales_s) + (int64_t)(c >> 7) * p.scales_g] = (uint8_t)code;
     }
-    if constexpr (LANES > 32) __syncthreads();  // the next row's sums
   }
 }
 
@@ -365,98 +527,118 @@ __global__ void __launch_bounds__(kThreads) k_norm8_fwd(const Params p, int turn
 // Persistent: a thread adds the parameter gradients of its channels over all
 // its rows in registers, a CTA adds its row groups in order and leaves one
 // partial sum, and a second kernel adds those in order.
-template <typename S, typename IO, int LANES, int PARTS, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_norm8_bwd(const Params p, uint32_t turns, bool drop) {
+template <typename S, typename IO, int LANES, int PARTS, bool VEC, bool FLAT, int T>
+__global__ void __launch_bounds__(kThreads, 2) k_norm8_bwd(const Params p, uint32_t turns) {
   using L = Lay<LANES, VEC>;
   constexpr int E = L::E, PER = kThreads / LANES;
-  __shared__ float sums[4][32];
-  extern __shared__ float part[];  // [2][C]
+  __shared__ float sums[2][T][8], sums2[2][T][8];
+  constexpr int N = PARTS * L::SPAN;  // channels that the threads of a row have places for (C at least)
+  __shared__ __align__(16) float prm[2 * N];  // gamma; in the end the parameters' gradients [2][C]
   wait_for_earlier_work();
   let_next_start();
   const int lane = threadIdx.x % LANES;
+  load_params<N>(prm, p.gamma, p.C, 1.f);
   PhiloxKey key{};
-  if (drop) key = philox_key(p.mask);
+  if (p.drop) key = philox_key(p.mask);
+  __syncthreads();
   float ag[PARTS][E], ab[PARTS][E];
 #pragma unroll
   for (int k = 0; k < PARTS; ++k)
 #pragma unroll
     for (int e = 0; e < E; ++e) ag[k][e] = ab[k][e] = 0.f;
-  uint64_t r = (uint64_t)blockIdx.x * PER + threadIdx.x / LANES;
 #pragma unroll 1
-  for (uint32_t t = 0; t < turns; ++t, r += (uint64_t)gridDim.x * PER) {
-    const bool on = r < p.rows;
-    const Row w = row_of(p, on ? (uint32_t)r : 0);
-    Raw<S, VEC> rx[PARTS], rd[PARTS];
-    Raw<IO, VEC> ry[PARTS];
-    const int64_t ax = w.at(p.x1.s), ad = w.at(p.dx1.s), ay = w.at(p.dy.s);
+  for (uint32_t turn = 0; turn < turns; ++turn) {
+    uint32_t r[T];
+    rows_of<T>(p, (turn * gridDim.x + blockIdx.x) * PER + threadIdx.x / LANES, r);
+    Raw<S, VEC> rx[T][PARTS], rd[T][PARTS];
+    Raw<IO, VEC> ry[T][PARTS];
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k) {
-      const int c = L::chan(lane, k);
-      load_part<S, VEC>(rx[k], p.x1.p, ax, c, p.C, on);
-      load_part<IO, VEC>(ry[k], p.dy.p, ay, c, p.C, on);
-      if (p.dx1.p) load_part<S, VEC>(rd[k], p.dx1.p, ad, c, p.C, on);
+    for (int t = 0; t < T; ++t) {
+      const bool on = r[t] < p.rows;
+      const Row<FLAT> w(p, on ? r[t] : 0);
+      const int64_t ax = w.at(p.x1.s), ad = w.at(p.dx1.s), ay = w.at(p.dy.s);
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k) {
+        const int c = L::chan(lane, k);
+        load_part<S, VEC>(rx[t][k], p.x1.p, ax, c, p.C, on);
+        load_part<IO, VEC>(ry[t][k], p.dy.p, ay, c, p.C, on);
+        if (p.dx1.p) load_part<S, VEC>(rd[t][k], p.dx1.p, ad, c, p.C, on);
+      }
     }
-    float h[PARTS][E], g[PARTS][E];
-    float sum = 0.f;
+    float h[T][PARTS][E], rstd[T], m1[T], m2[T];
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k) {
-      rx[k].get(h[k]);
-      ry[k].get(g[k]);
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += h[k][e];
-    }
-    float mean = 0.f;
-    if (!p.rms) mean = row_sum<LANES>(sum, sums, 0) * p.inv_c;
-    float sq = 0.f;
+      for (int k = 0; k < PARTS; ++k) rx[t][k].get(h[t][k]);
+    centre<LANES, PARTS, VEC, T, E>(p, lane, h, rstd, sums);
+    float g[T][PARTS][E];
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k)
+    for (int t = 0; t < T; ++t) {
+      float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = L::has(p.C, L::chan(lane, k), e) ? h[k][e] - mean : 0.f;
-        h[k][e] = d;
-        sq = fmaf(d, d, sq);
-      }
-    const float rstd = rsqrtf(row_sum<LANES>(sq, sums, 1) * p.inv_c + p.eps);
-    float m1 = 0.f, m2 = 0.f;
+      for (int k = 0; k < PARTS; ++k) {
+        ry[t][k].get(g[t][k]);
+        float ga[E];
+        get_params(prm, L::chan(lane, k), ga);
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k)
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = L::chan(lane, k) + L::off(e);
-        h[k][e] *= rstd;
-        ag[k][e] = fmaf(g[k][e], h[k][e], ag[k][e]);
-        ab[k][e] += g[k][e];
-        if (p.gamma && L::has(p.C, L::chan(lane, k), e)) g[k][e] *= p.gamma[c];
-        m1 = fmaf(g[k][e], h[k][e], m1);
-        m2 += g[k][e];
-      }
-    m1 = row_sum<LANES>(m1, sums, 2) * p.inv_c;
-    m2 = p.rms ? 0.f : row_sum<LANES>(m2, sums, 3) * p.inv_c;
-    const uint32_t mrow = drop ? (uint32_t)w.at(p.mask.s) : 0u;
-#pragma unroll
-    for (int k = 0; k < PARTS; ++k) {
-      const int c = L::chan(lane, k);
-      float d[E];
-      if (p.dx1.p) {
-        rd[k].get(d);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) d[e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) d[e] = fmaf(rstd, fmaf(-h[k][e], m1, g[k][e]) - m2, d[e]);
-      store_part<S, VEC>(p.dx.p, w.at(p.dx.s), c, p.C, on, d);
-      if (p.du.p) {
-        if (drop) {
-          const uint32_t bits = keep_bits<VEC>(key, p.mask.threshold, c, mrow);
-#pragma unroll
-          for (int e = 0; e < E; ++e) d[e] = (bits >> e & 1) ? d[e] * p.mask.scale : 0.f;
+        for (int e = 0; e < E; e += 2) {
+          const float2 hh = mul2(pair(&h[t][k][e]), both(rstd[t])), gg = pair(&g[t][k][e]);
+          put_pair(&h[t][k][e], hh);
+          put_pair(&ag[k][e], fma2(gg, hh, pair(&ag[k][e])));
+          put_pair(&ab[k][e], add2(gg, pair(&ab[k][e])));
+          const float2 ee = mul2(gg, pair(&ga[e]));
+          put_pair(&g[t][k][e], ee);
+          s1 = fma2(ee, hh, s1);
+          s2 = add2(ee, s2);
         }
-        store_part<IO, VEC>(p.du.p, w.at(p.du.s), c, p.C, on, d);
+      }
+      m1[t] = s1.x + s1.y;
+      m2[t] = s2.x + s2.y;
+    }
+    row_sums<LANES, T>(m1, sums2, 0);
+    if (!p.rms) row_sums<LANES, T>(m2, sums2, 1);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      m1[t] *= -p.inv_c;
+      m2[t] = p.rms ? 0.f : m2[t] * -p.inv_c;
+    }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+      const int c = L::chan(lane, k);
+      float m[E];
+      uint32_t drawn = 0xFFFFFFFFu;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const bool on = r[t] < p.rows;
+        const Row<FLAT> w(p, on ? r[t] : 0);
+        float d[E];
+        if (p.dx1.p) {
+          rd[t][k].get(d);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) d[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = fma2(pair(&h[t][k][e]), both(m1[t]), add2(pair(&g[t][k][e]), both(m2[t])));
+          put_pair(&d[e], fma2(both(rstd[t]), v, pair(&d[e])));
+        }
+        store_part<S, VEC>(p.dx.p, w.at(p.dx.s), c, p.C, on, d);
+        if (p.du.p) {
+          if (p.drop) {
+            const uint32_t row = mask_row(p, on ? r[t] : 0);
+            if (row != drawn) mask_factors<VEC>(key, p.mask, c, row, m);
+            drawn = row;
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = masked(m[e], d[e]);
+          }
+          store_part<IO, VEC>(p.du.p, w.at(p.du.s), c, p.C, on, d);
+        }
       }
     }
-    if constexpr (LANES > 32) __syncthreads();  // the next row's sums
+    if constexpr (LANES > 32) __syncthreads();  // the next rows' sums
   }
+  __syncthreads();
   // the row groups of the CTA, one after another
 #pragma unroll 1
   for (int q = 0; q < PER; ++q) {
@@ -467,19 +649,19 @@ __global__ void __launch_bounds__(kThreads) k_norm8_bwd(const Params p, uint32_t
         for (int e = 0; e < E; ++e) {
           const int c = L::chan(lane, k) + L::off(e);
           if (c < p.C) {
-            part[c] = q ? part[c] + ag[k][e] : ag[k][e];
-            part[p.C + c] = q ? part[p.C + c] + ab[k][e] : ab[k][e];
+            prm[c] = q ? prm[c] + ag[k][e] : ag[k][e];
+            prm[p.C + c] = q ? prm[p.C + c] + ab[k][e] : ab[k][e];
           }
         }
     __syncthreads();
   }
   float* out = p.ws + (int64_t)blockIdx.x * 2 * p.C;
-  for (int c = threadIdx.x; c < 2 * p.C; c += kThreads) out[c] = part[c];
+  for (int c = threadIdx.x; c < 2 * p.C; c += kThreads) out[c] = prm[c];
 }
 
 // Partial sums of `count` CTAs: 8 warps share 32 columns, each a stretch of the
 // CTAs, joined in order.
-template <typename T>
+template <typename S>
 __global__ void __launch_bounds__(256) k_norm8_reduce(const Params p, int count) {
   __shared__ float buf[8][32];
   wait_for_earlier_work();
@@ -511,16 +693,24 @@ inline bool aligned16(const RowOperand& o, size_t size) {
   return true;
 }
 
-inline Params params_of(const Norm8Call& c) {
+inline Params params_of(const Norm8Call& c, int T) {
   Params p{};
   p.rows = (uint32_t)c.n[0] * (uint32_t)c.n[1] * (uint32_t)c.n[2];
-  p.n1 = (uint32_t)c.n[1];
-  p.n2 = (uint32_t)c.n[2];
+  p.n1 = divide_by((uint32_t)c.n[1]);
+  p.n2 = divide_by((uint32_t)c.n[2]);
+  p.I = divide_by((uint32_t)c.given[1]);
+  p.J = divide_by((uint32_t)c.given[2]);
+  const auto shares = [&](int k) { return c.drop && c.given[k] > 1 && c.mask.s[k] == 0; };
+  p.shared = shares(0) || shares(1) || shares(2);
+  p.along_i = shares(1) && !shares(2);
+  p.blocks_i = (uint32_t)(c.given[1] + T - 1) / T;
+  p.by_blocks_i = divide_by(p.blocks_i);
+  p.groups = p.along_i ? (uint32_t)c.given[0] * p.blocks_i * (uint32_t)c.given[2] : (p.rows + T - 1) / T;
   p.C = c.C;
-  p.groups = (c.C + kGroup8 - 1) / kGroup8;
   p.inv_c = 1.0f / (float)c.C;
   p.eps = c.eps;
   p.rms = c.rms;
+  p.drop = c.drop;
   p.mask = c.mask;
   p.x = c.x; p.u = c.u; p.x1 = c.x1;
   p.dx1 = c.dx1; p.dy = c.dy; p.dx = c.dx; p.du = c.du;
@@ -531,52 +721,68 @@ inline Params params_of(const Norm8Call& c) {
   return p;
 }
 
-template <typename S, typename IO>
-cudaError_t run_dropout(const Norm8Call& c, cudaStream_t st) {
-  const Params p = params_of(c);
-  const bool vec = c.C % 8 == 0 && aligned16(c.x, sizeof(S)) && aligned16(c.x1, sizeof(S)) &&
-                   aligned16(c.u, sizeof(IO));
-  const uint32_t per_row = vec ? (uint32_t)c.C / 8 : (uint32_t)p.groups;
-  const uint64_t items = (uint64_t)p.rows * per_row, per_cta = vec ? 256 : 8;
-  const uint64_t grid = (items + per_cta - 1) / per_cta;
-  if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
-  return vec ? launch_early(k_dropout_add<S, IO, true>, (unsigned)grid, 256, 0, st, p, items, per_row, c.drop)
-             : launch_early(k_dropout_add<S, IO, false>, (unsigned)grid, 256, 0, st, p, items, per_row, c.drop);
+// Calls f(std::integral_constant<bool, v>).
+template <typename F>
+cudaError_t by_flag(bool v, F&& f) {
+  return v ? f(std::integral_constant<bool, true>{}) : f(std::integral_constant<bool, false>{});
 }
 
-// The threads of a row and the parts of each, by the channel count: up to 32
-// channels per thread, whole warps in one CTA beyond 1024 channels.
+template <typename S, typename IO>
+cudaError_t run_dropout(const Norm8Call& c, cudaStream_t st) {
+  constexpr int T = 4;
+  const Params p = params_of(c, T);
+  const bool vec = c.C % 8 == 0 && aligned16(c.x, sizeof(S)) && aligned16(c.x1, sizeof(S)) &&
+                   aligned16(c.u, sizeof(IO));
+  const uint32_t parts = vec ? (uint32_t)c.C / 8 : (uint32_t)(c.C + 127) / 128;
+  // (a part's index takes 31 bits)
+  const uint64_t items = (uint64_t)p.groups * parts, per_cta = vec ? kThreads : kThreads / 32;
+  if (items > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)((items + per_cta - 1) / per_cta);
+  return by_flag(vec, [&](auto v) {
+    return by_flag(c.n[0] == 1 && c.n[1] == 1, [&](auto flat) {
+      return launch_early(k_dropout_add<S, IO, decltype(v)::value, decltype(flat)::value, T>, grid, kThreads, 0, st, p,
+                          divide_by(parts), (uint32_t)items);
+    });
+  });
+}
+
+// The threads of a row, its parts per thread and the rows that a thread holds, by
+// the channel count: 16 channels of a row per thread at most, so that four rows'
+// (or two's) operands stay in registers; several warps from 513 channels on.
 template <bool VEC, typename F>
 cudaError_t by_width(int C, F&& f) {
-#define EVO_N8(lanes, parts) return f(std::integral_constant<int, lanes>{}, std::integral_constant<int, parts>{})
+#define EVO_N8(lanes, parts, rows) \
+  return f(std::integral_constant<int, lanes>{}, std::integral_constant<int, parts>{}, std::integral_constant<int, rows>{})
   if constexpr (VEC) {
-    if (C <= 64) EVO_N8(8, 1);
-    if (C <= 128) EVO_N8(16, 1);
-    if (C <= 256) EVO_N8(32, 1);
-    if (C <= 512) EVO_N8(32, 2);
-    if (C <= 1024) EVO_N8(32, 4);
-    if (C <= 2048) EVO_N8(64, 4);
-    EVO_N8(128, 4);
+    if (C <= 64) EVO_N8(8, 1, 4);
+    if (C <= 128) EVO_N8(16, 1, 4);
+    if (C <= 256) EVO_N8(32, 1, 4);
+    if (C <= 512) EVO_N8(32, 2, 2);
+    if (C <= 1024) EVO_N8(64, 2, 2);
+    if (C <= 2048) EVO_N8(128, 2, 2);
+    EVO_N8(256, 2, 2);
   } else {
-    if (C <= 128) EVO_N8(32, 1);
-    if (C <= 256) EVO_N8(32, 2);
-    if (C <= 512) EVO_N8(32, 4);
-    if (C <= 1024) EVO_N8(32, 8);
-    if (C <= 2048) EVO_N8(64, 8);
-    EVO_N8(128, 8);
+    if (C <= 128) EVO_N8(32, 1, 4);
+    if (C <= 256) EVO_N8(32, 2, 4);
+    if (C <= 512) EVO_N8(32, 4, 2);
+    if (C <= 1024) EVO_N8(64, 4, 2);
+    if (C <= 2048) EVO_N8(128, 4, 2);
+    EVO_N8(256, 4, 2);
   }
 #undef EVO_N8
 }
 
 template <typename S, typename IO, bool VEC>
 cudaError_t run_fwd_as(const Norm8Call& c, cudaStream_t st) {
-  const Params p = params_of(c);
-  return by_width<VEC>(c.C, [&](auto lanes, auto parts) {
-    constexpr int L = decltype(lanes)::value, P = decltype(parts)::value;
+  return by_width<VEC>(c.C, [&](auto lanes, auto parts, auto rows) {
+    constexpr int L = decltype(lanes)::value, P = decltype(parts)::value, T = decltype(rows)::value;
     constexpr uint32_t per = kThreads / L;
-    const int turns = 4;
-    const uint32_t grid = (uint32_t)(((uint64_t)p.rows + per * turns - 1) / (per * turns));
-    return launch_early(k_norm8_fwd<S, IO, L, P, VEC>, grid, kThreads, 0, st, p, turns, c.drop);
+    static_assert(2 * P * Lay<L, VEC>::SPAN * sizeof(float) <= 32 * 1024, "static shared memory");
+    const Params p = params_of(c, T);
+    return by_flag(c.n[0] == 1 && c.n[1] == 1, [&](auto flat) {
+      return launch_early(k_norm8_fwd<S, IO, L, P, VEC, decltype(flat)::value, T>, (p.groups + per - 1) / per, kThreads,
+                          0, st, p);
+    });
   });
 }
 
@@ -590,26 +796,28 @@ cudaError_t run_fwd(const Norm8Call& c, cudaStream_t st) {
 
 template <typename S, typename IO, bool VEC>
 cudaError_t run_bwd_as(const Norm8Call& c, cudaStream_t st) {
-  const Params p = params_of(c);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return by_width<VEC>(c.C, [&](auto lanes, auto parts) {
-    constexpr int L = decltype(lanes)::value, P = decltype(parts)::value;
+  return by_width<VEC>(c.C, [&](auto lanes, auto parts, auto rows) {
+    constexpr int L = decltype(lanes)::value, P = decltype(parts)::value, T = decltype(rows)::value / 2;
     constexpr uint32_t per = kThreads / L;
-    auto kern = k_norm8_bwd<S, IO, L, P, VEC>;
-    const size_t smem = (size_t)2 * c.C * sizeof(float);
-    int fit = 0;
-    cudaError_t e2 = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kThreads, smem);
-    if (e2 != cudaSuccess) return e2;
-    const uint32_t want = (uint32_t)(((uint64_t)p.rows + per - 1) / per);
-    const uint32_t most = std::min<uint32_t>(kNorm8MaxCtas, (uint32_t)std::max(1, fit * sms));
-    const uint32_t grid = std::min(want, most);
-    const uint32_t turns = (want + grid - 1) / grid;
-    e2 = launch_early(kern, grid, kThreads, smem, st, p, turns, c.drop);
-    if (e2 != cudaSuccess || (!p.dgamma && !p.dbeta)) return e2;
-    return launch_early(k_norm8_reduce<S>, (unsigned)(2 * c.C + 31) / 32, 256, 0, st, p, (int)grid);
+    const Params p = params_of(c, T);
+    const cudaError_t e2 = by_flag(c.n[0] == 1 && c.n[1] == 1, [&](auto flat) {
+      auto kern = k_norm8_bwd<S, IO, L, P, VEC, decltype(flat)::value, T>;
+      int fit = 0;
+      cudaError_t e3 = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kThreads, 0);
+      if (e3 != cudaSuccess) return e3;
+      const uint32_t want = (p.groups + per - 1) / per;
+      const uint32_t most = std::min<uint32_t>(kNorm8MaxCtas, (uint32_t)std::max(1, fit * sms));
+      const uint32_t turns = (want + most - 1) / most;
+      const uint32_t grid = (want + turns - 1) / turns;
+      e3 = launch_early(kern, grid, kThreads, 0, st, p, turns);
+      if (e3 != cudaSuccess || (!p.dgamma && !p.dbeta)) return e3;
+      return launch_early(k_norm8_reduce<S>, (unsigned)(2 * c.C + 31) / 32, 256, 0, st, p, (int)grid);
+    });
+    return e2;
   });
 }
 

@@ -16,6 +16,7 @@ constexpr int kNorm8MaxCtas = 608;  // CTAs of a backward launch (one partial su
 // allows it); operands that are not given have p = NULL.
 struct Norm8Call {
   int n[3];
+  int given[3];     // the row axes before they were merged (the mask's)
   int C;
   bool rms;
   float eps;
