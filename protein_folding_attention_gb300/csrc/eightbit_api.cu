@@ -82,6 +82,20 @@ void merge_axes(int (&n)[3], std::initializer_list<int64_t*> ops) {
   merge(0, 1);
 }
 
+// Exchanges the axes I and J where J is the outer one in memory for all of `by`, so
+// that rows are walked as they lie (rows of the ending node's views would each
+// come from another DRAM page).  `ops`: every stride array, `by` among them; NULL
+// for an operand that is not given.  Returns whether it did.
+bool rows_as_they_lie(int (&n)[3], std::initializer_list<const int64_t*> by, std::initializer_list<int64_t*> ops) {
+  if (n[1] == 1 || n[2] == 1) return false;
+  for (const int64_t* s : by)
+    if (s && s[1] >= s[2]) return false;
+  for (int64_t* s : ops)
+    if (s) std::swap(s[1], s[2]);
+  std::swap(n[1], n[2]);
+  return true;
+}
+
 // Scales of an output: distinct places for all of them.
 evoattn_status check_scales(const evoattn_rows& r, const int (&n)[3], int groups) {
   const int64_t extent[4] = {n[0], n[1], n[2], groups};
@@ -163,8 +177,10 @@ evoattn_status evoattn_dropout_add(const evoattn_dropout_add_args* args, cudaStr
   c.u = operand(a.u);
   c.x1 = operand(a.out);
   c.C = C;
+  int64_t *const x = c.x.p ? c.x.s : nullptr, *const mask = c.drop ? c.mask.s : nullptr;
+  c.turned = rows_as_they_lie(n, {x, c.u.s, c.x1.s}, {x, c.u.s, c.x1.s, mask});
   std::copy(n, n + 3, c.given);
-  merge_axes(n, {c.x.p ? c.x.s : nullptr, c.u.s, c.x1.s});
+  merge_axes(n, {x, c.u.s, c.x1.s});
   std::copy(n, n + 3, c.n);
   if (a.stream_dtype == EVOATTN_BF16)
     return cuda_status(a.dtype == EVOATTN_BF16 ? dropout_add_bf16(c, stream) : dropout_add_narrow(c, stream));
@@ -203,8 +219,10 @@ evoattn_status evoattn_norm8(const evoattn_norm8_args* args, cudaStream_t stream
   c.C = C;
   c.rms = a.kind == EVOATTN_NORM_RMS;
   c.eps = (float)a.eps;
+  int64_t *const u = c.u.p ? c.u.s : nullptr, *const x1 = c.u.p ? c.x1.s : nullptr;
+  c.turned = rows_as_they_lie(n, {c.x.s, u, x1}, {c.x.s, u, x1, c.codes_s, c.scales_s, c.drop ? c.mask.s : nullptr});
   std::copy(n, n + 3, c.given);
-  merge_axes(n, {c.x.s, c.u.p ? c.u.s : nullptr, c.u.p ? c.x1.s : nullptr, c.codes_s, c.scales_s});
+  merge_axes(n, {c.x.s, u, x1, c.codes_s, c.scales_s});
   std::copy(n, n + 3, c.n);
   if (sd == EVOATTN_BF16) return cuda_status(norm8_fwd_bf16(c, stream));
   return cuda_status(d == EVOATTN_BF16 ? norm8_fwd_mixed(c, stream) : norm8_fwd_f32(c, stream));
@@ -248,8 +266,11 @@ evoattn_status evoattn_norm8_bwd(const evoattn_norm8_bwd_args* args, cudaStream_
   c.C = C;
   c.rms = a.kind == EVOATTN_NORM_RMS;
   c.eps = (float)a.eps;
+  int64_t *const dx1 = c.dx1.p ? c.dx1.s : nullptr, *const du = c.du.p ? c.du.s : nullptr;
+  c.turned = rows_as_they_lie(n, {c.x1.s, c.dy.s, c.dx.s, dx1, du},
+                              {c.x1.s, c.dy.s, c.dx.s, dx1, du, c.drop ? c.mask.s : nullptr});
   std::copy(n, n + 3, c.given);
-  merge_axes(n, {c.x1.s, c.dy.s, c.dx.s, c.dx1.p ? c.dx1.s : nullptr, c.du.p ? c.du.s : nullptr});
+  merge_axes(n, {c.x1.s, c.dy.s, c.dx.s, dx1, du});
   std::copy(n, n + 3, c.n);
   if (sd == EVOATTN_BF16) return cuda_status(norm8_bwd_bf16(c, stream));
   return cuda_status(d == EVOATTN_BF16 ? norm8_bwd_mixed(c, stream) : norm8_bwd_f32(c, stream));

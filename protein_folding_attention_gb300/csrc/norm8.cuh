@@ -59,7 +59,7 @@ struct Params {
   Divide I, J;       // the same on the axes as they were given, for the mask
   // Groups of T rows: consecutive ones, or (along_i) T neighbours along axis I
   // with the same j, which share a mask row.
-  bool along_i, shared;  // shared: some rows share a mask row
+  bool along_i, shared;  // shared: a row's index is not its mask row's
   uint32_t blocks_i;     // ceil(I / T)
   Divide by_blocks_i;
   uint32_t groups;       // of rows
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout_add(const Params p, Divide
 // forward
 // ---------------------------------------------------------------------------
 template <typename S, typename IO, int LANES, int PARTS, bool VEC, bool FLAT, int T>
-__global__ void __launch_bounds__(kThreads) k_norm8_fwd(const Params p) {
+__global__ void __launch_bounds__(kThreads, VEC && PARTS == 1 && sizeof(S) == 2 ? 4 : 3) k_norm8_fwd(const Params p, uint32_t turns) {
   using L = Lay<LANES, VEC>;
   constexpr int E = L::E, PER = kThreads / LANES;
   __shared__ float sums[2][T][8];
@@ -411,112 +411,121 @@ __global__ void __launch_bounds__(kThreads) k_norm8_fwd(const Params p) {
   wait_for_earlier_work();
   let_next_start();
   const int lane = threadIdx.x % LANES;
-  uint32_t r[T];
-  rows_of<T>(p, blockIdx.x * PER + threadIdx.x / LANES, r);
-  Raw<S, VEC> rx[T][PARTS];
-  Raw<IO, VEC> ru[T][PARTS];
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
-    const bool on = r[t] < p.rows;
-    const Row<FLAT> w(p, on ? r[t] : 0);
-    const int64_t ax = w.at(p.x.s), au = w.at(p.u.s);
-#pragma unroll
-    for (int k = 0; k < PARTS; ++k) {
-      load_part<S, VEC>(rx[t][k], p.x.p, ax, L::chan(lane, k), p.C, on);
-      if (p.u.p) load_part<IO, VEC>(ru[t][k], p.u.p, au, L::chan(lane, k), p.C, on);
-    }
-  }
-  load_params<N>(prm, p.gamma, p.C, 1.f);
-  load_params<N>(prm_b, p.beta, p.C, 0.f);
   PhiloxKey key{};
   if (p.drop) key = philox_key(p.mask);
-  __syncthreads();
-  float x[T][PARTS][E];
-  if (p.u.p) {
-#pragma unroll
-    for (int k = 0; k < PARTS; ++k) {
-      const int c = L::chan(lane, k);
-      float m[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) m[e] = 1.f;
-      uint32_t drawn = 0xFFFFFFFFu;
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const bool on = r[t] < p.rows;
-        float f[E];
-        ru[t][k].get(f);
-        if (p.drop) {
-          const uint32_t row = mask_row(p, on ? r[t] : 0);
-          if (row != drawn) mask_factors<VEC>(key, p.mask, c, row, m);
-          drawn = row;
-#pragma unroll
-          for (int e = 0; e < E; ++e) f[e] = masked(m[e], f[e]);
-        }
-        rx[t][k].get(x[t][k]);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) put_pair(&x[t][k][e], add2(pair(&x[t][k][e]), pair(&f[e])));
-        const Row<FLAT> w(p, on ? r[t] : 0);
-        store_part<S, VEC>(p.x1.p, w.at(p.x1.s), c, p.C, on, x[t][k]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-#pragma unroll
-      for (int k = 0; k < PARTS; ++k) rx[t][k].get(x[t][k]);
-  }
-  float rstd[T];
-  centre<LANES, PARTS, VEC, T, E>(p, lane, x, rstd, sums);
-#pragma unroll
-  for (int k = 0; k < PARTS; ++k) {
-    const int c = L::chan(lane, k);
-    float ga[E], be[E];
-    get_params(prm, c, ga);
-    get_params(prm_b, c, be);
+  // (a loop only where a CTA takes several turns: it costs registers)
+  const uint32_t mine = LANES > 64 ? turns : 1;
+#pragma unroll 1
+  for (uint32_t turn = 0; turn < mine; ++turn) {
+    uint32_t r[T];
+    rows_of<T>(p, (blockIdx.x * mine + turn) * PER + threadIdx.x / LANES, r);
+    Raw<S, VEC> rx[T][PARTS];
+    Raw<IO, VEC> ru[T][PARTS];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const bool on = r[t] < p.rows;
       const Row<FLAT> w(p, on ? r[t] : 0);
-      float(&y)[E] = x[t][k];
+      const int64_t ax = w.at(p.x.s), au = w.at(p.u.s);
 #pragma unroll
-      for (int e = 0; e < E; e += 2)
-        put_pair(&y[e], fma2(mul2(pair(&y[e]), both(rstd[t])), pair(&ga[e]), pair(&be[e])));
-      if (!VEC) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = L::has(p.C, c, e) ? y[e] : 0.f;
+      for (int k = 0; k < PARTS; ++k) {
+        load_part<S, VEC>(rx[t][k], p.x.p, ax, L::chan(lane, k), p.C, on);
+        if (p.u.p) load_part<IO, VEC>(ru[t][k], p.u.p, au, L::chan(lane, k), p.C, on);
       }
-      const auto group_maximum = [&] {
-        float m = max_abs(y);
+    }
+    if (turn == 0) {
+      load_params<N>(prm, p.gamma, p.C, 1.f);
+      load_params<N>(prm_b, p.beta, p.C, 0.f);
+      __syncthreads();
+    } else if (LANES > 64) {
+      __syncthreads();  // the sums of the turn before
+    }
+    float x[T][PARTS][E];
+    if (p.u.p) {
 #pragma unroll
-        for (int o = (VEC ? (LANES < 16 ? LANES : 16) : 32) / 2; o > 0; o >>= 1)
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        return m;
-      };
-      if (VEC && c >= p.C) {  // (beta of a part beyond the row is 0, and so is y)
+      for (int k = 0; k < PARTS; ++k) {
+        const int c = L::chan(lane, k);
+        float m[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = 0.f;
+        for (int e = 0; e < E; ++e) m[e] = 1.f;
+        uint32_t drawn = 0xFFFFFFFFu;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const bool on = r[t] < p.rows;
+          float f[E];
+          ru[t][k].get(f);
+          if (p.drop) {
+            const uint32_t row = mask_row(p, on ? r[t] : 0);
+            if (row != drawn) mask_factors<VEC>(key, p.mask, c, row, m);
+            drawn = row;
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = masked(m[e], f[e]);
+          }
+          rx[t][k].get(x[t][k]);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) put_pair(&x[t][k][e], add2(pair(&x[t][k][e]), pair(&f[e])));
+          const Row<FLAT> w(p, on ? r[t] : 0);
+          store_part<S, VEC>(p.x1.p, w.at(p.x1.s), c, p.C, on, x[t][k]);
+        }
       }
-      float amax = group_maximum();
-      if (__any_sync(0xffffffffu, amax > FLT_MAX)) {
+    } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = infinity_to_nan(y[e]);
-        amax = group_maximum();
-      }
-      const uint32_t code = scale_code(amax);
-      const float inv = scale_inverse(code);
-      const int64_t ac = w.at(p.codes_s);
-      if constexpr (VEC) {
-        if (on && c < p.C)
-          *reinterpret_cast<uint2*>(p.codes + ac + c) =
-              make_uint2(e4m3_four(y[0], y[1], y[2], y[3], inv), e4m3_four(y[4], y[5], y[6], y[7], inv));
-      } else {
-        const uint32_t q = e4m3_four(y[0], y[1], y[2], y[3], inv);
+      for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (on && c + 32 * e < p.C) p.codes[ac + c + 32 * e] = (uint8_t)(q >> 8 * e);
+        for (int k = 0; k < PARTS; ++k) rx[t][k].get(x[t][k]);
+    }
+    float rstd[T];
+    centre<LANES, PARTS, VEC, T, E>(p, lane, x, rstd, sums);
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+      const int c = L::chan(lane, k);
+      float ga[E], be[E];
+      get_params(prm, c, ga);
+      get_params(prm_b, c, be);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const bool on = r[t] < p.rows;
+        const Row<FLAT> w(p, on ? r[t] : 0);
+        float(&y)[E] = x[t][k];
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+          put_pair(&y[e], fma2(mul2(pair(&y[e]), both(rstd[t])), pair(&ga[e]), pair(&be[e])));
+        if (!VEC) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[e] = L::has(p.C, c, e) ? y[e] : 0.f;
+        }
+        const auto group_maximum = [&] {
+          float m = max_abs(y);
+#pragma unroll
+          for (int o = (VEC ? (LANES < 16 ? LANES : 16) : 32) / 2; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          return m;
+        };
+        if (VEC && c >= p.C) {  // (beta of a part beyond the row is 0, and so is y)
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[e] = 0.f;
+        }
+        float amax = group_maximum();
+        if (__any_sync(0xffffffffu, amax > FLT_MAX)) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[e] = infinity_to_nan(y[e]);
+          amax = group_maximum();
+        }
+        const uint32_t code = scale_code(amax);
+        const float inv = scale_inverse(code);
+        const int64_t ac = w.at(p.codes_s);
+        if constexpr (VEC) {
+          if (on && c < p.C)
+            *reinterpret_cast<uint2*>(p.codes + ac + c) =
+                make_uint2(e4m3_four(y[0], y[1], y[2], y[3], inv), e4m3_four(y[4], y[5], y[6], y[7], inv));
+        } else {
+          const uint32_t q = e4m3_four(y[0], y[1], y[2], y[3], inv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (on && c + 32 * e < p.C) p.codes[ac + c + 32 * e] = (uint8_t)(q >> 8 * e);
+        }
+        if (on && (c & 127) == 0 && c < p.C)
+          p.scales[w.at(p.scales_s) + (int64_t)(c >> 7) * p.scales_g] = (uint8_t)code;
       }
-      if (on && (c & 127) == 0 && c < p.C)
-        p.scales[w.at(p.scales_s) + (int64_t)(c >> 7) * p.scales_g] = (uint8_t)code;
     }
   }
 }
@@ -527,6 +536,41 @@ __global__ void __launch_bounds__(kThreads) k_norm8_fwd(const Params p) {
 // Persistent: a thread adds the parameter gradients of its channels over all
 // its rows in registers, a CTA adds its row groups in order and leaves one
 // partial sum, and a second kernel adds those in order.
+//
+// The sums hold 128 registers and with them 16 warps per SM, too few to cover the
+// memory's latency with loads into registers (58 us for 147,456 bf16 rows of 128
+// where the bytes take 28).  Whole 16-byte units therefore come through a ring of
+// DEPTH turns in shared memory, filled by cp.async: a thread copies, and reads,
+// only its own units, so the ring needs no barrier.
+template <typename S, typename IO, int PARTS, int T>
+struct Ring {
+  static constexpr int UNITS_S = sizeof(S) / 2, UNITS_IO = sizeof(IO) / 2;  // of 16 bytes, for 8 elements
+  static constexpr int UNITS = T * PARTS * (2 * UNITS_S + UNITS_IO);        // of a thread's turn: x1, dx1, dy
+  static constexpr uint32_t STAGE = UNITS * kThreads * 16;
+  static constexpr int DEPTH = std::min<int>(4, std::max<int>(2, (int)(80 * 1024 / STAGE)));
+  static constexpr bool USED = sizeof(S) == 2;
+  static constexpr uint32_t BYTES = DEPTH * STAGE;
+};
+// (a unit of which nothing is read is zero)
+__device__ __forceinline__ void copy_unit(uint32_t to, const void* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void copy_part(uint32_t to, const void* base, int64_t at, int c, bool on) {
+  const T* p = static_cast<const T*>(base) + (on ? at + c : 0);
+#pragma unroll
+  for (int u = 0; u < (int)sizeof(T) / 2; ++u) copy_unit(to + u * kThreads * 16, p + u * 16 / sizeof(T), on);
+}
+template <typename T>
+__device__ __forceinline__ void read_part(const uint4* from, Raw<T, true>& r) {
+  if constexpr (sizeof(T) == 2) {
+    r.a = from[0];
+  } else {
+    r.a = *reinterpret_cast<const float4*>(from);
+    r.b = *reinterpret_cast<const float4*>(from + kThreads);
+  }
+}
+
 template <typename S, typename IO, int LANES, int PARTS, bool VEC, bool FLAT, int T>
 __global__ void __launch_bounds__(kThreads, 2) k_norm8_bwd(const Params p, uint32_t turns) {
   using L = Lay<LANES, VEC>;
@@ -546,23 +590,69 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm8_bwd(const Params p, uint3
   for (int k = 0; k < PARTS; ++k)
 #pragma unroll
     for (int e = 0; e < E; ++e) ag[k][e] = ab[k][e] = 0.f;
+  using R = Ring<S, IO, PARTS, T>;
+  extern __shared__ __align__(16) uint4 ring[];
+  const auto rows_at = [&](uint32_t turn, uint32_t (&r)[T]) {
+    rows_of<T>(p, (turn * gridDim.x + blockIdx.x) * PER + threadIdx.x / LANES, r);
+  };
+  // this thread's units of a turn into its slots
+  const auto fill = [&](uint32_t turn) {
+    if (turn < turns) {
+      uint32_t r[T];
+      rows_at(turn, r);
+      uint32_t to = smem_u32(ring) + (turn % R::DEPTH) * R::STAGE + threadIdx.x * 16;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const bool on = r[t] < p.rows;
+        const Row<FLAT> w(p, on ? r[t] : 0);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+          const int c = L::chan(lane, k);
+          copy_part<S>(to, p.x1.p, w.at(p.x1.s), c, on && c < p.C);
+          if (p.dx1.p) copy_part<S>(to + R::UNITS_S * kThreads * 16, p.dx1.p, w.at(p.dx1.s), c, on && c < p.C);
+          copy_part<IO>(to + 2 * R::UNITS_S * kThreads * 16, p.dy.p, w.at(p.dy.s), c, on && c < p.C);
+          to += (2 * R::UNITS_S + R::UNITS_IO) * kThreads * 16;
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (VEC && R::USED) {
+#pragma unroll
+    for (int k = 0; k < R::DEPTH - 1; ++k) fill(k);
+  }
 #pragma unroll 1
   for (uint32_t turn = 0; turn < turns; ++turn) {
     uint32_t r[T];
-    rows_of<T>(p, (turn * gridDim.x + blockIdx.x) * PER + threadIdx.x / LANES, r);
+    rows_at(turn, r);
     Raw<S, VEC> rx[T][PARTS], rd[T][PARTS];
     Raw<IO, VEC> ry[T][PARTS];
+    if constexpr (VEC && R::USED) {
+      fill(turn + R::DEPTH - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(R::DEPTH - 1) : "memory");
+      const uint4* from = ring + (turn % R::DEPTH) * (R::STAGE / 16) + threadIdx.x;
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const bool on = r[t] < p.rows;
-      const Row<FLAT> w(p, on ? r[t] : 0);
-      const int64_t ax = w.at(p.x1.s), ad = w.at(p.dx1.s), ay = w.at(p.dy.s);
+      for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) {
-        const int c = L::chan(lane, k);
-        load_part<S, VEC>(rx[t][k], p.x1.p, ax, c, p.C, on);
-        load_part<IO, VEC>(ry[t][k], p.dy.p, ay, c, p.C, on);
-        if (p.dx1.p) load_part<S, VEC>(rd[t][k], p.dx1.p, ad, c, p.C, on);
+        for (int k = 0; k < PARTS; ++k) {
+          read_part<S>(from, rx[t][k]);
+          if (p.dx1.p) read_part<S>(from + R::UNITS_S * kThreads, rd[t][k]);
+          read_part<IO>(from + 2 * R::UNITS_S * kThreads, ry[t][k]);
+          from += (2 * R::UNITS_S + R::UNITS_IO) * kThreads;
+        }
+    } else {
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const bool on = r[t] < p.rows;
+        const Row<FLAT> w(p, on ? r[t] : 0);
+        const int64_t ax = w.at(p.x1.s), ad = w.at(p.dx1.s), ay = w.at(p.dy.s);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+          const int c = L::chan(lane, k);
+          load_part<S, VEC>(rx[t][k], p.x1.p, ax, c, p.C, on);
+          load_part<IO, VEC>(ry[t][k], p.dy.p, ay, c, p.C, on);
+          if (p.dx1.p) load_part<S, VEC>(rd[t][k], p.dx1.p, ad, c, p.C, on);
+        }
       }
     }
     float h[T][PARTS][E], rstd[T], m1[T], m2[T];
@@ -659,26 +749,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm8_bwd(const Params p, uint3
   for (int c = threadIdx.x; c < 2 * p.C; c += kThreads) out[c] = prm[c];
 }
 
-// Partial sums of `count` CTAs: 8 warps share 32 columns, each a stretch of the
-// CTAs, joined in order.
+// Partial sums of `count` CTAs: 32 warps share 32 columns, each a stretch of the
+// CTAs (19 at most, so one or two rounds of loads), joined in a fixed order.
 template <typename S>
-__global__ void __launch_bounds__(256) k_norm8_reduce(const Params p, int count) {
-  __shared__ float buf[8][32];
+__global__ void __launch_bounds__(1024) k_norm8_reduce(const Params p, int count) {
+  __shared__ float buf[32][33];
   wait_for_earlier_work();
   let_next_start();
   const int warp = threadIdx.x >> 5, c = blockIdx.x * 32 + (threadIdx.x & 31);
-  const int per = (count + 7) / 8, lo = warp * per, hi = min(count, lo + per);
+  const int per = (count + 31) / 32, lo = warp * per, hi = min(count, lo + per);
   float s = 0.f;
   if (c < 2 * p.C)
-#pragma unroll 8
+#pragma unroll 10
     for (int k = lo; k < hi; ++k) s += p.ws[(int64_t)k * 2 * p.C + c];
   buf[warp][threadIdx.x & 31] = s;
   __syncthreads();
-  if (warp == 0 && c < 2 * p.C) {
+  // warp w adds column w's stretches
+  s = buf[threadIdx.x & 31][warp];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += buf[k][threadIdx.x];
-    float* out = c < p.C ? p.dgamma : p.dbeta;
-    if (out) out[c < p.C ? c : c - p.C] = s;
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int col = blockIdx.x * 32 + warp;
+  if ((threadIdx.x & 31) == 0 && col < 2 * p.C) {
+    float* out = col < p.C ? p.dgamma : p.dbeta;
+    if (out) out[col < p.C ? col : col - p.C] = s;
   }
 }
 
@@ -701,7 +794,7 @@ inline Params params_of(const Norm8Call& c, int T) {
   p.I = divide_by((uint32_t)c.given[1]);
   p.J = divide_by((uint32_t)c.given[2]);
   const auto shares = [&](int k) { return c.drop && c.given[k] > 1 && c.mask.s[k] == 0; };
-  p.shared = shares(0) || shares(1) || shares(2);
+  p.shared = c.drop && (c.turned || shares(0) || shares(1) || shares(2));
   p.along_i = shares(1) && !shares(2);
   p.blocks_i = (uint32_t)(c.given[1] + T - 1) / T;
   p.by_blocks_i = divide_by(p.blocks_i);
@@ -747,9 +840,10 @@ cudaError_t run_dropout(const Norm8Call& c, cudaStream_t st) {
 }
 
 // The threads of a row, its parts per thread and the rows that a thread holds, by
-// the channel count: 16 channels of a row per thread at most, so that four rows'
-// (or two's) operands stay in registers; several warps from 513 channels on.
-template <bool VEC, typename F>
+// the channel count: 16 channels of a row per thread at most, in the forward 24
+// where that fits 384 or 768 exactly (THREE; the backward's sums leave no registers
+// for it), so that four rows' (or two's) operands stay in registers.
+template <bool VEC, bool THREE, typename F>
 cudaError_t by_width(int C, F&& f) {
 #define EVO_N8(lanes, parts, rows) \
   return f(std::integral_constant<int, lanes>{}, std::integral_constant<int, parts>{}, std::integral_constant<int, rows>{})
@@ -757,7 +851,9 @@ cudaError_t by_width(int C, F&& f) {
     if (C <= 64) EVO_N8(8, 1, 4);
     if (C <= 128) EVO_N8(16, 1, 4);
     if (C <= 256) EVO_N8(32, 1, 4);
+    if (THREE && C <= 384) EVO_N8(16, 3, 2);
     if (C <= 512) EVO_N8(32, 2, 2);
+    if (THREE && C <= 768) EVO_N8(32, 3, 2);
     if (C <= 1024) EVO_N8(64, 2, 2);
     if (C <= 2048) EVO_N8(128, 2, 2);
     EVO_N8(256, 2, 2);
@@ -774,14 +870,22 @@ cudaError_t by_width(int C, F&& f) {
 
 template <typename S, typename IO, bool VEC>
 cudaError_t run_fwd_as(const Norm8Call& c, cudaStream_t st) {
-  return by_width<VEC>(c.C, [&](auto lanes, auto parts, auto rows) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  return by_width<VEC, true>(c.C, [&](auto lanes, auto parts, auto rows) {
     constexpr int L = decltype(lanes)::value, P = decltype(parts)::value, T = decltype(rows)::value;
     constexpr uint32_t per = kThreads / L;
     static_assert(2 * P * Lay<L, VEC>::SPAN * sizeof(float) <= 32 * 1024, "static shared memory");
     const Params p = params_of(c, T);
     return by_flag(c.n[0] == 1 && c.n[1] == 1, [&](auto flat) {
-      return launch_early(k_norm8_fwd<S, IO, L, P, VEC, decltype(flat)::value, T>, (p.groups + per - 1) / per, kThreads,
-                          0, st, p);
+      // Short CTAs; but a wide row's gamma and beta are read again by every CTA,
+      // so there four turns share them, as long as there are CTAs enough.
+      const uint32_t ctas = (p.groups + per - 1) / per;
+      const uint32_t turns = L <= 64 ? 1 : std::min<uint32_t>(4, std::max<uint32_t>(1, ctas / (6 * sms)));
+      return launch_early(k_norm8_fwd<S, IO, L, P, VEC, decltype(flat)::value, T>, (ctas + turns - 1) / turns, kThreads,
+                          0, st, p, turns);
     });
   });
 }
@@ -800,22 +904,24 @@ cudaError_t run_bwd_as(const Norm8Call& c, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return by_width<VEC>(c.C, [&](auto lanes, auto parts, auto rows) {
+  return by_width<VEC, false>(c.C, [&](auto lanes, auto parts, auto rows) {
     constexpr int L = decltype(lanes)::value, P = decltype(parts)::value, T = decltype(rows)::value / 2;
     constexpr uint32_t per = kThreads / L;
     const Params p = params_of(c, T);
     const cudaError_t e2 = by_flag(c.n[0] == 1 && c.n[1] == 1, [&](auto flat) {
       auto kern = k_norm8_bwd<S, IO, L, P, VEC, decltype(flat)::value, T>;
+      const size_t smem = VEC && Ring<S, IO, P, T>::USED ? Ring<S, IO, P, T>::BYTES : 0;
       int fit = 0;
-      cudaError_t e3 = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kThreads, 0);
+      cudaError_t e3 = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e3 == cudaSuccess) e3 = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kThreads, smem);
       if (e3 != cudaSuccess) return e3;
       const uint32_t want = (p.groups + per - 1) / per;
       const uint32_t most = std::min<uint32_t>(kNorm8MaxCtas, (uint32_t)std::max(1, fit * sms));
       const uint32_t turns = (want + most - 1) / most;
       const uint32_t grid = (want + turns - 1) / turns;
-      e3 = launch_early(kern, grid, kThreads, 0, st, p, turns);
+      e3 = launch_early(kern, grid, kThreads, smem, st, p, turns);
       if (e3 != cudaSuccess || (!p.dgamma && !p.dbeta)) return e3;
-      return launch_early(k_norm8_reduce<S>, (unsigned)(2 * c.C + 31) / 32, 256, 0, st, p, (int)grid);
+      return launch_early(k_norm8_reduce<S>, (unsigned)(2 * c.C + 31) / 32, 1024, 0, st, p, (int)grid);
     });
     return e2;
   });

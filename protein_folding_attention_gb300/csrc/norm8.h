@@ -17,6 +17,7 @@ constexpr int kNorm8MaxCtas = 608;  // CTAs of a backward launch (one partial su
 struct Norm8Call {
   int n[3];
   int given[3];     // the row axes before they were merged (the mask's)
+  bool turned;      // I and J are exchanged: a row's index is not its mask row's
   int C;
   bool rms;
   float eps;
