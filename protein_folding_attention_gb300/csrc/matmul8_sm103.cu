@@ -24,16 +24,17 @@
 // fp32 partial sums [piece][m][n], with b's rows on the lanes too; a second kernel
 // adds them in order.
 //
-// Warps (384 threads, one persistent CTA per SM, a ring of stages of 128 k):
+// Warps (384 or 640 threads, one persistent CTA per SM, a ring of stages of 128 k):
 //   0      TMA producer: both operands' codes (128-byte swizzle)
-//   1      MMA issuer: copies the stage's scales to tensor memory, four MMAs of
-//          32 k; commits free the stage
-//   2, 3   scales of the two operands' rows: bytes from global memory, each repeated
-//          over a word, in the order that the copy to tensor memory wants
-//          (word r / 32 of 16-byte row r % 32)
-//   4-11   epilogue: tensor memory -> registers -> out, two warps per lane
+//   1      MMA issuer: copies the scales of four groups to tensor memory at a
+//          time, four MMAs of 32 k per group; commits free the stage
+//   2, 3   scales of the two operands' rows: bytes from global memory, those of
+//          four groups in a word (the MMA names the byte), in the order that the
+//          copy to tensor memory wants (word r / 32 of 16-byte row r % 32)
+//   4-...  epilogue: tensor memory -> registers -> out, two warps per lane
 //          quarter with half the columns each; the accumulator is double
-//          buffered, so the next tile's sum runs meanwhile
+//          buffered, so the next tile's sum runs meanwhile, and with short sums
+//          each of the two has eight warps of its own
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,6 +42,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "divide.cuh"
 #include "launch.cuh"
 #include "matmul8.h"
 #include "sm103.h"
@@ -51,20 +53,24 @@ namespace {
 
 constexpr int kLanes = 128;  // rows of the operand on the lanes
 constexpr int kGroup = 128;  // elements along k of a stage, and of a scale
-constexpr int kThreads = 384;
+constexpr int kQuad = 4;     // groups whose scales go to tensor memory together
+constexpr int kAhead = 3;    // such fours that are requested before they are needed
 
 enum Mode { kStaged, kDirect, kPartial };  // a on the lanes; b on the lanes; that, and a piece of the sum
 
-template <int BQ_, Mode MODE>
+// BQ: rows of the operand on the columns.  SETS: groups of eight epilogue warps.
+template <int BQ_, Mode MODE, int SETS>
 struct Cfg {
   static constexpr int BQ = BQ_;
+  static constexpr int THREADS = 128 + SETS * 256;
   static constexpr uint32_t P_BYTES = kLanes * kGroup, Q_BYTES = BQ * kGroup;
-  static constexpr uint32_t S_BYTES = 512;  // scales of up to 128 rows
+  static constexpr uint32_t S_BYTES = 512;  // scales of up to 128 rows, four groups
   static constexpr uint32_t STAGE = P_BYTES + Q_BYTES;
-  static constexpr uint32_t STAGING = MODE == kStaged ? 8 * 4096 : 0;
-  static constexpr int STAGES = std::min<int>(8, (int)((220 * 1024 - STAGING) / (STAGE + 2 * S_BYTES)));
+  static constexpr int RING_S = 4;
+  static constexpr uint32_t STAGING = MODE == kStaged ? SETS * 8 * 4096 : 0;
+  static constexpr int STAGES = std::min<int>(8, (int)((222 * 1024 - STAGING - RING_S * 2 * S_BYTES) / STAGE));
   static constexpr uint32_t OFF_S = STAGES * STAGE;
-  static constexpr uint32_t OFF_STAGING = OFF_S + STAGES * 2 * S_BYTES;
+  static constexpr uint32_t OFF_STAGING = OFF_S + RING_S * 2 * S_BYTES;
   static constexpr uint32_t SMEM_ALLOC = OFF_STAGING + STAGING + 1024;
   static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ;  // scales: 4 columns for each operand
   static_assert(COL_S + 8 <= 512, "tensor memory");
@@ -74,8 +80,9 @@ struct Cfg {
 struct Params8 {
   Operand8 p, q;          // on the lanes, on the columns
   int P, Q;               // their rows
-  int tiles_p, tiles_q, groups, per_split, items;
+  int groups, per_split, items;
   int fast_q;             // items run over q first
+  Divide inner, outer;    // tiles along the axis that items run over first, and the other
   int M, N;
   void* out;
   int64_t ld_out;
@@ -111,10 +118,9 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const Params8& p, int item, int bq) {
   Item w;
-  const int inner = p.fast_q ? p.tiles_q : p.tiles_p, outer = p.fast_q ? p.tiles_p : p.tiles_q;
-  const int t = item / inner, i = item - t * inner;
-  w.split = t / outer;
-  const int o = t - w.split * outer;
+  const int t = (int)quotient(p.inner, item), i = item - t * (int)p.inner.d;
+  w.split = (int)quotient(p.outer, t);
+  const int o = t - w.split * (int)p.outer.d;
   w.p0 = (p.fast_q ? o : i) * kLanes;
   w.q0 = (p.fast_q ? i : o) * bq;
   w.g0 = w.split * p.per_split;
@@ -122,16 +128,18 @@ __device__ __forceinline__ Item item_of(const Params8& p, int item, int bq) {
   return w;
 }
 
-// Scale bytes of rows r0 + lane + 32 k (k < 4) of an operand for one group; rows
-// that the operand does not have get 1.
-__device__ __forceinline__ void scale_bytes(const Operand8& o, int rows, int r0, int width, int g, uint32_t (&s)[4]) {
+// Scale bytes of rows r0 + lane + 32 k (k < 4) of an operand for the groups g to
+// g + 3 (below g1); rows that the operand does not have get 1.
+__device__ __forceinline__ void scale_bytes(const Operand8& o, int rows, int r0, int width, int g, int g1,
+                                            uint32_t (&s)[4][kQuad]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int r = lane + 32 * k;
-    s[k] = r < width && r0 + r < rows
-               ? o.scales[(int64_t)((r0 + r) >> o.shift) * o.s_row + (int64_t)g * o.s_group]
-               : 127u;
+    const bool on = r < width && r0 + r < rows;
+    const uint8_t* at = o.scales + (on ? (int64_t)((r0 + r) >> o.shift) * o.s_row : 0) + (int64_t)g * o.s_group;
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j, at += o.s_group) s[k][j] = on && g + j < g1 ? *at : 127u;
   }
 }
 
@@ -228,15 +236,15 @@ __device__ __forceinline__ void stage_row(uint8_t* stg, const uint32_t (&lo)[32]
   }
 }
 
-template <typename T, int BQ, Mode MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int BQ, Mode MODE, int SETS>
+__global__ void __launch_bounds__(128 + SETS * 256, 1)
     k_matmul8(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q, const Params8 p) {
-  using C = Cfg<BQ, MODE>;
+  using C = Cfg<BQ, MODE, SETS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bar_full[C::STAGES], bar_scale[C::STAGES], bar_empty[C::STAGES], bar_done[2], bar_free[2],
-      bar_drain, bar_never;
+  __shared__ uint64_t bar_full[C::STAGES], bar_empty[C::STAGES], bar_scale[C::RING_S], bar_copied[C::RING_S], bar_done[2],
+      bar_free[2], bar_drain, bar_never;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -245,8 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&bar_full[i], 1);   // codes
-      mbar_init(&bar_scale[i], 2);  // scales of both operands
       mbar_init(&bar_empty[i], 1);  // the stage's MMAs have read it
+    }
+    for (int i = 0; i < C::RING_S; ++i) {
+      mbar_init(&bar_scale[i], 2);   // scales of both operands
+      mbar_init(&bar_copied[i], 1);  // they are in tensor memory
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_done[i], 1);
@@ -300,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t ds0 = umma_desc(smem_u32(smem + C::OFF_S), 16, 128, kSwNone);
     const uint32_t sp = tmem + C::COL_S, sq = sp + 4;
     bool ok = true;
-    int it = 0, n = 0;
+    int it = 0, is = 0, n = 0;
     for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x, ++n) {
       const Item w = item_of(p, item, BQ);
       const int buf = n & 1;
@@ -310,24 +321,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       for (int g = w.g0; g < w.g1; ++g, ++it) {
-        const int st = it % C::STAGES;
-        ok = mbar_wait(&bar_full[st], (it / C::STAGES) & 1, wctx) &&
-             mbar_wait(&bar_scale[st], (it / C::STAGES) & 1, wctx);
+        const int st = it % C::STAGES, j = (g - w.g0) % kQuad;
+        if (j == 0) ok = mbar_wait(&bar_scale[is % C::RING_S], (is / C::RING_S) & 1, wctx);
+        ok = ok && mbar_wait(&bar_full[st], (it / C::STAGES) & 1, wctx);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint64_t dp = dp0 + ((uint32_t)(st * C::STAGE) >> 4), dq = dq0 + ((uint32_t)(st * C::STAGE) >> 4);
-        const uint64_t ds = ds0 + ((uint32_t)(st * 2 * C::S_BYTES) >> 4);
         if (elect_one()) {
-          tmem_copy_scales(sp, ds);
-          tmem_copy_scales(sq, ds + (C::S_BYTES >> 4));
+          if (j == 0) {
+            const uint64_t ds = ds0 + ((uint32_t)((is % C::RING_S) * 2 * C::S_BYTES) >> 4);
+            tmem_copy_scales(sp, ds);
+            tmem_copy_scales(sq, ds + (C::S_BYTES >> 4));
+            umma_commit(&bar_copied[is % C::RING_S]);
+          }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_mxf8(tmem + buf * BQ, dp + 2 * kk, dq + 2 * kk, id, sp, sq, g > w.g0 || kk > 0 ? 1u : 0u);
+            umma_mxf8(tmem + buf * BQ, dp + 2 * kk, dq + 2 * kk, id | (uint32_t)j << 4 | (uint32_t)j << 29, sp, sq,
+                      g > w.g0 || kk > 0 ? 1u : 0u);
           umma_commit(&bar_empty[st]);
           if (g + 1 == w.g1) umma_commit(&bar_done[buf]);
         }
         __syncwarp();
+        if (j == 0) ++is;
       }
     }
     if (elect_one()) umma_commit(&bar_drain);
@@ -342,59 +358,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool of_q = warp == 3;
     const Operand8 o = of_q ? p.q : p.p;
     const int rows = of_q ? p.Q : p.P, width = of_q ? BQ : kLanes;
-    // A ring of AHEAD steps in registers: the bytes of a step are requested AHEAD
-    // steps before they are written, across items too (with one step ahead every
+    // A ring of fours in registers: the bytes of one are requested kAhead fours
+    // before they are written, across items too (requested one step ahead, every
     // step waited for L2: 950 cycles a step where its MMAs take 256).
-    constexpr int AHEAD = 8;
-    uint32_t s[AHEAD][4];
-    int item = blockIdx.x, g = 0;  // the step that is requested next
+    uint32_t s[kAhead][4][kQuad];
+    int item = blockIdx.x, g = 0;  // the four that is requested next
     Item w{};
     if (item < p.items) { w = item_of(p, item, BQ); g = w.g0; }
-    const auto request = [&](uint32_t (&to)[4]) {
+    const auto request = [&](uint32_t (&to)[4][kQuad]) {
       if (item >= p.items) return;
-      scale_bytes(o, rows, of_q ? w.q0 : w.p0, width, g, to);
-      if (++g == w.g1) {
+      scale_bytes(o, rows, of_q ? w.q0 : w.p0, width, g, w.g1, to);
+      g += kQuad;
+      if (g >= w.g1) {
         item += gridDim.x;
         if (item < p.items) { w = item_of(p, item, BQ); g = w.g0; }
       }
     };
-    int left = 0;  // steps of this CTA
-    for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
-      const Item v = item_of(p, i, BQ);
-      left += v.g1 - v.g0;
+    int left = 0;  // fours of this CTA
+    if (p.per_split >= p.groups) {  // (every item has all groups)
+      left = (p.items - 1 - (int)blockIdx.x + (int)gridDim.x) / (int)gridDim.x * ((p.groups + kQuad - 1) / kQuad);
+    } else {
+      for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+        const Item v = item_of(p, i, BQ);
+        left += (v.g1 - v.g0 + kQuad - 1) / kQuad;
+      }
     }
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) request(s[k]);
+    for (int k = 0; k < kAhead; ++k) request(s[k]);
     bool ok = true;
-    for (int it0 = 0; it0 < left && ok; it0 += AHEAD) {
+    for (int is0 = 0; is0 < left && ok; is0 += kAhead) {
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        const int it = it0 + k;
-        if (it < left && ok) {
-          const int st = it % C::STAGES;
-          const uint4 v = make_uint4(s[k][0] * 0x01010101u, s[k][1] * 0x01010101u, s[k][2] * 0x01010101u,
-                                     s[k][3] * 0x01010101u);
+      for (int k = 0; k < kAhead; ++k) {
+        const int is = is0 + k, at = is % C::RING_S;
+        if (is < left && ok) {
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = s[k][i][0] | s[k][i][1] << 8 | s[k][i][2] << 16 | s[k][i][3] << 24;
           request(s[k]);
-          if (it >= C::STAGES) ok = mbar_wait(&bar_empty[st], ((it / C::STAGES) - 1) & 1, wctx);
+          if (is >= C::RING_S) ok = mbar_wait(&bar_copied[at], ((is / C::RING_S) - 1) & 1, wctx);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
-            *reinterpret_cast<uint4*>(smem + C::OFF_S + (st * 2 + (of_q ? 1 : 0)) * C::S_BYTES + lane * 16) = v;
+            *reinterpret_cast<uint4*>(smem + C::OFF_S + (at * 2 + (of_q ? 1 : 0)) * C::S_BYTES + lane * 16) =
+                make_uint4(v[0], v[1], v[2], v[3]);
             fence_proxy_async_smem();  // generic writes, read by the copy to tensor memory
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_scale[st]);
+            if (lane == 0) mbar_arrive(&bar_scale[at]);
           }
         }
       }
     }
   } else {
     // ============================ epilogue =================================
-    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int quad = warp & 3, half = (warp - 4) >> 2 & 1, set = (warp - 4) >> 3;
     bool ok = true;
     if (p.wc.stall) ok = __all_sync(0xffffffffu, stall_wait(&bar_never, wctx));
     int n = 0;
     for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x, ++n) {
-      const Item w = item_of(p, item, BQ);
       const int buf = n & 1;
+      if (SETS == 2 && buf != set) continue;  // the other set's
+      const Item w = item_of(p, item, BQ);
       ok = __all_sync(0xffffffffu, mbar_wait(&bar_done[buf], (n >> 1) & 1, wctx));
       if (!ok) break;
       tc_fence_after();
@@ -506,9 +528,9 @@ int unit_of(const void* p, int64_t stride, int64_t width) {
   return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
 }
 
-template <typename T, int BQ, Mode MODE>
+template <typename T, int BQ, Mode MODE, int SETS = 1>
 cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  using C = Cfg<BQ, MODE>;
+  using C = Cfg<BQ, MODE, SETS>;
   Params8 p{};
   p.p = MODE == kStaged ? c.a : c.b;
   p.q = MODE == kStaged ? c.b : c.a;
@@ -519,8 +541,9 @@ cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStr
     *tmap_ok = false;
     return cudaErrorInvalidValue;
   }
-  p.tiles_p = pl.tiles_p; p.tiles_q = pl.tiles_q;
   p.fast_q = MODE == kStaged;  // out's columns first: the rows of a that are in flight are few
+  p.inner = divide_by(p.fast_q ? pl.tiles_q : pl.tiles_p);
+  p.outer = divide_by(p.fast_q ? pl.tiles_p : pl.tiles_q);
   p.groups = pl.groups; p.per_split = pl.per_split;
   p.items = pl.tiles_p * pl.tiles_q * pl.splits;
   p.M = c.M; p.N = c.N;
@@ -531,10 +554,10 @@ cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStr
   p.unit_add = unit_of(c.add, c.ld_add * size, c.N * size);
   p.ws = c.ws;
   p.wc = launch_wait(c.wait);
-  auto kern = k_matmul8<T, BQ, MODE>;
+  auto kern = k_matmul8<T, BQ, MODE, SETS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
-  return launch_early(kern, (unsigned)std::min(p.items, sms), kThreads, C::SMEM_ALLOC, st, tp, tq, p);
+  return launch_early(kern, (unsigned)std::min(p.items, sms), C::THREADS, C::SMEM_ALLOC, st, tp, tq, p);
 }
 
 template <typename T>
@@ -590,6 +613,9 @@ size_t matmul8_workspace_bytes(int M, int N, int K, int sms) {
 }
 
 cudaError_t matmul8(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
+  if (pl.staged && pl.groups <= 8)
+    return c.f32 ? launch<float, 128, kStaged, 2>(c, pl, sms, st, tmap_ok)
+                 : launch<__nv_bfloat16, 128, kStaged, 2>(c, pl, sms, st, tmap_ok);
   if (pl.staged)
     return c.f32 ? launch<float, 128, kStaged>(c, pl, sms, st, tmap_ok)
                  : launch<__nv_bfloat16, 128, kStaged>(c, pl, sms, st, tmap_ok);
