@@ -26,10 +26,10 @@
 //
 // Warps (384 or 640 threads, one persistent CTA per SM, a ring of stages of 128 k):
 //   0      TMA producer: both operands' codes (128-byte swizzle)
-//   1      MMA issuer: copies the scales of four groups to tensor memory at a
-//          time, four MMAs of 32 k per group; commits free the stage
+//   1      MMA issuer: copies the scales of four (or two) groups to tensor memory
+//          at a time, four MMAs of 32 k per group; commits free the stage
 //   2, 3   scales of the two operands' rows: bytes from global memory, those of
-//          four groups in a word (the MMA names the byte), in the order that the
+//          the groups in a word (the MMA names the byte), in the order that the
 //          copy to tensor memory wants (word r / 32 of 16-byte row r % 32)
 //   4-...  epilogue: tensor memory -> registers -> out, two warps per lane
 //          quarter with half the columns each; the accumulator is double
@@ -53,9 +53,6 @@ namespace {
 
 constexpr int kLanes = 128;  // rows of the operand on the lanes
 constexpr int kGroup = 128;  // elements along k of a stage, and of a scale
-constexpr int kQuad = 4;     // groups whose scales go to tensor memory together
-constexpr int kAhead = 3;    // such fours that are requested before they are needed
-
 enum Mode { kStaged, kDirect, kPartial };  // a on the lanes; b on the lanes; that, and a piece of the sum
 
 // BQ: rows of the operand on the columns.  SETS: groups of eight epilogue warps.
@@ -66,7 +63,10 @@ struct Cfg {
   static constexpr uint32_t P_BYTES = kLanes * kGroup, Q_BYTES = BQ * kGroup;
   static constexpr uint32_t S_BYTES = 512;  // scales of up to 128 rows, four groups
   static constexpr uint32_t STAGE = P_BYTES + Q_BYTES;
-  static constexpr int RING_S = 4;
+  // Scales: groups whose bytes go to tensor memory together (four fill a word; two
+  // where 640 threads leave 96 registers, which bytes that are underway have to
+  // fit: spilled, they are waited for), and such bundles requested ahead.
+  static constexpr int BUNDLE = SETS == 2 ? 2 : 4, AHEAD = 3, RING_S = 4;
   static constexpr uint32_t STAGING = MODE == kStaged ? SETS * 8 * 4096 : 0;
   static constexpr int STAGES = std::min<int>(8, (int)((222 * 1024 - STAGING - RING_S * 2 * S_BYTES) / STAGE));
   static constexpr uint32_t OFF_S = STAGES * STAGE;
@@ -128,18 +128,34 @@ __device__ __forceinline__ Item item_of(const Params8& p, int item, int bq) {
   return w;
 }
 
-// Scale bytes of rows r0 + lane + 32 k (k < 4) of an operand for the groups g to
-// g + 3 (below g1); rows that the operand does not have get 1.
-__device__ __forceinline__ void scale_bytes(const Operand8& o, int rows, int r0, int width, int g, int g1,
-                                            uint32_t (&s)[4][kQuad]) {
+// Where the scale bytes of rows r0 + lane + 32 k (k < 4) of an operand lie; NULL
+// for rows that the operand, or the tile, does not have.
+struct ScaleRows {
+  const uint8_t* at[4];
+};
+__device__ __forceinline__ void scale_rows(const Operand8& o, int rows, int r0, int width, ScaleRows& s) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int r = lane + 32 * k;
-    const bool on = r < width && r0 + r < rows;
-    const uint8_t* at = o.scales + (on ? (int64_t)((r0 + r) >> o.shift) * o.s_row : 0) + (int64_t)g * o.s_group;
+    s.at[k] = r < width && r0 + r < rows ? o.scales + (int64_t)((r0 + r) >> o.shift) * o.s_row : nullptr;
+  }
+}
+// ... and those of n groups from g on, each in a byte of the row's word (1 for
+// rows that there are not).
+template <int BUNDLE>
+__device__ __forceinline__ void scale_bytes(const ScaleRows& s, int64_t s_group, int g, int n, uint32_t (&to)[4][BUNDLE]) {
+  const int64_t off = g * s_group;
+  if (n == 1) {  // (the same for the whole warp)
 #pragma unroll
-    for (int j = 0; j < kQuad; ++j, at += o.s_group) s[k][j] = on && g + j < g1 ? *at : 127u;
+    for (int k = 0; k < 4; ++k) to[k][0] = s.at[k] ? s.at[k][off] : 127u;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < BUNDLE; ++j) {
+    if (j >= n) break;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[k][j] = s.at[k] ? s.at[k][off + j * s_group] : 127u;
   }
 }
 
@@ -321,7 +337,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
       }
       tc_fence_after();
       for (int g = w.g0; g < w.g1; ++g, ++it) {
-        const int st = it % C::STAGES, j = (g - w.g0) % kQuad;
+        const int st = it % C::STAGES, j = (g - w.g0) % C::BUNDLE;
         if (j == 0) ok = mbar_wait(&bar_scale[is % C::RING_S], (is / C::RING_S) & 1, wctx);
         ok = ok && mbar_wait(&bar_full[st], (it / C::STAGES) & 1, wctx);
         ok = __all_sync(0xffffffffu, ok);
@@ -358,42 +374,59 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     const bool of_q = warp == 3;
     const Operand8 o = of_q ? p.q : p.p;
     const int rows = of_q ? p.Q : p.P, width = of_q ? BQ : kLanes;
-    // A ring of fours in registers: the bytes of one are requested kAhead fours
+    // A ring of bundles in registers: the bytes of one are requested AHEAD bundles
     // before they are written, across items too (requested one step ahead, every
     // step waited for L2: 950 cycles a step where its MMAs take 256).
-    uint32_t s[kAhead][4][kQuad];
-    int item = blockIdx.x, g = 0;  // the four that is requested next
-    Item w{};
-    if (item < p.items) { w = item_of(p, item, BQ); g = w.g0; }
-    const auto request = [&](uint32_t (&to)[4][kQuad]) {
+    uint32_t s[C::AHEAD][4][C::BUNDLE];
+#pragma unroll
+    for (int k = 0; k < C::AHEAD; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < C::BUNDLE; ++j) s[k][i][j] = 0;  // (bytes of groups that there are not are not read)
+    int item = blockIdx.x, g = 0, g1 = 0;  // the bundle that is requested next
+    ScaleRows at;
+    const auto enter = [&] {
       if (item >= p.items) return;
-      scale_bytes(o, rows, of_q ? w.q0 : w.p0, width, g, w.g1, to);
-      g += kQuad;
-      if (g >= w.g1) {
+      const Item w = item_of(p, item, BQ);
+      g = w.g0;
+      g1 = w.g1;
+      scale_rows(o, rows, of_q ? w.q0 : w.p0, width, at);
+    };
+    enter();
+    const auto request = [&](uint32_t (&to)[4][C::BUNDLE]) {
+      if (item >= p.items) return;
+      scale_bytes(at, o.s_group, g, min(C::BUNDLE, g1 - g), to);
+      g += C::BUNDLE;
+      if (g >= g1) {
         item += gridDim.x;
-        if (item < p.items) { w = item_of(p, item, BQ); g = w.g0; }
+        enter();
       }
     };
-    int left = 0;  // fours of this CTA
+    int left = 0;  // bundles of this CTA
     if (p.per_split >= p.groups) {  // (every item has all groups)
-      left = (p.items - 1 - (int)blockIdx.x + (int)gridDim.x) / (int)gridDim.x * ((p.groups + kQuad - 1) / kQuad);
+      left = (p.items - 1 - (int)blockIdx.x + (int)gridDim.x) / (int)gridDim.x * ((p.groups + C::BUNDLE - 1) / C::BUNDLE);
     } else {
       for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
         const Item v = item_of(p, i, BQ);
-        left += (v.g1 - v.g0 + kQuad - 1) / kQuad;
+        left += (v.g1 - v.g0 + C::BUNDLE - 1) / C::BUNDLE;
       }
     }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) request(s[k]);
+    for (int k = 0; k < C::AHEAD; ++k) request(s[k]);
     bool ok = true;
-    for (int is0 = 0; is0 < left && ok; is0 += kAhead) {
+    for (int is0 = 0; is0 < left && ok; is0 += C::AHEAD) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < C::AHEAD; ++k) {
         const int is = is0 + k, at = is % C::RING_S;
         if (is < left && ok) {
           uint32_t v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = s[k][i][0] | s[k][i][1] << 8 | s[k][i][2] << 16 | s[k][i][3] << 24;
+          for (int i = 0; i < 4; ++i) {
+            v[i] = s[k][i][0];
+#pragma unroll
+            for (int j = 1; j < C::BUNDLE; ++j) v[i] |= s[k][i][j] << 8 * j;
+          }
           request(s[k]);
           if (is >= C::RING_S) ok = mbar_wait(&bar_copied[at], ((is / C::RING_S) - 1) & 1, wctx);
           ok = __all_sync(0xffffffffu, ok);
