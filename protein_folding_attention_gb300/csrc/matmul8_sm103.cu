@@ -20,6 +20,13 @@
 // down to 16) and b, the larger operand then, streams through the 128-row side;
 // a warp stores 32 consecutive columns of a row.
 //
+// With long sums over many rows the operands' way through L2 bounds the product
+// (128 x 128 tiles: 12.6 TB/s of it at 43 % of the tensor cores' rate).  There two
+// neighbouring CTAs, a cluster, take tiles of 128 x 192 or 240 with the same rows of
+// b: each loads half of those and multicasts it to both, so that a step of 480 MMA
+// cycles reads 31 KB instead of 32 KB for 256.  (240 and not 256: two
+// accumulators and the scales share the 512 columns of tensor memory.)
+//
 // Long sums with few tiles are cut into pieces along k, one per CTA, which leave
 // fp32 partial sums [piece][m][n], with b's rows on the lanes too; a second kernel
 // adds them in order.
@@ -40,6 +47,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "divide.cuh"
@@ -55,26 +63,29 @@ constexpr int kLanes = 128;  // rows of the operand on the lanes
 constexpr int kGroup = 128;  // elements along k of a stage, and of a scale
 enum Mode { kStaged, kDirect, kPartial };  // a on the lanes; b on the lanes; that, and a piece of the sum
 
-// BQ: rows of the operand on the columns.  SETS: groups of eight epilogue warps.
+// BQ: rows of the operand on the columns; above 128 in clusters of two CTAs.
+// SETS: groups of eight epilogue warps.
 template <int BQ_, Mode MODE, int SETS>
 struct Cfg {
   static constexpr int BQ = BQ_;
+  static constexpr bool PAIR = BQ > 128;
   static constexpr int THREADS = 128 + SETS * 256;
   static constexpr uint32_t P_BYTES = kLanes * kGroup, Q_BYTES = BQ * kGroup;
   static constexpr uint32_t S_BYTES = 512;  // scales of up to 128 rows, four groups
+  static constexpr uint32_t S_ENTRY = (PAIR ? 3 : 2) * S_BYTES;  // of p's rows, then q's
   static constexpr uint32_t STAGE = P_BYTES + Q_BYTES;
   // Scales: groups whose bytes go to tensor memory together (four fill a word; two
   // where 640 threads leave 96 registers, which bytes that are underway have to
   // fit: spilled, they are waited for), and such bundles requested ahead.
-  static constexpr int BUNDLE = SETS == 2 ? 2 : 4, AHEAD = 3, RING_S = 4;
+  static constexpr int BUNDLE = SETS == 2 ? 2 : 4, AHEAD = PAIR ? 2 : 3, RING_S = 4;
   static constexpr uint32_t STAGING = MODE == kStaged ? SETS * 8 * 4096 : 0;
-  static constexpr int STAGES = std::min<int>(8, (int)((222 * 1024 - STAGING - RING_S * 2 * S_BYTES) / STAGE));
+  static constexpr int STAGES = std::min<int>(8, (int)((224 * 1024 - STAGING - RING_S * S_ENTRY) / STAGE));
   static constexpr uint32_t OFF_S = STAGES * STAGE;
-  static constexpr uint32_t OFF_STAGING = OFF_S + RING_S * 2 * S_BYTES;
+  static constexpr uint32_t OFF_STAGING = OFF_S + RING_S * S_ENTRY;
   static constexpr uint32_t SMEM_ALLOC = OFF_STAGING + STAGING + 1024;
-  static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ;  // scales: 4 columns for each operand
-  static_assert(COL_S + 8 <= 512, "tensor memory");
-  static_assert(STAGE % 1024 == 0 && OFF_STAGING % 1024 == 0, "the swizzle repeats every 1024 bytes");
+  static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ;  // scales: 4 columns for each 128 rows
+  static_assert(COL_S + 12 <= 512 && SMEM_ALLOC <= 227 * 1024, "tensor memory, shared memory");
+  static_assert(STAGE % 1024 == 0 && OFF_STAGING % 1024 == 0 && (!PAIR || Q_BYTES % 2048 == 0), "the swizzle repeats every 1024 bytes");
 };
 
 struct Params8 {
@@ -112,50 +123,135 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) 
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
+// Clusters of two: barriers of both CTAs, loads and commits that reach both.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
 // Where an item of work lies.
 struct Item {
   int p0, q0, g0, g1, split;
 };
-__device__ __forceinline__ Item item_of(const Params8& p, int item, int bq) {
+template <typename C>
+__device__ __forceinline__ int first_item() { return C::PAIR ? blockIdx.x >> 1 : blockIdx.x; }
+template <typename C>
+__device__ __forceinline__ int item_step() { return C::PAIR ? gridDim.x >> 1 : gridDim.x; }
+template <typename C>
+__device__ __forceinline__ Item item_of(const Params8& p, int item) {
   Item w;
   const int t = (int)quotient(p.inner, item), i = item - t * (int)p.inner.d;
   w.split = (int)quotient(p.outer, t);
   const int o = t - w.split * (int)p.outer.d;
-  w.p0 = (p.fast_q ? o : i) * kLanes;
-  w.q0 = (p.fast_q ? i : o) * bq;
+  // (an item of a pair is two neighbouring tiles of p)
+  w.p0 = (C::PAIR ? 2 * o + (int)(blockIdx.x & 1) : p.fast_q ? o : i) * kLanes;
+  w.q0 = (p.fast_q ? i : o) * C::BQ;
   w.g0 = w.split * p.per_split;
   w.g1 = min(p.groups, w.g0 + p.per_split);
   return w;
 }
 
-// Where the scale bytes of rows r0 + lane + 32 k (k < 4) of an operand lie; NULL
-// for rows that the operand, or the tile, does not have.
-struct ScaleRows {
-  const uint8_t* at[4];
-};
-__device__ __forceinline__ void scale_rows(const Operand8& o, int rows, int r0, int width, ScaleRows& s) {
+// The scales of one operand's rows, RL for each lane: bytes from global memory
+// into the ring that the MMA issuer copies to tensor memory.
+template <typename C, int RL>
+__device__ __forceinline__ void scale_role(const Params8& p, bool of_q, uint8_t* ring, uint64_t* bar_scale,
+                                           uint64_t* bar_copied, const WaitCtx& wctx) {
+  const Operand8 o = of_q ? p.q : p.p;
+  const int rows = of_q ? p.Q : p.P, width = of_q ? C::BQ : kLanes;
   const int lane = threadIdx.x & 31;
+  // A ring of bundles in registers: the bytes of one are requested AHEAD bundles
+  // before they are written, across items too (requested one step ahead, every
+  // step waited for L2: 950 cycles a step where its MMAs take 256).
+  uint32_t s[C::AHEAD][RL][C::BUNDLE];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = lane + 32 * k;
-    s.at[k] = r < width && r0 + r < rows ? o.scales + (int64_t)((r0 + r) >> o.shift) * o.s_row : nullptr;
+  for (int k = 0; k < C::AHEAD; ++k)
+#pragma unroll
+    for (int i = 0; i < RL; ++i)
+#pragma unroll
+      for (int j = 0; j < C::BUNDLE; ++j) s[k][i][j] = 0;  // (bytes of groups that there are not are not read)
+  int item = first_item<C>(), g = 0, g1 = 0;  // the bundle that is requested next
+  const uint8_t* at[RL];  // where the rows' bytes lie; NULL for rows that there are not, whose scale is 1
+  const auto enter = [&] {
+    if (item >= p.items) return;
+    const Item w = item_of<C>(p, item);
+    g = w.g0;
+    g1 = w.g1;
+    const int r0 = of_q ? w.q0 : w.p0;
+#pragma unroll
+    for (int k = 0; k < RL; ++k) {
+      const int r = lane + 32 * k;
+      at[k] = r < width && r0 + r < rows ? o.scales + (int64_t)((r0 + r) >> o.shift) * o.s_row : nullptr;
+    }
+  };
+  enter();
+  const auto request = [&](uint32_t (&to)[RL][C::BUNDLE]) {
+    if (item >= p.items) return;
+    const int64_t off = g * o.s_group;
+    const int n = min(C::BUNDLE, g1 - g);  // (the same for the whole warp)
+#pragma unroll
+    for (int j = 0; j < C::BUNDLE; ++j) {
+      if (j >= n) break;
+#pragma unroll
+      for (int k = 0; k < RL; ++k) to[k][j] = at[k] ? at[k][off + j * o.s_group] : 127u;
+    }
+    g += C::BUNDLE;
+    if (g >= g1) {
+      item += item_step<C>();
+      enter();
+    }
+  };
+  int left = 0;  // bundles of this CTA
+  if (p.per_split >= p.groups) {  // (every item has all groups)
+    left = (p.items - 1 - first_item<C>() + item_step<C>()) / item_step<C>() *
+           ((p.groups + C::BUNDLE - 1) / C::BUNDLE);
+  } else {
+    for (int i = first_item<C>(); i < p.items; i += item_step<C>()) {
+      const Item v = item_of<C>(p, i);
+      left += (v.g1 - v.g0 + C::BUNDLE - 1) / C::BUNDLE;
+    }
   }
-}
-// ... and those of n groups from g on, each in a byte of the row's word (1 for
-// rows that there are not).
-template <int BUNDLE>
-__device__ __forceinline__ void scale_bytes(const ScaleRows& s, int64_t s_group, int g, int n, uint32_t (&to)[4][BUNDLE]) {
-  const int64_t off = g * s_group;
-  if (n == 1) {  // (the same for the whole warp)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) to[k][0] = s.at[k] ? s.at[k][off] : 127u;
-    return;
-  }
+  for (int k = 0; k < C::AHEAD; ++k) request(s[k]);
+  bool ok = true;
+  for (int is0 = 0; is0 < left && ok; is0 += C::AHEAD) {
 #pragma unroll
-  for (int j = 0; j < BUNDLE; ++j) {
-    if (j >= n) break;
+    for (int k = 0; k < C::AHEAD; ++k) {
+      const int is = is0 + k, slot = is % C::RING_S;
+      if (is < left && ok) {
+        uint32_t v[RL];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) to[k][j] = s.at[k] ? s.at[k][off + j * s_group] : 127u;
+        for (int i = 0; i < RL; ++i) {
+          v[i] = s[k][i][0];
+#pragma unroll
+          for (int j = 1; j < C::BUNDLE; ++j) v[i] |= s[k][i][j] << 8 * j;
+        }
+        request(s[k]);
+        if (is >= C::RING_S) ok = mbar_wait(&bar_copied[slot], ((is / C::RING_S) - 1) & 1, wctx);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+#pragma unroll
+          for (int h = 0; h < RL / 4; ++h)
+            *reinterpret_cast<uint4*>(ring + slot * C::S_ENTRY + ((of_q ? 1 : 0) + h) * C::S_BYTES + lane * 16) =
+                make_uint4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+          fence_proxy_async_smem();  // generic writes, read by the copy to tensor memory
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_scale[slot]);
+        }
+      }
+    }
   }
 }
 
@@ -269,7 +365,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     abort_flag = 0;
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&bar_full[i], 1);   // codes
-      mbar_init(&bar_empty[i], 1);  // the stage's MMAs have read it
+      mbar_init(&bar_empty[i], C::PAIR ? 2 : 1);  // the stage's MMAs have read it (both CTAs')
     }
     for (int i = 0; i < C::RING_S; ++i) {
       mbar_init(&bar_scale[i], 2);   // scales of both operands
@@ -288,6 +384,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (C::PAIR) cluster_sync();  // both CTAs' barriers are there
   const uint32_t tmem = tmem_slot;
   volatile int* abort_p = &abort_flag;
   const WaitCtx wctx{abort_p, p.wc};
@@ -298,8 +395,8 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     // ============================ codes ====================================
     bool ok = true;
     int it = 0;
-    for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-      const Item w = item_of(p, item, BQ);
+    for (int item = first_item<C>(); item < p.items && ok; item += item_step<C>()) {
+      const Item w = item_of<C>(p, item);
       for (int g = w.g0; g < w.g1; ++g, ++it) {
         const int st = it % C::STAGES;
         if (it >= C::STAGES) ok = mbar_wait(&bar_empty[st], ((it / C::STAGES) - 1) & 1, wctx);
@@ -308,15 +405,27 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar_full[st], C::STAGE);
           tma_load_2d(smem + st * C::STAGE, &tm_p, &bar_full[st], g * kGroup, w.p0);
-          tma_load_2d(smem + st * C::STAGE + C::P_BYTES, &tm_q, &bar_full[st], g * kGroup, w.q0);
+          uint8_t* q = smem + st * C::STAGE + C::P_BYTES;
+          if constexpr (C::PAIR) {  // this CTA's half, for both
+            const int h = blockIdx.x & 1;
+            tma_load_2d_both(q + h * (C::Q_BYTES / 2), &tm_q, &bar_full[st], g * kGroup, w.q0 + h * (C::BQ / 2));
+          } else {
+            tma_load_2d(q, &tm_q, &bar_full[st], g * kGroup, w.q0);
+          }
         }
         __syncwarp();
       }
     }
-    if (lane == 0) {  // every copy lands before the CTA may exit
+    if (lane == 0) {
       volatile int no_abort = 0;
-      for (int i = max(0, it - C::STAGES); i < it; ++i)
-        mbar_wait(&bar_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort);
+      if constexpr (C::PAIR) {
+        // the other CTA's arrivals for the last stages land before this one may exit
+        for (int i = max(0, it - C::STAGES); i < it && ok; ++i)
+          ok = mbar_wait(&bar_empty[i % C::STAGES], (i / C::STAGES) & 1, wctx);
+      } else {  // every copy lands before the CTA may exit
+        for (int i = max(0, it - C::STAGES); i < it; ++i)
+          mbar_wait(&bar_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -328,8 +437,8 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     const uint32_t sp = tmem + C::COL_S, sq = sp + 4;
     bool ok = true;
     int it = 0, is = 0, n = 0;
-    for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x, ++n) {
-      const Item w = item_of(p, item, BQ);
+    for (int item = first_item<C>(); item < p.items && ok; item += item_step<C>(), ++n) {
+      const Item w = item_of<C>(p, item);
       const int buf = n & 1;
       if (n >= 2) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bar_free[buf], ((n >> 1) - 1) & 1, wctx));
@@ -346,16 +455,20 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
         const uint64_t dp = dp0 + ((uint32_t)(st * C::STAGE) >> 4), dq = dq0 + ((uint32_t)(st * C::STAGE) >> 4);
         if (elect_one()) {
           if (j == 0) {
-            const uint64_t ds = ds0 + ((uint32_t)((is % C::RING_S) * 2 * C::S_BYTES) >> 4);
+            const uint64_t ds = ds0 + ((uint32_t)((is % C::RING_S) * C::S_ENTRY) >> 4);
             tmem_copy_scales(sp, ds);
             tmem_copy_scales(sq, ds + (C::S_BYTES >> 4));
+            if constexpr (C::PAIR) tmem_copy_scales(sq + 4, ds + (2 * C::S_BYTES >> 4));
             umma_commit(&bar_copied[is % C::RING_S]);
           }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_mxf8(tmem + buf * BQ, dp + 2 * kk, dq + 2 * kk, id | (uint32_t)j << 4 | (uint32_t)j << 29, sp, sq,
                       g > w.g0 || kk > 0 ? 1u : 0u);
-          umma_commit(&bar_empty[st]);
+          if constexpr (C::PAIR)
+            umma_commit_both(&bar_empty[st]);
+          else
+            umma_commit(&bar_empty[st]);
           if (g + 1 == w.g1) umma_commit(&bar_done[buf]);
         }
         __syncwarp();
@@ -371,74 +484,14 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     __syncwarp();
   } else if (warp < 4) {
     // ============================ scales ===================================
-    const bool of_q = warp == 3;
-    const Operand8 o = of_q ? p.q : p.p;
-    const int rows = of_q ? p.Q : p.P, width = of_q ? BQ : kLanes;
-    // A ring of bundles in registers: the bytes of one are requested AHEAD bundles
-    // before they are written, across items too (requested one step ahead, every
-    // step waited for L2: 950 cycles a step where its MMAs take 256).
-    uint32_t s[C::AHEAD][4][C::BUNDLE];
-#pragma unroll
-    for (int k = 0; k < C::AHEAD; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < C::BUNDLE; ++j) s[k][i][j] = 0;  // (bytes of groups that there are not are not read)
-    int item = blockIdx.x, g = 0, g1 = 0;  // the bundle that is requested next
-    ScaleRows at;
-    const auto enter = [&] {
-      if (item >= p.items) return;
-      const Item w = item_of(p, item, BQ);
-      g = w.g0;
-      g1 = w.g1;
-      scale_rows(o, rows, of_q ? w.q0 : w.p0, width, at);
-    };
-    enter();
-    const auto request = [&](uint32_t (&to)[4][C::BUNDLE]) {
-      if (item >= p.items) return;
-      scale_bytes(at, o.s_group, g, min(C::BUNDLE, g1 - g), to);
-      g += C::BUNDLE;
-      if (g >= g1) {
-        item += gridDim.x;
-        enter();
-      }
-    };
-    int left = 0;  // bundles of this CTA
-    if (p.per_split >= p.groups) {  // (every item has all groups)
-      left = (p.items - 1 - (int)blockIdx.x + (int)gridDim.x) / (int)gridDim.x * ((p.groups + C::BUNDLE - 1) / C::BUNDLE);
+    uint8_t* ring = smem + C::OFF_S;
+    if constexpr (C::PAIR) {
+      if (warp == 3)
+        scale_role<C, 8>(p, true, ring, bar_scale, bar_copied, wctx);
+      else
+        scale_role<C, 4>(p, false, ring, bar_scale, bar_copied, wctx);
     } else {
-      for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
-        const Item v = item_of(p, i, BQ);
-        left += (v.g1 - v.g0 + C::BUNDLE - 1) / C::BUNDLE;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < C::AHEAD; ++k) request(s[k]);
-    bool ok = true;
-    for (int is0 = 0; is0 < left && ok; is0 += C::AHEAD) {
-#pragma unroll
-      for (int k = 0; k < C::AHEAD; ++k) {
-        const int is = is0 + k, at = is % C::RING_S;
-        if (is < left && ok) {
-          uint32_t v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = s[k][i][0];
-#pragma unroll
-            for (int j = 1; j < C::BUNDLE; ++j) v[i] |= s[k][i][j] << 8 * j;
-          }
-          request(s[k]);
-          if (is >= C::RING_S) ok = mbar_wait(&bar_copied[at], ((is / C::RING_S) - 1) & 1, wctx);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            *reinterpret_cast<uint4*>(smem + C::OFF_S + (at * 2 + (of_q ? 1 : 0)) * C::S_BYTES + lane * 16) =
-                make_uint4(v[0], v[1], v[2], v[3]);
-            fence_proxy_async_smem();  // generic writes, read by the copy to tensor memory
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_scale[at]);
-          }
-        }
-      }
+      scale_role<C, 4>(p, warp == 3, ring, bar_scale, bar_copied, wctx);
     }
   } else {
     // ============================ epilogue =================================
@@ -446,10 +499,10 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     bool ok = true;
     if (p.wc.stall) ok = __all_sync(0xffffffffu, stall_wait(&bar_never, wctx));
     int n = 0;
-    for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x, ++n) {
+    for (int item = first_item<C>(); item < p.items && ok; item += item_step<C>(), ++n) {
       const int buf = n & 1;
       if (SETS == 2 && buf != set) continue;  // the other set's
-      const Item w = item_of(p, item, BQ);
+      const Item w = item_of<C>(p, item);
       ok = __all_sync(0xffffffffu, mbar_wait(&bar_done[buf], (n >> 1) & 1, wctx));
       if (!ok) break;
       tc_fence_after();
@@ -459,8 +512,8 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
         constexpr int SPAN = 128 / sizeof(T);  // columns of a chunk
         const int m = w.p0 + quad * 32, rows = min(32, p.M - m);
 #pragma unroll 1
-        for (int c = half * (BQ / 2); c < (half + 1) * (BQ / 2); c += SPAN) {
-          const int n = w.q0 + c, width = min(SPAN, p.N - n) * (int)sizeof(T);
+        for (int c = half * SPAN; c < BQ; c += 2 * SPAN) {
+          const int n = w.q0 + c, width = min(min(SPAN, BQ - c), p.N - n) * (int)sizeof(T);
           if (width <= 0 || rows <= 0) break;  // (the same for the whole warp)
           uint32_t lo[32], hi[32];
           tmem_ld32(base + c, lo);
@@ -525,6 +578,16 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0) report_abort(abort_p, p.wc);
+  if constexpr (C::PAIR) {
+    __syncwarp();
+    cluster_sync();  // nothing is issued to the other CTA after this
+    // After a give-up the two may have stopped at different steps, whose copies no
+    // barrier can tell the end of: they are given 0.2 ms to land.
+    if (*abort_p || launch_aborted(p.wc)) {
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 200000ull) {}
+    }
+  }
 }
 
 // Adds the pieces of the sums in order.
@@ -570,7 +633,7 @@ cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStr
   p.P = MODE == kStaged ? c.M : c.N;
   p.Q = MODE == kStaged ? c.N : c.M;
   CUtensorMap tp, tq;
-  if (!make_tmap_codes(&tp, p.p, p.P, c.K, kLanes) || !make_tmap_codes(&tq, p.q, p.Q, c.K, BQ)) {
+  if (!make_tmap_codes(&tp, p.p, p.P, c.K, kLanes) || !make_tmap_codes(&tq, p.q, p.Q, c.K, C::PAIR ? BQ / 2 : BQ)) {
     *tmap_ok = false;
     return cudaErrorInvalidValue;
   }
@@ -590,7 +653,23 @@ cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStr
   auto kern = k_matmul8<T, BQ, MODE, SETS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
-  return launch_early(kern, (unsigned)std::min(p.items, sms), C::THREADS, C::SMEM_ALLOC, st, tp, tq, p);
+  if constexpr (C::PAIR) {
+    // as many clusters as the device can hold at once (asked once per device)
+    static std::atomic<int> most[64];
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int clusters = dev < 64 ? most[dev].load() : 0;
+    if (clusters == 0) {
+      e = max_pairs(&clusters, kern, C::THREADS, C::SMEM_ALLOC);
+      if (e != cudaSuccess) return e;
+      if (clusters < 1) return cudaErrorInvalidConfiguration;
+      if (dev < 64) most[dev].store(clusters);
+    }
+    return launch_early_pairs(kern, 2u * (unsigned)std::min(p.items, clusters), C::THREADS, C::SMEM_ALLOC, st, tp, tq, p);
+  } else {
+    return launch_early(kern, (unsigned)std::min(p.items, sms), C::THREADS, C::SMEM_ALLOC, st, tp, tq, p);
+  }
 }
 
 template <typename T>
@@ -634,7 +713,13 @@ Matmul8Plan matmul8_plan(int M, int N, int K, int sms) {
   if (M > 64 && pl.splits == 1) {  // a's rows on the lanes
     pl.staged = true;
     pl.bq = 128;
-    pl.tiles_p = tiles(M, kLanes);
+    if (pl.groups > 8 && (int64_t)tiles(M, 2 * kLanes) * tiles(N, 240) >= sms / 2) {
+      // Pairs of CTAs.  A step of a pair's tiles costs 1 in units of a step of 128
+      // columns where it has 192, and 1.05 where it has 240: what is least over N.
+      const double by128 = 1.1 * tiles(N, 128), by192 = 1.0 * tiles(N, 192), by240 = 1.05 * tiles(N, 240);
+      if (by192 < by128 || by240 < by128) pl.bq = by192 < by240 ? 192 : 240;
+    }
+    pl.tiles_p = pl.bq > 128 ? tiles(M, 2 * kLanes) : tiles(M, kLanes);
     pl.tiles_q = tiles(N, pl.bq);
   }
   return pl;
@@ -649,6 +734,12 @@ cudaError_t matmul8(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaSt
   if (pl.staged && pl.groups <= 8)
     return c.f32 ? launch<float, 128, kStaged, 2>(c, pl, sms, st, tmap_ok)
                  : launch<__nv_bfloat16, 128, kStaged, 2>(c, pl, sms, st, tmap_ok);
+  if (pl.staged && pl.bq == 240)
+    return c.f32 ? launch<float, 240, kStaged>(c, pl, sms, st, tmap_ok)
+                 : launch<__nv_bfloat16, 240, kStaged>(c, pl, sms, st, tmap_ok);
+  if (pl.staged && pl.bq == 192)
+    return c.f32 ? launch<float, 192, kStaged>(c, pl, sms, st, tmap_ok)
+                 : launch<__nv_bfloat16, 192, kStaged>(c, pl, sms, st, tmap_ok);
   if (pl.staged)
     return c.f32 ? launch<float, 128, kStaged>(c, pl, sms, st, tmap_ok)
                  : launch<__nv_bfloat16, 128, kStaged>(c, pl, sms, st, tmap_ok);

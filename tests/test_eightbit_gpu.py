@@ -416,6 +416,27 @@ def test_matmul8(M, N, K, dtype, blocks):
     check_product(got, a, b)
 
 
+@pytest.mark.parametrize("M, N, K", [(4097, 1500, 1100), (2500, 1999, 1290), (3840, 1152, 1157), (20000, 240, 1281)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("extra", ["none", "blocks", "add"])
+def test_matmul8_wide(M, N, K, dtype, extra):
+    """Sizes that pairs of CTAs share, ragged in every direction: the values of a
+    sample of rows (every row of the last tiles among them), and nothing beyond."""
+    qa, sa, a = operand(M, K, 1)
+    qb, sb, b = operand(N, K, 2, extra == "blocks")
+    add = torch.randn(M, N, generator=gen(3)).to(dtype) if extra == "add" else None
+    frame = torch.full((M + 1, N + 3), 5.0, dtype=dtype, device=DEV)
+    out = frame[:M, :N]
+    evoattn.matmul8(codes_on_device(qa), sa.to(DEV), codes_on_device(qb), sb.to(DEV), dtype,
+                    add=None if add is None else add.to(DEV), out=out)
+    assert evoattn.device_status() == evoattn.OK
+    rows = torch.cat([torch.arange(0, M, 37), torch.arange(max(0, M - 260), M)])
+    check_product(out[rows.to(DEV)], a[rows], b, None if add is None else add[rows])
+    assert not torch.isnan(out).any()
+    frame[:M, :N] = 5.0
+    assert (frame == 5.0).all()
+
+
 @pytest.mark.parametrize("M, N, K", [(1, 300, 500), (40, 129, 4000), (200, 516, 256), (700, 33, 100)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("kind", ["full", "row", "in place", "wide"])
@@ -528,7 +549,7 @@ def test_matmul8_workspace():
 
 def test_matmul8_gives_up_and_recovers():
     """A wait that nothing ends: every CTA gives up, and the next call is right."""
-    for M, N, K in ((300, 300, 700), (4, 300, 3000)):
+    for M, N, K in ((300, 300, 700), (4, 300, 3000), (4097, 1200, 1300)):
         qa, sa, a = operand(M, K, 15)
         qb, sb, b = operand(N, K, 16)
         args = codes_on_device(qa), sa.to(DEV), codes_on_device(qb), sb.to(DEV), torch.float32
