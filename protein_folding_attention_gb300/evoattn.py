@@ -699,6 +699,8 @@ _PACK_MATMUL8 = struct.Struct("=22q").pack
 
 def _dropout(p, rng, site, shared, index):
     """The fields of evoattn_dropout."""
+    if p == 0.0 and not shared:
+        return 0, 0.0, site, 0
     mask = 0
     for axis in shared:
         if not 0 <= axis <= 2:
@@ -752,9 +754,12 @@ def dropout_add(u, p, rng, x=None, site=0, shared=(), out=None, out_dtype=None, 
 
 def _codes8(lead, cols, device):
     """Codes [*lead, cols] whose rows start at multiples of 16 bytes."""
-    ld = -(-cols // 16) * 16
-    t = torch.empty((*lead, ld), device=device, dtype=torch.float8_e4m3fn)
-    return t if ld == cols else t[..., :cols]
+    at = cols + 15 & ~15
+    strides = [1]
+    for n in reversed(lead):
+        strides.append(at)
+        at *= n
+    return torch.empty_strided((*lead, cols), strides[::-1], device=device, dtype=torch.float8_e4m3fn)
 
 
 def _scales8(lead, cols, rows, device):
@@ -762,24 +767,28 @@ def _scales8(lead, cols, rows, device):
     in memory."""
     strides, at = [rows], 1
     for n in reversed(lead):
-        strides.insert(0, at)
+        strides.append(at)
         at *= n
-    return torch.empty_strided((*lead, -(-cols // GROUP8)), strides, device=device, dtype=torch.float8_e8m0fnu)
+    return torch.empty_strided((*lead, (cols + 127) // GROUP8), strides[::-1], device=device,
+                               dtype=torch.float8_e8m0fnu)
 
 
 def _matrix(t, name):
     """(rows, row stride) of [..., cols] taken as a matrix with contiguous rows."""
-    rows, ld = 1, None
-    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last axis is not contiguous")
+    if len(shape) == 2 and shape[0] != 1:
+        return shape[0], strides[0]
+    rows, ld = 1, shape[-1] + 15 & ~15
+    for n, s in zip(shape[-2::-1], strides[-2::-1]):
         if n != 1:
-            if ld is None:
+            if rows == 1:
                 ld = s
             elif s != ld * rows:
                 raise ValueError(f"{name}: the leading axes do not form one row axis")
             rows *= n
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last axis is not contiguous")
-    return rows, -(-t.shape[-1] // 16) * 16 if ld is None else ld
+    return rows, ld
 
 
 def norm8(x, u=None, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0.0, rng=None, site=0,
@@ -817,11 +826,12 @@ def norm8(x, u=None, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0.0, rn
             words += x1.stride()
         else:
             _add_rows(words, ((x1, sd, "x1"),), shape, dev)
-        codes = _codes8((B, I, J), C, x.device)
-        scales = _scales8((B, I, J), C, B * I * J, x.device)
-    for t in (codes, scales):
-        words.append(t.data_ptr())
-        words += t.stride()
+        device, ld, IJ = x.device, C + 15 & ~15, I * J
+        s_codes, s_scales = (IJ * ld, J * ld, ld, 1), (IJ, J, 1, B * IJ)
+        codes = torch.empty_strided(shape, s_codes, device=device, dtype=torch.float8_e4m3fn)
+        scales = torch.empty_strided((B, I, J, (C + 127) // GROUP8), s_scales, device=device,
+                                     dtype=torch.float8_e8m0fnu)
+    words += (codes.data_ptr(), *s_codes, scales.data_ptr(), *s_scales)
     _add_vectors(words, ((gamma, "gamma"), (beta, "beta")), C, dev)
     if stream is not None:
         _used_on(stream, (x, u, x1, gamma, beta, codes, scales, rng if p else None))
@@ -903,7 +913,8 @@ def quantize8(x, rows=True, cols=False, blocks=False, stream=None):
     q = s = qt = t = None
     with _allocate_on(stream):
         if blocks:
-            s = torch.empty((-(-R // GROUP8), -(-K // GROUP8)), device=device, dtype=torch.float8_e8m0fnu)
+            rg, kg = (R + 127) // GROUP8, (K + 127) // GROUP8
+            s = torch.empty_strided((rg, kg), (kg, 1), device=device, dtype=torch.float8_e8m0fnu)
         if rows:
             q = _codes8(lead, K, device)
             if not blocks:
@@ -916,47 +927,49 @@ def quantize8(x, rows=True, cols=False, blocks=False, stream=None):
     if q is None:
         words += (0, 0)
     else:
-        words += (q.data_ptr(), -(-K // 16) * 16)
+        words += (q.data_ptr(), K + 15 & ~15)
     if s is None:
         words += (0, 0, 0)
     elif blocks:
-        words += (s.data_ptr(), *s.stride())
+        words += (s.data_ptr(), kg, 1)
     else:
         words += (s.data_ptr(), 1, R)
-    words += (0, 0) if qt is None else (qt.data_ptr(), qt.stride(0))
-    words += (0, 0, 0) if t is None else (t.data_ptr(), *t.stride())
+    words += (0, 0) if qt is None else (qt.data_ptr(), R + 15 & ~15)
+    words += (0, 0, 0) if t is None else (t.data_ptr(), 1, K)
     if stream is not None:
         _used_on(stream, (x,))
     st = load().evoattn_quantize8(_PACK_QUANTIZE8(*words), _raw_stream(stream, dev))
     if st != OK:
         _check(st, "evoattn_quantize8")
+    if not cols:
+        return q, s
     if blocks:
         t = s.t()
-    return (*((q, s) if rows else ()), *((qt, t) if cols else ()))
+    return (q, s, qt, t) if rows else (qt, t)
 
 
 def _operand8(codes, scales, name, index):
-    """The fields of evoattn_operand8, and the rows."""
+    """The rows of an operand, and the fields of evoattn_operand8."""
     if codes.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float8_e8m0fnu or \
             codes.get_device() != index or scales.get_device() != index:
         raise ValueError(f"{name}: expected float8_e4m3fn codes with float8_e8m0fnu scales on cuda:{index}")
     rows, ld = _matrix(codes, name)
-    groups = -(-codes.shape[-1] // GROUP8)
-    if scales.shape == (*codes.shape[:-1], groups):
-        per, sr = 1, 0
-        n = 1
-        for size, stride in zip(reversed(scales.shape[:-1]), reversed(scales.stride()[:-1])):
+    shape, got, strides = codes.shape, scales.shape, scales.stride()
+    groups = (shape[-1] + 127) // GROUP8
+    if got[-1] == groups and got[:-1] == shape[:-1]:
+        per, sr, n = 1, 0, 1
+        for size, stride in zip(got[-2::-1], strides[-2::-1]):
             if size != 1:
                 if n == 1:
                     sr = stride
                 elif stride != sr * n:
                     raise ValueError(f"{name}: the scales' leading axes do not form one row axis")
                 n *= size
-    elif scales.shape == (-(-rows // GROUP8), groups):
-        per, sr = GROUP8, scales.stride(0)
+    elif got == ((rows + 127) // GROUP8, groups):
+        per, sr = GROUP8, strides[0]
     else:
-        raise ValueError(f"{name}: scales {tuple(scales.shape)} for codes {tuple(codes.shape)}")
-    return rows, (codes.data_ptr(), ld, scales.data_ptr(), sr, scales.stride(-1), per)
+        raise ValueError(f"{name}: scales {tuple(got)} for codes {tuple(shape)}")
+    return rows, (codes.data_ptr(), ld, scales.data_ptr(), sr, strides[-1], per)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -981,34 +994,44 @@ def matmul8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, add=None, out=None
     shape = (*a.shape[:-1], N)
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is torch.bfloat16:
+        code = BF16
+    elif out_dtype is torch.float32:
+        code = F32
+    else:
         raise ValueError(f"out: bf16 or fp32, got {out_dtype}")
-    for t, name in ((add, "add"), (out, "out")):
-        if t is not None and (t.dtype is not out_dtype or t.get_device() != dev or t.shape != shape) and \
-                not (name == "add" and t.dtype is out_dtype and t.get_device() == dev and t.shape == (N,)):
-            raise ValueError(f"{name}: expected {shape} {out_dtype} on cuda:{dev}, got {tuple(t.shape)} {t.dtype} "
-                             f"on {t.device}")
-    ld_out, ld_add = N, 0
+    ld_out, at_add, ld_add = N, 0, 0
     if out is not None:
-        m, ld_out = _matrix(out, "out")
+        if out.get_device() != dev or out.shape != shape:
+            raise ValueError(f"out: expected {shape} on cuda:{dev}, got {tuple(out.shape)} on {out.device}")
+        _, ld_out = _matrix(out, "out")
     if add is not None:
-        m, ld_add = _matrix(add, "add")
-        if add.shape != shape:
+        row = add.shape == (N,)
+        if add.dtype is not out_dtype or add.get_device() != dev or not (row or add.shape == shape):
+            raise ValueError(f"add: expected {shape} or {(N,)} {out_dtype} on cuda:{dev}, got {tuple(add.shape)} "
+                             f"{add.dtype} on {add.device}")
+        _, ld_add = _matrix(add, "add")
+        at_add = add.data_ptr()
+        if row and len(shape) > 1:
             ld_add = 0
     need = _matmul8_workspace(M, N, K, dev)
     with _allocate_on(stream):
         if out is None:
-            out = torch.empty(shape, device=a.device, dtype=out_dtype)
+            strides, at = [1], N
+            for n in reversed(shape[:-1]):
+                strides.append(at)
+                at *= n
+            out = torch.empty_strided(shape, strides[::-1], device=a.device, dtype=out_dtype)
         if need and workspace is None:
-            workspace = torch.empty(need, device=a.device, dtype=torch.uint8)
+            workspace = torch.empty_strided((need,), (1,), device=a.device, dtype=torch.uint8)
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
     if stream is not None:
         _used_on(stream, (a, a_scale, b, b_scale, add, out, workspace))
     ws = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = load().evoattn_matmul8(
-        _PACK_MATMUL8(*left, *right, M, N, K, out.data_ptr(), ld_out, 0 if add is None else add.data_ptr(),
-                      ld_add, F32 if out_dtype is torch.float32 else BF16, *ws), _raw_stream(stream, dev))
+        _PACK_MATMUL8(*left, *right, M, N, K, out.data_ptr(), ld_out, at_add, ld_add, code, *ws),
+        _raw_stream(stream, dev))
     if st != OK:
         _check(st, "evoattn_matmul8")
     return out
