@@ -286,7 +286,7 @@ evoattn_status evoattn_quantize8(const evoattn_quantize8_args* args, cudaStream_
                                             (a.codes_t != nullptr) != (a.scales_t != nullptr)))
     return EVOATTN_ERR_INVALID_ARG;
   if (!type_ok(a.dtype)) return EVOATTN_ERR_UNSUPPORTED;
-  if (a.R > (int64_t)1 << 40 || a.K > (int64_t)1 << 40 || (__int128)rg * kg > 0x7FFFFFFF) return EVOATTN_ERR_UNSUPPORTED;
+  if (a.R > (int64_t)1 << 40 || a.K > (int64_t)1 << 40 || (__int128)rg * kg > 0x3FFFFFFF) return EVOATTN_ERR_UNSUPPORTED;
   const int bytes = bytes_of((evoattn_dtype)a.dtype);
   if (a.R > 1 && (a.ld < 0 || a.ld > kMaxSpan || (__int128)a.ld * a.R > kMaxSpan)) return EVOATTN_ERR_INVALID_ARG;
   if (a.scales && !scales_distinct(a.s_row, a.s_group, blocks ? rg : a.R, kg)) return EVOATTN_ERR_INVALID_ARG;

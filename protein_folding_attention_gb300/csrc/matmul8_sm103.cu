@@ -74,10 +74,10 @@ struct Cfg {
   static constexpr uint32_t S_BYTES = 512;  // scales of up to 128 rows, four groups
   static constexpr uint32_t S_ENTRY = (PAIR ? 3 : 2) * S_BYTES;  // of p's rows, then q's
   static constexpr uint32_t STAGE = P_BYTES + Q_BYTES;
-  // Scales: groups whose bytes go to tensor memory together (four fill a word; two
-  // where 640 threads leave 96 registers, which bytes that are underway have to
-  // fit: spilled, they are waited for), and such bundles requested ahead.
-  static constexpr int BUNDLE = SETS == 2 ? 2 : 4, AHEAD = PAIR ? 2 : 3, RING_S = 4;
+  // Scales: groups whose bytes go to tensor memory together (four fill a word;
+  // fewer where 640 threads leave 96 registers, which bytes that are underway have
+  // to fit: spilled, they are waited for), and such bundles requested ahead.
+  static constexpr int BUNDLE = SETS == 1 ? 4 : PAIR ? 1 : 2, AHEAD = PAIR && SETS == 1 ? 2 : 3, RING_S = 4;
   static constexpr uint32_t STAGING = MODE == kStaged ? SETS * 8 * 4096 : 0;
   static constexpr int STAGES = std::min<int>(8, (int)((224 * 1024 - STAGING - RING_S * S_ENTRY) / STAGE));
   static constexpr uint32_t OFF_S = STAGES * STAGE;
@@ -590,20 +590,39 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
   }
 }
 
-// Adds the pieces of the sums in order.
-template <typename T>
+// Adds the pieces of the sums: the eight warps of a CTA share 32 times V outputs,
+// warp w takes the pieces w, w + 8, ..., so that a thread's few loads are in flight
+// together, and the warps' sums are added in order.
+template <typename T, int V>
 __global__ void __launch_bounds__(256)
-    k_matmul8_sum(const float* ws, int splits, int M, int N, T* out, int64_t ld_out, const T* add, int64_t ld_add) {
+    k_matmul8_sum(const float* ws, int splits, int64_t total, Divide n, T* out, int64_t ld_out, const T* add, int64_t ld_add) {
+  using W = typename Unit<4 * V>::T;
+  __shared__ float part[8][32 * V];
   wait_for_earlier_work();
   let_next_start();
-  const int64_t total = (int64_t)M * N;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    float s = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < splits; ++k) s += ws[k * total + i];
-    const int64_t m = i / N, n = i - m * N;
-    if (add) s += load_one<T>(add + m * ld_add + n);
-    store_one(out + m * ld_out + n, s);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t first = (int64_t)blockIdx.x * (32 * V), i = first + lane * V;
+  float s[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) s[e] = 0.f;
+  if (i < total) {
+#pragma unroll 5
+    for (int k = warp; k < splits; k += 8) {
+      const W v = *reinterpret_cast<const W*>(ws + k * total + i);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] += reinterpret_cast<const float*>(&v)[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) part[warp][lane * V + e] = s[e];
+  __syncthreads();
+  if (threadIdx.x < 32 * V && first + threadIdx.x < total) {
+    float v = part[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += part[k][threadIdx.x];
+    const uint32_t at = (uint32_t)(first + threadIdx.x), m = quotient(n, at), col = at - m * n.d;
+    if (add) v += load_one<T>(add + m * ld_add + col);
+    store_one(out + m * ld_out + col, v);
   }
 }
 
@@ -674,10 +693,16 @@ cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStr
 
 template <typename T>
 cudaError_t launch_sum(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st) {
-  const int64_t blocks = ((int64_t)c.M * c.N + 255) / 256;
-  const unsigned grid = (unsigned)std::min<int64_t>(blocks, 8 * (int64_t)sms);
-  return launch_early(k_matmul8_sum<T>, grid, 256, 0, st, (const float*)c.ws, pl.splits, c.M, c.N,
-                      static_cast<T*>(c.out), c.ld_out, static_cast<const T*>(c.add), c.ld_add);
+  const int64_t total = (int64_t)c.M * c.N;  // (below 2^31: a product in pieces has few tiles)
+  const auto go = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    return launch_early(k_matmul8_sum<T, V>, (unsigned)((total + 32 * V - 1) / (32 * V)), 256, 0, st, (const float*)c.ws,
+                        pl.splits, total, divide_by((uint32_t)c.N), static_cast<T*>(c.out), c.ld_out,
+                        static_cast<const T*>(c.add), c.ld_add);
+  };
+  // pieces are 16-byte aligned one after another; small sums keep the SMs busy
+  return total % 4 == 0 && total >= 128 * (int64_t)sms ? go(std::integral_constant<int, 4>{})
+                                                       : go(std::integral_constant<int, 1>{});
 }
 
 template <int BQ>
@@ -713,7 +738,7 @@ Matmul8Plan matmul8_plan(int M, int N, int K, int sms) {
   if (M > 64 && pl.splits == 1) {  // a's rows on the lanes
     pl.staged = true;
     pl.bq = 128;
-    if (pl.groups > 8 && (int64_t)tiles(M, 2 * kLanes) * tiles(N, 240) >= sms / 2) {
+    if ((int64_t)tiles(M, 2 * kLanes) * tiles(N, 240) >= sms / 2) {
       // Pairs of CTAs.  A step of a pair's tiles costs 1 in units of a step of 128
       // columns where it has 192, and 1.05 where it has 240: what is least over N.
       const double by128 = 1.1 * tiles(N, 128), by192 = 1.0 * tiles(N, 192), by240 = 1.05 * tiles(N, 240);
@@ -731,6 +756,12 @@ size_t matmul8_workspace_bytes(int M, int N, int K, int sms) {
 }
 
 cudaError_t matmul8(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
+  if (pl.staged && pl.groups <= 8 && pl.bq == 240)
+    return c.f32 ? launch<float, 240, kStaged, 2>(c, pl, sms, st, tmap_ok)
+                 : launch<__nv_bfloat16, 240, kStaged, 2>(c, pl, sms, st, tmap_ok);
+  if (pl.staged && pl.groups <= 8 && pl.bq == 192)
+    return c.f32 ? launch<float, 192, kStaged, 2>(c, pl, sms, st, tmap_ok)
+                 : launch<__nv_bfloat16, 192, kStaged, 2>(c, pl, sms, st, tmap_ok);
   if (pl.staged && pl.groups <= 8)
     return c.f32 ? launch<float, 128, kStaged, 2>(c, pl, sms, st, tmap_ok)
                  : launch<__nv_bfloat16, 128, kStaged, 2>(c, pl, sms, st, tmap_ok);

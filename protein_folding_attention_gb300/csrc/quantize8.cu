@@ -16,11 +16,19 @@
 // magnitudes, which skips NaN, and infinities are looked for once per tile and
 // turned into NaN, instead of a test per element.
 //
+// bf16 tiles come through a ring of two in shared memory, filled by cp.async by
+// persistent CTAs while the tile before is worked on (a thread copies and reads
+// only its own units: no barrier): with loads into registers 48 % of the warps that
+// an SM can hold waited for them most of the time, 102 us for 147,456 x 512 where
+// the bytes take 45.  fp32 tiles, twice the size, are loaded into registers.
 // Rows that are no whole 16-byte units come through shared memory too: a warp
 // reads a row's elements 32 at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
+#include "divide.cuh"
 #include "launch.cuh"
 #include "quantize8.h"
 #include "scale8.cuh"
@@ -76,174 +84,223 @@ __device__ __forceinline__ void put_codes(uint8_t* p, uint2 q, int n) {
   for (int e = 0; e < n; ++e) p[e] = (uint8_t)(v >> 8 * e);
 }
 
+// Shared memory of a CTA: the ring or the tile as it was read, and the transposed
+// codes (which take the place of the latter).
 template <typename T, bool VEC, bool COLS>
-__global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c, uint32_t tiles_k) {
+struct Smem {
+  static constexpr bool RING = VEC && sizeof(T) == 2;
+  static constexpr int DEPTH = 2;
+  static constexpr uint32_t STAGE = kRows * kThreads * 16;
+  static constexpr uint32_t RAW = VEC ? 0 : kGroup8 * Load<T>::PITCH * sizeof(T);
+  static constexpr uint32_t TURNED = COLS ? kGroup8 * kGroup8 : 0;
+  static constexpr uint32_t BYTES = RING ? DEPTH * STAGE + TURNED : RAW > TURNED ? RAW : TURNED;
+};
+
+template <typename T, bool VEC, bool COLS>
+__global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c, Divide tiles_k, uint32_t tiles) {
+  using M = Smem<T, VEC, COLS>;
   __shared__ float col_max[COLS ? kThreads / 32 : 1][kGroup8];
   __shared__ float col_inv[kGroup8];
-  // the tile as it was read (rows that are no whole units), then transposed codes
-  extern __shared__ __align__(16) uint8_t tile[];
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* const tile = smem + (M::RING ? M::DEPTH * M::STAGE : 0);
   wait_for_earlier_work();
   let_next_start();
-  const uint32_t tr = blockIdx.x / tiles_k, tk = blockIdx.x - tr * tiles_k;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r0 = (int64_t)tr * kGroup8 + ty * kRows;
-  const int64_t k0 = (int64_t)tk * kGroup8 + tx * 8;
-  const int nk = (int)min((int64_t)8, c.K - k0);      // this thread's columns (may be negative)
-  const int nr = (int)min((int64_t)kRows, c.R - r0);  // and rows
-  float f[kRows][8];
-  const T* x = static_cast<const T*>(c.x);
-  if constexpr (VEC) {  // (K is a multiple of 8)
+  // this thread's units of a tile into the ring
+  const auto fill = [&](uint32_t t, int stage) {
+    if (t < tiles) {
+      const uint32_t tr = quotient(tiles_k, t), tk = t - tr * tiles_k.d;
+      const int64_t r = (int64_t)tr * kGroup8 + ty * kRows, k = (int64_t)tk * kGroup8 + tx * 8;
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem) + stage * M::STAGE + threadIdx.x * 16;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (i < nr && nk > 0) {
-        Load<T>::eight(x + (r0 + i) * c.ld + k0, f[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
+      for (int i = 0; i < kRows; ++i) {
+        const bool on = r + i < c.R && k < c.K;  // (K is a multiple of 8)
+        const T* from = static_cast<const T*>(c.x) + (on ? (r + i) * c.ld + k : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * kThreads * 16), "l"(from),
+                     "r"(on ? 16 : 0) : "memory");
       }
     }
-  } else {
-    T* rows = reinterpret_cast<T*>(tile);
-    constexpr int PER = kGroup8 / (kThreads / 32);  // rows of a warp
-    T v[PER][4];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int64_t r = (int64_t)tr * kGroup8 + warp * PER + i, k = (int64_t)tk * kGroup8 + lane;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[i][e] = r < c.R && k + 32 * e < c.K ? x[r * c.ld + k + 32 * e] : T(0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) rows[(warp * PER + i) * Load<T>::PITCH + lane + 32 * e] = v[i][e];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) Load<T>::eight_shared(rows + (ty * kRows + i) * Load<T>::PITCH + tx * 8, f[i]);
-  }
-  // row maxima, and whether there is an infinity (in the warp's rows, or, where
-  // columns need it, in the tile)
-  float row[kRows];
-  const auto row_maxima = [&] {
-    float all = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      row[i] = max_abs8(f[i]);
-      all = fmaxf(all, row[i]);
-    }
-    return all;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  const bool infinite = row_maxima() > FLT_MAX;
-  if (COLS ? __syncthreads_or(infinite) : __any_sync(0xffffffffu, infinite)) {
+  if constexpr (M::RING) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = infinity_to_nan(f[i][e]);
-    row_maxima();
+    for (int k = 0; k < M::DEPTH - 1; ++k) fill(blockIdx.x + k * gridDim.x, k);
   }
-  float block = 0.f;
-  if constexpr (COLS) {
-    // column maxima: 4 rows of this thread, the other half of the warp, 16 warps
+  uint32_t step = 0;
+#pragma unroll 1
+  for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x, ++step) {
+    const uint32_t tr = quotient(tiles_k, t), tk = t - tr * tiles_k.d;
+    const int64_t r0 = (int64_t)tr * kGroup8 + ty * kRows;
+    const int64_t k0 = (int64_t)tk * kGroup8 + tx * 8;
+    const int nk = (int)min((int64_t)8, c.K - k0);      // this thread's columns (may be negative)
+    const int nr = (int)min((int64_t)kRows, c.R - r0);  // and rows
+    float f[kRows][8];
+    const T* x = static_cast<const T*>(c.x);
+    if constexpr (M::RING) {
+      fill(t + (M::DEPTH - 1) * gridDim.x, (step + M::DEPTH - 1) % M::DEPTH);
+      asm volatile("cp.async.wait_group %0;" ::"n"(M::DEPTH - 1) : "memory");
+      const T* from = reinterpret_cast<const T*>(smem + (step % M::DEPTH) * M::STAGE + threadIdx.x * 16);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float m = max_abs3(f[0][e], f[1][e], max_abs3(f[2][e], f[3][e], 0.f));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      if (lane < 16) col_max[warp][tx * 8 + e] = m;
-    }
-    __syncthreads();
-    if (threadIdx.x < kGroup8) {
-      float m = col_max[0][threadIdx.x];
+      for (int i = 0; i < kRows; ++i) Load<T>::eight_shared(from + i * kThreads * 8, f[i]);
+    } else if constexpr (VEC) {  // (K is a multiple of 8)
 #pragma unroll
-      for (int k = 1; k < kThreads / 32; ++k) m = fmaxf(m, col_max[k][threadIdx.x]);
-      if (!c.blocks) {
-        const uint32_t code = scale_code(m);
-        m = scale_inverse(code);
-        const int64_t k = (int64_t)tk * kGroup8 + threadIdx.x;
-        if (k < c.K) c.scales_t[k * c.st_row + (int64_t)tr * c.st_group] = (uint8_t)code;
+      for (int i = 0; i < kRows; ++i) {
+        if (i < nr && nk > 0) {
+          Load<T>::eight(x + (r0 + i) * c.ld + k0, f[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
+        }
       }
-      col_inv[threadIdx.x] = m;
-    }
-    __syncthreads();
-    if (c.blocks) {
-      float m = 0.f;
+    } else {
+      T* rows = reinterpret_cast<T*>(tile);
+      constexpr int PER = kGroup8 / (kThreads / 32);  // rows of a warp
+      T v[PER][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m = fmaxf(m, col_inv[lane + 32 * k]);
+      for (int i = 0; i < PER; ++i) {
+        const int64_t r = (int64_t)tr * kGroup8 + warp * PER + i, k = (int64_t)tk * kGroup8 + lane;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const uint32_t code = scale_code(m);
-      block = scale_inverse(code);
-      if (threadIdx.x == 0) c.scales[(int64_t)tr * c.s_row + (int64_t)tk * c.s_group] = (uint8_t)code;
-    }
-  }
-  if (c.codes) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      float inv = block;
-      if (!COLS || !c.blocks) {
-        float m = row[i];
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t code = scale_code(m);
-        inv = scale_inverse(code);
-        if (tx == 0 && i < nr) c.scales[(r0 + i) * c.s_row + (int64_t)tk * c.s_group] = (uint8_t)code;
+        for (int e = 0; e < 4; ++e) v[i][e] = r < c.R && k + 32 * e < c.K ? x[r * c.ld + k + 32 * e] : T(0.f);
       }
-      if (i < nr && nk > 0)
-        put_codes(c.codes + (r0 + i) * c.ldc + k0,
-                  make_uint2(e4m3_four(f[i][0], f[i][1], f[i][2], f[i][3], inv),
-                             e4m3_four(f[i][4], f[i][5], f[i][6], f[i][7], inv)), nk);
-    }
-  }
-  if (COLS && c.codes_t) {
-    // (every thread is past its reads of the tile as it came: the barriers above)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int col = tx * 8 + e;
-      const float inv = c.blocks ? block : col_inv[col];
-      *reinterpret_cast<uint32_t*>(tile + col * kGroup8 + ((ty ^ 2 * tx) << 2)) =
-          e4m3_four(f[0][e], f[1][e], f[2][e], f[3][e], inv);
-    }
-    __syncthreads();
-    // eight threads write a column of the tile (128 bytes), 16 bytes each
+      for (int i = 0; i < PER; ++i)
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      const int col = pass * 64 + (threadIdx.x >> 3), word = (threadIdx.x & 7) * 4, turn = 2 * (col >> 3);
-      const int64_t k = (int64_t)tk * kGroup8 + col, r = (int64_t)tr * kGroup8 + word * 4;
-      const uint2 a = *reinterpret_cast<const uint2*>(tile + col * kGroup8 + ((word ^ turn) << 2));
-      const uint2 b = *reinterpret_cast<const uint2*>(tile + col * kGroup8 + (((word + 2) ^ turn) << 2));
-      if (k >= c.K) continue;
-      uint8_t* to = c.codes_t + k * c.ldt + r;
-      if (r + 16 <= c.R) {
-        *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
-      } else if (r < c.R) {
-        put_codes(to, a, (int)min((int64_t)8, c.R - r));
-        if (r + 8 < c.R) put_codes(to + 8, b, (int)min((int64_t)8, c.R - r - 8));
+        for (int e = 0; e < 4; ++e) rows[(warp * PER + i) * Load<T>::PITCH + lane + 32 * e] = v[i][e];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) Load<T>::eight_shared(rows + (ty * kRows + i) * Load<T>::PITCH + tx * 8, f[i]);
+    }
+    // row maxima, and whether there is an infinity (in the warp's rows, or, where
+    // columns need it, in the tile)
+    float row[kRows];
+    const auto row_maxima = [&] {
+      float all = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        row[i] = max_abs8(f[i]);
+        all = fmaxf(all, row[i]);
+      }
+      return all;
+    };
+    const bool infinite = row_maxima() > FLT_MAX;
+    if (COLS ? __syncthreads_or(infinite) : __any_sync(0xffffffffu, infinite)) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[i][e] = infinity_to_nan(f[i][e]);
+      row_maxima();
+    }
+    float block = 0.f;
+    if constexpr (COLS) {
+      // column maxima: 4 rows of this thread, the other half of the warp, 16 warps
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float m = max_abs3(f[0][e], f[1][e], max_abs3(f[2][e], f[3][e], 0.f));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (lane < 16) col_max[warp][tx * 8 + e] = m;
+      }
+      __syncthreads();
+      if (threadIdx.x < kGroup8) {
+        float m = col_max[0][threadIdx.x];
+#pragma unroll
+        for (int k = 1; k < kThreads / 32; ++k) m = fmaxf(m, col_max[k][threadIdx.x]);
+        if (!c.blocks) {
+          const uint32_t code = scale_code(m);
+          m = scale_inverse(code);
+          const int64_t k = (int64_t)tk * kGroup8 + threadIdx.x;
+          if (k < c.K) c.scales_t[k * c.st_row + (int64_t)tr * c.st_group] = (uint8_t)code;
+        }
+        col_inv[threadIdx.x] = m;
+      }
+      __syncthreads();
+      if (c.blocks) {
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = fmaxf(m, col_inv[lane + 32 * k]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t code = scale_code(m);
+        block = scale_inverse(code);
+        if (threadIdx.x == 0) c.scales[(int64_t)tr * c.s_row + (int64_t)tk * c.s_group] = (uint8_t)code;
+      }
+    }
+    if (c.codes) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        float inv = block;
+        if (!COLS || !c.blocks) {
+          float m = row[i];
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t code = scale_code(m);
+          inv = scale_inverse(code);
+          if (tx == 0 && i < nr) c.scales[(r0 + i) * c.s_row + (int64_t)tk * c.s_group] = (uint8_t)code;
+        }
+        if (i < nr && nk > 0)
+          put_codes(c.codes + (r0 + i) * c.ldc + k0,
+                    make_uint2(e4m3_four(f[i][0], f[i][1], f[i][2], f[i][3], inv),
+                               e4m3_four(f[i][4], f[i][5], f[i][6], f[i][7], inv)), nk);
+      }
+    }
+    if (COLS && c.codes_t) {
+      // (every thread is past its reads of the tile as it came: the barriers above)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int col = tx * 8 + e;
+        const float inv = c.blocks ? block : col_inv[col];
+        *reinterpret_cast<uint32_t*>(tile + col * kGroup8 + ((ty ^ 2 * tx) << 2)) =
+            e4m3_four(f[0][e], f[1][e], f[2][e], f[3][e], inv);
+      }
+      __syncthreads();
+      // eight threads write a column of the tile (128 bytes), 16 bytes each
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+        const int col = pass * 64 + (threadIdx.x >> 3), word = (threadIdx.x & 7) * 4, turn = 2 * (col >> 3);
+        const int64_t k = (int64_t)tk * kGroup8 + col, r = (int64_t)tr * kGroup8 + word * 4;
+        const uint2 a = *reinterpret_cast<const uint2*>(tile + col * kGroup8 + ((word ^ turn) << 2));
+        const uint2 b = *reinterpret_cast<const uint2*>(tile + col * kGroup8 + (((word + 2) ^ turn) << 2));
+        if (k >= c.K) continue;
+        uint8_t* to = c.codes_t + k * c.ldt + r;
+        if (r + 16 <= c.R) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
+        } else if (r < c.R) {
+          put_codes(to, a, (int)min((int64_t)8, c.R - r));
+          if (r + 8 < c.R) put_codes(to + 8, b, (int)min((int64_t)8, c.R - r - 8));
+        }
       }
     }
   }
 }
 
 template <typename T, bool VEC, bool COLS>
-cudaError_t launch(const Quantize8Call& c, uint64_t tiles, uint32_t tiles_k, cudaStream_t st) {
-  constexpr size_t raw = VEC ? 0 : (size_t)kGroup8 * Load<T>::PITCH * sizeof(T), turned = COLS ? kGroup8 * kGroup8 : 0;
-  constexpr size_t smem = raw > turned ? raw : turned;
+cudaError_t launch(const Quantize8Call& c, uint32_t tiles, Divide tiles_k, cudaStream_t st) {
+  using M = Smem<T, VEC, COLS>;
   auto kern = k_quantize8<T, VEC, COLS>;
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)M::BYTES);
+  uint32_t grid = tiles;
+  if (e == cudaSuccess && M::RING) {  // persistent: two CTAs per SM
+    int dev = 0, sms = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    grid = std::min(tiles, 2u * (uint32_t)std::max(sms, 1));
   }
-  return launch_early(kern, (unsigned)tiles, kThreads, smem, st, c, tiles_k);
+  if (e != cudaSuccess) return e;
+  return launch_early(kern, grid, kThreads, M::BYTES, st, c, tiles_k, tiles);
 }
 
 template <typename T>
 cudaError_t run(const Quantize8Call& c, cudaStream_t st) {
   const uint64_t tiles_k = (uint64_t)((c.K + kGroup8 - 1) / kGroup8);
   const uint64_t tiles = (uint64_t)((c.R + kGroup8 - 1) / kGroup8) * tiles_k;
-  if (tiles > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  if (tiles > 0x3FFFFFFFull)  // (with the steps behind the last one in 32 bits)
+    return cudaErrorInvalidConfiguration;
   const bool vec = c.K % 8 == 0 && reinterpret_cast<uintptr_t>(c.x) % 16 == 0 &&
                    c.ld * (int64_t)sizeof(T) % 16 == 0;
-  const uint32_t tk = (uint32_t)tiles_k;
+  const Divide tk = divide_by((uint32_t)tiles_k);
+  const uint32_t n = (uint32_t)tiles;
   if (c.codes_t || c.blocks)
-    return vec ? launch<T, true, true>(c, tiles, tk, st) : launch<T, false, true>(c, tiles, tk, st);
-  return vec ? launch<T, true, false>(c, tiles, tk, st) : launch<T, false, false>(c, tiles, tk, st);
+    return vec ? launch<T, true, true>(c, n, tk, st) : launch<T, false, true>(c, n, tk, st);
+  return vec ? launch<T, true, false>(c, n, tk, st) : launch<T, false, false>(c, n, tk, st);
 }
 
 }  // namespace
