@@ -63,12 +63,12 @@ constexpr int kLanes = 128;  // rows of the operand on the lanes
 constexpr int kGroup = 128;  // elements along k of a stage, and of a scale
 enum Mode { kStaged, kDirect, kPartial };  // a on the lanes; b on the lanes; that, and a piece of the sum
 
-// BQ: rows of the operand on the columns; above 128 in clusters of two CTAs.
-// SETS: groups of eight epilogue warps.
-template <int BQ_, Mode MODE, int SETS>
+// BQ: rows of the operand on the columns.  SETS: groups of eight epilogue warps.
+// PAIR: clusters of two CTAs with the same rows of the operand on the columns.
+template <int BQ_, Mode MODE, int SETS, bool PAIR_>
 struct Cfg {
   static constexpr int BQ = BQ_;
-  static constexpr bool PAIR = BQ > 128;
+  static constexpr bool PAIR = PAIR_;
   static constexpr int THREADS = 128 + SETS * 256;
   static constexpr uint32_t P_BYTES = kLanes * kGroup, Q_BYTES = BQ * kGroup;
   static constexpr uint32_t S_BYTES = 512;  // scales of up to 128 rows, four groups
@@ -77,7 +77,7 @@ struct Cfg {
   // Scales: groups whose bytes go to tensor memory together (four fill a word;
   // fewer where 640 threads leave 96 registers, which bytes that are underway have
   // to fit: spilled, they are waited for), and such bundles requested ahead.
-  static constexpr int BUNDLE = SETS == 1 ? 4 : PAIR ? 1 : 2, AHEAD = PAIR && SETS == 1 ? 2 : 3, RING_S = 4;
+  static constexpr int BUNDLE = SETS == 1 ? 4 : 2, AHEAD = PAIR ? 2 : 3, RING_S = 4;
   static constexpr uint32_t STAGING = MODE == kStaged ? SETS * 8 * 4096 : 0;
   static constexpr int STAGES = std::min<int>(8, (int)((224 * 1024 - STAGING - RING_S * S_ENTRY) / STAGE));
   static constexpr uint32_t OFF_S = STAGES * STAGE;
@@ -85,6 +85,7 @@ struct Cfg {
   static constexpr uint32_t SMEM_ALLOC = OFF_STAGING + STAGING + 1024;
   static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ;  // scales: 4 columns for each 128 rows
   static_assert(COL_S + 12 <= 512 && SMEM_ALLOC <= 227 * 1024, "tensor memory, shared memory");
+  static_assert(PAIR == (BQ > 128), "more than 128 rows on the columns: scales of two blocks");
   static_assert(STAGE % 1024 == 0 && OFF_STAGING % 1024 == 0 && (!PAIR || Q_BYTES % 2048 == 0), "the swizzle repeats every 1024 bytes");
 };
 
@@ -238,7 +239,6 @@ __device__ __forceinline__ void scale_role(const Params8& p, bool of_q, uint8_t*
 #pragma unroll
           for (int j = 1; j < C::BUNDLE; ++j) v[i] |= s[k][i][j] << 8 * j;
         }
-        request(s[k]);
         if (is >= C::RING_S) ok = mbar_wait(&bar_copied[slot], ((is / C::RING_S) - 1) & 1, wctx);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
@@ -249,6 +249,7 @@ __device__ __forceinline__ void scale_role(const Params8& p, bool of_q, uint8_t*
           fence_proxy_async_smem();  // generic writes, read by the copy to tensor memory
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_scale[slot]);
+          request(s[k]);  // (behind the fence, which waits for loads that are underway)
         }
       }
     }
@@ -265,10 +266,46 @@ __device__ __forceinline__ float load_one<__nv_bfloat16>(const __nv_bfloat16* p)
 __device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Shared memory by its own address (the compiler would take the generic one).
+__device__ __forceinline__ uint4 lds(uint32_t at, uint4) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds(uint32_t at, uint2) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds(uint32_t at, uint32_t) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t lds(uint32_t at, uint16_t) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts(uint32_t at, uint2 v) {
+  asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(at), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void sts(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts(uint32_t at, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
+}
+
 // Copies between a warp's staging buffer (rows of 128 bytes, 16-byte units XORed
 // with the row) and 32 rows of a matrix, V bytes per lane.  `at`: the first row's
 // first byte; `rows`, `width`: how many rows and bytes of a row there are (a
-// multiple of V).
+// multiple of V).  All of a lane's loads are issued before its stores (one after
+// the other, each store behind its load, 147,456 x 128 outputs with an addend took
+// 34 us).
 template <int V>
 struct Unit;
 template <>
@@ -281,28 +318,35 @@ template <>
 struct Unit<2> { using T = uint16_t; };
 
 template <int V, bool STORE>
-__device__ __forceinline__ void copy_rows(uint8_t* stg, uint8_t* at, int64_t stride, int rows, int width) {
+__device__ __forceinline__ void copy_rows(uint32_t stg, uint8_t* at, int64_t stride, int rows, int width) {
   using T = typename Unit<V>::T;
   constexpr int PER = 128 / V;                     // units of a row
   constexpr int STEP = PER <= 32 ? 32 / PER : 1;   // rows at a time
+  constexpr int COUNT = 32 / STEP;                 // units of a lane
   const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < (PER <= 32 ? 1 : PER / 32); ++h) {
     const int r0 = PER <= 32 ? lane / PER : 0, b = (PER <= 32 ? lane % PER : lane + 32 * h) * V;
     if (b >= width) continue;
     uint8_t* g = at + r0 * stride + b;
-#pragma unroll 8
-    for (int r = r0; r < rows; r += STEP, g += STEP * stride) {
-      T* const s = reinterpret_cast<T*>(stg + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
-      if constexpr (STORE)
-        *reinterpret_cast<T*>(g) = *s;
-      else
-        *s = *reinterpret_cast<const T*>(g);
+    const auto place = [&](int r) { return stg + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15); };
+    T v[COUNT];
+    if constexpr (STORE) {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) v[i] = lds(place(r0 + i * STEP), T{});
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i, g += STEP * stride)
+        if (r0 + i * STEP < rows) *reinterpret_cast<T*>(g) = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i, g += STEP * stride) v[i] = r0 + i * STEP < rows ? *reinterpret_cast<const T*>(g) : T{};
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) sts(place(r0 + i * STEP), v[i]);
     }
   }
 }
 template <bool STORE>
-__device__ __forceinline__ void copy_rows(int unit, uint8_t* stg, uint8_t* at, int64_t stride, int rows, int width) {
+__device__ __forceinline__ void copy_rows(int unit, uint32_t stg, uint8_t* at, int64_t stride, int rows, int width) {
   switch (unit) {
     case 16: return copy_rows<16, STORE>(stg, at, stride, rows, width);
     case 8: return copy_rows<8, STORE>(stg, at, stride, rows, width);
@@ -313,30 +357,32 @@ __device__ __forceinline__ void copy_rows(int unit, uint8_t* stg, uint8_t* at, i
 
 // 128 bytes of a row of out for this lane: from the accumulator's columns to the
 // lane's row of the staging buffer, with what the buffer holds of add.
-__device__ __forceinline__ void stage_row(uint8_t* stg, const uint32_t (&r)[32], bool add, float) {
+__device__ __forceinline__ void stage_row(uint32_t stg, const uint32_t (&r)[32], bool add) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    float4* to = reinterpret_cast<float4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4));
-    float4 v = make_float4(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]), __uint_as_float(r[4 * c + 2]),
-                           __uint_as_float(r[4 * c + 3]));
+    const uint32_t to = stg + lane * 128 + ((c ^ (lane & 7)) << 4);
+    uint4 v = make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
     if (add) {
-      const float4 a = *to;
-      v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+      const uint4 a = lds(to, uint4{});
+      v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(a.x));
+      v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(a.y));
+      v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(a.z));
+      v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(a.w));
     }
-    *to = v;
+    sts(to, v);
   }
 }
-__device__ __forceinline__ void stage_row(uint8_t* stg, const uint32_t (&lo)[32], const uint32_t (&hi)[32], bool add) {
+__device__ __forceinline__ void stage_row(uint32_t stg, const uint32_t (&lo)[32], const uint32_t (&hi)[32], bool add) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    uint4* to = reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4));
+    const uint32_t to = stg + lane * 128 + ((c ^ (lane & 7)) << 4);
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(c < 4 ? lo[8 * c + e] : hi[8 * (c - 4) + e]);
     if (add) {
-      const uint4 a = *to;
+      const uint4 a = lds(to, uint4{});
       const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -344,14 +390,14 @@ __device__ __forceinline__ void stage_row(uint8_t* stg, const uint32_t (&lo)[32]
         f[2 * e + 1] += bf16hi(w[e]);
       }
     }
-    *to = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    sts(to, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
   }
 }
 
-template <typename T, int BQ, Mode MODE, int SETS>
+template <typename T, int BQ, Mode MODE, int SETS, bool PAIR>
 __global__ void __launch_bounds__(128 + SETS * 256, 1)
     k_matmul8(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q, const Params8 p) {
-  using C = Cfg<BQ, MODE, SETS>;
+  using C = Cfg<BQ, MODE, SETS, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -507,8 +553,16 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + buf * BQ;
+      // The accumulator is free for the next tile but one as soon as its values are
+      // in registers.
+      bool held = true;
+      const auto release = [&] {
+        tc_fence_before();
+        mbar_arrive(&bar_free[buf]);
+        held = false;
+      };
       if constexpr (MODE == kStaged) {
-        uint8_t* stg = smem + C::OFF_STAGING + (warp - 4) * 4096;
+        const uint32_t stg = smem_u32(smem + C::OFF_STAGING + (warp - 4) * 4096);
         constexpr int SPAN = 128 / sizeof(T);  // columns of a chunk
         const int m = w.p0 + quad * 32, rows = min(32, p.M - m);
 #pragma unroll 1
@@ -519,20 +573,20 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
           tmem_ld32(base + c, lo);
           if constexpr (sizeof(T) == 2) tmem_ld32(base + c + 32, hi);
           __syncwarp();  // the previous chunk has left the buffer
+          tmem_wait_ld();
+          reg_fence32(lo);
+          if constexpr (sizeof(T) == 2) reg_fence32(hi);
+          if (c + 2 * SPAN >= BQ || n + 2 * SPAN >= p.N) release();
           if (p.add) {
             copy_rows<false>(p.unit_add, stg,
                              static_cast<uint8_t*>(const_cast<void*>(p.add)) + (m * p.ld_add + n) * (int64_t)sizeof(T),
                              p.ld_add * (int64_t)sizeof(T), rows, width);
             __syncwarp();
           }
-          tmem_wait_ld();
-          reg_fence32(lo);
-          if constexpr (sizeof(T) == 2) {
-            reg_fence32(hi);
+          if constexpr (sizeof(T) == 2)
             stage_row(stg, lo, hi, p.add != nullptr);
-          } else {
-            stage_row(stg, lo, p.add != nullptr, 0.f);
-          }
+          else
+            stage_row(stg, lo, p.add != nullptr);
           __syncwarp();
           copy_rows<true>(p.unit, stg, static_cast<uint8_t*>(p.out) + (m * p.ld_out + n) * (int64_t)sizeof(T),
                           p.ld_out * (int64_t)sizeof(T), rows, width);
@@ -548,6 +602,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
           tmem_ld16(base + c * 16, r);
           tmem_wait_ld();
           reg_fence16(r);
+          if (c + 2 >= BQ / 16 || m + 32 >= p.M) release();
           if constexpr (MODE == kPartial) {
             float* to = p.ws + ((int64_t)w.split * p.M + m) * p.N + col;
 #pragma unroll
@@ -567,8 +622,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
           }
         }
       }
-      tc_fence_before();
-      mbar_arrive(&bar_free[buf]);
+      if (held) release();
     }
   }
   tc_fence_before();
@@ -643,9 +697,9 @@ int unit_of(const void* p, int64_t stride, int64_t width) {
   return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
 }
 
-template <typename T, int BQ, Mode MODE, int SETS = 1>
+template <typename T, int BQ, Mode MODE, int SETS = 1, bool PAIR = false>
 cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  using C = Cfg<BQ, MODE, SETS>;
+  using C = Cfg<BQ, MODE, SETS, PAIR>;
   Params8 p{};
   p.p = MODE == kStaged ? c.a : c.b;
   p.q = MODE == kStaged ? c.b : c.a;
@@ -669,7 +723,7 @@ cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStr
   p.unit_add = unit_of(c.add, c.ld_add * size, c.N * size);
   p.ws = c.ws;
   p.wc = launch_wait(c.wait);
-  auto kern = k_matmul8<T, BQ, MODE, SETS>;
+  auto kern = k_matmul8<T, BQ, MODE, SETS, PAIR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
   if constexpr (C::PAIR) {
@@ -705,6 +759,12 @@ cudaError_t launch_sum(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cud
                                                        : go(std::integral_constant<int, 1>{});
 }
 
+template <int BQ, int SETS, bool PAIR>
+cudaError_t staged(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
+  return c.f32 ? launch<float, BQ, kStaged, SETS, PAIR>(c, pl, sms, st, tmap_ok)
+               : launch<__nv_bfloat16, BQ, kStaged, SETS, PAIR>(c, pl, sms, st, tmap_ok);
+}
+
 template <int BQ>
 cudaError_t few_rows(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
   if (pl.splits > 1) {
@@ -738,13 +798,14 @@ Matmul8Plan matmul8_plan(int M, int N, int K, int sms) {
   if (M > 64 && pl.splits == 1) {  // a's rows on the lanes
     pl.staged = true;
     pl.bq = 128;
-    if ((int64_t)tiles(M, 2 * kLanes) * tiles(N, 240) >= sms / 2) {
+    if (N > 128 && pl.groups > 8 && (int64_t)tiles(M, 2 * kLanes) * tiles(N, 240) >= sms / 2) {
       // Pairs of CTAs.  A step of a pair's tiles costs 1 in units of a step of 128
       // columns where it has 192, and 1.05 where it has 240: what is least over N.
       const double by128 = 1.1 * tiles(N, 128), by192 = 1.0 * tiles(N, 192), by240 = 1.05 * tiles(N, 240);
-      if (by192 < by128 || by240 < by128) pl.bq = by192 < by240 ? 192 : 240;
+      pl.pair = by192 < by128 || by240 < by128;
+      if (pl.pair) pl.bq = by192 < by240 ? 192 : 240;
     }
-    pl.tiles_p = pl.bq > 128 ? tiles(M, 2 * kLanes) : tiles(M, kLanes);
+    pl.tiles_p = tiles(M, pl.pair ? 2 * kLanes : kLanes);
     pl.tiles_q = tiles(N, pl.bq);
   }
   return pl;
@@ -756,24 +817,10 @@ size_t matmul8_workspace_bytes(int M, int N, int K, int sms) {
 }
 
 cudaError_t matmul8(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  if (pl.staged && pl.groups <= 8 && pl.bq == 240)
-    return c.f32 ? launch<float, 240, kStaged, 2>(c, pl, sms, st, tmap_ok)
-                 : launch<__nv_bfloat16, 240, kStaged, 2>(c, pl, sms, st, tmap_ok);
-  if (pl.staged && pl.groups <= 8 && pl.bq == 192)
-    return c.f32 ? launch<float, 192, kStaged, 2>(c, pl, sms, st, tmap_ok)
-                 : launch<__nv_bfloat16, 192, kStaged, 2>(c, pl, sms, st, tmap_ok);
-  if (pl.staged && pl.groups <= 8)
-    return c.f32 ? launch<float, 128, kStaged, 2>(c, pl, sms, st, tmap_ok)
-                 : launch<__nv_bfloat16, 128, kStaged, 2>(c, pl, sms, st, tmap_ok);
-  if (pl.staged && pl.bq == 240)
-    return c.f32 ? launch<float, 240, kStaged>(c, pl, sms, st, tmap_ok)
-                 : launch<__nv_bfloat16, 240, kStaged>(c, pl, sms, st, tmap_ok);
-  if (pl.staged && pl.bq == 192)
-    return c.f32 ? launch<float, 192, kStaged>(c, pl, sms, st, tmap_ok)
-                 : launch<__nv_bfloat16, 192, kStaged>(c, pl, sms, st, tmap_ok);
-  if (pl.staged)
-    return c.f32 ? launch<float, 128, kStaged>(c, pl, sms, st, tmap_ok)
-                 : launch<__nv_bfloat16, 128, kStaged>(c, pl, sms, st, tmap_ok);
+  if (pl.staged && pl.pair)
+    return pl.bq == 240 ? staged<240, 1, true>(c, pl, sms, st, tmap_ok) : staged<192, 1, true>(c, pl, sms, st, tmap_ok);
+  if (pl.staged && pl.groups <= 8) return staged<128, 2, false>(c, pl, sms, st, tmap_ok);
+  if (pl.staged) return staged<128, 1, false>(c, pl, sms, st, tmap_ok);
   switch (pl.bq) {
     case 16: return few_rows<16>(c, pl, sms, st, tmap_ok);
     case 32: return few_rows<32>(c, pl, sms, st, tmap_ok);
