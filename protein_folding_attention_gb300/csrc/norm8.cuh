@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "divide.cuh"
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm8_bwd(const Params p, uint3
   constexpr int E = L::E, PER = kThreads / LANES;
   __shared__ float sums[2][T][8], sums2[2][T][8];
   constexpr int N = PARTS * L::SPAN;  // channels that the threads of a row have places for (C at least)
-  __shared__ __align__(16) float prm[2 * N];  // gamma; in the end the parameters' gradients [2][C]
+  __shared__ __align__(16) float prm[N];  // gamma
   wait_for_earlier_work();
   let_next_start();
   const int lane = threadIdx.x % LANES;
@@ -716,25 +717,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm8_bwd(const Params p, uint3
     }
     if constexpr (LANES > 32) __syncthreads();  // the next rows' sums
   }
+  // The CTA's sums: a warp's row groups by shuffles, then each warp's sums lie in
+  // shared memory and are added in order.
+  constexpr int ROWS = LANES <= 32 ? kThreads / 32 : PER;  // sums of a channel that are left
+  float* const sums_g = reinterpret_cast<float*>(ring);
+  if constexpr (VEC && R::USED) asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();  // (every thread is through with the ring)
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float g = ag[k][e], b = ab[k][e];
+#pragma unroll
+      for (int o = 16; o >= LANES; o >>= 1) {
+        g += __shfl_xor_sync(0xffffffffu, g, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+      const int row = LANES <= 32 ? (int)threadIdx.x >> 5 : (int)threadIdx.x / LANES;
+      if (LANES >= 32 || (int)(threadIdx.x & 31) < LANES) {
+        float* to = sums_g + row * 2 * N + L::chan(lane, k) + L::off(e);
+        to[0] = g;
+        to[N] = b;
+      }
+    }
   __syncthreads();
-  // the row groups of the CTA, one after another
-#pragma unroll 1
-  for (int q = 0; q < PER; ++q) {
-    if ((int)threadIdx.x / LANES == q)
-#pragma unroll
-      for (int k = 0; k < PARTS; ++k)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int c = L::chan(lane, k) + L::off(e);
-          if (c < p.C) {
-            prm[c] = q ? prm[c] + ag[k][e] : ag[k][e];
-            prm[p.C + c] = q ? prm[p.C + c] + ab[k][e] : ab[k][e];
-          }
-        }
-    __syncthreads();
-  }
   float* out = p.ws + (int64_t)blockIdx.x * 2 * p.C;
-  for (int c = threadIdx.x; c < 2 * p.C; c += kThreads) out[c] = prm[c];
+  for (int c = threadIdx.x; c < 2 * p.C; c += kThreads) {
+    const float* from = sums_g + (c < p.C ? c : N + c - p.C);
+    float v = from[0];
+#pragma unroll
+    for (int q = 1; q < ROWS; ++q) v += from[q * 2 * N];
+    out[c] = v;
+  }
 }
 
 // Partial sums of `count` CTAs: 32 warps share 32 columns, each a stretch of the
@@ -839,9 +853,13 @@ cudaError_t by_width(int C, F&& f) {
     if (C <= 64) EVO_N8(8, 1, 4);
     if (C <= 128) EVO_N8(16, 1, 4);
     if (C <= 256) EVO_N8(32, 1, 4);
-    if (THREE && C <= 384) EVO_N8(16, 3, 2);
+    if constexpr (THREE) {
+      if (C <= 384) EVO_N8(16, 3, 2);
+    }
     if (C <= 512) EVO_N8(32, 2, 2);
-    if (THREE && C <= 768) EVO_N8(32, 3, 2);
+    if constexpr (THREE) {
+      if (C <= 768) EVO_N8(32, 3, 2);
+    }
     if (C <= 1024) EVO_N8(64, 2, 2);
     if (C <= 2048) EVO_N8(128, 2, 2);
     EVO_N8(256, 2, 2);
@@ -898,11 +916,19 @@ cudaError_t run_bwd_as(const Norm8Call& c, cudaStream_t st) {
     const Params p = params_of(c, T);
     const cudaError_t e2 = by_flag(c.n[0] == 1 && c.n[1] == 1, [&](auto flat) {
       auto kern = k_norm8_bwd<S, IO, L, P, VEC, decltype(flat)::value, T>;
-      const size_t smem = VEC && Ring<S, IO, P, T>::USED ? Ring<S, IO, P, T>::BYTES : 0;
-      int fit = 0;
+      // the ring, and in the end the sums of gamma and beta of eight warps
+      constexpr size_t sums = (size_t)(L <= 32 ? kThreads / 32 : kThreads / L) * 2 * P * Lay<L, VEC>::SPAN * sizeof(float);
+      constexpr size_t smem = std::max<size_t>(VEC && Ring<S, IO, P, T>::USED ? Ring<S, IO, P, T>::BYTES : 0, sums);
       cudaError_t e3 = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e3 == cudaSuccess) e3 = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kThreads, smem);
       if (e3 != cudaSuccess) return e3;
+      // CTAs that an SM holds (asked once per device: a property of the kernel)
+      static std::atomic<int> held[64];
+      int fit = dev < 64 ? held[dev].load() : 0;
+      if (fit == 0) {
+        e3 = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kThreads, smem);
+        if (e3 != cudaSuccess) return e3;
+        if (dev < 64) held[dev].store(fit);
+      }
       const uint32_t want = (p.groups + per - 1) / per;
       const uint32_t most = std::min<uint32_t>(kNorm8MaxCtas, (uint32_t)std::max(1, fit * sms));
       const uint32_t turns = (want + most - 1) / most;
