@@ -588,6 +588,7 @@ typedef struct {
  *
  *  x, out : `stream_dtype`; u: `dtype`.  All four pairs of types.  out may be x
  *           or u itself (same address, strides and type).
+ * Supported: C <= 4096, B * I * J < 2^31 - 2^21 and B * I * J * ceil(C / 8) < 2^32.
  */
 typedef struct {
     evoattn_rows x, u, out;
@@ -660,6 +661,7 @@ evoattn_status evoattn_norm8_bwd(const evoattn_norm8_bwd_args* args, cudaStream_
  *            [ceil(R / 128), ceil(K / 128)]; scales_t is then NULL.
  *  Codes are 16-byte aligned with row strides that are multiples of 16
  *  (otherwise EVOATTN_ERR_ALIGNMENT); bytes behind a row's end are not written.
+ * Supported: fewer than 2^30 blocks of 128 x 128.
  */
 typedef struct {
     const void* x;
@@ -688,8 +690,11 @@ size_t evoattn_matmul8_workspace_size(int M, int N, int K);
  *  out    : [M, N], `dtype`, row stride ld_out.
  *  add    : `dtype`, row stride ld_add (0: one row for all), or NULL; may be out
  *           itself.  out overlaps no other operand.
- *  workspace : 256-byte aligned, at least evoattn_matmul8_workspace_size bytes;
- *           NULL where that is 0.
+ *  workspace : 256-byte aligned, at least evoattn_matmul8_workspace_size bytes
+ *           (NULL where that is 0), overwritten; not to be used by another call that
+ *           runs concurrently.
+ * A row's bytes behind K are not read.  Rows of out whose address, stride and width
+ * are multiples of 16 bytes are stored fastest.
  */
 typedef struct {
     const void* codes;

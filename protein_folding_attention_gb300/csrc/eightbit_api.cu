@@ -167,6 +167,7 @@ evoattn_status evoattn_dropout_add(const evoattn_dropout_add_args* args, cudaStr
   // (any pair of types: the sizes are checked as for two of the same)
   st = check_sizes(n[0], n[1], n[2], C, EVOATTN_F32, EVOATTN_F32, EVOATTN_NORM_LAYER, 1.f);
   if (st != EVOATTN_OK) return st;
+  if ((uint64_t)n[0] * n[1] * n[2] * (uint64_t)((C + 7) / 8) > 0xFFFFFFFFull) return EVOATTN_ERR_UNSUPPORTED;
   const int wide = bytes_of((evoattn_dtype)a.stream_dtype), narrow = bytes_of((evoattn_dtype)a.dtype);
   st = check_rows({rows4(a.x, wide, false), rows4(a.u, narrow, false), rows4(a.out, wide, true)}, n, C, nullptr);
   if (st != EVOATTN_OK) return st;

@@ -95,6 +95,7 @@ def test_row_operands(lib, call, out):
 def test_dropout_add_rejects(lib):
     assert dropout(lib, u=NONE) == I
     assert dropout(lib, out=NONE) == I
+    assert dropout(lib, shape=(1, 2 ** 12, 2 ** 11, 4096)) == U   # 2^32 parts of eight channels
     assert dropout(lib, sd=F32, x=rows(FAKE + 2)) == A
     assert dropout(lib, io=F32, u=rows(FAKE + 2)) == A
 
@@ -146,6 +147,7 @@ def test_quantize8_rejects(lib):
         assert quant(lib, **{k: 0}) == I and quant(lib, **{k: -5}) == I
     assert quant(lib, dt=2) == U
     assert quant(lib, R=2 ** 39, K=2 ** 39) == U
+    assert quant(lib, R=2 ** 22, K=2 ** 22) == U
     assert quant(lib, ld=-300) == I and quant(lib, ld=2 ** 60) == I
     assert quant(lib, q=(FAKE, 299)) == I and quant(lib, qt=(FAKE, 9)) == I
     assert quant(lib, q=(FAKE, 312)) == A and quant(lib, q=(FAKE + 8, 304)) == A

@@ -503,7 +503,7 @@ def test_matmul8_values_at_the_edges():
     assert torch.isnan(got[:, 5]).all() and int(torch.isnan(got).sum()) == 20
 
 
-@pytest.mark.parametrize("M, N, K", [(4, 300, 3000), (600, 200, 256), (64, 64, 20000)])
+@pytest.mark.parametrize("M, N, K", [(4, 300, 3000), (600, 200, 256), (64, 64, 20000), (2900, 1500, 1100)])
 def test_matmul8_same_bits_and_streams(M, N, K):
     """Repeated, on two streams at once with workspaces of their own, and captured."""
     qa, sa, a = operand(M, K, 11)
