@@ -298,6 +298,14 @@ __device__ __forceinline__ float2 pair(const float* f) { return make_float2(f[0]
 __device__ __forceinline__ void put_pair(float* f, float2 v) { f[0] = v.x; f[1] = v.y; }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// 1 / sqrt(v): the approximation with a Newton step, which leaves its own roundings
+// (an error of y decides whether a maximum near the border between two scales
+// takes the one or the other).  0 for an infinite v, as the approximation has it.
+__device__ __forceinline__ float inverse_root(float v) {
+  const float r = rsqrtf(v), e = fmaf(-v * r, r, 1.f);
+  return fabsf(e) < 1.f ? fmaf(0.5f * r, e, r) : r;
+}
+
 // Rows minus their mean (layer norm), and 1 / sqrt(variance + eps).
 template <int LANES, int PARTS, bool VEC, int T, int E>
 __device__ __forceinline__ void centre(const Params& p, int lane, float (&x)[T][PARTS][E], float (&rstd)[T],
@@ -338,7 +346,7 @@ __device__ __forceinline__ void centre(const Params& p, int lane, float (&x)[T][
   }
   row_sums<LANES, T>(rstd, buf, 1);
 #pragma unroll
-  for (int t = 0; t < T; ++t) rstd[t] = rsqrtf(rstd[t] * p.inv_c + p.eps);
+  for (int t = 0; t < T; ++t) rstd[t] = inverse_root(rstd[t] * p.inv_c + p.eps);
 }
 
 // ---------------------------------------------------------------------------
@@ -397,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout_add(const Params p, Divide
 // forward
 // ---------------------------------------------------------------------------
 template <typename S, typename IO, int LANES, int PARTS, bool VEC, bool FLAT, int T>
-__global__ void __launch_bounds__(kThreads, VEC && PARTS == 1 && sizeof(S) == 2 ? 4 : 3) k_norm8_fwd(const Params p, uint32_t turns) {
+__global__ void __launch_bounds__(kThreads, VEC && FLAT && PARTS == 1 && sizeof(S) == 2 ? 4 : 3) k_norm8_fwd(const Params p, uint32_t turns) {
   using L = Lay<LANES, VEC>;
   constexpr int E = L::E, PER = kThreads / LANES;
   __shared__ float sums[2][T][8];

@@ -99,8 +99,8 @@ struct Smem {
 template <typename T, bool VEC, bool COLS>
 __global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c, Divide tiles_k, uint32_t tiles) {
   using M = Smem<T, VEC, COLS>;
-  __shared__ float col_max[COLS ? kThreads / 32 : 1][kGroup8];
-  __shared__ float col_inv[kGroup8];
+  __shared__ __align__(16) float col_max[COLS ? kThreads / 32 : 1][kGroup8];
+  __shared__ __align__(16) float col_inv[kGroup8];
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* const tile = smem + (M::RING ? M::DEPTH * M::STAGE : 0);
   wait_for_earlier_work();
@@ -110,14 +110,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c
   const auto fill = [&](uint32_t t, int stage) {
     if (t < tiles) {
       const uint32_t tr = quotient(tiles_k, t), tk = t - tr * tiles_k.d;
-      const int64_t r = (int64_t)tr * kGroup8 + ty * kRows, k = (int64_t)tk * kGroup8 + tx * 8;
+      const int64_t r = (int64_t)tr * kGroup8, k = (int64_t)tk * kGroup8;
+      // rows and columns of the tile that there are (K is a multiple of 8)
+      const int rows = (int)min((int64_t)kGroup8, c.R - r) - ty * kRows, cols = (int)min((int64_t)kGroup8, c.K - k) - tx * 8;
       const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem) + stage * M::STAGE + threadIdx.x * 16;
+      const T* from = static_cast<const T*>(c.x) + (rows > 0 && cols > 0 ? (r + ty * kRows) * c.ld + k + tx * 8 : 0);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const bool on = r + i < c.R && k < c.K;  // (K is a multiple of 8)
-        const T* from = static_cast<const T*>(c.x) + (on ? (r + i) * c.ld + k : 0);
+        const bool on = i < rows && cols > 0;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * kThreads * 16), "l"(from),
                      "r"(on ? 16 : 0) : "memory");
+        if (i + 1 < rows) from += c.ld;  // (an address in the matrix, whether it is read or not)
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -130,10 +133,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c
 #pragma unroll 1
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x, ++step) {
     const uint32_t tr = quotient(tiles_k, t), tk = t - tr * tiles_k.d;
-    const int64_t r0 = (int64_t)tr * kGroup8 + ty * kRows;
-    const int64_t k0 = (int64_t)tk * kGroup8 + tx * 8;
-    const int nk = (int)min((int64_t)8, c.K - k0);      // this thread's columns (may be negative)
-    const int nr = (int)min((int64_t)kRows, c.R - r0);  // and rows
+    const int64_t tile_r = (int64_t)tr * kGroup8, tile_k = (int64_t)tk * kGroup8;
+    const int rows_left = (int)min((int64_t)kGroup8, c.R - tile_r), cols_left = (int)min((int64_t)kGroup8, c.K - tile_k);
+    const int64_t r0 = tile_r + ty * kRows, k0 = tile_k + tx * 8;
+    const int nk = min(8, cols_left - tx * 8);          // this thread's columns (may be negative)
+    const int nr = min(kRows, rows_left - ty * kRows);  // and rows
     float f[kRows][8];
     const T* x = static_cast<const T*>(c.x);
     if constexpr (M::RING) {
@@ -158,9 +162,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c
       T v[PER][4];
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int64_t r = (int64_t)tr * kGroup8 + warp * PER + i, k = (int64_t)tk * kGroup8 + lane;
+        const bool on = warp * PER + i < rows_left;
+        const T* from = x + (on ? (tile_r + warp * PER + i) * c.ld + tile_k + lane : 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[i][e] = r < c.R && k + 32 * e < c.K ? x[r * c.ld + k + 32 * e] : T(0.f);
+        for (int e = 0; e < 4; ++e) v[i][e] = on && lane + 32 * e < cols_left ? from[32 * e] : T(0.f);
       }
 #pragma unroll
       for (int i = 0; i < PER; ++i)
@@ -193,12 +198,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c
     float block = 0.f;
     if constexpr (COLS) {
       // column maxima: 4 rows of this thread, the other half of the warp, 16 warps
+      float m8[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float m = max_abs3(f[0][e], f[1][e], max_abs3(f[2][e], f[3][e], 0.f));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        if (lane < 16) col_max[warp][tx * 8 + e] = m;
+        m8[e] = max_abs3(f[0][e], f[1][e], max_abs3(f[2][e], f[3][e], 0.f));
+        m8[e] = fmaxf(m8[e], __shfl_xor_sync(0xffffffffu, m8[e], 16));
       }
+      // (each half of the warp stores half of a thread's columns)
+      const bool high = lane >= 16;
+      reinterpret_cast<float4*>(&col_max[warp][tx * 8])[high] =
+          make_float4(high ? m8[4] : m8[0], high ? m8[5] : m8[1], high ? m8[6] : m8[2], high ? m8[7] : m8[3]);
       __syncthreads();
       if (threadIdx.x < kGroup8) {
         float m = col_max[0][threadIdx.x];
@@ -207,8 +216,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c
         if (!c.blocks) {
           const uint32_t code = scale_code(m);
           m = scale_inverse(code);
-          const int64_t k = (int64_t)tk * kGroup8 + threadIdx.x;
-          if (k < c.K) c.scales_t[k * c.st_row + (int64_t)tr * c.st_group] = (uint8_t)code;
+          if ((int)threadIdx.x < cols_left)
+            c.scales_t[(tile_k + threadIdx.x) * c.st_row + (int64_t)tr * c.st_group] = (uint8_t)code;
         }
         col_inv[threadIdx.x] = m;
       }
@@ -225,8 +234,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c
       }
     }
     if (c.codes) {
+      uint8_t* to = c.codes + (nr > 0 && nk > 0 ? r0 * c.ldc + k0 : 0);
+      uint8_t* scale = c.scales + (nr > 0 ? (c.blocks ? 0 : r0 * c.s_row) + (int64_t)tk * c.s_group : 0);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
+      for (int i = 0; i < kRows; ++i, to += c.ldc, scale += c.s_row) {
         float inv = block;
         if (!COLS || !c.blocks) {
           float m = row[i];
@@ -234,38 +245,46 @@ __global__ void __launch_bounds__(kThreads, 2) k_quantize8(const Quantize8Call c
           for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           const uint32_t code = scale_code(m);
           inv = scale_inverse(code);
-          if (tx == 0 && i < nr) c.scales[(r0 + i) * c.s_row + (int64_t)tk * c.s_group] = (uint8_t)code;
+          if (tx == 0 && i < nr) *scale = (uint8_t)code;
         }
         if (i < nr && nk > 0)
-          put_codes(c.codes + (r0 + i) * c.ldc + k0,
+          put_codes(to,
                     make_uint2(e4m3_four(f[i][0], f[i][1], f[i][2], f[i][3], inv),
                                e4m3_four(f[i][4], f[i][5], f[i][6], f[i][7], inv)), nk);
       }
     }
     if (COLS && c.codes_t) {
       // (every thread is past its reads of the tile as it came: the barriers above)
+      const float4 lo = reinterpret_cast<const float4*>(col_inv)[2 * tx], hi = reinterpret_cast<const float4*>(col_inv)[2 * tx + 1];
+      const float inv[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      uint8_t* const at = tile + tx * 8 * kGroup8 + ((ty ^ 2 * tx) << 2);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int col = tx * 8 + e;
-        const float inv = c.blocks ? block : col_inv[col];
-        *reinterpret_cast<uint32_t*>(tile + col * kGroup8 + ((ty ^ 2 * tx) << 2)) =
-            e4m3_four(f[0][e], f[1][e], f[2][e], f[3][e], inv);
-      }
+      for (int e = 0; e < 8; ++e)
+        *reinterpret_cast<uint32_t*>(at + e * kGroup8) =
+            e4m3_four(f[0][e], f[1][e], f[2][e], f[3][e], c.blocks ? block : inv[e]);
       __syncthreads();
-      // eight threads write a column of the tile (128 bytes), 16 bytes each
+      // Eight threads write a column of the tile (128 bytes), 16 bytes each.  Odd
+      // columns read their two halves in the other order: a warp's four columns
+      // would otherwise be read from the same banks.
+      const int word = (threadIdx.x & 7) * 4, left = rows_left - word * 4;
 #pragma unroll
       for (int pass = 0; pass < 2; ++pass) {
-        const int col = pass * 64 + (threadIdx.x >> 3), word = (threadIdx.x & 7) * 4, turn = 2 * (col >> 3);
-        const int64_t k = (int64_t)tk * kGroup8 + col, r = (int64_t)tr * kGroup8 + word * 4;
-        const uint2 a = *reinterpret_cast<const uint2*>(tile + col * kGroup8 + ((word ^ turn) << 2));
-        const uint2 b = *reinterpret_cast<const uint2*>(tile + col * kGroup8 + (((word + 2) ^ turn) << 2));
-        if (k >= c.K) continue;
-        uint8_t* to = c.codes_t + k * c.ldt + r;
-        if (r + 16 <= c.R) {
+        const int col = pass * 64 + (threadIdx.x >> 3), turn = 2 * (col >> 3), odd = col & 1;
+        const uint8_t* from = tile + col * kGroup8;
+        uint2 a = *reinterpret_cast<const uint2*>(from + (((word + 2 * odd) ^ turn) << 2));
+        uint2 b = *reinterpret_cast<const uint2*>(from + (((word + 2 - 2 * odd) ^ turn) << 2));
+        if (odd) {
+          const uint2 v = a;
+          a = b;
+          b = v;
+        }
+        if (col >= cols_left || left <= 0) continue;
+        uint8_t* to = c.codes_t + (tile_k + col) * c.ldt + tile_r + word * 4;
+        if (left >= 16) {
           *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
-        } else if (r < c.R) {
-          put_codes(to, a, (int)min((int64_t)8, c.R - r));
-          if (r + 8 < c.R) put_codes(to + 8, b, (int)min((int64_t)8, c.R - r - 8));
+        } else {
+          put_codes(to, a, min(8, left));
+          if (left > 8) put_codes(to + 8, b, left - 8);
         }
       }
     }

@@ -851,6 +851,8 @@ def norm8_bwd(dx1, dy, x1, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0
     returned it; branch: whether the forward had u; the rest as in the forward.
     dx=dx1 works in place.  Returns a dict with dx, du (with `branch`; in dy's
     type), and fp32 dgamma and dbeta of the parameters that were given."""
+    if dy is None or x1 is None:
+        raise ValueError("dy and x1 are needed")
     shape = x1.shape
     if len(shape) != 4:
         raise ValueError("x1 must be [B, I, J, C]")
