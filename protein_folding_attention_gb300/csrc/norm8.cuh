@@ -545,25 +545,33 @@ __global__ void __launch_bounds__(kThreads, VEC && FLAT && PARTS == 1 && sizeof(
 // memory's latency with loads into registers (58 us for 147,456 bf16 rows of 128
 // where the bytes take 28).  Whole 16-byte units therefore come through a ring of
 // DEPTH turns in shared memory, filled by cp.async: a thread copies, and reads,
-// only its own units, so the ring needs no barrier.
+// only its own units, so the ring needs no barrier.  A thread's fp32 part is two
+// units, which its neighbours' lie between: they go through L1, which keeps the other
+// half of a 32-byte sector (195,330 rows of 72 with an fp32 stream 58 -> 51 us, past L1
+// 70).  Rows that are fp32 throughout are loaded into registers (108 us for 262,144
+// of 128, 91 % of the copy rate).
 template <typename S, typename IO, int PARTS, int T>
 struct Ring {
   static constexpr int UNITS_S = sizeof(S) / 2, UNITS_IO = sizeof(IO) / 2;  // of 16 bytes, for 8 elements
   static constexpr int UNITS = T * PARTS * (2 * UNITS_S + UNITS_IO);        // of a thread's turn: x1, dx1, dy
   static constexpr uint32_t STAGE = UNITS * kThreads * 16;
   static constexpr int DEPTH = std::min<int>(4, std::max<int>(2, (int)(80 * 1024 / STAGE)));
-  static constexpr bool USED = sizeof(S) == 2;
+  static constexpr bool USED = sizeof(IO) == 2;
   static constexpr uint32_t BYTES = DEPTH * STAGE;
 };
 // (a unit of which nothing is read is zero)
+template <bool WHOLE>
 __device__ __forceinline__ void copy_unit(uint32_t to, const void* from, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+  if constexpr (WHOLE)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
 }
 template <typename T>
 __device__ __forceinline__ void copy_part(uint32_t to, const void* base, int64_t at, int c, bool on) {
   const T* p = static_cast<const T*>(base) + (on ? at + c : 0);
 #pragma unroll
-  for (int u = 0; u < (int)sizeof(T) / 2; ++u) copy_unit(to + u * kThreads * 16, p + u * 16 / sizeof(T), on);
+  for (int u = 0; u < (int)sizeof(T) / 2; ++u) copy_unit<sizeof(T) == 2>(to + u * kThreads * 16, p + u * 16 / sizeof(T), on);
 }
 template <typename T>
 __device__ __forceinline__ void read_part(const uint4* from, Raw<T, true>& r) {
