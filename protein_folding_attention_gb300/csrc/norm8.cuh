@@ -19,9 +19,9 @@
 // - divisions by extents are multiplications, and operands whose rows lie evenly
 //   spaced (FLAT) need none;
 // - arithmetic goes over pairs of fp32.
-// Measured (device time; of the copy rate): forward, 589,824 bf16 rows of 128 97 us
-// with a mask shared along i (80 %), 82 without dropout (96 %); 196,608 rows of 384
-// 122 with a mask of their own and 85 without (64, 91 %); 262,144 fp32 rows of 128 72
+// Measured (device time; of the copy rate): forward, 589,824 bf16 rows of 128 98 us
+// with a mask shared along i (79 %), 82 without dropout (95 %); 196,608 rows of 384
+// 123 with a mask of their own and 87 without (63, 89 %); 262,144 fp32 rows of 128 72
 // (90 %).  Backward, 589,824 rows 132 (84 %), 147,456 rows of the ending node's views 41
 // (68 %: starting, draining and the second kernel are a third of it), fp32 108 (91 %).
 // Rows of odd widths are bound by their single-element accesses: 147,456 bf16 rows
