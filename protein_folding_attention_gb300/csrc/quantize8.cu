@@ -20,8 +20,8 @@
 // persistent CTAs while the tile before is worked on (a thread copies and reads
 // only its own units: no barrier): with loads into registers 48 % of the warps that
 // an SM can hold waited for them most of the time (102 us for 147,456 x 512 where
-// the bytes take 45; with the ring, and without
-// bank conflicts, 61, rows alone 67 -> 36).  fp32 tiles, twice the size, are loaded into registers.
+// the bytes take 45; with the ring, and without bank conflicts, 61; rows alone 67 ->
+// 36 where they take 33).  fp32 tiles, twice the size, are loaded into registers.
 // Rows that are no whole 16-byte units come through shared memory too: a warp
 // reads a row's elements 32 at a time.
 #include <cuda_bf16.h>
