@@ -93,8 +93,10 @@ struct Cfg {
   static constexpr uint32_t OFF_S = STAGES * STAGE;
   static constexpr uint32_t OFF_STAGING = OFF_S + RING_S * S_ENTRY;
   static constexpr uint32_t SMEM_ALLOC = OFF_STAGING + STAGING + 1024;
-  static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ;  // scales: 4 columns for each 128 rows
-  static_assert(COL_S + 12 <= 512 && SMEM_ALLOC <= 227 * 1024, "tensor memory, shared memory");
+  // scales: 4 columns for each 128 rows, twice, so that a bundle is not copied over
+  // one whose MMAs were issued just before it
+  static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ, COLS_S = PAIR ? 12 : 8;
+  static_assert(COL_S + 2 * COLS_S <= 512 && SMEM_ALLOC <= 227 * 1024, "tensor memory, shared memory");
   static_assert(PAIR == (BQ > 128), "more than 128 rows on the columns: scales of two blocks");
   static_assert(STAGE % 1024 == 0 && OFF_STAGING % 1024 == 0 && (!PAIR || Q_BYTES % 2048 == 0), "the swizzle repeats every 1024 bytes");
 };
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     const uint64_t dp0 = umma_desc(smem_u32(smem), 16, 1024, kSw128);
     const uint64_t dq0 = umma_desc(smem_u32(smem + C::P_BYTES), 16, 1024, kSw128);
     const uint64_t ds0 = umma_desc(smem_u32(smem + C::OFF_S), 16, 128, kSwNone);
-    const uint32_t sp = tmem + C::COL_S, sq = sp + 4;
+    uint32_t sp = tmem + C::COL_S, sq = sp + 4;
     bool ok = true;
     int it = 0, is = 0, n = 0;
     for (int item = first_item<C>(); item < p.items && ok; item += item_step<C>(), ++n) {
@@ -504,7 +506,11 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
       tc_fence_after();
       for (int g = w.g0; g < w.g1; ++g, ++it) {
         const int st = it % C::STAGES, j = (g - w.g0) % C::BUNDLE;
-        if (j == 0) ok = mbar_wait(&bar_scale[is % C::RING_S], (is / C::RING_S) & 1, wctx);
+        if (j == 0) {
+          ok = mbar_wait(&bar_scale[is % C::RING_S], (is / C::RING_S) & 1, wctx);
+          sp = tmem + C::COL_S + (is & 1) * C::COLS_S;
+          sq = sp + 4;
+        }
         ok = ok && mbar_wait(&bar_full[st], (it / C::STAGES) & 1, wctx);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;

@@ -576,8 +576,8 @@ def layer_step(x, u, gamma, beta, w, dout, state, p, shared):
     h = evoattn.matmul8(y8, ys, w8, ws)
     g8, gs, g8t, gst = evoattn.quantize8(dout, cols=True)
     dy = evoattn.matmul8(g8, gs, w8t, wst)
-    values = y8.float() * ys.view(torch.uint8).sub(127).view(torch.int8).float().exp2().repeat_interleave(128, -1)[..., :x.shape[-1]]
-    y8t, yst = evoattn.quantize8(values.reshape(-1, x.shape[-1]), rows=False, cols=True)
+    _, y = evoattn.block_norm(x1, gamma_pre=gamma, beta_pre=beta)  # y again, along the other axis
+    y8t, yst = evoattn.quantize8(y, rows=False, cols=True)
     dw = evoattn.matmul8(g8t, gst, y8t, yst, torch.float32)
     grads = evoattn.norm8_bwd(None, dy, x1, gamma, beta, p=p, rng=state, site=1, shared=shared)
     return x1, h, {**grads, "dw": dw}
@@ -587,9 +587,10 @@ def test_a_layer_as_it_is_used():
     """Against the formula in 64 bits: a relative error of the sums of the sizes
     that the roundings to e4m3 give.  A code is off by 2^-4 of itself at most,
     uniform within its step by 2^-4 / sqrt(3) at the bottom of a binade and half
-    that at its top: below 0.027 in the root mean square.  h has two factors
-    rounded, dw three roundings (y twice), the rest as many: at most
-    sqrt(3) * 0.027 = 0.047 where the errors do not cancel with the terms."""
+    that at its top: below 0.027 in the root mean square.  h and dw have two factors
+    rounded, the gradients behind the input's product three roundings at most:
+    sqrt(3) * 0.027 = 0.047 where the errors do not cancel with the terms; dgamma
+    multiplies by the norm's output, which x1's rounding to bf16 moves too."""
     g = gen(20)
     shape, N, p, shared = (1, 24, 40, 128), 192, 0.25, (1,)
     x, u = draw(shape, torch.bfloat16, g), draw(shape, torch.bfloat16, g)
