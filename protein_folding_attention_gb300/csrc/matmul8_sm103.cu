@@ -51,7 +51,7 @@
 // copy rate: the epilogue's latency; rows of 1032 bytes are stored 8 bytes at a
 // time), 147,456 x 1024 at K = 128 65 us (73 %), 8192 x 4096 x 4096 113 us (2440
 // TFLOP/s, bound by the operands' way through L2), 512 x 128 over 147,456 25 us,
-// one row times 4096 x 1536 5 us.
+// one row times 4096 x 1536 7 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -806,9 +806,11 @@ Matmul8Plan matmul8_plan(int M, int N, int K, int sms) {
   pl.splits = 1;
   pl.per_split = pl.groups;
   const int64_t count = (int64_t)pl.tiles_p * pl.tiles_q;
-  if (2 * count <= sms && pl.groups > 3) {
-    // pieces of the sum, two groups at least, for as many CTAs as there are SMs
-    // (one row times 4096 x 1536 in four pieces 5 us)
+  if (2 * count <= sms && pl.groups > 16) {
+    // Pieces of the sum, two groups at least, for as many CTAs as there are SMs.  The
+    // second launch costs 1 to 2 us of the device and 6 of the host, a group 0.3:
+    // 16 x 4096 x 4096 7.5 us in pieces and 13.7 whole, 30 x 500 x 3000 5.0 and 10.9, but
+    // 1 x 4096 x 1536 5.1 and 6.9 (a call 22 and 15), 4 x 1000 x 600 4.8 and 4.2.
     const int64_t most = std::min<int64_t>(sms / count, pl.groups / 2);
     pl.per_split = (int)((pl.groups + most - 1) / most);
     pl.splits = (pl.groups + pl.per_split - 1) / pl.per_split;

@@ -401,7 +401,7 @@ def check_product(got, a, b, add=None):
 
 SHAPES = [(1, 1, 1), (1, 128, 128), (1, 700, 300), (3, 5, 16), (16, 129, 127), (17, 100, 129), (31, 516, 128),
           (33, 64, 1000), (64, 200, 640), (65, 256, 250), (128, 128, 4096), (129, 130, 131), (300, 516, 128),
-          (513, 1, 300), (1000, 300, 72), (2, 3, 5000), (500, 8, 33), (300, 140, 256), (3000, 272, 700), (700, 257, 1024)]
+          (513, 1, 300), (1000, 300, 72), (2, 3, 5000), (500, 8, 33), (300, 140, 256), (3000, 272, 700), (700, 257, 1024), (20, 300, 2100), (90, 260, 2176), (5, 40, 2048)]
 
 
 @pytest.mark.parametrize("M, N, K", SHAPES)
