@@ -843,6 +843,11 @@ def norm8(x, u=None, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0.0, rn
     return x1, codes, scales
 
 
+@functools.lru_cache(maxsize=4096)
+def _norm8_bwd_workspace(C):
+    return load().evoattn_norm8_bwd_workspace_size(C)
+
+
 def norm8_bwd(dx1, dy, x1, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0.0, rng=None, site=0,
               shared=(), branch=True, dx=None, workspace=None, stream=None):
     """Gradients of norm8, the rounding of y passed through (see
@@ -860,16 +865,23 @@ def norm8_bwd(dx1, dy, x1, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0
     drop = _dropout(p, rng, site, shared, dev)
     words, out = [], {}
     _add_rows(words, ((dx1, sd, "dx1"), (dy, io, "dy"), (x1, sd, "x1")), shape, dev)
-    lib = load()
     with _allocate_on(stream):
         if dx is None:
             dx = torch.empty_like(x1)
+            words.append(dx.data_ptr())
+            words += dx.stride()
+        else:
+            _add_rows(words, ((dx, sd, "dx"),), shape, dev)
         out["dx"] = dx
         if branch:
-            out["du"] = torch.empty_like(dy)
-        _add_rows(words, ((dx, sd, "dx"), (out.get("du"), io, "du")), shape, dev)
+            out["du"] = du = torch.empty_like(dy)
+            words.append(du.data_ptr())
+            words += du.stride()
+        else:
+            words += _NO_ROWS
         _add_vectors(words, ((gamma, "gamma"),), C, dev)
-        _add_vectors([], ((beta, "beta"),), C, dev)
+        if beta is not None:
+            _add_vectors([], ((beta, "beta"),), C, dev)
         for name, t in (("dgamma", gamma), ("dbeta", beta)):
             if t is None:
                 words.append(0)
@@ -877,12 +889,12 @@ def norm8_bwd(dx1, dy, x1, gamma=None, beta=None, kind=NORM_LAYER, eps=1e-5, p=0
                 out[name] = t = torch.empty_like(t)
                 words.append(t.data_ptr())
         if workspace is None:
-            workspace = torch.empty(lib.evoattn_norm8_bwd_workspace_size(C), device=x1.device, dtype=torch.uint8)
+            workspace = torch.empty_strided((_norm8_bwd_workspace(C),), (1,), device=x1.device, dtype=torch.uint8)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
     if stream is not None:
         _used_on(stream, (dx1, dy, x1, gamma, dx, workspace, rng if p else None))
-    st = lib.evoattn_norm8_bwd(
+    st = load().evoattn_norm8_bwd(
         _PACK_NORM8_BWD(*words, *drop, eps, *shape, _dtype_code(x1), F32 if io is torch.float32 else BF16,
                         kind, workspace.data_ptr(), workspace.numel() * workspace.element_size()),
         _raw_stream(stream, dev))

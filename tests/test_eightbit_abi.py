@@ -212,9 +212,12 @@ def told(monkeypatch):
     monkeypatch.setattr(evoattn, "_on_device", lambda t: t.get_device())
     monkeypatch.setattr(evoattn, "_raw_stream", lambda st, index: 0)
     monkeypatch.setattr(evoattn, "_allocate_on", lambda st: contextlib.nullcontext())
-    evoattn._matmul8_workspace.cache_clear()
+    caches = evoattn._matmul8_workspace, evoattn._norm8_bwd_workspace
+    for c in caches:
+        c.cache_clear()
     yield told
-    evoattn._matmul8_workspace.cache_clear()
+    for c in caches:
+        c.cache_clear()
 
 
 def addresses(*ts):
