@@ -198,6 +198,21 @@ def test_quantize8(R, K, dtype, blocks, how):
         assert torch.equal(bits(a), bits(b))
 
 
+@pytest.mark.parametrize("R, K", [(5000, 2000), (39000, 130), (130, 39000)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize8_more_tiles_than_places(R, K, dtype):
+    x = torch.randn(R, K, generator=gen(4)).to(dtype)
+    x[R // 2, K - 1], x[R - 1, 0] = float("inf"), float("nan")
+    for blocks in (False, True):
+        q, s, qt, st = evoattn.quantize8(x.to(DEV), cols=True, blocks=blocks)
+        want, k = eb.quantise_blocks(x) if blocks else eb.quantise(x)
+        same_codes(q, want)
+        same_scales(s, k)
+        want, k = (want.t(), k.t()) if blocks else eb.quantise(x.t())
+        same_codes(qt, want)
+        same_scales(st, k)
+
+
 def test_quantize8_values_at_the_edges():
     x = torch.zeros(16, 256)
     x[0, 0], x[0, 1] = 448.0, 2.0 ** -10                    # 2^-10 is a tie with zero
@@ -297,6 +312,27 @@ def test_norm8(shape, how, shared, types, kind, branch):
     check_codes(codes, scales, y, 64 * U * (1 + k) * terms)
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 8000, 1032), (1, 1, 8000, 1030), (1, 1, 4200, 4096), (1, 70, 300, 128)])
+@pytest.mark.parametrize("types", list(TYPES))
+def test_norm8_many_rows(shape, types):
+    """More rows than the kernel has places for: a sample of them."""
+    res, io = TYPES[types]
+    g = gen(12)
+    x, u = draw(shape, res, g), draw(shape, io, g)
+    gamma, beta = params(shape[-1], g, evoattn.NORM_LAYER)
+    got, codes, scales = evoattn.norm8(x.to(DEV), u.to(DEV), gamma.to(DEV), beta.to(DEV))
+    n = shape[1] * shape[2]
+    rows = torch.cat([torch.arange(0, n, 41), torch.arange(n - 40, n)])
+    pick = lambda t: t.reshape(1, 1, n, -1)[:, :, rows.to(t.device)]
+    x1, y = eb.norm8(pick(x), pick(u), gamma, beta)
+    stored(pick(got), x1, 4 * U * (d(pick(x)).abs() + d(pick(u)).abs()), "x1")
+    h, r = eb.normalise(x1, False, 1e-5)
+    k = x1.abs().amax(-1, keepdim=True) * r
+    terms = (h * gamma.double()).abs().amax(-1, keepdim=True) + d(beta).abs().max()
+    check_codes(pick(codes.view(torch.uint8)).view(torch.float8_e4m3fn),
+                pick(scales.view(torch.uint8)).contiguous().view(torch.float8_e8m0fnu), y, 64 * U * (1 + k) * terms)
+
+
 def test_norm8_without_parameters_and_in_place():
     g = gen(6)
     x, u = draw((1, 4, 5, 128), torch.float32, g), draw((1, 4, 5, 128), torch.bfloat16, g)
@@ -356,22 +392,30 @@ def test_norm8_bwd(shape, how, shared, types, kind, branch):
         near(got["dbeta"], want["dbeta"], 512 * U * d(dy).abs().sum(rows), "dbeta")
 
 
-def test_norm8_bwd_many_rows_in_place_and_again():
+@pytest.mark.parametrize("shape", [(1, 130, 150, 128), (1, 100, 130, 131), (1, 40, 60, 1032), (1, 30, 30, 4093)])
+@pytest.mark.parametrize("types", list(TYPES))
+def test_norm8_bwd_many_rows_in_place_and_again(shape, types):
     """More rows than the kernel has places for; the same bits every time."""
-    shape = (1, 130, 150, 128)
+    res, io = TYPES[types]
     g = gen(8)
-    dx1, dy, x1 = (draw(shape, torch.bfloat16, g) for _ in range(3))
-    gamma, beta = params(128, g, evoattn.NORM_LAYER)
+    dx1, dy, x1 = draw(shape, res, g), draw(shape, io, g), draw(shape, res, g)
+    gamma, beta = params(shape[-1], g, evoattn.NORM_LAYER)
     want = eb.norm8_bwd(dx1, dy, x1, gamma)
     args = dy.to(DEV), x1.to(DEV), gamma.to(DEV), beta.to(DEV)
-    ws = torch.full((evoattn.load().evoattn_norm8_bwd_workspace_size(128),), 255, dtype=torch.uint8, device=DEV)
+    ws = torch.full((evoattn.load().evoattn_norm8_bwd_workspace_size(shape[-1]),), 255, dtype=torch.uint8, device=DEV)
     a = evoattn.norm8_bwd(dx1.to(DEV), *args)
     dd = dx1.to(DEV)
     b = evoattn.norm8_bwd(dd, *args, dx=dd, workspace=ws)
     assert b["dx"] is dd
     for n in a:
         assert torch.equal(a[n], b[n]), n
-    h, _ = eb.normalise(d(x1), False, 1e-5)
+    h, r = eb.normalise(d(x1), False, 1e-5)
+    k = d(x1).abs().amax(-1, keepdim=True) * r
+    e = (d(dy) * gamma.double()).abs()
+    terms = r * (e + h.abs() * (e * h.abs()).mean(-1, keepdim=True) + e.mean(-1, keepdim=True)) + d(dx1).abs()
+    err = 128 * U * (1 + k) * terms.amax(-1, keepdim=True)
+    stored(a["dx"], want["dx"], err, "dx")
+    stored(a["du"], want["dx"], err, "du")
     for n, t in (("dgamma", d(dy) * h), ("dbeta", d(dy))):
         near(a[n], want[n], 1024 * U * t.abs().sum((0, 1, 2)), n)
 
