@@ -93,10 +93,13 @@ struct Cfg {
   static constexpr uint32_t OFF_S = STAGES * STAGE;
   static constexpr uint32_t OFF_STAGING = OFF_S + RING_S * S_ENTRY;
   static constexpr uint32_t SMEM_ALLOC = OFF_STAGING + STAGING + 1024;
-  // scales: 4 columns for each 128 rows, twice, so that a bundle is not copied over
-  // one whose MMAs were issued just before it
+  // scales: 4 columns for each 128 rows, in as many places as there is room for, so that a
+  // bundle is copied while the MMAs of those before it run (four instead of two: 1 % at
+  // 36,864 x 1536, K = 384)
   static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ, COLS_S = PAIR ? 12 : 8;
-  static_assert(COL_S + 2 * COLS_S <= 512 && SMEM_ALLOC <= 227 * 1024, "tensor memory, shared memory");
+  static constexpr int PLACES = PAIR ? 2 : 4;
+  static_assert(PLACES <= RING_S && (RING_S & (RING_S - 1)) == 0, "the copy that a place waits for is in the ring");
+  static_assert(COL_S + PLACES * COLS_S <= 512 && SMEM_ALLOC <= 227 * 1024, "tensor memory, shared memory");
   static_assert(PAIR == (BQ > 128), "more than 128 rows on the columns: scales of two blocks");
   static_assert(STAGE % 1024 == 0 && OFF_STAGING % 1024 == 0 && (!PAIR || Q_BYTES % 2048 == 0), "the swizzle repeats every 1024 bytes");
 };
@@ -507,8 +510,18 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
       for (int g = w.g0; g < w.g1; ++g, ++it) {
         const int st = it % C::STAGES, j = (g - w.g0) % C::BUNDLE;
         if (j == 0) {
+          // The copy below goes over the scales of bundle is - PLACES, which its MMAs read.
+          // Nothing orders a copy behind MMAs that were issued before it, but the commit
+          // behind the next bundle's copy does: those MMAs precede it.  (Looked at before
+          // the others, whose latency hides its own: waited for behind them, 589,824 x 516
+          // at K = 128 took 152 us.)
+          constexpr int NEXT = C::PLACES - 1;
+          uint64_t* const read = &bar_copied[(is - NEXT) & (C::RING_S - 1)];
+          const uint32_t turn = ((is - NEXT) / C::RING_S) & 1;
+          const bool free = is <= NEXT || mbar_test(read, turn);
           ok = mbar_wait(&bar_scale[is % C::RING_S], (is / C::RING_S) & 1, wctx);
-          sp = tmem + C::COL_S + (is & 1) * C::COLS_S;
+          if (!free) ok = ok && mbar_wait(read, turn, wctx);
+          sp = tmem + C::COL_S + (is % C::PLACES) * C::COLS_S;
           sq = sp + 4;
         }
         ok = ok && mbar_wait(&bar_full[st], (it / C::STAGES) & 1, wctx);
