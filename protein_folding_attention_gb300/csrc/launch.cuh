@@ -29,40 +29,4 @@ cudaError_t launch_early(K kernel, unsigned grid, unsigned threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The same in clusters of two CTAs.
-template <typename K, typename... A>
-cudaError_t launch_early_pairs(K kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
-                               const A&... args) {
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// Clusters of two CTAs that the current device holds at once.
-template <typename K>
-cudaError_t max_pairs(int* clusters, K kernel, unsigned threads, size_t smem) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
-}
-
 }  // namespace evo

@@ -34,7 +34,6 @@ struct Matmul8Call {
 // other; the sum over K in `splits` pieces of per_split groups.
 struct Matmul8Plan {
   bool staged;            // a's rows are the 128, else b's
-  bool pair;              // two CTAs share a tile of b: tiles_p counts pairs
   int bq, tiles_p, tiles_q, groups, per_split, splits;
 };
 Matmul8Plan matmul8_plan(int M, int N, int K, int sms);

@@ -20,12 +20,10 @@
 // down to 16) and b, the larger operand then, streams through the 128-row side;
 // a warp stores 32 consecutive columns of a row.
 //
-// With long sums over many rows the operands' way through L2 bounds the product
-// (128 x 128 tiles: 12.6 TB/s of it at 43 % of the tensor cores' rate).  There two
-// neighbouring CTAs, a cluster, take tiles of 128 x 192 or 240 with the same rows of
-// b: each loads half of those and multicasts it to both, so that a step of 480 MMA
-// cycles reads 31 KB instead of 32 KB for 256.  (240 and not 256: two
-// accumulators and the scales share the 512 columns of tensor memory.)
+// With long sums over many rows a wider tile of b pays (192 or 240 columns): a step of
+// 128 k reads 46 KB for 128 x 240 products where 128 x 128 take 32, and each MMA
+// instruction reads a's rows for more columns.  (240 and not 256: two accumulators and
+// the scales share the 512 columns of tensor memory.)
 //
 // Long sums with few tiles are cut into pieces along k, one per CTA, which leave
 // fp32 partial sums [piece][m][n], with b's rows on the lanes too; a second kernel
@@ -44,20 +42,17 @@
 //          short sums (up to 1024 k) each of the two has eight warps of its own
 //          (147,456 x 128 outputs with an addend 50 -> 35 us, x 512 in fp32 64 -> 56)
 //
-// The two CTAs of a cluster meet twice, before the first load and after the last:
-// both always get there, since every other wait is bounded.
-//
-// What it measures (device time): 589,824 x 516 at K = 128 145 us (69 % of the
+// What it measures (device time): 589,824 x 516 at K = 128 146 us (69 % of the
 // copy rate: the epilogue's latency; rows of 1032 bytes are stored 8 bytes at a
-// time), 147,456 x 1024 at K = 128 65 us (73 %), 8192 x 4096 x 4096 113 us (2440
-// TFLOP/s, bound by the operands' way through L2), 512 x 128 over 147,456 25 us,
+// time), 147,456 x 1024 at K = 128 65 us (72 %), 8192 x 4096 x 4096 117 us (2360
+// TFLOP/s: 8 rounds of tiles of which 7.6 are needed, 32 steps of 0.46 us in each,
+// the eighteenth tile of a row with 16 of 240 columns), 512 x 128 over 147,456 25 us,
 // one row times 4096 x 1536 7 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "common.cuh"
 #include "divide.cuh"
@@ -74,20 +69,19 @@ constexpr int kGroup = 128;  // elements along k of a stage, and of a scale
 enum Mode { kStaged, kDirect, kPartial };  // a on the lanes; b on the lanes; that, and a piece of the sum
 
 // BQ: rows of the operand on the columns.  SETS: groups of eight epilogue warps.
-// PAIR: clusters of two CTAs with the same rows of the operand on the columns.
-template <int BQ_, Mode MODE, int SETS, bool PAIR_>
+template <int BQ_, Mode MODE, int SETS>
 struct Cfg {
   static constexpr int BQ = BQ_;
-  static constexpr bool PAIR = PAIR_;
+  static constexpr bool WIDE = BQ > 128;  // scales of two blocks of 128 rows on the columns
   static constexpr int THREADS = 128 + SETS * 256;
   static constexpr uint32_t P_BYTES = kLanes * kGroup, Q_BYTES = BQ * kGroup;
   static constexpr uint32_t S_BYTES = 512;  // scales of up to 128 rows, four groups
-  static constexpr uint32_t S_ENTRY = (PAIR ? 3 : 2) * S_BYTES;  // of p's rows, then q's
+  static constexpr uint32_t S_ENTRY = (WIDE ? 3 : 2) * S_BYTES;  // of p's rows, then q's
   static constexpr uint32_t STAGE = P_BYTES + Q_BYTES;
   // Scales: groups whose bytes go to tensor memory together (four fill a word;
   // fewer where 640 threads leave 96 registers, which bytes that are underway have
   // to fit: spilled, they are waited for), and such bundles requested ahead.
-  static constexpr int BUNDLE = SETS == 1 ? 4 : 2, AHEAD = PAIR ? 2 : 3, RING_S = 4;
+  static constexpr int BUNDLE = SETS == 1 ? 4 : 2, AHEAD = WIDE ? 2 : 3, RING_S = 4;
   static constexpr uint32_t STAGING = MODE == kStaged ? SETS * 8 * 4096 : 0;
   static constexpr int STAGES = std::min<int>(8, (int)((224 * 1024 - STAGING - RING_S * S_ENTRY) / STAGE));
   static constexpr uint32_t OFF_S = STAGES * STAGE;
@@ -96,12 +90,11 @@ struct Cfg {
   // scales: 4 columns for each 128 rows, in as many places as there is room for, so that a
   // bundle is copied while the MMAs of those before it run (four instead of two: 1 % at
   // 36,864 x 1536, K = 384)
-  static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ, COLS_S = PAIR ? 12 : 8;
-  static constexpr int PLACES = PAIR ? 2 : 4;
+  static constexpr uint32_t COL_S = 2 * BQ < 32 ? 32 : 2 * BQ, COLS_S = WIDE ? 12 : 8;
+  static constexpr int PLACES = WIDE ? 2 : 4;
   static_assert(PLACES <= RING_S && (RING_S & (RING_S - 1)) == 0, "the copy that a place waits for is in the ring");
   static_assert(COL_S + PLACES * COLS_S <= 512 && SMEM_ALLOC <= 227 * 1024, "tensor memory, shared memory");
-  static_assert(PAIR == (BQ > 128), "more than 128 rows on the columns: scales of two blocks");
-  static_assert(STAGE % 1024 == 0 && OFF_STAGING % 1024 == 0 && (!PAIR || Q_BYTES % 2048 == 0), "the swizzle repeats every 1024 bytes");
+  static_assert(STAGE % 1024 == 0 && OFF_STAGING % 1024 == 0, "the swizzle repeats every 1024 bytes");
 };
 
 struct Params8 {
@@ -140,41 +133,17 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) 
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// Clusters of two: barriers of both CTAs, loads and commits that reach both.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
 // Where an item of work lies.
 struct Item {
   int p0, q0, g0, g1, split;
 };
-template <typename C>
-__device__ __forceinline__ int first_item() { return C::PAIR ? blockIdx.x >> 1 : blockIdx.x; }
-template <typename C>
-__device__ __forceinline__ int item_step() { return C::PAIR ? gridDim.x >> 1 : gridDim.x; }
 template <typename C>
 __device__ __forceinline__ Item item_of(const Params8& p, int item) {
   Item w;
   const int t = (int)quotient(p.inner, item), i = item - t * (int)p.inner.d;
   w.split = (int)quotient(p.outer, t);
   const int o = t - w.split * (int)p.outer.d;
-  // (an item of a pair is two neighbouring tiles of p)
-  w.p0 = (C::PAIR ? 2 * o + (int)(blockIdx.x & 1) : p.fast_q ? o : i) * kLanes;
+  w.p0 = (p.fast_q ? o : i) * kLanes;
   w.q0 = (p.fast_q ? i : o) * C::BQ;
   w.g0 = w.split * p.per_split;
   w.g1 = min(p.groups, w.g0 + p.per_split);
@@ -199,7 +168,7 @@ __device__ __forceinline__ void scale_role(const Params8& p, bool of_q, uint8_t*
     for (int i = 0; i < RL; ++i)
 #pragma unroll
       for (int j = 0; j < C::BUNDLE; ++j) s[k][i][j] = 0;  // (bytes of groups that there are not are not read)
-  int item = first_item<C>(), g = 0, g1 = 0;  // the bundle that is requested next
+  int item = (int)blockIdx.x, g = 0, g1 = 0;  // the bundle that is requested next
   const uint8_t* at[RL];  // where the rows' bytes lie; NULL for rows that there are not, whose scale is 1
   const auto enter = [&] {
     if (item >= p.items) return;
@@ -226,16 +195,16 @@ __device__ __forceinline__ void scale_role(const Params8& p, bool of_q, uint8_t*
     }
     g += C::BUNDLE;
     if (g >= g1) {
-      item += item_step<C>();
+      item += (int)gridDim.x;
       enter();
     }
   };
   int left = 0;  // bundles of this CTA
   if (p.per_split >= p.groups) {  // (every item has all groups)
-    left = (p.items - 1 - first_item<C>() + item_step<C>()) / item_step<C>() *
+    left = (p.items - 1 - (int)blockIdx.x + (int)gridDim.x) / (int)gridDim.x *
            ((p.groups + C::BUNDLE - 1) / C::BUNDLE);
   } else {
-    for (int i = first_item<C>(); i < p.items; i += item_step<C>()) {
+    for (int i = (int)blockIdx.x; i < p.items; i += (int)gridDim.x) {
       const Item v = item_of<C>(p, i);
       left += (v.g1 - v.g0 + C::BUNDLE - 1) / C::BUNDLE;
     }
@@ -410,10 +379,10 @@ __device__ __forceinline__ void stage_row(uint32_t stg, const uint32_t (&lo)[32]
   }
 }
 
-template <typename T, int BQ, Mode MODE, int SETS, bool PAIR>
+template <typename T, int BQ, Mode MODE, int SETS>
 __global__ void __launch_bounds__(128 + SETS * 256, 1)
     k_matmul8(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q, const Params8 p) {
-  using C = Cfg<BQ, MODE, SETS, PAIR>;
+  using C = Cfg<BQ, MODE, SETS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -427,7 +396,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     abort_flag = 0;
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&bar_full[i], 1);   // codes
-      mbar_init(&bar_empty[i], C::PAIR ? 2 : 1);  // the stage's MMAs have read it (both CTAs')
+      mbar_init(&bar_empty[i], 1);  // the stage's MMAs have read it
     }
     for (int i = 0; i < C::RING_S; ++i) {
       mbar_init(&bar_scale[i], 2);   // scales of both operands
@@ -446,7 +415,6 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (C::PAIR) cluster_sync();  // both CTAs' barriers are there
   const uint32_t tmem = tmem_slot;
   volatile int* abort_p = &abort_flag;
   const WaitCtx wctx{abort_p, p.wc};
@@ -457,7 +425,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     // ============================ codes ====================================
     bool ok = true;
     int it = 0;
-    for (int item = first_item<C>(); item < p.items && ok; item += item_step<C>()) {
+    for (int item = (int)blockIdx.x; item < p.items && ok; item += (int)gridDim.x) {
       const Item w = item_of<C>(p, item);
       for (int g = w.g0; g < w.g1; ++g, ++it) {
         const int st = it % C::STAGES;
@@ -467,27 +435,15 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar_full[st], C::STAGE);
           tma_load_2d(smem + st * C::STAGE, &tm_p, &bar_full[st], g * kGroup, w.p0);
-          uint8_t* q = smem + st * C::STAGE + C::P_BYTES;
-          if constexpr (C::PAIR) {  // this CTA's half, for both
-            const int h = blockIdx.x & 1;
-            tma_load_2d_both(q + h * (C::Q_BYTES / 2), &tm_q, &bar_full[st], g * kGroup, w.q0 + h * (C::BQ / 2));
-          } else {
-            tma_load_2d(q, &tm_q, &bar_full[st], g * kGroup, w.q0);
-          }
+          tma_load_2d(smem + st * C::STAGE + C::P_BYTES, &tm_q, &bar_full[st], g * kGroup, w.q0);
         }
         __syncwarp();
       }
     }
     if (lane == 0) {
       volatile int no_abort = 0;
-      if constexpr (C::PAIR) {
-        // the other CTA's arrivals for the last stages land before this one may exit
-        for (int i = max(0, it - C::STAGES); i < it && ok; ++i)
-          ok = mbar_wait(&bar_empty[i % C::STAGES], (i / C::STAGES) & 1, wctx);
-      } else {  // every copy lands before the CTA may exit
-        for (int i = max(0, it - C::STAGES); i < it; ++i)
-          mbar_wait(&bar_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort);
-      }
+      for (int i = max(0, it - C::STAGES); i < it; ++i)  // every copy lands before the CTA may exit
+        mbar_wait(&bar_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -499,7 +455,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     uint32_t sp = tmem + C::COL_S, sq = sp + 4;
     bool ok = true;
     int it = 0, is = 0, n = 0;
-    for (int item = first_item<C>(); item < p.items && ok; item += item_step<C>(), ++n) {
+    for (int item = (int)blockIdx.x; item < p.items && ok; item += (int)gridDim.x, ++n) {
       const Item w = item_of<C>(p, item);
       const int buf = n & 1;
       if (n >= 2) {
@@ -534,17 +490,14 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
             const uint64_t ds = ds0 + ((uint32_t)((is % C::RING_S) * C::S_ENTRY) >> 4);
             tmem_copy_scales(sp, ds);
             tmem_copy_scales(sq, ds + (C::S_BYTES >> 4));
-            if constexpr (C::PAIR) tmem_copy_scales(sq + 4, ds + (2 * C::S_BYTES >> 4));
+            if constexpr (C::WIDE) tmem_copy_scales(sq + 4, ds + (2 * C::S_BYTES >> 4));
             umma_commit(&bar_copied[is % C::RING_S]);
           }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_mxf8(tmem + buf * BQ, dp + 2 * kk, dq + 2 * kk, id | (uint32_t)j << 4 | (uint32_t)j << 29, sp, sq,
                       g > w.g0 || kk > 0 ? 1u : 0u);
-          if constexpr (C::PAIR)
-            umma_commit_both(&bar_empty[st]);
-          else
-            umma_commit(&bar_empty[st]);
+          umma_commit(&bar_empty[st]);
           if (g + 1 == w.g1) umma_commit(&bar_done[buf]);
         }
         __syncwarp();
@@ -561,7 +514,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
   } else if (warp < 4) {
     // ============================ scales ===================================
     uint8_t* ring = smem + C::OFF_S;
-    if constexpr (C::PAIR) {
+    if constexpr (C::WIDE) {
       if (warp == 3)
         scale_role<C, 8>(p, true, ring, bar_scale, bar_copied, wctx);
       else
@@ -575,7 +528,7 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     bool ok = true;
     if (p.wc.stall) ok = __all_sync(0xffffffffu, stall_wait(&bar_never, wctx));
     int n = 0;
-    for (int item = first_item<C>(); item < p.items && ok; item += item_step<C>(), ++n) {
+    for (int item = (int)blockIdx.x; item < p.items && ok; item += (int)gridDim.x, ++n) {
       const int buf = n & 1;
       if (SETS == 2 && buf != set) continue;  // the other set's
       const Item w = item_of<C>(p, item);
@@ -662,16 +615,6 @@ __global__ void __launch_bounds__(128 + SETS * 256, 1)
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0) report_abort(abort_p, p.wc);
-  if constexpr (C::PAIR) {
-    __syncwarp();
-    cluster_sync();  // nothing is issued to the other CTA after this
-    // After a give-up the two may have stopped at different steps, whose copies no
-    // barrier can tell the end of: they are given 0.2 ms to land.
-    if (*abort_p || launch_aborted(p.wc)) {
-      const unsigned long long t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 200000ull) {}
-    }
-  }
 }
 
 // Adds the pieces of the sums: the eight warps of a CTA share 32 times V outputs,
@@ -727,16 +670,16 @@ int unit_of(const void* p, int64_t stride, int64_t width) {
   return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
 }
 
-template <typename T, int BQ, Mode MODE, int SETS = 1, bool PAIR = false>
+template <typename T, int BQ, Mode MODE, int SETS = 1>
 cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  using C = Cfg<BQ, MODE, SETS, PAIR>;
+  using C = Cfg<BQ, MODE, SETS>;
   Params8 p{};
   p.p = MODE == kStaged ? c.a : c.b;
   p.q = MODE == kStaged ? c.b : c.a;
   p.P = MODE == kStaged ? c.M : c.N;
   p.Q = MODE == kStaged ? c.N : c.M;
   CUtensorMap tp, tq;
-  if (!make_tmap_codes(&tp, p.p, p.P, c.K, kLanes) || !make_tmap_codes(&tq, p.q, p.Q, c.K, C::PAIR ? BQ / 2 : BQ)) {
+  if (!make_tmap_codes(&tp, p.p, p.P, c.K, kLanes) || !make_tmap_codes(&tq, p.q, p.Q, c.K, BQ)) {
     *tmap_ok = false;
     return cudaErrorInvalidValue;
   }
@@ -753,26 +696,10 @@ cudaError_t launch(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStr
   p.unit_add = unit_of(c.add, c.ld_add * size, c.N * size);
   p.ws = c.ws;
   p.wc = launch_wait(c.wait);
-  auto kern = k_matmul8<T, BQ, MODE, SETS, PAIR>;
+  auto kern = k_matmul8<T, BQ, MODE, SETS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
-  if constexpr (C::PAIR) {
-    // as many clusters as the device can hold at once (asked once per device)
-    static std::atomic<int> most[64];
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    int clusters = dev < 64 ? most[dev].load() : 0;
-    if (clusters == 0) {
-      e = max_pairs(&clusters, kern, C::THREADS, C::SMEM_ALLOC);
-      if (e != cudaSuccess) return e;
-      if (clusters < 1) return cudaErrorInvalidConfiguration;
-      if (dev < 64) most[dev].store(clusters);
-    }
-    return launch_early_pairs(kern, 2u * (unsigned)std::min(p.items, clusters), C::THREADS, C::SMEM_ALLOC, st, tp, tq, p);
-  } else {
-    return launch_early(kern, (unsigned)std::min(p.items, sms), C::THREADS, C::SMEM_ALLOC, st, tp, tq, p);
-  }
+  return launch_early(kern, (unsigned)std::min(p.items, sms), C::THREADS, C::SMEM_ALLOC, st, tp, tq, p);
 }
 
 template <typename T>
@@ -789,10 +716,10 @@ cudaError_t launch_sum(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cud
                                                        : go(std::integral_constant<int, 1>{});
 }
 
-template <int BQ, int SETS, bool PAIR>
+template <int BQ, int SETS>
 cudaError_t staged(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  return c.f32 ? launch<float, BQ, kStaged, SETS, PAIR>(c, pl, sms, st, tmap_ok)
-               : launch<__nv_bfloat16, BQ, kStaged, SETS, PAIR>(c, pl, sms, st, tmap_ok);
+  return c.f32 ? launch<float, BQ, kStaged, SETS>(c, pl, sms, st, tmap_ok)
+               : launch<__nv_bfloat16, BQ, kStaged, SETS>(c, pl, sms, st, tmap_ok);
 }
 
 template <int BQ>
@@ -831,16 +758,20 @@ Matmul8Plan matmul8_plan(int M, int N, int K, int sms) {
   if (M > 64 && pl.splits == 1) {  // a's rows on the lanes
     pl.staged = true;
     pl.bq = 128;
-    if (N > 128 && pl.groups > 8 && (int64_t)tiles(M, 2 * kLanes) * tiles(N, 240) >= sms / 2) {
-      // Pairs of CTAs, where the sum is long (8192 x 4096 x 4096 172 -> 115 us, 4096^3
-      // 89 -> 62; at K = 384, where the epilogue decides, 43 -> 48) and there are
-      // tiles for every SM.  The bytes of a step of 128, 192 and 240 columns are as
-      // 32 : 28 : 31: what is least over N.
-      const double by128 = 32.0 * tiles(N, 128), by192 = 28.0 * tiles(N, 192), by240 = 31.0 * tiles(N, 240);
-      pl.pair = by192 < by128 || by240 < by128;
-      if (pl.pair) pl.bq = by192 < by240 ? 192 : 240;
+    if (pl.groups > 8) {
+      // Long sums, where the epilogue is hidden: the width of the fewest rounds of all SMs
+      // times what a step of 128 k takes, 0.40 us with 128 columns, 0.44 with 192, 0.48
+      // with 240.  With 128, 192 and 240: 8192 x 4096 x 4096 177, 137 and 117 us, 4096^3
+      // 91, 72, 62, 1300 x 4096 x 4096 41, 33, 34, 5000 x 400 x 3000 22.4, 16.3, 16.8,
+      // 16,384 x 512 x 2048 30, 27, 28, 147,456 x 256 x 1152 66, 74, 80,
+      // 2048 x 1024 x 1152 8.2, 10.3, 10.8.
+      const auto cost = [&](int bq, int step) {
+        return ((int64_t)tiles(M, kLanes) * tiles(N, bq) + sms - 1) / sms * step;
+      };
+      const int64_t by128 = cost(128, 20), by192 = cost(192, 22), by240 = cost(240, 24);
+      if (std::min(by192, by240) < by128) pl.bq = by192 < by240 ? 192 : 240;
     }
-    pl.tiles_p = tiles(M, pl.pair ? 2 * kLanes : kLanes);
+    pl.tiles_p = tiles(M, kLanes);
     pl.tiles_q = tiles(N, pl.bq);
   }
   return pl;
@@ -852,10 +783,11 @@ size_t matmul8_workspace_bytes(int M, int N, int K, int sms) {
 }
 
 cudaError_t matmul8(const Matmul8Call& c, const Matmul8Plan& pl, int sms, cudaStream_t st, bool* tmap_ok) {
-  if (pl.staged && pl.pair)
-    return pl.bq == 240 ? staged<240, 1, true>(c, pl, sms, st, tmap_ok) : staged<192, 1, true>(c, pl, sms, st, tmap_ok);
-  if (pl.staged && pl.groups <= 8) return staged<128, 2, false>(c, pl, sms, st, tmap_ok);
-  if (pl.staged) return staged<128, 1, false>(c, pl, sms, st, tmap_ok);
+  if (pl.staged) {
+    if (pl.bq == 240) return staged<240, 1>(c, pl, sms, st, tmap_ok);
+    if (pl.bq == 192) return staged<192, 1>(c, pl, sms, st, tmap_ok);
+    return pl.groups <= 8 ? staged<128, 2>(c, pl, sms, st, tmap_ok) : staged<128, 1>(c, pl, sms, st, tmap_ok);
+  }
   switch (pl.bq) {
     case 16: return few_rows<16>(c, pl, sms, st, tmap_ok);
     case 32: return few_rows<32>(c, pl, sms, st, tmap_ok);

@@ -48,3 +48,13 @@ def test_scales_of_many_groups(M, N, K, blocks):
     """Scales that change from group to group, many groups to a sum and many sums
     to a CTA: the columns of tensor memory that hold them are used again and again."""
     check(M, N, K, blocks)
+
+
+@pytest.mark.parametrize("M, N, K", [
+    (1300, 4096, 4096), (5000, 400, 3001), (4097, 1500, 1100), (2500, 1999, 1290),           # 192 columns at a time
+    (2000, 2000, 9000), (1000, 4000, 4000), (20000, 240, 1281), (4096, 4096, 1200),          # 240
+    (3840, 192, 1153)])                                                                      # 128 are as good
+@pytest.mark.parametrize("blocks", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_wide_tiles(M, N, K, blocks, dtype):
+    check(M, N, K, blocks, dtype)
