@@ -58,3 +58,28 @@ def test_scales_of_many_groups(M, N, K, blocks):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_wide_tiles(M, N, K, blocks, dtype):
     check(M, N, K, blocks, dtype)
+
+
+LONG = [(64, 64, 20000), (3, 200, 20001), (100, 130, 20001), (512, 128, 147456),   # in pieces
+        (40, 10000, 3001), (2000, 128, 3001), (2000, 2000, 3001)]                  # b, a on the lanes; wide tiles
+
+
+@pytest.mark.parametrize("M, N, K", LONG)
+def test_no_term_of_a_long_sum_is_lost(M, N, K):
+    check(M, N, K, False)
+
+
+@pytest.mark.parametrize("M, N, K", LONG)
+def test_single_terms_of_a_long_sum(M, N, K):
+    """One term alone: the first and the last, both sides of the last border
+    between groups, and of every third of the others."""
+    a, sa, va = whole(M, K, 3)
+    b, sb, vb = whole(N, K, 4)
+    last = (K - 1) // 128 * 128
+    borders = sorted({0, K - 1, last - 1, last, *range(128, last, 384), *range(127, last, 384)})
+    for k in borders[:20] + borders[20::40] + borders[-3:]:
+        one = torch.zeros((M, -(-K // 16) * 16), dtype=torch.uint8, device=DEV)
+        one[:, k] = a.view(torch.uint8)[:, k]
+        got = evoattn.matmul8(one.view(torch.float8_e4m3fn)[:, :K], sa, b, sb, torch.float32)
+        assert torch.equal(got.cpu(), va[:, k:k + 1] * vb[:, k]), k
+    assert evoattn.device_status() == evoattn.OK
