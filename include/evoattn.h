@@ -564,7 +564,7 @@ evoattn_status evoattn_adamw(const evoattn_adamw_tensor* tensors, int count, flo
  * Dropout: keep * u / (1 - p), where an element's keep is a function of
  * (seed, step, site) and its place: word c % 4 of the Philox4x32-10 block with
  * the counter (c / 4, mask row, site, step mod 2^32) and the key seed, at or
- * above round(p 2^32), for channel c.  The mask row is the row's index over the
+ * above round(p 2^32) (at most 2^32 - 1), for channel c.  The mask row is the row's index over the
  * axes that are not in `shared` (bit 0: B, 1: I, 2: J).  No mask is stored: a
  * backward pass with the same (seed, step, site) draws it again.
  */

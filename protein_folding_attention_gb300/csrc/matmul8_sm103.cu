@@ -6,7 +6,9 @@
 // (kind::mxf8f6f4): a row's scale is a byte in tensor memory beside the
 // accumulator, so the sum over all of K stays in tensor memory in fp32 and no
 // CUDA core touches it before the end.  (The hardware's block is 32 elements; the
-// four of a group of 128 get the same byte.)
+// four of a group of 128 get the same byte.  Its sums are rounded toward zero: off by
+// 2.4e-7 in the root mean square over 4096 terms and 1.3e-6 over 16,384, below fp32's
+// K 2^-24 and, for outputs in bf16, below their rounding.)
 //
 // One operand's rows lie on the 128 lanes of tensor memory (the M operand of the
 // MMA), the other's on BQ of its columns (the N operand).  With many rows a's are
@@ -747,10 +749,13 @@ Matmul8Plan matmul8_plan(int M, int N, int K, int sms) {
   pl.per_split = pl.groups;
   const int64_t count = (int64_t)pl.tiles_p * pl.tiles_q;
   if (2 * count <= sms && pl.groups > 16) {
-    // Pieces of the sum, two groups at least, for as many CTAs as there are SMs.  The
-    // second launch costs 1 to 2 us of the device and 6 of the host, a group 0.3:
-    // 16 x 4096 x 4096 7.5 us in pieces and 13.7 whole, 30 x 500 x 3000 5.0 and 10.9, but
-    // 1 x 4096 x 1536 5.1 and 6.9 (a call 22 and 15), 4 x 1000 x 600 4.8 and 4.2.
+    // Pieces of the sum, two groups at least, for as many CTAs as there are SMs.  On the
+    // device, whole and in pieces, at 8, 12, 16, 24 and 32 groups: 1 x 4096 5.3 7.0 8.3 11.1
+    // 13.8 and 5.0 5.3 5.6 6.7 7.4 us, 64 x 4096 5.8 7.4 8.9 11.8 14.6 and 6.9 7.2 7.6 8.6 9.3,
+    // 100 x 1500 6.9 8.2 9.7 12.6 15.5 and 6.1 6.2 6.6 7.0 7.4.  The second launch costs a
+    // call that is not captured 6 us of the host (24.5 instead of 18.5 at any of these
+    // lengths).  The device alone would put the border at 8 to 12 groups; up to 16 a
+    // captured call loses less than the other saves.
     const int64_t most = std::min<int64_t>(sms / count, pl.groups / 2);
     pl.per_split = (int)((pl.groups + most - 1) / most);
     pl.splits = (pl.groups + pl.per_split - 1) / pl.per_split;

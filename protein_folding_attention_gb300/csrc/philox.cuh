@@ -11,8 +11,9 @@
 // elements.  At the memory rate of bf16 rows (read, add, write: four elements a
 // cycle and SM) an SM would spend most of its issue slots on it: the residual add
 // of 589,824 rows of 128 takes 89 us with a mask of its own for every row, where the
-// bytes take 67.  Rows that share a mask are therefore worked on together, with one
-// draw (147,456 rows of 128: 20 us, bytes 17), and fp32 rows hide it (130 us, 133).
+// bytes take 67 at the copy rate.  Rows that share a mask are therefore worked on
+// together, with one draw (147,456 rows of 128: 20 us, 17 at the copy rate), and fp32 rows
+// hide it (130 us, 133 at the copy rate, which is that of one read for each write).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
