@@ -769,7 +769,9 @@ Matmul8Plan matmul8_plan(int M, int N, int K, int sms) {
       // with 240.  With 128, 192 and 240: 8192 x 4096 x 4096 177, 137 and 117 us, 4096^3
       // 91, 72, 62, 1300 x 4096 x 4096 41, 33, 34, 5000 x 400 x 3000 22.4, 16.3, 16.8,
       // 16,384 x 512 x 2048 30, 27, 28, 147,456 x 256 x 1152 66, 74, 80,
-      // 2048 x 1024 x 1152 8.2, 10.3, 10.8.
+      // 2048 x 1024 x 1152 8.2, 10.3, 10.8.  (In bf16.  In fp32 with an addend the epilogue
+      // still counts at 9 to 11 groups, where the choice is up to a quarter off:
+      // 16,384 x 960 x 1152 39, 41, 49; 4096^3 96, 78, 72.)
       const auto cost = [&](int bq, int step) {
         return ((int64_t)tiles(M, kLanes) * tiles(N, bq) + sms - 1) / sms * step;
       };
